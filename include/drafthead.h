@@ -323,6 +323,95 @@ int draft_head_top_tokens_static(const dh_head_t *hd, const void *h, int M, int3
  * on a device, it looks up the array's address like that entry point. */
 int draft_head_static_read_device_error(int *err, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Operators over many tokens: scoring and distilling a draft head.
+ * ------------------------------------------------------------------------ */
+
+/* Element types of their tensors. */
+typedef enum { DH_T_BF16 = 1, DH_T_F16 = 2, DH_T_F32 = 3 } dh_type;
+
+#define DH_MAX_TOP 128     /* alternatives per row of draft_head_token_logprobs */
+#define DH_MAX_TEACHER 512 /* teacher entries per row of draft_head_distill */
+
+/* Rows of logits. z: [M][C] of dh_type `type`, row stride ld elements (ld >= C
+ * when M > 1; any value when M == 1), aligned to its element type only (16-byte
+ * aligned rows are read fastest). 1 <= C <= 2^30. -inf marks a masked column;
+ * a row may be masked throughout.
+ *   temperature  t > 0, finite: probabilities are softmax(z / t).
+ *   row_of       int32 [V] or NULL: ids given to the operator are target ids and
+ *                row_of[id] is their column (-1: not kept); NULL: ids are columns.
+ *   idx          int32 [C] or NULL: id of each column, for ids that the operator
+ *                returns; NULL: the column.
+ * An id outside [0, V), of a row that is not kept, or whose column is outside
+ * [0, C) has no column. */
+typedef struct dh_logits {
+    const void *z;
+    int type;
+    int M;
+    int C;
+    int64_t ld;
+    float temperature;
+    const int32_t *row_of;
+    int V;
+    const int32_t *idx;
+} dh_logits_t;
+
+/* row_of[idx[n]] = n for n < n_kept and -1 elsewhere: the column of every
+ * target id, for dh_logits_t. idx: distinct ids (entries outside [0, V) are
+ * skipped); row_of: device int32 [V]. A memset and one kernel on `stream`. */
+int draft_head_row_map(const int32_t *idx, int n_kept, int32_t *row_of, int V, void *stream);
+
+/* Log-probabilities, entropy, normaliser and top alternatives of each row m of
+ * lg (the pages have no counterpart; the log-probability of a drafted token is
+ * what rejection sampling and acceptance estimates need). With
+ * d = (z - max z) / t and S = sum_c e^d_c, sums in 32 bits:
+ *   lse[m]         = max z / t + ln S               (fp32 [M], or NULL),
+ *   entropy[m]     = ln S - (sum_c e^d_c d_c) / S   (fp32 [M], or NULL),
+ *   logp[m][g]     = d_j - ln S, j the column of tokens[m][g]; -inf when the
+ *                    token has no column               (int32 / fp32 [M][G]),
+ *   top_ids[m][i], top_logp[m][i], i < top_k: the columns of the largest logits
+ *                    in descending order, equal ones by the lowest column (NaN
+ *                    counts as the largest, -0 equals 0), as ids through
+ *                    lg->idx, and their log-probabilities; -1 and -inf where
+ *                    fewer than top_k logits are above -inf (int32 / fp32 [M][top_k]).
+ * A row that is -inf throughout has lse -inf, entropy 0 and logp -inf. A NaN or
+ * +inf logit makes its row's lse, entropy and log-probabilities NaN.
+ * 0 <= top_k <= DH_MAX_TOP; tokens and logp may be NULL when G is 0, top_logp
+ * and top_ids when top_k is 0. One kernel launch, no workspace. Repeatable bit
+ * for bit (for logits at the same offset from a 16-byte boundary, which sets the
+ * order of the sums). Capturable in a CUDA graph. */
+int draft_head_token_logprobs(const dh_logits_t *lg, const int32_t *tokens, int G, float *logp,
+                              float *entropy, float *lse, int top_k, float *top_logp,
+                              int32_t *top_ids, void *stream);
+
+/* Distillation of the student's logits lg from a teacher's top K logits (the
+ * pages have no counterpart; it is how a reduced-vocabulary drafter is trained
+ * on the target's outputs). Row m has K entries: ids[m][j] (int32) and the
+ * teacher's logits val[m][j] (dh_type val_type), both contiguous [M][K]. An
+ * entry is in use when its id has a column, neither val nor the student's logit
+ * there is -inf, and weight[m] != 0. With p = softmax(val / t) over the entries
+ * in use, q = softmax(z / t) over all columns and w = weight[m] (1 when weight
+ * is NULL):
+ *   loss[m] = w t^2 sum_j p_j (log p_j - log q_j),
+ *   dz[m][c] = w t (q_c - sum over the entries j of column c of p_j),
+ * both 0 for a row with no entry in use. loss: fp32 [M]. dz: NULL (loss alone),
+ * or of lg's type, [M][C] with row stride ld_dz (every column < C is written, none
+ * beyond); dz may be lg->z itself with ld_dz == lg->ld, else they must not
+ * overlap. Vector stores need dz's rows at the same offset from a 16-byte boundary
+ * as z's rows. lse: NULL, or (with dz NULL) fp32 [M], the student's normaliser
+ * log sum e^(z / t) for draft_head_distill_backward. 1 <= K <= DH_MAX_TEACHER.
+ * One kernel launch, no workspace, repeatable like draft_head_token_logprobs. */
+int draft_head_distill(const dh_logits_t *lg, const int32_t *ids, const void *val, int val_type, int K,
+                       const float *weight, float *loss, float *lse, void *dz, int64_t ld_dz,
+                       void *stream);
+
+/* The gradient of draft_head_distill from its lse, for a caller that learns the
+ * row weights after the loss (weight[m] = the upstream gradient of loss[m] times
+ * the forward's weight; NULL: 1): dz as above, with q = e^(z / t - lse). */
+int draft_head_distill_backward(const dh_logits_t *lg, const int32_t *ids, const void *val, int val_type,
+                                int K, const float *lse, const float *weight, void *dz, int64_t ld_dz,
+                                void *stream);
+
 /* Self-test of the failure handling of the draft-step kernels (the pages have
  * no counterpart): a one-thread kernel waits for an event that nothing
  * produces and gives up after `rounds` tries, recording DH_DEVERR_TIMEOUT in

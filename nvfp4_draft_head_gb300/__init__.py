@@ -14,12 +14,19 @@ Names follow the C ABI in include/drafthead.h:
   NVFP4Linear              nvfp4_linear: an MTP-block linear, y = x W'^T
   DraftHead.top_keys       draft_head_top_keys: a vocabulary shard's argmax keys
   keys_to_ids              draft_head_keys_to_ids: combined keys -> target ids
+  draft_head_row_map       dh_idx -> column of every target id
+  token_logprobs           draft_head_token_logprobs: log-probabilities of given
+                           tokens, entropy, normaliser, top alternatives
+  distill_topk             draft_head_distill: distillation loss and gradient
+  (_forward, _backward)    the loss alone; the gradient from its normaliser
+  DistillTopK              the same as a torch.autograd function
 The vocabulary-sharded head (the local-argmax exchange) is in .sharded.
 """
 from __future__ import annotations
 
 import ctypes as C
 import os
+from typing import NamedTuple
 
 import numpy as np
 import torch
@@ -33,6 +40,8 @@ DH_WORKSPACE_ALIGN = 256
 DH_DEVERR_IDX = 1
 DH_DEVERR_TIMEOUT = 2
 DH_HEAD_IDX_ASCENDING = 1
+DH_T_BF16, DH_T_F16, DH_T_F32 = 1, 2, 3
+DH_MAX_TOP, DH_MAX_TEACHER = 128, 512
 
 EXPORTS = (
     "draft_head_build_index", "draft_head_quantize_workspace_bytes", "nvfp4_quantize_rows",
@@ -41,7 +50,8 @@ EXPORTS = (
     "draft_head_status_string", "draft_head_abi_version", "draft_head_top_tokens_static",
     "nvfp4_pack_head", "fp8_quantize_activations", "draft_head_last_cuda_error", "nvfp4_linear",
     "draft_head_wait_probe", "draft_head_top_tokens_host", "draft_head_top_keys", "draft_head_keys_to_ids",
-    "draft_head_static_read_device_error",
+    "draft_head_static_read_device_error", "draft_head_row_map", "draft_head_token_logprobs", "draft_head_distill",
+    "draft_head_distill_backward",
 )
 
 _lib = None
@@ -63,6 +73,11 @@ class dh_head_t(C.Structure):
     _fields_ = [("fmt", C.c_int), ("V", C.c_int), ("K", C.c_int), ("N", C.c_int),
                 ("n_kept", C.c_int), ("q", C.c_void_p), ("sf", C.c_void_p),
                 ("scale", C.c_void_p), ("idx", C.c_void_p), ("flags", C.c_uint)]
+
+
+class dh_logits_t(C.Structure):
+    _fields_ = [("z", C.c_void_p), ("type", C.c_int), ("M", C.c_int), ("C", C.c_int), ("ld", C.c_int64),
+                ("temperature", C.c_float), ("row_of", C.c_void_p), ("V", C.c_int), ("idx", C.c_void_p)]
 
 
 def library_path() -> str:
@@ -103,6 +118,11 @@ def lib():
         L.draft_head_top_keys.argtypes = [C.POINTER(dh_head_t), P, I, P, P, S, P]
         L.draft_head_keys_to_ids.argtypes = [P, I, P, P, P]
         L.draft_head_static_read_device_error.argtypes = [P, P]
+        LG = C.POINTER(dh_logits_t)
+        L.draft_head_row_map.argtypes = [P, I, P, I, P]
+        L.draft_head_token_logprobs.argtypes = [LG, P, I, P, P, P, I, P, P, P]
+        L.draft_head_distill.argtypes = [LG, P, P, I, I, P, P, P, P, C.c_int64, P]
+        L.draft_head_distill_backward.argtypes = [LG, P, P, I, I, P, P, P, C.c_int64, P]
         _lib = L
     return _lib
 
@@ -440,3 +460,197 @@ def bf16_truncated_head(W: torch.Tensor, n_rows: int) -> DraftHead:
     if n_rows % 64 or not 0 < n_rows <= W.shape[0]:
         raise ValueError("n_rows must be a multiple of 64 within the head")
     return DraftHead(DH_FMT_BF16, W.shape[0], W[:n_rows], None, n_rows)
+
+
+# --------------------------------------------------- operators on many tokens --
+
+_TYPES = {torch.bfloat16: DH_T_BF16, torch.float16: DH_T_F16, torch.float32: DH_T_F32}
+
+
+def _vector(t: torch.Tensor | None, name: str, dtype: torch.dtype, n: int | None, device) -> None:
+    if t is not None and (t.dtype != dtype or t.device != device or not t.is_contiguous() or (n is not None and t.numel() != n)):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor{'' if n is None else f' of {n} elements'} on {device}")
+
+
+def _keep_for(stream, *tensors) -> None:
+    """Tensors used on a stream other than the current one stay allocated until its work is done."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _logits_desc(logits: torch.Tensor, temperature: float, row_of: torch.Tensor | None,
+                 idx: torch.Tensor | None = None) -> dh_logits_t:
+    if logits.dim() != 2 or logits.dtype not in _TYPES or not logits.is_cuda:
+        raise ValueError("logits must be a [M, C] bfloat16, float16 or float32 CUDA tensor")
+    M, n = logits.shape
+    ld, step = logits.stride()
+    if (step != 1 and n > 1) or (M > 1 and ld < n):
+        raise ValueError("logits rows must be contiguous and must not overlap")
+    _vector(row_of, "row_of", torch.int32, None, logits.device)
+    if idx is not None:
+        _vector(idx, "idx", torch.int32, None, logits.device)
+        if idx.numel() < n:
+            raise ValueError(f"idx must hold the ids of all {n} columns")
+    return dh_logits_t(logits.data_ptr(), _TYPES[logits.dtype], M, n, ld, temperature, _ptr(row_of),
+                       0 if row_of is None else row_of.numel(), _ptr(idx))
+
+
+def draft_head_row_map(idx: torch.Tensor, n_kept: int, V: int, stream=None) -> torch.Tensor:
+    """int32[V]: the head row (logits column) of every target id, -1 for ids that
+    are not kept; the row_of argument of the operators below."""
+    if idx.dtype != torch.int32 or idx.dim() != 1 or not idx.is_cuda or not idx.is_contiguous() or idx.numel() < n_kept:
+        raise ValueError(f"idx must be a contiguous int32 CUDA vector of at least {n_kept} elements")
+    row_of = torch.empty(V, dtype=torch.int32, device=idx.device)
+    _check("draft_head_row_map",
+           lib().draft_head_row_map(idx.data_ptr(), n_kept, row_of.data_ptr(), V, _stream(stream)))
+    _keep_for(stream, idx, row_of)
+    return row_of
+
+
+class TokenLogprobs(NamedTuple):
+    """Results of token_logprobs for M rows: logp float32 [M, G] (None without
+    tokens), entropy and lse float32 [M], top_logp float32 and top_ids int32 [M, top_k]."""
+    logp: torch.Tensor | None
+    entropy: torch.Tensor
+    lse: torch.Tensor
+    top_logp: torch.Tensor
+    top_ids: torch.Tensor
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, top_k: int = 0, temperature: float = 1.0,
+                   idx: torch.Tensor | None = None, row_of: torch.Tensor | None = None, stream=None) -> TokenLogprobs:
+    """Log-probabilities of `tokens` (int32 [M] or [M, G]), entropy, normaliser and
+    the top_k alternatives of logits rows [M, C] (rows may be strided; pass
+    logits[:, :n_kept] to leave a head's padding rows out). With row_of
+    (draft_head_row_map) tokens are target ids, with idx (dh_idx) the alternatives
+    are returned as target ids; without them both are columns. A token without a
+    column has log-probability -inf; alternatives past the last logit above -inf
+    have id -1. See draft_head_token_logprobs."""
+    d = _logits_desc(logits, temperature, row_of, idx)
+    M, dev = d.M, logits.device
+    G = 0
+    if tokens is not None:
+        if tokens.dim() not in (1, 2) or tokens.shape[0] != M:
+            raise ValueError(f"tokens must be an int32 tensor [{M}] or [{M}, G]")
+        _vector(tokens, "tokens", torch.int32, None, dev)
+        G = 1 if tokens.dim() == 1 else tokens.shape[1]
+    if not 0 <= top_k <= DH_MAX_TOP:
+        raise ValueError(f"top_k must lie in 0 .. {DH_MAX_TOP}")
+    stats = torch.empty((2, M), dtype=torch.float32, device=dev)
+    logp = None if tokens is None else torch.empty(tokens.shape, dtype=torch.float32, device=dev)
+    top_logp = torch.empty((M, top_k), dtype=torch.float32, device=dev)
+    top_ids = torch.empty((M, top_k), dtype=torch.int32, device=dev)
+    entropy, lse = stats.unbind()
+    if M > 0:
+        _check("draft_head_token_logprobs",
+               lib().draft_head_token_logprobs(C.byref(d), _ptr(tokens), G, _ptr(logp), stats.data_ptr(),
+                                               stats.data_ptr() + 4 * M, top_k, top_logp.data_ptr(),
+                                               top_ids.data_ptr(), _stream(stream)))
+        _keep_for(stream, logits, tokens, idx, row_of, stats, logp, top_logp, top_ids)
+    return TokenLogprobs(logp, entropy, lse, top_logp, top_ids)
+
+
+def _teacher(logits, ids, val):
+    if ids.dim() != 2 or ids.shape[0] != logits.shape[0] or val.shape != ids.shape:
+        raise ValueError(f"teacher ids and logits must be [{logits.shape[0]}, K] tensors")
+    _vector(ids, "teacher ids", torch.int32, None, logits.device)
+    if val.dtype not in _TYPES:
+        raise ValueError("teacher logits must be bfloat16, float16 or float32")
+    _vector(val, "teacher logits", val.dtype, None, logits.device)
+    if not 1 <= ids.shape[1] <= DH_MAX_TEACHER:
+        raise ValueError(f"a row takes 1 .. {DH_MAX_TEACHER} teacher entries")
+    return ids.shape[1], _TYPES[val.dtype]
+
+
+def _gradient(logits: torch.Tensor, out: torch.Tensor | None) -> torch.Tensor:
+    """The caller's gradient buffer, checked, or a new one with the logits' row stride."""
+    M, n = logits.shape
+    if out is None:
+        ld = logits.stride(0)
+        if not n <= ld <= 2 * n:     # one row, or rows far apart: whole 16-byte vectors per row
+            ld = (n + 7) // 8 * 8
+        return torch.empty((M, ld), dtype=logits.dtype, device=logits.device)[:, :n]
+    if out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device or \
+            (out.stride(1) != 1 and n > 1) or (M > 1 and out.stride(0) < n):
+        raise ValueError("the gradient must be a tensor of the logits' shape, type and device with contiguous rows")
+    return out
+
+
+def distill_topk(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor, temperature: float = 1.0,
+                 weights: torch.Tensor | None = None, row_of: torch.Tensor | None = None,
+                 dlogits: torch.Tensor | None = None, stream=None):
+    """(loss float32 [M], dlogits [M, C]): per-row distillation loss of the
+    student's logits [M, C] from the teacher's top K ids (int32 [M, K]) and logits
+    [M, K], and the gradient of its sum, in one kernel. Ids are target ids with
+    row_of, columns without it; entries without a column, and masked (-inf) ones,
+    leave the teacher's distribution. weights: float32 [M], 0 for rows to leave
+    out. dlogits may be the logits tensor itself. See draft_head_distill."""
+    d = _logits_desc(logits, temperature, row_of)
+    K, vt = _teacher(logits, teacher_ids, teacher_logits)
+    _vector(weights, "weights", torch.float32, d.M, logits.device)
+    dz = _gradient(logits, dlogits)
+    loss = torch.empty(d.M, dtype=torch.float32, device=logits.device)
+    if d.M > 0:
+        _check("draft_head_distill",
+               lib().draft_head_distill(C.byref(d), teacher_ids.data_ptr(), teacher_logits.data_ptr(), vt, K, _ptr(weights),
+                                        loss.data_ptr(), None, dz.data_ptr(), dz.stride(0), _stream(stream)))
+        _keep_for(stream, logits, teacher_ids, teacher_logits, weights, row_of, dz, loss)
+    return loss, dz
+
+
+def distill_topk_forward(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
+                         temperature: float = 1.0, weights: torch.Tensor | None = None,
+                         row_of: torch.Tensor | None = None, stream=None):
+    """(loss, lse), both float32 [M]: the loss of distill_topk alone, and the
+    student's normaliser for distill_topk_backward."""
+    d = _logits_desc(logits, temperature, row_of)
+    K, vt = _teacher(logits, teacher_ids, teacher_logits)
+    _vector(weights, "weights", torch.float32, d.M, logits.device)
+    out = torch.empty((2, d.M), dtype=torch.float32, device=logits.device)
+    if d.M > 0:
+        _check("draft_head_distill",
+               lib().draft_head_distill(C.byref(d), teacher_ids.data_ptr(), teacher_logits.data_ptr(), vt, K, _ptr(weights),
+                                        out.data_ptr(), out.data_ptr() + 4 * d.M, None, 0, _stream(stream)))
+        _keep_for(stream, logits, teacher_ids, teacher_logits, weights, row_of, out)
+    return out.unbind()
+
+
+def distill_topk_backward(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor, lse: torch.Tensor,
+                          weights: torch.Tensor | None = None, temperature: float = 1.0,
+                          row_of: torch.Tensor | None = None, dlogits: torch.Tensor | None = None,
+                          stream=None) -> torch.Tensor:
+    """dlogits [M, C] from distill_topk_forward's lse; weights: float32 [M], the
+    upstream gradient of each row's loss times the forward's weight."""
+    d = _logits_desc(logits, temperature, row_of)
+    K, vt = _teacher(logits, teacher_ids, teacher_logits)
+    _vector(lse, "lse", torch.float32, d.M, logits.device)
+    _vector(weights, "weights", torch.float32, d.M, logits.device)
+    dz = _gradient(logits, dlogits)
+    if d.M > 0:
+        _check("draft_head_distill_backward",
+               lib().draft_head_distill_backward(C.byref(d), teacher_ids.data_ptr(), teacher_logits.data_ptr(), vt, K,
+                                                 lse.data_ptr(), _ptr(weights), dz.data_ptr(), dz.stride(0),
+                                                 _stream(stream)))
+        _keep_for(stream, logits, teacher_ids, teacher_logits, lse, weights, row_of, dz)
+    return dz
+
+
+class DistillTopK(torch.autograd.Function):
+    """loss [M] = DistillTopK.apply(logits, teacher_ids, teacher_logits, temperature,
+    weights, row_of); differentiable in the logits (the teacher is a constant)."""
+
+    @staticmethod
+    def forward(ctx, logits, teacher_ids, teacher_logits, temperature=1.0, weights=None, row_of=None):
+        loss, lse = distill_topk_forward(logits, teacher_ids, teacher_logits, temperature, weights, row_of)
+        ctx.save_for_backward(logits, teacher_ids, teacher_logits, lse, weights, row_of)
+        ctx.temperature = temperature
+        return loss
+
+    @staticmethod
+    def backward(ctx, dloss):
+        logits, ids, val, lse, weights, row_of = ctx.saved_tensors
+        up = dloss.float() if weights is None else dloss.float() * weights
+        dz = distill_topk_backward(logits, ids, val, lse, up.contiguous(), ctx.temperature, row_of)
+        return dz, None, None, None, None, None

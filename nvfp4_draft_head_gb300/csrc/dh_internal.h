@@ -88,5 +88,55 @@ int record_cuda_error(cudaError_t e);
 // Number of SMs of the current device (cached per device).
 int sm_count();
 
+// Logits rows of the token log-probability and distillation operators (dh_type
+// element types; ld in elements; inv_t = 1 / temperature; row_of may be null).
+struct LogprobArgs {
+    const void* z;
+    long long ld;
+    int M, C;
+    float inv_t;
+    const int32_t* row_of;
+    int V;
+    const int32_t* idx;      // column -> id of the alternatives, or null
+    const int32_t* tokens;   // [M][G]
+    int G;
+    float* logp;             // [M][G]
+    float* entropy;          // [M] or null
+    float* lse;              // [M] or null
+    int k;
+    float* top_logp;         // [M][k]
+    int32_t* top_ids;        // [M][k]
+    unsigned ncta;           // set by the launcher: CTAs per row
+};
+cudaError_t launch_token_logprobs(LogprobArgs a, int type, cudaStream_t s);
+
+struct DistillArgs {
+    const void* z;
+    long long ld;
+    int M, C;
+    float t, inv_t;
+    const int32_t* row_of;
+    int V;
+    const int32_t* ids;      // [M][K] teacher ids
+    const void* val;         // [M][K] teacher logits of val_type
+    int val_type;
+    int K;
+    const float* weight;     // [M] or null (1)
+    const float* lse_in;     // backward: [M]
+    float* loss;             // [M], forward and both
+    float* lse;              // [M] or null, forward
+    void* dz;                // [M][C] with row stride ld_dz, both and backward
+    long long ld_dz;
+    unsigned ncta;           // set by the launcher: CTAs per row
+};
+enum DistillMode { kDistillForward, kDistillBoth, kDistillBackward };
+cudaError_t launch_distill(DistillArgs a, int type, DistillMode mode, cudaStream_t s);
+
+// row_of[idx[i]] = i for i < n, -1 elsewhere.
+cudaError_t launch_row_map(const int32_t* idx, int n, int32_t* row_of, int V, cudaStream_t s);
+
+namespace rows {
+int cluster_size(int M, long long row_bytes);
+}
 
 }  // namespace dh
