@@ -333,6 +333,49 @@ typedef enum { DH_T_BF16 = 1, DH_T_F16 = 2, DH_T_F32 = 3 } dh_type;
 #define DH_MAX_TOP 128     /* alternatives per row of draft_head_token_logprobs */
 #define DH_MAX_TEACHER 512 /* teacher entries per row of draft_head_distill */
 
+/* NVFP4 x NVFP4 product of many tokens (W4A4), for the batches past the draft
+ * step's 16 rows: prefill and scoring through the head or an MTP-block linear
+ * (the pages run those linears W4A16; four-bit activations are this library's
+ * addition). Weights are an NVFP4 weight [N][K] as written by nvfp4_quantize_rows,
+ * laid out once by nvfp4_pack_matmul; the activations are quantised inside the
+ * call by the same recipe with one global scale per token: for row m,
+ *   gx = max(max_k |x[m, k]|, 1e-12) / 2688, per block of 16 s = E4M3_RNE(bamax /
+ *   fp32(6 gx)), codes = E2M1_RNE(clamp(x / fp32(dec(s) gx), +-6)) in fp32,
+ *   y[m, n] = scale * gx * sum_blocks sx[m] sw[n] sum_16 cx[m] cw[n],
+ * summed in fp32 on the tensor cores and rounded once to y's type. A row with a
+ * value that is not finite gives a row of NaN; rows do not affect one another. */
+typedef struct dh_matmul {
+    int N;               /* output features, N % 64 == 0 (<= 2^24) */
+    int K;               /* input features, K % 16 == 0 (<= 2^20) */
+    const void *packed;  /* nvfp4_matmul_packed_bytes(N, K) bytes from nvfp4_pack_matmul, 16-byte aligned */
+    const float *scale;  /* the weight's global scale, 1 float */
+} dh_matmul_t;
+
+/* Bytes of the packed weight: rows padded to 128, K to 256 (0 for an unsupported shape). */
+size_t nvfp4_matmul_packed_bytes(int N, int K);
+
+/* Lay out an NVFP4 weight (q [N][K/2], 16-byte aligned; sf [N][K/16]) for
+ * nvfp4_matmul: blocks of 128 rows x 256 k in the order [N/128][K/256], each the
+ * rows' 128 code bytes (16-byte piece p of row r at r * 128 + 16 (p ^ (r % 8))),
+ * then the scales, [k / 64][r % 32][r / 32][4]; zeros beyond N and K. packed:
+ * 16-byte aligned. One kernel on `stream`. */
+int nvfp4_pack_matmul(const uint8_t *q, const uint8_t *sf, int N, int K, uint8_t *packed, void *stream);
+
+/* Bytes of workspace of nvfp4_matmul for M tokens: the quantised activations
+ * (0 for an unsupported shape). */
+size_t nvfp4_matmul_workspace_bytes(int M, int K);
+
+/* y = x W'^T. x: [M][K] of dh_type x_type, row stride ldx elements; y: [M][N] of
+ * dh_type y_type, row stride ldy (strides are ignored when M == 1); both aligned
+ * to their element (16-byte aligned rows are read and written fastest). 1 <= M
+ * <= 2^24. ws: nvfp4_matmul_workspace_bytes(M, K) bytes, 256-byte aligned, no
+ * initialisation; calls that overlap on the GPU must not share one. error:
+ * NULL, or a device error word that a bounded wait which ran out sets to
+ * DH_DEVERR_TIMEOUT (the results are then invalid). Two kernels on `stream`;
+ * capturable in a CUDA graph. */
+int nvfp4_matmul(const dh_matmul_t *w, const void *x, int x_type, int64_t ldx, int M, void *y, int y_type,
+                 int64_t ldy, void *ws, size_t ws_bytes, unsigned int *error, void *stream);
+
 /* Rows of logits. z: [M][C] of dh_type `type`, row stride ld elements (ld >= C
  * when M > 1; any value when M == 1), aligned to its element type only (16-byte
  * aligned rows are read fastest). 1 <= C <= 2^30. -inf marks a masked column;

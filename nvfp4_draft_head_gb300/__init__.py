@@ -14,6 +14,8 @@ Names follow the C ABI in include/drafthead.h:
   NVFP4Linear              nvfp4_linear: an MTP-block linear, y = x W'^T
   DraftHead.top_keys       draft_head_top_keys: a vocabulary shard's argmax keys
   keys_to_ids              draft_head_keys_to_ids: combined keys -> target ids
+  NVFP4Matmul              nvfp4_matmul: y = x W'^T for many tokens, activations
+                           quantised to NVFP4 per token (W4A4)
   draft_head_row_map       dh_idx -> column of every target id
   token_logprobs           draft_head_token_logprobs: log-probabilities of given
                            tokens, entropy, normaliser, top alternatives
@@ -51,7 +53,8 @@ EXPORTS = (
     "nvfp4_pack_head", "fp8_quantize_activations", "draft_head_last_cuda_error", "nvfp4_linear",
     "draft_head_wait_probe", "draft_head_top_tokens_host", "draft_head_top_keys", "draft_head_keys_to_ids",
     "draft_head_static_read_device_error", "draft_head_row_map", "draft_head_token_logprobs", "draft_head_distill",
-    "draft_head_distill_backward",
+    "draft_head_distill_backward", "nvfp4_matmul_packed_bytes", "nvfp4_pack_matmul", "nvfp4_matmul_workspace_bytes",
+    "nvfp4_matmul",
 )
 
 _lib = None
@@ -78,6 +81,10 @@ class dh_head_t(C.Structure):
 class dh_logits_t(C.Structure):
     _fields_ = [("z", C.c_void_p), ("type", C.c_int), ("M", C.c_int), ("C", C.c_int), ("ld", C.c_int64),
                 ("temperature", C.c_float), ("row_of", C.c_void_p), ("V", C.c_int), ("idx", C.c_void_p)]
+
+
+class dh_matmul_t(C.Structure):
+    _fields_ = [("N", C.c_int), ("K", C.c_int), ("packed", C.c_void_p), ("scale", C.c_void_p)]
 
 
 def library_path() -> str:
@@ -123,6 +130,12 @@ def lib():
         L.draft_head_token_logprobs.argtypes = [LG, P, I, P, P, P, I, P, P, P]
         L.draft_head_distill.argtypes = [LG, P, P, I, I, P, P, P, P, C.c_int64, P]
         L.draft_head_distill_backward.argtypes = [LG, P, P, I, I, P, P, P, C.c_int64, P]
+        L.nvfp4_matmul_packed_bytes.argtypes = [I, I]
+        L.nvfp4_matmul_packed_bytes.restype = S
+        L.nvfp4_pack_matmul.argtypes = [P, P, I, I, P, P]
+        L.nvfp4_matmul_workspace_bytes.argtypes = [I, I]
+        L.nvfp4_matmul_workspace_bytes.restype = S
+        L.nvfp4_matmul.argtypes = [C.POINTER(dh_matmul_t), P, I, C.c_int64, I, P, I, C.c_int64, P, S, P, P]
         _lib = L
     return _lib
 
@@ -478,6 +491,74 @@ def _keep_for(stream, *tensors) -> None:
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
+
+
+class NVFP4Matmul:
+    """An NVFP4 weight for many-token products: forward(x) = x W'^T with x
+    quantised to NVFP4 per token (W4A4) and fp32 accumulation. q uint8 [N, K/2],
+    sf uint8 [N, K/16] and g float32 [1] as from nvfp4_quantize_rows; N % 64 == 0,
+    K % 16 == 0. For up to 16 tokens NVFP4Linear and DraftHead keep the
+    activations in bfloat16."""
+
+    def __init__(self, q: torch.Tensor, sf: torch.Tensor, g: torch.Tensor, stream=None):
+        if q.dtype != torch.uint8 or q.dim() != 2 or not q.is_cuda or not q.is_contiguous():
+            raise ValueError("q must be a contiguous [N, K/2] uint8 CUDA tensor")
+        self.N, self.K = q.shape[0], 2 * q.shape[1]
+        if sf.shape != (self.N, self.K // 16):
+            raise ValueError(f"sf must be uint8 [{self.N}, {self.K // 16}]")
+        _vector(sf, "sf", torch.uint8, None, q.device)
+        _vector(g, "g", torch.float32, 1, q.device)
+        self.g = g
+        nb = lib().nvfp4_matmul_packed_bytes(self.N, self.K)
+        if nb == 0:
+            raise DraftHeadError("nvfp4_matmul_packed_bytes", DH_ERR_SHAPE)
+        self.packed = torch.empty(nb, dtype=torch.uint8, device=q.device)
+        _check("nvfp4_pack_matmul",
+               lib().nvfp4_pack_matmul(q.data_ptr(), sf.data_ptr(), self.N, self.K, self.packed.data_ptr(), _stream(stream)))
+        self.error = torch.zeros(1, dtype=torch.int32, device=q.device)
+        self.desc = dh_matmul_t(self.N, self.K, self.packed.data_ptr(), g.data_ptr())
+        _keep_for(stream, q, sf, g, self.packed, self.error)
+
+    @classmethod
+    def from_weight(cls, W: torch.Tensor, idx: torch.Tensor | None = None, stream=None) -> "NVFP4Matmul":
+        """Quantise the rows W[idx] (all rows without idx) of a bfloat16 weight [V, K]."""
+        if idx is None:
+            idx = torch.arange(W.shape[0], dtype=torch.int32, device=W.device)
+        return cls(*nvfp4_quantize_rows(W, idx, stream), stream=stream)
+
+    def forward(self, x: torch.Tensor, y: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+                stream=None) -> torch.Tensor:
+        """y [M, N] (out_dtype: bfloat16, float16 or float32, or a given tensor's
+        type) = x W'^T for x [M, K] (bfloat16, float16 or float32, rows may be strided)."""
+        if x.dim() != 2 or x.shape[1] != self.K or x.dtype not in _TYPES or x.device != self.packed.device or \
+                x.stride(1) != 1 or (x.shape[0] > 1 and x.stride(0) < self.K):
+            raise ValueError(f"x must be a [M, {self.K}] bfloat16, float16 or float32 tensor with contiguous rows")
+        M = x.shape[0]
+        if y is None:
+            if out_dtype not in _TYPES:
+                raise ValueError("out_dtype must be bfloat16, float16 or float32")
+            y = torch.empty((M, self.N), dtype=out_dtype, device=x.device)
+        elif y.shape != (M, self.N) or y.dtype not in _TYPES or y.device != x.device or y.stride(1) != 1 or \
+                (M > 1 and y.stride(0) < self.N):
+            raise ValueError(f"y must be a [{M}, {self.N}] bfloat16, float16 or float32 tensor with contiguous rows")
+        if M == 0:
+            return y
+        nb = lib().nvfp4_matmul_workspace_bytes(M, self.K)
+        ws = torch.empty(nb, dtype=torch.uint8, device=x.device)   # the allocator's blocks are 512-byte aligned
+        _check("nvfp4_matmul",
+               lib().nvfp4_matmul(C.byref(self.desc), x.data_ptr(), _TYPES[x.dtype], x.stride(0), M, y.data_ptr(),
+                                  _TYPES[y.dtype], y.stride(0), ws.data_ptr(), nb, self.error.data_ptr(), _stream(stream)))
+        _keep_for(stream, x, y, ws, self.packed, self.g)
+        return y
+
+    __call__ = forward
+
+    def device_error(self) -> int:
+        """Read and clear the device error word (synchronises)."""
+        err = int(self.error.item())
+        if err:
+            self.error.zero_()
+        return err
 
 
 def _logits_desc(logits: torch.Tensor, temperature: float, row_of: torch.Tensor | None,

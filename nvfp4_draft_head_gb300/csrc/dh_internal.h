@@ -132,6 +132,25 @@ struct DistillArgs {
 enum DistillMode { kDistillForward, kDistillBoth, kDistillBackward };
 cudaError_t launch_distill(DistillArgs a, int type, DistillMode mode, cudaStream_t s);
 
+// Many-token NVFP4 x NVFP4 product (dh_matmul.cu).
+struct MatmulArgs {
+    const uint8_t* packed;   // weight blocks
+    const float* g;          // weight scale
+    int N, K, M;
+    const void* x;
+    int x_type;
+    long long ldx;
+    void* y;
+    int y_type;
+    long long ldy;
+    void* ws;
+    unsigned int* error;     // device error word or null
+};
+size_t matmul_packed_bytes(int N, int K);
+size_t matmul_workspace_bytes(int M, int K);
+cudaError_t launch_matmul_pack(const uint8_t* q, const uint8_t* sf, int N, int K, uint8_t* out, cudaStream_t s);
+cudaError_t launch_matmul(const MatmulArgs& m, cudaStream_t s);
+
 // row_of[idx[i]] = i for i < n, -1 elsewhere.
 cudaError_t launch_row_map(const int32_t* idx, int n, int32_t* row_of, int V, cudaStream_t s);
 

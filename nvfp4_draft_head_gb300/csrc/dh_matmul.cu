@@ -1,0 +1,430 @@
+// NVFP4 x NVFP4 product of many tokens (W4A4): y = x W'^T with the activations
+// quantised to NVFP4 per token on the fly.
+//
+//   g_m = max(max_k |x_mk|, 1e-12) / 2688,  s = E4M3_RNE(bamax / (6 g_m)) per
+//   block of 16, code = E2M1_RNE(clamp(x / fp32(dec(s) g_m), +-6)): the weights'
+//   recipe (dh_quantize.cu) with one global scale per token, so a token's
+//   result does not depend on the others in the batch;
+//   y_mn = g g_m sum_blocks s_mb s_nb sum_16 c_mk c_nk, accumulated in 32 bits.
+//
+// Operand layout ("blocks"): 128 rows x 256 k = 16,384 bytes of codes (rows of
+// 128 bytes, 16-byte pieces of row r permuted by XOR with r % 8: the 128-byte
+// swizzle that the tensor core reads) followed by 2,048 bytes of scales (for
+// each 64-wide k-step 512 bytes, [row % 32][row / 32][4 blocks]: the order in
+// which one copy moves them to tensor memory). Blocks are ordered [rows / 128]
+// [k / 256], rows and k padded with zeros, so a tile's operands for one k-stage are
+// contiguous and move with plain bulk copies; no tensor map is needed. Weights are
+// packed once (nvfp4_pack_matmul); the activations' quantiser writes its codes
+// straight into blocks.
+//
+// Product kernel: persistent, one CTA per SM; output tiles of 128 tokens x TN
+// weight rows. One thread streams blocks into a ring of shared-memory stages,
+// one issues the scale copies and the matrix instructions (kind::mxf4nvf4,
+// block 16), four warps read the accumulators from tensor memory, scale,
+// round once and store.
+#include <cfloat>
+
+#include "../../include/drafthead.h"
+#include "dh_internal.h"
+#include "dh_rows.cuh"
+#include "dh_tcgen05.cuh"
+
+namespace dh {
+namespace mm {
+
+constexpr int kRows = 128;                       // rows of a block
+constexpr int kStageK = 256;                     // k of a block
+constexpr int kCodes = kRows * kStageK / 2;      // 16,384
+constexpr int kScales = kRows * kStageK / 16;    // 2,048
+constexpr int kBlock = kCodes + kScales;         // 18,432
+
+__host__ __device__ inline int blocks_of(int n, int per) { return (n + per - 1) / per; }
+
+// Byte offsets inside a block: 16-byte piece p (32 codes) of row r, and the
+// scale of its 16-element block b (0..15).
+__device__ __forceinline__ int code_offset(int r, int p) { return r * 128 + ((p ^ (r & 7)) << 4); }
+__device__ __forceinline__ int scale_offset(int r, int b) {
+    return kCodes + (b >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (b & 3);
+}
+
+// ---------------------------------------------------------------- packing ----
+
+// One thread per (row, 32-wide piece): its codes and two scales, zeros beyond
+// N rows or K columns (K % 16 == 0).
+__global__ void pack_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sf, int N, int K, uint8_t* __restrict__ out) {
+    const int nk = blocks_of(K, kStageK), per_row = nk * (kStageK / 32);
+    const size_t total = static_cast<size_t>(blocks_of(N, kRows)) * kRows * per_row;
+    for (size_t i = blockIdx.x * static_cast<size_t>(blockDim.x) + threadIdx.x; i < total;
+         i += static_cast<size_t>(gridDim.x) * blockDim.x) {
+        const size_t row = i / per_row;
+        const int piece = static_cast<int>(i % per_row);
+        uint2 lo = make_uint2(0, 0), hi = make_uint2(0, 0);
+        uint32_t s0 = 0, s1 = 0;
+        const int k = piece * 32;
+        if (row < static_cast<size_t>(N)) {
+            const uint8_t* src = q + row * (K / 2) + k / 2;
+            const uint8_t* s = sf + row * (K / 16) + k / 16;
+            if (k < K) {
+                lo = *reinterpret_cast<const uint2*>(src);
+                s0 = s[0];
+            }
+            if (k + 16 < K) {
+                hi = *reinterpret_cast<const uint2*>(src + 8);
+                s1 = s[1];
+            }
+        }
+        uint8_t* blk = out + ((row / kRows) * nk + piece / 8) * kBlock;
+        const int r = static_cast<int>(row % kRows), p = piece % 8;
+        *reinterpret_cast<uint4*>(blk + code_offset(r, p)) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        *reinterpret_cast<uint16_t*>(blk + scale_offset(r, 2 * p)) = static_cast<uint16_t>(s0 | (s1 << 8));
+    }
+}
+
+// ------------------------------------------------------------ quantisation ----
+
+constexpr int kQThreads = 128;
+
+__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// 16 elements at p (alignment of the element type only when !VEC), as floats.
+template <class T, bool VEC>
+__device__ __forceinline__ void load16(const T* p, float (&x)[16]) {
+    if constexpr (VEC) {
+        constexpr int kVec = rows::Elem<T>::kVec;
+#pragma unroll
+        for (int i = 0; i < 16 / kVec; ++i)
+            rows::Elem<T>::unpack(*reinterpret_cast<const uint4*>(p + i * kVec), reinterpret_cast<float(&)[kVec]>(x[i * kVec]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = rows::Elem<T>::load(p + i);
+    }
+}
+
+// One CTA per token: the row's largest magnitude (as bits, so that NaN and
+// infinities come out on top), then codes and scales, one 32-wide piece per thread.
+// A row with a value that is not finite gets the scale NaN and zero codes:
+// its whole result is NaN.
+template <class T, bool VEC>
+__global__ void __launch_bounds__(kQThreads) quantize_kernel(const T* __restrict__ x, long long ldx, int K, uint8_t* __restrict__ out,
+                                                             float* __restrict__ scale) {
+    const int m = blockIdx.x, nk = blocks_of(K, kStageK), nb = K / 16;
+    const T* row = x + static_cast<size_t>(m) * ldx;
+    uint32_t top = 0;
+    for (int b = threadIdx.x; b < nb; b += kQThreads) {
+        float v[16];
+        load16<T, VEC>(row + b * 16, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    }
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    __shared__ uint32_t s_top[kQThreads / 32];
+    if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = top;
+    __syncthreads();
+    top = max(max(s_top[0], s_top[1]), max(s_top[2], s_top[3]));
+    const bool finite = top < 0x7F800000u;
+    const float g = finite ? __fdiv_rn(fmaxf(__uint_as_float(top), 1e-12f), 2688.0f) : __uint_as_float(0x7FC00000u);
+    const float den = __fmul_rn(6.0f, g);
+    if (threadIdx.x == 0) scale[m] = g;
+    uint8_t* blk0 = out + static_cast<size_t>(m / kRows) * nk * kBlock;
+    const int r = m % kRows;
+    for (int piece = threadIdx.x; piece < nk * 8; piece += kQThreads) {
+        uint32_t code[4] = {0, 0, 0, 0}, sc[2] = {0, 0};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int b = piece * 2 + h;
+            if (b >= nb || !finite) continue;
+            float v[16];
+            load16<T, VEC>(row + b * 16, v);
+            float bmax = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) bmax = fmaxf(bmax, fabsf(v[i]));
+            sc[h] = static_cast<uint32_t>(__nv_cvt_float_to_fp8(__fdiv_rn(bmax, den), __NV_SATFINITE, __NV_E4M3));
+            const float d = __fmul_rn(__half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(sc[h]), __NV_E4M3))), g);
+            if (d == 0.0f) continue;   // zeros (their sign does not matter to a sum of products)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                code[2 * h + i / 4] |= e2m1x2(__fdiv_rn(v[2 * i], d), __fdiv_rn(v[2 * i + 1], d)) << (8 * (i % 4));
+        }
+        uint8_t* blk = blk0 + static_cast<size_t>(piece / 8) * kBlock;
+        *reinterpret_cast<uint4*>(blk + code_offset(r, piece % 8)) = make_uint4(code[0], code[1], code[2], code[3]);
+        *reinterpret_cast<uint16_t*>(blk + scale_offset(r, 2 * (piece % 8))) = static_cast<uint16_t>(sc[0] | (sc[1] << 8));
+    }
+}
+
+// ----------------------------------------------------------------- product ----
+
+struct Args {
+    const uint8_t* a;       // activation blocks
+    const uint8_t* b;       // weight blocks
+    const float* ga;        // [M] token scales
+    const float* gb;        // weight scale
+    void* y;
+    long long ldy;
+    int M, N, nk;           // nk: k-stages
+    int tiles_m, tiles_n;
+    unsigned int* error;    // DH_DEVERR_* word or null
+};
+
+constexpr int kEpiWarps = 4;
+constexpr int kThreads = 32 * (kEpiWarps + 2);
+
+template <int TN>
+struct Cfg {
+    static constexpr int kNB = TN / kRows;                        // weight blocks per tile
+    static constexpr int kStageBytes = kBlock * (1 + kNB);
+    static constexpr int kStages = (227 * 1024 - 1024 - 512) / kStageBytes;   // 227 KB less alignment and barriers
+    static constexpr int kSmem = kStages * kStageBytes + 1024;    // + alignment to 1,024
+    // tensor-memory columns: accumulators, then per parity of the stage the scales of A and B
+    static constexpr int kSfA = TN;
+    static constexpr int kSfB = TN + 2 * 16;
+    static constexpr int kCols = 512;
+    static_assert(kSfB + 2 * 16 * kNB <= kCols, "tensor memory");
+};
+
+struct Sync {
+    uint64_t full[8], empty[8], acc_full, acc_empty;
+    uint32_t tmem;
+    unsigned int abort;
+};
+
+template <class TY> struct Out;
+template <> struct Out<float> {
+    __device__ static void store16(float* p, const float (&v)[16], bool vec) {
+        if (vec) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(p + 4 * i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) p[i] = v[i];
+        }
+    }
+};
+template <class T2>
+struct Out {
+    __device__ static void store16(T2* p, const float (&v)[16], bool vec) {
+        if (vec) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                *reinterpret_cast<uint4*>(p + 8 * i) = rows::Elem<T2>::pack(reinterpret_cast<const float(&)[8]>(v[8 * i]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) p[i] = rows::Elem<T2>::store(v[i]);
+        }
+    }
+};
+
+// A bounded wait that gives up at once when another role has.
+__device__ __forceinline__ bool wait_or_abort(Sync& sy, uint64_t* bar, uint32_t parity, const Args& a) {
+    if (mbar_test(bar, parity)) return true;
+    for (int i = 0; i < 64; ++i) {
+        if (mbar_wait(bar, parity, kWaitLimit / 64)) return true;
+        if (*const_cast<volatile unsigned int*>(&sy.abort) != 0u) return false;
+    }
+    *const_cast<volatile unsigned int*>(&sy.abort) = 1u;
+    if (a.error != nullptr) atomicOr(a.error, kDevErrTimeout);
+    return false;
+}
+
+template <class TY, int TN>
+__global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
+    using C = Cfg<TN>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Sync sy;
+    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&sy.full[i], 1);
+            mbar_init(&sy.empty[i], 1);
+        }
+        mbar_init(&sy.acc_full, 1);
+        mbar_init(&sy.acc_empty, kEpiWarps);
+        mbar_init_fence();
+        sy.abort = 0u;
+    }
+    __syncwarp();
+    if (warp == 0) tc::tmem_alloc(&sy.tmem, C::kCols);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = sy.tmem;
+    const int tiles = a.tiles_m * a.tiles_n;
+
+    if (warp == kEpiWarps && lane == 0) {
+        // producer: the blocks of every k-stage of every tile of this CTA
+        uint64_t keep, once;
+        asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+        asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(once));
+        uint32_t it = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+            const int tm = tile % a.tiles_m, tn = tile / a.tiles_m;
+            const int nb = min(C::kNB, blocks_of(a.N, kRows) - tn * C::kNB);
+            for (int k = 0; k < a.nk; ++k, ++it) {
+                const uint32_t s = it % C::kStages, use = it / C::kStages;
+                if (use > 0 && !(ok = wait_or_abort(sy, &sy.empty[s], (use - 1) & 1, a))) break;
+                uint8_t* st = smem + s * C::kStageBytes;
+                mbar_arrive_expect_tx(&sy.full[s], static_cast<uint32_t>(kBlock * (1 + nb)));
+                bulk_g2s(st, a.a + (static_cast<size_t>(tm) * a.nk + k) * kBlock, kBlock, &sy.full[s], keep);
+                for (int j = 0; j < nb; ++j) {   // codes of the weight blocks side by side, then their scales
+                    const uint8_t* src = a.b + (static_cast<size_t>(tn * C::kNB + j) * a.nk + k) * kBlock;
+                    bulk_g2s(st + kBlock + j * kCodes, src, kCodes, &sy.full[s], once);
+                    bulk_g2s(st + kBlock + C::kNB * kCodes + j * kScales, src + kCodes, kScales, &sy.full[s], once);
+                }
+            }
+        }
+        // on an abort, let the copies in flight land before the CTA ends (bounded)
+        if (!ok) {
+            for (uint32_t b = it > static_cast<uint32_t>(C::kStages) ? it - C::kStages : 0; b < it; ++b)
+                mbar_wait(&sy.full[b % C::kStages], (b / C::kStages) & 1, kWaitLimit / 64);
+        }
+    } else if (warp == kEpiWarps + 1 && lane == 0) {
+        // issuer: scale copies and matrix instructions
+        constexpr uint32_t kIdesc = tc::idesc_nvf4(kRows, TN);
+        uint32_t it = 0, n = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, ++n) {
+            if (n > 0 && !(ok = wait_or_abort(sy, &sy.acc_empty, (n - 1) & 1, a))) break;
+            tc::fence_after_sync();
+            for (int k = 0; k < a.nk; ++k, ++it) {
+                const uint32_t s = it % C::kStages;
+                if (!(ok = wait_or_abort(sy, &sy.full[s], (it / C::kStages) & 1, a))) break;
+                tc::fence_after_sync();
+                const uint32_t st = smem_u32(smem + s * C::kStageBytes);
+                const uint32_t sfa = tmem + C::kSfA + (it & 1) * 16, sfb = tmem + C::kSfB + (it & 1) * 16 * C::kNB;
+                const uint32_t b_sc = st + kBlock + C::kNB * kCodes;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    tc::copy_scales(sfa + 4 * j, tc::desc_scales(st + kCodes + 512 * j));
+#pragma unroll
+                    for (int b = 0; b < C::kNB; ++b)
+                        tc::copy_scales(sfb + 4 * (C::kNB * j + b), tc::desc_scales(b_sc + b * kScales + 512 * j));
+                }
+                const uint64_t da = tc::desc_operand(st), db = tc::desc_operand(st + kBlock);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)   // 64 of k: 32 bytes of the 128-byte rows
+                    tc::mma_nvf4(tmem, da + 2 * j, db + 2 * j, kIdesc, sfa + 4 * j, sfb + 4 * C::kNB * j, k > 0 || j > 0);
+                tc::commit(&sy.empty[s]);
+            }
+            if (ok) tc::commit(&sy.acc_full);
+        }
+        if (!ok) {   // let the issued instructions finish before tensor memory is freed (bounded)
+            tc::commit(&sy.acc_full);
+            mbar_wait(&sy.acc_full, n & 1, kWaitLimit / 64);
+        }
+    } else if (warp < kEpiWarps) {
+        const float gb = __ldg(a.gb);
+        const bool vec = (reinterpret_cast<uintptr_t>(a.y) & 15u) == 0 && (a.ldy * static_cast<long long>(sizeof(TY))) % 16 == 0;
+        uint32_t n = 0;
+        for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++n) {
+            const int m = (tile % a.tiles_m) * kRows + threadIdx.x, n0 = (tile / a.tiles_m) * TN;
+            const float g = m < a.M ? a.ga[m] * gb : 0.0f;
+            const bool ok = wait_or_abort(sy, &sy.acc_full, n & 1, a);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            tc::fence_after_sync();
+            TY* row = static_cast<TY*>(a.y) + static_cast<size_t>(m) * a.ldy + n0;
+            const int cols = min(TN, a.N - n0);
+            for (int c = 0; c < cols; c += 32) {
+                uint32_t r[32];
+                __syncwarp();
+                tc::tmem_load32(tmem + (static_cast<uint32_t>(warp) << 21) + c, r);
+                tc::tmem_load_wait();
+                if (m < a.M) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float v[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[16 * h + i]) * g;
+                        Out<TY>::store16(row + c + 16 * h, v, vec);
+                    }
+                }
+            }
+            tc::fence_before_sync();
+            if (lane == 0) mbar_arrive(&sy.acc_empty);
+        }
+    }
+    __syncwarp();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 0) tc::tmem_free(tmem, C::kCols);
+}
+
+template <class TY, int TN>
+static cudaError_t launch_product(Args a, cudaStream_t s) {
+    using C = Cfg<TN>;
+    const int sms = sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    a.tiles_n = blocks_of(a.N, TN);
+    const long long tiles = static_cast<long long>(a.tiles_m) * a.tiles_n;
+    const cudaError_t e = cudaFuncSetAttribute(product_kernel<TY, TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    product_kernel<TY, TN><<<static_cast<unsigned>(tiles < sms ? tiles : sms), kThreads, C::kSmem, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <class T>
+static cudaError_t launch_quantize(const void* x, long long ldx, int M, int K, uint8_t* out, float* scale, cudaStream_t s) {
+    const bool vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && (M == 1 || (ldx * static_cast<long long>(sizeof(T))) % 16 == 0);
+    if (vec) quantize_kernel<T, true><<<M, kQThreads, 0, s>>>(static_cast<const T*>(x), ldx, K, out, scale);
+    else quantize_kernel<T, false><<<M, kQThreads, 0, s>>>(static_cast<const T*>(x), ldx, K, out, scale);
+    return cudaGetLastError();
+}
+
+template <class TY>
+static cudaError_t launch_tiles(const Args& a, cudaStream_t s) {
+    // wide tiles read fewer operand bytes per product; narrow ones spread a small product over more SMs
+    const long long wide = static_cast<long long>(a.tiles_m) * blocks_of(a.N, 256);
+    return wide >= sm_count() ? launch_product<TY, 256>(a, s) : launch_product<TY, 128>(a, s);
+}
+
+}  // namespace mm
+
+size_t matmul_packed_bytes(int N, int K) {
+    return static_cast<size_t>(mm::blocks_of(N, mm::kRows)) * mm::blocks_of(K, mm::kStageK) * mm::kBlock;
+}
+
+size_t matmul_workspace_bytes(int M, int K) {
+    return matmul_packed_bytes(M, K) + (static_cast<size_t>(M) * sizeof(float) + 255) / 256 * 256;
+}
+
+cudaError_t launch_matmul_pack(const uint8_t* q, const uint8_t* sf, int N, int K, uint8_t* out, cudaStream_t s) {
+    const size_t total = matmul_packed_bytes(N, K) / mm::kBlock * mm::kRows * 8;
+    const int sms = sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    const size_t want = (total + 255) / 256, cap = static_cast<size_t>(sms) * 8;
+    mm::pack_kernel<<<static_cast<unsigned>(want < cap ? want : cap), 256, 0, s>>>(q, sf, N, K, out);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_matmul(const MatmulArgs& m, cudaStream_t s) {
+    uint8_t* blocks = static_cast<uint8_t*>(m.ws);
+    float* scale = reinterpret_cast<float*>(blocks + matmul_packed_bytes(m.M, m.K));
+    cudaError_t e = m.x_type == DH_T_BF16  ? mm::launch_quantize<__nv_bfloat16>(m.x, m.ldx, m.M, m.K, blocks, scale, s)
+                    : m.x_type == DH_T_F16 ? mm::launch_quantize<__half>(m.x, m.ldx, m.M, m.K, blocks, scale, s)
+                                           : mm::launch_quantize<float>(m.x, m.ldx, m.M, m.K, blocks, scale, s);
+    if (e != cudaSuccess) return e;
+    mm::Args a = {};
+    a.a = blocks;
+    a.b = m.packed;
+    a.ga = scale;
+    a.gb = m.g;
+    a.y = m.y;
+    a.ldy = m.ldy;
+    a.M = m.M;
+    a.N = m.N;
+    a.nk = mm::blocks_of(m.K, mm::kStageK);
+    a.tiles_m = mm::blocks_of(m.M, mm::kRows);
+    a.error = m.error;
+    switch (m.y_type) {
+        case DH_T_BF16: return mm::launch_tiles<__nv_bfloat16>(a, s);
+        case DH_T_F16: return mm::launch_tiles<__half>(a, s);
+        default: return mm::launch_tiles<float>(a, s);
+    }
+}
+
+}  // namespace dh
