@@ -28,6 +28,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from typing import NamedTuple
 
 import numpy as np
@@ -83,6 +84,11 @@ class dh_logits_t(C.Structure):
                 ("temperature", C.c_float), ("row_of", C.c_void_p), ("V", C.c_int), ("idx", C.c_void_p)]
 
 
+# a dh_logits_t as bytes: built once per call, in a sixth of the time of the ctypes structure
+_pack_logits = struct.Struct("@PiiiqfPiP").pack
+assert struct.calcsize("@PiiiqfPiP") == C.sizeof(dh_logits_t)
+
+
 class dh_matmul_t(C.Structure):
     _fields_ = [("N", C.c_int), ("K", C.c_int), ("packed", C.c_void_p), ("scale", C.c_void_p)]
 
@@ -125,11 +131,11 @@ def lib():
         L.draft_head_top_keys.argtypes = [C.POINTER(dh_head_t), P, I, P, P, S, P]
         L.draft_head_keys_to_ids.argtypes = [P, I, P, P, P]
         L.draft_head_static_read_device_error.argtypes = [P, P]
-        LG = C.POINTER(dh_logits_t)
+        # (a dh_logits_t as its bytes, or by reference)
         L.draft_head_row_map.argtypes = [P, I, P, I, P]
-        L.draft_head_token_logprobs.argtypes = [LG, P, I, P, P, P, I, P, P, P]
-        L.draft_head_distill.argtypes = [LG, P, P, I, I, P, P, P, P, C.c_int64, P]
-        L.draft_head_distill_backward.argtypes = [LG, P, P, I, I, P, P, P, C.c_int64, P]
+        L.draft_head_token_logprobs.argtypes = [P, P, I, P, P, P, I, P, P, P]
+        L.draft_head_distill.argtypes = [P, P, P, I, I, P, P, P, P, C.c_int64, P]
+        L.draft_head_distill_backward.argtypes = [P, P, P, I, I, P, P, P, C.c_int64, P]
         L.nvfp4_matmul_packed_bytes.argtypes = [I, I]
         L.nvfp4_matmul_packed_bytes.restype = S
         L.nvfp4_pack_matmul.argtypes = [P, P, I, I, P, P]
@@ -493,6 +499,13 @@ def _keep_for(stream, *tensors) -> None:
                 t.record_stream(stream)
 
 
+def _stream_of(t: torch.Tensor, stream) -> int:
+    """cudaStream_t of `stream`, or of the current stream of t's device."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return _stream(stream)
+
+
 class NVFP4Matmul:
     """An NVFP4 weight for many-token products: forward(x) = x W'^T with x
     quantised to NVFP4 per token (W4A4) and fp32 accumulation. q uint8 [N, K/2],
@@ -517,6 +530,7 @@ class NVFP4Matmul:
                lib().nvfp4_pack_matmul(q.data_ptr(), sf.data_ptr(), self.N, self.K, self.packed.data_ptr(), _stream(stream)))
         self.error = torch.zeros(1, dtype=torch.int32, device=q.device)
         self.desc = dh_matmul_t(self.N, self.K, self.packed.data_ptr(), g.data_ptr())
+        self.desc_ref, self.error_ptr = C.byref(self.desc), self.error.data_ptr()
         _keep_for(stream, q, sf, g, self.packed, self.error)
 
     @classmethod
@@ -543,11 +557,12 @@ class NVFP4Matmul:
             raise ValueError(f"y must be a [{M}, {self.N}] bfloat16, float16 or float32 tensor with contiguous rows")
         if M == 0:
             return y
-        nb = lib().nvfp4_matmul_workspace_bytes(M, self.K)
+        L = lib()
+        nb = L.nvfp4_matmul_workspace_bytes(M, self.K)
         ws = torch.empty(nb, dtype=torch.uint8, device=x.device)   # the allocator's blocks are 512-byte aligned
         _check("nvfp4_matmul",
-               lib().nvfp4_matmul(C.byref(self.desc), x.data_ptr(), _TYPES[x.dtype], x.stride(0), M, y.data_ptr(),
-                                  _TYPES[y.dtype], y.stride(0), ws.data_ptr(), nb, self.error.data_ptr(), _stream(stream)))
+               L.nvfp4_matmul(self.desc_ref, x.data_ptr(), _TYPES[x.dtype], x.stride(0), M, y.data_ptr(),
+                                  _TYPES[y.dtype], y.stride(0), ws.data_ptr(), nb, self.error_ptr, _stream_of(x, stream)))
         _keep_for(stream, x, y, ws, self.packed, self.g)
         return y
 
@@ -562,20 +577,24 @@ class NVFP4Matmul:
 
 
 def _logits_desc(logits: torch.Tensor, temperature: float, row_of: torch.Tensor | None,
-                 idx: torch.Tensor | None = None) -> dh_logits_t:
-    if logits.dim() != 2 or logits.dtype not in _TYPES or not logits.is_cuda:
+                 idx: torch.Tensor | None = None) -> bytes:
+    """The dh_logits_t of logits [M, C], as bytes."""
+    dtype = _TYPES.get(logits.dtype)
+    if logits.dim() != 2 or dtype is None or not logits.is_cuda:
         raise ValueError("logits must be a [M, C] bfloat16, float16 or float32 CUDA tensor")
     M, n = logits.shape
     ld, step = logits.stride()
     if (step != 1 and n > 1) or (M > 1 and ld < n):
         raise ValueError("logits rows must be contiguous and must not overlap")
-    _vector(row_of, "row_of", torch.int32, None, logits.device)
+    V = 0
+    if row_of is not None:
+        _vector(row_of, "row_of", torch.int32, None, logits.device)
+        V = row_of.numel()
     if idx is not None:
         _vector(idx, "idx", torch.int32, None, logits.device)
         if idx.numel() < n:
             raise ValueError(f"idx must hold the ids of all {n} columns")
-    return dh_logits_t(logits.data_ptr(), _TYPES[logits.dtype], M, n, ld, temperature, _ptr(row_of),
-                       0 if row_of is None else row_of.numel(), _ptr(idx))
+    return _pack_logits(logits.data_ptr(), dtype, M, n, ld, temperature, _ptr(row_of) or 0, V, _ptr(idx) or 0)
 
 
 def draft_head_row_map(idx: torch.Tensor, n_kept: int, V: int, stream=None) -> torch.Tensor:
@@ -610,7 +629,7 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, top
     column has log-probability -inf; alternatives past the last logit above -inf
     have id -1. See draft_head_token_logprobs."""
     d = _logits_desc(logits, temperature, row_of, idx)
-    M, dev = d.M, logits.device
+    M, dev, f32 = logits.shape[0], logits.device, torch.float32
     G = 0
     if tokens is not None:
         if tokens.dim() not in (1, 2) or tokens.shape[0] != M:
@@ -619,22 +638,22 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, top
         G = 1 if tokens.dim() == 1 else tokens.shape[1]
     if not 0 <= top_k <= DH_MAX_TOP:
         raise ValueError(f"top_k must lie in 0 .. {DH_MAX_TOP}")
-    stats = torch.empty((2, M), dtype=torch.float32, device=dev)
-    logp = None if tokens is None else torch.empty(tokens.shape, dtype=torch.float32, device=dev)
-    top_logp = torch.empty((M, top_k), dtype=torch.float32, device=dev)
+    logp = None if tokens is None else torch.empty(tokens.shape, dtype=f32, device=dev)
+    entropy, lse = torch.empty(M, dtype=f32, device=dev), torch.empty(M, dtype=f32, device=dev)
+    top_logp = torch.empty((M, top_k), dtype=f32, device=dev)
     top_ids = torch.empty((M, top_k), dtype=torch.int32, device=dev)
-    entropy, lse = stats.unbind()
     if M > 0:
         _check("draft_head_token_logprobs",
-               lib().draft_head_token_logprobs(C.byref(d), _ptr(tokens), G, _ptr(logp), stats.data_ptr(),
-                                               stats.data_ptr() + 4 * M, top_k, top_logp.data_ptr(),
-                                               top_ids.data_ptr(), _stream(stream)))
-        _keep_for(stream, logits, tokens, idx, row_of, stats, logp, top_logp, top_ids)
+               lib().draft_head_token_logprobs(d, _ptr(tokens), G, _ptr(logp), entropy.data_ptr(), lse.data_ptr(), top_k,
+                                               top_logp.data_ptr(), top_ids.data_ptr(), _stream_of(logits, stream)))
+        if stream is not None:
+            _keep_for(stream, logits, tokens, idx, row_of, logp, entropy, lse, top_logp, top_ids)
     return TokenLogprobs(logp, entropy, lse, top_logp, top_ids)
 
 
 def _teacher(logits, ids, val):
-    if ids.dim() != 2 or ids.shape[0] != logits.shape[0] or val.shape != ids.shape:
+    shape = ids.shape
+    if len(shape) != 2 or shape[0] != logits.shape[0] or val.shape != shape:
         raise ValueError(f"teacher ids and logits must be [{logits.shape[0]}, K] tensors")
     _vector(ids, "teacher ids", torch.int32, None, logits.device)
     if val.dtype not in _TYPES:
@@ -652,7 +671,7 @@ def _gradient(logits: torch.Tensor, out: torch.Tensor | None) -> torch.Tensor:
         ld = logits.stride(0)
         if not n <= ld <= 2 * n:     # one row, or rows far apart: whole 16-byte vectors per row
             ld = (n + 7) // 8 * 8
-        return torch.empty((M, ld), dtype=logits.dtype, device=logits.device)[:, :n]
+        return torch.empty_strided((M, n), (ld, 1), dtype=logits.dtype, device=logits.device)
     if out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device or \
             (out.stride(1) != 1 and n > 1) or (M > 1 and out.stride(0) < n):
         raise ValueError("the gradient must be a tensor of the logits' shape, type and device with contiguous rows")
@@ -670,13 +689,13 @@ def distill_topk(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits
     out. dlogits may be the logits tensor itself. See draft_head_distill."""
     d = _logits_desc(logits, temperature, row_of)
     K, vt = _teacher(logits, teacher_ids, teacher_logits)
-    _vector(weights, "weights", torch.float32, d.M, logits.device)
+    _vector(weights, "weights", torch.float32, logits.shape[0], logits.device)
     dz = _gradient(logits, dlogits)
-    loss = torch.empty(d.M, dtype=torch.float32, device=logits.device)
-    if d.M > 0:
+    loss = torch.empty(logits.shape[0], dtype=torch.float32, device=logits.device)
+    if logits.shape[0] > 0:
         _check("draft_head_distill",
-               lib().draft_head_distill(C.byref(d), teacher_ids.data_ptr(), teacher_logits.data_ptr(), vt, K, _ptr(weights),
-                                        loss.data_ptr(), None, dz.data_ptr(), dz.stride(0), _stream(stream)))
+               lib().draft_head_distill(d, teacher_ids.data_ptr(), teacher_logits.data_ptr(), vt, K, _ptr(weights),
+                                        loss.data_ptr(), None, dz.data_ptr(), dz.stride(0), _stream_of(logits, stream)))
         _keep_for(stream, logits, teacher_ids, teacher_logits, weights, row_of, dz, loss)
     return loss, dz
 
@@ -688,14 +707,15 @@ def distill_topk_forward(logits: torch.Tensor, teacher_ids: torch.Tensor, teache
     student's normaliser for distill_topk_backward."""
     d = _logits_desc(logits, temperature, row_of)
     K, vt = _teacher(logits, teacher_ids, teacher_logits)
-    _vector(weights, "weights", torch.float32, d.M, logits.device)
-    out = torch.empty((2, d.M), dtype=torch.float32, device=logits.device)
-    if d.M > 0:
+    _vector(weights, "weights", torch.float32, logits.shape[0], logits.device)
+    M, dev = logits.shape[0], logits.device
+    loss, lse = torch.empty(M, dtype=torch.float32, device=dev), torch.empty(M, dtype=torch.float32, device=dev)
+    if logits.shape[0] > 0:
         _check("draft_head_distill",
-               lib().draft_head_distill(C.byref(d), teacher_ids.data_ptr(), teacher_logits.data_ptr(), vt, K, _ptr(weights),
-                                        out.data_ptr(), out.data_ptr() + 4 * d.M, None, 0, _stream(stream)))
-        _keep_for(stream, logits, teacher_ids, teacher_logits, weights, row_of, out)
-    return out.unbind()
+               lib().draft_head_distill(d, teacher_ids.data_ptr(), teacher_logits.data_ptr(), vt, K, _ptr(weights),
+                                        loss.data_ptr(), lse.data_ptr(), None, 0, _stream_of(logits, stream)))
+        _keep_for(stream, logits, teacher_ids, teacher_logits, weights, row_of, loss, lse)
+    return loss, lse
 
 
 def distill_topk_backward(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor, lse: torch.Tensor,
@@ -706,14 +726,14 @@ def distill_topk_backward(logits: torch.Tensor, teacher_ids: torch.Tensor, teach
     upstream gradient of each row's loss times the forward's weight."""
     d = _logits_desc(logits, temperature, row_of)
     K, vt = _teacher(logits, teacher_ids, teacher_logits)
-    _vector(lse, "lse", torch.float32, d.M, logits.device)
-    _vector(weights, "weights", torch.float32, d.M, logits.device)
+    _vector(lse, "lse", torch.float32, logits.shape[0], logits.device)
+    _vector(weights, "weights", torch.float32, logits.shape[0], logits.device)
     dz = _gradient(logits, dlogits)
-    if d.M > 0:
+    if logits.shape[0] > 0:
         _check("draft_head_distill_backward",
-               lib().draft_head_distill_backward(C.byref(d), teacher_ids.data_ptr(), teacher_logits.data_ptr(), vt, K,
+               lib().draft_head_distill_backward(d, teacher_ids.data_ptr(), teacher_logits.data_ptr(), vt, K,
                                                  lse.data_ptr(), _ptr(weights), dz.data_ptr(), dz.stride(0),
-                                                 _stream(stream)))
+                                                 _stream_of(logits, stream)))
         _keep_for(stream, logits, teacher_ids, teacher_logits, lse, weights, row_of, dz)
     return dz
 

@@ -10,17 +10,20 @@
 // entry in use has loss 0 and gradient 0. (d(log q_j)/dz_c = (delta_jc - q_c)/t
 // and sum p = 1 give the gradient.) Entries that name one column twice add up.
 //
-// One cluster of 1..8 CTAs per row. Every CTA takes the whole teacher row (one
-// entry per thread, its column and the student's logit there fetched before
-// the row is streamed), the statistics of its slice as in dh_rows.cuh, and
-// writes its slice of the gradient: first w t q everywhere, then, after a
-// barrier, the columns of the teacher's entries again with p taken off. The
-// sums are joined in a fixed order, so results repeat bit for bit. The gradient
-// may be written over the logits: a CTA reads every logit that it needs outside
-// its slice before the cluster barrier that precedes the first write.
+// Persistent clusters of 1..8 CTAs take the rows in turn. Every CTA takes the
+// whole teacher row (one entry per thread, its column looked up a row ahead and
+// the student's logit there fetched before the row is worked on), the statistics
+// of its slice as in dh_rows.cuh, and writes its slice of the gradient: first
+// w t q everywhere, then the columns of the teacher's entries again with p taken
+// off (after the next row's barrier, so that a row costs one barrier). The sums are joined in a fixed order, so results repeat
+// bit for bit. The gradient may be written over the logits: a CTA reads every
+// logit that it needs outside its slice before the cluster barrier that precedes
+// the first write.
 //
-// Bound: HBM. Loss and gradient together read the row twice; the second time
-// it comes from L2 (see the launcher).
+// Loss and gradient together stream every row twice; the second time it comes
+// from L2, where the rows in work (two per SM) fit.
+//
+// Bound: HBM (one read, and one write where there is a gradient).
 #include "../../include/drafthead.h"
 #include "dh_internal.h"
 #include "dh_rows.cuh"
@@ -28,35 +31,46 @@
 namespace dh {
 namespace rows {
 
-constexpr int kUnroll = 4;   // vectors in flight per thread
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kUnroll = 4;    // vectors per batch and thread
+constexpr int kDepth = 4;     // batches in flight: 64 KB per CTA
+constexpr int kPerSm = 3;     // CTAs per SM
 
 struct DistillSmem {
-    float warp[kWarps][3];
-    float teach[kWarps][3];
-    float cta[kMaxCluster][3];
-    float red[kWarps];
-    int col[kThreads];
-    float p[kThreads];
+    float warp[2][kWarps][3];
+    float plain[kWarps][3];
+    float teach[2][kWarps][3];
+    float cta[2][kMaxCluster][3];
+    float cta_plain[kMaxCluster][3];
+    int used[2][kWarps];
+    float red[2][kWarps];
+    alignas(16) int col[2][DH_MAX_TEACHER];
+    float p[2][DH_MAX_TEACHER];
 };
 
-// Plain (coherent) 16-byte load: the row may be overwritten by this kernel.
-__device__ __forceinline__ uint4 ld_v4(const void* p) {
-    uint4 r;
-    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
-    return r;
-}
 __device__ __forceinline__ void st_v4(void* p, const uint4& v) {
     asm volatile("st.global.v4.u32 [%0], {%1,%2,%3,%4};" :: "l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-__device__ __forceinline__ float block_sum(float x, float* buf) {
+// A vector of gradients, element by element where the rows of the gradient lie at
+// another offset from a 16-byte boundary than the logits'.
+template <class T>
+__device__ __forceinline__ void store_vec(T* p, const uint4& g, bool whole) {
+    if (whole) {
+        st_v4(p, g);
+    } else {
+        const uint32_t w[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
-    __syncthreads();
-    float r = 0.0f;
-    for (int w = 0; w < kWarps; ++w) r += buf[w];
-    return r;
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                reinterpret_cast<uint32_t*>(p)[i] = w[i];
+            } else {
+                reinterpret_cast<uint16_t*>(p)[2 * i] = static_cast<uint16_t>(w[i]);
+                reinterpret_cast<uint16_t*>(p)[2 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
+            }
+        }
+    }
 }
 
 // Element i of an array whose type is known at run time.
@@ -66,160 +80,238 @@ __device__ __forceinline__ float load_as(const void* p, size_t i, int type) {
     return static_cast<const float*>(p)[i];
 }
 
-template <class T, DistillMode MODE>
-__global__ void __launch_bounds__(kThreads, 2) distill_kernel(const DistillArgs a) {
+// E: teacher entries per thread.
+template <class T, DistillMode MODE, int E>
+__global__ void __launch_bounds__(kThreads, kPerSm) distill_kernel(const DistillArgs a) {
+    using St = Stream<T, kThreads, kUnroll, kDepth>;
     constexpr int kVec = Elem<T>::kVec;
     constexpr bool kGrad = MODE != kDistillForward, kStats = MODE != kDistillBackward;
+    extern __shared__ __align__(16) uint8_t ring[];
     __shared__ DistillSmem sm;
-    const unsigned rank = cluster_ctarank(), ncta = a.ncta;
-    const int row = blockIdx.x / ncta, tid = threadIdx.x;
-    if (ncta > 1) cluster_arrive_release();
-    const T* z = static_cast<const T*>(a.z) + static_cast<size_t>(row) * a.ld;
-    const Slice sl = make_slice(z, a.C, rank, ncta);
-    const int edge = edge_column(sl, a.C, rank, ncta);
+    const unsigned lg = a.lg, ncta = 1u << lg, rank = ncta > 1 ? cluster_ctarank() : 0u;
+    const int first = blockIdx.x >> lg, stride = gridDim.x >> lg, tid = threadIdx.x, warp = tid >> 5;
+    const int nt = min((a.K + 31) >> 5, kWarps);   // warps with teacher entries
+    const bool teacher = warp < nt;
+    static_assert(DH_MAX_TEACHER <= 2 * kThreads, "at most two teacher entries per thread");
     const float c = a.inv_t * kLog2e;
-    const float w = a.weight != nullptr ? __ldg(a.weight + row) : 1.0f;
-
-    // the teacher's entry of this thread
-    int col = -1;
-    float t = kNegInf, zt = kNegInf;
-    if (tid < a.K && w != 0.0f) {
-        const size_t at = static_cast<size_t>(row) * a.K + tid;
-        col = column_of(a.ids[at], a.row_of, a.V, a.C);
-        t = load_as(a.val, at, a.val_type);
-        if (col >= 0) zt = Elem<T>::load(z + col);
-    }
-    const bool used = col >= 0 && t != kNegInf && zt != kNegInf;
-    const bool some = __syncthreads_or(used);
-
-    Stat all = stat_empty();
-    if (kStats && (some || MODE == kDistillForward)) {
-        Stat st = stat_empty();
-        for (int v0 = sl.v0 + tid; v0 < sl.v1; v0 += kUnroll * kThreads) {
-            uint4 b[kUnroll];
+    St stream;
+    stream.start(static_cast<const T*>(a.z), a.ld, a.M, a.C, rank, lg, first, stride, ring, MODE == kDistillBoth ? 2 : 1);
+    IdAhead ahead[E];
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int v = v0 + u * kThreads;
-                b[u] = v < sl.v1 ? ld_v4(z + sl.head + static_cast<size_t>(v) * kVec) : neg_inf_vec<T>();
+    for (int e = 0; e < E; ++e) {
+        ahead[e] = {a.ids, a.row_of, a.K, a.V, a.C, a.M, stride, tid + e * kThreads, -1, -1, -1};
+        ahead[e].start(first);
+    }
+    if (ncta > 1) {   // every peer runs before its shared memory is written
+        cluster_arrive_release();
+        cluster_wait_acquire();
+    }
+    // the end of a row, after the barrier that follows its gradient
+    struct {
+        int col[E];       // the teacher's columns of this thread in this slice, or -1
+        float base[E];    // w t q there
+        float wt;         // w t
+        T* dz;
+        float loss_w;     // w t^2 (0: no entry in use)
+        int row;          // -1: none yet
+    } end = {};
+    end.row = -1;
+#pragma unroll
+    for (int e = 0; e < E; ++e) end.col[e] = -1;
+    const auto finish = [&](int turn) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            if (!kGrad || end.col[e] < 0) continue;
+            // one thread per column, the first entry that names it
+            const int col = end.col[e], entry = tid + e * kThreads;
+            float sum = 0.0f;
+            bool mine = true;
+            const int4* cols = reinterpret_cast<const int4*>(sm.col[turn]);
+            for (int j = 0; j < a.K; j += 4) {
+                const int4 q = cols[j >> 2];
+                if (q.x != col && q.y != col && q.z != col && q.w != col) continue;
+                for (int i = j; i < min(j + 4, a.K); ++i) {
+                    if (sm.col[turn][i] != col) continue;
+                    mine = mine && i >= entry;
+                    sum += sm.p[turn][i];
+                }
             }
-            float x[kUnroll * kVec];
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) Elem<T>::unpack(b[u], reinterpret_cast<float(&)[kVec]>(x[u * kVec]));
-            stat_add<false>(st, x, c);
+            if (mine) end.dz[col] = Elem<T>::store(end.base[e] - end.wt * sum);
         }
-        if (edge >= 0) stat_add1<false>(st, Elem<T>::load(z + edge), c);
-        all = stat_block<false>(st, c, sm.warp);
-    }
-    // every CTA of the cluster takes the same path here: `some` is the row's
-    if (kStats) {
-        all = stat_cluster<false>(all, c, sm.cta, rank, ncta);
-    } else if (ncta > 1) {
-        cluster_wait_acquire();
-        cluster_arrive_release();   // no CTA writes its slice before all have read theirs from it
-        cluster_wait_acquire();
-    }
-
-    // the teacher's distribution over the entries in use
-    float p = 0.0f, logp = 0.0f;
-    if (some) {
-        Stat ts = stat_empty();
-        if (used) stat_add1<false>(ts, t, c);
-        ts = stat_block<false>(ts, c, sm.teach);
-        if (used) {
-            const float d = (t - ts.m) * a.inv_t;
-            p = expf(d) / ts.s;
-            logp = d - logf(ts.s);
+        if (kStats && rank == 0 && tid == 0 && end.row >= 0) {
+            float loss = 0.0f;
+            if (end.loss_w != 0.0f)
+                for (int i = 0; i < nt; ++i) loss += sm.red[turn][i];
+            a.loss[end.row] = end.loss_w != 0.0f ? end.loss_w * loss : 0.0f;
         }
-    }
-
-    if (kStats && rank == 0) {
-        const float ln_s = logf(all.s);
-        if (MODE == kDistillForward && tid == 0 && a.lse != nullptr)
-            a.lse[row] = all.s == 0.0f ? kNegInf : all.m * a.inv_t + ln_s;
-        float loss = 0.0f;
-        if (some) {
-            // an entry whose probability underflows adds nothing
-            const float logq = (zt - all.m) * a.inv_t - ln_s;
-            loss = block_sum(used && p != 0.0f ? p * (logp - logq) : 0.0f, sm.red);
-        }
-        if (tid == 0) a.loss[row] = some ? w * a.t * a.t * loss : 0.0f;
-    }
-    if (!kGrad) return;
-
-    // dz = scale * 2^((z - m) c) with scale = w t / S; from a kept normaliser, w t e^(z / t - lse)
-    const float wt = w * a.t;
-    const float shift = kStats ? all.m : a.lse_in[row];
-    const float scale = !some ? 0.0f : kStats ? wt / all.s : wt;
-    const auto wtq = [&](float x) {
-        return scale * ex2(kStats ? (x - shift) * c : fmaf(x, a.inv_t, -shift) * kLog2e);
     };
-    T* dz = static_cast<T*>(a.dz) + static_cast<size_t>(row) * a.ld_dz;
-    const bool vec_out = ((reinterpret_cast<uintptr_t>(dz) ^ reinterpret_cast<uintptr_t>(z)) & 15u) == 0;
-    for (int v0 = sl.v0 + tid; v0 < sl.v1; v0 += kUnroll * kThreads) {
-        uint4 b[kUnroll];
-        if (some) {
+    uint32_t slot = 0;
+    int turn = 0;
+    const T* z = static_cast<const T*>(a.z) + static_cast<size_t>(first) * a.ld;
+    T* dz = static_cast<T*>(a.dz) + static_cast<size_t>(first) * a.ld_dz;
+    Slice sl = make_slice(z, a.C, rank, lg);
+    for (int row = first; row < a.M;
+         row += stride, turn ^= 1, z += static_cast<size_t>(stride) * a.ld, dz += static_cast<size_t>(stride) * a.ld_dz) {
+        if (!stream.alike) sl = make_slice(z, a.C, rank, lg);
+        const int edge = edge_column(sl, a.C, rank, ncta), batches = St::batches_of(sl);
+        const float w = a.weight != nullptr ? __ldg(a.weight + row) : 1.0f;
+        int col[E];
+        float t[E], zt[E], ze = kNegInf;
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int v = v0 + u * kThreads;
-                b[u] = v < sl.v1 ? ld_v4(z + sl.head + static_cast<size_t>(v) * kVec) : neg_inf_vec<T>();
+        for (int e = 0; e < E; ++e) {
+            col[e] = ahead[e].take(row);
+            t[e] = zt[e] = kNegInf;
+            if (col[e] >= 0) {
+                t[e] = load_as(a.val, static_cast<size_t>(row) * a.K + ahead[e].entry, a.val_type);
+                zt[e] = Elem<T>::load(z + col[e]);
             }
         }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int v = v0 + u * kThreads;
-            if (v >= sl.v1) break;
-            float x[kVec];
-            if (some) {
-                Elem<T>::unpack(b[u], x);
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) x[j] = wtq(x[j]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) x[j] = 0.0f;
-            }
-            T* out = dz + sl.head + static_cast<size_t>(v) * kVec;
-            if (vec_out) {
-                st_v4(out, Elem<T>::pack(x));
-            } else {
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) out[j] = Elem<T>::store(x[j]);
-            }
-        }
-    }
-    if (edge >= 0) dz[edge] = Elem<T>::store(some ? wtq(Elem<T>::load(z + edge)) : 0.0f);
-    if (!some) return;
+        if (edge >= 0) ze = Elem<T>::load(z + edge);
 
-    // the teacher's columns of this slice: one thread per column, the first entry that names it
-    if (tid < a.K) {
-        sm.col[tid] = used ? col : -1;
-        sm.p[tid] = p;
-    }
-    __syncthreads();   // also orders the stores above before those below
-    if (used && col >= sl.lo && col < sl.hi) {
-        float sum = 0.0f;
-        bool first = true;
-        for (int j = 0; j < a.K; ++j) {
-            if (sm.col[j] != col) continue;
-            first = first && j >= tid;
-            sum += sm.p[j];
+        // the statistics of the slice
+        Stat all = {a.floor, 0.0f, 0.0f};
+        if (kStats) {
+            for (int b = 0; b < batches; ++b) {
+                cp_async_wait<kDepth - 1>();
+                uint4 v[kUnroll];
+                stream.read(slot, sl, b, v);
+                stream.fetch();
+                slot = St::next(slot);
+                stat_add<T, false, kUnroll>(all, v, c, a.floor2);
+            }
+            if (edge >= 0) stat_add1<false>(all, ze, c, a.floor);
+            stat_leave(stat_warp<false, false>(all, c), sm.warp[turn]);
         }
-        if (first) dz[col] = Elem<T>::store(wtq(zt) - wt * sum);
+        // the teacher's entries in use, and the sums of their softmax (the student's
+        // logits there are in hand before any cluster barrier of this row)
+        bool used[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) used[e] = col[e] >= 0 && w != 0.0f && t[e] != kNegInf && zt[e] != kNegInf;
+        if (teacher) {
+            Stat ts = {-FLT_MAX, 0.0f, 0.0f};
+            bool any = false;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                if (used[e]) plain_add1<false>(ts, t[e], c);
+                any = any || used[e];
+            }
+            any = __any_sync(0xFFFFFFFFu, any);
+            stat_leave(stat_warp<false, true>(ts, c), sm.teach[turn]);
+            if ((tid & 31) == 0) sm.used[turn][warp] = any;
+        }
+        __syncthreads();
+        finish(turn ^ 1);
+        const int l = tid & 31;
+        const bool some = __any_sync(0xFFFFFFFFu, l < nt && sm.used[turn][l]);
+
+        // the statistics of the row
+        bool plain = false;
+        if (kStats) {
+            all = stat_gather<false, false>(kWarps, c, sm.warp[turn], a.floor);
+            all = stat_cluster<false, false>(all, c, sm.cta[turn], rank, ncta);
+            plain = !stat_fits(all.m, c, a.floor);
+            if (plain) {
+                float top;
+                all = plain_slice<T, false, kThreads>(z, sl, ze, c, sm.plain, top);
+                all = stat_cluster<false, true>(all, c, sm.cta_plain, rank, ncta);
+            }
+        } else if (ncta > 1) {   // no CTA writes its slice before all have read theirs from it
+            cluster_arrive_release();
+            cluster_wait_acquire();
+        }
+
+        const float ln_s = kStats ? logf(all.s) - (plain ? 0.0f : shift_rest(all.m, c) * kLn2) : 0.0f;
+        if (teacher && some) {
+            const Stat ts = stat_gather<false, true>(nt, c, sm.teach[turn], -FLT_MAX);
+            float part = 0.0f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                float p = 0.0f;
+                if (used[e]) {
+                    const float d = (t[e] - ts.m) * a.inv_t;
+                    p = expf(d) / ts.s;
+                    // an entry whose probability underflows adds nothing
+                    if (kStats && p != 0.0f) part += p * (d - logf(ts.s) - ((zt[e] - all.m) * a.inv_t - ln_s));
+                }
+                if (kGrad && ahead[e].entry < a.K) {
+                    sm.col[turn][ahead[e].entry] = used[e] ? col[e] : -1;
+                    sm.p[turn][ahead[e].entry] = p;
+                }
+            }
+            if (kStats) {
+                part = warp_sum(part);
+                if (l == 0) sm.red[turn][warp] = part;
+            }
+        }
+        if (MODE == kDistillForward && tid == 0 && rank == 0 && a.lse != nullptr)
+            a.lse[row] = all.s == 0.0f ? kNegInf : all.m * a.inv_t + ln_s;
+
+        const float wt = w * a.t;
+        if (kGrad) {
+            // w t q = scale * 2^(z c - mc), or 2^((z - m) c) where the plain form was needed,
+            // with scale = w t / s; from a kept normaliser, w t e^(z / t - lse)
+            const float lse = kStats ? 0.0f : a.lse_in[row];
+            const float scale = !some ? 0.0f : kStats ? wt / all.s : wt;
+            const float nmc = -shift_of(all.m, c);
+            const auto wtq = [&](float x) {
+                if (!kStats) return scale * ex2(fmaf(x, a.inv_t, -lse) * kLog2e);
+                return scale * ex2(plain ? (x - all.m) * c : fmaf(x, c, nmc));
+            };
+            const bool vec_out = ((reinterpret_cast<uintptr_t>(dz) ^ reinterpret_cast<uintptr_t>(z)) & 15u) == 0;
+            const uint64_t mul2 = kStats ? pack_f32x2(c, c) : pack_f32x2(a.inv_t, a.inv_t);
+            const uint64_t add2 = kStats ? pack_f32x2(nmc, nmc) : pack_f32x2(-lse, -lse), scale2 = pack_f32x2(scale, scale);
+            T* out = dz + sl.head + (static_cast<size_t>(sl.v0) + tid) * kVec;
+            for (int b = 0; b < batches; ++b, out += kUnroll * kThreads * kVec) {
+                cp_async_wait<kDepth - 1>();
+                uint4 v[kUnroll];
+                stream.read(slot, sl, b, v);
+                stream.fetch();
+                slot = St::next(slot);
+                const int n = sl.v1 - sl.v0 - b * (kUnroll * kThreads) - tid;   // vectors left from this one on
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) {
+                    float x[kVec];
+                    Elem<T>::unpack(v[u], x);
+                    if (!kStats || !plain) {
+#pragma unroll
+                        for (int j = 0; j < kVec; j += 2) {
+                            uint64_t y = fma_f32x2(pack_f32x2(x[j], x[j + 1]), mul2, add2);
+                            if (!kStats) y = mul_f32x2(y, pack_f32x2(kLog2e, kLog2e));
+                            float y0, y1;
+                            unpack_f32x2(y, y0, y1);
+                            unpack_f32x2(mul_f32x2(pack_f32x2(ex2(y0), ex2(y1)), scale2), x[j], x[j + 1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < kVec; ++j) x[j] = scale * ex2((x[j] - all.m) * c);
+                    }
+                    uint4 g = Elem<T>::pack(x);
+                    if (!some) g = make_uint4(0, 0, 0, 0);
+                    if (u * kThreads < n) store_vec<T>(out + u * (kThreads * kVec), g, vec_out);
+                }
+            }
+            if (edge >= 0) dz[edge] = Elem<T>::store(some ? wtq(ze) : 0.0f);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                end.col[e] = used[e] && col[e] >= sl.lo && col[e] < sl.hi ? col[e] : -1;
+                end.base[e] = wtq(zt[e]);
+            }
+            end.wt = wt;
+            end.dz = dz;
+        }
+        end.loss_w = some ? wt * a.t : 0.0f;
+        end.row = row;
     }
+    __syncthreads();
+    finish(turn ^ 1);
 }
 
 template <class T, DistillMode MODE>
 static cudaError_t launch(const DistillArgs& a, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.M) * a.ncta);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = a.ncta;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, distill_kernel<T, MODE>, a);
+    using St = Stream<T, kThreads, kUnroll, kDepth>;
+    const long long bytes = static_cast<long long>(a.C) * sizeof(T);
+    if (a.K <= kThreads) return launch_rows<DistillArgs, distill_kernel<T, MODE, 1>>(a, bytes, kThreads, St::kBytes, s);
+    return launch_rows<DistillArgs, distill_kernel<T, MODE, 2>>(a, bytes, kThreads, St::kBytes, s);
 }
 
 template <class T>
@@ -235,7 +327,7 @@ static cudaError_t launch_mode(const DistillArgs& a, DistillMode mode, cudaStrea
 
 cudaError_t launch_distill(DistillArgs a, int type, DistillMode mode, cudaStream_t s) {
     using namespace rows;
-    a.ncta = static_cast<unsigned>(cluster_size(a.M, static_cast<long long>(a.C) * (type == DH_T_F32 ? 4 : 2)));
+    set_floor(type, a.inv_t * kLog2e, a.floor, a.floor2);
     switch (type) {
         case DH_T_BF16: return launch_mode<__nv_bfloat16>(a, mode, s);
         case DH_T_F16: return launch_mode<__half>(a, mode, s);

@@ -106,7 +106,9 @@ struct LogprobArgs {
     int k;
     float* top_logp;         // [M][k]
     int32_t* top_ids;        // [M][k]
-    unsigned ncta;           // set by the launcher: CTAs per row
+    unsigned lg;             // set by the launcher: log2 of the CTAs per row
+    float floor;             // set by the launcher (dh_rows.cuh)
+    uint32_t floor2;
 };
 cudaError_t launch_token_logprobs(LogprobArgs a, int type, cudaStream_t s);
 
@@ -127,7 +129,9 @@ struct DistillArgs {
     float* lse;              // [M] or null, forward
     void* dz;                // [M][C] with row stride ld_dz, both and backward
     long long ld_dz;
-    unsigned ncta;           // set by the launcher: CTAs per row
+    unsigned lg;             // set by the launcher: log2 of the CTAs per row
+    float floor;             // set by the launcher (dh_rows.cuh)
+    uint32_t floor2;
 };
 enum DistillMode { kDistillForward, kDistillBoth, kDistillBackward };
 cudaError_t launch_distill(DistillArgs a, int type, DistillMode mode, cudaStream_t s);
@@ -153,9 +157,5 @@ cudaError_t launch_matmul(const MatmulArgs& m, cudaStream_t s);
 
 // row_of[idx[i]] = i for i < n, -1 elsewhere.
 cudaError_t launch_row_map(const int32_t* idx, int n, int32_t* row_of, int V, cudaStream_t s);
-
-namespace rows {
-int cluster_size(int M, long long row_bytes);
-}
 
 }  // namespace dh

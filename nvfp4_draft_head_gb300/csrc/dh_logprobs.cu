@@ -4,22 +4,23 @@
 //   d = (z - max z) / t,  S = sum e^d,
 //   lse = max z / t + ln S,  H = ln S - (sum e^d d) / S,  log p(j) = d_j - ln S.
 //
-// One cluster of 1..16 CTAs per row. Every thread keeps the running statistics
-// of its vectors (dh_rows.cuh), joined by shuffles, through shared memory and,
-// between CTAs, by stores into the peers' shared memory. The row is read once.
+// Persistent clusters of 1..8 CTAs take the rows in turn. Every thread streams
+// its vectors through shared memory and keeps their running statistics
+// (dh_rows.cuh), joined by shuffles, through shared memory and, between CTAs,
+// by stores into the peers' shared memory. The row is read once.
 //
 // Top alternatives. The largest logit of each thread's vectors comes out of
-// the statistics. A value T that at least k of a CTA's 512 thread maxima reach
+// the statistics. A value T that at least k of a CTA's 256 thread maxima reach
 // is a lower bound on the CTA's k-th largest logit, so only the vectors of the
 // threads whose maximum reaches T can hold one of its top k. T is found bit by
 // bit with block-wide counts, stopping at a count of up to k + k/2 + 4; those
-// threads' vectors (about k/512 of the slice, still in L2) are read again by the
+// threads' vectors (about k/256 of the slice, still in L2) are read again by the
 // whole CTA, elements >= T become candidates, and the rank of each among
 // the candidates is counted. Candidates are 64-bit keys (ordered value, then
 // the complement of the column), so equal logits go to the lowest column and
 // the arrival order does not matter. More than kCand candidates (rows of many
-// equal values) or a NaN send the CTA to an exact radix selection over its
-// slice instead. The CTAs' sorted lists are merged by the first CTA.
+// equal values), a NaN, or too few logits above the floor of the statistics
+// send the CTA to an exact radix selection over its slice instead. The CTAs' sorted lists are merged by the first CTA.
 //
 // Bound: HBM (C elements read per row); see the launcher for the measurements.
 #include "../../include/drafthead.h"
@@ -29,20 +30,28 @@
 namespace dh {
 namespace rows {
 
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 constexpr int kCand = 1024;   // candidates a CTA ranks by counting
-constexpr int kUnroll = 4;    // vectors in flight per thread
+constexpr int kUnroll = 4;    // vectors per batch and thread
+constexpr int kDepth = 2;     // batches in flight: 32 KB per CTA
+constexpr int kPerSm = 3;     // CTAs per SM
 
 struct LogprobSmem {
-    float warp[kWarps][3];
-    float cta[kMaxCluster][3];
-    int n_active, n_cand;
+    float warp[2][kWarps][3];
+    float plain[kWarps][3];
+    float cta[2][kMaxCluster][3];
+    float cta_plain[kMaxCluster][3];
+    uint32_t key_min[2][kWarps], key_max[2][kWarps];   // of the warps' thread maxima above the floor
+    int key_n[2][kWarps];
+    int n_active, n_cand, n_top;
     uint32_t sel_bin, sel_need;
     int scan[kWarps];
     int active[kThreads];
     uint32_t hist[256];
-    unsigned long long cand[kCand];
-    unsigned long long top[DH_MAX_TOP];                  // this CTA's list, descending; 0 = none
-    unsigned long long peers[kMaxCluster][DH_MAX_TOP];   // the first CTA: every CTA's list
+    alignas(16) unsigned long long cand[kCand];
+    unsigned long long top[DH_MAX_TOP];                     // this CTA's list, descending; 0 = none
+    unsigned long long peers[2][kMaxCluster][DH_MAX_TOP];   // the first CTA: every CTA's list
 };
 
 __device__ __forceinline__ void push_candidate(LogprobSmem& sm, float z, uint32_t col) {
@@ -53,11 +62,20 @@ __device__ __forceinline__ void push_candidate(LogprobSmem& sm, float z, uint32_
 // Sort the n <= kCand candidates (distinct keys) and keep the k largest.
 __device__ __forceinline__ void rank_candidates(LogprobSmem& sm, int n, int k) {
     for (int e = threadIdx.x; e < k; e += kThreads) sm.top[e] = 0ull;
+    if (threadIdx.x == 0) {
+        sm.n_top = min(n, k);
+        if ((n & 1) && n < kCand) sm.cand[n] = 0ull;   // read in pairs
+    }
     __syncthreads();
+    const ulonglong2* pairs = reinterpret_cast<const ulonglong2*>(sm.cand);
     for (int e = threadIdx.x; e < n; e += kThreads) {
         const unsigned long long mine = sm.cand[e];
         int above = 0;
-        for (int j = 0; j < n; ++j) above += sm.cand[j] > mine;
+#pragma unroll 4
+        for (int j = 0; j < (n + 1) / 2; ++j) {
+            const ulonglong2 p = pairs[j];
+            above += (p.x > mine) + (p.y > mine);
+        }
         if (above < k) sm.top[above] = mine;
     }
     __syncthreads();
@@ -142,46 +160,105 @@ __device__ __noinline__ void radix_top(LogprobSmem& sm, const T* z, int lo, int 
     rank_candidates(sm, sm.n_cand, k);
 }
 
-// The CTA's k largest logits into sm.top. `mx` is this thread's largest logit.
+// A bound that at least k of the CTA's keys reach (0 where there are fewer), bit by
+// bit from `t` down (which at least k reach), and that at most k + k/2 + 4 reach
+// where the keys allow it.
+__device__ __forceinline__ uint32_t kth_bound(uint32_t key, int k, uint32_t t, int bit) {
+    for (; bit >= 0; --bit) {
+        const uint32_t up = t | (1u << bit);
+        const int n = __syncthreads_count(key >= up);
+        if (n >= k) {
+            t = up;
+            if (n <= k + k / 2 + 4) break;
+        }
+    }
+    return t;
+}
+
+// The range of a warp's thread maxima that lie above the floor, for key_start().
+__device__ __forceinline__ void key_leave(LogprobSmem& sm, int turn, float mx, float floor) {
+    const bool in = mx > floor;
+    const uint32_t key = ordered_key(mx);
+    const uint32_t lo = __reduce_min_sync(0xFFFFFFFFu, in ? key : 0xFFFFFFFFu);
+    const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, in ? key : 0u);
+    const int n = __popc(__ballot_sync(0xFFFFFFFFu, in));
+    if ((threadIdx.x & 31) == 0) {
+        const int w = threadIdx.x >> 5;
+        sm.key_min[turn][w] = lo;
+        sm.key_max[turn][w] = hi;
+        sm.key_n[turn][w] = n;
+    }
+}
+
+// The CTA's k largest logits into sm.top. `mx` is this thread's largest logit, or
+// the floor where it has none above that; `ze` its edge logit (or -inf).
 template <class T>
-__device__ __forceinline__ void cta_top(LogprobSmem& sm, const T* z, const Slice& sl, int edge, float mx, bool nan, int k) {
+__device__ __forceinline__ void cta_top(LogprobSmem& sm, const T* z, const Slice& sl, int edge, float ze, float mx, int turn,
+                                        bool nan, int k) {
     constexpr int kVec = Elem<T>::kVec;
     if (nan) {
         radix_top(sm, z, sl.lo, sl.hi, k);
         return;
     }
-    const uint32_t key = ordered_key(mx);
-    uint32_t T_key = 0;
+    uint32_t key = ordered_key(mx), bound_key = 0;
     if (threadIdx.x == 0) sm.n_active = sm.n_cand = 0;
     if (sl.hi - sl.lo > kCand) {
-        for (int bit = 31; bit >= 0; --bit) {
-            const uint32_t t = T_key | (1u << bit);
-            const int n = __syncthreads_count(key >= t);
-            if (n >= k) {
-                T_key = t;
-                if (n <= k + k / 2 + 4) break;
+        const int l = threadIdx.x & 31;
+        const bool in = l < kWarps;
+        const uint32_t lo = __reduce_min_sync(0xFFFFFFFFu, in ? sm.key_min[turn][l] : 0xFFFFFFFFu);
+        const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, in ? sm.key_max[turn][l] : 0u);
+        if (__reduce_add_sync(0xFFFFFFFFu, in ? sm.key_n[turn][l] : 0) >= k) {
+            // enough maxima above the floor: start from the bits that all of them share
+            const int bit = 31 - __clz(static_cast<int>(lo ^ hi));
+            bound_key = kth_bound(key, k, bit >= 31 ? 0u : lo >> (bit + 1) << (bit + 1), bit);
+        } else {
+            // the maxima at the floor may be anything below it: take them anew
+            float top = ze;
+            for (int v = sl.v0 + threadIdx.x; v < sl.v1; v += kThreads) {
+                const uint4 w[1] = {ld_stream_v4(z + sl.head + static_cast<size_t>(v) * kVec)};
+                top = fmaxf(top, Elem<T>::template max_of<1>(w));
             }
+            key = ordered_key(top);
+            bound_key = kth_bound(key, k, 0u, 31);
         }
     }
     __syncthreads();
-    if (key >= T_key && sl.v0 + static_cast<int>(threadIdx.x) < sl.v1)
-        sm.active[atomicAdd(&sm.n_active, 1)] = threadIdx.x;
-    if (edge >= 0) {
-        const float v = Elem<T>::load(z + edge);
-        if (v > kNegInf && ordered_key(v) >= T_key) push_candidate(sm, v, static_cast<uint32_t>(edge));
-    }
+    // the threads that reach the bound, each warp's in a row
+    const bool active = key >= bound_key && key > ordered_key(kNegInf) && sl.v0 + static_cast<int>(threadIdx.x) < sl.v1;
+    const unsigned votes = __ballot_sync(0xFFFFFFFFu, active);
+    int at = 0;
+    if ((threadIdx.x & 31) == 0 && votes != 0u) at = atomicAdd(&sm.n_active, __popc(votes));
+    at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(votes & ((1u << (threadIdx.x & 31)) - 1u));
+    if (active) sm.active[at] = threadIdx.x;
+    if (edge >= 0 && ze > kNegInf && ordered_key(ze) >= bound_key) push_candidate(sm, ze, static_cast<uint32_t>(edge));
     __syncthreads();
-    // vector i of active thread a is v0 + a + i * kThreads
+    // their vectors (i of thread a: v0 + a + i * kThreads) over the whole CTA, four at a time;
+    // the bound as a value (below every logit's key: any logit above -inf)
+    const float bound = bound_key <= ordered_key(kNegInf) ? -FLT_MAX : ordered_value(bound_key);
     const int per = (sl.v1 - sl.v0 + kThreads - 1) / kThreads, total = sm.n_active * per;
-    for (int f = threadIdx.x; f < total; f += kThreads) {
-        const int a = f / per, v = sl.v0 + sm.active[a] + (f - a * per) * kThreads;
-        if (v >= sl.v1) continue;
-        const int col = sl.head + v * kVec;
-        float x[kVec];
-        Elem<T>::unpack(ld_stream_v4(z + col), x);
+    for (int f0 = threadIdx.x; f0 < total; f0 += 4 * kThreads) {
+        uint4 w[4][1];
+        int col[4];
 #pragma unroll
-        for (int j = 0; j < kVec; ++j)
-            if (x[j] > kNegInf && ordered_key(x[j]) >= T_key) push_candidate(sm, x[j], static_cast<uint32_t>(col + j));
+        for (int i = 0; i < 4; ++i) {
+            const int f = f0 + i * kThreads;
+            w[i][0] = neg_inf_vec<T>();
+            col[i] = 0;
+            if (f < total) {
+                const int a = f / per, v = sl.v0 + sm.active[a] + (f - a * per) * kThreads;
+                col[i] = sl.head + v * kVec;
+                if (v < sl.v1) w[i][0] = ld_stream_v4(z + col[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (Elem<T>::template max_of<1>(w[i]) < bound) continue;
+            float x[kVec];
+            Elem<T>::unpack(w[i][0], x);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j)
+                if (x[j] >= bound) push_candidate(sm, x[j], static_cast<uint32_t>(col[i] + j));
+        }
     }
     __syncthreads();
     const int n = sm.n_cand;
@@ -193,131 +270,140 @@ __device__ __forceinline__ void cta_top(LogprobSmem& sm, const T* z, const Slice
     }
 }
 
+// How many keys of a descending list lie above `key`.
+__device__ __forceinline__ int list_count(const unsigned long long* list, int k, unsigned long long key) {
+    int lo = 0, hi = k;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (list[mid] > key) lo = mid + 1;
+        else hi = mid;
+    }
+    return lo;
+}
+
 template <class T>
-__global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const LogprobArgs a) {
-    constexpr int kVec = Elem<T>::kVec;
+__global__ void __launch_bounds__(kThreads, kPerSm) token_logprobs_kernel(const LogprobArgs a) {
+    using St = Stream<T, kThreads, kUnroll, kDepth>;
+    extern __shared__ __align__(16) uint8_t ring[];
     __shared__ LogprobSmem sm;
-    const unsigned rank = cluster_ctarank(), ncta = a.ncta;
-    const int row = blockIdx.x / ncta;
-    if (ncta > 1) cluster_arrive_release();
-    const T* z = static_cast<const T*>(a.z) + static_cast<size_t>(row) * a.ld;
-    const Slice sl = make_slice(z, a.C, rank, ncta);
+    const unsigned lg = a.lg, ncta = 1u << lg, rank = ncta > 1 ? cluster_ctarank() : 0u;
+    const int first = blockIdx.x >> lg, stride = gridDim.x >> lg;
     const float c = a.inv_t * kLog2e;
-
-    Stat st = stat_empty();
-    for (int v0 = sl.v0 + threadIdx.x; v0 < sl.v1; v0 += kUnroll * kThreads) {
-        uint4 w[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int v = v0 + u * kThreads;
-            w[u] = v < sl.v1 ? ld_stream_v4(z + sl.head + static_cast<size_t>(v) * kVec) : neg_inf_vec<T>();
-        }
-        float x[kUnroll * kVec];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) Elem<T>::unpack(w[u], reinterpret_cast<float(&)[kVec]>(x[u * kVec]));
-        stat_add<true>(st, x, c);
-    }
-    const int edge = edge_column(sl, a.C, rank, ncta);
-    if (edge >= 0) stat_add1<true>(st, Elem<T>::load(z + edge), c);
-
-    const Stat mine = stat_block<true>(st, c, sm.warp);
-    if (a.k > 0) {
-        // a NaN in the slice (its values alone decide: an infinity makes s a NaN too, and is selected exactly)
-        cta_top(sm, z, sl, edge, st.m, mine.s != mine.s, a.k);
-    }
-    const Stat all = stat_cluster<true>(mine, c, sm.cta, rank, ncta);
-    if (a.k > 0 && ncta > 1) {
-        for (int i = threadIdx.x; i < a.k; i += kThreads)
-            st_cluster_u64(cluster_map(&sm.peers[rank][i], 0), sm.top[i]);
+    St stream;
+    stream.start(static_cast<const T*>(a.z), a.ld, a.M, a.C, rank, lg, first, stride, ring);
+    IdAhead tokens = {a.tokens, a.row_of, a.G, a.V, a.C, a.M, stride, static_cast<int>(threadIdx.x), -1, -1, -1};
+    if (rank == 0) tokens.start(first);
+    if (ncta > 1) {   // every peer runs before its shared memory is written
         cluster_arrive_release();
         cluster_wait_acquire();
     }
-    if (rank != 0) return;
+    uint32_t slot = 0;
+    int turn = 0;
+    const T* z = static_cast<const T*>(a.z) + static_cast<size_t>(first) * a.ld;
+    Slice sl = make_slice(z, a.C, rank, lg);
+    for (int row = first; row < a.M; row += stride, turn ^= 1, z += static_cast<size_t>(stride) * a.ld) {
+        if (!stream.alike) sl = make_slice(z, a.C, rank, lg);
+        const int edge = edge_column(sl, a.C, rank, ncta);
+        float zt = kNegInf, ze = kNegInf;
+        int col = -1;
+        if (rank == 0) col = tokens.take(row);
+        if (col >= 0) zt = Elem<T>::load(z + col);
+        if (edge >= 0) ze = Elem<T>::load(z + edge);
 
-    // ln S with S = sum e^((z - max)/t)
-    const bool empty = all.s == 0.0f;
-    const float ln_s = logf(all.s);
-    if (threadIdx.x == 0) {
-        if (a.lse != nullptr) a.lse[row] = empty ? kNegInf : all.m * a.inv_t + ln_s;
-        if (a.entropy != nullptr) a.entropy[row] = empty ? 0.0f : ln_s - all.s1 * kLn2 / all.s;
-    }
-    for (int g = threadIdx.x; g < a.G; g += kThreads) {
-        const size_t at = static_cast<size_t>(row) * a.G + g;
-        const int col = column_of(a.tokens[at], a.row_of, a.V, a.C);
-        a.logp[at] = col < 0 || empty ? kNegInf : (Elem<T>::load(z + col) - all.m) * a.inv_t - ln_s;
-    }
-    // merge: the place of a key is its place in its own list plus the keys above it in the others
-    for (int i = threadIdx.x; i < a.k * static_cast<int>(ncta); i += kThreads) {
-        const unsigned r = static_cast<unsigned>(i) / a.k;
-        int place = i - static_cast<int>(r) * a.k;
-        const unsigned long long key = ncta > 1 ? sm.peers[r][place] : sm.top[place];
-        if (ncta > 1 && key != 0ull) {
-            for (unsigned o = 0; o < ncta; ++o) {
-                if (o == r) continue;
-                int lo = 0, hi = a.k;
-                while (lo < hi) {
-                    const int mid = (lo + hi) >> 1;
-                    if (sm.peers[o][mid] > key) lo = mid + 1;
-                    else hi = mid;
-                }
-                place += lo;
+        Stat st = {a.floor, 0.0f, 0.0f};
+        const int batches = St::batches_of(sl);
+        for (int b = 0; b < batches; ++b) {
+            cp_async_wait<kDepth - 1>();
+            uint4 w[kUnroll];
+            stream.read(slot, sl, b, w);
+            stream.fetch();
+            slot = St::next(slot);
+            stat_add<T, true, kUnroll>(st, w, c, a.floor2);
+        }
+        if (edge >= 0) stat_add1<true>(st, ze, c, a.floor);
+
+        float top = st.m;
+        if (a.k > 0) key_leave(sm, turn, top, a.floor);
+        stat_leave(stat_warp<true, false>(st, c), sm.warp[turn]);
+        __syncthreads();
+        const Stat mine = stat_gather<true, false>(kWarps, c, sm.warp[turn], a.floor);
+        Stat all = stat_cluster<true, false>(mine, c, sm.cta[turn], rank, ncta);
+        // ln S, and the mean of (z - max) / t
+        float ln_s, mean;
+        bool empty = false;
+        if (stat_fits(all.m, c, a.floor)) {
+            const float r = shift_rest(all.m, c);
+            ln_s = logf(all.s) - r * kLn2;
+            mean = (all.s1 / all.s - r) * kLn2;
+        } else {
+            all = plain_slice<T, true, kThreads>(z, sl, ze, c, sm.plain, top);
+            all = stat_cluster<true, true>(all, c, sm.cta_plain, rank, ncta);
+            empty = all.s == 0.0f;
+            ln_s = logf(all.s);
+            mean = all.s1 * kLn2 / all.s;
+        }
+        if (a.k > 0) {
+            cta_top(sm, z, sl, edge, ze, top, turn, mine.s != mine.s, a.k);
+            if (ncta > 1) {
+                for (int i = threadIdx.x; i < a.k; i += kThreads)
+                    st_cluster_u64(cluster_map(&sm.peers[turn][rank][i], 0), sm.top[i]);
+                cluster_arrive_release();
+                cluster_wait_acquire();
             }
         }
-        if (key == 0ull || place >= a.k) continue;
-        const size_t at = static_cast<size_t>(row) * a.k + place;
-        const uint32_t col = 0xFFFFFFFFu - static_cast<uint32_t>(key);
-        a.top_logp[at] = (ordered_value(static_cast<uint32_t>(key >> 32)) - all.m) * a.inv_t - ln_s;
-        a.top_ids[at] = a.idx != nullptr ? __ldg(a.idx + col) : static_cast<int32_t>(col);
-    }
-    // places that no key took
-    int n = 0;
-    if (a.k > 0) {
-        for (unsigned r = 0; r < ncta; ++r) {
-            int lo = 0, hi = a.k;
-            const unsigned long long* list = ncta > 1 ? sm.peers[r] : sm.top;
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (list[mid] != 0ull) lo = mid + 1;
-                else hi = mid;
-            }
-            n += lo;
-        }
-        for (int i = n + threadIdx.x; i < a.k; i += kThreads) {
-            a.top_logp[static_cast<size_t>(row) * a.k + i] = kNegInf;
-            a.top_ids[static_cast<size_t>(row) * a.k + i] = -1;
-        }
-    }
-}
+        if (rank != 0) continue;
 
-// CTAs per row: enough to give the GPU two CTAs per SM, each with at least
-// 8 KB of the row to read (below that a slice's fixed costs outweigh it).
-int cluster_size(int M, long long row_bytes) {
-    const int sms = sm_count();
-    int n = 1;
-    while (n < 8 && static_cast<long long>(M) * n * 2 <= 2ll * sms && row_bytes / (2 * n) >= 8192) n *= 2;
-    return n;
+        if (threadIdx.x == 0) {
+            if (a.lse != nullptr) a.lse[row] = empty ? kNegInf : all.m * a.inv_t + ln_s;
+            if (a.entropy != nullptr) a.entropy[row] = empty ? 0.0f : ln_s - mean;
+        }
+        for (int g = threadIdx.x; g < a.G; g += kThreads) {
+            const size_t at = static_cast<size_t>(row) * a.G + g;
+            if (g >= kThreads) {
+                col = column_of(a.tokens[at], a.row_of, a.V, a.C);
+                zt = col >= 0 ? Elem<T>::load(z + col) : 0.0f;
+            }
+            a.logp[at] = col < 0 || empty ? kNegInf : (zt - all.m) * a.inv_t - ln_s;
+        }
+        // merge: the place of a key is its place in its own list plus the keys above it in the others
+        const unsigned long long(*peers)[DH_MAX_TOP] = sm.peers[turn];
+        for (int i = threadIdx.x; i < a.k * static_cast<int>(ncta); i += kThreads) {
+            const unsigned r = static_cast<unsigned>(i) / a.k;
+            int place = i - static_cast<int>(r) * a.k;
+            const unsigned long long key = ncta > 1 ? peers[r][place] : sm.top[place];
+            if (ncta > 1 && key != 0ull) {
+                for (unsigned o = 0; o < ncta; ++o)
+                    if (o != r) place += list_count(peers[o], a.k, key);
+            }
+            if (key == 0ull || place >= a.k) continue;
+            const size_t at = static_cast<size_t>(row) * a.k + place;
+            const uint32_t id = 0xFFFFFFFFu - static_cast<uint32_t>(key);
+            a.top_logp[at] = (ordered_value(static_cast<uint32_t>(key >> 32)) - all.m) * a.inv_t - ln_s;
+            a.top_ids[at] = a.idx != nullptr ? __ldg(a.idx + id) : static_cast<int32_t>(id);
+        }
+        if (a.k > 0) {   // places that no key took
+            int n = ncta > 1 ? 0 : sm.n_top;
+            for (unsigned r = 0; ncta > 1 && r < ncta; ++r) n += list_count(peers[r], a.k, 0ull);
+            for (int i = n + threadIdx.x; i < a.k; i += kThreads) {
+                a.top_logp[static_cast<size_t>(row) * a.k + i] = kNegInf;
+                a.top_ids[static_cast<size_t>(row) * a.k + i] = -1;
+            }
+            if (ncta == 1) __syncthreads();   // sm.top is read before the next row writes it
+        }
+    }
 }
 
 template <class T>
 static cudaError_t launch(const LogprobArgs& a, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.M) * a.ncta);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = a.ncta;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T>, a);
+    using St = Stream<T, kThreads, kUnroll, kDepth>;
+    return launch_rows<LogprobArgs, token_logprobs_kernel<T>>(a, static_cast<long long>(a.C) * sizeof(T), kThreads, St::kBytes, s);
 }
 
 }  // namespace rows
 
 cudaError_t launch_token_logprobs(LogprobArgs a, int type, cudaStream_t s) {
     using namespace rows;
-    a.ncta = static_cast<unsigned>(cluster_size(a.M, static_cast<long long>(a.C) * (type == DH_T_F32 ? 4 : 2)));
+    set_floor(type, a.inv_t * kLog2e, a.floor, a.floor2);
     switch (type) {
         case DH_T_BF16: return launch<__nv_bfloat16>(a, s);
         case DH_T_F16: return launch<__half>(a, s);
