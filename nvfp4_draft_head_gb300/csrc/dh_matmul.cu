@@ -18,10 +18,11 @@
 // straight into blocks.
 //
 // Product kernel: persistent, one CTA per SM; output tiles of 128 tokens x TN
-// weight rows. One thread streams blocks into a ring of shared-memory stages,
-// one issues the scale copies and the matrix instructions (kind::mxf4nvf4,
-// block 16), four warps read the accumulators from tensor memory, scale,
-// round once and store.
+// weight rows. One thread streams blocks into a ring of shared-memory stages;
+// four warps, one per group of 32 lanes of tensor memory, move a stage's scales
+// there through registers; one thread issues the matrix instructions
+// (kind::mxf4nvf4, block 16); eight warps read a tile's accumulators into
+// registers, scaled and rounded, free them for the next tile and store.
 #include <cfloat>
 
 #include "../../include/drafthead.h"
@@ -169,52 +170,27 @@ struct Args {
     unsigned int* error;    // DH_DEVERR_* word or null
 };
 
-constexpr int kEpiWarps = 4;
-constexpr int kThreads = 32 * (kEpiWarps + 2);
+constexpr int kEpiWarps = 8, kSfWarps = 4;
+constexpr int kThreads = 32 * (kEpiWarps + kSfWarps + 2);
 
 template <int TN>
 struct Cfg {
     static constexpr int kNB = TN / kRows;                        // weight blocks per tile
-    static constexpr int kStageBytes = kBlock * (1 + kNB);
+    // a stage: the token block, the codes of the weight blocks, their scales
+    static constexpr int kB = kBlock, kSf = kBlock + kNB * kCodes, kStageBytes = kSf + kNB * kScales;
     static constexpr int kStages = (227 * 1024 - 1024 - 512) / kStageBytes;   // 227 KB less alignment and barriers
     static constexpr int kSmem = kStages * kStageBytes + 1024;    // + alignment to 1,024
-    // tensor-memory columns: accumulators, then per parity of the stage the scales of A and B
-    static constexpr int kSfA = TN;
-    static constexpr int kSfB = TN + 2 * 16;
+    // tensor-memory columns: accumulators, then every stage's scales (16 of A, 16 per block of B)
+    static constexpr int kSfA = TN, kSfB = TN + 16, kSfStep = 16 + 16 * kNB;
     static constexpr int kCols = 512;
-    static_assert(kSfB + 2 * 16 * kNB <= kCols, "tensor memory");
+    static_assert(kSfA + kStages * kSfStep <= kCols, "tensor memory");
+    static_assert(kStages <= 8 && kStageBytes % 1024 == 0, "stage layout");
 };
 
 struct Sync {
-    uint64_t full[8], empty[8], acc_full, acc_empty;
+    uint64_t full[8], empty[8], sf_full[8], acc_full, acc_empty;
     uint32_t tmem;
     unsigned int abort;
-};
-
-template <class TY> struct Out;
-template <> struct Out<float> {
-    __device__ static void store16(float* p, const float (&v)[16], bool vec) {
-        if (vec) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(p + 4 * i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) p[i] = v[i];
-        }
-    }
-};
-template <class T2>
-struct Out {
-    __device__ static void store16(T2* p, const float (&v)[16], bool vec) {
-        if (vec) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                *reinterpret_cast<uint4*>(p + 8 * i) = rows::Elem<T2>::pack(reinterpret_cast<const float(&)[8]>(v[8 * i]));
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) p[i] = rows::Elem<T2>::store(v[i]);
-        }
-    }
 };
 
 // A bounded wait that gives up at once when another role has.
@@ -229,17 +205,29 @@ __device__ __forceinline__ bool wait_or_abort(Sync& sy, uint64_t* bar, uint32_t 
     return false;
 }
 
+__device__ __forceinline__ void lds16(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(addr) : "memory");
+}
+
+// 32 bytes, 32-byte aligned, in one store.
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 :: "l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+}
+
 template <class TY, int TN>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
     using C = Cfg<TN>;
+    constexpr int kStages = C::kStages, kCols = TN / 2;   // columns per epilogue warp
     extern __shared__ uint8_t smem_raw[];
     __shared__ Sync sy;
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::kStages; ++i) {
+        for (int i = 0; i < kStages; ++i) {
             mbar_init(&sy.full[i], 1);
             mbar_init(&sy.empty[i], 1);
+            mbar_init(&sy.sf_full[i], kSfWarps);
         }
         mbar_init(&sy.acc_full, 1);
         mbar_init(&sy.acc_empty, kEpiWarps);
@@ -252,59 +240,53 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = sy.tmem;
-    const int tiles = a.tiles_m * a.tiles_n;
+    const int tiles = a.tiles_m * a.tiles_n, first = blockIdx.x, stride = gridDim.x;
 
-    if (warp == kEpiWarps && lane == 0) {
+    if (warp == kEpiWarps + kSfWarps && lane == 0) {
         // producer: the blocks of every k-stage of every tile of this CTA
         uint64_t keep, once;
         asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
         asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(once));
+        const int blocks_n = blocks_of(a.N, kRows);
         uint32_t it = 0;
         bool ok = true;
-        for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-            const int tm = tile % a.tiles_m, tn = tile / a.tiles_m;
-            const int nb = min(C::kNB, blocks_of(a.N, kRows) - tn * C::kNB);
-            for (int k = 0; k < a.nk; ++k, ++it) {
-                const uint32_t s = it % C::kStages, use = it / C::kStages;
+        for (int tile = first; ok && tile < tiles; tile += stride) {
+            const int tm = tile % a.tiles_m, tn = tile / a.tiles_m, nb = min(C::kNB, blocks_n - tn * C::kNB);
+            const uint8_t* src_a = a.a + static_cast<size_t>(tm) * a.nk * kBlock;
+            const uint8_t* src_b = a.b + static_cast<size_t>(tn * C::kNB) * a.nk * kBlock;
+            for (int k = 0; k < a.nk; ++k, ++it, src_a += kBlock, src_b += kBlock) {
+                const uint32_t s = it % kStages, use = it / kStages;
                 if (use > 0 && !(ok = wait_or_abort(sy, &sy.empty[s], (use - 1) & 1, a))) break;
                 uint8_t* st = smem + s * C::kStageBytes;
                 mbar_arrive_expect_tx(&sy.full[s], static_cast<uint32_t>(kBlock * (1 + nb)));
-                bulk_g2s(st, a.a + (static_cast<size_t>(tm) * a.nk + k) * kBlock, kBlock, &sy.full[s], keep);
+                bulk_g2s(st, src_a, kBlock, &sy.full[s], keep);
                 for (int j = 0; j < nb; ++j) {   // codes of the weight blocks side by side, then their scales
-                    const uint8_t* src = a.b + (static_cast<size_t>(tn * C::kNB + j) * a.nk + k) * kBlock;
-                    bulk_g2s(st + kBlock + j * kCodes, src, kCodes, &sy.full[s], once);
-                    bulk_g2s(st + kBlock + C::kNB * kCodes + j * kScales, src + kCodes, kScales, &sy.full[s], once);
+                    const uint8_t* src = src_b + static_cast<size_t>(j) * a.nk * kBlock;
+                    bulk_g2s(st + C::kB + j * kCodes, src, kCodes, &sy.full[s], once);
+                    bulk_g2s(st + C::kSf + j * kScales, src + kCodes, kScales, &sy.full[s], once);
                 }
             }
         }
         // on an abort, let the copies in flight land before the CTA ends (bounded)
         if (!ok) {
-            for (uint32_t b = it > static_cast<uint32_t>(C::kStages) ? it - C::kStages : 0; b < it; ++b)
-                mbar_wait(&sy.full[b % C::kStages], (b / C::kStages) & 1, kWaitLimit / 64);
+            for (uint32_t b = it > static_cast<uint32_t>(kStages) ? it - kStages : 0; b < it; ++b)
+                mbar_wait(&sy.full[b % kStages], (b / kStages) & 1, kWaitLimit / 64);
         }
-    } else if (warp == kEpiWarps + 1 && lane == 0) {
-        // issuer: scale copies and matrix instructions
+    } else if (warp == kEpiWarps + kSfWarps + 1 && lane == 0) {
+        // issuer
         constexpr uint32_t kIdesc = tc::idesc_nvf4(kRows, TN);
         uint32_t it = 0, n = 0;
         bool ok = true;
-        for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, ++n) {
+        for (int tile = first; ok && tile < tiles; tile += stride, ++n) {
             if (n > 0 && !(ok = wait_or_abort(sy, &sy.acc_empty, (n - 1) & 1, a))) break;
-            tc::fence_after_sync();
             for (int k = 0; k < a.nk; ++k, ++it) {
-                const uint32_t s = it % C::kStages;
-                if (!(ok = wait_or_abort(sy, &sy.full[s], (it / C::kStages) & 1, a))) break;
+                const uint32_t s = it % kStages;
+                // the scales are stored, hence the operands have landed
+                if (!(ok = wait_or_abort(sy, &sy.sf_full[s], (it / kStages) & 1, a))) break;
                 tc::fence_after_sync();
                 const uint32_t st = smem_u32(smem + s * C::kStageBytes);
-                const uint32_t sfa = tmem + C::kSfA + (it & 1) * 16, sfb = tmem + C::kSfB + (it & 1) * 16 * C::kNB;
-                const uint32_t b_sc = st + kBlock + C::kNB * kCodes;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    tc::copy_scales(sfa + 4 * j, tc::desc_scales(st + kCodes + 512 * j));
-#pragma unroll
-                    for (int b = 0; b < C::kNB; ++b)
-                        tc::copy_scales(sfb + 4 * (C::kNB * j + b), tc::desc_scales(b_sc + b * kScales + 512 * j));
-                }
-                const uint64_t da = tc::desc_operand(st), db = tc::desc_operand(st + kBlock);
+                const uint64_t da = tc::desc_operand(st), db = tc::desc_operand(st + C::kB);
+                const uint32_t sfa = tmem + C::kSfA + s * C::kSfStep, sfb = tmem + C::kSfB + s * C::kSfStep;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)   // 64 of k: 32 bytes of the 128-byte rows
                     tc::mma_nvf4(tmem, da + 2 * j, db + 2 * j, kIdesc, sfa + 4 * j, sfb + 4 * C::kNB * j, k > 0 || j > 0);
@@ -316,35 +298,103 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
             tc::commit(&sy.acc_full);
             mbar_wait(&sy.acc_full, n & 1, kWaitLimit / 64);
         }
+    } else if (warp >= kEpiWarps && warp < kEpiWarps + kSfWarps) {
+        // scales: shared memory -> registers -> this warp's 32 lanes of tensor memory
+        const uint32_t at = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+        uint32_t it = 0;
+        bool ok = true;
+        for (int tile = first; ok && tile < tiles; tile += stride) {
+            for (int k = 0; k < a.nk; ++k, ++it) {
+                const uint32_t s = it % kStages;
+                // (a landed stage means that its slot's last one, and so its scales, have been multiplied)
+                ok = __all_sync(0xFFFFFFFFu, wait_or_abort(sy, &sy.full[s], (it / kStages) & 1, a));
+                if (!ok) break;
+                tc::fence_after_sync();
+                const uint32_t st = smem_u32(smem + s * C::kStageBytes) + lane * 16;
+                uint32_t w[C::kSfStep];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    lds16(st + kCodes + 512 * j, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+#pragma unroll
+                    for (int b = 0; b < C::kNB; ++b) {
+                        const int o = 16 + 4 * (C::kNB * j + b);
+                        lds16(st + C::kSf + b * kScales + 512 * j, w[o], w[o + 1], w[o + 2], w[o + 3]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < C::kSfStep; j += 16) tc::tmem_store16(at + C::kSfA + s * C::kSfStep + j, w + j);
+                tc::tmem_store_wait();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sy.sf_full[s]);
+            }
+        }
     } else if (warp < kEpiWarps) {
         const float gb = __ldg(a.gb);
-        const bool vec = (reinterpret_cast<uintptr_t>(a.y) & 15u) == 0 && (a.ldy * static_cast<long long>(sizeof(TY))) % 16 == 0;
+        const int quarter = warp & 3, half = warp >> 2;
+        const bool vec = (reinterpret_cast<uintptr_t>(a.y) & 31u) == 0 && (a.ldy * static_cast<long long>(sizeof(TY))) % 32 == 0;
+        const uint32_t acc = tmem + (static_cast<uint32_t>(quarter) << 21) + half * kCols;
         uint32_t n = 0;
-        for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++n) {
-            const int m = (tile % a.tiles_m) * kRows + threadIdx.x, n0 = (tile / a.tiles_m) * TN;
+        for (int tile = first; tile < tiles; tile += stride, ++n) {
+            const int m = (tile % a.tiles_m) * kRows + quarter * 32 + lane, n0 = (tile / a.tiles_m) * TN + half * kCols;
             const float g = m < a.M ? a.ga[m] * gb : 0.0f;
             const bool ok = wait_or_abort(sy, &sy.acc_full, n & 1, a);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             tc::fence_after_sync();
             TY* row = static_cast<TY*>(a.y) + static_cast<size_t>(m) * a.ldy + n0;
-            const int cols = min(TN, a.N - n0);
-            for (int c = 0; c < cols; c += 32) {
-                uint32_t r[32];
-                __syncwarp();
-                tc::tmem_load32(tmem + (static_cast<uint32_t>(warp) << 21) + c, r);
-                tc::tmem_load_wait();
+            if constexpr (sizeof(TY) == 2) {
+                uint32_t w[kCols / 32][16];   // the rounded results
+#pragma unroll
+                for (int c = 0; c < kCols / 32; ++c) {
+                    uint32_t r[32];
+                    tc::tmem_load32(acc + 32 * c, r);
+                    tc::tmem_load_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        w[c][i] = rows::Elem<TY>::pack2(__uint_as_float(r[2 * i]) * g, __uint_as_float(r[2 * i + 1]) * g);
+                }
+                tc::fence_before_sync();
+                if (lane == 0) mbar_arrive(&sy.acc_empty);
                 if (m < a.M) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float v[16];
+                    for (int c = 0; c < kCols / 32; ++c) {
+                        if (n0 + 32 * c >= a.N) break;
+                        if (vec) {
+                            store32(row + 32 * c, &w[c][0]);
+                            store32(row + 32 * c + 16, &w[c][8]);
+                        } else {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[16 * h + i]) * g;
-                        Out<TY>::store16(row + c + 16 * h, v, vec);
+                            for (int i = 0; i < 16; ++i) {
+                                reinterpret_cast<uint16_t*>(row)[32 * c + 2 * i] = static_cast<uint16_t>(w[c][i]);
+                                reinterpret_cast<uint16_t*>(row)[32 * c + 2 * i + 1] = static_cast<uint16_t>(w[c][i] >> 16);
+                            }
+                        }
                     }
                 }
+            } else {   // this many 32-bit results do not fit beside the rest: store as they are read
+                for (int c = 0; c < kCols / 32; ++c) {
+                    uint32_t r[32];
+                    tc::tmem_load32(acc + 32 * c, r);
+                    tc::tmem_load_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * g);
+                    if (m < a.M && n0 + 32 * c < a.N) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (vec) {
+                                store32(row + 32 * c + 8 * i, &r[8 * i]);
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) row[32 * c + 8 * i + j] = __uint_as_float(r[8 * i + j]);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                }
+                tc::fence_before_sync();
+                if (lane == 0) mbar_arrive(&sy.acc_empty);
             }
-            tc::fence_before_sync();
-            if (lane == 0) mbar_arrive(&sy.acc_empty);
+            __syncwarp();
         }
     }
     __syncwarp();

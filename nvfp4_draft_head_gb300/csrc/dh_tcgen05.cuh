@@ -28,22 +28,12 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(smem_u32(bar)) : "memory");
 }
 
-// Shared-memory descriptor: bits 0-13 address / 16, 16-29 leading and 32-45
-// stride byte offset / 16, 46-48 version 1, 61-63 swizzle (0 none, 2: 128 bytes).
-//  - operand tiles: K-major rows of 128 bytes, 128-byte swizzle, 8-row groups
-//    1,024 bytes apart; a step along K inside the swizzle row adds its bytes;
-//  - scale factors: 8 x 16-byte core matrices, 128 bytes apart, no swizzle.
+// Shared-memory descriptor of an operand tile, K-major rows of 128 bytes with the
+// 128-byte swizzle, 8-row groups 1,024 bytes apart: bits 0-13 address / 16, 16-29
+// leading and 32-45 stride byte offset / 16, 46-48 version 1, 61-63 swizzle mode 2.
+// A step along K inside the 128 bytes adds its bytes to the address.
 __device__ __forceinline__ uint64_t desc_operand(uint32_t addr) {
     return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
-__device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
-    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (8ull << 16) | (8ull << 32) | (1ull << 46);
-}
-
-// Copy 32 rows of 16 bytes from shared memory into four tensor-memory columns,
-// repeated for the four 32-lane groups (the form in which scales are read).
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(tmem), "l"(desc) : "memory");
 }
 
 // Instruction descriptor of kind::mxf4nvf4, E2M1 operands (1 at bits 7 and 10),
@@ -52,7 +42,9 @@ __host__ __device__ constexpr uint32_t idesc_nvf4(int M, int N) {
     return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// D (+)= sum over 4 blocks of 16 of scaleA scaleB A B, K = 64 per instruction.
+// D (+)= sum over 4 blocks of 16 of scaleA scaleB A B, K = 64 per instruction. The
+// scales are in tensor memory: row r's four (a 32-bit word) in lane r % 32 of
+// column r / 32, the same in each group of 32 lanes.
 __device__ __forceinline__ void mma_nvf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, bool add) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
                  "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
@@ -70,6 +62,15 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
                    "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
                  : "r"(addr));
 }
+// 16 columns of this warp's 32 lanes, written from registers: lane l's columns from thread l.
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
+                 :: "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+                    "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+                    "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 }  // namespace tc
