@@ -170,7 +170,7 @@ struct Args {
     unsigned int* error;    // DH_DEVERR_* word or null
 };
 
-constexpr int kEpiWarps = 8, kSfWarps = 4;
+constexpr int kEpiWarps = 16, kSfWarps = 4;
 constexpr int kThreads = 32 * (kEpiWarps + kSfWarps + 2);
 
 template <int TN>
@@ -180,15 +180,17 @@ struct Cfg {
     static constexpr int kB = kBlock, kSf = kBlock + kNB * kCodes, kStageBytes = kSf + kNB * kScales;
     static constexpr int kStages = (227 * 1024 - 1024 - 512) / kStageBytes;   // 227 KB less alignment and barriers
     static constexpr int kSmem = kStages * kStageBytes + 1024;    // + alignment to 1,024
-    // tensor-memory columns: accumulators, then every stage's scales (16 of A, 16 per block of B)
-    static constexpr int kSfA = TN, kSfB = TN + 16, kSfStep = 16 + 16 * kNB;
+    // tensor-memory columns: accumulators (of two tiles where they fit), then every stage's
+    // scales (16 of A, 16 per block of B)
+    static constexpr int kAcc = TN == 128 ? 2 : 1;
+    static constexpr int kSfA = kAcc * TN, kSfB = kSfA + 16, kSfStep = 16 + 16 * kNB;
     static constexpr int kCols = 512;
     static_assert(kSfA + kStages * kSfStep <= kCols, "tensor memory");
     static_assert(kStages <= 8 && kStageBytes % 1024 == 0, "stage layout");
 };
 
 struct Sync {
-    uint64_t full[8], empty[8], sf_full[8], acc_full, acc_empty;
+    uint64_t full[8], empty[8], sf_full[8], acc_full[2], acc_empty[2];
     uint32_t tmem;
     unsigned int abort;
 };
@@ -218,7 +220,7 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* w) {
 template <class TY, int TN>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
     using C = Cfg<TN>;
-    constexpr int kStages = C::kStages, kCols = TN / 2;   // columns per epilogue warp
+    constexpr int kStages = C::kStages, kCols = TN * 4 / kEpiWarps;   // columns per epilogue warp
     extern __shared__ uint8_t smem_raw[];
     __shared__ Sync sy;
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -229,8 +231,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
             mbar_init(&sy.empty[i], 1);
             mbar_init(&sy.sf_full[i], kSfWarps);
         }
-        mbar_init(&sy.acc_full, 1);
-        mbar_init(&sy.acc_empty, kEpiWarps);
+        for (int i = 0; i < C::kAcc; ++i) {
+            mbar_init(&sy.acc_full[i], 1);
+            mbar_init(&sy.acc_empty[i], kEpiWarps);
+        }
         mbar_init_fence();
         sy.abort = 0u;
     }
@@ -278,7 +282,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
         uint32_t it = 0, n = 0;
         bool ok = true;
         for (int tile = first; ok && tile < tiles; tile += stride, ++n) {
-            if (n > 0 && !(ok = wait_or_abort(sy, &sy.acc_empty, (n - 1) & 1, a))) break;
+            const uint32_t buf = n % C::kAcc, use = n / C::kAcc;
+            if (use > 0 && !(ok = wait_or_abort(sy, &sy.acc_empty[buf], (use - 1) & 1, a))) break;
             for (int k = 0; k < a.nk; ++k, ++it) {
                 const uint32_t s = it % kStages;
                 // the scales are stored, hence the operands have landed
@@ -289,14 +294,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
                 const uint32_t sfa = tmem + C::kSfA + s * C::kSfStep, sfb = tmem + C::kSfB + s * C::kSfStep;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)   // 64 of k: 32 bytes of the 128-byte rows
-                    tc::mma_nvf4(tmem, da + 2 * j, db + 2 * j, kIdesc, sfa + 4 * j, sfb + 4 * C::kNB * j, k > 0 || j > 0);
+                    tc::mma_nvf4(tmem + buf * TN, da + 2 * j, db + 2 * j, kIdesc, sfa + 4 * j, sfb + 4 * C::kNB * j, k > 0 || j > 0);
                 tc::commit(&sy.empty[s]);
             }
-            if (ok) tc::commit(&sy.acc_full);
+            if (ok) tc::commit(&sy.acc_full[buf]);
         }
         if (!ok) {   // let the issued instructions finish before tensor memory is freed (bounded)
-            tc::commit(&sy.acc_full);
-            mbar_wait(&sy.acc_full, n & 1, kWaitLimit / 64);
+            tc::commit(&sy.acc_full[n % C::kAcc]);
+            mbar_wait(&sy.acc_full[n % C::kAcc], (n / C::kAcc) & 1, kWaitLimit / 64);
         }
     } else if (warp >= kEpiWarps && warp < kEpiWarps + kSfWarps) {
         // scales: shared memory -> registers -> this warp's 32 lanes of tensor memory
@@ -331,68 +336,67 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
         }
     } else if (warp < kEpiWarps) {
         const float gb = __ldg(a.gb);
-        const int quarter = warp & 3, half = warp >> 2;
+        const int quarter = warp & 3, part = warp >> 2;
         const bool vec = (reinterpret_cast<uintptr_t>(a.y) & 31u) == 0 && (a.ldy * static_cast<long long>(sizeof(TY))) % 32 == 0;
-        const uint32_t acc = tmem + (static_cast<uint32_t>(quarter) << 21) + half * kCols;
         uint32_t n = 0;
         for (int tile = first; tile < tiles; tile += stride, ++n) {
-            const int m = (tile % a.tiles_m) * kRows + quarter * 32 + lane, n0 = (tile / a.tiles_m) * TN + half * kCols;
+            const int m = (tile % a.tiles_m) * kRows + quarter * 32 + lane, n0 = (tile / a.tiles_m) * TN + part * kCols;
             const float g = m < a.M ? a.ga[m] * gb : 0.0f;
-            const bool ok = wait_or_abort(sy, &sy.acc_full, n & 1, a);
+            const uint32_t buf = n % C::kAcc, acc = tmem + (static_cast<uint32_t>(quarter) << 21) + buf * TN + part * kCols;
+            const bool ok = wait_or_abort(sy, &sy.acc_full[buf], (n / C::kAcc) & 1, a);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             tc::fence_after_sync();
             TY* row = static_cast<TY*>(a.y) + static_cast<size_t>(m) * a.ldy + n0;
             if constexpr (sizeof(TY) == 2) {
-                uint32_t w[kCols / 32][16];   // the rounded results
+                uint32_t w[kCols / 16][8];   // the rounded results
 #pragma unroll
-                for (int c = 0; c < kCols / 32; ++c) {
-                    uint32_t r[32];
-                    tc::tmem_load32(acc + 32 * c, r);
+                for (int c = 0; c < kCols / 16; ++c) {
+                    uint32_t r[16];
+                    tc::tmem_load16(acc + 16 * c, r);
                     tc::tmem_load_wait();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
+                    for (int i = 0; i < 8; ++i)
                         w[c][i] = rows::Elem<TY>::pack2(__uint_as_float(r[2 * i]) * g, __uint_as_float(r[2 * i + 1]) * g);
                 }
                 tc::fence_before_sync();
-                if (lane == 0) mbar_arrive(&sy.acc_empty);
+                if (lane == 0) mbar_arrive(&sy.acc_empty[buf]);
                 if (m < a.M) {
 #pragma unroll
-                    for (int c = 0; c < kCols / 32; ++c) {
-                        if (n0 + 32 * c >= a.N) break;
+                    for (int c = 0; c < kCols / 16; ++c) {
+                        if (n0 + 16 * c >= a.N) break;
                         if (vec) {
-                            store32(row + 32 * c, &w[c][0]);
-                            store32(row + 32 * c + 16, &w[c][8]);
+                            store32(row + 16 * c, w[c]);
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                reinterpret_cast<uint16_t*>(row)[32 * c + 2 * i] = static_cast<uint16_t>(w[c][i]);
-                                reinterpret_cast<uint16_t*>(row)[32 * c + 2 * i + 1] = static_cast<uint16_t>(w[c][i] >> 16);
+                            for (int i = 0; i < 8; ++i) {
+                                reinterpret_cast<uint16_t*>(row)[16 * c + 2 * i] = static_cast<uint16_t>(w[c][i]);
+                                reinterpret_cast<uint16_t*>(row)[16 * c + 2 * i + 1] = static_cast<uint16_t>(w[c][i] >> 16);
                             }
                         }
                     }
                 }
             } else {   // this many 32-bit results do not fit beside the rest: store as they are read
-                for (int c = 0; c < kCols / 32; ++c) {
-                    uint32_t r[32];
-                    tc::tmem_load32(acc + 32 * c, r);
+                for (int c = 0; c < kCols / 16; ++c) {
+                    uint32_t r[16];
+                    tc::tmem_load16(acc + 16 * c, r);
                     tc::tmem_load_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * g);
-                    if (m < a.M && n0 + 32 * c < a.N) {
+                    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * g);
+                    if (m < a.M && n0 + 16 * c < a.N) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < 2; ++i) {
                             if (vec) {
-                                store32(row + 32 * c + 8 * i, &r[8 * i]);
+                                store32(row + 16 * c + 8 * i, &r[8 * i]);
                             } else {
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) row[32 * c + 8 * i + j] = __uint_as_float(r[8 * i + j]);
+                                for (int j = 0; j < 8; ++j) row[16 * c + 8 * i + j] = __uint_as_float(r[8 * i + j]);
                             }
                         }
                     }
                     __syncwarp();
                 }
                 tc::fence_before_sync();
-                if (lane == 0) mbar_arrive(&sy.acc_empty);
+                if (lane == 0) mbar_arrive(&sy.acc_empty[buf]);
             }
             __syncwarp();
         }
