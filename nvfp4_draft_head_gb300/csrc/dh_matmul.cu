@@ -213,7 +213,7 @@ __device__ __forceinline__ void lds16(uint32_t addr, uint32_t& a, uint32_t& b, u
 
 // 32 bytes, 32-byte aligned, in one store.
 __device__ __forceinline__ void store32(void* p, const uint32_t* w) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+    asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
                  :: "l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
 }
 
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
         // producer: the blocks of every k-stage of every tile of this CTA
         uint64_t keep, once;
         asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
-        asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(once));
+        asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(once));
         const int blocks_n = blocks_of(a.N, kRows);
         uint32_t it = 0;
         bool ok = true;
