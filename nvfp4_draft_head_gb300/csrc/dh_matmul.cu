@@ -23,6 +23,7 @@
 // there through registers; one thread issues the matrix instructions
 // (kind::mxf4nvf4, block 16); eight warps read a tile's accumulators into
 // registers, scaled and rounded, free them for the next tile and store.
+#include <atomic>
 #include <cfloat>
 
 #include "../../include/drafthead.h"
@@ -248,9 +249,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
 
     if (warp == kEpiWarps + kSfWarps && lane == 0) {
         // producer: the blocks of every k-stage of every tile of this CTA
-        uint64_t keep, once;
+        uint64_t keep;   // operands stay in L2 against the stream of results
         asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
-        asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(once));
         const int blocks_n = blocks_of(a.N, kRows);
         uint32_t it = 0;
         bool ok = true;
@@ -266,8 +266,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
                 bulk_g2s(st, src_a, kBlock, &sy.full[s], keep);
                 for (int j = 0; j < nb; ++j) {   // codes of the weight blocks side by side, then their scales
                     const uint8_t* src = src_b + static_cast<size_t>(j) * a.nk * kBlock;
-                    bulk_g2s(st + C::kB + j * kCodes, src, kCodes, &sy.full[s], once);
-                    bulk_g2s(st + C::kSf + j * kScales, src + kCodes, kScales, &sy.full[s], once);
+                    bulk_g2s(st + C::kB + j * kCodes, src, kCodes, &sy.full[s], keep);
+                    bulk_g2s(st + C::kSf + j * kScales, src + kCodes, kScales, &sy.full[s], keep);
                 }
             }
         }
@@ -415,8 +415,17 @@ static cudaError_t launch_product(Args a, cudaStream_t s) {
     if (sms <= 0) return cudaErrorInvalidDevice;
     a.tiles_n = blocks_of(a.N, TN);
     const long long tiles = static_cast<long long>(a.tiles_m) * a.tiles_n;
-    const cudaError_t e = cudaFuncSetAttribute(product_kernel<TY, TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    constexpr int kDevices = 64;
+    static std::atomic<bool> known[kDevices];   // per device: the kernel's shared memory has been allowed
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (dev >= kDevices) return cudaErrorInvalidDevice;
+    if (!known[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(product_kernel<TY, TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        if (e != cudaSuccess) return e;
+        known[dev].store(true, std::memory_order_release);
+    }
     product_kernel<TY, TN><<<static_cast<unsigned>(tiles < sms ? tiles : sms), kThreads, C::kSmem, s>>>(a);
     return cudaGetLastError();
 }
