@@ -13,7 +13,7 @@
 // the statistics. A value T that at least k of a CTA's 256 thread maxima reach
 // is a lower bound on the CTA's k-th largest logit, so only the vectors of the
 // threads whose maximum reaches T can hold one of its top k. T is found bit by
-// bit with block-wide counts, stopping at a count of up to k + k/2 + 4; those
+// bit stopping at a count of up to k + k/2 + 4; those
 // threads' vectors (about k/256 of the slice, still in L2) are read again by the
 // whole CTA, elements >= T become candidates, and the rank of each among
 // the candidates is counted. Candidates are 64-bit keys (ordered value, then
@@ -33,6 +33,7 @@ namespace rows {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCand = 1024;   // candidates a CTA ranks by counting
+constexpr int kFew = 256;     // columns that are all candidates
 constexpr int kUnroll = 4;    // vectors per batch and thread
 constexpr int kDepth = 2;     // batches in flight: 32 KB per CTA
 constexpr int kPerSm = 3;     // CTAs per SM
@@ -42,8 +43,8 @@ struct LogprobSmem {
     float plain[kWarps][3];
     float cta[2][kMaxCluster][3];
     float cta_plain[kMaxCluster][3];
-    uint32_t key_min[2][kWarps], key_max[2][kWarps];   // of the warps' thread maxima above the floor
-    int key_n[2][kWarps];
+    uint32_t key[kThreads];   // the threads' maxima
+    uint32_t bound;
     int n_active, n_cand, n_top;
     uint32_t sel_bin, sel_need;
     int scan[kWarps];
@@ -160,40 +161,56 @@ __device__ __noinline__ void radix_top(LogprobSmem& sm, const T* z, int lo, int 
     rank_candidates(sm, sm.n_cand, k);
 }
 
-// A bound that at least k of the CTA's keys reach (0 where there are fewer), bit by
-// bit from `t` down (which at least k reach), and that at most k + k/2 + 4 reach
-// where the keys allow it.
-__device__ __forceinline__ uint32_t kth_bound(uint32_t key, int k, uint32_t t, int bit) {
-    for (; bit >= 0; --bit) {
-        const uint32_t up = t | (1u << bit);
-        const int n = __syncthreads_count(key >= up);
-        if (n >= k) {
-            t = up;
-            if (n <= k + k / 2 + 4) break;
+// A bound that at least k of the CTA's keys (a maximum per thread) reach, and that at
+// most k + k/2 + 4 reach where the keys allow it; 0 where fewer than k lie above
+// `floor_key`. The first warp looks for it bit by bit, from the bits that all keys
+// above the floor share: a count of 256 keys in one warp's registers is a few
+// instructions, where a barrier per bit cost 20 us a row at the worst.
+__device__ __forceinline__ uint32_t kth_bound(LogprobSmem& sm, uint32_t key, int k, uint32_t floor_key) {
+    sm.key[threadIdx.x] = key;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        constexpr int kPer = kThreads / 32;
+        uint32_t mine[kPer], lo = 0xFFFFFFFFu, hi = 0u;
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            mine[i] = sm.key[threadIdx.x + 32 * i];
+            const bool in = mine[i] > floor_key;
+            lo = in ? min(lo, mine[i]) : lo;
+            hi = in ? max(hi, mine[i]) : hi;
+            n += in;
         }
+        n = __reduce_add_sync(0xFFFFFFFFu, n);
+        uint32_t t = 0;
+        if (n >= k) {
+            lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+            hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+            int bit = 31 - __clz(static_cast<int>(lo ^ hi));
+            t = bit >= 31 ? 0u : lo >> (bit + 1) << (bit + 1);
+#pragma unroll 1
+            for (; bit >= 0 && n > k + k / 2 + 4; --bit) {
+                const uint32_t up = t | (1u << bit);
+                int c = 0;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) c += mine[i] >= up;
+                c = __reduce_add_sync(0xFFFFFFFFu, c);
+                if (c >= k) {
+                    t = up;
+                    n = c;
+                }
+            }
+        }
+        if (threadIdx.x == 0) sm.bound = t;
     }
-    return t;
-}
-
-// The range of a warp's thread maxima that lie above the floor, for key_start().
-__device__ __forceinline__ void key_leave(LogprobSmem& sm, int turn, float mx, float floor) {
-    const bool in = mx > floor;
-    const uint32_t key = ordered_key(mx);
-    const uint32_t lo = __reduce_min_sync(0xFFFFFFFFu, in ? key : 0xFFFFFFFFu);
-    const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, in ? key : 0u);
-    const int n = __popc(__ballot_sync(0xFFFFFFFFu, in));
-    if ((threadIdx.x & 31) == 0) {
-        const int w = threadIdx.x >> 5;
-        sm.key_min[turn][w] = lo;
-        sm.key_max[turn][w] = hi;
-        sm.key_n[turn][w] = n;
-    }
+    __syncthreads();
+    return sm.bound;
 }
 
 // The CTA's k largest logits into sm.top. `mx` is this thread's largest logit, or
 // the floor where it has none above that; `ze` its edge logit (or -inf).
 template <class T>
-__device__ __forceinline__ void cta_top(LogprobSmem& sm, const T* z, const Slice& sl, int edge, float ze, float mx, int turn,
+__device__ __forceinline__ void cta_top(LogprobSmem& sm, const T* z, const Slice& sl, int edge, float ze, float mx, float floor,
                                         bool nan, int k) {
     constexpr int kVec = Elem<T>::kVec;
     if (nan) {
@@ -202,24 +219,17 @@ __device__ __forceinline__ void cta_top(LogprobSmem& sm, const T* z, const Slice
     }
     uint32_t key = ordered_key(mx), bound_key = 0;
     if (threadIdx.x == 0) sm.n_active = sm.n_cand = 0;
-    if (sl.hi - sl.lo > kCand) {
-        const int l = threadIdx.x & 31;
-        const bool in = l < kWarps;
-        const uint32_t lo = __reduce_min_sync(0xFFFFFFFFu, in ? sm.key_min[turn][l] : 0xFFFFFFFFu);
-        const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, in ? sm.key_max[turn][l] : 0u);
-        if (__reduce_add_sync(0xFFFFFFFFu, in ? sm.key_n[turn][l] : 0) >= k) {
-            // enough maxima above the floor: start from the bits that all of them share
-            const int bit = 31 - __clz(static_cast<int>(lo ^ hi));
-            bound_key = kth_bound(key, k, bit >= 31 ? 0u : lo >> (bit + 1) << (bit + 1), bit);
-        } else {
-            // the maxima at the floor may be anything below it: take them anew
+    if (sl.hi - sl.lo > kFew) {
+        bound_key = kth_bound(sm, key, k, ordered_key(floor));
+        if (bound_key == 0) {   // too few above the floor; a maximum at it may be anything below: take them anew
             float top = ze;
             for (int v = sl.v0 + threadIdx.x; v < sl.v1; v += kThreads) {
                 const uint4 w[1] = {ld_stream_v4(z + sl.head + static_cast<size_t>(v) * kVec)};
                 top = fmaxf(top, Elem<T>::template max_of<1>(w));
             }
             key = ordered_key(top);
-            bound_key = kth_bound(key, k, 0u, 31);
+            __syncthreads();   // sm.bound has been read
+            bound_key = kth_bound(sm, key, k, ordered_key(kNegInf));
         }
     }
     __syncthreads();
@@ -236,19 +246,15 @@ __device__ __forceinline__ void cta_top(LogprobSmem& sm, const T* z, const Slice
     // the bound as a value (below every logit's key: any logit above -inf)
     const float bound = bound_key <= ordered_key(kNegInf) ? -FLT_MAX : ordered_value(bound_key);
     const int per = (sl.v1 - sl.v0 + kThreads - 1) / kThreads, total = sm.n_active * per;
+#pragma unroll 1
     for (int f0 = threadIdx.x; f0 < total; f0 += 4 * kThreads) {
         uint4 w[4][1];
-        int col[4];
+        int v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int f = f0 + i * kThreads;
-            w[i][0] = neg_inf_vec<T>();
-            col[i] = 0;
-            if (f < total) {
-                const int a = f / per, v = sl.v0 + sm.active[a] + (f - a * per) * kThreads;
-                col[i] = sl.head + v * kVec;
-                if (v < sl.v1) w[i][0] = ld_stream_v4(z + col[i]);
-            }
+            const int f = f0 + i * kThreads, a = f / per;
+            v[i] = f < total ? sl.v0 + sm.active[a] + (f - a * per) * kThreads : sl.v1;
+            w[i][0] = v[i] < sl.v1 ? ld_stream_v4(z + sl.head + static_cast<size_t>(v[i]) * kVec) : neg_inf_vec<T>();
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -257,7 +263,7 @@ __device__ __forceinline__ void cta_top(LogprobSmem& sm, const T* z, const Slice
             Elem<T>::unpack(w[i][0], x);
 #pragma unroll
             for (int j = 0; j < kVec; ++j)
-                if (x[j] >= bound) push_candidate(sm, x[j], static_cast<uint32_t>(col[i] + j));
+                if (x[j] >= bound) push_candidate(sm, x[j], static_cast<uint32_t>(sl.head + v[i] * kVec + j));
         }
     }
     __syncthreads();
@@ -323,27 +329,19 @@ __global__ void __launch_bounds__(kThreads, kPerSm) token_logprobs_kernel(const 
         if (edge >= 0) stat_add1<true>(st, ze, c, a.floor);
 
         float top = st.m;
-        if (a.k > 0) key_leave(sm, turn, top, a.floor);
         stat_leave(stat_warp<true, false>(st, c), sm.warp[turn]);
         __syncthreads();
         const Stat mine = stat_gather<true, false>(kWarps, c, sm.warp[turn], a.floor);
         Stat all = stat_cluster<true, false>(mine, c, sm.cta[turn], rank, ncta);
-        // ln S, and the mean of (z - max) / t
-        float ln_s, mean;
-        bool empty = false;
+        float rest = 0.0f;   // m c less its rounding, which the sums carry
         if (stat_fits(all.m, c, a.floor)) {
-            const float r = shift_rest(all.m, c);
-            ln_s = logf(all.s) - r * kLn2;
-            mean = (all.s1 / all.s - r) * kLn2;
+            rest = shift_rest(all.m, c);
         } else {
             all = plain_slice<T, true, kThreads>(z, sl, ze, c, sm.plain, top);
             all = stat_cluster<true, true>(all, c, sm.cta_plain, rank, ncta);
-            empty = all.s == 0.0f;
-            ln_s = logf(all.s);
-            mean = all.s1 * kLn2 / all.s;
         }
         if (a.k > 0) {
-            cta_top(sm, z, sl, edge, ze, top, turn, mine.s != mine.s, a.k);
+            cta_top(sm, z, sl, edge, ze, top, a.floor, mine.s != mine.s, a.k);
             if (ncta > 1) {
                 for (int i = threadIdx.x; i < a.k; i += kThreads)
                     st_cluster_u64(cluster_map(&sm.peers[turn][rank][i], 0), sm.top[i]);
@@ -353,9 +351,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm) token_logprobs_kernel(const 
         }
         if (rank != 0) continue;
 
+        // results (a warp without any only passes the barrier at the end)
+        const bool empty = all.s == 0.0f;
+        float ln_s = 0.0f;
+        if (static_cast<int>(threadIdx.x & ~31u) < max(max(a.G, a.k * static_cast<int>(ncta)), 1)) ln_s = logf(all.s) - rest * kLn2;
         if (threadIdx.x == 0) {
             if (a.lse != nullptr) a.lse[row] = empty ? kNegInf : all.m * a.inv_t + ln_s;
-            if (a.entropy != nullptr) a.entropy[row] = empty ? 0.0f : ln_s - mean;
+            // the mean of (z - max) / t is (s1 / s - rest) ln 2
+            if (a.entropy != nullptr) a.entropy[row] = empty ? 0.0f : ln_s - (all.s1 / all.s - rest) * kLn2;
         }
         for (int g = threadIdx.x; g < a.G; g += kThreads) {
             const size_t at = static_cast<size_t>(row) * a.G + g;
@@ -383,7 +386,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) token_logprobs_kernel(const 
         }
         if (a.k > 0) {   // places that no key took
             int n = ncta > 1 ? 0 : sm.n_top;
-            for (unsigned r = 0; ncta > 1 && r < ncta; ++r) n += list_count(peers[r], a.k, 0ull);
+            for (unsigned r = 0; n < a.k && ncta > 1 && r < ncta; ++r)
+                n += peers[r][a.k - 1] != 0ull ? a.k : list_count(peers[r], a.k, 0ull);
             for (int i = n + threadIdx.x; i < a.k; i += kThreads) {
                 a.top_logp[static_cast<size_t>(row) * a.k + i] = kNegInf;
                 a.top_ids[static_cast<size_t>(row) * a.k + i] = -1;

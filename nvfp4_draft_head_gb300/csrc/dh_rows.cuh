@@ -540,6 +540,7 @@ struct Stream {
         slot = 0;
         left = 0;
         open_row(true);
+#pragma unroll 1
         for (int i = 0; i < P; ++i) fetch();
     }
     __device__ static __forceinline__ uint32_t next(uint32_t s) { return s + kSlot == kBytes ? 0 : s + kSlot; }
@@ -674,7 +675,8 @@ static cudaError_t row_launch_setup(int threads, int smem, RowLaunch& out) {
 
 // Launch a persistent kernel over M rows. CTAs per row, by the time of the
 // longest-working CTA: rounds of rows that a cluster takes times its CTA's share
-// of a row, plus for each round a fixed cost worth 8 KB of reading. Few rows are so
+// of a row, plus for each round a fixed cost worth 32 KB of reading
+// (about 2 us). Few rows are so
 // split over up to 8 CTAs, and a number of rows that fills its last round badly in two.
 template <class A, void (*KERNEL)(A)>
 static cudaError_t launch_rows(A a, long long row_bytes, int threads, int smem, cudaStream_t s) {
@@ -695,7 +697,7 @@ static cudaError_t launch_rows(A a, long long row_bytes, int threads, int smem, 
     unsigned lg = 0;
     long long best = 0;
     for (unsigned l = 0; l < 4 && fit.fit[l] > 0; ++l) {
-        const long long cost = (a.M + fit.fit[l] - 1) / fit.fit[l] * ((row_bytes >> l) + 8192);
+        const long long cost = (a.M + fit.fit[l] - 1) / fit.fit[l] * ((row_bytes >> l) + 32768);
         if (l == 0 || cost < best) {
             best = cost;
             lg = l;
