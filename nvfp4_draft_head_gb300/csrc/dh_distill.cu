@@ -268,11 +268,11 @@ __global__ void __launch_bounds__(kThreads, kPerSm) distill_kernel(const Distill
                 stream.fetch();
                 slot = St::next(slot);
                 const int n = sl.v1 - sl.v0 - b * (kUnroll * kThreads) - tid;   // vectors left from this one on
+                if (some && !plain) {
 #pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    float x[kVec];
-                    Elem<T>::unpack(v[u], x);
-                    if (!kStats || !plain) {
+                    for (int u = 0; u < kUnroll; ++u) {
+                        float x[kVec];
+                        Elem<T>::unpack(v[u], x);
 #pragma unroll
                         for (int j = 0; j < kVec; j += 2) {
                             uint64_t y = fma_f32x2(pack_f32x2(x[j], x[j + 1]), mul2, add2);
@@ -281,13 +281,18 @@ __global__ void __launch_bounds__(kThreads, kPerSm) distill_kernel(const Distill
                             unpack_f32x2(y, y0, y1);
                             unpack_f32x2(mul_f32x2(pack_f32x2(ex2(y0), ex2(y1)), scale2), x[j], x[j + 1]);
                         }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < kVec; ++j) x[j] = scale * ex2((x[j] - all.m) * c);
+                        if (u * kThreads < n) store_vec<T>(out + u * (kThreads * kVec), Elem<T>::pack(x), vec_out);
                     }
-                    uint4 g = Elem<T>::pack(x);
-                    if (!some) g = make_uint4(0, 0, 0, 0);
-                    if (u * kThreads < n) store_vec<T>(out + u * (kThreads * kVec), g, vec_out);
+                } else {   // a row out of use, or summed in the plain form
+#pragma unroll 1
+                    for (int u = 0; u * kThreads < n && u < kUnroll; ++u) {
+                        const uint4 w = u == 0 ? v[0] : u == 1 ? v[1] : u == 2 ? v[2] : v[3];
+                        float x[kVec];
+                        Elem<T>::unpack(w, x);
+#pragma unroll
+                        for (int j = 0; j < kVec; ++j) x[j] = some ? wtq(x[j]) : 0.0f;
+                        store_vec<T>(out + u * (kThreads * kVec), Elem<T>::pack(x), vec_out);
+                    }
                 }
             }
             if (edge >= 0) dz[edge] = Elem<T>::store(some ? wtq(ze) : 0.0f);

@@ -13,7 +13,7 @@
 // the statistics. A value T that at least k of a CTA's 256 thread maxima reach
 // is a lower bound on the CTA's k-th largest logit, so only the vectors of the
 // threads whose maximum reaches T can hold one of its top k. T is found bit by
-// bit stopping at a count of up to k + k/2 + 4; those
+// bit stopping at a count of up to k + k/8 + 2; those
 // threads' vectors (about k/256 of the slice, still in L2) are read again by the
 // whole CTA, elements >= T become candidates, and the rank of each among
 // the candidates is counted. Candidates are 64-bit keys (ordered value, then
@@ -162,7 +162,7 @@ __device__ __noinline__ void radix_top(LogprobSmem& sm, const T* z, int lo, int 
 }
 
 // A bound that at least k of the CTA's keys (a maximum per thread) reach, and that at
-// most k + k/2 + 4 reach where the keys allow it; 0 where fewer than k lie above
+// most k + k/8 + 2 reach where the keys allow it; 0 where fewer than k lie above
 // `floor_key`. The first warp looks for it bit by bit, from the bits that all keys
 // above the floor share: a count of 256 keys in one warp's registers is a few
 // instructions, where a barrier per bit cost 20 us a row at the worst.
@@ -189,7 +189,7 @@ __device__ __forceinline__ uint32_t kth_bound(LogprobSmem& sm, uint32_t key, int
             int bit = 31 - __clz(static_cast<int>(lo ^ hi));
             t = bit >= 31 ? 0u : lo >> (bit + 1) << (bit + 1);
 #pragma unroll 1
-            for (; bit >= 0 && n > k + k / 2 + 4; --bit) {
+            for (; bit >= 0 && n > k + k / 8 + 2; --bit) {
                 const uint32_t up = t | (1u << bit);
                 int c = 0;
 #pragma unroll
