@@ -34,7 +34,7 @@ namespace rows {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;    // vectors per batch and thread
-constexpr int kDepth = 4;     // batches in flight: 64 KB per CTA
+constexpr int kDepth = 2;     // batches in flight: 32 KB per CTA
 constexpr int kPerSm = 3;     // CTAs per SM
 
 struct DistillSmem {
