@@ -21,8 +21,26 @@
 // weight rows. One thread streams blocks into a ring of shared-memory stages;
 // four warps, one per group of 32 lanes of tensor memory, move a stage's scales
 // there through registers; one thread issues the matrix instructions
-// (kind::mxf4nvf4, block 16); eight warps read a tile's accumulators into
+// (kind::mxf4nvf4, block 16); sixteen warps read a tile's accumulators into
 // registers, scaled and rounded, free them for the next tile and store.
+//
+// Bound, 8,192 tokens on a 64,064 x 2,560 head (602 us with the quantiser's 20:
+// 4.5 PFLOP/s; 1.05 GB of results alone take 155 us at the measured copy rate):
+// the operands' way from L2. Each tile loads 55 KB per 128 x 256 x 256 step, 8.9 TB in
+// all; with the matrix instructions taken out the kernel takes 536 us, with the
+// loads taken out 524, with both and the scales out 363 (figures at 652 us). What
+// the choices measured there:
+//  - scales: tcgen05.cp takes its turn among the matrix instructions (24 ns a copy,
+//    12 copies against 270 ns of matrix instructions per stage); stored from
+//    registers while the stages before multiply: 1,067 -> 703 us (with eight
+//    epilogue warps that free the accumulators before they store, not four after);
+//  - sixteen epilogue warps (a shorter read of the single accumulator buffer): 653;
+//  - results stored past L1, whose data array the ring shares: 620; both operands
+//    kept in L2 against the results (evict_last): 600;
+//  - pairs of CTAs on one 256 x 256 tile (cta_group::2) need a third less of the
+//    operands, but each ring slot's round trip crosses the pair twice: 913, with the
+//    scales through registers 1,021; operands multicast in clusters of four and
+//    eight 971 to 1,163.
 #include <atomic>
 #include <cfloat>
 
@@ -109,7 +127,9 @@ __device__ __forceinline__ void load16(const T* p, float (&x)[16]) {
 // One CTA per token: the row's largest magnitude (as bits, so that NaN and
 // infinities come out on top), then codes and scales, one 32-wide piece per thread.
 // A row with a value that is not finite gets the scale NaN and zero codes:
-// its whole result is NaN.
+// its whole result is NaN. Bound by latency: 3 us for 100 rows of 2,560, 20 us for
+// 8,192 (42 MB read, 12 written: 2.7 TB/s; the second reading comes from L1). Rows
+// held in registers between the two readings cost occupancy: 21.5 us.
 template <class T, bool VEC>
 __global__ void __launch_bounds__(kQThreads) quantize_kernel(const T* __restrict__ x, long long ldx, int K, uint8_t* __restrict__ out,
                                                              float* __restrict__ scale) {
@@ -440,9 +460,18 @@ static cudaError_t launch_quantize(const void* x, long long ldx, int M, int K, u
 
 template <class TY>
 static cudaError_t launch_tiles(const Args& a, cudaStream_t s) {
-    // wide tiles read fewer operand bytes per product; narrow ones spread a small product over more SMs
-    const long long wide = static_cast<long long>(a.tiles_m) * blocks_of(a.N, 256);
-    return wide >= sm_count() ? launch_product<TY, 256>(a, s) : launch_product<TY, 128>(a, s);
+    // Wide tiles read fewer operand bytes per product, narrow ones spread a small
+    // product over more SMs. By rounds of tiles times the tile's width, wide where that
+    // is at most an eighth more (us, wide / narrow): 8,192 x 64,064 x 2,560 602 / 745,
+    // 517 x 4,608 x 2,560 11.6 / 13.4 (one round against two), 32 x 2,560 x 5,120
+    // 14.8 / 13.3, 100 x 64,064 x 2,560 26.7 / 27.0.
+    const int sms = sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    const auto cost = [&](int tn) {
+        const long long tiles = static_cast<long long>(a.tiles_m) * blocks_of(a.N, tn);
+        return (tiles + sms - 1) / sms * tn;
+    };
+    return 8 * cost(256) <= 9 * cost(128) ? launch_product<TY, 256>(a, s) : launch_product<TY, 128>(a, s);
 }
 
 }  // namespace mm

@@ -675,9 +675,10 @@ static cudaError_t row_launch_setup(int threads, int smem, RowLaunch& out) {
 
 // Launch a persistent kernel over M rows. CTAs per row, by the time of the
 // longest-working CTA: rounds of rows that a cluster takes times its CTA's share
-// of a row, plus for each round a fixed cost worth 32 KB of reading
-// (about 2 us). Few rows are so
-// split over up to 8 CTAs, and a number of rows that fills its last round badly in two.
+// of a row, plus for each round a fixed cost worth 32 KB of reading (about 2 us). Few
+// rows are so split over up to 8 CTAs (16 rows of 248,320 f32 over 8: 16.6 us), and
+// rows that fill the GPU are not (268 rows of 34,166 bf16, 20 alternatives: 11.0 us
+// unsplit, 32 us over clusters of four in three rounds).
 template <class A, void (*KERNEL)(A)>
 static cudaError_t launch_rows(A a, long long row_bytes, int threads, int smem, cudaStream_t s) {
     constexpr int kDevices = 64;
