@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) distill_kernel(const Distill
 
         // the statistics of the slice
         Stat all = {a.floor, 0.0f, 0.0f};
+        float top = ze;
         if (kStats) {
             for (int b = 0; b < batches; ++b) {
                 cp_async_wait<kDepth - 1>();
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) distill_kernel(const Distill
                 stream.read(slot, sl, b, v);
                 stream.fetch();
                 slot = St::next(slot);
-                stat_add<T, false, kUnroll>(all, v, c, a.floor2);
+                stat_add<T, false, kUnroll>(all, top, v, c, a.floor2);
             }
             if (edge >= 0) stat_add1<false>(all, ze, c, a.floor);
             stat_leave(stat_warp<false, false>(all, c), sm.warp[turn]);
@@ -216,10 +217,13 @@ __global__ void __launch_bounds__(kThreads, kPerSm) distill_kernel(const Distill
             all = stat_gather<false, false>(kWarps, c, sm.warp[turn], a.floor);
             all = stat_cluster<false, false>(all, c, sm.cta[turn], rank, ncta);
             plain = !stat_fits(all.m, c, a.floor);
-            if (plain) {
-                float top;
-                all = plain_slice<T, false, kThreads>(z, sl, ze, c, sm.plain, top);
-                all = stat_cluster<false, true>(all, c, sm.cta_plain, rank, ncta);
+            if (plain) {   // masked throughout (and no NaN), or summed in the plain form
+                if (row_top<kThreads>(top, sm.plain, sm.cta_plain, rank, ncta) == kNegInf && all.s == all.s) {
+                    all = Stat{0.0f, 0.0f, 0.0f};
+                } else {
+                    all = plain_slice<T, false, kThreads>(z, sl, ze, c, sm.plain);
+                    all = stat_cluster<false, true>(all, c, sm.cta_plain, rank, ncta);
+                }
             }
         } else if (ncta > 1) {   // no CTA writes its slice before all have read theirs from it
             cluster_arrive_release();

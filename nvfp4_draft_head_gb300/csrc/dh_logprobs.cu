@@ -19,8 +19,8 @@
 // the candidates is counted. Candidates are 64-bit keys (ordered value, then
 // the complement of the column), so equal logits go to the lowest column and
 // the arrival order does not matter. More than kCand candidates (rows of many
-// equal values), a NaN, or too few logits above the floor of the statistics
-// send the CTA to an exact radix selection over its slice instead. The CTAs' sorted lists are merged by the first CTA.
+// equal values) or a NaN send the CTA to an exact radix selection over its slice
+// instead. The CTAs' sorted lists are merged by the first CTA.
 //
 // Bound: instruction issue. 4,096 rows of 64,026 bf16, 20 alternatives: 131 us, 4.0 of
 // the measured 6.8 TB/s (78 us); 7 instructions per 32 logits go into the statistics,
@@ -172,10 +172,11 @@ __device__ __noinline__ void radix_top(LogprobSmem& sm, const T* z, int lo, int 
 
 // A bound that at least k of the CTA's keys (a maximum per thread) reach, and that at
 // most k + k/8 + 2 reach where the keys allow it; 0 where fewer than k lie above
-// `floor_key`. The first warp looks for it bit by bit, from the bits that all keys
-// above the floor share: a count of 256 keys in one warp's registers is a few
+// -inf. The first warp looks for it bit by bit, from the bits that all keys above
+// -inf share: a count of 256 keys in one warp's registers is a few
 // instructions, where a barrier per bit is tens of cycles (4,096 x 64,026: 143 -> 137 us).
-__device__ __forceinline__ uint32_t kth_bound(LogprobSmem& sm, uint32_t key, int k, uint32_t floor_key) {
+__device__ __forceinline__ uint32_t kth_bound(LogprobSmem& sm, uint32_t key, int k) {
+    const uint32_t floor_key = ordered_key(kNegInf);
     sm.key[threadIdx.x] = key;
     __syncthreads();
     if (threadIdx.x < 32) {
@@ -216,30 +217,21 @@ __device__ __forceinline__ uint32_t kth_bound(LogprobSmem& sm, uint32_t key, int
     return sm.bound;
 }
 
-// The CTA's k largest logits into sm.top. `mx` is this thread's largest logit, or
-// the floor where it has none above that; `ze` its edge logit (or -inf).
+// The CTA's k largest logits into sm.top. `mx` is this thread's largest logit and `ze`
+// its edge logit (-inf: none).
 template <class T>
-__device__ __forceinline__ void cta_top(LogprobSmem& sm, const T* z, const Slice& sl, int edge, float ze, float mx, float floor,
-                                        bool nan, int k) {
+__device__ __forceinline__ void cta_top(LogprobSmem& sm, const T* z, const Slice& sl, int edge, float ze, float mx, bool nan,
+                                        int k) {
     constexpr int kVec = Elem<T>::kVec;
     if (nan) {
         radix_top(sm, z, sl.lo, sl.hi, k);
         return;
     }
-    uint32_t key = ordered_key(mx), bound_key = 0;
+    const uint32_t key = ordered_key(mx);
+    uint32_t bound_key = 0;
     if (threadIdx.x == 0) sm.n_active = sm.n_cand = 0;
     if (sl.hi - sl.lo > kFew) {
-        bound_key = kth_bound(sm, key, k, ordered_key(floor));
-        if (bound_key == 0) {   // too few above the floor; a maximum at it may be anything below: take them anew
-            float top = ze;
-            for (int v = sl.v0 + threadIdx.x; v < sl.v1; v += kThreads) {
-                const uint4 w[1] = {ld_stream_v4(z + sl.head + static_cast<size_t>(v) * kVec)};
-                top = fmaxf(top, Elem<T>::template max_of<1>(w));
-            }
-            key = ordered_key(top);
-            __syncthreads();   // sm.bound has been read
-            bound_key = kth_bound(sm, key, k, ordered_key(kNegInf));
-        }
+        bound_key = kth_bound(sm, key, k);
     }
     __syncthreads();
     // the threads that reach the bound, each warp's in a row
@@ -326,6 +318,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) token_logprobs_kernel(const 
         if (edge >= 0) ze = Elem<T>::load(z + edge);
 
         Stat st = {a.floor, 0.0f, 0.0f};
+        float top = ze;
         const int batches = St::batches_of(sl);
         for (int b = 0; b < batches; ++b) {
             cp_async_wait<kDepth - 1>();
@@ -333,11 +326,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) token_logprobs_kernel(const 
             stream.read(slot, sl, b, w);
             stream.fetch();
             slot = St::next(slot);
-            stat_add<T, true, kUnroll>(st, w, c, a.floor2);
+            stat_add<T, true, kUnroll>(st, top, w, c, a.floor2);
         }
         if (edge >= 0) stat_add1<true>(st, ze, c, a.floor);
 
-        float top = st.m;
         stat_leave(stat_warp<true, false>(st, c), sm.warp[turn]);
         __syncthreads();
         const Stat mine = stat_gather<true, false>(kWarps, c, sm.warp[turn], a.floor);
@@ -346,11 +338,16 @@ __global__ void __launch_bounds__(kThreads, kPerSm) token_logprobs_kernel(const 
         if (stat_fits(all.m, c, a.floor)) {
             rest = shift_rest(all.m, c);
         } else {
-            all = plain_slice<T, true, kThreads>(z, sl, ze, c, sm.plain, top);
-            all = stat_cluster<true, true>(all, c, sm.cta_plain, rank, ncta);
+            // masked throughout (and no NaN), or summed in the plain form
+            if (row_top<kThreads>(top, sm.plain, sm.cta_plain, rank, ncta) == kNegInf && all.s == all.s) {
+                all = Stat{0.0f, 0.0f, 0.0f};
+            } else {
+                all = plain_slice<T, true, kThreads>(z, sl, ze, c, sm.plain);
+                all = stat_cluster<true, true>(all, c, sm.cta_plain, rank, ncta);
+            }
         }
         if (a.k > 0) {
-            cta_top(sm, z, sl, edge, ze, top, a.floor, mine.s != mine.s, a.k);
+            cta_top(sm, z, sl, edge, ze, top, mine.s != mine.s, a.k);
             if (ncta > 1) {
                 for (int i = threadIdx.x; i < a.k; i += kThreads)
                     st_cluster_u64(cluster_map(&sm.peers[turn][rank][i], 0), sm.top[i]);

@@ -270,13 +270,15 @@ __device__ __forceinline__ Stat stat_join(Stat a, Stat b, float c) {
 
 // Add U vectors to st (st.m >= floor throughout): one shift of the sums, then
 // a multiply-add, an exponential and an addition per logit, all but the
-// exponential on pairs (with the entropy, another multiply-add; there the logits are raised to the floor first, so that
-// a zero never meets an infinite exponent). The maximum is taken on packed
-// pairs of 16-bit logits.
+// exponential on pairs (with the entropy, another multiply-add; there the logits
+// are raised to the floor first, so that a zero never meets an infinite
+// exponent). The maximum is taken on packed pairs of 16-bit logits; `top` is the
+// thread's largest logit itself, below the floor too (-inf: none).
 template <class T, bool ENTROPY, int U>
-__device__ __forceinline__ void stat_add(Stat& st, uint4 (&w)[U], float c, uint32_t floor2) {
+__device__ __forceinline__ void stat_add(Stat& st, float& top, uint4 (&w)[U], float c, uint32_t floor2) {
     constexpr int kVec = Elem<T>::kVec;
-    float m = fmaxf(st.m, Elem<T>::template max_of<U>(w));
+    top = fmaxf(top, Elem<T>::template max_of<U>(w));
+    const float m = fmaxf(st.m, top);
     if (ENTROPY) {
 #pragma unroll
         for (int u = 0; u < U; ++u) Elem<T>::raise(w[u], floor2);
@@ -452,14 +454,33 @@ __device__ __forceinline__ int column_of(int id, const int32_t* row_of, int V, i
     return id >= 0 && id < C ? id : -1;
 }
 
+// The largest of the threads' `top` over the row (every thread of its cluster calls
+// this; rare). buf and all as for the row's statistics.
+template <int NT>
+__device__ __noinline__ float row_top(float top, float (*buf)[3], float (*all)[3], unsigned rank, unsigned ncta) {
+    const float w = warp_max(top);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5][0] = w;
+    __syncthreads();
+    float m = warp_max(buf[(threadIdx.x & 31) % (NT / 32)][0]);
+    __syncthreads();
+    if (ncta > 1) {
+        if (threadIdx.x < ncta) st_cluster_f32(cluster_map(&all[rank][0], threadIdx.x), m);
+        cluster_arrive_release();
+        cluster_wait_acquire();
+        for (unsigned i = 0; i < ncta; ++i) m = fmaxf(m, all[i][0]);
+        cluster_arrive_release();   // read before the entries are written again
+        cluster_wait_acquire();
+    }
+    return m;
+}
+
 // The statistics of a CTA's slice in the plain form, from global memory (rows that
-// stat_fits() refuses; rare), and the thread's largest logit of the vectors that it
-// owns in a stream of NT threads and of its edge logit `ze` (-inf: none).
+// stat_fits() refuses and that are not masked throughout; rare).
 template <class T, bool ENTROPY, int NT>
-__device__ __noinline__ Stat plain_slice(const T* z, const Slice& sl, float ze, float c, float (*buf)[3], float& top) {
+__device__ __noinline__ Stat plain_slice(const T* z, const Slice& sl, float ze, float c, float (*buf)[3]) {
     constexpr int kVec = Elem<T>::kVec, U = 4;
     Stat st = {-FLT_MAX, 0.0f, 0.0f};
-    top = ze;
     plain_add1<ENTROPY>(st, ze, c);
     for (int v0 = sl.v0 + threadIdx.x; v0 < sl.v1; v0 += U * NT) {
         uint4 w[U];
@@ -467,7 +488,6 @@ __device__ __noinline__ Stat plain_slice(const T* z, const Slice& sl, float ze, 
         for (int u = 0; u < U; ++u)
             w[u] = v0 + u * NT < sl.v1 ? *reinterpret_cast<const uint4*>(z + sl.head + static_cast<size_t>(v0 + u * NT) * kVec)
                                        : neg_inf_vec<T>();
-        top = fmaxf(top, Elem<T>::template max_of<U>(w));
         plain_add<T, ENTROPY, U>(st, w, c);
     }
     st = stat_warp<ENTROPY, true>(st, c);
