@@ -695,10 +695,12 @@ static cudaError_t row_launch_setup(int threads, int smem, RowLaunch& out) {
 
 // Launch a persistent kernel over M rows. CTAs per row, by the time of the
 // longest-working CTA: rounds of rows that a cluster takes times its CTA's share
-// of a row, plus for each round a fixed cost worth 32 KB of reading (about 2 us). Few
-// rows are so split over up to 8 CTAs (16 rows of 248,320 f32 over 8: 16.6 us), and
-// rows that fill the GPU are not (268 rows of 34,166 bf16, 20 alternatives: 11.0 us
-// unsplit, 32 us over clusters of four in three rounds).
+// of a row, plus for each round a fixed cost worth 32 KB of reading (about 2 us) and
+// for a cluster's exchanges and launch worth another 48 KB. Few long rows are so
+// split over up to 8 CTAs (16 rows of 248,320 f32 over 8: 13.5 us), and rows that fill
+// the GPU or are short are not (20 alternatives of 268 rows of 34,166 bf16: 9.9 us
+// unsplit, 32 over clusters of four in three rounds; of 4 rows of 2,743 f32: 6.6
+// unsplit, 10.5 over eight).
 template <class A, void (*KERNEL)(A)>
 static cudaError_t launch_rows(A a, long long row_bytes, int threads, int smem, cudaStream_t s) {
     constexpr int kDevices = 64;
@@ -718,7 +720,7 @@ static cudaError_t launch_rows(A a, long long row_bytes, int threads, int smem, 
     unsigned lg = 0;
     long long best = 0;
     for (unsigned l = 0; l < 4 && fit.fit[l] > 0; ++l) {
-        const long long cost = (a.M + fit.fit[l] - 1) / fit.fit[l] * ((row_bytes >> l) + 32768);
+        const long long cost = (a.M + fit.fit[l] - 1) / fit.fit[l] * ((row_bytes >> l) + 32768 + (l > 0 ? 49152 : 0));
         if (l == 0 || cost < best) {
             best = cost;
             lg = l;
