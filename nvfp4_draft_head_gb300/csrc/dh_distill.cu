@@ -325,8 +325,10 @@ template <class T, DistillMode MODE>
 static cudaError_t launch(const DistillArgs& a, cudaStream_t s) {
     using St = Stream<T, kThreads, kUnroll, kDepth>;
     const long long bytes = static_cast<long long>(a.C) * sizeof(T);
-    if (a.K <= kThreads) return launch_rows<DistillArgs, distill_kernel<T, MODE, 1>>(a, bytes, kThreads, St::kBytes, s);
-    return launch_rows<DistillArgs, distill_kernel<T, MODE, 2>>(a, bytes, kThreads, St::kBytes, s);
+    // (the loss alone is split as the loss with its gradient, so that both give the same sums)
+    const RowCost cost = {16 << 10, 16 << 10, MODE != kDistillBackward};
+    if (a.K <= kThreads) return launch_rows<DistillArgs, distill_kernel<T, MODE, 1>>(a, bytes, cost, kThreads, St::kBytes, s);
+    return launch_rows<DistillArgs, distill_kernel<T, MODE, 2>>(a, bytes, cost, kThreads, St::kBytes, s);
 }
 
 template <class T>

@@ -406,7 +406,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) token_logprobs_kernel(const 
 template <class T>
 static cudaError_t launch(const LogprobArgs& a, cudaStream_t s) {
     using St = Stream<T, kThreads, kUnroll, kDepth>;
-    return launch_rows<LogprobArgs, token_logprobs_kernel<T>>(a, static_cast<long long>(a.C) * sizeof(T), kThreads, St::kBytes, s);
+    return launch_rows<LogprobArgs, token_logprobs_kernel<T>>(a, static_cast<long long>(a.C) * sizeof(T), RowCost{32 << 10, 48 << 10, false},
+                                                             kThreads, St::kBytes, s);
 }
 
 }  // namespace rows

@@ -693,16 +693,26 @@ static cudaError_t row_launch_setup(int threads, int smem, RowLaunch& out) {
     return e;
 }
 
+// Costs of a row beyond reading it, in bytes read in the same time: `fixed` for
+// its ends, `exchange` more where a cluster shares it; `twice`: the row is streamed
+// twice, from L2 the second time if the rows in work fit there.
+struct RowCost {
+    long long fixed, exchange;
+    bool twice;
+};
+constexpr long long kRowsInL2 = 64ll << 20;   // of the 129 MB, beside what is written
+
 // Launch a persistent kernel over M rows. CTAs per row, by the time of the
 // longest-working CTA: rounds of rows that a cluster takes times its CTA's share
-// of a row, plus for each round a fixed cost worth 32 KB of reading (about 2 us) and
-// for a cluster's exchanges and launch worth another 48 KB. Few long rows are so
-// split over up to 8 CTAs (16 rows of 248,320 f32 over 8: 13.5 us), and rows that fill
-// the GPU or are short are not (20 alternatives of 268 rows of 34,166 bf16: 9.9 us
-// unsplit, 32 over clusters of four in three rounds; of 4 rows of 2,743 f32: 6.6
-// unsplit, 10.5 over eight).
+// of a row (half as much again for a row streamed twice that does not stay in L2)
+// and its costs. Few long rows are so split over up to 8 CTAs (16 rows of 248,320
+// f32, log-probabilities: 13.5 us), long rows streamed twice over as many as keep
+// them in L2 (573 rows of 228,680 f32, loss and gradient: 203 us over eight CTAs, 260 unsplit;
+// 1,200 of 128,000 bf16: 123 over two, 142), and rows that fill the GPU or are short are not split
+// (20 alternatives of 268 rows of 34,166 bf16: 9.9 us unsplit, 32 over clusters
+// of four in three rounds; of 4 rows of 2,743 f32: 6.6 unsplit, 10.5 over eight).
 template <class A, void (*KERNEL)(A)>
-static cudaError_t launch_rows(A a, long long row_bytes, int threads, int smem, cudaStream_t s) {
+static cudaError_t launch_rows(A a, long long row_bytes, RowCost c, int threads, int smem, cudaStream_t s) {
     constexpr int kDevices = 64;
     static std::atomic<bool> known[kDevices];
     static RowLaunch info[kDevices];   // written with equal values by concurrent first callers
@@ -720,7 +730,10 @@ static cudaError_t launch_rows(A a, long long row_bytes, int threads, int smem, 
     unsigned lg = 0;
     long long best = 0;
     for (unsigned l = 0; l < 4 && fit.fit[l] > 0; ++l) {
-        const long long cost = (a.M + fit.fit[l] - 1) / fit.fit[l] * ((row_bytes >> l) + 32768 + (l > 0 ? 49152 : 0));
+        const long long rounds = (a.M + fit.fit[l] - 1) / fit.fit[l];
+        const bool spills = c.twice && (a.M < fit.fit[l] ? a.M : fit.fit[l]) * row_bytes > kRowsInL2;
+        const long long share = row_bytes >> l;
+        const long long cost = rounds * ((spills ? share + share / 2 : share) + c.fixed + (l > 0 ? c.exchange : 0));
         if (l == 0 || cost < best) {
             best = cost;
             lg = l;
