@@ -269,8 +269,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
 
     if (warp == kEpiWarps + kSfWarps && lane == 0) {
         // producer: the blocks of every k-stage of every tile of this CTA
-        uint64_t keep;   // operands stay in L2 against the stream of results
+        // operands that other tiles read too stay in L2 against the stream of results; weights
+        // for one row of tiles are read once
+        uint64_t keep, weights;
         asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+        weights = a.tiles_m > 1 ? keep : policy_evict_first();
         const int blocks_n = blocks_of(a.N, kRows);
         uint32_t it = 0;
         bool ok = true;
@@ -286,8 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
                 bulk_g2s(st, src_a, kBlock, &sy.full[s], keep);
                 for (int j = 0; j < nb; ++j) {   // codes of the weight blocks side by side, then their scales
                     const uint8_t* src = src_b + static_cast<size_t>(j) * a.nk * kBlock;
-                    bulk_g2s(st + C::kB + j * kCodes, src, kCodes, &sy.full[s], keep);
-                    bulk_g2s(st + C::kSf + j * kScales, src + kCodes, kScales, &sy.full[s], keep);
+                    bulk_g2s(st + C::kB + j * kCodes, src, kCodes, &sy.full[s], weights);
+                    bulk_g2s(st + C::kSf + j * kScales, src + kCodes, kScales, &sy.full[s], weights);
                 }
             }
         }
