@@ -275,22 +275,29 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
         asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
         weights = a.tiles_m > 1 ? keep : policy_evict_first();
         const int blocks_n = blocks_of(a.N, kRows);
-        uint32_t it = 0;
+        // (this thread is on the way of every stage's refill: pointers and phases run along)
+        const size_t next_block = static_cast<size_t>(a.nk) * kBlock;
+        uint32_t it = 0, s = 0, phase = 1;   // the phase of `empty` before the current use of the slot
         bool ok = true;
         for (int tile = first; ok && tile < tiles; tile += stride) {
             const int tm = tile % a.tiles_m, tn = tile / a.tiles_m, nb = min(C::kNB, blocks_n - tn * C::kNB);
-            const uint8_t* src_a = a.a + static_cast<size_t>(tm) * a.nk * kBlock;
-            const uint8_t* src_b = a.b + static_cast<size_t>(tn * C::kNB) * a.nk * kBlock;
-            for (int k = 0; k < a.nk; ++k, ++it, src_a += kBlock, src_b += kBlock) {
-                const uint32_t s = it % kStages, use = it / kStages;
-                if (use > 0 && !(ok = wait_or_abort(sy, &sy.empty[s], (use - 1) & 1, a))) break;
+            const uint32_t bytes = static_cast<uint32_t>(kBlock * (1 + nb));
+            const uint8_t* src_a = a.a + static_cast<size_t>(tm) * next_block;
+            const uint8_t* src_b = a.b + static_cast<size_t>(tn * C::kNB) * next_block;
+            const uint8_t* src_c = src_b + next_block;   // the second weight block
+            for (int k = 0; k < a.nk; ++k, ++it, src_a += kBlock, src_b += kBlock, src_c += kBlock) {
+                if (it >= static_cast<uint32_t>(kStages) && !(ok = wait_or_abort(sy, &sy.empty[s], phase, a))) break;
                 uint8_t* st = smem + s * C::kStageBytes;
-                mbar_arrive_expect_tx(&sy.full[s], static_cast<uint32_t>(kBlock * (1 + nb)));
+                mbar_arrive_expect_tx(&sy.full[s], bytes);
                 bulk_g2s(st, src_a, kBlock, &sy.full[s], keep);
-                for (int j = 0; j < nb; ++j) {   // codes of the weight blocks side by side, then their scales
-                    const uint8_t* src = src_b + static_cast<size_t>(j) * a.nk * kBlock;
-                    bulk_g2s(st + C::kB + j * kCodes, src, kCodes, &sy.full[s], weights);
-                    bulk_g2s(st + C::kSf + j * kScales, src + kCodes, kScales, &sy.full[s], weights);
+                // codes of the weight blocks side by side, then their scales
+                bulk_g2s(st + C::kB, src_b, kCodes, &sy.full[s], weights);
+                if (nb > 1) bulk_g2s(st + C::kB + kCodes, src_c, kCodes, &sy.full[s], weights);
+                bulk_g2s(st + C::kSf, src_b + kCodes, kScales, &sy.full[s], weights);
+                if (nb > 1) bulk_g2s(st + C::kSf + kScales, src_c + kCodes, kScales, &sy.full[s], weights);
+                if (++s == static_cast<uint32_t>(kStages)) {
+                    s = 0;
+                    phase ^= 1u;
                 }
             }
         }
