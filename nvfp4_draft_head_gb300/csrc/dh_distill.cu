@@ -267,6 +267,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) distill_kernel(const Distill
                 if (!kStats) return scale * ex2(fmaf(x, a.inv_t, -lse) * kLog2e);
                 return scale * ex2(plain ? (x - all.m) * c : fmaf(x, c, nmc));
             };
+            // (S itself for the teacher's columns, where q meets p: 2^rest taken off)
+            const float sum_t = kStats && teacher && !plain ? all.s * expf(-shift_rest(all.m, c) * kLn2) : all.s;
             const bool vec_out = ((reinterpret_cast<uintptr_t>(dz) ^ reinterpret_cast<uintptr_t>(z)) & 15u) == 0;
             const uint64_t mul2 = kStats ? pack_f32x2(c, c) : pack_f32x2(a.inv_t, a.inv_t);
             const uint64_t add2 = kStats ? pack_f32x2(nmc, nmc) : pack_f32x2(-lse, -lse), scale2 = pack_f32x2(scale, scale);
@@ -309,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) distill_kernel(const Distill
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 end.col[e] = used[e] && col[e] >= sl.lo && col[e] < sl.hi ? col[e] : -1;
-                end.base[e] = wtq(zt[e]);
+                end.base[e] = kStats ? wt * expf((zt[e] - all.m) * a.inv_t) / sum_t : wtq(zt[e]);
             }
             end.wt = wt;
             end.dz = dz;

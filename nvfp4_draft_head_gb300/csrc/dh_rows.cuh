@@ -286,7 +286,7 @@ __device__ __forceinline__ void stat_add(Stat& st, float& top, uint4 (&w)[U], fl
     stat_shift<ENTROPY>(st, m, c);
     const float mc = shift_of(m, c);
     const uint64_t c2 = pack_f32x2(c, c), nmc2 = pack_f32x2(-mc, -mc);
-    uint64_t s = pack_f32x2(st.s, 0.0f), s1 = pack_f32x2(st.s1, 0.0f);
+    uint64_t s[2] = {0, 0}, s1[2] = {0, 0};   // of these vectors alone: few roundings at the size of the running sum
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         float z[kVec];
@@ -297,16 +297,16 @@ __device__ __forceinline__ void stat_add(Stat& st, float& top, uint4 (&w)[U], fl
             float x0, x1;
             unpack_f32x2(x, x0, x1);
             const uint64_t e = pack_f32x2(ex2(x0), ex2(x1));
-            s = add_f32x2(s, e);
-            if (ENTROPY) s1 = fma_f32x2(e, x, s1);
+            s[(i >> 1) & 1] = add_f32x2(s[(i >> 1) & 1], e);
+            if (ENTROPY) s1[(i >> 1) & 1] = fma_f32x2(e, x, s1[(i >> 1) & 1]);
         }
     }
     float lo, hi;
-    unpack_f32x2(s, lo, hi);
-    st.s = lo + hi;
+    unpack_f32x2(add_f32x2(s[0], s[1]), lo, hi);
+    st.s += lo + hi;
     if (ENTROPY) {
-        unpack_f32x2(s1, lo, hi);
-        st.s1 = lo + hi;
+        unpack_f32x2(add_f32x2(s1[0], s1[1]), lo, hi);
+        st.s1 += lo + hi;
     }
 }
 
