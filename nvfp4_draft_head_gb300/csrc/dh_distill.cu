@@ -24,9 +24,9 @@
 // from L2, where the rows in work (three per SM) fit.
 //
 // Bound: instruction issue, near HBM. Loss and gradient of 4,096 rows of 64,026 bf16:
-// 201 us, 5.2 of the measured 6.8 TB/s (155 us); 14 instructions per 32 logits and
+// 202 us, 5.2 of the measured 6.8 TB/s (155 us); 14 instructions per 32 logits and
 // 5,600 a row. The gradient alone, 256 rows of 248,320 f32: 84 us (75), the loss alone,
-// 1,021 rows of 64,026 bf16, a tenth of them masked throughout: 38 us (19). Three CTAs
+// 1,021 rows of 64,026 bf16, a tenth of them masked throughout: 30 us (19). Three CTAs
 // of 256 threads per SM (512 threads twice: 244 us; 256 threads twice 206, four
 // times 240). A row held whole in shared memory between its two passes, one CTA of
 // 512 or 1,024 threads per SM: 265 to 360 us, the ends of a row then run alone.

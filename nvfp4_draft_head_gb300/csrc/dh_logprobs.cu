@@ -22,16 +22,16 @@
 // equal values) or a NaN send the CTA to an exact radix selection over its slice
 // instead. The CTAs' sorted lists are merged by the first CTA.
 //
-// Bound: instruction issue. 4,096 rows of 64,026 bf16, 20 alternatives: 131 us, 4.0 of
-// the measured 6.8 TB/s (78 us); 7 instructions per 32 logits go into the statistics,
+// Bound: instruction issue. 4,096 rows of 64,026 bf16, 20 alternatives: 130 us, 4.0 of
+// the measured 6.8 TB/s (77 us); 7 instructions per 32 logits go into the statistics,
 // about 1.5 into reading the candidates' vectors again and 5,600 into a row's ends,
-// and the SMs issue in 53 of 100 cycles. Three CTAs of 256 threads per SM, so that
+// and the SMs issue in 56 of 100 cycles. Three CTAs of 256 threads per SM, so that
 // one row's ends run under the others' streaming (two CTAs of 512 threads: 169 us,
 // 256 threads twice 159, four times 149, 128 threads four times 183), with two batches of
 // four vectors in flight each (two vectors, four batches: 150; four and three: 169).
 // Steps: one kernel per row without a stream 164 us; logits streamed, exponents by
 // one multiply-add and sums in pairs 140; the k-th bound searched in one warp and
-// down to k + k/8 + 2 131. One row of 64,026 f32: 9.9 us, on 8 CTAs.
+// down to k + k/8 + 2 131. One row of 64,026 f32: 9.7 us, on 8 CTAs.
 #include "../../include/drafthead.h"
 #include "dh_internal.h"
 #include "dh_rows.cuh"

@@ -24,8 +24,8 @@
 // (kind::mxf4nvf4, block 16); sixteen warps read a tile's accumulators into
 // registers, scaled and rounded, free them for the next tile and store.
 //
-// Bound, 8,192 tokens on a 64,064 x 2,560 head (602 us with the quantiser's 20:
-// 4.5 PFLOP/s; 1.05 GB of results alone take 155 us at the measured copy rate):
+// Bound, 8,192 tokens on a 64,064 x 2,560 head (590 us with the quantiser's 20:
+// 4.6 PFLOP/s; 1.05 GB of results alone take 155 us at the measured copy rate):
 // the operands' way from L2. Each tile loads 55 KB per 128 x 256 x 256 step, 8.9 TB in
 // all; with the matrix instructions taken out the kernel takes 536 us, with the
 // loads taken out 524, with both and the scales out 363 (figures at 652 us). What
@@ -36,7 +36,8 @@
 //    epilogue warps that free the accumulators before they store, not four after);
 //  - sixteen epilogue warps (a shorter read of the single accumulator buffer): 653;
 //  - results stored past L1, whose data array the ring shares: 620; both operands
-//    kept in L2 against the results (evict_last): 600;
+//    kept in L2 against the results (evict_last): 600; the producer's pointers and
+//    phases running along: 590. 100 tokens: weights, read once, not kept 26.7 -> 24.6;
 //  - pairs of CTAs on one 256 x 256 tile (cta_group::2) need a third less of the
 //    operands, but each ring slot's round trip crosses the pair twice: 913, with the
 //    scales through registers 1,021; operands multicast in clusters of four and
@@ -474,7 +475,7 @@ static cudaError_t launch_tiles(const Args& a, cudaStream_t s) {
     // product over more SMs. By rounds of tiles times the tile's width, wide where that
     // is at most an eighth more (us, wide / narrow): 8,192 x 64,064 x 2,560 602 / 745,
     // 517 x 4,608 x 2,560 11.6 / 13.4 (one round against two), 32 x 2,560 x 5,120
-    // 14.8 / 13.3, 100 x 64,064 x 2,560 26.7 / 27.0.
+    // 14.8 / 13.3, 100 x 64,064 x 2,560 26.7 / 27.0 (before the last two steps above).
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     const auto cost = [&](int tn) {
