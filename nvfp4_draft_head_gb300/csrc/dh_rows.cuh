@@ -13,10 +13,11 @@
 //
 // That form needs |m c| small against 2^24 (r is up to 2^-24 of it, and is an
 // exponent), so the running maximum starts at the floor F = -2^k with |F c| in
-// (2^18, 2^20] and logits below F count as F. A row whose maximum is not well
-// above F (rows masked throughout, or filled with a type's lowest value), or
-// is above -F (infinities too), is summed again in the plain form 2^((z - m) c)
-// with the subtraction first (stat_plain), where any two finite values work.
+// (2^19, 2^20] and logits below F count as F. A row whose maximum is not well
+// above F (filled with a type's lowest value, say), or is above -F (infinities
+// too), is summed again in the plain form 2^((z - m) c) with the subtraction
+// first (stat_plain), where any two finite values work; a row masked throughout
+// is told by its maximum, and not read again.
 // A NaN makes s a NaN, and so does +inf, as exp(z - max) does.
 #pragma once
 
