@@ -20,16 +20,19 @@
 // Product kernel: persistent, one CTA per SM; output tiles of 128 tokens x TN
 // weight rows. One thread streams blocks into a ring of shared-memory stages;
 // four warps, one per group of 32 lanes of tensor memory, move a stage's scales
-// there through registers; one thread issues the matrix instructions
+// there through registers, two such groups in turn; one thread issues the matrix instructions
 // (kind::mxf4nvf4, block 16); sixteen warps read a tile's accumulators into
 // registers, scaled and rounded, free them for the next tile and store.
 //
-// Bound, 8,192 tokens on a 64,064 x 2,560 head (590 us with the quantiser's 20:
-// 4.6 PFLOP/s; 1.05 GB of results alone take 155 us at the measured copy rate):
-// the operands' way from L2. Each tile loads 55 KB per 128 x 256 x 256 step, 8.9 TB in
-// all; with the matrix instructions taken out the kernel takes 536 us, with the
-// loads taken out 524, with both and the scales out 363 (figures at 652 us). What
-// the choices measured there:
+// Bound, 8,192 tokens on a 64,064 x 2,560 head (565 us with the quantiser's 20:
+// 4.8 PFLOP/s; 1.05 GB of results alone take 155 us at the measured copy rate):
+// shared memory, by its arithmetic. Per 128 x 256 x 256 step it takes 55 KB from L2,
+// gives the matrix instructions 48 KB and the scale warps 24 KB (each of the four
+// reads all scales), 1,000 cycles at 128 bytes of the 1,000 that a step takes; the
+// matrix instructions alone take half of that. Tiles of 256 x 192 move a fifth less
+// from L2, but read as much of shared memory: 583 against 594, each with one group of
+// scale warps (their three slots do not go round between two).
+// What the choices measured there:
 //  - scales: tcgen05.cp takes its turn among the matrix instructions (24 ns a copy,
 //    12 copies against 270 ns of matrix instructions per stage); stored from
 //    registers while the stages before multiply: 1,067 -> 703 us (with eight
@@ -37,11 +40,13 @@
 //  - sixteen epilogue warps (a shorter read of the single accumulator buffer): 653;
 //  - results stored past L1, whose data array the ring shares: 620; both operands
 //    kept in L2 against the results (evict_last): 600; the producer's pointers and
-//    phases running along: 590. 100 tokens: weights, read once, not kept 26.7 -> 24.6;
+//    phases running along: 590; two groups of scale warps in turn (fewer held results
+//    for the registers): 565. 100 tokens: weights, read once, not kept 26.7 -> 24.6;
 //  - pairs of CTAs on one 256 x 256 tile (cta_group::2) need a third less of the
 //    operands, but each ring slot's round trip crosses the pair twice: 913, with the
 //    scales through registers 1,021; operands multicast in clusters of four and
-//    eight 971 to 1,163.
+//    eight 971 to 1,163; blocks of 128 k, twice as many stages of half the size, 763;
+//    the tokens' scales by tcgen05.cp, the weights' through registers 609.
 #include <atomic>
 #include <cfloat>
 
@@ -192,8 +197,9 @@ struct Args {
     unsigned int* error;    // DH_DEVERR_* word or null
 };
 
-constexpr int kEpiWarps = 16, kSfWarps = 4;
-constexpr int kThreads = 32 * (kEpiWarps + kSfWarps + 2);
+// Warps: epilogue, groups of scale warps that take the stages in turn, producer, issuer.
+constexpr int kEpiWarps = 16, kSfWarps = 4, kSfGroups = 2, kProducer = kEpiWarps + kSfGroups * kSfWarps, kIssuer = kProducer + 1;
+constexpr int kThreads = 32 * (kIssuer + 1);
 
 template <int TN>
 struct Cfg {
@@ -209,6 +215,10 @@ struct Cfg {
     static constexpr int kCols = 512;
     static_assert(kSfA + kStages * kSfStep <= kCols, "tensor memory");
     static_assert(kStages <= 8 && kStageBytes % 1024 == 0, "stage layout");
+    // A group of scale warps waits for a slot's phases by their parity, so it has to have
+    // seen the one before: every use of a slot is the same group's (stages may land out
+    // of order).
+    static_assert(kStages % kSfGroups == 0, "scale groups");
 };
 
 struct Sync {
@@ -268,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
     const uint32_t tmem = sy.tmem;
     const int tiles = a.tiles_m * a.tiles_n, first = blockIdx.x, stride = gridDim.x;
 
-    if (warp == kEpiWarps + kSfWarps && lane == 0) {
+    if (warp == kProducer && lane == 0) {
         // producer: the blocks of every k-stage of every tile of this CTA
         // operands that other tiles read too stay in L2 against the stream of results; weights
         // for one row of tiles are read once
@@ -307,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
             for (uint32_t b = it > static_cast<uint32_t>(kStages) ? it - kStages : 0; b < it; ++b)
                 mbar_wait(&sy.full[b % kStages], (b / kStages) & 1, kWaitLimit / 64);
         }
-    } else if (warp == kEpiWarps + kSfWarps + 1 && lane == 0) {
+    } else if (warp == kIssuer && lane == 0) {
         // issuer
         constexpr uint32_t kIdesc = tc::idesc_nvf4(kRows, TN);
         uint32_t it = 0, n = 0;
@@ -334,13 +344,15 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
             tc::commit(&sy.acc_full[n % C::kAcc]);
             mbar_wait(&sy.acc_full[n % C::kAcc], (n / C::kAcc) & 1, kWaitLimit / 64);
         }
-    } else if (warp >= kEpiWarps && warp < kEpiWarps + kSfWarps) {
+    } else if (warp >= kEpiWarps && warp < kProducer) {
         // scales: shared memory -> registers -> this warp's 32 lanes of tensor memory
         const uint32_t at = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+        const uint32_t group = static_cast<uint32_t>(warp - kEpiWarps) / kSfWarps;
         uint32_t it = 0;
         bool ok = true;
         for (int tile = first; ok && tile < tiles; tile += stride) {
             for (int k = 0; k < a.nk; ++k, ++it) {
+                if (it % kSfGroups != group) continue;
                 const uint32_t s = it % kStages;
                 // (a landed stage means that its slot's last one, and so its scales, have been multiplied)
                 ok = __all_sync(0xFFFFFFFFu, wait_or_abort(sy, &sy.full[s], (it / kStages) & 1, a));
@@ -379,33 +391,42 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
             tc::fence_after_sync();
             TY* row = static_cast<TY*>(a.y) + static_cast<size_t>(m) * a.ldy + n0;
             if constexpr (sizeof(TY) == 2) {
-                uint32_t w[kCols / 16][8];   // the rounded results
-#pragma unroll
-                for (int c = 0; c < kCols / 16; ++c) {
+                constexpr int kChunks = kCols / 16, kHeld = kChunks < 2 ? kChunks : 2;
+                const auto read = [&](int c, uint32_t* w) {   // 16 results, rounded
                     uint32_t r[16];
                     tc::tmem_load16(acc + 16 * c, r);
                     tc::tmem_load_wait();
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        w[c][i] = rows::Elem<TY>::pack2(__uint_as_float(r[2 * i]) * g, __uint_as_float(r[2 * i + 1]) * g);
-                }
-                tc::fence_before_sync();
-                if (lane == 0) mbar_arrive(&sy.acc_empty[buf]);
-                if (m < a.M) {
+                        w[i] = rows::Elem<TY>::pack2(__uint_as_float(r[2 * i]) * g, __uint_as_float(r[2 * i + 1]) * g);
+                };
+                const auto write = [&](int c, const uint32_t* w) {
+                    if (m >= a.M || n0 + 16 * c >= a.N) return;
+                    if (vec) {
+                        store32(row + 16 * c, w);
+                    } else {
 #pragma unroll
-                    for (int c = 0; c < kCols / 16; ++c) {
-                        if (n0 + 16 * c >= a.N) break;
-                        if (vec) {
-                            store32(row + 16 * c, w[c]);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                reinterpret_cast<uint16_t*>(row)[16 * c + 2 * i] = static_cast<uint16_t>(w[c][i]);
-                                reinterpret_cast<uint16_t*>(row)[16 * c + 2 * i + 1] = static_cast<uint16_t>(w[c][i] >> 16);
-                            }
+                        for (int i = 0; i < 8; ++i) {
+                            reinterpret_cast<uint16_t*>(row)[16 * c + 2 * i] = static_cast<uint16_t>(w[i]);
+                            reinterpret_cast<uint16_t*>(row)[16 * c + 2 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
                         }
                     }
+                };
+                // as many as registers hold are stored after the accumulators are free
+#pragma unroll
+                for (int c = 0; c < kChunks - kHeld; ++c) {
+                    uint32_t w[8];
+                    read(c, w);
+                    write(c, w);
+                    __syncwarp();
                 }
+                uint32_t w[kHeld][8];
+#pragma unroll
+                for (int c = 0; c < kHeld; ++c) read(kChunks - kHeld + c, w[c]);
+                tc::fence_before_sync();
+                if (lane == 0) mbar_arrive(&sy.acc_empty[buf]);
+#pragma unroll
+                for (int c = 0; c < kHeld; ++c) write(kChunks - kHeld + c, w[c]);
             } else {   // this many 32-bit results do not fit beside the rest: store as they are read
                 for (int c = 0; c < kCols / 16; ++c) {
                     uint32_t r[16];

@@ -212,3 +212,18 @@ def test_refusals():
             dh.NVFP4Matmul(*args)
     with pytest.raises(dh.DraftHeadError):
         dh.NVFP4Matmul(*weight(96, 32, 1)[:3])   # N % 64 != 0
+
+
+@pytest.mark.parametrize("M, N, K, yt, ldy", [
+    (600, 29440, 272, "bf16", 0), (513, 29504, 48, "f32", 0), (640, 29632, 1040, "f16", 0),
+    (129, 87808, 16, "bf16", 0), (600, 29440, 528, "bf16", 29443)])
+def test_many_tiles(M, N, K, yt, ldy):
+    """Products of several rounds of the largest tiles, with ragged last tiles in
+    both directions; a token's result is that of a call of its own."""
+    q, sf, g, w = weight(N, K, M)
+    mm = dh.NVFP4Matmul(q, sf, g)
+    x = rand_x(M, K, torch.bfloat16, 3)
+    y = torch.empty((M, ldy), dtype=TYPES[yt], device="cuda")[:, :N] if ldy else None
+    got = check(mm, x, w, TYPES[yt], y)
+    for rows in (slice(0, 3), slice(M - 2, M)):
+        assert torch.equal(mm(x[rows], out_dtype=TYPES[yt]), got[rows])
