@@ -24,14 +24,14 @@
 // (kind::mxf4nvf4, block 16); sixteen warps read a tile's accumulators into
 // registers, scaled and rounded, free them for the next tile and store.
 //
-// Bound, 8,192 tokens on a 64,064 x 2,560 head (565 us with the quantiser's 20:
-// 4.8 PFLOP/s; 1.05 GB of results alone take 155 us at the measured copy rate):
-// shared memory, by its arithmetic. Per 128 x 256 x 256 step it takes 55 KB from L2,
-// gives the matrix instructions 48 KB and the scale warps 24 KB (each of the four
-// reads all scales), 1,000 cycles at 128 bytes of the 1,000 that a step takes; the
-// matrix instructions alone take half of that. Tiles of 256 x 192 move a fifth less
-// from L2, but read as much of shared memory: 583 against 594, each with one group of
-// scale warps (their three slots do not go round between two).
+// Bound, 8,192 tokens on a 64,064 x 2,560 head (567 us with the quantiser's 20:
+// 4.8 PFLOP/s; 1.05 GB of results alone take 155 us at the measured copy rate): a
+// stage's way through the ring. A 128 x 256 x 256 step takes 515 ns, 270 of them
+// matrix instructions; it moves 55 KB into shared memory and reads 72 KB there (48
+// for the matrix instructions, 24 for the scales: each of four warps reads them all),
+// 122 bytes a cycle, half of the banks' peak. Tiles of 256 x 192 move a fifth less from
+// L2, but have room for three stages: 583 against 594, each with one group of scale
+// warps (three slots do not go round between two).
 // What the choices measured there:
 //  - scales: tcgen05.cp takes its turn among the matrix instructions (24 ns a copy,
 //    12 copies against 270 ns of matrix instructions per stage); stored from
@@ -41,12 +41,13 @@
 //  - results stored past L1, whose data array the ring shares: 620; both operands
 //    kept in L2 against the results (evict_last): 600; the producer's pointers and
 //    phases running along: 590; two groups of scale warps in turn (fewer held results
-//    for the registers): 565. 100 tokens: weights, read once, not kept 26.7 -> 24.6;
+//    for the registers): 567. 100 tokens: weights, read once, not kept 26.7 -> 24.6;
 //  - pairs of CTAs on one 256 x 256 tile (cta_group::2) need a third less of the
 //    operands, but each ring slot's round trip crosses the pair twice: 913, with the
 //    scales through registers 1,021; operands multicast in clusters of four and
 //    eight 971 to 1,163; blocks of 128 k, twice as many stages of half the size, 763;
-//    the tokens' scales by tcgen05.cp, the weights' through registers 609.
+//    the tokens' scales by tcgen05.cp, the weights' through registers 609; four groups
+//    of scale warps beside eight epilogue warps 572.
 #include <atomic>
 #include <cfloat>
 
@@ -412,7 +413,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
                         }
                     }
                 };
-                // as many as registers hold are stored after the accumulators are free
+                // the last two chunks are stored after the accumulators are free (all four held
+                // spill registers: 586 us against 567)
 #pragma unroll
                 for (int c = 0; c < kChunks - kHeld; ++c) {
                     uint32_t w[8];
