@@ -22,6 +22,8 @@ Names follow the C ABI in include/drafthead.h:
   distill_topk             draft_head_distill: distillation loss and gradient
   (_forward, _backward)    the loss alone; the gradient from its normaliser
   DistillTopK              the same as a torch.autograd function
+From NVFP4Matmul on, a call given stream= works and allocates on that stream: its
+arguments have to be ready there, and its results are, for what follows on it.
 The vocabulary-sharded head (the local-argmax exchange) is in .sharded.
 """
 from __future__ import annotations
@@ -491,19 +493,29 @@ def _vector(t: torch.Tensor | None, name: str, dtype: torch.dtype, n: int | None
         raise ValueError(f"{name} must be a contiguous {dtype} tensor{'' if n is None else f' of {n} elements'} on {device}")
 
 
-def _keep_for(stream, *tensors) -> None:
-    """Tensors used on a stream other than the current one stay allocated until its work is done."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _keep_for(stream, *values) -> None:
+    """Tensors (of any values) used on `stream`, not their own, stay allocated until its work is done."""
+    for t in values:
+        if isinstance(t, torch.Tensor):
+            t.record_stream(stream)
 
 
-def _stream_of(t: torch.Tensor, stream) -> int:
-    """cudaStream_t of `stream`, or of the current stream of t's device."""
-    if stream is None and _raw_stream is not None:
-        return _raw_stream(t.get_device())
-    return _stream(stream)
+def _on_stream(stream, call, *args):
+    """call(*args) with `stream` current, for a caller that asked for it: what the
+    call allocates comes from that stream's own pool (a block of the caller's
+    stream may still be in use by work pending there) and is filled on it. The
+    arguments stay allocated for `stream`'s work, the results for the caller's."""
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        out = call(*args)
+    _keep_for(stream, *args)
+    _keep_for(here, *(out if isinstance(out, tuple) else (out,)))
+    return out
+
+
+def _stream_of(t: torch.Tensor) -> int:
+    """cudaStream_t of the current stream of t's device."""
+    return _raw_stream(t.get_device()) if _raw_stream is not None else _stream()
 
 
 class NVFP4Matmul:
@@ -514,6 +526,9 @@ class NVFP4Matmul:
     activations in bfloat16."""
 
     def __init__(self, q: torch.Tensor, sf: torch.Tensor, g: torch.Tensor, stream=None):
+        if stream is not None:
+            _on_stream(stream, self.__init__, q, sf, g)
+            return _keep_for(torch.cuda.current_stream(stream.device), self.packed, self.error)
         if q.dtype != torch.uint8 or q.dim() != 2 or not q.is_cuda or not q.is_contiguous():
             raise ValueError("q must be a contiguous [N, K/2] uint8 CUDA tensor")
         self.N, self.K = q.shape[0], 2 * q.shape[1]
@@ -527,11 +542,10 @@ class NVFP4Matmul:
             raise DraftHeadError("nvfp4_matmul_packed_bytes", DH_ERR_SHAPE)
         self.packed = torch.empty(nb, dtype=torch.uint8, device=q.device)
         _check("nvfp4_pack_matmul",
-               lib().nvfp4_pack_matmul(q.data_ptr(), sf.data_ptr(), self.N, self.K, self.packed.data_ptr(), _stream(stream)))
+               lib().nvfp4_pack_matmul(q.data_ptr(), sf.data_ptr(), self.N, self.K, self.packed.data_ptr(), _stream_of(q)))
         self.error = torch.zeros(1, dtype=torch.int32, device=q.device)
         self.desc = dh_matmul_t(self.N, self.K, self.packed.data_ptr(), g.data_ptr())
         self.desc_ref, self.error_ptr = C.byref(self.desc), self.error.data_ptr()
-        _keep_for(stream, q, sf, g, self.packed, self.error)
 
     @classmethod
     def from_weight(cls, W: torch.Tensor, idx: torch.Tensor | None = None, stream=None) -> "NVFP4Matmul":
@@ -544,6 +558,9 @@ class NVFP4Matmul:
                 stream=None) -> torch.Tensor:
         """y [M, N] (out_dtype: bfloat16, float16 or float32, or a given tensor's
         type) = x W'^T for x [M, K] (bfloat16, float16 or float32, rows may be strided)."""
+        if stream is not None:
+            _keep_for(stream, self.packed, self.g, self.error)
+            return _on_stream(stream, self.forward, x, y, out_dtype)
         if x.dim() != 2 or x.shape[1] != self.K or x.dtype not in _TYPES or x.device != self.packed.device or \
                 x.stride(1) != 1 or (x.shape[0] > 1 and x.stride(0) < self.K):
             raise ValueError(f"x must be a [M, {self.K}] bfloat16, float16 or float32 tensor with contiguous rows")
@@ -562,8 +579,7 @@ class NVFP4Matmul:
         ws = torch.empty(nb, dtype=torch.uint8, device=x.device)   # the allocator's blocks are 512-byte aligned
         _check("nvfp4_matmul",
                L.nvfp4_matmul(self.desc_ref, x.data_ptr(), _TYPES[x.dtype], x.stride(0), M, y.data_ptr(),
-                                  _TYPES[y.dtype], y.stride(0), ws.data_ptr(), nb, self.error_ptr, _stream_of(x, stream)))
-        _keep_for(stream, x, y, ws, self.packed, self.g)
+                                  _TYPES[y.dtype], y.stride(0), ws.data_ptr(), nb, self.error_ptr, _stream_of(x)))
         return y
 
     __call__ = forward
@@ -600,12 +616,13 @@ def _logits_desc(logits: torch.Tensor, temperature: float, row_of: torch.Tensor 
 def draft_head_row_map(idx: torch.Tensor, n_kept: int, V: int, stream=None) -> torch.Tensor:
     """int32[V]: the head row (logits column) of every target id, -1 for ids that
     are not kept; the row_of argument of the operators below."""
+    if stream is not None:
+        return _on_stream(stream, draft_head_row_map, idx, n_kept, V)
     if idx.dtype != torch.int32 or idx.dim() != 1 or not idx.is_cuda or not idx.is_contiguous() or idx.numel() < n_kept:
         raise ValueError(f"idx must be a contiguous int32 CUDA vector of at least {n_kept} elements")
     row_of = torch.empty(V, dtype=torch.int32, device=idx.device)
     _check("draft_head_row_map",
-           lib().draft_head_row_map(idx.data_ptr(), n_kept, row_of.data_ptr(), V, _stream(stream)))
-    _keep_for(stream, idx, row_of)
+           lib().draft_head_row_map(idx.data_ptr(), n_kept, row_of.data_ptr(), V, _stream_of(idx)))
     return row_of
 
 
@@ -628,6 +645,8 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, top
     are returned as target ids; without them both are columns. A token without a
     column has log-probability -inf; alternatives past the last logit above -inf
     have id -1. See draft_head_token_logprobs."""
+    if stream is not None:
+        return _on_stream(stream, token_logprobs, logits, tokens, top_k, temperature, idx, row_of)
     d = _logits_desc(logits, temperature, row_of, idx)
     M, dev, f32 = logits.shape[0], logits.device, torch.float32
     G = 0
@@ -645,9 +664,7 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, top
     if M > 0:
         _check("draft_head_token_logprobs",
                lib().draft_head_token_logprobs(d, _ptr(tokens), G, _ptr(logp), entropy.data_ptr(), lse.data_ptr(), top_k,
-                                               top_logp.data_ptr(), top_ids.data_ptr(), _stream_of(logits, stream)))
-        if stream is not None:
-            _keep_for(stream, logits, tokens, idx, row_of, logp, entropy, lse, top_logp, top_ids)
+                                               top_logp.data_ptr(), top_ids.data_ptr(), _stream_of(logits)))
     return TokenLogprobs(logp, entropy, lse, top_logp, top_ids)
 
 
@@ -687,6 +704,8 @@ def distill_topk(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits
     row_of, columns without it; entries without a column, and masked (-inf) ones,
     leave the teacher's distribution. weights: float32 [M], 0 for rows to leave
     out. dlogits may be the logits tensor itself. See draft_head_distill."""
+    if stream is not None:
+        return _on_stream(stream, distill_topk, logits, teacher_ids, teacher_logits, temperature, weights, row_of, dlogits)
     d = _logits_desc(logits, temperature, row_of)
     K, vt = _teacher(logits, teacher_ids, teacher_logits)
     _vector(weights, "weights", torch.float32, logits.shape[0], logits.device)
@@ -695,8 +714,7 @@ def distill_topk(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits
     if logits.shape[0] > 0:
         _check("draft_head_distill",
                lib().draft_head_distill(d, teacher_ids.data_ptr(), teacher_logits.data_ptr(), vt, K, _ptr(weights),
-                                        loss.data_ptr(), None, dz.data_ptr(), dz.stride(0), _stream_of(logits, stream)))
-        _keep_for(stream, logits, teacher_ids, teacher_logits, weights, row_of, dz, loss)
+                                        loss.data_ptr(), None, dz.data_ptr(), dz.stride(0), _stream_of(logits)))
     return loss, dz
 
 
@@ -705,6 +723,8 @@ def distill_topk_forward(logits: torch.Tensor, teacher_ids: torch.Tensor, teache
                          row_of: torch.Tensor | None = None, stream=None):
     """(loss, lse), both float32 [M]: the loss of distill_topk alone, and the
     student's normaliser for distill_topk_backward."""
+    if stream is not None:
+        return _on_stream(stream, distill_topk_forward, logits, teacher_ids, teacher_logits, temperature, weights, row_of)
     d = _logits_desc(logits, temperature, row_of)
     K, vt = _teacher(logits, teacher_ids, teacher_logits)
     _vector(weights, "weights", torch.float32, logits.shape[0], logits.device)
@@ -713,8 +733,7 @@ def distill_topk_forward(logits: torch.Tensor, teacher_ids: torch.Tensor, teache
     if logits.shape[0] > 0:
         _check("draft_head_distill",
                lib().draft_head_distill(d, teacher_ids.data_ptr(), teacher_logits.data_ptr(), vt, K, _ptr(weights),
-                                        loss.data_ptr(), lse.data_ptr(), None, 0, _stream_of(logits, stream)))
-        _keep_for(stream, logits, teacher_ids, teacher_logits, weights, row_of, loss, lse)
+                                        loss.data_ptr(), lse.data_ptr(), None, 0, _stream_of(logits)))
     return loss, lse
 
 
@@ -724,6 +743,9 @@ def distill_topk_backward(logits: torch.Tensor, teacher_ids: torch.Tensor, teach
                           stream=None) -> torch.Tensor:
     """dlogits [M, C] from distill_topk_forward's lse; weights: float32 [M], the
     upstream gradient of each row's loss times the forward's weight."""
+    if stream is not None:
+        return _on_stream(stream, distill_topk_backward, logits, teacher_ids, teacher_logits, lse, weights, temperature, row_of,
+                          dlogits)
     d = _logits_desc(logits, temperature, row_of)
     K, vt = _teacher(logits, teacher_ids, teacher_logits)
     _vector(lse, "lse", torch.float32, logits.shape[0], logits.device)
@@ -733,8 +755,7 @@ def distill_topk_backward(logits: torch.Tensor, teacher_ids: torch.Tensor, teach
         _check("draft_head_distill_backward",
                lib().draft_head_distill_backward(d, teacher_ids.data_ptr(), teacher_logits.data_ptr(), vt, K,
                                                  lse.data_ptr(), _ptr(weights), dz.data_ptr(), dz.stride(0),
-                                                 _stream_of(logits, stream)))
-        _keep_for(stream, logits, teacher_ids, teacher_logits, lse, weights, row_of, dz)
+                                                 _stream_of(logits)))
     return dz
 
 
