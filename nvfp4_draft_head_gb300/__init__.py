@@ -550,9 +550,13 @@ class NVFP4Matmul:
     @classmethod
     def from_weight(cls, W: torch.Tensor, idx: torch.Tensor | None = None, stream=None) -> "NVFP4Matmul":
         """Quantise the rows W[idx] (all rows without idx) of a bfloat16 weight [V, K]."""
+        if stream is not None:
+            new = _on_stream(stream, cls.from_weight, W, idx)
+            _keep_for(torch.cuda.current_stream(stream.device), new.packed, new.g, new.error)
+            return new
         if idx is None:
             idx = torch.arange(W.shape[0], dtype=torch.int32, device=W.device)
-        return cls(*nvfp4_quantize_rows(W, idx, stream), stream=stream)
+        return cls(*nvfp4_quantize_rows(W, idx))
 
     def forward(self, x: torch.Tensor, y: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
                 stream=None) -> torch.Tensor:

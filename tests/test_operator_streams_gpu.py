@@ -64,6 +64,15 @@ def test_product_constructor():
     beside_pending_work(lambda s: dh.NVFP4Matmul(q, sf, g, stream=s))
 
 
+@pytest.mark.parametrize("given", [False, True])
+def test_product_from_bf16_rows(given):
+    """The row ids that the call makes for itself, the quantiser's scratch and the
+    weight are all made on the stream that reads them."""
+    W = (torch.randn((1088, 528), generator=torch.Generator("cuda").manual_seed(4), device="cuda") * 0.02).bfloat16()
+    idx = torch.arange(1087, -1, -1, dtype=torch.int32, device="cuda") if given else None
+    beside_pending_work(lambda s: dh.NVFP4Matmul.from_weight(W, idx, stream=s), [1088 * 4, 1088 * 528 // 2, 1088 * 528 // 16, 4, 1024])
+
+
 def test_row_map():
     idx = torch.randperm(9000, generator=torch.Generator().manual_seed(1))[:3777].int().cuda()
     beside_pending_work(lambda s: dh.draft_head_row_map(idx, 3777, 9000, stream=s))
