@@ -513,9 +513,17 @@ def _on_stream(stream, call, *args):
     return out
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream_of(t: torch.Tensor) -> int:
-    """cudaStream_t of the current stream of t's device."""
-    return _raw_stream(t.get_device()) if _raw_stream is not None else _stream()
+    """cudaStream_t of the current stream; t's device has to be the current one, where
+    the library launches."""
+    device = t.get_device()
+    if device != _current_device():
+        raise ValueError(f"the tensors are on cuda:{device}, which is not the device of the call: make it the current device "
+                         "(torch.cuda.device) and pass a stream of that device")
+    return _raw_stream(device) if _raw_stream is not None else _stream()
 
 
 class NVFP4Matmul:
@@ -554,6 +562,8 @@ class NVFP4Matmul:
             new = _on_stream(stream, cls.from_weight, W, idx)
             _keep_for(torch.cuda.current_stream(stream.device), new.packed, new.g, new.error)
             return new
+        if W.is_cuda:
+            _stream_of(W)   # refuses before the first launch
         if idx is None:
             idx = torch.arange(W.shape[0], dtype=torch.int32, device=W.device)
         return cls(*nvfp4_quantize_rows(W, idx))
