@@ -773,9 +773,21 @@ def distill_topk_backward(logits: torch.Tensor, teacher_ids: torch.Tensor, teach
     return dz
 
 
+class _DifferentiableOnce(torch.autograd.Function):
+    """A computed gradient, tied to what it was computed from: differentiating it again raises."""
+
+    @staticmethod
+    def forward(ctx, gradient, *sources):
+        return gradient.view_as(gradient)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("DistillTopK is differentiable once: its gradient has no derivative")
+
+
 class DistillTopK(torch.autograd.Function):
     """loss [M] = DistillTopK.apply(logits, teacher_ids, teacher_logits, temperature,
-    weights, row_of); differentiable in the logits (the teacher is a constant)."""
+    weights, row_of); differentiable once in the logits (the teacher is a constant)."""
 
     @staticmethod
     def forward(ctx, logits, teacher_ids, teacher_logits, temperature=1.0, weights=None, row_of=None):
@@ -787,6 +799,9 @@ class DistillTopK(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dloss):
         logits, ids, val, lse, weights, row_of = ctx.saved_tensors
-        up = dloss.float() if weights is None else dloss.float() * weights
-        dz = distill_topk_backward(logits, ids, val, lse, up.contiguous(), ctx.temperature, row_of)
+        with torch.no_grad():
+            up = dloss.float() if weights is None else dloss.float() * weights
+            dz = distill_topk_backward(logits, ids, val, lse, up.contiguous(), ctx.temperature, row_of)
+        if torch.is_grad_enabled():   # the caller asked for the gradient's graph
+            dz = _DifferentiableOnce.apply(dz, logits, dloss, weights)
         return dz, None, None, None, None, None
