@@ -787,7 +787,8 @@ class _DifferentiableOnce(torch.autograd.Function):
 
 class DistillTopK(torch.autograd.Function):
     """loss [M] = DistillTopK.apply(logits, teacher_ids, teacher_logits, temperature,
-    weights, row_of); differentiable once in the logits (the teacher is a constant)."""
+    weights, row_of); differentiable once in the logits and the weights (the teacher
+    is a constant). A weight's derivative is the loss that its row has at weight 1."""
 
     @staticmethod
     def forward(ctx, logits, teacher_ids, teacher_logits, temperature=1.0, weights=None, row_of=None):
@@ -799,9 +800,14 @@ class DistillTopK(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dloss):
         logits, ids, val, lse, weights, row_of = ctx.saved_tensors
+        dz = dw = None
         with torch.no_grad():
-            up = dloss.float() if weights is None else dloss.float() * weights
-            dz = distill_topk_backward(logits, ids, val, lse, up.contiguous(), ctx.temperature, row_of)
-        if torch.is_grad_enabled():   # the caller asked for the gradient's graph
-            dz = _DifferentiableOnce.apply(dz, logits, dloss, weights)
-        return dz, None, None, None, None, None
+            up = dloss.float()
+            if ctx.needs_input_grad[0]:
+                w = (up if weights is None else up * weights).contiguous()
+                dz = distill_topk_backward(logits, ids, val, lse, w, ctx.temperature, row_of)
+            if weights is not None and ctx.needs_input_grad[4]:
+                dw = up * distill_topk_forward(logits, ids, val, ctx.temperature, None, row_of)[0]
+        if torch.is_grad_enabled():   # the caller asked for the gradients' graph
+            dz, dw = (None if d is None else _DifferentiableOnce.apply(d, logits, dloss, weights) for d in (dz, dw))
+        return dz, None, None, None, dw, None

@@ -29,3 +29,26 @@ def test_second_derivatives_are_refused():
     (dz,) = torch.autograd.grad((dh.DistillTopK.apply(z, ids, val) * scale).sum(), z, create_graph=True)
     with pytest.raises(RuntimeError, match="differentiable once"):
         torch.autograd.grad(dz.sum() + scale, scale)
+
+
+@pytest.mark.parametrize("logits_too", [False, True])
+def test_gradient_of_the_row_weights(logits_too):
+    """loss_m is linear in w_m: its derivative is the row's loss at weight 1, for a
+    row of weight 0 too. Tolerance: that of the loss, times the upstream gradient."""
+    M, n, K, t = 40, 1031, 9, 1.5
+    z = rand_rows(M, n, torch.float32, 3)
+    ids, val = teacher(z, K, 4)
+    ids[7] = -1                                  # no entry in use: nothing depends on this weight
+    w = torch.rand(M, generator=torch.Generator("cuda").manual_seed(5), device="cuda")
+    w[3] = 0.0
+    up = torch.rand(M, generator=torch.Generator("cuda").manual_seed(6), device="cuda")
+    z.requires_grad_(logits_too)
+    w.requires_grad_()
+    loss = dh.DistillTopK.apply(z, ids, val, t, w)
+    (loss * up).sum().backward()
+    base, tol = ref_distill(z.detach(), ids, val, t, None, None)[:2]
+    close(w.grad, base * up, tol * up + 1e-6 * (base * up).abs(), "weights")
+    assert w.grad[7] == 0 and loss[3] == 0
+    if logits_too:
+        ref = ref_distill(z.detach(), ids, val, t, w.detach() * up, None)
+        close(z.grad, ref[2], ref[3] + 1e-6, "logits")
