@@ -773,22 +773,31 @@ def distill_topk_backward(logits: torch.Tensor, teacher_ids: torch.Tensor, teach
     return dz
 
 
-class _DifferentiableOnce(torch.autograd.Function):
-    """A computed gradient, tied to what it was computed from: differentiating it again raises."""
+class _Refuse(torch.autograd.Function):
+    """A tensor whose gradient is refused: a backward pass that comes back to it, or
+    by it to the sources that it was computed from, raises."""
 
     @staticmethod
-    def forward(ctx, gradient, *sources):
-        return gradient.view_as(gradient)
+    def forward(ctx, message, tensor, *sources):
+        ctx.message = message
+        return tensor.view_as(tensor)
 
     @staticmethod
     def backward(ctx, *grads):
-        raise RuntimeError("DistillTopK is differentiable once: its gradient has no derivative")
+        raise RuntimeError(ctx.message)
 
 
 class DistillTopK(torch.autograd.Function):
     """loss [M] = DistillTopK.apply(logits, teacher_ids, teacher_logits, temperature,
     weights, row_of); differentiable once in the logits and the weights (the teacher
-    is a constant). A weight's derivative is the loss that its row has at weight 1."""
+    is a constant: a backward pass that would reach its logits raises, detach them). A
+    weight's derivative is the loss that its row has at weight 1."""
+
+    @classmethod
+    def apply(cls, logits, teacher_ids, teacher_logits, *rest):
+        if teacher_logits.requires_grad and torch.is_grad_enabled():
+            teacher_logits = _Refuse.apply("DistillTopK has no gradient for the teacher's logits: detach them", teacher_logits)
+        return super().apply(logits, teacher_ids, teacher_logits, *rest)
 
     @staticmethod
     def forward(ctx, logits, teacher_ids, teacher_logits, temperature=1.0, weights=None, row_of=None):
@@ -809,5 +818,6 @@ class DistillTopK(torch.autograd.Function):
             if weights is not None and ctx.needs_input_grad[4]:
                 dw = up * distill_topk_forward(logits, ids, val, ctx.temperature, None, row_of)[0]
         if torch.is_grad_enabled():   # the caller asked for the gradients' graph
-            dz, dw = (None if d is None else _DifferentiableOnce.apply(d, logits, dloss, weights) for d in (dz, dw))
+            dz, dw = (None if d is None else _Refuse.apply("DistillTopK is differentiable once: its gradient has no derivative",
+                                                           d, logits, dloss, weights) for d in (dz, dw))
         return dz, None, None, None, dw, None

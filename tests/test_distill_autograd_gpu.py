@@ -52,3 +52,19 @@ def test_gradient_of_the_row_weights(logits_too):
     if logits_too:
         ref = ref_distill(z.detach(), ids, val, t, w.detach() * up, None)
         close(z.grad, ref[2], ref[3] + 1e-6, "logits")
+
+
+def test_a_gradient_for_the_teacher_is_refused():
+    z = rand_rows(5, 70, torch.float32, 1).requires_grad_()
+    ids, val = teacher(z.detach(), 6, 2)
+    val.requires_grad_()
+    with pytest.raises(RuntimeError, match="teacher"):
+        dh.DistillTopK.apply(z, ids, val).sum().backward()
+    (dz,) = torch.autograd.grad(dh.DistillTopK.apply(z, ids, val).sum(), z)   # the logits' alone, and the loss alone
+    ref = ref_distill(z.detach(), ids, val.detach(), 1.0, None, None)
+    close(dz, ref[2], ref[3] + 1e-6, "logits")
+    with torch.no_grad():
+        close(dh.DistillTopK.apply(z, ids, val), ref[0], ref[1], "loss")
+    z.grad = None   # (the refused pass had reached the logits)
+    dh.DistillTopK.apply(z, ids, val.detach()).sum().backward()
+    assert torch.equal(z.grad, dz)
