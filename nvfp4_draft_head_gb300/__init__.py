@@ -526,12 +526,17 @@ def _stream_of(t: torch.Tensor) -> int:
     return _raw_stream(device) if _raw_stream is not None else _stream()
 
 
+def _no_gradient(t: torch.Tensor, name: str) -> None:
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} require a gradient, which this operator does not have: detach them, or call it under torch.no_grad()")
+
+
 class NVFP4Matmul:
     """An NVFP4 weight for many-token products: forward(x) = x W'^T with x
     quantised to NVFP4 per token (W4A4) and fp32 accumulation. q uint8 [N, K/2],
     sf uint8 [N, K/16] and g float32 [1] as from nvfp4_quantize_rows; N % 64 == 0,
     K % 16 == 0. For up to 16 tokens NVFP4Linear and DraftHead keep the
-    activations in bfloat16."""
+    activations in bfloat16. No gradient: an x that requires one is refused."""
 
     def __init__(self, q: torch.Tensor, sf: torch.Tensor, g: torch.Tensor, stream=None):
         if stream is not None:
@@ -578,6 +583,7 @@ class NVFP4Matmul:
         if x.dim() != 2 or x.shape[1] != self.K or x.dtype not in _TYPES or x.device != self.packed.device or \
                 x.stride(1) != 1 or (x.shape[0] > 1 and x.stride(0) < self.K):
             raise ValueError(f"x must be a [M, {self.K}] bfloat16, float16 or float32 tensor with contiguous rows")
+        _no_gradient(x, "the activations")
         M = x.shape[0]
         if y is None:
             if out_dtype not in _TYPES:
@@ -658,9 +664,11 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, top
     (draft_head_row_map) tokens are target ids, with idx (dh_idx) the alternatives
     are returned as target ids; without them both are columns. A token without a
     column has log-probability -inf; alternatives past the last logit above -inf
-    have id -1. See draft_head_token_logprobs."""
+    have id -1. No gradient: logits that require one are refused. See
+    draft_head_token_logprobs."""
     if stream is not None:
         return _on_stream(stream, token_logprobs, logits, tokens, top_k, temperature, idx, row_of)
+    _no_gradient(logits, "the logits")
     d = _logits_desc(logits, temperature, row_of, idx)
     M, dev, f32 = logits.shape[0], logits.device, torch.float32
     G = 0
@@ -717,7 +725,9 @@ def distill_topk(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits
     [M, K], and the gradient of its sum, in one kernel. Ids are target ids with
     row_of, columns without it; entries without a column, and masked (-inf) ones,
     leave the teacher's distribution. weights: float32 [M], 0 for rows to leave
-    out. dlogits may be the logits tensor itself. See draft_head_distill."""
+    out. dlogits may be the logits tensor itself. The loss has no autograd graph
+    (the gradient is at hand; DistillTopK is the differentiable form). See
+    draft_head_distill."""
     if stream is not None:
         return _on_stream(stream, distill_topk, logits, teacher_ids, teacher_logits, temperature, weights, row_of, dlogits)
     d = _logits_desc(logits, temperature, row_of)
