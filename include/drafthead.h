@@ -380,7 +380,8 @@ int nvfp4_matmul(const dh_matmul_t *w, const void *x, int x_type, int64_t ldx, i
  * when M > 1; any value when M == 1), aligned to its element type only (16-byte
  * aligned rows are read fastest). 1 <= C <= 2^30. -inf marks a masked column;
  * a row may be masked throughout.
- *   temperature  t > 0, finite: probabilities are softmax(z / t).
+ *   temperature  t > 0, finite, with log2(e) / t finite in fp32 (t >= 4.3e-39):
+ *                probabilities are softmax(z / t).
  *   row_of       int32 [V] or NULL: ids given to the operator are target ids and
  *                row_of[id] is their column (-1: not kept); NULL: ids are columns.
  *   idx          int32 [C] or NULL: id of each column, for ids that the operator

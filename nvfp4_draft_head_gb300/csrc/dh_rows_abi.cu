@@ -23,7 +23,9 @@ int check_logits(const dh_logits_t* lg) {
     if (lg == nullptr || lg->z == nullptr) return DH_ERR_ARG;
     const int b = type_bytes(lg->type);
     if (b == 0) return DH_ERR_ARG;
-    if (!(lg->temperature > 0.0f) || !std::isfinite(lg->temperature) || !std::isfinite(1.0f / lg->temperature)) return DH_ERR_ARG;
+    // the kernels scale exponents by (1 / t) log2(e), which is infinite for the smallest t
+    if (!(lg->temperature > 0.0f) || !std::isfinite(lg->temperature) || !std::isfinite(1.0f / lg->temperature * 1.44269504f))
+        return DH_ERR_ARG;
     if (lg->M < 1 || lg->M > kMaxRows || lg->C < 1 || lg->C > (1 << 30)) return DH_ERR_SHAPE;
     if (lg->M > 1 && lg->ld < lg->C) return DH_ERR_SHAPE;
     if (lg->row_of != nullptr && lg->V < 1) return DH_ERR_SHAPE;

@@ -1,0 +1,19 @@
+"""Refusals of the operators on logits rows at the ends of their arguments' ranges
+(answered before any CUDA call; the addresses are never dereferenced)."""
+import pytest
+
+import nvfp4_draft_head_gb300 as dh
+from test_rows_abi import A, L, desc  # noqa: F401
+
+
+@pytest.mark.parametrize("t", [1e-45, 2e-39, 3e-39, 4.2e-39])
+def test_temperatures_whose_scale_overflows(L, t):  # noqa: F811
+    """1 / t, or the exponents' scale log2(e) / t, is infinite in fp32."""
+    d = desc(temperature=t)
+    assert L.draft_head_token_logprobs(d, A, 1, A, A, A, 5, A, A, None) == dh.DH_ERR_ARG
+    assert L.draft_head_distill(d, A, A, dh.DH_T_F32, 8, None, A, None, None, 0, None) == dh.DH_ERR_ARG
+    assert L.draft_head_distill_backward(d, A, A, dh.DH_T_F32, 8, A, None, A, 104, None) == dh.DH_ERR_ARG
+
+
+def test_the_smallest_temperature_gets_past_that_check(L):  # noqa: F811
+    assert L.draft_head_token_logprobs(desc(temperature=4.3e-39), A, -1, A, A, A, 5, A, A, None) == dh.DH_ERR_SHAPE
