@@ -605,7 +605,9 @@ class NVFP4Matmul:
     __call__ = forward
 
     def device_error(self) -> int:
-        """Read and clear the device error word (synchronises)."""
+        """Read and clear the device error word (waits for the device: products may be
+        pending on any stream)."""
+        torch.cuda.synchronize(self.error.device)
         err = int(self.error.item())
         if err:
             self.error.zero_()

@@ -113,3 +113,16 @@ def test_results_outlive_the_callers_work():
     later = [mm(other, stream=side) for _ in range(4)]
     torch.cuda.synchronize()
     assert torch.equal(kept, want) and torch.equal(later[0], mm(other))
+
+
+def test_device_error_waits_for_every_stream():
+    """An error recorded by work still pending on another stream is read (here the
+    word is set by a fill behind a busy side stream)."""
+    mm = dh.NVFP4Matmul(*weight(64, 32, 1)[:3])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(BUSY)
+        mm.error.fill_(dh.DH_DEVERR_TIMEOUT)
+    assert mm.device_error() == dh.DH_DEVERR_TIMEOUT
+    assert mm.device_error() == 0
