@@ -632,7 +632,10 @@ def _logits_desc(logits: torch.Tensor, temperature: float, row_of: torch.Tensor 
         _vector(idx, "idx", torch.int32, None, logits.device)
         if idx.numel() < n:
             raise ValueError(f"idx must hold the ids of all {n} columns")
-    return _pack_logits(logits.data_ptr(), dtype, M, n, ld, temperature, _ptr(row_of) or 0, V, _ptr(idx) or 0)
+    try:
+        return _pack_logits(logits.data_ptr(), dtype, M, n, ld, temperature, _ptr(row_of) or 0, V, _ptr(idx) or 0)
+    except (struct.error, OverflowError):   # a size past 32 bits, a temperature that fp32 does not hold or no number
+        raise DraftHeadError("dh_logits_t", DH_ERR_SHAPE if max(M, n, V) >= 2 ** 31 else DH_ERR_ARG) from None
 
 
 def draft_head_row_map(idx: torch.Tensor, n_kept: int, V: int, stream=None) -> torch.Tensor:
