@@ -30,10 +30,18 @@ def stand_in(M, n):
 
 
 @pytest.mark.parametrize("M, n, t, status", [
-    (4, 100, 1e39, dh.DH_ERR_ARG), (4, 100, 1e300, dh.DH_ERR_ARG), (4, 100, "1", dh.DH_ERR_ARG), (4, 100, None, dh.DH_ERR_ARG),
-    (2 ** 31, 100, 1.0, dh.DH_ERR_SHAPE), (1, 2 ** 31, 1.0, dh.DH_ERR_SHAPE)])
+    (4, 100, "1", dh.DH_ERR_ARG), (4, 100, None, dh.DH_ERR_ARG), (4, 100, 10 ** 400, dh.DH_ERR_ARG),
+    (2 ** 31, 100, 1.0, dh.DH_ERR_SHAPE), (1, 2 ** 31, 1.0, dh.DH_ERR_SHAPE)],
+                         ids=["text", "none", "past float64", "rows", "columns"])
 def test_arguments_past_the_descriptors_fields(L, M, n, t, status):  # noqa: F811
     with pytest.raises(dh.DraftHeadError) as e:
         dh._logits_desc(stand_in(M, n), t, None)
     assert e.value.status == status
     assert len(dh._logits_desc(stand_in(4, 100), 1.0, None)) == C.sizeof(dh.dh_logits_t)
+
+
+@pytest.mark.parametrize("t", [1e39, -1e39, 1e300, 1e-50])
+def test_temperatures_that_fp32_does_not_hold(L, t):  # noqa: F811
+    """They become infinite or zero in the descriptor, which the library refuses."""
+    d = dh._logits_desc(stand_in(4, 100), t, None)
+    assert L.draft_head_token_logprobs(d, A, 1, A, A, A, 5, A, A, None) == dh.DH_ERR_ARG
