@@ -76,6 +76,7 @@ typedef enum {
 /* Bits of the device error word. */
 #define DH_DEVERR_IDX 1u      /* a dh_idx entry was outside [0, V) */
 #define DH_DEVERR_TIMEOUT 2u  /* a bounded device wait gave up (results invalid) */
+#define DH_DEVERR_UNFINISHED 4u  /* nvfp4_matmul_wait_probe only: see there */
 
 typedef enum {
     DH_FMT_NVFP4 = 1,
@@ -375,6 +376,18 @@ size_t nvfp4_matmul_workspace_bytes(int M, int K);
  * capturable in a CUDA graph. */
 int nvfp4_matmul(const dh_matmul_t *w, const void *x, int x_type, int64_t ldx, int M, void *y, int y_type,
                  int64_t ldy, void *ws, size_t ws_bytes, unsigned int *error, void *stream);
+
+/* Self-test of the failure handling of nvfp4_matmul: the same product (x and y
+ * bfloat16, contiguous) with one role of the kernel's warps doing nothing (0: the
+ * operands' copies, 1: the scales, 2: the matrix instructions, 3: the results) and a
+ * limit of 64 x rounds tries of about 1 us on every wait (1 <= rounds <= 4096; a
+ * product's own limit is 65,536). Whoever waits for the idle role gives up, the others
+ * follow, and the kernel ends as a product whose wait ran out does: DH_DEVERR_TIMEOUT
+ * in *error (not NULL), the context usable, y undefined. (An idle role 3 is waited for
+ * only where an SM takes a third tile of 128 x 128, or a second of 128 x 256.)
+ * DH_DEVERR_UNFINISHED is set too if the kernel ended with work of its own in flight. */
+int nvfp4_matmul_wait_probe(const dh_matmul_t *w, const void *x, int M, void *y, void *ws, size_t ws_bytes, int role,
+                            unsigned int rounds, unsigned int *error, void *stream);
 
 /* Rows of logits. z: [M][C] of dh_type `type`, row stride ld elements (ld >= C
  * when M > 1; any value when M == 1), aligned to its element type only (16-byte

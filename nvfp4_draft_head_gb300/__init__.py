@@ -44,6 +44,7 @@ DH_MAX_M = 16
 DH_WORKSPACE_ALIGN = 256
 DH_DEVERR_IDX = 1
 DH_DEVERR_TIMEOUT = 2
+DH_DEVERR_UNFINISHED = 4
 DH_HEAD_IDX_ASCENDING = 1
 DH_T_BF16, DH_T_F16, DH_T_F32 = 1, 2, 3
 DH_MAX_TOP, DH_MAX_TEACHER = 128, 512
@@ -57,7 +58,7 @@ EXPORTS = (
     "draft_head_wait_probe", "draft_head_top_tokens_host", "draft_head_top_keys", "draft_head_keys_to_ids",
     "draft_head_static_read_device_error", "draft_head_row_map", "draft_head_token_logprobs", "draft_head_distill",
     "draft_head_distill_backward", "nvfp4_matmul_packed_bytes", "nvfp4_pack_matmul", "nvfp4_matmul_workspace_bytes",
-    "nvfp4_matmul",
+    "nvfp4_matmul", "nvfp4_matmul_wait_probe",
 )
 
 _lib = None
@@ -144,6 +145,7 @@ def lib():
         L.nvfp4_matmul_workspace_bytes.argtypes = [I, I]
         L.nvfp4_matmul_workspace_bytes.restype = S
         L.nvfp4_matmul.argtypes = [C.POINTER(dh_matmul_t), P, I, C.c_int64, I, P, I, C.c_int64, P, S, P, P]
+        L.nvfp4_matmul_wait_probe.argtypes = [C.POINTER(dh_matmul_t), P, I, P, P, S, I, C.c_uint, P, P]
         _lib = L
     return _lib
 
@@ -603,6 +605,21 @@ class NVFP4Matmul:
         return y
 
     __call__ = forward
+
+    def wait_probe(self, x: torch.Tensor, role: int, rounds: int) -> None:
+        """Enqueue the self-test of the product's bounded waits on x [M, K] (bfloat16,
+        contiguous): `role` of the kernel's warps does nothing (see nvfp4_matmul_wait_probe);
+        device_error() tells how it ended."""
+        if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != self.K or x.device != self.packed.device or \
+                not x.is_contiguous():
+            raise ValueError(f"x must be a contiguous [M, {self.K}] bfloat16 tensor")
+        M = x.shape[0]
+        y = torch.empty((M, self.N), dtype=torch.bfloat16, device=x.device)
+        nb = lib().nvfp4_matmul_workspace_bytes(M, self.K)
+        ws = torch.empty(nb, dtype=torch.uint8, device=x.device)
+        _check("nvfp4_matmul_wait_probe",
+               lib().nvfp4_matmul_wait_probe(self.desc_ref, x.data_ptr(), M, y.data_ptr(), ws.data_ptr(), nb, role, rounds,
+                                             self.error_ptr, _stream_of(x)))
 
     def device_error(self) -> int:
         """Read and clear the device error word (waits for the device: products may be

@@ -165,6 +165,7 @@ __device__ __forceinline__ int f16_prescale_exponent(float amax) {
 namespace dh {
 
 constexpr unsigned int kDevErrTimeout = 2u;   // a bounded pipeline wait gave up
+constexpr unsigned int kDevErrUnfinished = 4u;   // self-test of a kernel that gave up: it ended with work of its own in flight
 constexpr uint32_t kWaitLimit = 1u << 22;     // try_wait rounds before giving up
 constexpr uint32_t kSuspendNs = 1000;         // suspend-time hint of a try_wait round (ns)
 

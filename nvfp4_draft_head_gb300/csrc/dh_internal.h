@@ -149,6 +149,8 @@ struct MatmulArgs {
     long long ldy;
     void* ws;
     unsigned int* error;     // device error word or null
+    int probe_role;          // the self-test of its waits (bf16 y), where probe_rounds is not 0
+    uint32_t probe_rounds;
 };
 size_t matmul_packed_bytes(int N, int K);
 size_t matmul_workspace_bytes(int M, int K);

@@ -196,7 +196,14 @@ struct Args {
     int M, N, nk;           // nk: k-stages
     int tiles_m, tiles_n;
     unsigned int* error;    // DH_DEVERR_* word or null
+    int idle;               // self-test: the role that does nothing
+    uint32_t rounds;        // self-test: tries of a wait, times kWaitSlices
 };
+
+// Roles of the warps: a bounded wait tries kWaitSlices times kWaitLimit / kWaitSlices rounds.
+enum Role { kRoleProducer, kRoleScales, kRoleIssuer, kRoleEpilogue };
+constexpr int kWaitSlices = 64;
+constexpr uint32_t kDrainRounds = kWaitLimit / kWaitSlices;   // for a role's own work in flight
 
 // Warps: epilogue, groups of scale warps that take the stages in turn, producer, issuer.
 constexpr int kEpiWarps = 16, kSfWarps = 4, kSfGroups = 2, kProducer = kEpiWarps + kSfGroups * kSfWarps, kIssuer = kProducer + 1;
@@ -223,16 +230,17 @@ struct Cfg {
 };
 
 struct Sync {
-    uint64_t full[8], empty[8], sf_full[8], acc_full[2], acc_empty[2];
+    uint64_t full[8], empty[8], sf_full[8], acc_full[2], acc_empty[2], issued;
     uint32_t tmem;
     unsigned int abort;
 };
 
 // A bounded wait that gives up at once when another role has.
+template <bool PROBE>
 __device__ __forceinline__ bool wait_or_abort(Sync& sy, uint64_t* bar, uint32_t parity, const Args& a) {
     if (mbar_test(bar, parity)) return true;
-    for (int i = 0; i < 64; ++i) {
-        if (mbar_wait(bar, parity, kWaitLimit / 64)) return true;
+    for (int i = 0; i < kWaitSlices; ++i) {
+        if (mbar_wait(bar, parity, PROBE ? a.rounds : kWaitLimit / kWaitSlices)) return true;
         if (*const_cast<volatile unsigned int*>(&sy.abort) != 0u) return false;
     }
     *const_cast<volatile unsigned int*>(&sy.abort) = 1u;
@@ -250,7 +258,9 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* w) {
                  :: "l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
 }
 
-template <class TY, int TN>
+// PROBE: the self-test of the waits (nvfp4_matmul_wait_probe): the role a.idle does
+// nothing, waits are short, and work still in flight at the end is recorded.
+template <class TY, int TN, bool PROBE>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
     using C = Cfg<TN>;
     constexpr int kStages = C::kStages, kCols = TN * 4 / kEpiWarps;   // columns per epilogue warp
@@ -268,6 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
             mbar_init(&sy.acc_full[i], 1);
             mbar_init(&sy.acc_empty[i], kEpiWarps);
         }
+        mbar_init(&sy.issued, 1);
         mbar_init_fence();
         sy.abort = 0u;
     }
@@ -278,8 +289,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
     tc::fence_after_sync();
     const uint32_t tmem = sy.tmem;
     const int tiles = a.tiles_m * a.tiles_n, first = blockIdx.x, stride = gridDim.x;
+    const int idle = PROBE ? a.idle : -1;
 
-    if (warp == kProducer && lane == 0) {
+    if (warp == kProducer && lane == 0 && idle != kRoleProducer) {
         // producer: the blocks of every k-stage of every tile of this CTA
         // operands that other tiles read too stay in L2 against the stream of results; weights
         // for one row of tiles are read once
@@ -298,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
             const uint8_t* src_b = a.b + static_cast<size_t>(tn * C::kNB) * next_block;
             const uint8_t* src_c = src_b + next_block;   // the second weight block
             for (int k = 0; k < a.nk; ++k, ++it, src_a += kBlock, src_b += kBlock, src_c += kBlock) {
-                if (it >= static_cast<uint32_t>(kStages) && !(ok = wait_or_abort(sy, &sy.empty[s], phase, a))) break;
+                if (it >= static_cast<uint32_t>(kStages) && !(ok = wait_or_abort<PROBE>(sy, &sy.empty[s], phase, a))) break;
                 uint8_t* st = smem + s * C::kStageBytes;
                 mbar_arrive_expect_tx(&sy.full[s], bytes);
                 bulk_g2s(st, src_a, kBlock, &sy.full[s], keep);
@@ -316,20 +328,20 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
         // on an abort, let the copies in flight land before the CTA ends (bounded)
         if (!ok) {
             for (uint32_t b = it > static_cast<uint32_t>(kStages) ? it - kStages : 0; b < it; ++b)
-                mbar_wait(&sy.full[b % kStages], (b / kStages) & 1, kWaitLimit / 64);
+                mbar_wait(&sy.full[b % kStages], (b / kStages) & 1, kDrainRounds);
         }
-    } else if (warp == kIssuer && lane == 0) {
+    } else if (warp == kIssuer && lane == 0 && idle != kRoleIssuer) {
         // issuer
         constexpr uint32_t kIdesc = tc::idesc_nvf4(kRows, TN);
         uint32_t it = 0, n = 0;
         bool ok = true;
         for (int tile = first; ok && tile < tiles; tile += stride, ++n) {
             const uint32_t buf = n % C::kAcc, use = n / C::kAcc;
-            if (use > 0 && !(ok = wait_or_abort(sy, &sy.acc_empty[buf], (use - 1) & 1, a))) break;
+            if (use > 0 && !(ok = wait_or_abort<PROBE>(sy, &sy.acc_empty[buf], (use - 1) & 1, a))) break;
             for (int k = 0; k < a.nk; ++k, ++it) {
                 const uint32_t s = it % kStages;
                 // the scales are stored, hence the operands have landed
-                if (!(ok = wait_or_abort(sy, &sy.sf_full[s], (it / kStages) & 1, a))) break;
+                if (!(ok = wait_or_abort<PROBE>(sy, &sy.sf_full[s], (it / kStages) & 1, a))) break;
                 tc::fence_after_sync();
                 const uint32_t st = smem_u32(smem + s * C::kStageBytes);
                 const uint64_t da = tc::desc_operand(st), db = tc::desc_operand(st + C::kB);
@@ -341,11 +353,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
             }
             if (ok) tc::commit(&sy.acc_full[buf]);
         }
-        if (!ok) {   // let the issued instructions finish before tensor memory is freed (bounded)
-            tc::commit(&sy.acc_full[n % C::kAcc]);
-            mbar_wait(&sy.acc_full[n % C::kAcc], (n / C::kAcc) & 1, kWaitLimit / 64);
-        }
-    } else if (warp >= kEpiWarps && warp < kProducer) {
+        // the issued instructions finish before tensor memory is freed, whoever gave up (bounded;
+        // a barrier of their own: an accumulator's phases depend on where this loop was left)
+        tc::commit(&sy.issued);
+        mbar_wait(&sy.issued, 0, kDrainRounds);
+    } else if (warp >= kEpiWarps && warp < kProducer && idle != kRoleScales) {
         // scales: shared memory -> registers -> this warp's 32 lanes of tensor memory
         const uint32_t at = tmem + (static_cast<uint32_t>(warp & 3) << 21);
         const uint32_t group = static_cast<uint32_t>(warp - kEpiWarps) / kSfWarps;
@@ -356,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
                 if (it % kSfGroups != group) continue;
                 const uint32_t s = it % kStages;
                 // (a landed stage means that its slot's last one, and so its scales, have been multiplied)
-                ok = __all_sync(0xFFFFFFFFu, wait_or_abort(sy, &sy.full[s], (it / kStages) & 1, a));
+                ok = __all_sync(0xFFFFFFFFu, wait_or_abort<PROBE>(sy, &sy.full[s], (it / kStages) & 1, a));
                 if (!ok) break;
                 tc::fence_after_sync();
                 const uint32_t st = smem_u32(smem + s * C::kStageBytes) + lane * 16;
@@ -378,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
                 if (lane == 0) mbar_arrive(&sy.sf_full[s]);
             }
         }
-    } else if (warp < kEpiWarps) {
+    } else if (warp < kEpiWarps && idle != kRoleEpilogue) {
         const float gb = __ldg(a.gb);
         const int quarter = warp & 3, part = warp >> 2;
         const bool vec = (reinterpret_cast<uintptr_t>(a.y) & 31u) == 0 && (a.ldy * static_cast<long long>(sizeof(TY))) % 32 == 0;
@@ -387,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
             const int m = (tile % a.tiles_m) * kRows + quarter * 32 + lane, n0 = (tile / a.tiles_m) * TN + part * kCols;
             const float g = m < a.M ? a.ga[m] * gb : 0.0f;
             const uint32_t buf = n % C::kAcc, acc = tmem + (static_cast<uint32_t>(quarter) << 21) + buf * TN + part * kCols;
-            const bool ok = wait_or_abort(sy, &sy.acc_full[buf], (n / C::kAcc) & 1, a);
+            const bool ok = wait_or_abort<PROBE>(sy, &sy.acc_full[buf], (n / C::kAcc) & 1, a);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             tc::fence_after_sync();
             TY* row = static_cast<TY*>(a.y) + static_cast<size_t>(m) * a.ldy + n0;
@@ -459,10 +471,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
+    if (PROBE && threadIdx.x == 0 && a.error != nullptr && idle != kRoleIssuer && !mbar_test(&sy.issued, 0))
+        atomicOr(a.error, kDevErrUnfinished);
     if (warp == 0) tc::tmem_free(tmem, C::kCols);
 }
 
-template <class TY, int TN>
+template <class TY, int TN, bool PROBE>
 static cudaError_t launch_product(Args a, cudaStream_t s) {
     using C = Cfg<TN>;
     const int sms = sm_count();
@@ -476,11 +490,11 @@ static cudaError_t launch_product(Args a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev >= kDevices) return cudaErrorInvalidDevice;
     if (!known[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(product_kernel<TY, TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        e = cudaFuncSetAttribute(product_kernel<TY, TN, PROBE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
         if (e != cudaSuccess) return e;
         known[dev].store(true, std::memory_order_release);
     }
-    product_kernel<TY, TN><<<static_cast<unsigned>(tiles < sms ? tiles : sms), kThreads, C::kSmem, s>>>(a);
+    product_kernel<TY, TN, PROBE><<<static_cast<unsigned>(tiles < sms ? tiles : sms), kThreads, C::kSmem, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -492,7 +506,7 @@ static cudaError_t launch_quantize(const void* x, long long ldx, int M, int K, u
     return cudaGetLastError();
 }
 
-template <class TY>
+template <class TY, bool PROBE = false>
 static cudaError_t launch_tiles(const Args& a, cudaStream_t s) {
     // Wide tiles read fewer operand bytes per product, narrow ones spread a small
     // product over more SMs. By rounds of tiles times the tile's width, wide where that
@@ -505,7 +519,7 @@ static cudaError_t launch_tiles(const Args& a, cudaStream_t s) {
         const long long tiles = static_cast<long long>(a.tiles_m) * blocks_of(a.N, tn);
         return (tiles + sms - 1) / sms * tn;
     };
-    return 8 * cost(256) <= 9 * cost(128) ? launch_product<TY, 256>(a, s) : launch_product<TY, 128>(a, s);
+    return 8 * cost(256) <= 9 * cost(128) ? launch_product<TY, 256, PROBE>(a, s) : launch_product<TY, 128, PROBE>(a, s);
 }
 
 }  // namespace mm
@@ -546,6 +560,11 @@ cudaError_t launch_matmul(const MatmulArgs& m, cudaStream_t s) {
     a.nk = mm::blocks_of(m.K, mm::kStageK);
     a.tiles_m = mm::blocks_of(m.M, mm::kRows);
     a.error = m.error;
+    if (m.probe_rounds != 0) {
+        a.idle = m.probe_role;
+        a.rounds = m.probe_rounds;
+        return mm::launch_tiles<__nv_bfloat16, true>(a, s);
+    }
     switch (m.y_type) {
         case DH_T_BF16: return mm::launch_tiles<__nv_bfloat16>(a, s);
         case DH_T_F16: return mm::launch_tiles<__half>(a, s);
