@@ -233,6 +233,7 @@ struct Sync {
     uint64_t full[8], empty[8], sf_full[8], acc_full[2], acc_empty[2], issued;
     uint32_t tmem;
     unsigned int abort;
+    uint32_t copies;   // self-test: stages that the producer filled
 };
 
 // A bounded wait that gives up at once when another role has.
@@ -281,6 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
         mbar_init(&sy.issued, 1);
         mbar_init_fence();
         sy.abort = 0u;
+        sy.copies = 0u;
     }
     __syncwarp();
     if (warp == 0) tc::tmem_alloc(&sy.tmem, C::kCols);
@@ -325,11 +327,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
                 }
             }
         }
-        // on an abort, let the copies in flight land before the CTA ends (bounded)
-        if (!ok) {
-            for (uint32_t b = it > static_cast<uint32_t>(kStages) ? it - kStages : 0; b < it; ++b)
-                mbar_wait(&sy.full[b % kStages], (b / kStages) & 1, kDrainRounds);
-        }
+        // the copies in flight land before the CTA ends, whoever gave up (bounded)
+        for (uint32_t b = it > static_cast<uint32_t>(kStages) ? it - kStages : 0; b < it; ++b)
+            mbar_wait(&sy.full[b % kStages], (b / kStages) & 1, kDrainRounds);
+        if (PROBE) sy.copies = it;
     } else if (warp == kIssuer && lane == 0 && idle != kRoleIssuer) {
         // issuer
         constexpr uint32_t kIdesc = tc::idesc_nvf4(kRows, TN);
@@ -471,8 +472,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Args a) {
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (PROBE && threadIdx.x == 0 && a.error != nullptr && idle != kRoleIssuer && !mbar_test(&sy.issued, 0))
-        atomicOr(a.error, kDevErrUnfinished);
+    if (PROBE && threadIdx.x == 0) {
+        bool done = idle == kRoleIssuer || mbar_test(&sy.issued, 0);
+        for (uint32_t i = 0; i < static_cast<uint32_t>(kStages); ++i)   // the last use of slot i
+            if (i < sy.copies) done = mbar_test(&sy.full[i], ((sy.copies - 1 - i) / kStages) & 1) && done;
+        if (!done && a.error != nullptr) atomicOr(a.error, kDevErrUnfinished);
+    }
     if (warp == 0) tc::tmem_free(tmem, C::kCols);
 }
 
