@@ -716,7 +716,7 @@ template <class A, void (*KERNEL)(A)>
 static cudaError_t launch_rows(A a, long long row_bytes, RowCost c, int threads, int smem, cudaStream_t s) {
     constexpr int kDevices = 64;
     static std::atomic<bool> known[kDevices];
-    static RowLaunch info[kDevices];   // written with equal values by concurrent first callers
+    static std::atomic<int> fits[kDevices][4];   // (concurrent first callers store equal values)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -724,10 +724,11 @@ static cudaError_t launch_rows(A a, long long row_bytes, RowCost c, int threads,
     if (!known[dev].load(std::memory_order_acquire)) {
         RowLaunch l = {};
         if ((e = row_launch_setup<A, KERNEL>(threads, smem, l)) != cudaSuccess) return e;
-        info[dev] = l;
+        for (int i = 0; i < 4; ++i) fits[dev][i].store(l.fit[i], std::memory_order_relaxed);
         known[dev].store(true, std::memory_order_release);
     }
-    const RowLaunch& fit = info[dev];
+    RowLaunch fit;
+    for (int i = 0; i < 4; ++i) fit.fit[i] = fits[dev][i].load(std::memory_order_relaxed);
     unsigned lg = 0;
     long long best = 0;
     for (unsigned l = 0; l < 4 && fit.fit[l] > 0; ++l) {
