@@ -464,7 +464,9 @@ int draft_head_distill(const dh_logits_t *lg, const int32_t *ids, const void *va
 
 /* The gradient of draft_head_distill from its lse, for a caller that learns the
  * row weights after the loss (weight[m] = the upstream gradient of loss[m] times
- * the forward's weight; NULL: 1): dz as above, with q = e^(z / t - lse). */
+ * the forward's weight; NULL: 1): dz as above, with q = e^(z / t - lse), which
+ * carries lse's rounding to fp32 (2^-24 |lse| at most, relative). A row with |lse| >= 1024
+ * or not finite is summed again from its logits instead. */
 int draft_head_distill_backward(const dh_logits_t *lg, const int32_t *ids, const void *val, int val_type,
                                 int K, const float *lse, const float *weight, void *dz, int64_t ld_dz,
                                 void *stream);

@@ -42,6 +42,11 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;    // vectors per batch and thread
 constexpr int kDepth = 2;     // batches in flight: 32 KB per CTA
 constexpr int kPerSm = 3;     // CTAs per SM
+// A kept normaliser is rounded to 32 bits, and e^(z / t - lse) carries that rounding, half the
+// spacing of such numbers: 3e-5 up to this limit. Rows farther from zero (at a type's lowest value throughout, say, where
+// the logarithm of the sum is lost altogether) are summed again from their logits: 256 rows of
+// 248,320 f32, all of them so, 127 us against 86.
+constexpr float kLseLimit = 1024.0f;
 
 struct DistillSmem {
     float warp[2][kWarps][3];
@@ -161,6 +166,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) distill_kernel(const Distill
         if (!stream.alike) sl = make_slice(z, a.C, rank, lg);
         const int edge = edge_column(sl, a.C, rank, ncta), batches = St::batches_of(sl);
         const float w = a.weight != nullptr ? __ldg(a.weight + row) : 1.0f;
+        const float lse = kStats ? 0.0f : __ldg(a.lse_in + row);
         int col[E];
         float t[E], zt[E], ze = kNegInf;
 #pragma unroll
@@ -259,19 +265,26 @@ __global__ void __launch_bounds__(kThreads, kPerSm) distill_kernel(const Distill
         const float wt = w * a.t;
         if (kGrad) {
             // w t q = scale * 2^(z c - mc), or 2^((z - m) c) where the plain form was needed,
-            // with scale = w t / s; from a kept normaliser, w t e^(z / t - lse)
-            const float lse = kStats ? 0.0f : a.lse_in[row];
-            const float scale = !some ? 0.0f : kStats ? wt / all.s : wt;
-            const float nmc = -shift_of(all.m, c);
-            const auto wtq = [&](float x) {
-                if (!kStats) return scale * ex2(fmaf(x, a.inv_t, -lse) * kLog2e);
-                return scale * ex2(plain ? (x - all.m) * c : fmaf(x, c, nmc));
-            };
+            // with scale = w t / s; from a kept normaliser scale * 2^((z - m) c) too, with m = lse t and
+            // what its rounding leaves in scale, or as in the plain form where lse does not serve
+            float scale = 0.0f;
+            if (!kStats && some) {
+                all.m = __fmul_rn(lse, a.t);
+                scale = wt * expf(-fmaf(lse, a.t, -all.m) * a.inv_t);
+                if (!(fabsf(lse) < kLseLimit)) {
+                    all = plain_slice_of<T, false, kThreads, 4>(z, sl, ze, c, sm.plain);
+                    all = stat_cluster<false, true>(all, c, sm.cta_plain, rank, ncta);
+                    scale = wt / all.s;
+                }
+            } else if (some) {
+                scale = wt / all.s;
+            }
+            const float nmc = kStats ? -shift_of(all.m, c) : -all.m;
+            const auto wtq = [&](float x) { return scale * ex2(!kStats || plain ? (x - all.m) * c : fmaf(x, c, nmc)); };
             // (S itself for the teacher's columns, where q meets p: 2^rest taken off)
             const float sum_t = kStats && teacher && !plain ? all.s * expf(-shift_rest(all.m, c) * kLn2) : all.s;
             const bool vec_out = ((reinterpret_cast<uintptr_t>(dz) ^ reinterpret_cast<uintptr_t>(z)) & 15u) == 0;
-            const uint64_t mul2 = kStats ? pack_f32x2(c, c) : pack_f32x2(a.inv_t, a.inv_t);
-            const uint64_t add2 = kStats ? pack_f32x2(nmc, nmc) : pack_f32x2(-lse, -lse), scale2 = pack_f32x2(scale, scale);
+            const uint64_t mul2 = pack_f32x2(c, c), add2 = pack_f32x2(nmc, nmc), scale2 = pack_f32x2(scale, scale);
             T* out = dz + sl.head + (static_cast<size_t>(sl.v0) + tid) * kVec;
             for (int b = 0; b < batches; ++b, out += kUnroll * kThreads * kVec) {
                 cp_async_wait<kDepth - 1>();
@@ -287,8 +300,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) distill_kernel(const Distill
                         Elem<T>::unpack(v[u], x);
 #pragma unroll
                         for (int j = 0; j < kVec; j += 2) {
-                            uint64_t y = fma_f32x2(pack_f32x2(x[j], x[j + 1]), mul2, add2);
-                            if (!kStats) y = mul_f32x2(y, pack_f32x2(kLog2e, kLog2e));
+                            const uint64_t z2 = pack_f32x2(x[j], x[j + 1]);
+                            const uint64_t y = kStats ? fma_f32x2(z2, mul2, add2) : mul_f32x2(add_f32x2(z2, add2), mul2);
                             float y0, y1;
                             unpack_f32x2(y, y0, y1);
                             unpack_f32x2(mul_f32x2(pack_f32x2(ex2(y0), ex2(y1)), scale2), x[j], x[j + 1]);

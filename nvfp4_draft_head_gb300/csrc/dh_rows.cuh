@@ -476,13 +476,13 @@ __device__ __noinline__ float row_top(float top, float (*buf)[3], float (*all)[3
     return m;
 }
 
-// The statistics of a CTA's slice in the plain form, from global memory (rows that
-// stat_fits() refuses and that are not masked throughout; rare).
-template <class T, bool ENTROPY, int NT>
-__device__ __noinline__ Stat plain_slice(const T* z, const Slice& sl, float ze, float c, float (*buf)[3]) {
-    constexpr int kVec = Elem<T>::kVec, U = 4;
+// The statistics of a CTA's slice in the plain form, from global memory, U vectors at a time.
+template <class T, bool ENTROPY, int NT, int U>
+__device__ __forceinline__ Stat plain_slice_of(const T* z, const Slice& sl, float ze, float c, float (*buf)[3]) {
+    constexpr int kVec = Elem<T>::kVec;
     Stat st = {-FLT_MAX, 0.0f, 0.0f};
     plain_add1<ENTROPY>(st, ze, c);
+#pragma unroll 1
     for (int v0 = sl.v0 + threadIdx.x; v0 < sl.v1; v0 += U * NT) {
         uint4 w[U];
 #pragma unroll
@@ -495,6 +495,13 @@ __device__ __noinline__ Stat plain_slice(const T* z, const Slice& sl, float ze, 
     stat_leave(st, buf);
     __syncthreads();
     return stat_gather<ENTROPY, true>(NT / 32, c, buf, -FLT_MAX);
+}
+
+// The same out of line, for rows that stat_fits() refuses and that are not masked
+// throughout (rare).
+template <class T, bool ENTROPY, int NT>
+__device__ __noinline__ Stat plain_slice(const T* z, const Slice& sl, float ze, float c, float (*buf)[3]) {
+    return plain_slice_of<T, ENTROPY, NT, 4>(z, sl, ze, c, buf);
 }
 
 // ---------------------------------------------------------------- streaming --
