@@ -43,9 +43,9 @@ constexpr int kUnroll = 4;    // vectors per batch and thread
 constexpr int kDepth = 2;     // batches in flight: 32 KB per CTA
 constexpr int kPerSm = 3;     // CTAs per SM
 // A kept normaliser is rounded to 32 bits, and e^(z / t - lse) carries that rounding, half the
-// spacing of such numbers: 3e-5 up to this limit. Rows farther from zero (at a type's lowest value throughout, say, where
-// the logarithm of the sum is lost altogether) are summed again from their logits: 256 rows of
-// 248,320 f32, all of them so, 127 us against 86.
+// spacing of such numbers: 3e-5 up to this limit. Rows farther from zero (at a type's lowest
+// value throughout, say, where the logarithm of the sum is lost altogether) are summed again from
+// their logits: 256 rows of 248,320 f32, all of them so, 127 us against 86.
 constexpr float kLseLimit = 1024.0f;
 
 struct DistillSmem {
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) distill_kernel(const Distill
             if (!kStats && some) {
                 all.m = __fmul_rn(lse, a.t);
                 scale = wt * expf(-fmaf(lse, a.t, -all.m) * a.inv_t);
-                if (!(fabsf(lse) < kLseLimit)) {
+                if (!(fabsf(lse) < kLseLimit && fabsf(all.m) <= FLT_MAX)) {
                     all = plain_slice_of<T, false, kThreads, 4>(z, sl, ze, c, sm.plain);
                     all = stat_cluster<false, true>(all, c, sm.cta_plain, rank, ncta);
                     scale = wt / all.s;

@@ -52,3 +52,20 @@ def test_rows_far_from_zero(dtype, M, n, t):
     want = dh.distill_topk_backward(z, ids, val, lse, w, temperature=t)
     got = dh.distill_topk_backward(z, ids, val, lse, w, temperature=t, dlogits=z)
     assert torch.equal(got.nan_to_num(7.0), want.nan_to_num(7.0))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("t", [1e-38, 1e-20, 1e20, 1e37])
+def test_ends_of_the_temperatures_range(dtype, t):
+    """The normaliser is ordinary, its product with t is not. (At 1e-38 and 1e-20 the
+    logits are scaled with t, so that the probabilities are ordinary too.)"""
+    z = rand_rows(7, 901, TYPES[dtype], 4)
+    ids, val = teacher(z, 5, 1)
+    if t < 1:
+        z, val = (z.float() * t).to(z.dtype), val * t
+    ref = ref_distill(z, ids, val, t, None, None)
+    _, _, e, S = ref_stats(z, t)
+    _, lse = dh.distill_topk_forward(z, ids, val, temperature=t)
+    got = dh.distill_topk_backward(z, ids, val, lse, temperature=t)
+    # (results below the normal range are rounded to its spacing there, or flushed)
+    close(got, ref[2], ref[3] + t * 7e-5 * e / S + 2.0 ** -126, "backward")
