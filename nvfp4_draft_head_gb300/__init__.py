@@ -22,8 +22,8 @@ Names follow the C ABI in include/drafthead.h:
   distill_topk             draft_head_distill: distillation loss and gradient
   (_forward, _backward)    the loss alone; the gradient from its normaliser
   DistillTopK              the same as a torch.autograd function
-From NVFP4Matmul on, a call given stream= works and allocates on that stream: its
-arguments have to be ready there, and its results are, for what follows on it.
+A call given stream= works and allocates on that stream: its arguments have to be
+ready there, and its results are, for what follows on it.
 The vocabulary-sharded head (the local-argmax exchange) is in .sharded.
 """
 from __future__ import annotations
@@ -172,6 +172,26 @@ def _stream(stream=None) -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+def _keep_for(stream, *values) -> None:
+    """Tensors (of any values) used on `stream`, not their own, stay allocated until its work is done."""
+    for t in values:
+        if isinstance(t, torch.Tensor):
+            t.record_stream(stream)
+
+
+def _on_stream(stream, call, *args):
+    """call(*args) with `stream` current, for a caller that asked for it: what the
+    call allocates comes from that stream's own pool (a block of the caller's
+    stream may still be in use by work pending there) and is filled on it. The
+    arguments stay allocated for `stream`'s work, the results for the caller's."""
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        out = call(*args)
+    _keep_for(stream, *args)
+    _keep_for(here, *(out if isinstance(out, tuple) else (out,)))
+    return out
+
+
 def _workspace(nbytes: int, device) -> torch.Tensor:
     """Zeroed device buffer whose data pointer is DH_WORKSPACE_ALIGN-aligned."""
     buf = torch.zeros(nbytes + DH_WORKSPACE_ALIGN, dtype=torch.uint8, device=device)
@@ -203,6 +223,8 @@ def _gather_args(W: torch.Tensor, idx: torch.Tensor):
 
 def nvfp4_quantize_rows(W: torch.Tensor, idx: torch.Tensor, stream=None):
     """(q uint8[N, K/2], sf uint8[N, K/16], g float32[1]) of the rows W[idx]."""
+    if stream is not None:
+        return _on_stream(stream, nvfp4_quantize_rows, W, idx)
     V, K, N = _gather_args(W, idx)
     q = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device)
     sf = torch.empty((N, K // 16), dtype=torch.uint8, device=W.device)
@@ -211,13 +233,15 @@ def nvfp4_quantize_rows(W: torch.Tensor, idx: torch.Tensor, stream=None):
     ws = _workspace(nb, W.device)
     _check("nvfp4_quantize_rows",
            lib().nvfp4_quantize_rows(W.data_ptr(), V, K, idx.data_ptr(), N, q.data_ptr(),
-                                     sf.data_ptr(), g.data_ptr(), ws.data_ptr(), nb, _stream(stream)))
-    _raise_device_error(ws, stream, "nvfp4_quantize_rows")
+                                     sf.data_ptr(), g.data_ptr(), ws.data_ptr(), nb, _stream()))
+    _raise_device_error(ws, "nvfp4_quantize_rows")
     return q, sf, g
 
 
 def fp8_quantize_rows(W: torch.Tensor, idx: torch.Tensor, stream=None):
     """(q uint8[N, K] E4M3 codes, scale float32[1]) of the rows W[idx]."""
+    if stream is not None:
+        return _on_stream(stream, fp8_quantize_rows, W, idx)
     V, K, N = _gather_args(W, idx)
     q = torch.empty((N, K), dtype=torch.uint8, device=W.device)
     s = torch.empty(1, dtype=torch.float32, device=W.device)
@@ -225,33 +249,37 @@ def fp8_quantize_rows(W: torch.Tensor, idx: torch.Tensor, stream=None):
     ws = _workspace(nb, W.device)
     _check("fp8_quantize_rows",
            lib().fp8_quantize_rows(W.data_ptr(), V, K, idx.data_ptr(), N, q.data_ptr(),
-                                   s.data_ptr(), ws.data_ptr(), nb, _stream(stream)))
-    _raise_device_error(ws, stream, "fp8_quantize_rows")
+                                   s.data_ptr(), ws.data_ptr(), nb, _stream()))
+    _raise_device_error(ws, "fp8_quantize_rows")
     return q, s
 
 
 def nvfp4_pack_head(q: torch.Tensor, sf: torch.Tensor, stream=None) -> torch.Tensor:
     """Tile-major copy of an NVFP4 head (DH_FMT_NVFP4_PACKED): uint8 [N/16, K/128, 1152]."""
+    if stream is not None:
+        return _on_stream(stream, nvfp4_pack_head, q, sf)
     N, Kh = q.shape
     K = 2 * Kh
     if sf.shape != (N, K // 16) or q.dtype != torch.uint8 or sf.dtype != torch.uint8:
         raise ValueError("q must be uint8 [N, K/2] and sf uint8 [N, K/16]")
     packed = torch.empty((N // 16, K // 128, 1152), dtype=torch.uint8, device=q.device)
     _check("nvfp4_pack_head",
-           lib().nvfp4_pack_head(q.data_ptr(), sf.data_ptr(), N, K, packed.data_ptr(), _stream(stream)))
+           lib().nvfp4_pack_head(q.data_ptr(), sf.data_ptr(), N, K, packed.data_ptr(), _stream()))
     return packed
 
 
 def fp8_quantize_activations(h: torch.Tensor, stream=None):
     """(qx uint8[M, K] E4M3 codes, sx float32[M] scales): per-token dynamic FP8
     quantisation of BF16 hidden states, as the W8A8 head's draft step does it."""
+    if stream is not None:
+        return _on_stream(stream, fp8_quantize_activations, h)
     if h.dtype != torch.bfloat16 or h.dim() != 2 or not h.is_cuda or not h.is_contiguous():
         raise ValueError("h must be a contiguous [M, K] bfloat16 CUDA tensor")
     M, K = h.shape
     qx = torch.empty((M, K), dtype=torch.uint8, device=h.device)
     sx = torch.empty(M, dtype=torch.float32, device=h.device)
     _check("fp8_quantize_activations",
-           lib().fp8_quantize_activations(h.data_ptr(), M, K, qx.data_ptr(), sx.data_ptr(), _stream(stream)))
+           lib().fp8_quantize_activations(h.data_ptr(), M, K, qx.data_ptr(), sx.data_ptr(), _stream()))
     return qx, sx
 
 
@@ -279,8 +307,8 @@ def draft_head_wait_probe(ws: torch.Tensor | None, kind: int, rounds: int, strea
                                        _stream(stream)))
 
 
-def _raise_device_error(ws, stream, fn):
-    err = draft_head_read_device_error(ws, stream)
+def _raise_device_error(ws, fn):
+    err = draft_head_read_device_error(ws)
     if err:
         raise RuntimeError(f"{fn}: device error word {err:#x} (a dh_idx entry outside [0, V))")
 
@@ -330,6 +358,8 @@ class DraftHead:
     def top_tokens(self, h: torch.Tensor, ids: torch.Tensor | None = None,
                    top: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """get_top_tokens: int32[M] target ids of the argmax over kept rows."""
+        if ids is None and stream is not None:
+            return _on_stream(stream, self.top_tokens, h, None, top)
         M = self._check_h(h)
         if ids is None:
             ids = torch.empty(M, dtype=torch.int32, device=h.device)
@@ -343,6 +373,8 @@ class DraftHead:
         """This head as one vocabulary shard: int64[M] argmax keys (largest
         logit, then lowest target id) whose maximum over shards is the whole
         head's; needs an ascending dh_idx."""
+        if keys is None and stream is not None:
+            return _on_stream(stream, self.top_keys, h)
         M = self._check_h(h)
         if keys is None:
             keys = torch.empty(M, dtype=torch.int64, device=h.device)
@@ -377,6 +409,8 @@ class DraftHead:
     def compute_logits(self, h: torch.Tensor, out: torch.Tensor | None = None,
                        stream=None) -> torch.Tensor:
         """compute_logits: float32[M, V], -inf outside the kept ids."""
+        if out is None and stream is not None:
+            return _on_stream(stream, self.compute_logits, h)
         M = self._check_h(h)
         if out is None:
             out = torch.empty((M, self.V), dtype=torch.float32, device=h.device)
@@ -397,6 +431,8 @@ class DraftHead:
 def keys_to_ids(keys: torch.Tensor, ids: torch.Tensor | None = None, top: torch.Tensor | None = None,
                 stream=None) -> torch.Tensor:
     """Target ids (and, into `top`, the winning logits) of argmax keys."""
+    if ids is None and stream is not None:
+        return _on_stream(stream, keys_to_ids, keys, None, top)
     M = keys.numel()
     if keys.dtype != torch.int64 or not keys.is_contiguous():
         raise ValueError("keys must be a contiguous int64 tensor")
@@ -435,11 +471,14 @@ class NVFP4Linear:
     x W'^T in fp32. N % 64 == 0."""
 
     def __init__(self, W: torch.Tensor, stream=None):
+        if stream is not None:
+            _on_stream(stream, self.__init__, W)
+            return _keep_for(torch.cuda.current_stream(stream.device), self.q, self.sf, self.g, self.packed, self.ws)
         N, K = W.shape
         idx = torch.arange(N, dtype=torch.int32, device=W.device)
-        q, sf, g = nvfp4_quantize_rows(W, idx, stream)
+        q, sf, g = nvfp4_quantize_rows(W, idx)
         self.q, self.sf, self.g = q, sf, g
-        self.packed = nvfp4_pack_head(q, sf, stream)
+        self.packed = nvfp4_pack_head(q, sf)
         self.N, self.K = N, K
         self.desc = dh_head_t(DH_FMT_NVFP4_PACKED, N, K, N, N, _ptr(self.packed), None, _ptr(g), None, 0)
         self.ws_bytes = lib().draft_head_workspace_bytes(C.byref(self.desc), DH_MAX_M)
@@ -457,6 +496,8 @@ class NVFP4Linear:
     def forward(self, x: torch.Tensor, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != self.K or not x.is_contiguous():
             raise ValueError(f"x must be a contiguous [M, {self.K}] bfloat16 tensor")
+        if y is None and stream is not None:
+            return _on_stream(stream, self.forward, x)
         M = x.shape[0]
         if y is None:
             y = torch.empty((M, self.N), dtype=torch.float32, device=x.device)
@@ -493,26 +534,6 @@ _TYPES = {torch.bfloat16: DH_T_BF16, torch.float16: DH_T_F16, torch.float32: DH_
 def _vector(t: torch.Tensor | None, name: str, dtype: torch.dtype, n: int | None, device) -> None:
     if t is not None and (t.dtype != dtype or t.device != device or not t.is_contiguous() or (n is not None and t.numel() != n)):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor{'' if n is None else f' of {n} elements'} on {device}")
-
-
-def _keep_for(stream, *values) -> None:
-    """Tensors (of any values) used on `stream`, not their own, stay allocated until its work is done."""
-    for t in values:
-        if isinstance(t, torch.Tensor):
-            t.record_stream(stream)
-
-
-def _on_stream(stream, call, *args):
-    """call(*args) with `stream` current, for a caller that asked for it: what the
-    call allocates comes from that stream's own pool (a block of the caller's
-    stream may still be in use by work pending there) and is filled on it. The
-    arguments stay allocated for `stream`'s work, the results for the caller's."""
-    here = torch.cuda.current_stream(stream.device)
-    with torch.cuda.stream(stream):
-        out = call(*args)
-    _keep_for(stream, *args)
-    _keep_for(here, *(out if isinstance(out, tuple) else (out,)))
-    return out
 
 
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
