@@ -20,7 +20,7 @@ import numpy as np
 import torch
 import torch.distributed as dist
 
-from . import DH_FMT_NVFP4, DH_FMT_NVFP4_PACKED, DraftHead, keys_to_ids, nvfp4_pack_head
+from . import DH_FMT_NVFP4, DH_FMT_NVFP4_PACKED, DraftHead, _on_stream, keys_to_ids, nvfp4_pack_head
 
 
 class ShardExchangeError(RuntimeError):
@@ -77,12 +77,16 @@ class ShardedDraftHead:
 
     def top_tokens(self, h: torch.Tensor, ids: torch.Tensor | None = None, top: torch.Tensor | None = None,
                    stream=None) -> torch.Tensor:
-        keys = self.shard.top_keys(h, stream=stream)
+        if stream is not None:   # the exchange is ordered on the current stream
+            return _on_stream(stream, self.top_tokens, h, ids, top)
+        keys = self.shard.top_keys(h)
         exchange_keys(keys, self.group)
-        return keys_to_ids(keys, ids, top, stream)
+        return keys_to_ids(keys, ids, top)
 
     def compute_logits(self, h: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-        out = self.shard.compute_logits(h, out, stream)
+        if stream is not None:
+            return _on_stream(stream, self.compute_logits, h, out)
+        out = self.shard.compute_logits(h, out)
         try:
             dist.all_reduce(out, op=dist.ReduceOp.MAX, group=self.group)
         except Exception as e:

@@ -61,3 +61,32 @@ def test_linear(h):
         made = dh.NVFP4Linear(W, stream=s)
         return made.q, made.sf, made.g, made.packed
     beside_pending_work(build, [4 * N])
+
+
+def test_sharded_exchange_runs_on_the_given_stream(head, h, monkeypatch):
+    """The exchange (a stand-in here: one shard, whose keys and logits it rewrites on the
+    current stream) is ordered between the shard's step and what follows."""
+    from nvfp4_draft_head_gb300 import sharded
+    seen = []
+
+    def exchange(t, *args, **kw):
+        seen.append(torch.cuda.current_stream())
+        t.copy_(t.clone())
+        return t
+
+    monkeypatch.setattr(sharded, "exchange_keys", exchange)
+    monkeypatch.setattr(sharded.dist, "all_reduce", exchange)
+    shard = sharded.ShardedDraftHead(head)
+    want_ids, want = head.top_tokens(h), head.compute_logits(h)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    ids, out = torch.empty_like(want_ids), torch.empty_like(want)
+    made = shard.top_tokens(h, stream=side), shard.compute_logits(h, stream=side)
+    shard.top_tokens(h, ids, stream=side)
+    shard.compute_logits(h, out, stream=side)
+    assert seen == [side] * 4
+    side.synchronize()
+    torch.cuda.synchronize()
+    for got in (made, (ids, out)):
+        assert torch.equal(got[0], want_ids) and torch.equal(got[1], want)
