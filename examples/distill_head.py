@@ -12,6 +12,10 @@ in front of the reduced-vocabulary NVFP4 head):
             weights and activations are taken straight through) into the layer;
   scoring   token_logprobs of the target's tokens under the drafter.
 
+Student and scores are those of the W4A4 product. A drafter that is served through the
+W4A16 draft step samples from slightly other logits (see NVFP4Matmul): acceptance is
+measured on DraftHead.compute_logits.
+
 Run: python examples/distill_head.py [--steps N] (needs the GPU; sizes of the small
 head: 16,384 ids, 4,000 kept, 256 wide).
 """

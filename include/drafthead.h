@@ -337,7 +337,8 @@ typedef enum { DH_T_BF16 = 1, DH_T_F16 = 2, DH_T_F32 = 3 } dh_type;
 /* NVFP4 x NVFP4 product of many tokens (W4A4), for the batches past the draft
  * step's 16 rows: prefill and scoring through the head or an MTP-block linear
  * (the pages run those linears W4A16; four-bit activations are this library's
- * addition). Weights are an NVFP4 weight [N][K] as written by nvfp4_quantize_rows,
+ * addition, and change a logit by about a tenth of the logits' spread against the
+ * draft step's W4A16). Weights are an NVFP4 weight [N][K] as written by nvfp4_quantize_rows,
  * laid out once by nvfp4_pack_matmul; the activations are quantised inside the
  * call by the same recipe with one global scale per token: for row m,
  *   gx = max(max_k |x[m, k]|, 1e-12) / 2688, per block of 16 s = E4M3_RNE(bamax /

@@ -558,8 +558,14 @@ class NVFP4Matmul:
     """An NVFP4 weight for many-token products: forward(x) = x W'^T with x
     quantised to NVFP4 per token (W4A4) and fp32 accumulation. q uint8 [N, K/2],
     sf uint8 [N, K/16] and g float32 [1] as from nvfp4_quantize_rows; N % 64 == 0,
-    K % 16 == 0. For up to 16 tokens NVFP4Linear and DraftHead keep the
-    activations in bfloat16. No gradient: an x that requires one is refused."""
+    K % 16 == 0. No gradient: an x that requires one is refused.
+
+    These are not the logits of the draft step: for up to 16 tokens NVFP4Linear and
+    DraftHead keep the activations in bfloat16 (W4A16). Four-bit activations change a
+    logit by about a tenth of the logits' spread (a 64,064 x 2,560 head on normal
+    hidden states: rms 0.096 of the standard deviation; 0.16 where one channel in 211
+    is 30 times the rest), so what is scored here is the W4A4 head: for acceptance
+    rates and rejection sampling of a served W4A16 head take DraftHead.compute_logits."""
 
     def __init__(self, q: torch.Tensor, sf: torch.Tensor, g: torch.Tensor, stream=None):
         if stream is not None:

@@ -23,8 +23,9 @@
 // Loss and gradient together stream every row twice; the second time it comes
 // from L2, where the rows in work (three per SM) fit.
 //
-// Bound: instruction issue, near HBM. Loss and gradient of 4,096 rows of 64,026 bf16:
-// 202 us, 5.2 of the measured 6.8 TB/s (155 us); 14 instructions per 32 logits and
+// Bound: latency at three CTAs per SM (issue 57 of 100 cycles, loads and the barriers of
+// a row's ends the largest stalls), near HBM. Loss and gradient of 4,096 rows of 64,026
+// bf16: 202 us, 5.2 of the measured 6.8 TB/s (155 us); 14 instructions per 32 logits and
 // 5,600 a row. The gradient alone, 256 rows of 248,320 f32: 84 us (75), the loss alone,
 // 1,021 rows of 64,026 bf16, a tenth of them masked throughout: 30 us (19). Three CTAs
 // of 256 threads per SM (512 threads twice: 244 us; 256 threads twice 206, four

@@ -22,10 +22,11 @@
 // equal values) or a NaN send the CTA to an exact radix selection over its slice
 // instead. The CTAs' sorted lists are merged by the first CTA.
 //
-// Bound: instruction issue. 4,096 rows of 64,026 bf16, 20 alternatives: 130 us, 4.0 of
-// the measured 6.8 TB/s (77 us); 7 instructions per 32 logits go into the statistics,
-// about 1.5 into reading the candidates' vectors again and 5,600 into a row's ends,
-// and the SMs issue in 56 of 100 cycles. Three CTAs of 256 threads per SM, so that
+// Bound: latency, with three CTAs per SM to hide it: 4,096 rows of 64,026 bf16, 20
+// alternatives, take 130 us, 4.0 of the measured 6.8 TB/s (77 us). The SMs issue in 56
+// of 100 cycles and DRAM is busy in 42; the largest stall is the barriers of a row's
+// ends. 7 instructions per 32 logits go into the statistics, about 1.5 into reading the
+// candidates' vectors again and 5,600 into a row's ends. Three CTAs of 256 threads per SM, so that
 // one row's ends run under the others' streaming (two CTAs of 512 threads: 169 us,
 // 256 threads twice 159, four times 149, 128 threads four times 183), with two batches of
 // four vectors in flight each (two vectors, four batches: 150; four and three: 169).

@@ -26,10 +26,12 @@
 //
 // Bound, 8,192 tokens on a 64,064 x 2,560 head (567 us with the quantiser's 20:
 // 4.8 PFLOP/s; 1.05 GB of results alone take 155 us at the measured copy rate): a
-// stage's way through the ring. A 128 x 256 x 256 step takes 515 ns, 270 of them
-// matrix instructions; it moves 55 KB into shared memory and reads 72 KB there (48
-// for the matrix instructions, 24 for the scales: each of four warps reads them all),
-// 122 bytes a cycle, half of the banks' peak. Tiles of 256 x 192 move a fifth less from
+// stage's way through the ring; no unit is saturated. A 128 x 256 x 256 step takes
+// 515 ns, 270 of them matrix instructions (64 of k each; the 96-wide ones of sm_103a,
+// nominally half as fast again, are not used); it moves 55 KB into shared memory and reads 72 KB there (48 for
+// the matrix instructions, 24 for the scales: each of four warps reads them all), 122
+// bytes a cycle, half of the banks' peak. 47 bytes a cycle enter an SM from L2, 37 of 100
+// that its port takes (2,048 x 32,000 x 2,560: 13.7 TB/s over the GPU). Tiles of 256 x 192 move a fifth less from
 // L2, but have room for three stages: 583 against 594, each with one group of scale
 // warps (three slots do not go round between two).
 // What the choices measured there:

@@ -16,7 +16,7 @@
 // (2^19, 2^20] and logits below F count as F. A row whose maximum is not well
 // above F (filled with a type's lowest value, say), or is above -F (infinities
 // too), is summed again in the plain form 2^((z - m) c) with the subtraction
-// first (stat_plain), where any two finite values work; a row masked throughout
+// first (plain_slice), where any two finite values work; a row masked throughout
 // is told by its maximum, and not read again.
 // A NaN makes s a NaN, and so does +inf, as exp(z - max) does.
 #pragma once
