@@ -32,14 +32,12 @@ SIZES = {"one stage": (5, 64, 256), "two stages": (40, 320, 512), "a ring and mo
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("size", list(SIZES))
-@pytest.mark.parametrize("role", [PRODUCER, SCALES, ISSUER, EPILOGUE])
+@pytest.mark.parametrize("size, role", [(s, r) for s in SIZES for r in (PRODUCER, SCALES, ISSUER, EPILOGUE)
+                                        if r != EPILOGUE or "tiles" in s])   # (one tile per SM: nobody waits for the results)
 def test_an_idle_role_is_given_up_on(size, role):
     from nvfp4_draft_head_gb300 import build
     build.build()
     M, N, K = SIZES[size]
-    if role == EPILOGUE and "tiles" not in size:
-        pytest.skip("one tile per SM: nobody waits for the results")
     W = (torch.randn((N, K), generator=torch.Generator("cuda").manual_seed(1), device="cuda") * 0.02).bfloat16()
     mm = dh.NVFP4Matmul.from_weight(W)
     x = torch.randn((M, K), generator=torch.Generator("cuda").manual_seed(2), device="cuda").bfloat16()
