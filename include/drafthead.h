@@ -472,6 +472,69 @@ int draft_head_distill_backward(const dh_logits_t *lg, const int32_t *ids, const
                                 int K, const float *lse, const float *weight, void *dz, int64_t ld_dz,
                                 void *stream);
 
+/* Softmax cross entropy of T hidden states against the vocabulary given by N head
+ * rows, and its gradients, without logits in memory (the pages have no counterpart: it
+ * is how the BF16 rows of a draft head are trained on the tokens themselves, before
+ * they are quantised). With z = h_t . W_n and y_t the head row of tokens[t]:
+ *   lse_t  = log sum_n e^z_tn,  loss_t = w_t (lse_t - z_ty),
+ *   g_tn   = w_t (e^(z_tn - lse_t) - [n = y_t]),  dh = g W,  dW = g^T h.
+ * A token without a head row (row_of[token] < 0, an id outside [0, V), a row outside
+ * [0, N); ids such as -100) and a row of weight 0 is left out: its loss is 0, its dh
+ * zeros, and it adds nothing to dW, whatever its hidden state holds (it still has an
+ * lse). A hidden state with a value that is not finite makes its own loss, lse and dh
+ * NaN, and, where it is not left out, dW.
+ *   hidden  [T][K], row stride ld_hidden; head [N][K], row stride ld_head: both of
+ *           dh_type `type` (DH_T_BF16 or DH_T_F16), rows 16-byte aligned (strides
+ *           multiples of 8 elements; ignored for a single row). K % 8 == 0, K <= 2^20;
+ *           T, N <= 2^24.
+ *   tokens  int32 [T]; target ids with row_of (int32 [V], draft_head_row_map), head
+ *           rows with row_of NULL.
+ *   weight  fp32 [T], or NULL: 1. */
+typedef struct dh_cross_entropy {
+    const void *hidden;
+    const void *head;
+    int type;
+    int T;
+    int K;
+    int N;
+    int64_t ld_hidden;
+    int64_t ld_head;
+    const int32_t* tokens;
+    const float* weight;
+    const int32_t* row_of;
+    int V;
+} dh_cross_entropy_t;
+
+/* What a call computes, for its workspace. */
+#define DH_CE_LOSS 1u
+#define DH_CE_DHIDDEN 2u
+#define DH_CE_DHEAD 4u
+
+/* Bytes of workspace of a call with these outputs (0 for an unsupported shape): 8 bytes
+ * per token and 128 head rows for the loss; for the gradients g of a piece of the
+ * vocabulary in 16 bits (512 MiB at most while T <= 131,072) and, each where it is
+ * wanted, 32-bit sums of dh and a copy of the hidden states. */
+size_t draft_head_cross_entropy_workspace_bytes(int T, int N, int K, unsigned int outputs);
+
+/* The loss (fp32 [T]) and, where their pointers are not NULL, the normaliser lse (fp32
+ * [T]), what rounding it to fp32 left over, rest (fp32 [T]), dhidden ([T][K]) and dhead
+ * ([N][K]) of the inputs' type, rows 16-byte aligned; the gradients are those of the
+ * losses' sum. None of the outputs may overlap an input. ws: 256-byte aligned, no
+ * initialisation; calls that overlap on the GPU must not share one. error: as for
+ * nvfp4_matmul. Sums in 32 bits; g is rounded to 16 bits between its products (with a
+ * power of two taken out), the gradients once more. Repeatable bit for bit. Capturable
+ * in a CUDA graph. */
+int draft_head_cross_entropy(const dh_cross_entropy_t* c, float* loss, float* lse, float* rest, void* dhidden, int64_t ld_dhidden,
+                             void* dhead, int64_t ld_dhead, void* ws, size_t ws_bytes, unsigned int* error, void* stream);
+
+/* The gradients from the normaliser lse + rest (rest NULL: 0, which carries lse's
+ * rounding, 2^-24 |lse| relative), for a caller that learns the row weights after the
+ * loss (weight[t] = the upstream gradient of loss[t] times the forward's weight). One of
+ * dhidden and dhead may be NULL. */
+int draft_head_cross_entropy_backward(const dh_cross_entropy_t* c, const float* lse, const float* rest, void* dhidden,
+                                      int64_t ld_dhidden, void* dhead, int64_t ld_dhead, void* ws, size_t ws_bytes,
+                                      unsigned int* error, void* stream);
+
 /* Self-test of the failure handling of the draft-step kernels (the pages have
  * no counterpart): a one-thread kernel waits for an event that nothing
  * produces and gives up after `rounds` tries, recording DH_DEVERR_TIMEOUT in

@@ -22,6 +22,10 @@ Names follow the C ABI in include/drafthead.h:
   distill_topk             draft_head_distill: distillation loss and gradient
   (_forward, _backward)    the loss alone; the gradient from its normaliser
   DistillTopK              the same as a torch.autograd function
+  linear_cross_entropy     draft_head_cross_entropy: loss of the tokens under head rows
+                           and its gradients, without logits in memory
+  (_forward, _backward)    the loss alone; the gradients from its normaliser
+  LinearCrossEntropy       the same as a torch.autograd function
 A call given stream= works and allocates on that stream: its arguments have to be
 ready there, and its results are, for what follows on it.
 The vocabulary-sharded head (the local-argmax exchange) is in .sharded.
@@ -48,6 +52,7 @@ DH_DEVERR_UNFINISHED = 4
 DH_HEAD_IDX_ASCENDING = 1
 DH_T_BF16, DH_T_F16, DH_T_F32 = 1, 2, 3
 DH_MAX_TOP, DH_MAX_TEACHER = 128, 512
+DH_CE_LOSS, DH_CE_DHIDDEN, DH_CE_DHEAD = 1, 2, 4
 
 EXPORTS = (
     "draft_head_build_index", "draft_head_quantize_workspace_bytes", "nvfp4_quantize_rows",
@@ -58,7 +63,8 @@ EXPORTS = (
     "draft_head_wait_probe", "draft_head_top_tokens_host", "draft_head_top_keys", "draft_head_keys_to_ids",
     "draft_head_static_read_device_error", "draft_head_row_map", "draft_head_token_logprobs", "draft_head_distill",
     "draft_head_distill_backward", "nvfp4_matmul_packed_bytes", "nvfp4_pack_matmul", "nvfp4_matmul_workspace_bytes",
-    "nvfp4_matmul", "nvfp4_matmul_wait_probe",
+    "nvfp4_matmul", "nvfp4_matmul_wait_probe", "draft_head_cross_entropy_workspace_bytes", "draft_head_cross_entropy",
+    "draft_head_cross_entropy_backward",
 )
 
 _lib = None
@@ -94,6 +100,12 @@ assert struct.calcsize("@PiiiqfPiP") == C.sizeof(dh_logits_t)
 
 class dh_matmul_t(C.Structure):
     _fields_ = [("N", C.c_int), ("K", C.c_int), ("packed", C.c_void_p), ("scale", C.c_void_p)]
+
+
+class dh_cross_entropy_t(C.Structure):
+    _fields_ = [("hidden", C.c_void_p), ("head", C.c_void_p), ("type", C.c_int), ("T", C.c_int), ("K", C.c_int), ("N", C.c_int),
+                ("ld_hidden", C.c_int64), ("ld_head", C.c_int64), ("tokens", C.c_void_p), ("weight", C.c_void_p),
+                ("row_of", C.c_void_p), ("V", C.c_int)]
 
 
 def library_path() -> str:
@@ -146,6 +158,10 @@ def lib():
         L.nvfp4_matmul_workspace_bytes.restype = S
         L.nvfp4_matmul.argtypes = [C.POINTER(dh_matmul_t), P, I, C.c_int64, I, P, I, C.c_int64, P, S, P, P]
         L.nvfp4_matmul_wait_probe.argtypes = [C.POINTER(dh_matmul_t), P, I, P, P, S, I, C.c_uint, P, P]
+        L.draft_head_cross_entropy_workspace_bytes.argtypes = [I, I, I, C.c_uint]
+        L.draft_head_cross_entropy_workspace_bytes.restype = S
+        L.draft_head_cross_entropy.argtypes = [C.POINTER(dh_cross_entropy_t), P, P, P, P, C.c_int64, P, C.c_int64, P, S, P, P]
+        L.draft_head_cross_entropy_backward.argtypes = [C.POINTER(dh_cross_entropy_t), P, P, P, C.c_int64, P, C.c_int64, P, S, P, P]
         _lib = L
     return _lib
 
@@ -880,3 +896,142 @@ class DistillTopK(torch.autograd.Function):
             dz, dw = (None if d is None else _Refuse.apply("DistillTopK is differentiable once: its gradient has no derivative",
                                                            d, logits, dloss, weights) for d in (dz, dw))
         return dz, None, None, None, dw, None
+
+
+# ------------------------------------------- cross entropy against head rows --
+
+_error_words: dict = {}
+
+
+def _error_word(device) -> torch.Tensor | None:
+    """This device's error word of operators without a handle (none for a call that is
+    captured before the first eager one: the word has to outlive the graph's pool)."""
+    word = _error_words.get(device)
+    if word is None and not torch.cuda.is_current_stream_capturing():
+        word = _error_words.setdefault(device, torch.zeros(1, dtype=torch.int32, device=device))
+    return word
+
+
+def linear_cross_entropy_device_error(device=None) -> int:
+    """Read and clear the device error word of the linear_cross_entropy calls on `device`
+    (the current one), after waiting for the device: DH_DEVERR_TIMEOUT where a bounded
+    wait ran out, which makes results since the last reading invalid."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    torch.cuda.synchronize(device)
+    word = _error_words.get(device)
+    err = 0 if word is None else int(word.item())
+    if err:
+        word.zero_()
+    return err
+
+
+def _rows16(t: torch.Tensor, name: str, shape, like: torch.Tensor | None = None) -> int:
+    """The row stride of a matrix with 16-byte aligned rows, checked."""
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)) or t.stride(1) != 1 and t.shape[1] > 1 or \
+            (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name} must be a {'[T, K]' if shape is None else list(shape)} tensor with contiguous rows that do not overlap")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must be {like.dtype} on {like.device}, as the hidden states are")
+    if t.data_ptr() % 16 or (t.shape[0] > 1 and t.stride(0) % 8):
+        raise ValueError(f"{name}: rows must be 16-byte aligned (a row stride that is a multiple of 8 elements)")
+    return t.stride(0)
+
+
+def _cross_entropy(hidden, head, tokens, weights, row_of) -> dh_cross_entropy_t:
+    """The descriptor of a call on T >= 1 tokens, its tensors checked."""
+    if hidden.dtype not in (torch.bfloat16, torch.float16) or not hidden.is_cuda:
+        raise ValueError("hidden must be a [T, K] bfloat16 or float16 CUDA tensor")
+    ld_hidden = _rows16(hidden, "hidden", None)
+    T, K = hidden.shape
+    if head.dim() != 2 or head.shape[1] != K or head.shape[0] < 1:
+        raise ValueError(f"head must be a [N, {K}] tensor of at least one row")
+    ld_head = _rows16(head, "head", head.shape, hidden)
+    _vector(tokens, "tokens", torch.int32, T, hidden.device)
+    _vector(weights, "weights", torch.float32, T, hidden.device)
+    _vector(row_of, "row_of", torch.int32, None, hidden.device)
+    return dh_cross_entropy_t(hidden.data_ptr(), head.data_ptr(), _TYPES[hidden.dtype], T, K, head.shape[0], ld_hidden, ld_head,
+                              tokens.data_ptr(), _ptr(weights), _ptr(row_of), 0 if row_of is None else row_of.numel())
+
+
+def _gradient_rows(out: torch.Tensor | None, like: torch.Tensor, name: str) -> torch.Tensor:
+    if out is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    _rows16(out, name, like.shape, like)
+    return out
+
+
+def _cross_entropy_space(d: dh_cross_entropy_t, outputs: int, device) -> torch.Tensor:
+    nb = lib().draft_head_cross_entropy_workspace_bytes(d.T, d.N, d.K, outputs)
+    if nb == 0:
+        raise DraftHeadError("draft_head_cross_entropy_workspace_bytes", DH_ERR_SHAPE)
+    return torch.empty(nb, dtype=torch.uint8, device=device)
+
+
+def linear_cross_entropy(hidden: torch.Tensor, head: torch.Tensor, tokens: torch.Tensor, weights: torch.Tensor | None = None,
+                         row_of: torch.Tensor | None = None, dhidden: torch.Tensor | None = None, dhead: torch.Tensor | None = None,
+                         stream=None):
+    """(loss float32 [T], dhidden [T, K], dhead [N, K]): per-token softmax cross entropy of
+    hidden states [T, K] against the vocabulary of the head rows [N, K] (both bfloat16 or
+    both float16, rows 16-byte aligned), and the gradients of its sum, without logits in
+    memory. tokens: int32 [T], target ids with row_of (draft_head_row_map), head rows without
+    it; a token without a head row (-100, say) is left out, as a row of weight 0 is. weights:
+    float32 [T]. dhidden and dhead may be given tensors. The loss has no autograd graph (the
+    gradients are at hand; LinearCrossEntropy is the differentiable form). See
+    draft_head_cross_entropy."""
+    if stream is not None:
+        return _on_stream(stream, linear_cross_entropy, hidden, head, tokens, weights, row_of, dhidden, dhead)
+    d = _cross_entropy(hidden, head, tokens, weights, row_of)
+    dx, dw = _gradient_rows(dhidden, hidden, "dhidden"), _gradient_rows(dhead, head, "dhead")
+    loss = torch.empty(d.T, dtype=torch.float32, device=hidden.device)
+    if d.T == 0:
+        return loss, dx, dw.zero_()
+    s = _stream_of(hidden)
+    ws = _cross_entropy_space(d, DH_CE_LOSS | DH_CE_DHIDDEN | DH_CE_DHEAD, hidden.device)
+    _check("draft_head_cross_entropy",
+           lib().draft_head_cross_entropy(C.byref(d), loss.data_ptr(), None, None, dx.data_ptr(), dx.stride(0), dw.data_ptr(),
+                                          dw.stride(0), ws.data_ptr(), ws.numel(), _ptr(_error_word(hidden.device)), s))
+    return loss, dx, dw
+
+
+def linear_cross_entropy_forward(hidden: torch.Tensor, head: torch.Tensor, tokens: torch.Tensor, weights: torch.Tensor | None = None,
+                                 row_of: torch.Tensor | None = None, stream=None):
+    """(loss, lse, rest), all float32 [T]: the loss of linear_cross_entropy alone, the
+    normaliser for linear_cross_entropy_backward, and what rounding it left over."""
+    if stream is not None:
+        return _on_stream(stream, linear_cross_entropy_forward, hidden, head, tokens, weights, row_of)
+    d = _cross_entropy(hidden, head, tokens, weights, row_of)
+    loss, lse, rest = (torch.empty(d.T, dtype=torch.float32, device=hidden.device) for _ in range(3))
+    if d.T > 0:
+        s = _stream_of(hidden)
+        ws = _cross_entropy_space(d, DH_CE_LOSS, hidden.device)
+        _check("draft_head_cross_entropy",
+               lib().draft_head_cross_entropy(C.byref(d), loss.data_ptr(), lse.data_ptr(), rest.data_ptr(), None, 0, None, 0,
+                                              ws.data_ptr(), ws.numel(), _ptr(_error_word(hidden.device)), s))
+    return loss, lse, rest
+
+
+def linear_cross_entropy_backward(hidden: torch.Tensor, head: torch.Tensor, tokens: torch.Tensor, lse: torch.Tensor,
+                                  weights: torch.Tensor | None = None, rest: torch.Tensor | None = None,
+                                  row_of: torch.Tensor | None = None, dhidden=True, dhead=True, stream=None):
+    """(dhidden, dhead) from linear_cross_entropy_forward's lse (and rest, which is 0 if it is
+    not given); weights: float32 [T], the upstream gradient of each row's loss times the
+    forward's weight. dhidden and dhead: True, a tensor to write, or False for none (then
+    None is returned in its place; not both)."""
+    if stream is not None:
+        return _on_stream(stream, linear_cross_entropy_backward, hidden, head, tokens, lse, weights, rest, row_of, dhidden, dhead)
+    if dhidden is False and dhead is False:
+        raise ValueError("at least one of dhidden and dhead has to be wanted")
+    d = _cross_entropy(hidden, head, tokens, weights, row_of)
+    _vector(lse, "lse", torch.float32, d.T, hidden.device)
+    _vector(rest, "rest", torch.float32, d.T, hidden.device)
+    dx = None if dhidden is False else _gradient_rows(None if dhidden is True else dhidden, hidden, "dhidden")
+    dw = None if dhead is False else _gradient_rows(None if dhead is True else dhead, head, "dhead")
+    if d.T == 0:
+        return dx, None if dw is None else dw.zero_()
+    s = _stream_of(hidden)
+    ws = _cross_entropy_space(d, (DH_CE_DHIDDEN if dx is not None else 0) | (DH_CE_DHEAD if dw is not None else 0), hidden.device)
+    _check("draft_head_cross_entropy_backward",
+           lib().draft_head_cross_entropy_backward(C.byref(d), lse.data_ptr(), _ptr(rest), _ptr(dx), 0 if dx is None else dx.stride(0),
+                                                   _ptr(dw), 0 if dw is None else dw.stride(0), ws.data_ptr(), ws.numel(),
+                                                   _ptr(_error_word(hidden.device)), s))
+    return dx, dw

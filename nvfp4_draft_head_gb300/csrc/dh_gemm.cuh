@@ -1,0 +1,327 @@
+// The tensor-core product under the operators of many tokens with 16-bit and FP8 operands
+// (cross entropy, FP8 blocks): a persistent kernel whose operands come row-major from global
+// memory by tensor maps (TMA, 128-byte swizzle) and whose results each operator takes from
+// tensor memory in its own way (Op::tile).
+//
+// A tile is 128 P rows x TN columns, P the CTAs that share it. With a pair (P = 2) each CTA
+// loads its 128 rows of A and half of B: two thirds of the bytes that two single CTAs need
+// for the same 256 x TN, at 32 bytes of K per instruction. A stage is 128 bytes of K (64
+// 16-bit elements, 128 FP8). An operand is K-major (its rows run along the contraction) or
+// MN-major (its rows run along M or N, one row per step of the contraction): both gradients
+// of a layer then read the matrices as they lie, without transposed copies.
+//
+// Warps: eight epilogue warps (four groups of 32 lanes, two halves of the columns), a
+// producer thread, an issuer thread (rank 0's alone works). Every wait is bounded; who gives
+// up sets the CTA's abort flag and the caller's error word, and the others follow.
+#pragma once
+
+#include <atomic>
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "../../include/drafthead.h"
+#include "dh_internal.h"
+#include "dh_tcgen05.cuh"
+
+namespace dh {
+namespace gemm {
+
+constexpr int kRows = 128;            // rows of a CTA's part of a tile: the lanes of tensor memory
+constexpr int kStageBytes = 128;      // bytes of K in a stage
+constexpr int kEpiWarps = 8, kProducer = kEpiWarps, kIssuer = kProducer + 1;
+constexpr int kThreads = 32 * (kIssuer + 1);
+constexpr int kWaitSlices = 64;
+constexpr uint32_t kDrainRounds = kWaitLimit / kWaitSlices;
+
+__host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// What a launch multiplies: tiles, the steps of K, and where the operands start in their maps.
+struct Shape {
+    int tiles_m, tiles_n, splits;   // splits: parts of the contraction, each a tile of its own
+    int steps, split_steps;         // steps of K in all, and in a part (the last may have fewer)
+    int a_mn, a_k, b_mn, b_k;       // first row (M / N) and first element of K of each operand
+    unsigned int* error;            // DH_DEVERR_* word or null
+    uint32_t rounds;                // tries of a bounded wait, times kWaitSlices
+    int idle;                       // self-test: the role that does nothing (-1: none)
+};
+
+enum Role { kRoleProducer, kRoleIssuer, kRoleEpilogue };
+
+// Tiles that are in work at the same time share operands in L2: groups of kGroup rows of
+// tiles, columns along a group.
+constexpr int kGroup = 8;
+struct Tile { int m, n, split; };
+__device__ __forceinline__ Tile tile_at(const Shape& s, int i) {
+    const int per = s.tiles_m * s.tiles_n, split = i / per;
+    i -= split * per;
+    const int g = i / (kGroup * s.tiles_n), rows = min(kGroup, s.tiles_m - g * kGroup);
+    i -= g * kGroup * s.tiles_n;
+    return {g * kGroup + i % rows, i / rows, split};
+}
+__device__ __forceinline__ int steps_of(const Shape& s, int split) { return min(s.split_steps, s.steps - split * s.split_steps); }
+
+template <int P, int TN, int ELEM, bool A_MN, bool B_MN>
+struct Layout {
+    static constexpr int kP = P, kTN = TN, kElem = ELEM;
+    static constexpr bool kAMn = A_MN, kBMn = B_MN;
+    static constexpr int kK = kStageBytes / ELEM;                       // elements of K per stage
+    static constexpr int kSpan = 128 / ELEM;                            // elements of an MN-major box's rows
+    static constexpr int kBRows = TN / P;                               // columns of B that a CTA loads
+    static constexpr int kABytes = kRows * kStageBytes, kBBytes = kBRows * kStageBytes;
+    static constexpr int kBytes = kABytes + kBBytes;
+    static constexpr int kStages = (227 * 1024 - 1024 - 1024) / kBytes < 8 ? (227 * 1024 - 1024 - 1024) / kBytes : 8;
+    static constexpr int kSmem = kStages * kBytes + 1024;
+    static constexpr int kBuffers = 512 / TN < 4 ? 512 / TN : 4;        // accumulators in tensor memory
+    static_assert(!(A_MN && kRows % kSpan != 0) && !(B_MN && kBRows % kSpan != 0), "whole boxes");
+    static_assert(kBytes % 1024 == 0 && TN % 32 == 0 && kStages >= 3, "stage layout");
+};
+
+struct Sync {
+    uint64_t full[8], empty[8], acc_full[4], acc_empty[4], issued;
+    uint32_t tmem;
+    unsigned int abort;
+};
+
+// A bounded wait that gives up at once when another role of this CTA has.
+__device__ __forceinline__ bool wait_or_abort(Sync& sy, uint64_t* bar, uint32_t parity, const Shape& s) {
+    if (mbar_test(bar, parity)) return true;
+    for (int i = 0; i < kWaitSlices; ++i) {
+        if (mbar_wait(bar, parity, s.rounds)) return true;
+        if (*const_cast<volatile unsigned int*>(&sy.abort) != 0u) return false;
+    }
+    *const_cast<volatile unsigned int*>(&sy.abort) = 1u;
+    if (s.error != nullptr) atomicOr(s.error, kDevErrTimeout);
+    return false;
+}
+
+// A box of a tensor map into this CTA's shared memory, completing on `bar` (with a pair: a
+// shared::cluster address, rank 0's barrier).
+template <int P>
+__device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint64_t policy) {
+    if constexpr (P == 1)
+        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+                     " [%0], [%1, {%2, %3}], [%4], %5;"
+                     :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar), "l"(policy) : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
+                     " [%0], [%1, {%2, %3}], [%4], %5;"
+                     :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar), "l"(policy) : "memory");
+}
+
+__device__ __forceinline__ uint64_t policy_evict_last() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+// An operand's part of a stage: `rows` of M or N from `mn`, kK elements of K from `k`.
+template <class L, bool MN>
+__device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* map, int rows, int mn, int k, uint32_t bar,
+                                             uint64_t policy) {
+    if constexpr (!MN) {
+        tma_2d<L::kP>(dst, map, k, mn, bar, policy);
+    } else {
+        for (int i = 0; i < rows / L::kSpan; ++i)   // boxes of kSpan elements x kK rows
+            tma_2d<L::kP>(dst + i * L::kK * 128, map, mn + i * L::kSpan, k, bar, policy);
+    }
+}
+
+// The epilogue warps' turn through the accumulators.
+template <class L>
+struct Acc {
+    Sync& sy;
+    const Shape& shape;
+    uint32_t tmem, n = 0;
+    __device__ Acc(Sync& s, const Shape& sh, uint32_t t) : sy(s), shape(sh), tmem(t) {}
+    // Waits for the next accumulator: its first column, or ~0 if the wait gave up.
+    __device__ __forceinline__ uint32_t next() {
+        const uint32_t b = n % L::kBuffers;
+        const bool ok = wait_or_abort(sy, &sy.acc_full[b], (n / L::kBuffers) & 1, shape);
+        if (!__all_sync(0xFFFFFFFFu, ok)) return ~0u;
+        tc::fence_after_sync();
+        return tmem + b * L::kTN;
+    }
+    // This warp has read the accumulator (all of its loads waited for).
+    __device__ __forceinline__ void release() {
+        tc::fence_before_sync();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) {
+            uint64_t* bar = &sy.acc_empty[n % L::kBuffers];
+            if constexpr (L::kP == 1) mbar_arrive(bar);
+            else mbar_arrive_remote(cluster_map(bar, 0));
+        }
+        ++n;
+    }
+};
+
+// Op: Layout, Args (with `Shape shape`), kFormat (idesc_f), kPerStep (an accumulator per step of
+// K, for results that are scaled step by step; else one per tile), kAKeep / kBKeep (the operand is
+// read by other tiles too: kept in L2), and tile(args, tile, warp, lane, rank, acc), false when a
+// wait gave up.
+template <class Op>
+__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ CUtensorMap map_a,
+                                                              const __grid_constant__ CUtensorMap map_b,
+                                                              const __grid_constant__ typename Op::Args a) {
+    using L = typename Op::Layout;
+    constexpr int P = L::kP, kStages = L::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Sync sy;
+    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = P == 1 ? 0 : static_cast<int>(cluster_ctarank());
+    const Shape& s = a.shape;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sy.full[i], 1);
+            mbar_init(&sy.empty[i], 1);
+        }
+        for (int i = 0; i < L::kBuffers; ++i) {
+            mbar_init(&sy.acc_full[i], 1);
+            mbar_init(&sy.acc_empty[i], kEpiWarps * P);
+        }
+        mbar_init(&sy.issued, 1);
+        mbar_init_fence();
+        sy.abort = 0u;
+    }
+    __syncwarp();
+    if (warp == 0) tc::tmem_alloc_of<P>(&sy.tmem, 512);
+    tc::fence_before_sync();
+    __syncthreads();
+    if constexpr (P > 1) {   // the other CTA's barriers are ready too
+        cluster_fence();
+        cluster_sync_all();
+    }
+    tc::fence_after_sync();
+    const uint32_t tmem = sy.tmem;
+    const int tiles = s.tiles_m * s.tiles_n * s.splits;
+    const int first = static_cast<int>(blockIdx.x) / P, stride = static_cast<int>(gridDim.x) / P;
+
+    if (warp == kProducer && lane == 0 && s.idle != kRoleProducer) {
+        const uint64_t keep = policy_evict_last(), once = policy_evict_first();
+        const uint64_t pol_a = Op::kAKeep ? keep : once, pol_b = Op::kBKeep ? keep : once;
+        uint32_t it = 0, st = 0, phase = 1;
+        bool ok = true;
+        for (int i = first; ok && i < tiles; i += stride) {
+            const Tile t = tile_at(s, i);
+            const int am = s.a_mn + (t.m * P + rank) * kRows, bn = s.b_mn + t.n * L::kTN + rank * L::kBRows;
+            const int steps = steps_of(s, t.split), k0 = t.split * s.split_steps * L::kK;
+            for (int k = 0; k < steps; ++k, ++it) {
+                if (it >= static_cast<uint32_t>(kStages) && !(ok = wait_or_abort(sy, &sy.empty[st], phase, s))) break;
+                uint8_t* dst = smem + st * L::kBytes;
+                uint32_t bar;
+                if constexpr (P == 1) bar = smem_u32(&sy.full[st]);
+                else bar = cluster_map(&sy.full[st], 0);
+                if (rank == 0) mbar_arrive_expect_tx(&sy.full[st], P * L::kBytes);
+                load_operand<L, L::kAMn>(dst, &map_a, kRows, am, s.a_k + k0 + k * L::kK, bar, pol_a);
+                load_operand<L, L::kBMn>(dst + L::kABytes, &map_b, L::kBRows, bn, s.b_k + k0 + k * L::kK, bar, pol_b);
+                if (++st == static_cast<uint32_t>(kStages)) {
+                    st = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        // The copies in flight land before the CTAs end, whoever gave up: a pair's complete on
+        // rank 0's barriers; rank 1 waits for the last signals to its own (both bounded).
+        for (uint32_t b = it > static_cast<uint32_t>(kStages) ? it - kStages : 0; b < it; ++b)
+            if (!mbar_wait(rank == 0 ? &sy.full[b % kStages] : &sy.empty[b % kStages], (b / kStages) & 1, kDrainRounds)) break;
+    } else if (warp == kIssuer && lane == 0 && rank == 0 && s.idle != kRoleIssuer) {
+        constexpr uint32_t kIdesc = tc::idesc_f(Op::kFormat, L::kAMn, L::kBMn, kRows * P, L::kTN);
+        constexpr bool kF8 = L::kElem == 1;
+        // 32 bytes of K: along a 128-byte row, or (MN-major) as many whole rows as elements
+        constexpr uint32_t kStepA = L::kAMn ? 32 / L::kElem * 128 / 16 : 2, kStepB = L::kBMn ? 32 / L::kElem * 128 / 16 : 2;
+        uint32_t it = 0, n = 0, st = 0, phase = 0;
+        bool ok = true;
+        for (int i = first; ok && i < tiles; i += stride) {
+            const int steps = steps_of(s, tile_at(s, i).split);
+            for (int k = 0; k < steps; ++k, ++it) {
+                if (Op::kPerStep || k == 0) {
+                    const uint32_t use = n / L::kBuffers;
+                    if (use > 0 && !(ok = wait_or_abort(sy, &sy.acc_empty[n % L::kBuffers], (use - 1) & 1, s))) break;
+                }
+                if (!(ok = wait_or_abort(sy, &sy.full[st], phase, s))) break;
+                tc::fence_after_sync();
+                const uint32_t base = smem_u32(smem + st * L::kBytes);
+                const uint64_t da = L::kAMn ? tc::desc_operand_mn(base, L::kK) : tc::desc_operand(base);
+                const uint64_t db = L::kBMn ? tc::desc_operand_mn(base + L::kABytes, L::kK) : tc::desc_operand(base + L::kABytes);
+                const uint32_t d = tmem + (n % L::kBuffers) * L::kTN;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    tc::mma_f<P, kF8>(d, da + kStepA * j, db + kStepB * j, kIdesc, (!Op::kPerStep && k > 0) || j > 0);
+                tc::commit_all<P>(&sy.empty[st]);
+                if (Op::kPerStep || k == steps - 1) tc::commit_all<P>(&sy.acc_full[n++ % L::kBuffers]);
+                if (++st == static_cast<uint32_t>(kStages)) {
+                    st = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        // the issued instructions finish before tensor memory is freed, whoever gave up (bounded)
+        tc::commit_own<P>(&sy.issued);
+        mbar_wait(&sy.issued, 0, kDrainRounds);
+    } else if (warp < kEpiWarps && s.idle != kRoleEpilogue) {
+        Acc<L> acc(sy, s, tmem);
+        for (int i = first; i < tiles; i += stride)
+            if (!Op::tile(a, tile_at(s, i), warp, lane, rank, acc)) break;
+    }
+    __syncwarp();
+    tc::fence_before_sync();
+    __syncthreads();
+    if constexpr (P > 1) {   // neither CTA ends while the other still reads or signals it
+        cluster_fence();
+        cluster_sync_all();
+    }
+    tc::fence_after_sync();
+    if (warp == 0) tc::tmem_free_of<P>(tmem, 512);
+}
+
+// ------------------------------------------------------------------- host ----
+
+// A tensor map of a row-major matrix: `rows` rows of `cols` elements, `ld` bytes apart, read in
+// boxes of 128 bytes by box_rows with the 128-byte swizzle; what lies outside reads as zeros.
+// base and ld: multiples of 16 bytes.
+cudaError_t encode_map(CUtensorMap* map, const void* base, int elem, uint64_t cols, uint64_t rows, uint64_t ld, uint32_t box_rows);
+
+// The maps of an operand of `Layout` L: K-major, mn rows of k elements; MN-major, k rows of mn.
+template <class L, bool MN>
+cudaError_t encode_operand(CUtensorMap* map, const void* base, uint64_t mn, uint64_t k, uint64_t ld_bytes, int box_mn) {
+    return MN ? encode_map(map, base, L::kElem, mn, k, ld_bytes, L::kK) : encode_map(map, base, L::kElem, k, mn, ld_bytes, box_mn);
+}
+
+template <class Op>
+cudaError_t launch(const CUtensorMap& map_a, const CUtensorMap& map_b, typename Op::Args a, cudaStream_t stream) {
+    using L = typename Op::Layout;
+    const int sms = sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    constexpr int kDevices = 64;
+    static std::atomic<bool> known[kDevices];   // per device: the kernel's shared memory has been allowed
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= kDevices) return cudaErrorInvalidDevice;
+    if (!known[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(product_kernel<Op>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+        if (e != cudaSuccess) return e;
+        known[dev].store(true, std::memory_order_release);
+    }
+    if (a.shape.rounds == 0) {
+        a.shape.rounds = kWaitLimit / kWaitSlices;
+        a.shape.idle = -1;
+    }
+    const long long tiles = static_cast<long long>(a.shape.tiles_m) * a.shape.tiles_n * a.shape.splits;
+    const long long most = sms / L::kP;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((tiles < most ? tiles : most) * L::kP));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = L::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = L::kP;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = L::kP > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, product_kernel<Op>, map_a, map_b, a);
+}
+
+}  // namespace gemm
+}  // namespace dh

@@ -157,6 +157,33 @@ size_t matmul_workspace_bytes(int M, int K);
 cudaError_t launch_matmul_pack(const uint8_t* q, const uint8_t* sf, int N, int K, uint8_t* out, cudaStream_t s);
 cudaError_t launch_matmul(const MatmulArgs& m, cudaStream_t s);
 
+// Cross entropy against head rows, and its gradients (dh_cross_entropy.cu). The loss is wanted
+// where `loss` is set (lse_in and rest_in then unused), each gradient where its pointer is.
+struct CrossEntropyArgs {
+    const void* hidden;      // [T][K] of `type`
+    const void* head;        // [N][K]
+    int type;                // DH_T_BF16 or DH_T_F16
+    int T, N, K;
+    long long ld_hidden, ld_head;
+    const int32_t* tokens;   // [T]
+    const float* weight;     // [T] or null (1)
+    const int32_t* row_of;
+    int V;
+    float* loss;             // [T]
+    float* lse;              // [T] or null
+    float* rest;             // [T] or null
+    const float* lse_in;     // [T]
+    const float* rest_in;    // [T] or null (0)
+    void* dhidden;           // [T][K] or null
+    long long ld_dhidden;
+    void* dhead;             // [N][K] or null
+    long long ld_dhead;
+    void* ws;
+    unsigned int* error;
+};
+size_t cross_entropy_workspace_bytes(int T, int N, int K, bool loss, bool dhidden, bool dhead);
+cudaError_t launch_cross_entropy(const CrossEntropyArgs& a, cudaStream_t s);
+
 // row_of[idx[i]] = i for i < n, -1 elsewhere.
 cudaError_t launch_row_map(const int32_t* idx, int n, int32_t* row_of, int V, cudaStream_t s);
 
