@@ -472,6 +472,46 @@ int draft_head_distill_backward(const dh_logits_t *lg, const int32_t *ids, const
                                 int K, const float *lse, const float *weight, void *dz, int64_t ld_dz,
                                 void *stream);
 
+/* FP8 (E4M3) weight with one scale per block of 128 x 128, as FP8 checkpoints of MTP
+ * blocks hold their linears: w'[n][k] = scale[n / 128][k / 128] dec(q[n][k]). Any N;
+ * the last block of a side may be smaller. */
+typedef struct dh_fp8_blocks {
+    int N;               /* output features, 1 <= N <= 2^24 */
+    int K;               /* input features, K % 16 == 0 (<= 2^20) */
+    const void *q;       /* E4M3 codes [N][K] row-major, 16-byte aligned */
+    const float *scale;  /* fp32 [ceil(N / 128)][ceil(K / 128)] */
+} dh_fp8_blocks_t;
+
+/* Gather + quantisation of the rows W[idx[n], :] into such a weight: scale =
+ * max(amax of the block, 1e-12) / 448 in fp32, q = E4M3_RNE(clamp(w / scale, +-448)): the
+ * per-tensor FP8 recipe (fp8_quantize_rows) block by block. W, idx, ws as there, N as
+ * above; the error word of ws has to be zero, an id outside [0, V) leaves its row of q and
+ * sets DH_DEVERR_IDX. One kernel on `stream`. */
+int fp8_quantize_blocks(const void *W, int V, int K, const int32_t *idx, int N, uint8_t *q, float *scale, void *ws, size_t ws_bytes,
+                        void *stream);
+
+/* Bytes of workspace of the two products below for M tokens of `width` features (K for
+ * fp8_block_matmul, N for the gradient): the quantised activations (0 for an unsupported
+ * shape). */
+size_t fp8_block_matmul_workspace_bytes(int M, int width);
+
+/* y = x W'^T with the activations quantised per token and block of 128 features, inside
+ * the call, by the same recipe (IEEE divisions, fp32):
+ *   y[m, n] = sum_b sx[m, b] scale[n / 128, b] sum_(k in b) cx[m, k] dec(q[n, k]),
+ * products exact, sums in fp32, one rounding to y's type. A block of x with a value that is
+ * not finite makes its token's results NaN; tokens do not affect one another. x: [M][K] of
+ * dh_type x_type, row stride ldx elements; y: [M][N] of y_type, stride ldy (ignored when
+ * M == 1); both aligned to their element. 1 <= M <= 2^24. ws, error: as for nvfp4_matmul.
+ * Repeatable bit for bit. Capturable in a CUDA graph. */
+int fp8_block_matmul(const dh_fp8_blocks_t *w, const void *x, int x_type, int64_t ldx, int M, void *y, int y_type, int64_t ldy, void *ws,
+                     size_t ws_bytes, unsigned int *error, void *stream);
+
+/* The gradient of fp8_block_matmul in x, dx = dy W', with dy quantised per token and
+ * block of 128 of its features (as FP8 training does; the quantisation of x passes the
+ * gradient straight through): dy [M][N], dx [M][K]; everything else as above. */
+int fp8_block_matmul_input_gradient(const dh_fp8_blocks_t *w, const void *dy, int dy_type, int64_t lddy, int M, void *dx, int dx_type,
+                                    int64_t lddx, void *ws, size_t ws_bytes, unsigned int *error, void *stream);
+
 /* Softmax cross entropy of T hidden states against the vocabulary given by N head
  * rows, and its gradients, without logits in memory (the pages have no counterpart: it
  * is how the BF16 rows of a draft head are trained on the tokens themselves, before
@@ -499,9 +539,9 @@ typedef struct dh_cross_entropy {
     int N;
     int64_t ld_hidden;
     int64_t ld_head;
-    const int32_t* tokens;
-    const float* weight;
-    const int32_t* row_of;
+    const int32_t *tokens;
+    const float *weight;
+    const int32_t *row_of;
     int V;
 } dh_cross_entropy_t;
 
@@ -524,16 +564,16 @@ size_t draft_head_cross_entropy_workspace_bytes(int T, int N, int K, unsigned in
  * nvfp4_matmul. Sums in 32 bits; g is rounded to 16 bits between its products (with a
  * power of two taken out), the gradients once more. Repeatable bit for bit. Capturable
  * in a CUDA graph. */
-int draft_head_cross_entropy(const dh_cross_entropy_t* c, float* loss, float* lse, float* rest, void* dhidden, int64_t ld_dhidden,
-                             void* dhead, int64_t ld_dhead, void* ws, size_t ws_bytes, unsigned int* error, void* stream);
+int draft_head_cross_entropy(const dh_cross_entropy_t *c, float *loss, float *lse, float *rest, void *dhidden, int64_t ld_dhidden,
+                             void *dhead, int64_t ld_dhead, void *ws, size_t ws_bytes, unsigned int *error, void *stream);
 
 /* The gradients from the normaliser lse + rest (rest NULL: 0, which carries lse's
  * rounding, 2^-24 |lse| relative), for a caller that learns the row weights after the
  * loss (weight[t] = the upstream gradient of loss[t] times the forward's weight). One of
  * dhidden and dhead may be NULL. */
-int draft_head_cross_entropy_backward(const dh_cross_entropy_t* c, const float* lse, const float* rest, void* dhidden,
-                                      int64_t ld_dhidden, void* dhead, int64_t ld_dhead, void* ws, size_t ws_bytes,
-                                      unsigned int* error, void* stream);
+int draft_head_cross_entropy_backward(const dh_cross_entropy_t *c, const float *lse, const float *rest, void *dhidden,
+                                      int64_t ld_dhidden, void *dhead, int64_t ld_dhead, void *ws, size_t ws_bytes,
+                                      unsigned int *error, void *stream);
 
 /* Self-test of the failure handling of the draft-step kernels (the pages have
  * no counterpart): a one-thread kernel waits for an event that nothing

@@ -16,6 +16,10 @@ Names follow the C ABI in include/drafthead.h:
   keys_to_ids              draft_head_keys_to_ids: combined keys -> target ids
   NVFP4Matmul              nvfp4_matmul: y = x W'^T for many tokens, activations
                            quantised to NVFP4 per token (W4A4)
+  fp8_quantize_blocks      gather + FP8 E4M3 quantisation with a scale per 128 x 128
+  FP8BlockMatmul           fp8_block_matmul: y = x W'^T for such a weight, activations
+                           quantised per token and 128 features; .input_gradient: dx = dy W'
+  FP8BlockLinear           the same as a torch.autograd function
   draft_head_row_map       dh_idx -> column of every target id
   token_logprobs           draft_head_token_logprobs: log-probabilities of given
                            tokens, entropy, normaliser, top alternatives
@@ -64,7 +68,8 @@ EXPORTS = (
     "draft_head_static_read_device_error", "draft_head_row_map", "draft_head_token_logprobs", "draft_head_distill",
     "draft_head_distill_backward", "nvfp4_matmul_packed_bytes", "nvfp4_pack_matmul", "nvfp4_matmul_workspace_bytes",
     "nvfp4_matmul", "nvfp4_matmul_wait_probe", "draft_head_cross_entropy_workspace_bytes", "draft_head_cross_entropy",
-    "draft_head_cross_entropy_backward",
+    "draft_head_cross_entropy_backward", "fp8_quantize_blocks", "fp8_block_matmul_workspace_bytes", "fp8_block_matmul",
+    "fp8_block_matmul_input_gradient",
 )
 
 _lib = None
@@ -100,6 +105,10 @@ assert struct.calcsize("@PiiiqfPiP") == C.sizeof(dh_logits_t)
 
 class dh_matmul_t(C.Structure):
     _fields_ = [("N", C.c_int), ("K", C.c_int), ("packed", C.c_void_p), ("scale", C.c_void_p)]
+
+
+class dh_fp8_blocks_t(C.Structure):
+    _fields_ = [("N", C.c_int), ("K", C.c_int), ("q", C.c_void_p), ("scale", C.c_void_p)]
 
 
 class dh_cross_entropy_t(C.Structure):
@@ -162,6 +171,11 @@ def lib():
         L.draft_head_cross_entropy_workspace_bytes.restype = S
         L.draft_head_cross_entropy.argtypes = [C.POINTER(dh_cross_entropy_t), P, P, P, P, C.c_int64, P, C.c_int64, P, S, P, P]
         L.draft_head_cross_entropy_backward.argtypes = [C.POINTER(dh_cross_entropy_t), P, P, P, C.c_int64, P, C.c_int64, P, S, P, P]
+        L.fp8_quantize_blocks.argtypes = [P, I, I, P, I, P, P, P, S, P]
+        L.fp8_block_matmul_workspace_bytes.argtypes = [I, I]
+        L.fp8_block_matmul_workspace_bytes.restype = S
+        for fn in (L.fp8_block_matmul, L.fp8_block_matmul_input_gradient):
+            fn.argtypes = [C.POINTER(dh_fp8_blocks_t), P, I, C.c_int64, I, P, I, C.c_int64, P, S, P, P]
         _lib = L
     return _lib
 
@@ -674,6 +688,119 @@ class NVFP4Matmul:
         return err
 
 
+def fp8_quantize_blocks(W: torch.Tensor, idx: torch.Tensor | None = None, stream=None):
+    """(q uint8[N, K] E4M3 codes, scale float32[ceil(N / 128), ceil(K / 128)]) of the rows
+    W[idx] (all rows without idx) of a bfloat16 weight [V, K], one scale per block of 128 x
+    128; K % 16 == 0."""
+    if stream is not None:
+        return _on_stream(stream, fp8_quantize_blocks, W, idx)
+    if idx is None:
+        idx = torch.arange(W.shape[0], dtype=torch.int32, device=W.device)
+    V, K, N = _gather_args(W, idx)
+    s = _stream_of(W)
+    q = torch.zeros((N, K), dtype=torch.uint8, device=W.device)
+    scale = torch.empty((-(-N // 128), -(-K // 128)), dtype=torch.float32, device=W.device)
+    nb = lib().draft_head_quantize_workspace_bytes()
+    ws = _workspace(nb, W.device)
+    _check("fp8_quantize_blocks",
+           lib().fp8_quantize_blocks(W.data_ptr(), V, K, idx.data_ptr(), N, q.data_ptr(), scale.data_ptr(), ws.data_ptr(), nb, s))
+    _raise_device_error(ws, "fp8_quantize_blocks")
+    return q, scale
+
+
+class FP8BlockMatmul:
+    """An FP8 (E4M3) weight with one scale per block of 128 x 128, used in place: q uint8 (or
+    float8_e4m3fn) [N, K], scale float32 [ceil(N / 128), ceil(K / 128)], as from
+    fp8_quantize_blocks or an FP8 checkpoint (its weight_scale_inv); K % 16 == 0, any N.
+    forward(x) = x W'^T for any number of tokens, x quantised per token and 128 features
+    (W8A8), fp32 sums. An x that requires a gradient is refused: FP8BlockLinear is the
+    differentiable form."""
+
+    def __init__(self, q: torch.Tensor, scale: torch.Tensor, stream=None):
+        if stream is not None:
+            _on_stream(stream, self.__init__, q, scale)
+            return _keep_for(torch.cuda.current_stream(stream.device), self.error)
+        if q.dtype not in (torch.uint8, torch.float8_e4m3fn) or q.dim() != 2 or not q.is_cuda or not q.is_contiguous():
+            raise ValueError("q must be a contiguous [N, K] uint8 or float8_e4m3fn CUDA tensor")
+        self.N, self.K = q.shape
+        if self.N < 1 or self.K < 16 or self.K % 16:
+            raise DraftHeadError("fp8_block_matmul", DH_ERR_SHAPE)
+        if q.data_ptr() % 16:
+            raise DraftHeadError("fp8_block_matmul", DH_ERR_ALIGN)
+        if scale.shape != (-(-self.N // 128), -(-self.K // 128)):
+            raise ValueError(f"scale must be float32 [{-(-self.N // 128)}, {-(-self.K // 128)}]")
+        _vector(scale, "scale", torch.float32, None, q.device)
+        _stream_of(q)   # refuses another device than the current one
+        self.q, self.scale = q, scale
+        self.error = torch.zeros(1, dtype=torch.int32, device=q.device)
+        self.desc = dh_fp8_blocks_t(self.N, self.K, q.data_ptr(), scale.data_ptr())
+        self.desc_ref, self.error_ptr = C.byref(self.desc), self.error.data_ptr()
+
+    @classmethod
+    def from_weight(cls, W: torch.Tensor, idx: torch.Tensor | None = None, stream=None) -> "FP8BlockMatmul":
+        """Quantise the rows W[idx] (all rows without idx) of a bfloat16 weight [V, K]."""
+        if stream is not None:
+            new = _on_stream(stream, cls.from_weight, W, idx)
+            _keep_for(torch.cuda.current_stream(stream.device), new.q, new.scale, new.error)
+            return new
+        return cls(*fp8_quantize_blocks(W, idx))
+
+    def forward(self, x: torch.Tensor, y: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+                stream=None) -> torch.Tensor:
+        """y [M, N] (out_dtype: bfloat16, float16 or float32, or a given tensor's type) =
+        x W'^T for x [M, K] (bfloat16, float16 or float32, rows may be strided)."""
+        if stream is not None:
+            _keep_for(stream, self.q, self.scale, self.error)
+            return _on_stream(stream, self.forward, x, y, out_dtype)
+        _no_gradient(x, "the activations")
+        return self._product("fp8_block_matmul", x, y, out_dtype, self.K, self.N)
+
+    __call__ = forward
+
+    def input_gradient(self, dy: torch.Tensor, dx: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+                       stream=None) -> torch.Tensor:
+        """dx [M, K] = dy W' for dy [M, N], quantised per token and 128 of its features:
+        the gradient of forward in x. Types and strides as there."""
+        if stream is not None:
+            _keep_for(stream, self.q, self.scale, self.error)
+            return _on_stream(stream, self.input_gradient, dy, dx, out_dtype)
+        _no_gradient(dy, "the gradients")
+        return self._product("fp8_block_matmul_input_gradient", dy, dx, out_dtype, self.N, self.K)
+
+    def _product(self, name, x, y, out_dtype, width, out):
+        if x.dim() != 2 or x.shape[1] != width or x.dtype not in _TYPES or x.device != self.q.device or \
+                (x.stride(1) != 1 and width > 1) or (x.shape[0] > 1 and x.stride(0) < width):
+            raise ValueError(f"the input must be a [M, {width}] bfloat16, float16 or float32 tensor with contiguous rows on {self.q.device}")
+        M = x.shape[0]
+        if y is None:
+            if out_dtype not in _TYPES:
+                raise ValueError("out_dtype must be bfloat16, float16 or float32")
+            y = torch.empty((M, out), dtype=out_dtype, device=x.device)
+        elif y.shape != (M, out) or y.dtype not in _TYPES or y.device != x.device or (y.stride(1) != 1 and out > 1) or \
+                (M > 1 and y.stride(0) < out):
+            raise ValueError(f"the result must be a [{M}, {out}] bfloat16, float16 or float32 tensor with contiguous rows")
+        if M == 0:
+            return y
+        L = lib()
+        nb = L.fp8_block_matmul_workspace_bytes(M, width)
+        if nb == 0:
+            raise DraftHeadError(name, DH_ERR_SHAPE)
+        s = _stream_of(x)
+        ws = torch.empty(nb, dtype=torch.uint8, device=x.device)
+        _check(name, getattr(L, name)(self.desc_ref, x.data_ptr(), _TYPES[x.dtype], x.stride(0), M, y.data_ptr(), _TYPES[y.dtype],
+                                      y.stride(0), ws.data_ptr(), nb, self.error_ptr, s))
+        return y
+
+    def device_error(self) -> int:
+        """Read and clear the device error word (waits for the device: products may be
+        pending on any stream)."""
+        torch.cuda.synchronize(self.error.device)
+        err = int(self.error.item())
+        if err:
+            self.error.zero_()
+        return err
+
+
 def _logits_desc(logits: torch.Tensor, temperature: float, row_of: torch.Tensor | None,
                  idx: torch.Tensor | None = None) -> bytes:
     """The dh_logits_t of logits [M, C], as bytes."""
@@ -1035,3 +1162,57 @@ def linear_cross_entropy_backward(hidden: torch.Tensor, head: torch.Tensor, toke
                                                    _ptr(dw), 0 if dw is None else dw.stride(0), ws.data_ptr(), ws.numel(),
                                                    _ptr(_error_word(hidden.device)), s))
     return dx, dw
+
+
+class LinearCrossEntropy(torch.autograd.Function):
+    """loss [T] = LinearCrossEntropy.apply(hidden, head, tokens, weights, row_of);
+    differentiable once in the hidden states, the head and the weights (a weight's
+    derivative is the loss that its row has at weight 1). No logits are kept between the
+    passes: the backward pass multiplies them again from the normaliser."""
+
+    @staticmethod
+    def forward(ctx, hidden, head, tokens, weights=None, row_of=None):
+        loss, lse, rest = linear_cross_entropy_forward(hidden, head, tokens, weights, row_of)
+        ctx.save_for_backward(hidden, head, tokens, lse, rest, weights, row_of)
+        return loss
+
+    @staticmethod
+    def backward(ctx, dloss):
+        hidden, head, tokens, lse, rest, weights, row_of = ctx.saved_tensors
+        dx = dw = dweights = None
+        with torch.no_grad():
+            up = dloss.float()
+            if ctx.needs_input_grad[0] or ctx.needs_input_grad[1]:
+                w = (up if weights is None else up * weights).contiguous()
+                dx, dw = linear_cross_entropy_backward(hidden, head, tokens, lse, w, rest, row_of, dhidden=ctx.needs_input_grad[0],
+                                                       dhead=ctx.needs_input_grad[1])
+            if weights is not None and ctx.needs_input_grad[3]:
+                dweights = up * linear_cross_entropy_forward(hidden, head, tokens, None, row_of)[0]
+        if torch.is_grad_enabled():   # the caller asked for the gradients' graph
+            dx, dw, dweights = (None if d is None else
+                                _Refuse.apply("LinearCrossEntropy is differentiable once: its gradient has no derivative", d, hidden,
+                                              head, dloss, weights) for d in (dx, dw, dweights))
+        return dx, dw, None, dweights, None
+
+
+class FP8BlockLinear(torch.autograd.Function):
+    """y [M, N] = FP8BlockLinear.apply(x, matmul, out_dtype): matmul (an FP8BlockMatmul) as a
+    frozen layer, differentiable once in x: dx = matmul.input_gradient(dy), of x's type (the
+    rounding of x to FP8 passes the gradient straight through)."""
+
+    @staticmethod
+    def forward(ctx, x, matmul, out_dtype=torch.bfloat16):
+        ctx.matmul, ctx.dtype = matmul, x.dtype
+        ctx.save_for_backward(x)
+        return matmul(x.detach(), out_dtype=out_dtype)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, = ctx.saved_tensors
+        with torch.no_grad():
+            if dy.shape[0] > 1 and dy.stride(0) < dy.shape[1] or dy.stride(1) != 1:   # an expanded gradient
+                dy = dy.contiguous()
+            dx = ctx.matmul.input_gradient(dy, out_dtype=ctx.dtype)
+        if torch.is_grad_enabled():
+            dx = _Refuse.apply("FP8BlockLinear is differentiable once: its gradient has no derivative", dx, x, dy)
+        return dx, None, None

@@ -1,0 +1,278 @@
+// FP8 (E4M3) product with one scale per block of 128: y = x W'^T, and the gradient in its
+// input, dx = dy W'.
+//
+//   activations, per token and 128 features: s = max(amax, 1e-12) / 448,
+//     c = E4M3_RNE(clamp(x / s, +-448));  weights the same per 128 x 128 block;
+//   y_mn = sum_b sx_mb sw_(n/128)b sum_(k in b) cx_mk cw_nk,
+//   dx_mk = sum_b sdy_mb sw_b(k/128) sum_(n in b) cdy_mn cw_nk.
+// The inner sums run on the tensor cores (kind::f8f6f4, exact products, 32-bit accumulators);
+// 128 is one stage of K (dh_gemm.cuh), so each step leaves an accumulator of its own, which the
+// epilogue multiplies by the two scales and adds to 32-bit sums in registers.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "dh_gemm.cuh"
+#include "dh_rows.cuh"
+
+namespace dh {
+namespace f8 {
+
+using gemm::Acc;
+using gemm::ceil_div;
+using gemm::Tile;
+
+constexpr int kBlock = 128;   // elements of a scale
+
+// ------------------------------------------------------------ quantisation ----
+
+// Codes and scales of rows x [M][width]: eight lanes per block of 128, 16 elements each.
+// codes [M][ldc] (ldc = width rounded up to 16, zeros beyond width), scales [blocks][M]. A block
+// with a value that is not finite gets the scale NaN: its token's results are NaN.
+constexpr int kQThreads = 256;
+template <class T, bool VEC>
+__global__ void __launch_bounds__(kQThreads) quantize_kernel(const T* __restrict__ x, long long ldx, int M, int width,
+                                                             uint8_t* __restrict__ codes, int ldc, float* __restrict__ scales) {
+    const unsigned per_row = static_cast<unsigned>(ceil_div(width, kBlock));
+    const unsigned unit = blockIdx.x * (kQThreads / 8) + (threadIdx.x >> 3);   // < 2^31 (checked)
+    const unsigned m = unit / per_row, b = unit - m * per_row;
+    const bool in = m < static_cast<unsigned>(M);
+    const int k = static_cast<int>(b) * kBlock + (threadIdx.x & 7) * 16;
+    const int n = in ? min(16, width - k) : 0;
+    float v[16];
+    const T* src = x + static_cast<size_t>(m) * ldx + k;
+    if (n == 16) {
+        rows::load16<T, VEC>(src, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = i < n ? rows::Elem<T>::load(src + i) : 0.0f;
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    const bool finite = top < 0x7F800000u;
+    const float s = finite ? act_fp8_scale(__uint_as_float(top)) : __uint_as_float(0x7FC00000u);
+    if (in && (threadIdx.x & 7) == 0) scales[static_cast<size_t>(b) * M + m] = s;
+    if (n <= 0) return;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float q[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = fminf(fmaxf(__fdiv_rn(v[4 * i + j], s), -448.0f), 448.0f);
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q[2], q[3]), __NV_SATFINITE, __NV_E4M3);
+        w[i] = lo | (hi << 16);
+    }
+    *reinterpret_cast<uint4*>(codes + static_cast<size_t>(m) * ldc + k) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A weight's blocks: one CTA per 128 x 128, its 16,384 values in registers between the maximum
+// and the codes. Rows W[idx[n]]; an id outside [0, V) leaves its row and sets the error word.
+constexpr int kWThreads = 256;
+__global__ void __launch_bounds__(kWThreads) blocks_kernel(const uint16_t* __restrict__ W, int V, int K, const int32_t* __restrict__ idx,
+                                                           int N, uint8_t* __restrict__ q, float* __restrict__ scale, Workspace* ws) {
+    const int nb = blockIdx.x, kb = blockIdx.y, piece = threadIdx.x & 15, k = kb * kBlock + piece * 8;   // 8 values of a row
+    uint4 v[8];
+    uint32_t there = 0;
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int n = nb * kBlock + i * 16 + (threadIdx.x >> 4);
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (n >= N || k >= K) continue;
+        const int id = idx[n];
+        if (id < 0 || id >= V) {
+            atomicOr(&ws->error, kDevErrIdx);
+            continue;
+        }
+        there |= 1u << i;
+        v[i] = *reinterpret_cast<const uint4*>(W + static_cast<size_t>(id) * K + k);
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[j])), fabsf(bf16_hi(w[j]))));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    __shared__ float s_top[kWThreads / 32];
+    if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = top;
+    __syncthreads();
+    top = s_top[0];
+#pragma unroll
+    for (int i = 1; i < kWThreads / 32; ++i) top = fmaxf(top, s_top[i]);
+    const float s = act_fp8_scale(top);
+    if (threadIdx.x == 0) scale[static_cast<size_t>(nb) * gridDim.y + kb] = s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (!(there >> i & 1u)) continue;
+        const int n = nb * kBlock + i * 16 + (threadIdx.x >> 4);
+        *reinterpret_cast<uint2*>(q + static_cast<size_t>(n) * K + k) =
+            make_uint2(act_fp8_pair(v[i].x, s) | (act_fp8_pair(v[i].y, s) << 16), act_fp8_pair(v[i].z, s) | (act_fp8_pair(v[i].w, s) << 16));
+    }
+}
+
+// ----------------------------------------------------------------- product ----
+
+// 32 bytes, 32-byte aligned, in one store.
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+    asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 :: "l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+}
+
+// 32 results of a row at `out`, `valid` of them wanted.
+template <class TY, bool VEC>
+__device__ __forceinline__ void store_row(TY* out, const float* v, int valid) {
+    constexpr int kPer = 32 / sizeof(TY);   // results in 32 bytes
+#pragma unroll
+    for (int i = 0; i < 32; i += kPer) {
+        if (VEC && valid >= i + kPer) {
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if constexpr (sizeof(TY) == 2) w[j] = rows::Elem<TY>::pack2(v[i + 2 * j], v[i + 2 * j + 1]);
+                else w[j] = __float_as_uint(v[i + j]);
+            }
+            store32(out + i, w);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j)
+                if (i + j < valid) out[i + j] = rows::Elem<TY>::store(v[i + j]);
+        }
+    }
+}
+
+// Tokens along the rows of a tile, output features along its columns; W K-major for y, and
+// MN-major (its rows along the contraction) for dx.
+template <class TY, bool GRADIENT>
+struct Product {
+    using Layout = gemm::Layout<2, 256, 1, false, GRADIENT>;
+    static constexpr int kFormat = 0;
+    static constexpr bool kPerStep = true, kAKeep = true, kBKeep = true;
+    struct Args {
+        gemm::Shape shape;
+        const float* sx;      // [steps][M]
+        const float* sw;      // scale of output block j and step b at j * sw_j + b * sw_b
+        int sw_j, sw_b;
+        int M, N;             // tokens, output features
+        TY* y;
+        long long ldy;
+        int vec;              // rows 32-byte aligned
+    };
+    __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int rank, Acc<Layout>& acc) {
+        constexpr int kHalf = Layout::kTN / 2;
+        static_assert(kHalf == kBlock, "one weight scale per step and warp");
+        const int row = (t.m * Layout::kP + rank) * gemm::kRows + (warp & 3) * 32 + lane, half = warp >> 2;
+        const int n0 = t.n * Layout::kTN + half * kHalf, steps = a.shape.steps;
+        const bool in = row < a.M;
+        // (columns beyond N: any scale)
+        const float* sw = a.sw + static_cast<size_t>(n0 < a.N ? n0 / kBlock : 0) * a.sw_j;
+        const float* sx = a.sx + (in ? row : 0);
+        float sum[kHalf];
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i) sum[i] = 0.0f;
+        float next_x = __ldg(sx), next_w = __ldg(sw);
+#pragma unroll 1
+        for (int b = 0; b < steps; ++b) {
+            const float s = next_x * next_w;
+            if (b + 1 < steps) {
+                next_x = __ldg(sx + static_cast<size_t>(b + 1) * a.M);
+                next_w = __ldg(sw + static_cast<size_t>(b + 1) * a.sw_b);
+            }
+            const uint32_t at = acc.next();
+            if (at == ~0u) return false;
+            const uint32_t from = at + (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf;
+#pragma unroll
+            for (int c = 0; c < kHalf; c += 16) {
+                uint32_t r[16];
+                tc::tmem_load16(from + c, r);
+                tc::tmem_load_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sum[c + i] = fmaf(s, __uint_as_float(r[i]), sum[c + i]);
+            }
+            acc.release();
+        }
+        if (in && n0 < a.N) {
+            TY* out = a.y + static_cast<size_t>(row) * a.ldy + n0;
+#pragma unroll
+            for (int c = 0; c < kHalf; c += 32) {
+                if (a.vec) store_row<TY, true>(out + c, sum + c, a.N - n0 - c);
+                else store_row<TY, false>(out + c, sum + c, a.N - n0 - c);
+            }
+        }
+        __syncwarp();
+        return true;
+    }
+};
+
+// ------------------------------------------------------------------- host ----
+
+template <class T>
+cudaError_t quantize(const Fp8BlockArgs& f, int width, uint8_t* codes, int ldc, float* scales, cudaStream_t s) {
+    const bool vec = (reinterpret_cast<uintptr_t>(f.x) & 15u) == 0 && (f.M == 1 || (f.ldx * static_cast<long long>(sizeof(T))) % 16 == 0);
+    const unsigned units = static_cast<unsigned>(f.M) * static_cast<unsigned>(ceil_div(width, kBlock));
+    const unsigned grid = (units + kQThreads / 8 - 1) / (kQThreads / 8);
+    if (vec) quantize_kernel<T, true><<<grid, kQThreads, 0, s>>>(static_cast<const T*>(f.x), f.ldx, f.M, width, codes, ldc, scales);
+    else quantize_kernel<T, false><<<grid, kQThreads, 0, s>>>(static_cast<const T*>(f.x), f.ldx, f.M, width, codes, ldc, scales);
+    return cudaGetLastError();
+}
+
+template <class TY, bool GRADIENT>
+cudaError_t product(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, const float* scales, cudaStream_t s) {
+    using P = Product<TY, GRADIENT>;
+    using L = typename P::Layout;
+    const int width = GRADIENT ? f.N : f.K, out = GRADIENT ? f.K : f.N, kb = ceil_div(f.K, kBlock);
+    CUtensorMap map_a, map_b;
+    cudaError_t e = gemm::encode_operand<L, false>(&map_a, codes, f.M, width, ldc, gemm::kRows);
+    if (e != cudaSuccess) return e;
+    if ((e = gemm::encode_operand<L, GRADIENT>(&map_b, f.q, out, width, f.K, L::kBRows)) != cudaSuccess) return e;
+    typename P::Args a = {};
+    const int steps = ceil_div(width, kBlock);
+    a.shape = {ceil_div(f.M, 256), ceil_div(out, L::kTN), 1, steps, steps, 0, 0, 0, 0, f.error, 0, 0};
+    a.sx = scales;
+    a.sw = f.scale;
+    a.sw_j = GRADIENT ? 1 : kb;
+    a.sw_b = GRADIENT ? kb : 1;
+    a.M = f.M;
+    a.N = out;
+    a.y = static_cast<TY*>(f.y);
+    a.ldy = f.ldy;
+    a.vec = (reinterpret_cast<uintptr_t>(f.y) & 31u) == 0 && (f.M == 1 || (f.ldy * static_cast<long long>(sizeof(TY))) % 32 == 0);
+    return gemm::launch<P>(map_a, map_b, a, s);
+}
+
+template <class TY>
+cudaError_t run(const Fp8BlockArgs& f, cudaStream_t s) {
+    const int width = f.gradient ? f.N : f.K, ldc = ceil_div(width, 16) * 16;
+    uint8_t* codes = static_cast<uint8_t*>(f.ws);
+    float* scales = reinterpret_cast<float*>(codes + (static_cast<size_t>(f.M) * ldc + 255) / 256 * 256);
+    cudaError_t e = f.x_type == DH_T_BF16  ? quantize<__nv_bfloat16>(f, width, codes, ldc, scales, s)
+                    : f.x_type == DH_T_F16 ? quantize<__half>(f, width, codes, ldc, scales, s)
+                                           : quantize<float>(f, width, codes, ldc, scales, s);
+    if (e != cudaSuccess) return e;
+    return f.gradient ? product<TY, true>(f, codes, ldc, scales, s) : product<TY, false>(f, codes, ldc, scales, s);
+}
+
+}  // namespace f8
+
+size_t fp8_block_workspace_bytes(int M, int width) {
+    const size_t codes = (static_cast<size_t>(M) * (f8::ceil_div(width, 16) * 16) + 255) / 256 * 256;
+    return codes + (static_cast<size_t>(M) * f8::ceil_div(width, f8::kBlock) * sizeof(float) + 255) / 256 * 256;
+}
+
+cudaError_t launch_fp8_quantize_blocks(const uint16_t* W, int V, int K, const int32_t* idx, int N, uint8_t* q, float* scale, Workspace* ws,
+                                       cudaStream_t s) {
+    const dim3 grid(static_cast<unsigned>(f8::ceil_div(N, f8::kBlock)), static_cast<unsigned>(f8::ceil_div(K, f8::kBlock)));
+    f8::blocks_kernel<<<grid, f8::kWThreads, 0, s>>>(W, V, K, idx, N, q, scale, ws);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_fp8_blocks(const Fp8BlockArgs& f, cudaStream_t s) {
+    switch (f.y_type) {
+        case DH_T_BF16: return f8::run<__nv_bfloat16>(f, s);
+        case DH_T_F16: return f8::run<__half>(f, s);
+        default: return f8::run<float>(f, s);
+    }
+}
+
+}  // namespace dh

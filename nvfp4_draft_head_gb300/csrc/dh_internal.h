@@ -184,6 +184,27 @@ struct CrossEntropyArgs {
 size_t cross_entropy_workspace_bytes(int T, int N, int K, bool loss, bool dhidden, bool dhead);
 cudaError_t launch_cross_entropy(const CrossEntropyArgs& a, cudaStream_t s);
 
+// FP8 product with a scale per block of 128 (dh_fp8_blocks.cu): y = x W'^T, or (gradient) with
+// x [M][N], y [M][K]: y = x W'.
+struct Fp8BlockArgs {
+    const uint8_t* q;        // [N][K] codes
+    const float* scale;      // [ceil(N / 128)][ceil(K / 128)]
+    int N, K, M;
+    int gradient;
+    const void* x;
+    int x_type;
+    long long ldx;
+    void* y;
+    int y_type;
+    long long ldy;
+    void* ws;
+    unsigned int* error;     // device error word or null
+};
+size_t fp8_block_workspace_bytes(int M, int width);
+cudaError_t launch_fp8_quantize_blocks(const uint16_t* W, int V, int K, const int32_t* idx, int N, uint8_t* q, float* scale, Workspace* ws,
+                                       cudaStream_t s);
+cudaError_t launch_fp8_blocks(const Fp8BlockArgs& f, cudaStream_t s);
+
 // row_of[idx[i]] = i for i < n, -1 elsewhere.
 cudaError_t launch_row_map(const int32_t* idx, int n, int32_t* row_of, int V, cudaStream_t s);
 

@@ -119,20 +119,6 @@ __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
     return r;
 }
 
-// 16 elements at p (alignment of the element type only when !VEC), as floats.
-template <class T, bool VEC>
-__device__ __forceinline__ void load16(const T* p, float (&x)[16]) {
-    if constexpr (VEC) {
-        constexpr int kVec = rows::Elem<T>::kVec;
-#pragma unroll
-        for (int i = 0; i < 16 / kVec; ++i)
-            rows::Elem<T>::unpack(*reinterpret_cast<const uint4*>(p + i * kVec), reinterpret_cast<float(&)[kVec]>(x[i * kVec]));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = rows::Elem<T>::load(p + i);
-    }
-}
-
 // One CTA per token: the row's largest magnitude (as bits, so that NaN and
 // infinities come out on top), then codes and scales, one 32-wide piece per thread.
 // A row with a value that is not finite gets the scale NaN and zero codes:
@@ -147,7 +133,7 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const T* __restrict
     uint32_t top = 0;
     for (int b = threadIdx.x; b < nb; b += kQThreads) {
         float v[16];
-        load16<T, VEC>(row + b * 16, v);
+        rows::load16<T, VEC>(row + b * 16, v);
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
     }
@@ -169,7 +155,7 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const T* __restrict
             const int b = piece * 2 + h;
             if (b >= nb || !finite) continue;
             float v[16];
-            load16<T, VEC>(row + b * 16, v);
+            rows::load16<T, VEC>(row + b * 16, v);
             float bmax = 0.0f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) bmax = fmaxf(bmax, fabsf(v[i]));

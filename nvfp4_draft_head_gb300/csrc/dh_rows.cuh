@@ -157,6 +157,20 @@ template <> struct Elem<float> {
     __device__ static float store(float x) { return x; }
 };
 
+// 16 elements at p (alignment of the element type only when !VEC), as floats.
+template <class T, bool VEC>
+__device__ __forceinline__ void load16(const T* p, float (&x)[16]) {
+    if constexpr (VEC) {
+        constexpr int kVec = Elem<T>::kVec;
+#pragma unroll
+        for (int i = 0; i < 16 / kVec; ++i)
+            Elem<T>::unpack(*reinterpret_cast<const uint4*>(p + i * kVec), reinterpret_cast<float(&)[kVec]>(x[i * kVec]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = Elem<T>::load(p + i);
+    }
+}
+
 // 16 bytes whose elements are all -inf (what a lane past the slice holds).
 template <class T> __device__ __forceinline__ uint4 neg_inf_vec();
 template <> __device__ __forceinline__ uint4 neg_inf_vec<float>() {
