@@ -120,13 +120,13 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* w) {
                  :: "l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
 }
 
-// 32 results of a row at `out`, `valid` of them wanted.
-template <class TY, bool VEC>
+// 32 results of a row at `out`, 32-byte aligned, `valid` of them wanted.
+template <class TY>
 __device__ __forceinline__ void store_row(TY* out, const float* v, int valid) {
     constexpr int kPer = 32 / sizeof(TY);   // results in 32 bytes
 #pragma unroll
     for (int i = 0; i < 32; i += kPer) {
-        if (VEC && valid >= i + kPer) {
+        if (valid >= i + kPer) {
             uint32_t w[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -142,11 +142,27 @@ __device__ __forceinline__ void store_row(TY* out, const float* v, int valid) {
     }
 }
 
+// A warp's 32 x 32 values, lane r's v[c] to lane c's v[r]: five exchanges between lanes (and
+// values) that differ in one bit.
+__device__ __forceinline__ void transpose32(float* v, int lane) {
+#pragma unroll
+    for (int b = 16; b > 0; b >>= 1) {
+        const bool up = (lane & b) != 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            if (i & b) continue;
+            const float other = __shfl_xor_sync(0xFFFFFFFFu, up ? v[i] : v[i | b], b);
+            if (up) v[i] = other;
+            else v[i | b] = other;
+        }
+    }
+}
+
 // Tokens along the rows of a tile, output features along its columns; W K-major for y, and
 // MN-major (its rows along the contraction) for dx.
 template <class TY, bool GRADIENT>
 struct Product {
-    using Layout = gemm::Layout<2, 256, 1, false, GRADIENT>;
+    using Layout = gemm::Layout<2, 256, 1, false, GRADIENT, 16, 2>;
     static constexpr int kFormat = 0;
     static constexpr bool kPerStep = true, kAKeep = true, kBKeep = true;
     struct Args {
@@ -160,30 +176,35 @@ struct Product {
         int vec;              // rows 32-byte aligned
     };
     __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int rank, Acc<Layout>& acc) {
-        constexpr int kHalf = Layout::kTN / 2;
-        static_assert(kHalf == kBlock, "one weight scale per step and warp");
-        const int row = (t.m * Layout::kP + rank) * gemm::kRows + (warp & 3) * 32 + lane, half = warp >> 2;
-        const int n0 = t.n * Layout::kTN + half * kHalf, steps = a.shape.steps;
+        constexpr int kPart = Layout::kPart;
+        static_assert(kPart == 64 && Layout::kTN == 2 * kBlock && Layout::kP == 2, "a warp's columns lie in one block of the weight");
+        // A group's accumulator: its first half from rank 0's rows of B (block 0 of the tile's
+        // two), the second from rank 1's (block 1).
+        const int row0 = (t.m * Layout::kP + rank) * gemm::kRows + (warp & 3) * 32, row = row0 + lane;
+        const int group = warp / Layout::kSet, block = warp / 4 % 2, steps = a.shape.steps;
+        const int n0 = t.n * Layout::kTN + block * kBlock + group * kPart;
         const bool in = row < a.M;
         // (columns beyond N: any scale)
         const float* sw = a.sw + static_cast<size_t>(n0 < a.N ? n0 / kBlock : 0) * a.sw_j;
         const float* sx = a.sx + (in ? row : 0);
-        float sum[kHalf];
+        float sum[kPart];
 #pragma unroll
-        for (int i = 0; i < kHalf; ++i) sum[i] = 0.0f;
-        float next_x = __ldg(sx), next_w = __ldg(sw);
+        for (int i = 0; i < kPart; ++i) sum[i] = 0.0f;
+        const auto scale_at = [&](int b) {
+            b = b < steps ? b : steps - 1;
+            return make_float2(__ldg(sx + static_cast<size_t>(b) * a.M), __ldg(sw + static_cast<size_t>(b) * a.sw_b));
+        };
+        float2 s1 = scale_at(0), s2 = scale_at(1);   // two steps ahead: a load takes longer than a step
 #pragma unroll 1
         for (int b = 0; b < steps; ++b) {
-            const float s = next_x * next_w;
-            if (b + 1 < steps) {
-                next_x = __ldg(sx + static_cast<size_t>(b + 1) * a.M);
-                next_w = __ldg(sw + static_cast<size_t>(b + 1) * a.sw_b);
-            }
+            const float s = s1.x * s1.y;
+            s1 = s2;
+            s2 = scale_at(b + 2);
             const uint32_t at = acc.next();
             if (at == ~0u) return false;
-            const uint32_t from = at + (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf;
+            const uint32_t from = at + (static_cast<uint32_t>(warp & 3) << 21) + block * kPart;
 #pragma unroll
-            for (int c = 0; c < kHalf; c += 16) {
+            for (int c = 0; c < kPart; c += 16) {
                 uint32_t r[16];
                 tc::tmem_load16(from + c, r);
                 tc::tmem_load_wait();
@@ -192,12 +213,21 @@ struct Product {
             }
             acc.release();
         }
-        if (in && n0 < a.N) {
-            TY* out = a.y + static_cast<size_t>(row) * a.ldy + n0;
+        if (a.vec) {
+            if (in && n0 < a.N) {
+                TY* out = a.y + static_cast<size_t>(row) * a.ldy + n0;
 #pragma unroll
-            for (int c = 0; c < kHalf; c += 32) {
-                if (a.vec) store_row<TY, true>(out + c, sum + c, a.N - n0 - c);
-                else store_row<TY, false>(out + c, sum + c, a.N - n0 - c);
+                for (int c = 0; c < kPart; c += 32) store_row<TY>(out + c, sum + c, a.N - n0 - c);
+            }
+        } else {   // rows at any address: lanes along the columns
+#pragma unroll
+            for (int c = 0; c < kPart; c += 32) {
+                transpose32(sum + c, lane);
+                const int col = n0 + c + lane, left = col < a.N ? a.M - row0 : 0;
+                TY* out = a.y + static_cast<size_t>(row0) * a.ldy + col;
+#pragma unroll
+                for (int i = 0; i < 32; ++i, out += a.ldy)
+                    if (i < left) *out = rows::Elem<TY>::store(sum[c + i]);
             }
         }
         __syncwarp();

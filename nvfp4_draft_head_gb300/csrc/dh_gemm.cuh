@@ -10,7 +10,7 @@
 // MN-major (its rows run along M or N, one row per step of the contraction): both gradients
 // of a layer then read the matrices as they lie, without transposed copies.
 //
-// Warps: eight epilogue warps (four groups of 32 lanes, two halves of the columns), a
+// Warps: eight or sixteen epilogue warps (four groups of 32 lanes, parts of the columns), a
 // producer thread, an issuer thread (rank 0's alone works). Every wait is bounded; who gives
 // up sets the CTA's abort flag and the caller's error word, and the others follow.
 #pragma once
@@ -28,8 +28,6 @@ namespace gemm {
 
 constexpr int kRows = 128;            // rows of a CTA's part of a tile: the lanes of tensor memory
 constexpr int kStageBytes = 128;      // bytes of K in a stage
-constexpr int kEpiWarps = 8, kProducer = kEpiWarps, kIssuer = kProducer + 1;
-constexpr int kThreads = 32 * (kIssuer + 1);
 constexpr int kWaitSlices = 64;
 constexpr uint32_t kDrainRounds = kWaitLimit / kWaitSlices;
 
@@ -60,9 +58,13 @@ __device__ __forceinline__ Tile tile_at(const Shape& s, int i) {
 }
 __device__ __forceinline__ int steps_of(const Shape& s, int split) { return min(s.split_steps, s.steps - split * s.split_steps); }
 
-template <int P, int TN, int ELEM, bool A_MN, bool B_MN>
+template <int P, int TN, int ELEM, bool A_MN, bool B_MN, int EPI = 8, int GROUPS = 1>
 struct Layout {
     static constexpr int kP = P, kTN = TN, kElem = ELEM;
+    static constexpr int kEpiWarps = EPI, kProducer = EPI, kIssuer = EPI + 1, kThreads = 32 * (EPI + 2);
+    static constexpr int kGroups = GROUPS, kGN = TN / GROUPS;           // a tile's columns as accumulators of their own
+    static constexpr int kSet = EPI / GROUPS;                           // epilogue warps of a group
+    static constexpr int kPart = kGN / (kSet / 4);                      // columns of one
     static constexpr bool kAMn = A_MN, kBMn = B_MN;
     static constexpr int kK = kStageBytes / ELEM;                       // elements of K per stage
     static constexpr int kSpan = 128 / ELEM;                            // elements of an MN-major box's rows
@@ -71,9 +73,12 @@ struct Layout {
     static constexpr int kBytes = kABytes + kBBytes;
     static constexpr int kStages = (227 * 1024 - 1024 - 1024) / kBytes < 8 ? (227 * 1024 - 1024 - 1024) / kBytes : 8;
     static constexpr int kSmem = kStages * kBytes + 1024;
-    static constexpr int kBuffers = 512 / TN < 4 ? 512 / TN : 4;        // accumulators in tensor memory
+    static constexpr int kBuffers = 512 / kGN < 4 ? 512 / kGN : 4;      // accumulators in tensor memory
+    // a group's first column of B in a stage: its rows of 128 bytes, or (MN-major) its bytes of them
+    static constexpr int kGroupStep = (kGN / P) * (B_MN ? ELEM : kStageBytes) / 16;
+    static_assert(GROUPS == 1 || !B_MN || kBRows * ELEM == 128, "groups inside one MN-major box");
     static_assert(!(A_MN && kRows % kSpan != 0) && !(B_MN && kBRows % kSpan != 0), "whole boxes");
-    static_assert(kBytes % 1024 == 0 && TN % 32 == 0 && kStages >= 3, "stage layout");
+    static_assert(kBytes % 1024 == 0 && TN % (32 * GROUPS) == 0 && kStages >= 3, "stage layout");
 };
 
 struct Sync {
@@ -82,16 +87,28 @@ struct Sync {
     unsigned int abort;
 };
 
+// One lane of a converged warp, known to the compiler as such: what it issues takes its
+// operands from uniform registers. (Loops of one lane alone, with the same instructions, took
+// 870 cycles for an issuer's step.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0u;
+}
+
 // A bounded wait that gives up at once when another role of this CTA has.
-__device__ __forceinline__ bool wait_or_abort(Sync& sy, uint64_t* bar, uint32_t parity, const Shape& s) {
-    if (mbar_test(bar, parity)) return true;
+static __device__ __noinline__ bool wait_longer(volatile unsigned int* abort, uint64_t* bar, uint32_t parity, uint32_t rounds,
+                                                unsigned int* error) {
     for (int i = 0; i < kWaitSlices; ++i) {
-        if (mbar_wait(bar, parity, s.rounds)) return true;
-        if (*const_cast<volatile unsigned int*>(&sy.abort) != 0u) return false;
+        if (mbar_wait<false>(bar, parity, rounds)) return true;
+        if (*abort != 0u) return false;
     }
-    *const_cast<volatile unsigned int*>(&sy.abort) = 1u;
-    if (s.error != nullptr) atomicOr(s.error, kDevErrTimeout);
+    *abort = 1u;
+    if (error != nullptr) atomicOr(error, kDevErrTimeout);
     return false;
+}
+__device__ __forceinline__ bool wait_or_abort(Sync& sy, uint64_t* bar, uint32_t parity, const Shape& s) {
+    return mbar_wait<false>(bar, parity, 1) || wait_longer(&sy.abort, bar, parity, s.rounds, s.error);
 }
 
 // A box of a tensor map into this CTA's shared memory, completing on `bar` (with a pair: a
@@ -114,6 +131,13 @@ __device__ __forceinline__ uint64_t policy_evict_last() {
     return p;
 }
 
+// Arrive on rank 0's barrier. What the arrival orders are tensor-memory loads, by the tcgen05
+// fences; released at cluster scope it would wait for this thread's global accesses in flight
+// too, and a step of the FP8 product took 1.05 us.
+__device__ __forceinline__ void arrive_rank0(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_map(bar, 0)) : "memory");
+}
+
 // An operand's part of a stage: `rows` of M or N from `mn`, kK elements of K from `k`.
 template <class L, bool MN>
 __device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* map, int rows, int mn, int k, uint32_t bar,
@@ -131,35 +155,31 @@ template <class L>
 struct Acc {
     Sync& sy;
     const Shape& shape;
-    uint32_t tmem, n = 0;
-    __device__ Acc(Sync& s, const Shape& sh, uint32_t t) : sy(s), shape(sh), tmem(t) {}
+    uint32_t tmem, n;   // n: accumulators in the issuer's order; a set's are its group's
+    __device__ Acc(Sync& s, const Shape& sh, uint32_t t, int warp) : sy(s), shape(sh), tmem(t), n(warp / L::kSet) {}
     // Waits for the next accumulator: its first column, or ~0 if the wait gave up.
     __device__ __forceinline__ uint32_t next() {
         const uint32_t b = n % L::kBuffers;
         const bool ok = wait_or_abort(sy, &sy.acc_full[b], (n / L::kBuffers) & 1, shape);
         if (!__all_sync(0xFFFFFFFFu, ok)) return ~0u;
         tc::fence_after_sync();
-        return tmem + b * L::kTN;
+        return tmem + b * L::kGN;
     }
     // This warp has read the accumulator (all of its loads waited for).
     __device__ __forceinline__ void release() {
         tc::fence_before_sync();
         __syncwarp();
-        if ((threadIdx.x & 31) == 0) {
-            uint64_t* bar = &sy.acc_empty[n % L::kBuffers];
-            if constexpr (L::kP == 1) mbar_arrive(bar);
-            else mbar_arrive_remote(cluster_map(bar, 0));
-        }
-        ++n;
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&sy.acc_empty[n % L::kBuffers]);
+        n += L::kGroups;
     }
 };
 
 // Op: Layout, Args (with `Shape shape`), kFormat (idesc_f), kPerStep (an accumulator per step of
-// K, for results that are scaled step by step; else one per tile), kAKeep / kBKeep (the operand is
+// K and group of columns, for results that are scaled step by step; else one per tile), kAKeep / kBKeep (the operand is
 // read by other tiles too: kept in L2), and tile(args, tile, warp, lane, rank, acc), false when a
 // wait gave up.
 template <class Op>
-__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ CUtensorMap map_a,
+__global__ void __launch_bounds__(Op::Layout::kThreads, 1) product_kernel(const __grid_constant__ CUtensorMap map_a,
                                                               const __grid_constant__ CUtensorMap map_b,
                                                               const __grid_constant__ typename Op::Args a) {
     using L = typename Op::Layout;
@@ -167,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     extern __shared__ uint8_t smem_raw[];
     __shared__ Sync sy;
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = P == 1 ? 0 : static_cast<int>(cluster_ctarank());
     const Shape& s = a.shape;
     if (threadIdx.x == 0) {
@@ -177,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         }
         for (int i = 0; i < L::kBuffers; ++i) {
             mbar_init(&sy.acc_full[i], 1);
-            mbar_init(&sy.acc_empty[i], kEpiWarps * P);
+            mbar_init(&sy.acc_empty[i], L::kSet + (rank == 0 ? P - 1 : 0));   // rank 0: rank 1's forwarder too
         }
         mbar_init(&sy.issued, 1);
         mbar_init_fence();
@@ -196,7 +216,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const int tiles = s.tiles_m * s.tiles_n * s.splits;
     const int first = static_cast<int>(blockIdx.x) / P, stride = static_cast<int>(gridDim.x) / P;
 
-    if (warp == kProducer && lane == 0 && s.idle != kRoleProducer) {
+    // (the producer's and the issuer's warps run their loops whole, one elected lane issues)
+    if (warp == L::kProducer && s.idle != kRoleProducer) {
         const uint64_t keep = policy_evict_last(), once = policy_evict_first();
         const uint64_t pol_a = Op::kAKeep ? keep : once, pol_b = Op::kBKeep ? keep : once;
         uint32_t it = 0, st = 0, phase = 1;
@@ -206,14 +227,17 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const int am = s.a_mn + (t.m * P + rank) * kRows, bn = s.b_mn + t.n * L::kTN + rank * L::kBRows;
             const int steps = steps_of(s, t.split), k0 = t.split * s.split_steps * L::kK;
             for (int k = 0; k < steps; ++k, ++it) {
-                if (it >= static_cast<uint32_t>(kStages) && !(ok = wait_or_abort(sy, &sy.empty[st], phase, s))) break;
+                if (it >= static_cast<uint32_t>(kStages) && !(ok = __all_sync(~0u, wait_or_abort(sy, &sy.empty[st], phase, s)))) break;
                 uint8_t* dst = smem + st * L::kBytes;
                 uint32_t bar;
                 if constexpr (P == 1) bar = smem_u32(&sy.full[st]);
                 else bar = cluster_map(&sy.full[st], 0);
-                if (rank == 0) mbar_arrive_expect_tx(&sy.full[st], P * L::kBytes);
-                load_operand<L, L::kAMn>(dst, &map_a, kRows, am, s.a_k + k0 + k * L::kK, bar, pol_a);
-                load_operand<L, L::kBMn>(dst + L::kABytes, &map_b, L::kBRows, bn, s.b_k + k0 + k * L::kK, bar, pol_b);
+                if (elect_one()) {
+                    if (rank == 0) mbar_arrive_expect_tx(&sy.full[st], P * L::kBytes);
+                    load_operand<L, L::kAMn>(dst, &map_a, kRows, am, s.a_k + k0 + k * L::kK, bar, pol_a);
+                    load_operand<L, L::kBMn>(dst + L::kABytes, &map_b, L::kBRows, bn, s.b_k + k0 + k * L::kK, bar, pol_b);
+                }
+                __syncwarp();
                 if (++st == static_cast<uint32_t>(kStages)) {
                     st = 0;
                     phase ^= 1u;
@@ -224,31 +248,43 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         // rank 0's barriers; rank 1 waits for the last signals to its own (both bounded).
         for (uint32_t b = it > static_cast<uint32_t>(kStages) ? it - kStages : 0; b < it; ++b)
             if (!mbar_wait(rank == 0 ? &sy.full[b % kStages] : &sy.empty[b % kStages], (b / kStages) & 1, kDrainRounds)) break;
-    } else if (warp == kIssuer && lane == 0 && rank == 0 && s.idle != kRoleIssuer) {
-        constexpr uint32_t kIdesc = tc::idesc_f(Op::kFormat, L::kAMn, L::kBMn, kRows * P, L::kTN);
+    } else if (warp == L::kIssuer && rank == 0 && s.idle != kRoleIssuer) {
+        constexpr uint32_t kIdesc = tc::idesc_f(Op::kFormat, L::kAMn, L::kBMn, kRows * P, L::kGN);
+        static_assert(Op::kPerStep || L::kGroups == 1, "one accumulator per tile");
         constexpr bool kF8 = L::kElem == 1;
         // 32 bytes of K: along a 128-byte row, or (MN-major) as many whole rows as elements
         constexpr uint32_t kStepA = L::kAMn ? 32 / L::kElem * 128 / 16 : 2, kStepB = L::kBMn ? 32 / L::kElem * 128 / 16 : 2;
-        uint32_t it = 0, n = 0, st = 0, phase = 0;
+        const uint32_t base = smem_u32(smem);
+        const uint64_t first_a = L::kAMn ? tc::desc_operand_mn(base, L::kK) : tc::desc_operand(base);
+        const uint64_t first_b = L::kBMn ? tc::desc_operand_mn(base + L::kABytes, L::kK) : tc::desc_operand(base + L::kABytes);
+        uint32_t n = 0, st = 0, phase = 0;
         bool ok = true;
+        const auto accumulator = [&] {   // the next accumulator has been read
+            const uint32_t use = n / L::kBuffers;
+            return use == 0 || __all_sync(~0u, wait_or_abort(sy, &sy.acc_empty[n % L::kBuffers], (use - 1) & 1, s));
+        };
         for (int i = first; ok && i < tiles; i += stride) {
             const int steps = steps_of(s, tile_at(s, i).split);
-            for (int k = 0; k < steps; ++k, ++it) {
-                if (Op::kPerStep || k == 0) {
-                    const uint32_t use = n / L::kBuffers;
-                    if (use > 0 && !(ok = wait_or_abort(sy, &sy.acc_empty[n % L::kBuffers], (use - 1) & 1, s))) break;
-                }
-                if (!(ok = wait_or_abort(sy, &sy.full[st], phase, s))) break;
-                tc::fence_after_sync();
-                const uint32_t base = smem_u32(smem + st * L::kBytes);
-                const uint64_t da = L::kAMn ? tc::desc_operand_mn(base, L::kK) : tc::desc_operand(base);
-                const uint64_t db = L::kBMn ? tc::desc_operand_mn(base + L::kABytes, L::kK) : tc::desc_operand(base + L::kABytes);
-                const uint32_t d = tmem + (n % L::kBuffers) * L::kTN;
+            for (int k = 0; ok && k < steps; ++k) {
+                if (!Op::kPerStep && k == 0 && !(ok = accumulator())) break;
+                if (!(ok = __all_sync(~0u, wait_or_abort(sy, &sy.full[st], phase, s)))) break;
+                const uint64_t da = first_a + st * (L::kBytes / 16), db = first_b + st * (L::kBytes / 16);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    tc::mma_f<P, kF8>(d, da + kStepA * j, db + kStepB * j, kIdesc, (!Op::kPerStep && k > 0) || j > 0);
-                tc::commit_all<P>(&sy.empty[st]);
-                if (Op::kPerStep || k == steps - 1) tc::commit_all<P>(&sy.acc_full[n++ % L::kBuffers]);
+                for (int g = 0; g < L::kGroups; ++g) {
+                    if (Op::kPerStep && !(ok = accumulator())) break;
+                    tc::fence_after_sync();
+                    const uint32_t b = n % L::kBuffers, d = tmem + b * L::kGN;
+                    const bool last = Op::kPerStep || k == steps - 1;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            tc::mma_f<P, kF8>(d, da + kStepA * j, db + L::kGroupStep * g + kStepB * j, kIdesc, (!Op::kPerStep && k > 0) || j > 0);
+                        if (last) tc::commit_all<P>(&sy.acc_full[b]);
+                        if (g == L::kGroups - 1) tc::commit_all<P>(&sy.empty[st]);
+                    }
+                    __syncwarp();
+                    if (last) ++n;
+                }
                 if (++st == static_cast<uint32_t>(kStages)) {
                     st = 0;
                     phase ^= 1u;
@@ -256,10 +292,19 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             }
         }
         // the issued instructions finish before tensor memory is freed, whoever gave up (bounded)
-        tc::commit_own<P>(&sy.issued);
+        if (elect_one()) tc::commit_own<P>(&sy.issued);
+        __syncwarp();
         mbar_wait(&sy.issued, 0, kDrainRounds);
-    } else if (warp < kEpiWarps && s.idle != kRoleEpilogue) {
-        Acc<L> acc(sy, s, tmem);
+    } else if (P > 1 && warp == L::kIssuer && lane == 0 && rank == 1 && s.idle != kRoleIssuer) {
+        // rank 1's forwarder: its CTA has read an accumulator (one arrival from another CTA, in
+        // place of one per warp)
+        uint32_t n = 0;
+        bool ok = true;
+        for (int i = first; ok && i < tiles; i += stride)
+            for (int u = Op::kPerStep ? steps_of(s, tile_at(s, i).split) * L::kGroups : 1; ok && u > 0; --u, ++n)
+                if ((ok = wait_or_abort(sy, &sy.acc_empty[n % L::kBuffers], (n / L::kBuffers) & 1, s))) arrive_rank0(&sy.acc_empty[n % L::kBuffers]);
+    } else if (warp < L::kEpiWarps && s.idle != kRoleEpilogue) {
+        Acc<L> acc(sy, s, tmem, warp);
         for (int i = first; i < tiles; i += stride)
             if (!Op::tile(a, tile_at(s, i), warp, lane, rank, acc)) break;
     }
@@ -311,7 +356,7 @@ cudaError_t launch(const CUtensorMap& map_a, const CUtensorMap& map_b, typename 
     const long long most = sms / L::kP;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((tiles < most ? tiles : most) * L::kP));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(L::kThreads);
     cfg.dynamicSmemBytes = L::kSmem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
