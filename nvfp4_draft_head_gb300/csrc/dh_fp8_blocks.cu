@@ -8,11 +8,7 @@
 // The inner sums run on the tensor cores (kind::f8f6f4, exact products, 32-bit accumulators);
 // 128 is one stage of K (dh_gemm.cuh), so each step leaves an accumulator of its own, which the
 // epilogue multiplies by the two scales and adds to 32-bit sums in registers.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include "dh_gemm.cuh"
-#include "dh_rows.cuh"
+#include "dh_fp8_blocks.cuh"
 
 namespace dh {
 namespace f8 {
@@ -21,13 +17,10 @@ using gemm::Acc;
 using gemm::ceil_div;
 using gemm::Tile;
 
-constexpr int kBlock = 128;   // elements of a scale
-
 // ------------------------------------------------------------ quantisation ----
 
 // Codes and scales of rows x [M][width]: eight lanes per block of 128, 16 elements each.
-// codes [M][ldc] (ldc = width rounded up to 16, zeros beyond width), scales [blocks][M]. A block
-// with a value that is not finite gets the scale NaN: its token's results are NaN.
+// codes [M][ldc] (ldc = width rounded up to 16, zeros beyond width), scales [blocks][M].
 constexpr int kQThreads = 256;
 template <class T, bool VEC>
 __global__ void __launch_bounds__(kQThreads) quantize_kernel(const T* __restrict__ x, long long ldx, int M, int width,
@@ -36,36 +29,11 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const T* __restrict
     const unsigned unit = blockIdx.x * (kQThreads / 8) + (threadIdx.x >> 3);   // < 2^31 (checked)
     const unsigned m = unit / per_row, b = unit - m * per_row;
     const bool in = m < static_cast<unsigned>(M);
-    const int k = static_cast<int>(b) * kBlock + (threadIdx.x & 7) * 16;
-    const int n = in ? min(16, width - k) : 0;
-    float v[16];
-    const T* src = x + static_cast<size_t>(m) * ldx + k;
-    if (n == 16) {
-        rows::load16<T, VEC>(src, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = i < n ? rows::Elem<T>::load(src + i) : 0.0f;
-    }
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    const bool finite = top < 0x7F800000u;
-    const float s = finite ? act_fp8_scale(__uint_as_float(top)) : __uint_as_float(0x7FC00000u);
+    const int k = static_cast<int>(b) * kBlock + (threadIdx.x & 7) * 16, n = in ? min(16, width - k) : 0;
+    uint4 w;
+    const float s = encode16<T, VEC>(x + static_cast<size_t>(m) * ldx + k, n, w);
     if (in && (threadIdx.x & 7) == 0) scales[static_cast<size_t>(b) * M + m] = s;
-    if (n <= 0) return;
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float q[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) q[j] = fminf(fmaxf(__fdiv_rn(v[4 * i + j], s), -448.0f), 448.0f);
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q[2], q[3]), __NV_SATFINITE, __NV_E4M3);
-        w[i] = lo | (hi << 16);
-    }
-    *reinterpret_cast<uint4*>(codes + static_cast<size_t>(m) * ldc + k) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (n > 0) *reinterpret_cast<uint4*>(codes + static_cast<size_t>(m) * ldc + k) = w;
 }
 
 // A weight's blocks: one CTA per 128 x 128, its 16,384 values in registers between the maximum
@@ -162,7 +130,7 @@ __device__ __forceinline__ void transpose32(float* v, int lane) {
 // MN-major (its rows along the contraction) for dx.
 template <class TY, bool GRADIENT>
 struct Product {
-    using Layout = gemm::Layout<2, 256, 1, false, GRADIENT, 16, 2>;
+    using Layout = gemm::Layout<1, 256, 1, false, GRADIENT, 16>;
     static constexpr int kFormat = 0;
     static constexpr bool kPerStep = true, kAKeep = true, kBKeep = true;
     struct Args {
@@ -177,12 +145,9 @@ struct Product {
     };
     __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int rank, Acc<Layout>& acc) {
         constexpr int kPart = Layout::kPart;
-        static_assert(kPart == 64 && Layout::kTN == 2 * kBlock && Layout::kP == 2, "a warp's columns lie in one block of the weight");
-        // A group's accumulator: its first half from rank 0's rows of B (block 0 of the tile's
-        // two), the second from rank 1's (block 1).
-        const int row0 = (t.m * Layout::kP + rank) * gemm::kRows + (warp & 3) * 32, row = row0 + lane;
-        const int group = warp / Layout::kSet, block = warp / 4 % 2, steps = a.shape.steps;
-        const int n0 = t.n * Layout::kTN + block * kBlock + group * kPart;
+        static_assert(kBlock % kPart == 0 && Layout::kP == 1, "a warp's columns lie in one block of the weight");
+        const int row0 = t.m * gemm::kRows + (warp & 3) * 32, row = row0 + lane, steps = a.shape.steps;
+        const int n0 = t.n * Layout::kTN + (warp >> 2) * kPart;
         const bool in = row < a.M;
         // (columns beyond N: any scale)
         const float* sw = a.sw + static_cast<size_t>(n0 < a.N ? n0 / kBlock : 0) * a.sw_j;
@@ -202,7 +167,7 @@ struct Product {
             s2 = scale_at(b + 2);
             const uint32_t at = acc.next();
             if (at == ~0u) return false;
-            const uint32_t from = at + (static_cast<uint32_t>(warp & 3) << 21) + block * kPart;
+            const uint32_t from = at + (static_cast<uint32_t>(warp & 3) << 21) + (warp >> 2) * kPart;
 #pragma unroll
             for (int c = 0; c < kPart; c += 16) {
                 uint32_t r[16];
@@ -239,7 +204,7 @@ struct Product {
 
 template <class T>
 cudaError_t quantize(const Fp8BlockArgs& f, int width, uint8_t* codes, int ldc, float* scales, cudaStream_t s) {
-    const bool vec = (reinterpret_cast<uintptr_t>(f.x) & 15u) == 0 && (f.M == 1 || (f.ldx * static_cast<long long>(sizeof(T))) % 16 == 0);
+    const bool vec = rows_aligned16(f.x, f.ldx * static_cast<long long>(sizeof(T)), f.M);
     const unsigned units = static_cast<unsigned>(f.M) * static_cast<unsigned>(ceil_div(width, kBlock));
     const unsigned grid = (units + kQThreads / 8 - 1) / (kQThreads / 8);
     if (vec) quantize_kernel<T, true><<<grid, kQThreads, 0, s>>>(static_cast<const T*>(f.x), f.ldx, f.M, width, codes, ldc, scales);
@@ -258,7 +223,7 @@ cudaError_t product(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, const 
     if ((e = gemm::encode_operand<L, GRADIENT>(&map_b, f.q, out, width, f.K, L::kBRows)) != cudaSuccess) return e;
     typename P::Args a = {};
     const int steps = ceil_div(width, kBlock);
-    a.shape = {ceil_div(f.M, 256), ceil_div(out, L::kTN), 1, steps, steps, 0, 0, 0, 0, f.error, 0, 0};
+    a.shape = {ceil_div(f.M, gemm::kRows * L::kP), ceil_div(out, L::kTN), 1, steps, steps, 0, 0, 0, 0, f.error, 0, 0};
     a.sx = scales;
     a.sw = f.scale;
     a.sw_j = GRADIENT ? 1 : kb;
@@ -272,15 +237,24 @@ cudaError_t product(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, const 
 }
 
 template <class TY>
+cudaError_t run_many(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, const float* scales, cudaStream_t s) {
+    return f.gradient ? product<TY, true>(f, codes, ldc, scales, s) : product<TY, false>(f, codes, ldc, scales, s);
+}
+
 cudaError_t run(const Fp8BlockArgs& f, cudaStream_t s) {
+    const bool few = few_supported(f);
+    if (few && f.M <= kFusedTokens) return launch_few(f, nullptr, 0, nullptr, s);
     const int width = f.gradient ? f.N : f.K, ldc = ceil_div(width, 16) * 16;
     uint8_t* codes = static_cast<uint8_t*>(f.ws);
     float* scales = reinterpret_cast<float*>(codes + (static_cast<size_t>(f.M) * ldc + 255) / 256 * 256);
-    cudaError_t e = f.x_type == DH_T_BF16  ? quantize<__nv_bfloat16>(f, width, codes, ldc, scales, s)
-                    : f.x_type == DH_T_F16 ? quantize<__half>(f, width, codes, ldc, scales, s)
-                                           : quantize<float>(f, width, codes, ldc, scales, s);
+    const cudaError_t e = f.x_type == DH_T_BF16  ? quantize<__nv_bfloat16>(f, width, codes, ldc, scales, s)
+                          : f.x_type == DH_T_F16 ? quantize<__half>(f, width, codes, ldc, scales, s)
+                                                 : quantize<float>(f, width, codes, ldc, scales, s);
     if (e != cudaSuccess) return e;
-    return f.gradient ? product<TY, true>(f, codes, ldc, scales, s) : product<TY, false>(f, codes, ldc, scales, s);
+    if (few) return launch_few(f, codes, ldc, scales, s);
+    return f.y_type == DH_T_BF16  ? run_many<__nv_bfloat16>(f, codes, ldc, scales, s)
+           : f.y_type == DH_T_F16 ? run_many<__half>(f, codes, ldc, scales, s)
+                                  : run_many<float>(f, codes, ldc, scales, s);
 }
 
 }  // namespace f8
@@ -297,12 +271,6 @@ cudaError_t launch_fp8_quantize_blocks(const uint16_t* W, int V, int K, const in
     return cudaGetLastError();
 }
 
-cudaError_t launch_fp8_blocks(const Fp8BlockArgs& f, cudaStream_t s) {
-    switch (f.y_type) {
-        case DH_T_BF16: return f8::run<__nv_bfloat16>(f, s);
-        case DH_T_F16: return f8::run<__half>(f, s);
-        default: return f8::run<float>(f, s);
-    }
-}
+cudaError_t launch_fp8_blocks(const Fp8BlockArgs& f, cudaStream_t s) { return f8::run(f, s); }
 
 }  // namespace dh

@@ -75,8 +75,8 @@ struct Layout {
     static constexpr int kSmem = kStages * kBytes + 1024;
     static constexpr int kBuffers = 512 / kGN < 4 ? 512 / kGN : 4;      // accumulators in tensor memory
     // a group's first column of B in a stage: its rows of 128 bytes, or (MN-major) its bytes of them
-    static constexpr int kGroupStep = (kGN / P) * (B_MN ? ELEM : kStageBytes) / 16;
-    static_assert(GROUPS == 1 || !B_MN || kBRows * ELEM == 128, "groups inside one MN-major box");
+    // (or whole boxes)
+    static constexpr int kGroupStep = (!B_MN ? (kGN / P) * kStageBytes : kGN / P >= kSpan ? kGN / P / kSpan * kK * 128 : kGN / P * ELEM) / 16;
     static_assert(!(A_MN && kRows % kSpan != 0) && !(B_MN && kBRows % kSpan != 0), "whole boxes");
     static_assert(kBytes % 1024 == 0 && TN % (32 * GROUPS) == 0 && kStages >= 3, "stage layout");
 };
