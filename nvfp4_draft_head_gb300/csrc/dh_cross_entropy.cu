@@ -81,11 +81,13 @@ struct Stats {
         Tokens tok;
         float2* part;   // [2 tiles_n][T]: maximum and sum of 128 columns
         float* target;  // [T]: the token's logit
+        uint32_t* wmax; // cleared for what follows
     };
     __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int rank, Acc<Layout>& acc) {
         const int row = (t.m * kPair + rank) * gemm::kRows + (warp & 3) * 32 + lane, half = warp >> 2;
         const int n0 = t.n * kTN + half * kHalf;
         const int y = row < a.tok.T ? a.tok.row(row) : -1;
+        if (row == 0 && n0 == 0) *a.wmax = 0u;
         const uint32_t at = acc.next();
         if (at == ~0u) return false;
         const uint32_t from = at + (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf;
@@ -127,60 +129,80 @@ struct Stats {
     }
 };
 
-// Joins the parts: 32 tokens per CTA, its warps over the parts, then over the warps.
-constexpr int kJoinWarps = 32;
+// What the gradients need of a row: the largest finite row weight in use (bits of its
+// magnitude), and, where dW is wanted, the hidden states with zeros in the rows that are left
+// out: their g is 0, but 0 times what a padding row may hold (infinities, NaN) is not.
+struct Rows {
+    const void* hidden;      // 16-bit rows
+    long long ld;
+    int K;
+    void* copy;              // [T][K] or null
+    uint32_t* wmax;
+    __device__ __forceinline__ void weigh(float w, bool live) const {
+        const uint32_t bits = __float_as_uint(w) & 0x7FFFFFFFu;
+        if (live && bits < 0x7F800000u) atomicMax(wmax, bits);   // (a maximum: the order does not matter)
+    }
+    __device__ __forceinline__ void move(int t, bool live, int i, int step) const {
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(hidden) + static_cast<size_t>(t) * ld);
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(copy) + static_cast<size_t>(t) * K);
+        for (; i < K / 8; i += step) dst[i] = live ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+    }
+};
+
+// Joins the parts: 8 tokens per CTA, the CTA's 1,024 threads over the parts, then over the
+// threads of a token. With gradients to come it prepares their rows too.
+constexpr int kJoinTokens = 8, kJoinThreads = 1024, kJoinWarps = kJoinThreads / 32;
 __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
     const float top = fmaxf(m, m2), ref = top == kNegInf ? 0.0f : top;
     s = s * exp2_approx((m - ref) * kLog2e) + s2 * exp2_approx((m2 - ref) * kLog2e);
     m = top;
 }
-__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Tokens tok, const float2* __restrict__ part, int parts,
-                                                               const float* __restrict__ target, float* __restrict__ loss,
-                                                               float* __restrict__ lse, float* __restrict__ rest) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = blockIdx.x * 32 + lane;
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Tokens tok, const float2* __restrict__ part, int parts,
+                                                            const float* __restrict__ target, float* __restrict__ loss,
+                                                            float* __restrict__ lse, float* __restrict__ rest, const Rows rows) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, token = threadIdx.x % kJoinTokens, t = blockIdx.x * kJoinTokens + token;
     float m = kNegInf, s = 0.0f;
-    if (t < tok.T)
-        for (int j = warp; j < parts; j += kJoinWarps) {
+    if (t < tok.T) {
+#pragma unroll 4
+        for (int j = threadIdx.x / kJoinTokens; j < parts; j += kJoinThreads / kJoinTokens) {
             const float2 p = part[static_cast<size_t>(j) * tok.T + t];
             join(m, s, p.x, p.y);
         }
-    __shared__ float2 all[kJoinWarps][33];
-    all[warp][lane] = make_float2(m, s);
-    __syncthreads();
-    if (warp != 0 || t >= tok.T) return;
-#pragma unroll 4
-    for (int j = 1; j < kJoinWarps; ++j) join(m, s, all[j][lane].x, all[j][lane].y);
-    const float ln = logf(s), sum = m + ln;
-    if (loss != nullptr) {
-        const float w = tok.w(t);
-        loss[t] = w != 0.0f && tok.row(t) >= 0 ? w * (ln + (m - target[t])) : 0.0f;
     }
-    if (lse != nullptr) lse[t] = sum;
-    if (rest != nullptr) {   // what the sum rounded away (two-sum)
-        const float b = sum - m;
-        rest[t] = (m - (sum - b)) + (ln - b);
+#pragma unroll
+    for (int o = kJoinTokens; o < 32; o <<= 1) join(m, s, __shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, s, o));
+    __shared__ float2 all[kJoinWarps][kJoinTokens];
+    if (lane < kJoinTokens) all[warp][lane] = make_float2(m, s);
+    __syncthreads();
+    if (warp == 0 && lane < kJoinTokens && t < tok.T) {
+#pragma unroll 4
+        for (int j = 1; j < kJoinWarps; ++j) join(m, s, all[j][lane].x, all[j][lane].y);
+        const float ln = logf(s), sum = m + ln, w = tok.w(t);
+        const bool live = w != 0.0f && tok.row(t) >= 0;
+        if (loss != nullptr) loss[t] = live ? w * (ln + (m - target[t])) : 0.0f;
+        if (lse != nullptr) lse[t] = sum;
+        if (rest != nullptr) {   // what the sum rounded away (two-sum)
+            const float b = sum - m;
+            rest[t] = (m - (sum - b)) + (ln - b);
+        }
+        if (rows.wmax != nullptr) rows.weigh(w, live);
+    }
+    if (rows.copy != nullptr) {
+        constexpr int kPer = kJoinThreads / kJoinTokens;   // threads of a row
+        const int row = blockIdx.x * kJoinTokens + threadIdx.x / kPer;
+        if (row < tok.T) rows.move(row, tok.w(row) != 0.0f && tok.row(row) >= 0, threadIdx.x % kPer, kPer);
     }
 }
 
 // --------------------------------------------------------------- gradients ----
 
-// The largest finite row weight in use (bits of its magnitude), and, where dW is wanted, the
-// hidden states with zeros in the rows that are left out: their g is 0, but 0 times what a
-// padding row may hold (infinities, NaN) is not.
-template <class T>
-__global__ void __launch_bounds__(128) rows_kernel(const Tokens tok, const T* __restrict__ h, long long ld, int K, T* __restrict__ out,
-                                                   uint32_t* __restrict__ wmax) {
+// The rows' work where there is no loss to join.
+__global__ void __launch_bounds__(128) rows_kernel(const Tokens tok, const Rows rows) {
     const int t = blockIdx.x;
     const float w = tok.w(t);
     const bool live = w != 0.0f && tok.row(t) >= 0;
-    if (threadIdx.x == 0 && live) {
-        const uint32_t bits = __float_as_uint(w) & 0x7FFFFFFFu;
-        if (bits < 0x7F800000u) atomicMax(wmax, bits);   // (a maximum: the order does not matter)
-    }
-    if (out == nullptr) return;
-    const uint4* src = reinterpret_cast<const uint4*>(h + static_cast<size_t>(t) * ld);
-    uint4* dst = reinterpret_cast<uint4*>(out + static_cast<size_t>(t) * K);
-    for (int i = threadIdx.x; i < K / 8; i += blockDim.x) dst[i] = live ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+    if (threadIdx.x == 0) rows.weigh(w, live);
+    if (rows.copy != nullptr) rows.move(t, live, threadIdx.x, blockDim.x);
 }
 
 template <class T>
@@ -244,7 +266,8 @@ struct Weights {   // g of a piece
     }
 };
 
-// dh: g (along the piece) times the piece's head rows, as 32-bit sums per part of the piece.
+// dh: g (along the piece) times the piece's head rows, as 32-bit sums: [T][K] of whole tiles
+// and first parts, then the other parts of the tiles that are split, [split - 1][tile][256][256].
 template <class T>
 struct Hidden {
     using Layout = gemm::Layout<kPair, kTN, 2, false, true>;
@@ -253,16 +276,23 @@ struct Hidden {
     struct Args {
         gemm::Shape shape;
         int T_, K;
-        float* sum;   // [splits][T][K]
+        float* sum;
+        float* parts;
         int add;      // to what earlier pieces left
     };
     __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int rank, Acc<Layout>& acc) {
-        const int row = (t.m * kPair + rank) * gemm::kRows + (warp & 3) * 32 + lane, half = warp >> 2;
+        const int local = rank * gemm::kRows + (warp & 3) * 32 + lane, row = t.m * kTM + local, half = warp >> 2;
         const int n0 = t.n * kTN + half * kHalf;
+        float* out;
+        if (t.split <= 0) {
+            out = a.sum + static_cast<size_t>(row) * a.K + n0;
+        } else {
+            const int rest = a.shape.tiles() - a.shape.whole, at = gemm::tile_index(a.shape.tiles_m, a.shape.tiles_n, t.m, t.n) - a.shape.whole;
+            out = a.parts + (static_cast<size_t>((t.split - 1) * rest + at) * kTM + local) * kTN + half * kHalf;
+        }
         const uint32_t at = acc.next();
         if (at == ~0u) return false;
         const uint32_t from = at + (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf;
-        float* out = a.sum + (static_cast<size_t>(t.split) * a.T_ + row) * a.K + n0;
 #pragma unroll 1
         for (int c = 0; c < kHalf && n0 + c < a.K; c += 32) {
             uint32_t r[32];
@@ -329,26 +359,37 @@ struct Head {
     }
 };
 
-// dh from the sums of its parts: eight elements per thread, parts in order. Rows that are left
-// out are zeros whatever the head holds.
+// dh from the sums: eight elements per thread, the parts of a split tile in order. Rows that are
+// left out are zeros whatever the head holds.
+struct Sums {
+    const float* sum;
+    const float* parts;
+    int tiles_m, tiles_n, whole, splits;
+};
 template <class T>
-__global__ void __launch_bounds__(256) sum_kernel(const Tokens tok, const float* __restrict__ sum, int parts, int K,
-                                                  const uint32_t* __restrict__ wmax, T* __restrict__ out, long long ld) {
+__global__ void __launch_bounds__(256) sum_kernel(const Tokens tok, const Sums a, int K, const uint32_t* __restrict__ wmax,
+                                                  T* __restrict__ out, long long ld) {
     const float scale = exp2i(-scale_exponent<std::is_same<T, __half>::value>(*wmax));
-    const size_t per_row = K / 8, total = static_cast<size_t>(tok.T) * per_row, step = static_cast<size_t>(tok.T) * K;
+    const unsigned per_row = K / 8;
+    const size_t total = static_cast<size_t>(tok.T) * per_row;
     for (size_t i = blockIdx.x * static_cast<size_t>(blockDim.x) + threadIdx.x; i < total; i += static_cast<size_t>(gridDim.x) * blockDim.x) {
-        const float* p = sum + i * 8;
-        float v[8] = {};
-        for (int s = 0; s < parts; ++s, p += step) {
-            const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p + 4));
-            v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-            v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+        const int row = static_cast<int>(i / per_row), col = static_cast<int>(i % per_row) * 8;
+        const bool live = tok.w(row) != 0.0f && tok.row(row) >= 0;
+        const float4 x = __ldcs(reinterpret_cast<const float4*>(a.sum + i * 8)), y = __ldcs(reinterpret_cast<const float4*>(a.sum + i * 8 + 4));
+        float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        const int at = gemm::tile_index(a.tiles_m, a.tiles_n, row / kTM, col / kTN) - a.whole;
+        if (at >= 0) {
+            const size_t step = static_cast<size_t>(a.tiles_m * a.tiles_n - a.whole) * kTM * kTN;
+            const float* p = a.parts + (static_cast<size_t>(at) * kTM + row % kTM) * kTN + col % kTN;
+            for (int s = 1; s < a.splits; ++s, p += step) {
+                const float4 b = __ldcs(reinterpret_cast<const float4*>(p)), c = __ldcs(reinterpret_cast<const float4*>(p + 4));
+                v[0] += b.x; v[1] += b.y; v[2] += b.z; v[3] += b.w;
+                v[4] += c.x; v[5] += c.y; v[6] += c.z; v[7] += c.w;
+            }
         }
-        const size_t row = i / per_row, col = i % per_row * 8;
-        const bool live = tok.w(static_cast<int>(row)) != 0.0f && tok.row(static_cast<int>(row)) >= 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = live ? v[j] * scale : 0.0f;
-        *reinterpret_cast<uint4*>(out + row * ld + col) = rows::Elem<T>::pack(v);
+        *reinterpret_cast<uint4*>(out + static_cast<size_t>(row) * ld + col) = rows::Elem<T>::pack(v);
     }
 }
 
@@ -364,18 +405,28 @@ int piece_rows(int T, int N) {
     return static_cast<int>(least < all ? least : all);
 }
 
-// Parts of a piece's contraction for dh: enough to fill the pairs of SMs once, at least eight
-// steps long.
-void hidden_parts(int T, int K, int piece, int* parts, int* steps) {
-    const int tiles = ceil_div(T, kTM) * ceil_div(K, kTN), all = ceil_div(piece, 64);
-    int p = tiles < 76 ? 76 / tiles : 1;
-    if (p > all / 8) p = all / 8 > 0 ? all / 8 : 1;
-    *steps = ceil_div(all, p);
-    *parts = ceil_div(all, *steps);
+// dh's tiles: whole ones as long as they fill all pairs of SMs, the rest in parts (at least
+// eight steps long) such that its rounds take the fewest steps, a part counted as eight more.
+// 4,096 x 64,026 x 2,560 (160 tiles for 76 pairs): see the top of the file.
+gemm::Shape hidden_tiles(int T, int K, int piece, unsigned int* error) {
+    gemm::Shape s = gemm::whole_tiles(ceil_div(T, kTM), ceil_div(K, kTN), ceil_div(piece, 64), error);
+    const int pairs = sm_count() / 2 > 0 ? sm_count() / 2 : 1, rest = s.whole % pairs;
+    if (rest == 0) return s;
+    s.whole -= rest;
+    long long least = 0;
+    for (int p = 1; p <= 32 && (p == 1 || s.steps / p >= 8); ++p) {
+        const long long cost = static_cast<long long>(ceil_div(rest * p, pairs)) * ceil_div(s.steps, p) + 8 * p;
+        if (p == 1 || cost < least) {
+            least = cost;
+            s.split_steps = ceil_div(s.steps, p);
+        }
+    }
+    s.splits = ceil_div(s.steps, s.split_steps);
+    return s;
 }
 
 struct Space {
-    size_t wmax, part, target, lse, rest, g, hidden, sum, bytes;
+    size_t wmax, part, target, lse, rest, g, hidden, sum, parts, bytes;
 };
 Space space_of(int T, int N, int K, bool loss, bool dh, bool dw) {
     Space s = {};
@@ -395,9 +446,9 @@ Space space_of(int T, int N, int K, bool loss, bool dh, bool dw) {
     if (dh || dw) s.g = take(t * piece_rows(T, N) * 2);
     if (dw) s.hidden = take(t * K * 2);
     if (dh) {
-        int parts, steps;
-        hidden_parts(T, K, piece_rows(T, N), &parts, &steps);
-        s.sum = take(t * K * 4 * parts);
+        const gemm::Shape h = hidden_tiles(T, K, piece_rows(T, N), nullptr);
+        s.sum = take(t * K * 4);
+        s.parts = take(static_cast<size_t>(h.tiles() - h.whole) * (h.splits - 1) * kTM * kTN * 4);
     }
     s.bytes = at;
     return s;
@@ -411,6 +462,8 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
     Tokens tok = {c.tokens, c.row_of, c.weight, c.V, c.T, c.N};
     uint32_t* wmax = reinterpret_cast<uint32_t*>(ws + sp.wmax);
     const int tiles_m = ceil_div(c.T, kTM);
+    T* hidden = dw ? reinterpret_cast<T*>(ws + sp.hidden) : nullptr;
+    const Rows rows = {c.hidden, c.ld_hidden, c.K, hidden, wmax};
     cudaError_t e;
     CUtensorMap map_h, map_w;
     using K1 = typename Stats<T>::Layout;
@@ -421,34 +474,37 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
     const float* rest = c.rest_in;
     if (loss) {
         typename Stats<T>::Args a = {};
-        a.shape = {tiles_m, ceil_div(c.N, kTN), 1, steps, steps, 0, 0, 0, 0, c.error, 0, 0};
+        a.shape = gemm::whole_tiles(tiles_m, ceil_div(c.N, kTN), steps, c.error);
         a.tok = tok;
         a.part = reinterpret_cast<float2*>(ws + sp.part);
         a.target = reinterpret_cast<float*>(ws + sp.target);
+        a.wmax = wmax;
         if ((e = gemm::launch<Stats<T>>(map_h, map_w, a, stream)) != cudaSuccess) return e;
         float* l = c.lse != nullptr ? c.lse : reinterpret_cast<float*>(ws + sp.lse);
         float* r = c.rest != nullptr ? c.rest : reinterpret_cast<float*>(ws + sp.rest);
-        join_kernel<<<ceil_div(c.T, 32), 32 * kJoinWarps, 0, stream>>>(tok, a.part, 2 * a.shape.tiles_n, a.target, c.loss, l, r);
+        join_kernel<<<ceil_div(c.T, kJoinTokens), kJoinThreads, 0, stream>>>(tok, a.part, 2 * a.shape.tiles_n, a.target, c.loss, l, r,
+                                                                              dh || dw ? rows : Rows{});
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         lse = l;
         rest = r;
     }
     if (!dh && !dw) return cudaSuccess;
 
-    T* hidden = dw ? reinterpret_cast<T*>(ws + sp.hidden) : nullptr;
-    if ((e = cudaMemsetAsync(wmax, 0, 4, stream)) != cudaSuccess) return e;
-    rows_kernel<T><<<c.T, 128, 0, stream>>>(tok, static_cast<const T*>(c.hidden), c.ld_hidden, c.K, hidden, wmax);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (!loss) {
+        if ((e = cudaMemsetAsync(wmax, 0, 4, stream)) != cudaSuccess) return e;
+        rows_kernel<<<c.T, 128, 0, stream>>>(tok, rows);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
     const int piece = piece_rows(c.T, c.N);
-    int parts, part_steps;
-    hidden_parts(c.T, c.K, piece, &parts, &part_steps);
+    const gemm::Shape tiles_h = hidden_tiles(c.T, c.K, piece, c.error);   // of a full piece
     T* g = reinterpret_cast<T*>(ws + sp.g);
     float* sum = reinterpret_cast<float*>(ws + sp.sum);
-    int filled = 0;   // parts of dh that hold sums
+    int splits = 1;   // of dh's split tiles: those of the first piece, which is the largest
     for (int first = 0; first < c.N; first += piece) {
         const int count = c.N - first < piece ? c.N - first : piece;
         typename Weights<T>::Args a = {};
-        a.shape = {tiles_m, ceil_div(count, kTN), 1, steps, steps, 0, 0, first, 0, c.error, 0, 0};
+        a.shape = gemm::whole_tiles(tiles_m, ceil_div(count, kTN), steps, c.error);
+        a.shape.b_mn = first;
         a.tok = tok;
         a.lse = lse;
         a.rest = rest;
@@ -464,14 +520,16 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
             if ((e = gemm::encode_operand<L, false>(&map_a, g, c.T, count, static_cast<uint64_t>(piece) * 2, gemm::kRows)) != cudaSuccess) return e;
             if ((e = gemm::encode_operand<L, true>(&map_b, c.head, c.K, c.N, c.ld_head * 2, 0)) != cudaSuccess) return e;
             typename Hidden<T>::Args b = {};
-            const int all = ceil_div(count, L::kK);
-            b.shape = {tiles_m, ceil_div(c.K, kTN), ceil_div(all, part_steps), all, part_steps, 0, 0, 0, first, c.error, 0, 0};
-            b.shape.a_k = 0;
+            b.shape = tiles_h;
+            b.shape.steps = ceil_div(count, L::kK);
+            b.shape.splits = ceil_div(b.shape.steps, tiles_h.split_steps);
+            b.shape.b_k = first;
             b.T_ = c.T;
             b.K = c.K;
             b.sum = sum;
+            b.parts = reinterpret_cast<float*>(ws + sp.parts);
             b.add = first > 0;
-            if (first == 0) filled = b.shape.splits;
+            if (first == 0) splits = b.shape.splits;
             if ((e = gemm::launch<Hidden<T>>(map_a, map_b, b, stream)) != cudaSuccess) return e;
         }
         if (dw) {
@@ -480,7 +538,7 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
             if ((e = gemm::encode_operand<L, true>(&map_b, hidden, c.K, c.T, static_cast<uint64_t>(c.K) * 2, 0)) != cudaSuccess) return e;
             typename Head<T>::Args b = {};
             const int all = ceil_div(c.T, L::kK);
-            b.shape = {ceil_div(count, kTM), ceil_div(c.K, kTN), 1, all, all, 0, 0, 0, 0, c.error, 0, 0};
+            b.shape = gemm::whole_tiles(ceil_div(count, kTM), ceil_div(c.K, kTN), all, c.error);
             b.rows = count;
             b.K = c.K;
             b.wmax = wmax;
@@ -491,7 +549,8 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
     }
     if (dh) {
         const size_t total = static_cast<size_t>(c.T) * (c.K / 8), want = (total + 255) / 256, cap = static_cast<size_t>(sm_count()) * 8;
-        sum_kernel<T><<<static_cast<unsigned>(want < cap ? want : cap), 256, 0, stream>>>(tok, sum, filled, c.K, wmax, static_cast<T*>(c.dhidden),
+        sum_kernel<T><<<static_cast<unsigned>(want < cap ? want : cap), 256, 0, stream>>>(
+            tok, Sums{sum, reinterpret_cast<float*>(ws + sp.parts), tiles_h.tiles_m, tiles_h.tiles_n, tiles_h.whole, splits}, c.K, wmax, static_cast<T*>(c.dhidden),
                                                                                       c.ld_dhidden);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }

@@ -223,7 +223,7 @@ cudaError_t product(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, const 
     if ((e = gemm::encode_operand<L, GRADIENT>(&map_b, f.q, out, width, f.K, L::kBRows)) != cudaSuccess) return e;
     typename P::Args a = {};
     const int steps = ceil_div(width, kBlock);
-    a.shape = {ceil_div(f.M, gemm::kRows * L::kP), ceil_div(out, L::kTN), 1, steps, steps, 0, 0, 0, 0, f.error, 0, 0};
+    a.shape = gemm::whole_tiles(ceil_div(f.M, gemm::kRows * L::kP), ceil_div(out, L::kTN), steps, f.error);
     a.sx = scales;
     a.sw = f.scale;
     a.sw_j = GRADIENT ? 1 : kb;

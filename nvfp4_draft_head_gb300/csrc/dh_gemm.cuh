@@ -34,13 +34,18 @@ constexpr uint32_t kDrainRounds = kWaitLimit / kWaitSlices;
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // What a launch multiplies: tiles, the steps of K, and where the operands start in their maps.
+// The first `whole` tiles are multiplied whole; each of the rest in `splits` parts of
+// split_steps steps of K (the last may have fewer), so that the last round of tiles over the SMs
+// can be a full one.
 struct Shape {
-    int tiles_m, tiles_n, splits;   // splits: parts of the contraction, each a tile of its own
-    int steps, split_steps;         // steps of K in all, and in a part (the last may have fewer)
+    int tiles_m, tiles_n, whole, splits;
+    int steps, split_steps;
     int a_mn, a_k, b_mn, b_k;       // first row (M / N) and first element of K of each operand
     unsigned int* error;            // DH_DEVERR_* word or null
     uint32_t rounds;                // tries of a bounded wait, times kWaitSlices
     int idle;                       // self-test: the role that does nothing (-1: none)
+    __host__ __device__ int tiles() const { return tiles_m * tiles_n; }
+    __host__ __device__ int units() const { return whole + (tiles() - whole) * splits; }
 };
 
 enum Role { kRoleProducer, kRoleIssuer, kRoleEpilogue };
@@ -48,15 +53,27 @@ enum Role { kRoleProducer, kRoleIssuer, kRoleEpilogue };
 // Tiles that are in work at the same time share operands in L2: groups of kGroup rows of
 // tiles, columns along a group.
 constexpr int kGroup = 8;
-struct Tile { int m, n, split; };
+struct Tile { int m, n, split, k0, steps; };   // split: the part, -1 for a whole tile; k0: its first step
 __device__ __forceinline__ Tile tile_at(const Shape& s, int i) {
-    const int per = s.tiles_m * s.tiles_n, split = i / per;
-    i -= split * per;
+    Tile t = {0, 0, -1, 0, s.steps};
+    if (i >= s.whole) {
+        const int rest = s.tiles() - s.whole, j = i - s.whole;
+        t.split = j / rest;
+        t.k0 = t.split * s.split_steps;
+        t.steps = min(s.split_steps, s.steps - t.k0);
+        i = s.whole + j - t.split * rest;
+    }
     const int g = i / (kGroup * s.tiles_n), rows = min(kGroup, s.tiles_m - g * kGroup);
     i -= g * kGroup * s.tiles_n;
-    return {g * kGroup + i % rows, i / rows, split};
+    t.n = i / rows;
+    t.m = g * kGroup + i - t.n * rows;
+    return t;
 }
-__device__ __forceinline__ int steps_of(const Shape& s, int split) { return min(s.split_steps, s.steps - split * s.split_steps); }
+// The place of tile (m, n) in that order.
+__host__ __device__ inline int tile_index(int tiles_m, int tiles_n, int m, int n) {
+    const int g = m / kGroup, rows = tiles_m - g * kGroup < kGroup ? tiles_m - g * kGroup : kGroup;
+    return g * kGroup * tiles_n + n * rows + m - g * kGroup;
+}
 
 template <int P, int TN, int ELEM, bool A_MN, bool B_MN, int EPI = 8, int GROUPS = 1>
 struct Layout {
@@ -213,7 +230,7 @@ __global__ void __launch_bounds__(Op::Layout::kThreads, 1) product_kernel(const 
     }
     tc::fence_after_sync();
     const uint32_t tmem = sy.tmem;
-    const int tiles = s.tiles_m * s.tiles_n * s.splits;
+    const int tiles = s.units();
     const int first = static_cast<int>(blockIdx.x) / P, stride = static_cast<int>(gridDim.x) / P;
 
     // (the producer's and the issuer's warps run their loops whole, one elected lane issues)
@@ -225,7 +242,7 @@ __global__ void __launch_bounds__(Op::Layout::kThreads, 1) product_kernel(const 
         for (int i = first; ok && i < tiles; i += stride) {
             const Tile t = tile_at(s, i);
             const int am = s.a_mn + (t.m * P + rank) * kRows, bn = s.b_mn + t.n * L::kTN + rank * L::kBRows;
-            const int steps = steps_of(s, t.split), k0 = t.split * s.split_steps * L::kK;
+            const int steps = t.steps, k0 = t.k0 * L::kK;
             for (int k = 0; k < steps; ++k, ++it) {
                 if (it >= static_cast<uint32_t>(kStages) && !(ok = __all_sync(~0u, wait_or_abort(sy, &sy.empty[st], phase, s)))) break;
                 uint8_t* dst = smem + st * L::kBytes;
@@ -264,7 +281,7 @@ __global__ void __launch_bounds__(Op::Layout::kThreads, 1) product_kernel(const 
             return use == 0 || __all_sync(~0u, wait_or_abort(sy, &sy.acc_empty[n % L::kBuffers], (use - 1) & 1, s));
         };
         for (int i = first; ok && i < tiles; i += stride) {
-            const int steps = steps_of(s, tile_at(s, i).split);
+            const int steps = tile_at(s, i).steps;
             for (int k = 0; ok && k < steps; ++k) {
                 if (!Op::kPerStep && k == 0 && !(ok = accumulator())) break;
                 if (!(ok = __all_sync(~0u, wait_or_abort(sy, &sy.full[st], phase, s)))) break;
@@ -301,7 +318,7 @@ __global__ void __launch_bounds__(Op::Layout::kThreads, 1) product_kernel(const 
         uint32_t n = 0;
         bool ok = true;
         for (int i = first; ok && i < tiles; i += stride)
-            for (int u = Op::kPerStep ? steps_of(s, tile_at(s, i).split) * L::kGroups : 1; ok && u > 0; --u, ++n)
+            for (int u = Op::kPerStep ? tile_at(s, i).steps * L::kGroups : 1; ok && u > 0; --u, ++n)
                 if ((ok = wait_or_abort(sy, &sy.acc_empty[n % L::kBuffers], (n / L::kBuffers) & 1, s))) arrive_rank0(&sy.acc_empty[n % L::kBuffers]);
     } else if (warp < L::kEpiWarps && s.idle != kRoleEpilogue) {
         Acc<L> acc(sy, s, tmem, warp);
@@ -320,6 +337,17 @@ __global__ void __launch_bounds__(Op::Layout::kThreads, 1) product_kernel(const 
 }
 
 // ------------------------------------------------------------------- host ----
+
+inline Shape whole_tiles(int tiles_m, int tiles_n, int steps, unsigned int* error) {
+    Shape s = {};
+    s.tiles_m = tiles_m;
+    s.tiles_n = tiles_n;
+    s.whole = tiles_m * tiles_n;
+    s.splits = 1;
+    s.steps = s.split_steps = steps;
+    s.error = error;
+    return s;
+}
 
 // A tensor map of a row-major matrix: `rows` rows of `cols` elements, `ld` bytes apart, read in
 // boxes of 128 bytes by box_rows with the 128-byte swizzle; what lies outside reads as zeros.
@@ -352,7 +380,7 @@ cudaError_t launch(const CUtensorMap& map_a, const CUtensorMap& map_b, typename 
         a.shape.rounds = kWaitLimit / kWaitSlices;
         a.shape.idle = -1;
     }
-    const long long tiles = static_cast<long long>(a.shape.tiles_m) * a.shape.tiles_n * a.shape.splits;
+    const long long tiles = a.shape.units();
     const long long most = sms / L::kP;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((tiles < most ? tiles : most) * L::kP));
