@@ -329,6 +329,7 @@ struct Head {
         const uint32_t* wmax;
         T* out;                  // the piece's first row
         long long ld;
+        int wide;                // rows 32-byte aligned
     };
     __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int rank, Acc<Layout>& acc) {
         const int row = (t.m * kPair + rank) * gemm::kRows + (warp & 3) * 32 + lane, half = warp >> 2;
@@ -344,13 +345,18 @@ struct Head {
             tc::tmem_load32(from + c, r);
             tc::tmem_load_wait();
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
+            for (int i = 0; i < 32; i += 16) {
                 if (row >= a.rows || n0 + c + i >= a.K) break;
-                uint32_t v[4];
+                uint32_t v[8];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < 8; ++j)
                     v[j] = rows::Elem<T>::pack2(__uint_as_float(r[i + 2 * j]) * scale, __uint_as_float(r[i + 2 * j + 1]) * scale);
-                __stcg(reinterpret_cast<uint4*>(out + c + i), make_uint4(v[0], v[1], v[2], v[3]));
+                if (a.wide) {   // (then K is a multiple of 16)
+                    store32(out + c + i, v);
+                } else {
+                    __stcg(reinterpret_cast<uint4*>(out + c + i), make_uint4(v[0], v[1], v[2], v[3]));
+                    if (n0 + c + i + 8 < a.K) __stcg(reinterpret_cast<uint4*>(out + c + i + 8), make_uint4(v[4], v[5], v[6], v[7]));
+                }
             }
             __syncwarp();
         }
@@ -544,6 +550,7 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
             b.wmax = wmax;
             b.out = static_cast<T*>(c.dhead) + static_cast<size_t>(first) * c.ld_dhead;
             b.ld = c.ld_dhead;
+            b.wide = reinterpret_cast<uintptr_t>(c.dhead) % 32 == 0 && c.K % 16 == 0 && c.ld_dhead % 16 == 0;
             if ((e = gemm::launch<Head<T>>(map_a, map_b, b, stream)) != cudaSuccess) return e;
         }
     }

@@ -128,9 +128,9 @@ __device__ __forceinline__ void transpose32(float* v, int lane) {
 
 // Tokens along the rows of a tile, output features along its columns; W K-major for y, and
 // MN-major (its rows along the contraction) for dx.
-template <class TY, bool GRADIENT>
+template <class TY, bool GRADIENT, int TN>
 struct Product {
-    using Layout = gemm::Layout<1, 256, 1, false, GRADIENT, 16>;
+    using Layout = gemm::Layout<1, TN, 1, false, GRADIENT, TN / 16>;
     static constexpr int kFormat = 0;
     static constexpr bool kPerStep = true, kAKeep = true, kBKeep = true;
     struct Args {
@@ -212,9 +212,9 @@ cudaError_t quantize(const Fp8BlockArgs& f, int width, uint8_t* codes, int ldc, 
     return cudaGetLastError();
 }
 
-template <class TY, bool GRADIENT>
+template <class TY, bool GRADIENT, int TN>
 cudaError_t product(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, const float* scales, cudaStream_t s) {
-    using P = Product<TY, GRADIENT>;
+    using P = Product<TY, GRADIENT, TN>;
     using L = typename P::Layout;
     const int width = GRADIENT ? f.N : f.K, out = GRADIENT ? f.K : f.N, kb = ceil_div(f.K, kBlock);
     CUtensorMap map_a, map_b;
@@ -236,9 +236,19 @@ cudaError_t product(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, const 
     return gemm::launch<P>(map_a, map_b, a, s);
 }
 
+// Wide tiles read fewer operand bytes, narrow ones spread a small product over more SMs: by
+// rounds of tiles times the tile's time, 20 to 13 for the widths (measured on full rounds).
 template <class TY>
 cudaError_t run_many(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, const float* scales, cudaStream_t s) {
-    return f.gradient ? product<TY, true>(f, codes, ldc, scales, s) : product<TY, false>(f, codes, ldc, scales, s);
+    const int sms = sm_count(), out = f.gradient ? f.K : f.N;
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    const auto rounds = [&](int tn) {
+        const long long tiles = static_cast<long long>(ceil_div(f.M, gemm::kRows)) * ceil_div(out, tn);
+        return (tiles + sms - 1) / sms;
+    };
+    if (20 * rounds(256) <= 13 * rounds(128))
+        return f.gradient ? product<TY, true, 256>(f, codes, ldc, scales, s) : product<TY, false, 256>(f, codes, ldc, scales, s);
+    return f.gradient ? product<TY, true, 128>(f, codes, ldc, scales, s) : product<TY, false, 128>(f, codes, ldc, scales, s);
 }
 
 cudaError_t run(const Fp8BlockArgs& f, cudaStream_t s) {
