@@ -110,18 +110,61 @@ __device__ __forceinline__ void store_row(TY* out, const float* v, int valid) {
     }
 }
 
-// A warp's 32 x 32 values, lane r's v[c] to lane c's v[r]: five exchanges between lanes (and
-// values) that differ in one bit.
-__device__ __forceinline__ void transpose32(float* v, int lane) {
+// A warp's 32 x 32 words, lane r's v[c] to lane c's v[r]: five exchanges between lanes (and
+// words) that differ in one bit.
+__device__ __forceinline__ void transpose32(uint32_t* v, int lane) {
 #pragma unroll
     for (int b = 16; b > 0; b >>= 1) {
         const bool up = (lane & b) != 0;
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
             if (i & b) continue;
-            const float other = __shfl_xor_sync(0xFFFFFFFFu, up ? v[i] : v[i | b], b);
+            const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, up ? v[i] : v[i | b], b);
             if (up) v[i] = other;
             else v[i | b] = other;
+        }
+    }
+}
+
+// How rows of results lie: whole 32-byte pieces, whole 32-bit words, or at any address.
+enum RowAlign { kAny, kWords, kPieces };
+
+// A warp's results, 64 columns of 32 rows (lane = row; `rows` of them wanted, `valid` columns),
+// to the row-major y of its first row. Rows in whole 32-byte pieces: each lane its own. Others:
+// transposed, so that the lanes store neighbouring words (or, at odd addresses of 16-bit types,
+// elements).
+template <class TY>
+__device__ __forceinline__ void store64(TY* y, long long ldy, const float (&v)[64], int rows_, int valid, int align, int lane) {
+    if (align == kPieces) {
+        if (lane < rows_) {
+#pragma unroll
+            for (int c = 0; c < 64; c += 32) store_row<TY>(y + lane * ldy + c, v + c, valid - c);
+        }
+    } else if (sizeof(TY) == 2 && align == kWords) {
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if constexpr (sizeof(TY) == 2) w[i] = rows::Elem<TY>::pack2(v[2 * i], v[2 * i + 1]);
+        transpose32(w, lane);
+        y += 2 * lane;
+        const int left = valid - 2 * lane;
+#pragma unroll
+        for (int i = 0; i < 32; ++i, y += ldy) {
+            if (i < rows_ && left > 1) *reinterpret_cast<uint32_t*>(y) = w[i];
+            else if (i < rows_ && left > 0) *reinterpret_cast<uint16_t*>(y) = static_cast<uint16_t>(w[i]);
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[c + i]);
+            transpose32(w, lane);
+            TY* out = y + c + lane;
+            const int left = valid - c - lane > 0 ? rows_ : 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i, out += ldy)
+                if (i < left) *out = rows::Elem<TY>::store(__uint_as_float(w[i]));
         }
     }
 }
@@ -141,11 +184,11 @@ struct Product {
         int M, N;             // tokens, output features
         TY* y;
         long long ldy;
-        int vec;              // rows 32-byte aligned
+        int align;            // RowAlign of y
     };
     __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int rank, Acc<Layout>& acc) {
         constexpr int kPart = Layout::kPart;
-        static_assert(kBlock % kPart == 0 && Layout::kP == 1, "a warp's columns lie in one block of the weight");
+        static_assert(kPart == 64 && Layout::kP == 1, "a warp's columns lie in one block of the weight");
         const int row0 = t.m * gemm::kRows + (warp & 3) * 32, row = row0 + lane, steps = a.shape.steps;
         const int n0 = t.n * Layout::kTN + (warp >> 2) * kPart;
         const bool in = row < a.M;
@@ -178,23 +221,7 @@ struct Product {
             }
             acc.release();
         }
-        if (a.vec) {
-            if (in && n0 < a.N) {
-                TY* out = a.y + static_cast<size_t>(row) * a.ldy + n0;
-#pragma unroll
-                for (int c = 0; c < kPart; c += 32) store_row<TY>(out + c, sum + c, a.N - n0 - c);
-            }
-        } else {   // rows at any address: lanes along the columns
-#pragma unroll
-            for (int c = 0; c < kPart; c += 32) {
-                transpose32(sum + c, lane);
-                const int col = n0 + c + lane, left = col < a.N ? a.M - row0 : 0;
-                TY* out = a.y + static_cast<size_t>(row0) * a.ldy + col;
-#pragma unroll
-                for (int i = 0; i < 32; ++i, out += a.ldy)
-                    if (i < left) *out = rows::Elem<TY>::store(sum[c + i]);
-            }
-        }
+        if (n0 < a.N) store64<TY>(a.y + static_cast<size_t>(row0) * a.ldy + n0, a.ldy, sum, a.M - row0, a.N - n0, a.align, lane);
         __syncwarp();
         return true;
     }
@@ -223,7 +250,7 @@ cudaError_t product(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, const 
     if ((e = gemm::encode_operand<L, GRADIENT>(&map_b, f.q, out, width, f.K, L::kBRows)) != cudaSuccess) return e;
     typename P::Args a = {};
     const int steps = ceil_div(width, kBlock);
-    a.shape = gemm::whole_tiles(ceil_div(f.M, gemm::kRows * L::kP), ceil_div(out, L::kTN), steps, f.error);
+    a.shape = gemm::whole_tiles(ceil_div(f.M, gemm::kRows), ceil_div(out, L::kTN), steps, f.error);
     a.sx = scales;
     a.sw = f.scale;
     a.sw_j = GRADIENT ? 1 : kb;
@@ -232,12 +259,14 @@ cudaError_t product(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, const 
     a.N = out;
     a.y = static_cast<TY*>(f.y);
     a.ldy = f.ldy;
-    a.vec = (reinterpret_cast<uintptr_t>(f.y) & 31u) == 0 && (f.M == 1 || (f.ldy * static_cast<long long>(sizeof(TY))) % 32 == 0);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(f.y) | (f.M == 1 ? 0 : static_cast<uintptr_t>(f.ldy) * sizeof(TY));
+    a.align = at % 32 == 0 ? kPieces : at % 4 == 0 ? kWords : kAny;
     return gemm::launch<P>(map_a, map_b, a, s);
 }
 
-// Wide tiles read fewer operand bytes, narrow ones spread a small product over more SMs: by
-// rounds of tiles times the tile's time, 20 to 13 for the widths (measured on full rounds).
+// Wide tiles have twice the work between two hand-overs, narrow ones spread a small product over
+// more SMs: by rounds of tiles times a step's time, 0.43 us in a 256-wide tile, 0.38 in a
+// 128-wide one.
 template <class TY>
 cudaError_t run_many(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, const float* scales, cudaStream_t s) {
     const int sms = sm_count(), out = f.gradient ? f.K : f.N;
@@ -246,7 +275,7 @@ cudaError_t run_many(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, const
         const long long tiles = static_cast<long long>(ceil_div(f.M, gemm::kRows)) * ceil_div(out, tn);
         return (tiles + sms - 1) / sms;
     };
-    if (20 * rounds(256) <= 13 * rounds(128))
+    if (43 * rounds(256) <= 38 * rounds(128))
         return f.gradient ? product<TY, true, 256>(f, codes, ldc, scales, s) : product<TY, false, 256>(f, codes, ldc, scales, s);
     return f.gradient ? product<TY, true, 128>(f, codes, ldc, scales, s) : product<TY, false, 128>(f, codes, ldc, scales, s);
 }

@@ -5,7 +5,9 @@
 //
 // A tile is 128 P rows x TN columns, P the CTAs that share it. With a pair (P = 2) each CTA
 // loads its 128 rows of A and half of B: two thirds of the bytes that two single CTAs need
-// for the same 256 x TN, at 32 bytes of K per instruction. A stage is 128 bytes of K (64
+// for the same 256 x TN, at 32 bytes of K per instruction. Single CTAs are for
+// products with an accumulator per step of K, which would wait for a pair's hand-over between
+// its CTAs. A stage is 128 bytes of K (64
 // 16-bit elements, 128 FP8). An operand is K-major (its rows run along the contraction) or
 // MN-major (its rows run along M or N, one row per step of the contraction): both gradients
 // of a layer then read the matrices as they lie, without transposed copies.
@@ -75,13 +77,11 @@ __host__ __device__ inline int tile_index(int tiles_m, int tiles_n, int m, int n
     return g * kGroup * tiles_n + n * rows + m - g * kGroup;
 }
 
-template <int P, int TN, int ELEM, bool A_MN, bool B_MN, int EPI = 8, int GROUPS = 1>
+template <int P, int TN, int ELEM, bool A_MN, bool B_MN, int EPI = 8>
 struct Layout {
     static constexpr int kP = P, kTN = TN, kElem = ELEM;
     static constexpr int kEpiWarps = EPI, kProducer = EPI, kIssuer = EPI + 1, kThreads = 32 * (EPI + 2);
-    static constexpr int kGroups = GROUPS, kGN = TN / GROUPS;           // a tile's columns as accumulators of their own
-    static constexpr int kSet = EPI / GROUPS;                           // epilogue warps of a group
-    static constexpr int kPart = kGN / (kSet / 4);                      // columns of one
+    static constexpr int kPart = TN / (EPI / 4);                        // columns of an epilogue warp
     static constexpr bool kAMn = A_MN, kBMn = B_MN;
     static constexpr int kK = kStageBytes / ELEM;                       // elements of K per stage
     static constexpr int kSpan = 128 / ELEM;                            // elements of an MN-major box's rows
@@ -90,12 +90,9 @@ struct Layout {
     static constexpr int kBytes = kABytes + kBBytes;
     static constexpr int kStages = (227 * 1024 - 1024 - 1024) / kBytes < 8 ? (227 * 1024 - 1024 - 1024) / kBytes : 8;
     static constexpr int kSmem = kStages * kBytes + 1024;
-    static constexpr int kBuffers = 512 / kGN < 4 ? 512 / kGN : 4;      // accumulators in tensor memory
-    // a group's first column of B in a stage: its rows of 128 bytes, or (MN-major) its bytes of them
-    // (or whole boxes)
-    static constexpr int kGroupStep = (!B_MN ? (kGN / P) * kStageBytes : kGN / P >= kSpan ? kGN / P / kSpan * kK * 128 : kGN / P * ELEM) / 16;
+    static constexpr int kBuffers = 512 / TN < 4 ? 512 / TN : 4;        // accumulators in tensor memory
     static_assert(!(A_MN && kRows % kSpan != 0) && !(B_MN && kBRows % kSpan != 0), "whole boxes");
-    static_assert(kBytes % 1024 == 0 && TN % (32 * GROUPS) == 0 && kStages >= 3, "stage layout");
+    static_assert(kBytes % 1024 == 0 && TN % 32 == 0 && kStages >= 3, "stage layout");
 };
 
 struct Sync {
@@ -172,27 +169,27 @@ template <class L>
 struct Acc {
     Sync& sy;
     const Shape& shape;
-    uint32_t tmem, n;   // n: accumulators in the issuer's order; a set's are its group's
-    __device__ Acc(Sync& s, const Shape& sh, uint32_t t, int warp) : sy(s), shape(sh), tmem(t), n(warp / L::kSet) {}
+    uint32_t tmem, n = 0;
+    __device__ Acc(Sync& s, const Shape& sh, uint32_t t) : sy(s), shape(sh), tmem(t) {}
     // Waits for the next accumulator: its first column, or ~0 if the wait gave up.
     __device__ __forceinline__ uint32_t next() {
         const uint32_t b = n % L::kBuffers;
         const bool ok = wait_or_abort(sy, &sy.acc_full[b], (n / L::kBuffers) & 1, shape);
         if (!__all_sync(0xFFFFFFFFu, ok)) return ~0u;
         tc::fence_after_sync();
-        return tmem + b * L::kGN;
+        return tmem + b * L::kTN;
     }
     // This warp has read the accumulator (all of its loads waited for).
     __device__ __forceinline__ void release() {
         tc::fence_before_sync();
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(&sy.acc_empty[n % L::kBuffers]);
-        n += L::kGroups;
+        ++n;
     }
 };
 
 // Op: Layout, Args (with `Shape shape`), kFormat (idesc_f), kPerStep (an accumulator per step of
-// K and group of columns, for results that are scaled step by step; else one per tile), kAKeep / kBKeep (the operand is
+// K, for results that are scaled step by step; else one per tile), kAKeep / kBKeep (the operand is
 // read by other tiles too: kept in L2), and tile(args, tile, warp, lane, rank, acc), false when a
 // wait gave up.
 template <class Op>
@@ -214,7 +211,7 @@ __global__ void __launch_bounds__(Op::Layout::kThreads, 1) product_kernel(const 
         }
         for (int i = 0; i < L::kBuffers; ++i) {
             mbar_init(&sy.acc_full[i], 1);
-            mbar_init(&sy.acc_empty[i], L::kSet + (rank == 0 ? P - 1 : 0));   // rank 0: rank 1's forwarder too
+            mbar_init(&sy.acc_empty[i], L::kEpiWarps + (rank == 0 ? P - 1 : 0));   // rank 0: rank 1's forwarder too
         }
         mbar_init(&sy.issued, 1);
         mbar_init_fence();
@@ -261,13 +258,14 @@ __global__ void __launch_bounds__(Op::Layout::kThreads, 1) product_kernel(const 
                 }
             }
         }
-        // The copies in flight land before the CTAs end, whoever gave up: a pair's complete on
-        // rank 0's barriers; rank 1 waits for the last signals to its own (both bounded).
-        for (uint32_t b = it > static_cast<uint32_t>(kStages) ? it - kStages : 0; b < it; ++b)
-            if (!mbar_wait(rank == 0 ? &sy.full[b % kStages] : &sy.empty[b % kStages], (b / kStages) & 1, kDrainRounds)) break;
+        // The copies in flight land, and the last signals of other CTAs, before the CTAs end,
+        // whoever gave up (a pair's copies complete on rank 0's barriers; all bounded).
+        for (uint32_t b = it > static_cast<uint32_t>(kStages) ? it - kStages : 0; b < it; ++b) {
+            if (rank == 0 && !mbar_wait(&sy.full[b % kStages], (b / kStages) & 1, kDrainRounds)) break;
+            if (P > 1 && !mbar_wait(&sy.empty[b % kStages], (b / kStages) & 1, kDrainRounds)) break;
+        }
     } else if (warp == L::kIssuer && rank == 0 && s.idle != kRoleIssuer) {
-        constexpr uint32_t kIdesc = tc::idesc_f(Op::kFormat, L::kAMn, L::kBMn, kRows * P, L::kGN);
-        static_assert(Op::kPerStep || L::kGroups == 1, "one accumulator per tile");
+        constexpr uint32_t kIdesc = tc::idesc_f(Op::kFormat, L::kAMn, L::kBMn, kRows * P, L::kTN);
         constexpr bool kF8 = L::kElem == 1;
         // 32 bytes of K: along a 128-byte row, or (MN-major) as many whole rows as elements
         constexpr uint32_t kStepA = L::kAMn ? 32 / L::kElem * 128 / 16 : 2, kStepB = L::kBMn ? 32 / L::kElem * 128 / 16 : 2;
@@ -286,22 +284,18 @@ __global__ void __launch_bounds__(Op::Layout::kThreads, 1) product_kernel(const 
                 if (!Op::kPerStep && k == 0 && !(ok = accumulator())) break;
                 if (!(ok = __all_sync(~0u, wait_or_abort(sy, &sy.full[st], phase, s)))) break;
                 const uint64_t da = first_a + st * (L::kBytes / 16), db = first_b + st * (L::kBytes / 16);
+                if (Op::kPerStep && !(ok = accumulator())) break;
+                tc::fence_after_sync();
+                const uint32_t b = n % L::kBuffers, d = tmem + b * L::kTN;
+                const bool last = Op::kPerStep || k == steps - 1;
+                if (elect_one()) {
 #pragma unroll
-                for (int g = 0; g < L::kGroups; ++g) {
-                    if (Op::kPerStep && !(ok = accumulator())) break;
-                    tc::fence_after_sync();
-                    const uint32_t b = n % L::kBuffers, d = tmem + b * L::kGN;
-                    const bool last = Op::kPerStep || k == steps - 1;
-                    if (elect_one()) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            tc::mma_f<P, kF8>(d, da + kStepA * j, db + L::kGroupStep * g + kStepB * j, kIdesc, (!Op::kPerStep && k > 0) || j > 0);
-                        if (last) tc::commit_all<P>(&sy.acc_full[b]);
-                        if (g == L::kGroups - 1) tc::commit_all<P>(&sy.empty[st]);
-                    }
-                    __syncwarp();
-                    if (last) ++n;
+                    for (int j = 0; j < 4; ++j) tc::mma_f<P, kF8>(d, da + kStepA * j, db + kStepB * j, kIdesc, (!Op::kPerStep && k > 0) || j > 0);
+                    if (last) tc::commit_all<P>(&sy.acc_full[b]);
+                    tc::commit_all<P>(&sy.empty[st]);
                 }
+                __syncwarp();
+                if (last) ++n;
                 if (++st == static_cast<uint32_t>(kStages)) {
                     st = 0;
                     phase ^= 1u;
@@ -318,10 +312,10 @@ __global__ void __launch_bounds__(Op::Layout::kThreads, 1) product_kernel(const 
         uint32_t n = 0;
         bool ok = true;
         for (int i = first; ok && i < tiles; i += stride)
-            for (int u = Op::kPerStep ? tile_at(s, i).steps * L::kGroups : 1; ok && u > 0; --u, ++n)
+            for (int u = Op::kPerStep ? tile_at(s, i).steps : 1; ok && u > 0; --u, ++n)
                 if ((ok = wait_or_abort(sy, &sy.acc_empty[n % L::kBuffers], (n / L::kBuffers) & 1, s))) arrive_rank0(&sy.acc_empty[n % L::kBuffers]);
     } else if (warp < L::kEpiWarps && s.idle != kRoleEpilogue) {
-        Acc<L> acc(sy, s, tmem, warp);
+        Acc<L> acc(sy, s, tmem);
         for (int i = first; i < tiles; i += stride)
             if (!Op::tile(a, tile_at(s, i), warp, lane, rank, acc)) break;
     }
