@@ -490,10 +490,11 @@ typedef struct dh_fp8_blocks {
 int fp8_quantize_blocks(const void *W, int V, int K, const int32_t *idx, int N, uint8_t *q, float *scale, void *ws, size_t ws_bytes,
                         void *stream);
 
-/* Bytes of workspace of the two products below for M tokens of `width` features (K for
- * fp8_block_matmul, N for the gradient): the quantised activations (0 for an unsupported
- * shape). */
-size_t fp8_block_matmul_workspace_bytes(int M, int width);
+/* Bytes of workspace of the two products below for M tokens of `width` features with `out`
+ * results each (K and N for fp8_block_matmul, N and K for the gradient): the quantised
+ * activations, and the sums of the contraction's parts where it is split (0 for an
+ * unsupported shape). */
+size_t fp8_block_matmul_workspace_bytes(int M, int width, int out);
 
 /* y = x W'^T with the activations quantised per token and block of 128 features, inside
  * the call, by the same recipe (IEEE divisions, fp32):

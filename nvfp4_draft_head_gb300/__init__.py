@@ -172,7 +172,7 @@ def lib():
         L.draft_head_cross_entropy.argtypes = [C.POINTER(dh_cross_entropy_t), P, P, P, P, C.c_int64, P, C.c_int64, P, S, P, P]
         L.draft_head_cross_entropy_backward.argtypes = [C.POINTER(dh_cross_entropy_t), P, P, P, C.c_int64, P, C.c_int64, P, S, P, P]
         L.fp8_quantize_blocks.argtypes = [P, I, I, P, I, P, P, P, S, P]
-        L.fp8_block_matmul_workspace_bytes.argtypes = [I, I]
+        L.fp8_block_matmul_workspace_bytes.argtypes = [I, I, I]
         L.fp8_block_matmul_workspace_bytes.restype = S
         for fn in (L.fp8_block_matmul, L.fp8_block_matmul_input_gradient):
             fn.argtypes = [C.POINTER(dh_fp8_blocks_t), P, I, C.c_int64, I, P, I, C.c_int64, P, S, P, P]
@@ -782,7 +782,7 @@ class FP8BlockMatmul:
         if M == 0:
             return y
         L = lib()
-        nb = L.fp8_block_matmul_workspace_bytes(M, width)
+        nb = L.fp8_block_matmul_workspace_bytes(M, width, out)
         if nb == 0:
             raise DraftHeadError(name, DH_ERR_SHAPE)
         s = _stream_of(x)

@@ -185,16 +185,18 @@ struct Product {
         TY* y;
         long long ldy;
         int align;            // RowAlign of y
+        float* parts;         // the contraction in parts: their sums, [split][M][ldp]
+        long long ldp;
     };
     __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int rank, Acc<Layout>& acc) {
         constexpr int kPart = Layout::kPart;
         static_assert(kPart == 64 && Layout::kP == 1, "a warp's columns lie in one block of the weight");
-        const int row0 = t.m * gemm::kRows + (warp & 3) * 32, row = row0 + lane, steps = a.shape.steps;
+        const int row0 = t.m * gemm::kRows + (warp & 3) * 32, row = row0 + lane, steps = t.steps;
         const int n0 = t.n * Layout::kTN + (warp >> 2) * kPart;
         const bool in = row < a.M;
         // (columns beyond N: any scale)
-        const float* sw = a.sw + static_cast<size_t>(n0 < a.N ? n0 / kBlock : 0) * a.sw_j;
-        const float* sx = a.sx + (in ? row : 0);
+        const float* sw = a.sw + static_cast<size_t>(n0 < a.N ? n0 / kBlock : 0) * a.sw_j + static_cast<size_t>(t.k0) * a.sw_b;
+        const float* sx = a.sx + static_cast<size_t>(t.k0) * a.M + (in ? row : 0);
         float sum[kPart];
 #pragma unroll
         for (int i = 0; i < kPart; ++i) sum[i] = 0.0f;
@@ -221,13 +223,62 @@ struct Product {
             }
             acc.release();
         }
-        if (n0 < a.N) store64<TY>(a.y + static_cast<size_t>(row0) * a.ldy + n0, a.ldy, sum, a.M - row0, a.N - n0, a.align, lane);
+        if (n0 < a.N && a.parts != nullptr)
+            store64<float>(a.parts + (static_cast<size_t>(t.split) * a.M + row0) * a.ldp + n0, a.ldp, sum, a.M - row0, a.N - n0, kPieces, lane);
+        else if (n0 < a.N) store64<TY>(a.y + static_cast<size_t>(row0) * a.ldy + n0, a.ldy, sum, a.M - row0, a.N - n0, a.align, lane);
         __syncwarp();
         return true;
     }
 };
 
+// y from the sums of the parts, in order.
+template <class TY>
+__global__ void __launch_bounds__(256) sum_kernel(const float* __restrict__ parts, int splits, int M, int N, long long ldp, TY* __restrict__ y,
+                                                  long long ldy) {
+    const unsigned n = blockIdx.x * 256 + threadIdx.x, m = blockIdx.y;
+    if (n >= static_cast<unsigned>(N)) return;
+    const float* p = parts + static_cast<size_t>(m) * ldp + n;
+    float v = *p;
+#pragma unroll 4
+    for (int s = 1; s < splits; ++s) v += p[static_cast<size_t>(s) * M * ldp];
+    y[static_cast<size_t>(m) * ldy + n] = rows::Elem<TY>::store(v);
+}
+
 // ------------------------------------------------------------------- host ----
+
+// How a product of many tokens runs: the width of its tiles, and the parts of its contraction
+// where the tiles alone would leave SMs idle.
+struct Plan {
+    int tn, parts, part_steps;
+    float us;
+};
+
+// By rounds of tiles over the 152 SMs times a step's time (0.43 us in a 256-wide tile, 0.38 in a
+// 128-wide one: wide tiles have twice the work between two hand-overs, narrow ones spread a small
+// product over more SMs), or by reading the weight. Parts cost a second kernel. Measured, us: 200
+// tokens, gradient of 64,026 x 2,560 193 in one part; 512 x 4,608 x 2,560 15.0 wide, 13.3 narrow.
+Plan plan_of(int M, int out, int width) {
+    constexpr int kSms = 152;
+    const int steps = ceil_div(width, kBlock);
+    Plan best = {256, 1, steps, 0.0f};
+    for (int tn = 256; tn >= 128; tn /= 2) {
+        const long long tiles = static_cast<long long>(ceil_div(M, gemm::kRows)) * ceil_div(out, tn);
+        for (int p = 1; p <= 16 && (p == 1 || (p * tiles <= kSms && steps / p >= 4)); ++p) {
+            const int part = ceil_div(steps, p);
+            const float us = static_cast<float>((tiles * p + kSms - 1) / kSms) * (part * (tn == 256 ? 0.43f : 0.38f) + 1.5f) +
+                             (p > 1 ? 3.0f + p * static_cast<float>(M) * out * 1.0e-6f : 0.0f);
+            if ((tn == 256 && p == 1) || us < best.us) best = {tn, ceil_div(steps, part), part, us};
+        }
+    }
+    const float read = static_cast<float>(width) * out * (1.0f / 4.4e6f);
+    if (best.us < read) best.us = read;
+    return best;
+}
+long long part_stride(int out) { return (out + 7) / 8 * 8; }
+size_t parts_bytes(int M, int out, int width) {
+    const Plan p = plan_of(M, out, width);
+    return p.parts > 1 ? static_cast<size_t>(p.parts) * M * part_stride(out) * sizeof(float) : 0;
+}
 
 template <class T>
 cudaError_t quantize(const Fp8BlockArgs& f, int width, uint8_t* codes, int ldc, float* scales, cudaStream_t s) {
@@ -240,7 +291,7 @@ cudaError_t quantize(const Fp8BlockArgs& f, int width, uint8_t* codes, int ldc, 
 }
 
 template <class TY, bool GRADIENT, int TN>
-cudaError_t product(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, const float* scales, cudaStream_t s) {
+cudaError_t product(const Fp8BlockArgs& f, const Plan& plan, const uint8_t* codes, int ldc, const float* scales, float* parts, cudaStream_t s) {
     using P = Product<TY, GRADIENT, TN>;
     using L = typename P::Layout;
     const int width = GRADIENT ? f.N : f.K, out = GRADIENT ? f.K : f.N, kb = ceil_div(f.K, kBlock);
@@ -261,46 +312,52 @@ cudaError_t product(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, const 
     a.ldy = f.ldy;
     const uintptr_t at = reinterpret_cast<uintptr_t>(f.y) | (f.M == 1 ? 0 : static_cast<uintptr_t>(f.ldy) * sizeof(TY));
     a.align = at % 32 == 0 ? kPieces : at % 4 == 0 ? kWords : kAny;
-    return gemm::launch<P>(map_a, map_b, a, s);
+    if (plan.parts == 1) return gemm::launch<P>(map_a, map_b, a, s);
+    a.shape.whole = 0;
+    a.shape.splits = plan.parts;
+    a.shape.split_steps = plan.part_steps;
+    a.parts = parts;
+    a.ldp = part_stride(out);
+    if ((e = gemm::launch<P>(map_a, map_b, a, s)) != cudaSuccess) return e;
+    const dim3 grid(static_cast<unsigned>(ceil_div(out, 256)), static_cast<unsigned>(f.M));
+    sum_kernel<TY><<<grid, 256, 0, s>>>(parts, plan.parts, f.M, out, a.ldp, a.y, a.ldy);
+    return cudaGetLastError();
 }
 
-// Wide tiles have twice the work between two hand-overs, narrow ones spread a small product over
-// more SMs: by rounds of tiles times a step's time, 0.43 us in a 256-wide tile, 0.38 in a
-// 128-wide one.
 template <class TY>
-cudaError_t run_many(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, const float* scales, cudaStream_t s) {
-    const int sms = sm_count(), out = f.gradient ? f.K : f.N;
-    if (sms <= 0) return cudaErrorInvalidDevice;
-    const auto rounds = [&](int tn) {
-        const long long tiles = static_cast<long long>(ceil_div(f.M, gemm::kRows)) * ceil_div(out, tn);
-        return (tiles + sms - 1) / sms;
-    };
-    if (43 * rounds(256) <= 38 * rounds(128))
-        return f.gradient ? product<TY, true, 256>(f, codes, ldc, scales, s) : product<TY, false, 256>(f, codes, ldc, scales, s);
-    return f.gradient ? product<TY, true, 128>(f, codes, ldc, scales, s) : product<TY, false, 128>(f, codes, ldc, scales, s);
+cudaError_t run_many(const Fp8BlockArgs& f, const Plan& p, const uint8_t* codes, int ldc, const float* scales, float* parts, cudaStream_t s) {
+    if (p.tn == 256)
+        return f.gradient ? product<TY, true, 256>(f, p, codes, ldc, scales, parts, s) : product<TY, false, 256>(f, p, codes, ldc, scales, parts, s);
+    return f.gradient ? product<TY, true, 128>(f, p, codes, ldc, scales, parts, s) : product<TY, false, 128>(f, p, codes, ldc, scales, parts, s);
 }
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 cudaError_t run(const Fp8BlockArgs& f, cudaStream_t s) {
-    const bool few = few_supported(f);
+    float few_us = 0.0f;
+    const bool few = few_supported(f, &few_us);
     if (few && f.M <= kFusedTokens) return launch_few(f, nullptr, 0, nullptr, s);
-    const int width = f.gradient ? f.N : f.K, ldc = ceil_div(width, 16) * 16;
+    const int width = f.gradient ? f.N : f.K, out = f.gradient ? f.K : f.N, ldc = ceil_div(width, 16) * 16;
     uint8_t* codes = static_cast<uint8_t*>(f.ws);
-    float* scales = reinterpret_cast<float*>(codes + (static_cast<size_t>(f.M) * ldc + 255) / 256 * 256);
+    float* scales = reinterpret_cast<float*>(codes + up256(static_cast<size_t>(f.M) * ldc));
+    float* parts = reinterpret_cast<float*>(codes + up256(static_cast<size_t>(f.M) * ldc) +
+                                            up256(static_cast<size_t>(f.M) * ceil_div(width, kBlock) * sizeof(float)));
     const cudaError_t e = f.x_type == DH_T_BF16  ? quantize<__nv_bfloat16>(f, width, codes, ldc, scales, s)
                           : f.x_type == DH_T_F16 ? quantize<__half>(f, width, codes, ldc, scales, s)
                                                  : quantize<float>(f, width, codes, ldc, scales, s);
     if (e != cudaSuccess) return e;
-    if (few) return launch_few(f, codes, ldc, scales, s);
-    return f.y_type == DH_T_BF16  ? run_many<__nv_bfloat16>(f, codes, ldc, scales, s)
-           : f.y_type == DH_T_F16 ? run_many<__half>(f, codes, ldc, scales, s)
-                                  : run_many<float>(f, codes, ldc, scales, s);
+    const Plan p = plan_of(f.M, out, width);
+    if (few && few_us <= p.us) return launch_few(f, codes, ldc, scales, s);
+    return f.y_type == DH_T_BF16  ? run_many<__nv_bfloat16>(f, p, codes, ldc, scales, parts, s)
+           : f.y_type == DH_T_F16 ? run_many<__half>(f, p, codes, ldc, scales, parts, s)
+                                  : run_many<float>(f, p, codes, ldc, scales, parts, s);
 }
 
 }  // namespace f8
 
-size_t fp8_block_workspace_bytes(int M, int width) {
-    const size_t codes = (static_cast<size_t>(M) * (f8::ceil_div(width, 16) * 16) + 255) / 256 * 256;
-    return codes + (static_cast<size_t>(M) * f8::ceil_div(width, f8::kBlock) * sizeof(float) + 255) / 256 * 256;
+size_t fp8_block_workspace_bytes(int M, int width, int out) {
+    return f8::up256(static_cast<size_t>(M) * (f8::ceil_div(width, 16) * 16)) +
+           f8::up256(static_cast<size_t>(M) * f8::ceil_div(width, f8::kBlock) * sizeof(float)) + f8::up256(f8::parts_bytes(M, out, width));
 }
 
 cudaError_t launch_fp8_quantize_blocks(const uint16_t* W, int V, int K, const int32_t* idx, int N, uint8_t* q, float* scale, Workspace* ws,

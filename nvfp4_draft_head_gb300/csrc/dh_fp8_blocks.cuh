@@ -56,7 +56,9 @@ inline bool rows_aligned16(const void* x, long long ld_bytes, int rows) {
 
 // Products of up to kFewTokens tokens (dh_fp8_few.cu); scales null: x is quantised in the kernel.
 constexpr int kFewTokens = 128, kFusedTokens = 16;
-bool few_supported(const Fp8BlockArgs& f);
+// Whether that form can take a product (its share of the steps fits a CTA), and about how long
+// it would be.
+bool few_supported(const Fp8BlockArgs& f, float* us);
 cudaError_t launch_few(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, const float* scales, cudaStream_t s);
 
 }  // namespace f8

@@ -19,8 +19,10 @@ constexpr int kMaxN = 1 << 24, kMaxK = 1 << 20, kMaxM = 1 << 24;
 
 bool weight_ok(int N, int K) { return N >= 1 && N <= kMaxN && K >= 16 && K <= kMaxK && K % 16 == 0; }
 
-bool tokens_ok(int M, int width) {
-    return M >= 1 && M <= kMaxM && width >= 1 && width <= kMaxN && static_cast<int64_t>(M) * ((width + 127) / 128) < (1ll << 31);
+bool tokens_ok(int M, int width, int out) {
+    return M >= 1 && M <= kMaxM && width >= 1 && width <= kMaxN && out >= 1 && out <= kMaxN &&
+           static_cast<int64_t>(M) * ((width + 127) / 128) < (1ll << 31) &&
+           ((static_cast<int64_t>(M) + 127) / 128) * ((out + 127) / 128) <= (1 << 30);
 }
 
 int product(const dh_fp8_blocks_t* w, bool gradient, const void* x, int x_type, int64_t ldx, int M, void* y, int y_type, int64_t ldy,
@@ -29,12 +31,12 @@ int product(const dh_fp8_blocks_t* w, bool gradient, const void* x, int x_type, 
     if (type_bytes(x_type) == 0 || type_bytes(y_type) == 0) return DH_ERR_ARG;
     if (!weight_ok(w->N, w->K)) return DH_ERR_SHAPE;
     const int width = gradient ? w->N : w->K, out = gradient ? w->K : w->N;
-    if (!tokens_ok(M, width) || ((static_cast<int64_t>(M) + 127) / 128) * ((out + 127) / 128) > (1 << 30)) return DH_ERR_SHAPE;
+    if (!tokens_ok(M, width, out)) return DH_ERR_SHAPE;
     if (M > 1 && (ldx < width || ldy < out)) return DH_ERR_SHAPE;
     if (!aligned(w->q, 16) || !aligned(w->scale, 4) || !aligned(x, type_bytes(x_type)) || !aligned(y, type_bytes(y_type)) || !aligned(error, 4))
         return DH_ERR_ALIGN;
     if (ws == nullptr) return DH_ERR_ARG;
-    if (!aligned(ws, DH_WORKSPACE_ALIGN) || ws_bytes < dh::fp8_block_workspace_bytes(M, width)) return DH_ERR_WORKSPACE;
+    if (!aligned(ws, DH_WORKSPACE_ALIGN) || ws_bytes < dh::fp8_block_workspace_bytes(M, width, out)) return DH_ERR_WORKSPACE;
     dh::Fp8BlockArgs a = {};
     a.q = static_cast<const uint8_t*>(w->q);
     a.scale = w->scale;
@@ -67,7 +69,9 @@ int fp8_quantize_blocks(const void* W, int V, int K, const int32_t* idx, int N, 
                                                       static_cast<cudaStream_t>(stream)));
 }
 
-size_t fp8_block_matmul_workspace_bytes(int M, int width) { return tokens_ok(M, width) ? dh::fp8_block_workspace_bytes(M, width) : 0; }
+size_t fp8_block_matmul_workspace_bytes(int M, int width, int out) {
+    return tokens_ok(M, width, out) ? dh::fp8_block_workspace_bytes(M, width, out) : 0;
+}
 
 int fp8_block_matmul(const dh_fp8_blocks_t* w, const void* x, int x_type, int64_t ldx, int M, void* y, int y_type, int64_t ldy, void* ws,
                      size_t ws_bytes, unsigned int* error, void* stream) {

@@ -62,10 +62,9 @@ struct Few {
     static constexpr int kPart = NT / 2;                                 // tokens of an epilogue warp
     static constexpr int kStage = kABytes + (FUSED ? 0 : NT * kBlock);
     static constexpr int kCols = kBuffers * NT < 32 ? 32 : kBuffers * NT;
-    static constexpr int kExchange = NT * kBlock * 4;
     // Shared memory besides the stages for CTAs of `per` steps in clusters of `splits`.
     __host__ __device__ static constexpr int rest(int per, int splits) {
-        return (FUSED ? per * NT * kBlock : 0) + (per * NT * 4 + 1023) / 1024 * 1024 + (splits > 1 ? kExchange : 0);
+        return (FUSED ? per * NT * kBlock : 0) + (per * NT * 4 + 1023) / 1024 * 1024 + (splits > 1 ? splits * ((NT + splits - 1) / splits) * kBlock * 4 : 0);
     }
 };
 
@@ -89,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     const int b0 = rank * a.per, count = min(a.per, a.steps - b0);
     uint8_t* codes = smem + a.stages * F::kStage;                        // FUSED: [count][NT][128]
     float* scales = reinterpret_cast<float*>(codes + (FUSED ? a.per * NT * kBlock : 0));   // [count][NT]
-    float* exchange = scales + (a.per * NT * 4 + 1023) / 1024 * 256;     // [rank][NT / splits][128]
+    float* exchange = scales + (a.per * NT * 4 + 1023) / 1024 * 256;     // [rank][ceil(NT / splits)][128]
     const uint32_t stages = static_cast<uint32_t>(a.stages);
     if (threadIdx.x == 0) {
         for (int i = 0; i < a.stages; ++i) {
@@ -247,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             }
             // token m to rank m % splits; what the others sent last has been read everywhere first
             if (e > 0 && !__all_sync(~0u, wait_cluster(sy, &sy.room, (e - 1) & 1, a))) break;
-            const int slots = NT / splits;
+            const int slots = (NT + splits - 1) / splits;
 #pragma unroll
             for (int i = 0; i < F::kPart; ++i) {
                 const int m = part * F::kPart + i;
@@ -280,20 +279,49 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
 
 // ------------------------------------------------------------------- host ----
 
-// CTAs per cluster for `tiles` tiles of `steps` steps: the fewest steps in a row over all
-// rounds, a tile's end counted as four steps; 0 where a CTA's share does not fit its shared memory.
+// Clusters of `size` CTAs of this memory that the device runs at once (clusters do not span its
+// graphics processing clusters: 152, 76, 46, 36, 28, 23, 15, 15 for 1 to 8).
+int clusters_of(int size) {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices][kMaxSplits + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 0;
+    int n = known[dev][size].load(std::memory_order_acquire);
+    if (n > 0) return n;
+    const auto kernel = few_kernel<float, float, 32, false, false>;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(static_cast<unsigned>(size));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSpace + 1024;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(size);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSpace + 1024) != cudaSuccess) return 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) return 0;
+    known[dev][size].store(n, std::memory_order_release);
+    return n;
+}
+
+// CTAs per cluster for `tiles` tiles of `steps` steps, by the time that a product would take:
+// rounds of tiles times a step's time (0.40 us; 0.60 where 128 tokens' sums are what takes it)
+// and a tile's end, which an exchange makes longer by the tokens. 0 where a CTA's share does not
+// fit its shared memory. Measured, us: 24 tokens x 4,608 x 2,560 9.2, 64 12, 128 16 (4 CTAs
+// each); 32 x 64,026 x 2,560 36 (1).
 template <int NT, bool FUSED>
-int choose_splits(int tiles, int steps, int sms) {
+int choose_splits(int tiles, int steps, float* us) {
     using F = Few<NT, FUSED>;
     int best = 0;
-    long long least = 0;
-    for (int s = 1; s <= kMaxSplits; s *= 2) {
-        const int per = ceil_div(steps, s);
-        if ((s - 1) * per >= steps || F::rest(per, s) + 3 * F::kStage > kSpace) continue;
-        const long long cost = static_cast<long long>(ceil_div(tiles, sms / s)) * (per + 4);
-        if (best == 0 || cost < least) {
+    for (int s = 1; s <= kMaxSplits; ++s) {
+        const int per = ceil_div(steps, s), clusters = clusters_of(s);
+        if (clusters == 0 || (s - 1) * per >= steps || F::rest(per, s) + 3 * F::kStage > kSpace) continue;
+        const float end = s == 1 ? 0.6f : 1.5f + 0.06f * NT;
+        const float cost = ceil_div(tiles, clusters) * (per * (NT < 128 ? 0.40f : 0.60f) + end);
+        if (best == 0 || cost < *us) {
             best = s;
-            least = cost;
+            *us = cost;
         }
     }
     return best;
@@ -316,7 +344,7 @@ cudaError_t launch_kernel(const CUtensorMap& map_w, const CUtensorMap& map_x, Fe
     const int fit = (kSpace - F::rest(a.per, splits)) / F::kStage;
     a.stages = fit < 16 ? fit : 16;
     a.rounds = kWaitLimit / gemm::kWaitSlices;
-    const int clusters = sm_count() / splits, want = a.tiles < clusters ? a.tiles : clusters;
+    const int clusters = clusters_of(splits), want = a.tiles < clusters ? a.tiles : clusters;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(want * splits));
     cfg.blockDim = dim3(kThreads);
@@ -350,7 +378,8 @@ cudaError_t launch_sized(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, c
     a.y = f.y;
     a.ldy = f.ldy;
     a.error = f.error;
-    const int splits = choose_splits<NT, FUSED>(a.tiles, a.steps, sm_count());
+    float us;
+    const int splits = choose_splits<NT, FUSED>(a.tiles, a.steps, &us);
     if (splits == 0) return cudaErrorInvalidValue;
     a.per = ceil_div(a.steps, splits);
     CUtensorMap map_w, map_x;
@@ -375,14 +404,13 @@ cudaError_t launch_typed(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, c
     return launch_sized<float, TY, 128, false>(f, codes, ldc, scales, s);
 }
 
-// Whether a product runs here: few tokens, and each CTA's share of the steps fits its memory.
-bool few_supported(const Fp8BlockArgs& f) {
-    const int out = f.gradient ? f.K : f.N, tiles = ceil_div(out, kBlock), steps = ceil_div(f.gradient ? f.N : f.K, kBlock), sms = sm_count();
-    if (f.M > kFewTokens || sms < kMaxSplits) return false;
-    return (f.M <= 16   ? choose_splits<16, true>(tiles, steps, sms)
-            : f.M <= 32 ? choose_splits<32, false>(tiles, steps, sms)
-            : f.M <= 64 ? choose_splits<64, false>(tiles, steps, sms)
-                        : choose_splits<128, false>(tiles, steps, sms)) != 0;
+bool few_supported(const Fp8BlockArgs& f, float* us) {
+    const int tiles = ceil_div(f.gradient ? f.K : f.N, kBlock), steps = ceil_div(f.gradient ? f.N : f.K, kBlock);
+    if (f.M > kFewTokens) return false;
+    return (f.M <= 16   ? choose_splits<16, true>(tiles, steps, us)
+            : f.M <= 32 ? choose_splits<32, false>(tiles, steps, us)
+            : f.M <= 64 ? choose_splits<64, false>(tiles, steps, us)
+                        : choose_splits<128, false>(tiles, steps, us)) != 0;
 }
 
 cudaError_t launch_few(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, const float* scales, cudaStream_t s) {

@@ -274,17 +274,15 @@ __global__ void __launch_bounds__(Op::Layout::kThreads, 1) product_kernel(const 
         const uint64_t first_b = L::kBMn ? tc::desc_operand_mn(base + L::kABytes, L::kK) : tc::desc_operand(base + L::kABytes);
         uint32_t n = 0, st = 0, phase = 0;
         bool ok = true;
-        const auto accumulator = [&] {   // the next accumulator has been read
-            const uint32_t use = n / L::kBuffers;
-            return use == 0 || __all_sync(~0u, wait_or_abort(sy, &sy.acc_empty[n % L::kBuffers], (use - 1) & 1, s));
-        };
         for (int i = first; ok && i < tiles; i += stride) {
             const int steps = tile_at(s, i).steps;
-            for (int k = 0; ok && k < steps; ++k) {
-                if (!Op::kPerStep && k == 0 && !(ok = accumulator())) break;
-                if (!(ok = __all_sync(~0u, wait_or_abort(sy, &sy.full[st], phase, s)))) break;
+            for (int k = 0; k < steps; ++k) {
+                const uint32_t use = n / L::kBuffers;
+                ok = wait_or_abort(sy, &sy.full[st], phase, s);   // the operands have landed,
+                if ((Op::kPerStep || k == 0) && use > 0)           // and the accumulator has been read
+                    ok = ok && wait_or_abort(sy, &sy.acc_empty[n % L::kBuffers], (use - 1) & 1, s);
+                if (!(ok = __all_sync(~0u, ok))) break;
                 const uint64_t da = first_a + st * (L::kBytes / 16), db = first_b + st * (L::kBytes / 16);
-                if (Op::kPerStep && !(ok = accumulator())) break;
                 tc::fence_after_sync();
                 const uint32_t b = n % L::kBuffers, d = tmem + b * L::kTN;
                 const bool last = Op::kPerStep || k == steps - 1;

@@ -200,7 +200,7 @@ struct Fp8BlockArgs {
     void* ws;
     unsigned int* error;     // device error word or null
 };
-size_t fp8_block_workspace_bytes(int M, int width);
+size_t fp8_block_workspace_bytes(int M, int width, int out);
 cudaError_t launch_fp8_quantize_blocks(const uint16_t* W, int V, int K, const int32_t* idx, int N, uint8_t* q, float* scale, Workspace* ws,
                                        cudaStream_t s);
 cudaError_t launch_fp8_blocks(const Fp8BlockArgs& f, cudaStream_t s);
