@@ -735,6 +735,9 @@ class FP8BlockMatmul:
         self.error = torch.zeros(1, dtype=torch.int32, device=q.device)
         self.desc = dh_fp8_blocks_t(self.N, self.K, q.data_ptr(), scale.data_ptr())
         self.desc_ref, self.error_ptr = C.byref(self.desc), self.error.data_ptr()
+        # what stands in for the workspace of a product that uses none
+        self._none = _workspace(DH_WORKSPACE_ALIGN, q.device)
+        self._bytes = {}    # (tokens, input width) -> bytes of workspace
 
     @classmethod
     def from_weight(cls, W: torch.Tensor, idx: torch.Tensor | None = None, stream=None) -> "FP8BlockMatmul":
@@ -768,27 +771,35 @@ class FP8BlockMatmul:
         return self._product("fp8_block_matmul_input_gradient", dy, dx, out_dtype, self.N, self.K)
 
     def _product(self, name, x, y, out_dtype, width, out):
-        if x.dim() != 2 or x.shape[1] != width or x.dtype not in _TYPES or x.device != self.q.device or \
-                (x.stride(1) != 1 and width > 1) or (x.shape[0] > 1 and x.stride(0) < width):
-            raise ValueError(f"the input must be a [M, {width}] bfloat16, float16 or float32 tensor with contiguous rows on {self.q.device}")
-        M = x.shape[0]
+        q, t = self.q, _TYPES.get(x.dtype)
+        shape, device = x.shape, q.device
+        M = shape[0] if len(shape) == 2 else -1
+        if M < 0 or shape[1] != width or t is None or x.device != device:
+            raise ValueError(f"the input must be a [M, {width}] bfloat16, float16 or float32 tensor on {device}")
+        ldx, step = x.stride()
+        if (step != 1 and width > 1) or (M > 1 and ldx < width):
+            raise ValueError("the input's rows must be contiguous and must not overlap")
         if y is None:
             if out_dtype not in _TYPES:
                 raise ValueError("out_dtype must be bfloat16, float16 or float32")
-            y = torch.empty((M, out), dtype=out_dtype, device=x.device)
-        elif y.shape != (M, out) or y.dtype not in _TYPES or y.device != x.device or (y.stride(1) != 1 and out > 1) or \
-                (M > 1 and y.stride(0) < out):
-            raise ValueError(f"the result must be a [{M}, {out}] bfloat16, float16 or float32 tensor with contiguous rows")
+            y, ldy = torch.empty((M, out), dtype=out_dtype, device=device), out
+        else:
+            if y.shape != (M, out) or y.dtype not in _TYPES or y.device != device or (y.stride(1) != 1 and out > 1) or \
+                    (M > 1 and y.stride(0) < out):
+                raise ValueError(f"the result must be a [{M}, {out}] bfloat16, float16 or float32 tensor with contiguous rows on {device}")
+            out_dtype, ldy = y.dtype, y.stride(0)
         if M == 0:
             return y
-        L = lib()
-        nb = L.fp8_block_matmul_workspace_bytes(M, width, out)
-        if nb == 0:
-            raise DraftHeadError(name, DH_ERR_SHAPE)
-        s = _stream_of(x)
-        ws = torch.empty(nb, dtype=torch.uint8, device=x.device)
-        _check(name, getattr(L, name)(self.desc_ref, x.data_ptr(), _TYPES[x.dtype], x.stride(0), M, y.data_ptr(), _TYPES[y.dtype],
-                                      y.stride(0), ws.data_ptr(), nb, self.error_ptr, s))
+        L, s = lib(), _stream_of(x)
+        nb = self._bytes.get((M, width))
+        if nb is None:
+            nb = self._bytes[M, width] = L.fp8_block_matmul_workspace_bytes(M, width, out)
+            if nb == 0:
+                raise DraftHeadError(name, DH_ERR_SHAPE)
+        ws = self._none if nb == DH_WORKSPACE_ALIGN else torch.empty(nb, dtype=torch.uint8, device=device)
+        st = getattr(L, name)(self.desc_ref, x.data_ptr(), t, ldx, M, y.data_ptr(), _TYPES[out_dtype], ldy, ws.data_ptr(), nb, self.error_ptr, s)
+        if st != DH_OK:
+            raise DraftHeadError(name, st)
         return y
 
     def device_error(self) -> int:

@@ -334,10 +334,10 @@ cudaError_t run_many(const Fp8BlockArgs& f, const Plan& p, const uint8_t* codes,
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 cudaError_t run(const Fp8BlockArgs& f, cudaStream_t s) {
-    float few_us = 0.0f;
-    const bool few = few_supported(f, &few_us);
-    if (few && f.M <= kFusedTokens) return launch_few(f, nullptr, 0, nullptr, s);
     const int width = f.gradient ? f.N : f.K, out = f.gradient ? f.K : f.N, ldc = ceil_div(width, 16) * 16;
+    if (f.M <= kFusedTokens && fused_fits(ceil_div(width, kBlock))) return launch_few(f, nullptr, 0, nullptr, s);
+    float few_us = 0.0f;
+    const bool few = f.M > kFusedTokens && few_supported(f, &few_us);
     uint8_t* codes = static_cast<uint8_t*>(f.ws);
     float* scales = reinterpret_cast<float*>(codes + up256(static_cast<size_t>(f.M) * ldc));
     float* parts = reinterpret_cast<float*>(codes + up256(static_cast<size_t>(f.M) * ldc) +
@@ -356,6 +356,7 @@ cudaError_t run(const Fp8BlockArgs& f, cudaStream_t s) {
 }  // namespace f8
 
 size_t fp8_block_workspace_bytes(int M, int width, int out) {
+    if (M <= f8::kFusedTokens && f8::fused_fits(f8::ceil_div(width, f8::kBlock))) return DH_WORKSPACE_ALIGN;   // not used
     return f8::up256(static_cast<size_t>(M) * (f8::ceil_div(width, 16) * 16)) +
            f8::up256(static_cast<size_t>(M) * f8::ceil_div(width, f8::kBlock) * sizeof(float)) + f8::up256(f8::parts_bytes(M, out, width));
 }

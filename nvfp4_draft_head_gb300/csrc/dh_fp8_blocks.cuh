@@ -59,6 +59,9 @@ constexpr int kFewTokens = 128, kFusedTokens = 16;
 // Whether that form can take a product (its share of the steps fits a CTA), and about how long
 // it would be.
 bool few_supported(const Fp8BlockArgs& f, float* us);
+// Whether its fused form can take a product of this many steps, by the sizes alone: such a product
+// needs no workspace.
+bool fused_fits(int steps);
 cudaError_t launch_few(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, const float* scales, cudaStream_t s);
 
 }  // namespace f8

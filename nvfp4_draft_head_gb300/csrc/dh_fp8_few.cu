@@ -327,6 +327,15 @@ int choose_splits(int tiles, int steps, float* us) {
     return best;
 }
 
+bool fused_fits(int steps) {
+    using F = Few<16, true>;
+    for (int s = 1; s <= kMaxSplits; ++s) {
+        const int per = ceil_div(steps, s);
+        if ((s - 1) * per < steps && F::rest(per, s) + 3 * F::kStage <= kSpace) return true;
+    }
+    return false;
+}
+
 template <class TX, class TY, int NT, bool FUSED, bool GRADIENT>
 cudaError_t launch_kernel(const CUtensorMap& map_w, const CUtensorMap& map_x, FewArgs a, int splits, cudaStream_t stream) {
     using F = Few<NT, FUSED>;
@@ -407,8 +416,7 @@ cudaError_t launch_typed(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, c
 bool few_supported(const Fp8BlockArgs& f, float* us) {
     const int tiles = ceil_div(f.gradient ? f.K : f.N, kBlock), steps = ceil_div(f.gradient ? f.N : f.K, kBlock);
     if (f.M > kFewTokens) return false;
-    return (f.M <= 16   ? choose_splits<16, true>(tiles, steps, us)
-            : f.M <= 32 ? choose_splits<32, false>(tiles, steps, us)
+    return (f.M <= 32   ? choose_splits<32, false>(tiles, steps, us)
             : f.M <= 64 ? choose_splits<64, false>(tiles, steps, us)
                         : choose_splits<128, false>(tiles, steps, us)) != 0;
 }
