@@ -353,4 +353,13 @@ __device__ __forceinline__ void named_bar_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
 }
 
+// For a kernel launched with programmatic stream serialisation: waits until the kernel before
+// it on the stream has completed and its writes are visible; only then may the next one
+// start, so that a kernel's start says that everything before its predecessor is done. Before
+// it, such a kernel touches no global memory.
+__device__ __forceinline__ void programmatic_wait() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+}
+
 }  // namespace dh

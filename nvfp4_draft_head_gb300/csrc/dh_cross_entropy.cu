@@ -160,6 +160,7 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Tokens tok, const float2* __restrict__ part, int parts,
                                                             const float* __restrict__ target, float* __restrict__ loss,
                                                             float* __restrict__ lse, float* __restrict__ rest, const Rows rows) {
+    programmatic_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, token = threadIdx.x % kJoinTokens, t = blockIdx.x * kJoinTokens + token;
     float m = kNegInf, s = 0.0f;
     if (t < tok.T) {
@@ -198,6 +199,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Tokens tok, co
 
 // The rows' work where there is no loss to join.
 __global__ void __launch_bounds__(128) rows_kernel(const Tokens tok, const Rows rows) {
+    programmatic_wait();
     const int t = blockIdx.x;
     const float w = tok.w(t);
     const bool live = w != 0.0f && tok.row(t) >= 0;
@@ -375,6 +377,7 @@ struct Sums {
 template <class T>
 __global__ void __launch_bounds__(256) sum_kernel(const Tokens tok, const Sums a, int K, const uint32_t* __restrict__ wmax,
                                                   T* __restrict__ out, long long ld) {
+    programmatic_wait();
     const float scale = exp2i(-scale_exponent<std::is_same<T, __half>::value>(*wmax));
     const unsigned per_row = K / 8;
     const size_t total = static_cast<size_t>(tok.T) * per_row;
@@ -488,9 +491,9 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
         if ((e = gemm::launch<Stats<T>>(map_h, map_w, a, stream)) != cudaSuccess) return e;
         float* l = c.lse != nullptr ? c.lse : reinterpret_cast<float*>(ws + sp.lse);
         float* r = c.rest != nullptr ? c.rest : reinterpret_cast<float*>(ws + sp.rest);
-        join_kernel<<<ceil_div(c.T, kJoinTokens), kJoinThreads, 0, stream>>>(tok, a.part, 2 * a.shape.tiles_n, a.target, c.loss, l, r,
-                                                                              dh || dw ? rows : Rows{});
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        e = gemm::launch_early(join_kernel, dim3(static_cast<unsigned>(ceil_div(c.T, kJoinTokens))), kJoinThreads, 0, 1, stream, tok, a.part,
+                               2 * a.shape.tiles_n, a.target, c.loss, l, r, dh || dw ? rows : Rows{});
+        if (e != cudaSuccess) return e;
         lse = l;
         rest = r;
     }
@@ -498,8 +501,7 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
 
     if (!loss) {
         if ((e = cudaMemsetAsync(wmax, 0, 4, stream)) != cudaSuccess) return e;
-        rows_kernel<<<c.T, 128, 0, stream>>>(tok, rows);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = gemm::launch_early(rows_kernel, dim3(static_cast<unsigned>(c.T)), 128, 0, 1, stream, tok, rows)) != cudaSuccess) return e;
     }
     const int piece = piece_rows(c.T, c.N);
     const gemm::Shape tiles_h = hidden_tiles(c.T, c.K, piece, c.error);   // of a full piece
@@ -556,10 +558,10 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
     }
     if (dh) {
         const size_t total = static_cast<size_t>(c.T) * (c.K / 8), want = (total + 255) / 256, cap = static_cast<size_t>(sm_count()) * 8;
-        sum_kernel<T><<<static_cast<unsigned>(want < cap ? want : cap), 256, 0, stream>>>(
-            tok, Sums{sum, reinterpret_cast<float*>(ws + sp.parts), tiles_h.tiles_m, tiles_h.tiles_n, tiles_h.whole, splits}, c.K, wmax, static_cast<T*>(c.dhidden),
-                                                                                      c.ld_dhidden);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        const Sums sums = {sum, reinterpret_cast<float*>(ws + sp.parts), tiles_h.tiles_m, tiles_h.tiles_n, tiles_h.whole, splits};
+        e = gemm::launch_early(sum_kernel<T>, dim3(static_cast<unsigned>(want < cap ? want : cap)), 256, 0, 1, stream, tok, sums, c.K, wmax,
+                               static_cast<T*>(c.dhidden), c.ld_dhidden);
+        if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }

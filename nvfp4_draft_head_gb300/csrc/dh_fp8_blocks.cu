@@ -25,6 +25,7 @@ constexpr int kQThreads = 256;
 template <class T, bool VEC>
 __global__ void __launch_bounds__(kQThreads) quantize_kernel(const T* __restrict__ x, long long ldx, int M, int width,
                                                              uint8_t* __restrict__ codes, int ldc, float* __restrict__ scales) {
+    programmatic_wait();
     const unsigned per_row = static_cast<unsigned>(ceil_div(width, kBlock));
     const unsigned unit = blockIdx.x * (kQThreads / 8) + (threadIdx.x >> 3);   // < 2^31 (checked)
     const unsigned m = unit / per_row, b = unit - m * per_row;
@@ -235,6 +236,7 @@ struct Product {
 template <class TY>
 __global__ void __launch_bounds__(256) sum_kernel(const float* __restrict__ parts, int splits, int M, int N, long long ldp, TY* __restrict__ y,
                                                   long long ldy) {
+    programmatic_wait();
     const unsigned n = blockIdx.x * 256 + threadIdx.x, m = blockIdx.y;
     if (n >= static_cast<unsigned>(N)) return;
     const float* p = parts + static_cast<size_t>(m) * ldp + n;
@@ -285,9 +287,8 @@ cudaError_t quantize(const Fp8BlockArgs& f, int width, uint8_t* codes, int ldc, 
     const bool vec = rows_aligned16(f.x, f.ldx * static_cast<long long>(sizeof(T)), f.M);
     const unsigned units = static_cast<unsigned>(f.M) * static_cast<unsigned>(ceil_div(width, kBlock));
     const unsigned grid = (units + kQThreads / 8 - 1) / (kQThreads / 8);
-    if (vec) quantize_kernel<T, true><<<grid, kQThreads, 0, s>>>(static_cast<const T*>(f.x), f.ldx, f.M, width, codes, ldc, scales);
-    else quantize_kernel<T, false><<<grid, kQThreads, 0, s>>>(static_cast<const T*>(f.x), f.ldx, f.M, width, codes, ldc, scales);
-    return cudaGetLastError();
+    return gemm::launch_early(vec ? quantize_kernel<T, true> : quantize_kernel<T, false>, dim3(grid), kQThreads, 0, 1, s,
+                              static_cast<const T*>(f.x), f.ldx, f.M, width, codes, ldc, scales);
 }
 
 template <class TY, bool GRADIENT, int TN>
@@ -319,9 +320,8 @@ cudaError_t product(const Fp8BlockArgs& f, const Plan& plan, const uint8_t* code
     a.parts = parts;
     a.ldp = part_stride(out);
     if ((e = gemm::launch<P>(map_a, map_b, a, s)) != cudaSuccess) return e;
-    const dim3 grid(static_cast<unsigned>(ceil_div(out, 256)), static_cast<unsigned>(f.M));
-    sum_kernel<TY><<<grid, 256, 0, s>>>(parts, plan.parts, f.M, out, a.ldp, a.y, a.ldy);
-    return cudaGetLastError();
+    const dim3 grid(static_cast<unsigned>(ceil_div(out, 256)), static_cast<unsigned>(f.M));   // (parts: M is below 152 x 128)
+    return gemm::launch_early(sum_kernel<TY>, grid, 256, 0, 1, s, parts, plan.parts, f.M, out, a.ldp, a.y, a.ldy);
 }
 
 template <class TY>

@@ -110,11 +110,14 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     if (warp == kIssuer) tc::tmem_alloc(&sy.tmem, F::kCols);
     tc::fence_before_sync();
     __syncthreads();
+    // The other CTAs' barriers are ready before the first exchange: arrived here, waited for there
+    // (and by the producer and the issuer at their ends).
     if (splits > 1) {
         cluster_fence();
-        cluster_sync_all();
+        cluster_arrive();
     }
     tc::fence_after_sync();
+    programmatic_wait();
     const uint32_t tmem = sy.tmem;
 
     if (warp == kProducer) {
@@ -141,6 +144,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         // the copies in flight land before the CTA ends, whoever gave up (bounded)
         for (uint32_t b = it > stages ? it - stages : 0; b < it; ++b)
             if (!mbar_wait(&sy.full[b % stages], (b / stages) & 1, gemm::kDrainRounds)) break;
+        __syncwarp();
+        if (splits > 1) cluster_wait();
     } else if (warp == kIssuer) {
         constexpr uint32_t kIdesc = tc::idesc_f(0, GRADIENT, false, kBlock, NT), kStepA = GRADIENT ? 256 : 2;
         const uint32_t base = smem_u32(smem);
@@ -170,6 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         if (gemm::elect_one()) tc::commit(&sy.issued);
         __syncwarp();
         mbar_wait(&sy.issued, 0, gemm::kDrainRounds);
+        __syncwarp();
+        if (splits > 1) cluster_wait();
     } else {
         if (FUSED) {   // eight lanes per token and step
             const TX* x = static_cast<const TX*>(a.x);
@@ -195,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         named_bar_sync(1, 32 * kEpiWarps);   // the scales are there for every warp
         const int quarter = warp & 3, part = warp >> 2, local = quarter * 32 + lane;
         uint32_t n = 0, e = 0;
+        bool joined = splits == 1;   // the cluster's start has been waited for
         for (int t = first; t < a.tiles; t += stride, ++e) {
             const int row = t * kBlock + local;
             const float* sw = a.sw + static_cast<size_t>(t) * a.sw_j + static_cast<size_t>(b0) * a.sw_b;
@@ -244,6 +252,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                 __syncwarp();
                 continue;
             }
+            if (!joined) cluster_wait();
+            joined = true;
             // token m to rank m % splits; what the others sent last has been read everywhere first
             if (e > 0 && !__all_sync(~0u, wait_cluster(sy, &sy.room, (e - 1) & 1, a))) break;
             const int slots = (NT + splits - 1) / splits;
@@ -265,6 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             if (lane < splits) mbar_arrive_remote(cluster_map(&sy.room, lane));
             __syncwarp();
         }
+        if (!joined) cluster_wait();
     }
     __syncwarp();
     tc::fence_before_sync();
@@ -339,7 +350,7 @@ bool fused_fits(int steps) {
 template <class TX, class TY, int NT, bool FUSED, bool GRADIENT>
 cudaError_t launch_kernel(const CUtensorMap& map_w, const CUtensorMap& map_x, FewArgs a, int splits, cudaStream_t stream) {
     using F = Few<NT, FUSED>;
-    const auto kernel = few_kernel<TX, TY, NT, FUSED, GRADIENT>;
+    constexpr auto kernel = few_kernel<TX, TY, NT, FUSED, GRADIENT>;
     constexpr int kDevices = 64, kSmem = kSpace + 1024;
     static std::atomic<bool> known[kDevices];   // per device: the kernel's shared memory has been allowed
     int dev = 0;
@@ -354,18 +365,7 @@ cudaError_t launch_kernel(const CUtensorMap& map_w, const CUtensorMap& map_x, Fe
     a.stages = fit < 16 ? fit : 16;
     a.rounds = kWaitLimit / gemm::kWaitSlices;
     const int clusters = clusters_of(splits), want = a.tiles < clusters ? a.tiles : clusters;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(want * splits));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = splits > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, map_w, map_x, a);
+    return gemm::launch_early(kernel, dim3(static_cast<unsigned>(want * splits)), kThreads, kSmem, splits, stream, map_w, map_x, a);
 }
 
 template <class TX, class TY, int NT, bool FUSED>

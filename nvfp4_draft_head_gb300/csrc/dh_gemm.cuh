@@ -18,6 +18,8 @@
 #pragma once
 
 #include <atomic>
+#include <utility>
+
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -226,6 +228,7 @@ __global__ void __launch_bounds__(Op::Layout::kThreads, 1) product_kernel(const 
         cluster_sync_all();
     }
     tc::fence_after_sync();
+    programmatic_wait();
     const uint32_t tmem = sy.tmem;
     const int tiles = s.units();
     const int first = static_cast<int>(blockIdx.x) / P, stride = static_cast<int>(gridDim.x) / P;
@@ -330,6 +333,26 @@ __global__ void __launch_bounds__(Op::Layout::kThreads, 1) product_kernel(const 
 
 // ------------------------------------------------------------------- host ----
 
+// Launches in clusters of `ctas`, allowed to start (up to its programmatic_wait) while the kernel
+// before it on the stream finishes.
+template <class... Params, class... Given>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, int smem, int ctas, cudaStream_t stream, Given&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Given>(args)...);
+}
+
 inline Shape whole_tiles(int tiles_m, int tiles_n, int steps, unsigned int* error) {
     Shape s = {};
     s.tiles_m = tiles_m;
@@ -374,18 +397,8 @@ cudaError_t launch(const CUtensorMap& map_a, const CUtensorMap& map_b, typename 
     }
     const long long tiles = a.shape.units();
     const long long most = sms / L::kP;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((tiles < most ? tiles : most) * L::kP));
-    cfg.blockDim = dim3(L::kThreads);
-    cfg.dynamicSmemBytes = L::kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = L::kP;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = L::kP > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, product_kernel<Op>, map_a, map_b, a);
+    return launch_early(product_kernel<Op>, dim3(static_cast<unsigned>((tiles < most ? tiles : most) * L::kP)), L::kThreads, L::kSmem, L::kP, stream,
+                        map_a, map_b, a);
 }
 
 }  // namespace gemm
