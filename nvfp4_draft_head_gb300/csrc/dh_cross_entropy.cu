@@ -71,9 +71,9 @@ __device__ __forceinline__ int scale_exponent(uint32_t wmax) {
 
 // ---------------------------------------------------------------- the loss ----
 
-template <class T>
+template <class T, int P>
 struct Stats {
-    using Layout = gemm::Layout<kPair, kTN, 2, false, false>;
+    using Layout = gemm::Layout<P, kTN, 2, false, false>;
     static constexpr int kFormat = std::is_same<T, __half>::value ? 0 : 1;
     static constexpr bool kPerStep = false, kAKeep = true, kBKeep = true;
     struct Args {
@@ -84,7 +84,7 @@ struct Stats {
         uint32_t* wmax; // cleared for what follows
     };
     __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int rank, Acc<Layout>& acc) {
-        const int row = (t.m * kPair + rank) * gemm::kRows + (warp & 3) * 32 + lane, half = warp >> 2;
+        const int row = (t.m * P + rank) * gemm::kRows + (warp & 3) * 32 + lane, half = warp >> 2;
         const int n0 = t.n * kTN + half * kHalf;
         const int y = row < a.tok.T ? a.tok.row(row) : -1;
         if (row == 0 && n0 == 0) *a.wmax = 0u;
@@ -207,9 +207,9 @@ __global__ void __launch_bounds__(128) rows_kernel(const Tokens tok, const Rows 
     if (rows.copy != nullptr) rows.move(t, live, threadIdx.x, blockDim.x);
 }
 
-template <class T>
+template <class T, int P>
 struct Weights {   // g of a piece
-    using Layout = gemm::Layout<kPair, kTN, 2, false, false>;
+    using Layout = gemm::Layout<P, kTN, 2, false, false>;
     static constexpr bool kF16 = std::is_same<T, __half>::value;
     static constexpr int kFormat = kF16 ? 0 : 1;
     static constexpr bool kPerStep = false, kAKeep = true, kBKeep = true;
@@ -224,7 +224,7 @@ struct Weights {   // g of a piece
         int first, count;       // the piece's rows of the head
     };
     __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int rank, Acc<Layout>& acc) {
-        const int row = (t.m * kPair + rank) * gemm::kRows + (warp & 3) * 32 + lane, half = warp >> 2;
+        const int row = (t.m * P + rank) * gemm::kRows + (warp & 3) * 32 + lane, half = warp >> 2;
         const int c0 = t.n * kTN + half * kHalf;   // in the piece
         int y = -1;
         float w = 0.0f, lse = 0.0f, rest = 0.0f;
@@ -463,32 +463,34 @@ Space space_of(int T, int N, int K, bool loss, bool dh, bool dw) {
     return s;
 }
 
-template <class T>
+// P: CTAs of a tile of the logits (their products read the head and are bound by that for few
+// tokens).
+template <class T, int P>
 cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
     const bool loss = c.loss != nullptr, dh = c.dhidden != nullptr, dw = c.dhead != nullptr;
     const Space sp = space_of(c.T, c.N, c.K, loss, dh, dw);
     uint8_t* ws = static_cast<uint8_t*>(c.ws);
     Tokens tok = {c.tokens, c.row_of, c.weight, c.V, c.T, c.N};
     uint32_t* wmax = reinterpret_cast<uint32_t*>(ws + sp.wmax);
-    const int tiles_m = ceil_div(c.T, kTM);
+    const int tiles_m = ceil_div(c.T, gemm::kRows * P);
     T* hidden = dw ? reinterpret_cast<T*>(ws + sp.hidden) : nullptr;
     const Rows rows = {c.hidden, c.ld_hidden, c.K, hidden, wmax};
     cudaError_t e;
     CUtensorMap map_h, map_w;
-    using K1 = typename Stats<T>::Layout;
+    using K1 = typename Stats<T, P>::Layout;
     if ((e = gemm::encode_operand<K1, false>(&map_h, c.hidden, c.T, c.K, c.ld_hidden * 2, gemm::kRows)) != cudaSuccess) return e;
     if ((e = gemm::encode_operand<K1, false>(&map_w, c.head, c.N, c.K, c.ld_head * 2, K1::kBRows)) != cudaSuccess) return e;
     const int steps = ceil_div(c.K, K1::kK);
     const float* lse = c.lse_in;
     const float* rest = c.rest_in;
     if (loss) {
-        typename Stats<T>::Args a = {};
+        typename Stats<T, P>::Args a = {};
         a.shape = gemm::whole_tiles(tiles_m, ceil_div(c.N, kTN), steps, c.error);
         a.tok = tok;
         a.part = reinterpret_cast<float2*>(ws + sp.part);
         a.target = reinterpret_cast<float*>(ws + sp.target);
         a.wmax = wmax;
-        if ((e = gemm::launch<Stats<T>>(map_h, map_w, a, stream)) != cudaSuccess) return e;
+        if ((e = gemm::launch<Stats<T, P>>(map_h, map_w, a, stream)) != cudaSuccess) return e;
         float* l = c.lse != nullptr ? c.lse : reinterpret_cast<float*>(ws + sp.lse);
         float* r = c.rest != nullptr ? c.rest : reinterpret_cast<float*>(ws + sp.rest);
         e = gemm::launch_early(join_kernel, dim3(static_cast<unsigned>(ceil_div(c.T, kJoinTokens))), kJoinThreads, 0, 1, stream, tok, a.part,
@@ -510,7 +512,7 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
     int splits = 1;   // of dh's split tiles: those of the first piece, which is the largest
     for (int first = 0; first < c.N; first += piece) {
         const int count = c.N - first < piece ? c.N - first : piece;
-        typename Weights<T>::Args a = {};
+        typename Weights<T, P>::Args a = {};
         a.shape = gemm::whole_tiles(tiles_m, ceil_div(count, kTN), steps, c.error);
         a.shape.b_mn = first;
         a.tok = tok;
@@ -521,7 +523,7 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
         a.ldg = piece;
         a.first = first;
         a.count = count;
-        if ((e = gemm::launch<Weights<T>>(map_h, map_w, a, stream)) != cudaSuccess) return e;
+        if ((e = gemm::launch<Weights<T, P>>(map_h, map_w, a, stream)) != cudaSuccess) return e;
         CUtensorMap map_a, map_b;
         if (dh) {
             using L = typename Hidden<T>::Layout;
@@ -566,6 +568,12 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
     return cudaSuccess;
 }
 
+// One CTA per tile of the logits for tokens that fill no pair's 256 rows, a pair otherwise.
+template <class T>
+cudaError_t run_typed(const CrossEntropyArgs& c, cudaStream_t stream) {
+    return c.T <= gemm::kRows ? run<T, 1>(c, stream) : run<T, 2>(c, stream);
+}
+
 }  // namespace ce
 
 size_t cross_entropy_workspace_bytes(int T, int N, int K, bool loss, bool dhidden, bool dhead) {
@@ -573,7 +581,7 @@ size_t cross_entropy_workspace_bytes(int T, int N, int K, bool loss, bool dhidde
 }
 
 cudaError_t launch_cross_entropy(const CrossEntropyArgs& a, cudaStream_t s) {
-    return a.type == DH_T_F16 ? ce::run<__half>(a, s) : ce::run<__nv_bfloat16>(a, s);
+    return a.type == DH_T_F16 ? ce::run_typed<__half>(a, s) : ce::run_typed<__nv_bfloat16>(a, s);
 }
 
 }  // namespace dh
