@@ -71,11 +71,39 @@ __device__ __forceinline__ int scale_exponent(uint32_t wmax) {
 
 // ---------------------------------------------------------------- the loss ----
 
+// The tensor cores' 32-bit sums are truncated, not rounded, as they grow: over the 160
+// instructions of 2,560 features a large logit loses 2e-6 of itself, four times what a product
+// in 32 bits is off by. So they sum 512 features at a time, which the epilogue adds up, rounded
+// (the loss of 4,095 x 64,026: off by 1.8e-6 -> see the top of the file).
+constexpr int kLogitChunk = 8;
+
+// A thread's 128 logits of one row.
+template <class L>
+__device__ __forceinline__ bool sum_logits(Acc<L>& acc, int steps, uint32_t offset, float (&z)[kHalf]) {
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i) z[i] = 0.0f;
+#pragma unroll 1
+    for (int k = 0; k < steps; k += kLogitChunk) {
+        const uint32_t at = acc.next();
+        if (at == ~0u) return false;
+#pragma unroll
+        for (int c = 0; c < kHalf; c += 16) {
+            uint32_t r[16];
+            tc::tmem_load16(at + offset + c, r);
+            tc::tmem_load_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) z[c + i] += __uint_as_float(r[i]);
+        }
+        acc.release();
+    }
+    return true;
+}
+
 template <class T, int P>
 struct Stats {
     using Layout = gemm::Layout<P, kTN, 2, false, false>;
-    static constexpr int kFormat = std::is_same<T, __half>::value ? 0 : 1;
-    static constexpr bool kPerStep = false, kAKeep = true, kBKeep = true;
+    static constexpr int kFormat = std::is_same<T, __half>::value ? 0 : 1, kChunk = kLogitChunk;
+    static constexpr bool kAKeep = true, kBKeep = true;
     struct Args {
         gemm::Shape shape;
         Tokens tok;
@@ -85,46 +113,30 @@ struct Stats {
     };
     __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int rank, Acc<Layout>& acc) {
         const int row = (t.m * P + rank) * gemm::kRows + (warp & 3) * 32 + lane, half = warp >> 2;
-        const int n0 = t.n * kTN + half * kHalf;
-        const int y = row < a.tok.T ? a.tok.row(row) : -1;
+        const int n0 = t.n * kTN + half * kHalf, valid = a.tok.N - n0;
+        const int j = (row < a.tok.T ? a.tok.row(row) : -1) - n0;
         if (row == 0 && n0 == 0) *a.wmax = 0u;
-        const uint32_t at = acc.next();
-        if (at == ~0u) return false;
-        const uint32_t from = at + (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf;
-        float m = kNegInf, s = 0.0f;
-#pragma unroll 1
-        for (int c = 0; c < kHalf && n0 + c < a.tok.N; c += 32) {
-            uint32_t r[32];
-            tc::tmem_load32(from + c, r);
-            tc::tmem_load_wait();
-            const int valid = a.tok.N - (n0 + c);
-            if (valid < 32) {
+        float z[kHalf];
+        if (!sum_logits(acc, t.steps, (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf, z)) return false;
+        if (valid < kHalf) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) r[i] = i < valid ? r[i] : __float_as_uint(kNegInf);
-            }
-            float top[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top[i] = __uint_as_float(r[i]);
-#pragma unroll
-            for (int i = 4; i < 32; ++i) top[i & 3] = fmaxf(top[i & 3], __uint_as_float(r[i]));
-            const float next = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
-            const float ref = next == kNegInf ? 0.0f : next;   // nothing above -inf yet
-            float sum[4] = {s * exp2_approx((m - ref) * kLog2e), 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int i = 0; i < 32; ++i) sum[i & 3] += exp2_approx((__uint_as_float(r[i]) - ref) * kLog2e);
-            s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            m = next;
-            const int j = y - (n0 + c);
-            if (__any_sync(0xFFFFFFFFu, j >= 0 && j < 32)) {
-                float z = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) z = i == j ? __uint_as_float(r[i]) : z;
-                if (j >= 0 && j < 32) a.target[row] = z;
-                __syncwarp();
-            }
+            for (int i = 0; i < kHalf; ++i) z[i] = i < valid ? z[i] : kNegInf;
         }
-        acc.release();
-        if (row < a.tok.T) a.part[static_cast<size_t>(2 * t.n + half) * a.tok.T + row] = make_float2(m, s);
+        if (__any_sync(0xFFFFFFFFu, j >= 0 && j < kHalf)) {
+            float y = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kHalf; ++i) y = i == j ? z[i] : y;
+            if (j >= 0 && j < kHalf) a.target[row] = y;
+            __syncwarp();
+        }
+        float top[4] = {z[0], z[1], z[2], z[3]};
+#pragma unroll
+        for (int i = 4; i < kHalf; ++i) top[i & 3] = fmaxf(top[i & 3], z[i]);
+        const float m = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), kNegInf), ref = m == kNegInf ? 0.0f : m;
+        float sum[4] = {};
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i) sum[i & 3] += exp2_approx((z[i] - ref) * kLog2e);
+        if (row < a.tok.T) a.part[static_cast<size_t>(2 * t.n + half) * a.tok.T + row] = make_float2(m, (sum[0] + sum[1]) + (sum[2] + sum[3]));
         return true;
     }
 };
@@ -212,7 +224,8 @@ struct Weights {   // g of a piece
     using Layout = gemm::Layout<P, kTN, 2, false, false>;
     static constexpr bool kF16 = std::is_same<T, __half>::value;
     static constexpr int kFormat = kF16 ? 0 : 1;
-    static constexpr bool kPerStep = false, kAKeep = true, kBKeep = true;
+    static constexpr int kChunk = kLogitChunk;
+    static constexpr bool kAKeep = true, kBKeep = true;
     struct Args {
         gemm::Shape shape;
         Tokens tok;
@@ -236,34 +249,26 @@ struct Weights {   // g of a piece
         }
         const bool live = w != 0.0f;
         w = ldexpf(w, scale_exponent<kF16>(*a.wmax));
-        const uint32_t at = acc.next();
-        if (at == ~0u) return false;
-        const uint32_t from = at + (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf;
+        float z[kHalf];
+        if (!sum_logits(acc, t.steps, (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf, z)) return false;
+        const int j = y - (a.first + c0);
+        const bool hit = __any_sync(0xFFFFFFFFu, j >= 0 && j < kHalf);
         T* out = a.g + static_cast<size_t>(row) * a.ldg + c0;
-#pragma unroll 1
-        for (int c = 0; c < kHalf && c0 + c < a.count; c += 32) {
-            uint32_t r[32];
-            tc::tmem_load32(from + c, r);
-            tc::tmem_load_wait();
-            const int j = y - (a.first + c0 + c);
-            const bool hit = __any_sync(0xFFFFFFFFu, j >= 0 && j < 32);
-            float g[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) g[i] = exp2_approx(((__uint_as_float(r[i]) - lse) - rest) * kLog2e);
+        for (int c = 0; c < kHalf; c += 16) {
+            float g[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) g[i] = exp2_approx(((z[c + i] - lse) - rest) * kLog2e);
             if (hit) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) g[i] = i == j ? g[i] - 1.0f : g[i];
+                for (int i = 0; i < 16; ++i) g[i] = c + i == j ? g[i] - 1.0f : g[i];
             }
-            uint32_t v[16];
+            uint32_t v[8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = live ? rows::Elem<T>::pack2(g[2 * i] * w, g[2 * i + 1] * w) : 0u;
-            if (row < a.tok.T) {
-                store32(out + c, v);
-                store32(out + c + 16, v + 8);
-            }
-            __syncwarp();
+            for (int i = 0; i < 8; ++i) v[i] = live ? rows::Elem<T>::pack2(g[2 * i] * w, g[2 * i + 1] * w) : 0u;
+            if (row < a.tok.T && c0 + c < a.count) store32(out + c, v);
         }
-        acc.release();
+        __syncwarp();
         return true;
     }
 };
@@ -274,7 +279,8 @@ template <class T>
 struct Hidden {
     using Layout = gemm::Layout<kPair, kTN, 2, false, true>;
     static constexpr int kFormat = std::is_same<T, __half>::value ? 0 : 1;
-    static constexpr bool kPerStep = false, kAKeep = true, kBKeep = true;
+    static constexpr int kChunk = gemm::kWholeTile;
+    static constexpr bool kAKeep = true, kBKeep = true;
     struct Args {
         gemm::Shape shape;
         int T_, K;
@@ -324,7 +330,8 @@ struct Head {
     using Layout = gemm::Layout<kPair, kTN, 2, true, true>;
     static constexpr bool kF16 = std::is_same<T, __half>::value;
     static constexpr int kFormat = kF16 ? 0 : 1;
-    static constexpr bool kPerStep = false, kAKeep = true, kBKeep = true;
+    static constexpr int kChunk = gemm::kWholeTile;
+    static constexpr bool kAKeep = true, kBKeep = true;
     struct Args {
         gemm::Shape shape;
         int rows, K;             // head rows of the piece

@@ -176,7 +176,8 @@ template <class TY, bool GRADIENT, int TN>
 struct Product {
     using Layout = gemm::Layout<1, TN, 1, false, GRADIENT, TN / 16>;
     static constexpr int kFormat = 0;
-    static constexpr bool kPerStep = true, kAKeep = true, kBKeep = true;
+    static constexpr int kChunk = 1;
+    static constexpr bool kAKeep = true, kBKeep = true;
     struct Args {
         gemm::Shape shape;
         const float* sx;      // [steps][M]

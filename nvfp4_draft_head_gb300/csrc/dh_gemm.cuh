@@ -52,6 +52,8 @@ struct Shape {
     __host__ __device__ int units() const { return whole + (tiles() - whole) * splits; }
 };
 
+constexpr int kWholeTile = 1 << 30;
+
 enum Role { kRoleProducer, kRoleIssuer, kRoleEpilogue };
 
 // Tiles that are in work at the same time share operands in L2: groups of kGroup rows of
@@ -190,8 +192,9 @@ struct Acc {
     }
 };
 
-// Op: Layout, Args (with `Shape shape`), kFormat (idesc_f), kPerStep (an accumulator per step of
-// K, for results that are scaled step by step; else one per tile), kAKeep / kBKeep (the operand is
+// Op: Layout, Args (with `Shape shape`), kFormat (idesc_f), kChunk (steps of K that share an
+// accumulator: results that are scaled step by step take 1, those of a tile summed throughout by
+// the tensor cores kWholeTile), kAKeep / kBKeep (the operand is
 // read by other tiles too: kept in L2), and tile(args, tile, warp, lane, rank, acc), false when a
 // wait gave up.
 template <class Op>
@@ -282,16 +285,16 @@ __global__ void __launch_bounds__(Op::Layout::kThreads, 1) product_kernel(const 
             for (int k = 0; k < steps; ++k) {
                 const uint32_t use = n / L::kBuffers;
                 ok = wait_or_abort(sy, &sy.full[st], phase, s);   // the operands have landed,
-                if ((Op::kPerStep || k == 0) && use > 0)           // and the accumulator has been read
+                if (k % Op::kChunk == 0 && use > 0)                // and the accumulator has been read
                     ok = ok && wait_or_abort(sy, &sy.acc_empty[n % L::kBuffers], (use - 1) & 1, s);
                 if (!(ok = __all_sync(~0u, ok))) break;
                 const uint64_t da = first_a + st * (L::kBytes / 16), db = first_b + st * (L::kBytes / 16);
                 tc::fence_after_sync();
                 const uint32_t b = n % L::kBuffers, d = tmem + b * L::kTN;
-                const bool last = Op::kPerStep || k == steps - 1;
+                const bool last = (k + 1) % Op::kChunk == 0 || k == steps - 1;
                 if (elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) tc::mma_f<P, kF8>(d, da + kStepA * j, db + kStepB * j, kIdesc, (!Op::kPerStep && k > 0) || j > 0);
+                    for (int j = 0; j < 4; ++j) tc::mma_f<P, kF8>(d, da + kStepA * j, db + kStepB * j, kIdesc, k % Op::kChunk != 0 || j > 0);
                     if (last) tc::commit_all<P>(&sy.acc_full[b]);
                     tc::commit_all<P>(&sy.empty[st]);
                 }
@@ -313,7 +316,7 @@ __global__ void __launch_bounds__(Op::Layout::kThreads, 1) product_kernel(const 
         uint32_t n = 0;
         bool ok = true;
         for (int i = first; ok && i < tiles; i += stride)
-            for (int u = Op::kPerStep ? tile_at(s, i).steps : 1; ok && u > 0; --u, ++n)
+            for (int u = (tile_at(s, i).steps - 1) / Op::kChunk; ok && u >= 0; --u, ++n)
                 if ((ok = wait_or_abort(sy, &sy.acc_empty[n % L::kBuffers], (n / L::kBuffers) & 1, s))) arrive_rank0(&sy.acc_empty[n % L::kBuffers]);
     } else if (warp < L::kEpiWarps && s.idle != kRoleEpilogue) {
         Acc<L> acc(sy, s, tmem);
