@@ -76,7 +76,7 @@ typedef enum {
 /* Bits of the device error word. */
 #define DH_DEVERR_IDX 1u      /* a dh_idx entry was outside [0, V) */
 #define DH_DEVERR_TIMEOUT 2u  /* a bounded device wait gave up (results invalid) */
-#define DH_DEVERR_UNFINISHED 4u  /* nvfp4_matmul_wait_probe only: see there */
+#define DH_DEVERR_UNFINISHED 4u  /* wait probes of the many-token operators only: see nvfp4_matmul_wait_probe */
 
 typedef enum {
     DH_FMT_NVFP4 = 1,
@@ -513,6 +513,15 @@ int fp8_block_matmul(const dh_fp8_blocks_t *w, const void *x, int x_type, int64_
 int fp8_block_matmul_input_gradient(const dh_fp8_blocks_t *w, const void *dy, int dy_type, int64_t lddy, int M, void *dx, int dx_type,
                                     int64_t lddx, void *ws, size_t ws_bytes, unsigned int *error, void *stream);
 
+/* Self-test of the failure handling of fp8_block_matmul: the same product (x and y
+ * bfloat16, contiguous) with one role of the kernel's warps doing nothing (0: the
+ * operands' copies, 1: the matrix instructions, 2: the results) and a limit of 64 x rounds
+ * tries of about 1 us on every wait; otherwise as nvfp4_matmul_wait_probe. (An idle role 2
+ * is waited for only where an SM has more steps of 128 features than accumulators: 2 for
+ * 256-wide tiles, else 4.) */
+int fp8_block_matmul_wait_probe(const dh_fp8_blocks_t *w, const void *x, int M, void *y, void *ws, size_t ws_bytes, int role,
+                                unsigned int rounds, unsigned int *error, void *stream);
+
 /* Softmax cross entropy of T hidden states against the vocabulary given by N head
  * rows, and its gradients, without logits in memory (the pages have no counterpart: it
  * is how the BF16 rows of a draft head are trained on the tokens themselves, before
@@ -575,6 +584,12 @@ int draft_head_cross_entropy(const dh_cross_entropy_t *c, float *loss, float *ls
 int draft_head_cross_entropy_backward(const dh_cross_entropy_t *c, const float *lse, const float *rest, void *dhidden,
                                       int64_t ld_dhidden, void *dhead, int64_t ld_dhead, void *ws, size_t ws_bytes,
                                       unsigned int *error, void *stream);
+
+/* The self-test of draft_head_cross_entropy's waits, on the loss alone: roles, rounds and
+ * error as for fp8_block_matmul_wait_probe (role 2 is waited for where an SM has more than
+ * 1,024 features or two tiles). */
+int draft_head_cross_entropy_wait_probe(const dh_cross_entropy_t *c, float *loss, void *ws, size_t ws_bytes, int role, unsigned int rounds,
+                                        unsigned int *error, void *stream);
 
 /* Self-test of the failure handling of the draft-step kernels (the pages have
  * no counterpart): a one-thread kernel waits for an event that nothing

@@ -69,7 +69,7 @@ EXPORTS = (
     "draft_head_distill_backward", "nvfp4_matmul_packed_bytes", "nvfp4_pack_matmul", "nvfp4_matmul_workspace_bytes",
     "nvfp4_matmul", "nvfp4_matmul_wait_probe", "draft_head_cross_entropy_workspace_bytes", "draft_head_cross_entropy",
     "draft_head_cross_entropy_backward", "fp8_quantize_blocks", "fp8_block_matmul_workspace_bytes", "fp8_block_matmul",
-    "fp8_block_matmul_input_gradient",
+    "fp8_block_matmul_input_gradient", "fp8_block_matmul_wait_probe", "draft_head_cross_entropy_wait_probe",
 )
 
 _lib = None
@@ -176,6 +176,8 @@ def lib():
         L.fp8_block_matmul_workspace_bytes.restype = S
         for fn in (L.fp8_block_matmul, L.fp8_block_matmul_input_gradient):
             fn.argtypes = [C.POINTER(dh_fp8_blocks_t), P, I, C.c_int64, I, P, I, C.c_int64, P, S, P, P]
+        L.fp8_block_matmul_wait_probe.argtypes = [C.POINTER(dh_fp8_blocks_t), P, I, P, P, S, I, C.c_uint, P, P]
+        L.draft_head_cross_entropy_wait_probe.argtypes = [C.POINTER(dh_cross_entropy_t), P, P, S, I, C.c_uint, P, P]
         _lib = L
     return _lib
 
@@ -802,6 +804,20 @@ class FP8BlockMatmul:
             raise DraftHeadError(name, st)
         return y
 
+    def wait_probe(self, x: torch.Tensor, role: int, rounds: int) -> None:
+        """Enqueue the self-test of the product's bounded waits on x [M, K] (bfloat16,
+        contiguous): `role` of the kernel's warps does nothing (see
+        fp8_block_matmul_wait_probe); device_error() tells how it ended."""
+        if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != self.K or x.device != self.q.device or not x.is_contiguous():
+            raise ValueError(f"x must be a contiguous [M, {self.K}] bfloat16 tensor")
+        M, s = x.shape[0], _stream_of(x)
+        y = torch.empty((M, self.N), dtype=torch.bfloat16, device=x.device)
+        nb = lib().fp8_block_matmul_workspace_bytes(M, self.K, self.N)
+        ws = torch.empty(nb, dtype=torch.uint8, device=x.device)
+        _check("fp8_block_matmul_wait_probe",
+               lib().fp8_block_matmul_wait_probe(self.desc_ref, x.data_ptr(), M, y.data_ptr(), ws.data_ptr(), nb, role, rounds,
+                                                 self.error_ptr, s))
+
     def device_error(self) -> int:
         """Read and clear the device error word (waits for the device: products may be
         pending on any stream)."""
@@ -1173,6 +1189,18 @@ def linear_cross_entropy_backward(hidden: torch.Tensor, head: torch.Tensor, toke
                                                    _ptr(dw), 0 if dw is None else dw.stride(0), ws.data_ptr(), ws.numel(),
                                                    _ptr(_error_word(hidden.device)), s))
     return dx, dw
+
+
+def linear_cross_entropy_wait_probe(hidden: torch.Tensor, head: torch.Tensor, tokens: torch.Tensor, role: int, rounds: int) -> None:
+    """Enqueue the self-test of the bounded waits of linear_cross_entropy's products
+    (draft_head_cross_entropy_wait_probe); linear_cross_entropy_device_error() tells how it
+    ended."""
+    d = _cross_entropy(hidden, head, tokens, None, None)
+    s, loss = _stream_of(hidden), torch.empty(d.T, dtype=torch.float32, device=hidden.device)
+    ws = _cross_entropy_space(d, DH_CE_LOSS, hidden.device)
+    _check("draft_head_cross_entropy_wait_probe",
+           lib().draft_head_cross_entropy_wait_probe(C.byref(d), loss.data_ptr(), ws.data_ptr(), ws.numel(), role, rounds,
+                                                     _ptr(_error_word(hidden.device)), s))
 
 
 class LinearCrossEntropy(torch.autograd.Function):

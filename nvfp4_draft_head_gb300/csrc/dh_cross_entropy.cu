@@ -493,6 +493,8 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
     if (loss) {
         typename Stats<T, P>::Args a = {};
         a.shape = gemm::whole_tiles(tiles_m, ceil_div(c.N, kTN), steps, c.error);
+        a.shape.rounds = c.probe_rounds;
+        a.shape.idle = c.probe_role;
         a.tok = tok;
         a.part = reinterpret_cast<float2*>(ws + sp.part);
         a.target = reinterpret_cast<float*>(ws + sp.target);

@@ -21,9 +21,10 @@ bool shape_ok(int T, int N, int K) {
            ((static_cast<int64_t>(N) + 255) / 256) * ((K + 255) / 256) <= (1 << 29);
 }
 
-// A [rows][K] matrix: 16-byte rows (their stride means nothing for a single one).
+// A [rows][K] matrix: 16-byte rows (their stride, below a tensor map's 2^40 bytes, means nothing
+// for a single one).
 int check_rows(const void* p, int64_t ld, int rows, int K) {
-    if (rows > 1 && ld < K) return DH_ERR_SHAPE;
+    if (rows > 1 && (ld < K || ld >= (1ll << 39))) return DH_ERR_SHAPE;
     return aligned(p, 16) && (rows == 1 || ld % 8 == 0) ? DH_OK : DH_ERR_ALIGN;
 }
 
@@ -33,6 +34,7 @@ int check(const dh_cross_entropy_t* c, void* dhidden, int64_t ld_dhidden, void* 
           const unsigned int* error, dh::CrossEntropyArgs& a) {
     if (c == nullptr || c->hidden == nullptr || c->head == nullptr || c->tokens == nullptr || ws == nullptr) return DH_ERR_ARG;
     if (c->type != DH_T_BF16 && c->type != DH_T_F16) return DH_ERR_ARG;
+    if (dhidden == c->hidden || dhead == c->head) return DH_ERR_ARG;   // not in place
     if (!shape_ok(c->T, c->N, c->K)) return DH_ERR_SHAPE;
     if (c->row_of != nullptr && c->V < 1) return DH_ERR_SHAPE;
     int st;
@@ -104,6 +106,21 @@ int draft_head_cross_entropy_backward(const dh_cross_entropy_t* c, const float* 
     a.rest_in = rest;
     if ((st = check_space(a, ws, ws_bytes)) != DH_OK) return st;
     a.ws = ws;
+    return cuda_status(dh::launch_cross_entropy(a, static_cast<cudaStream_t>(stream)));
+}
+
+int draft_head_cross_entropy_wait_probe(const dh_cross_entropy_t* c, float* loss, void* ws, size_t ws_bytes, int role, unsigned int rounds,
+                                        unsigned int* error, void* stream) {
+    if (loss == nullptr || error == nullptr || role < 0 || role > 2 || rounds < 1 || rounds > 4096) return DH_ERR_ARG;
+    dh::CrossEntropyArgs a = {};
+    int st = check(c, nullptr, 0, nullptr, 0, ws, error, a);
+    if (st != DH_OK) return st;
+    if (!aligned(loss, 4)) return DH_ERR_ALIGN;
+    a.loss = loss;
+    if ((st = check_space(a, ws, ws_bytes)) != DH_OK) return st;
+    a.ws = ws;
+    a.probe_role = role;
+    a.probe_rounds = rounds;
     return cuda_status(dh::launch_cross_entropy(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -304,6 +304,8 @@ cudaError_t product(const Fp8BlockArgs& f, const Plan& plan, const uint8_t* code
     typename P::Args a = {};
     const int steps = ceil_div(width, kBlock);
     a.shape = gemm::whole_tiles(ceil_div(f.M, gemm::kRows), ceil_div(out, L::kTN), steps, f.error);
+    a.shape.rounds = f.probe_rounds;
+    a.shape.idle = f.probe_role;
     a.sx = scales;
     a.sw = f.scale;
     a.sw_j = GRADIENT ? 1 : kb;

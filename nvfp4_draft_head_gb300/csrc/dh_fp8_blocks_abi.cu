@@ -26,7 +26,7 @@ bool tokens_ok(int M, int width, int out) {
 }
 
 int product(const dh_fp8_blocks_t* w, bool gradient, const void* x, int x_type, int64_t ldx, int M, void* y, int y_type, int64_t ldy,
-            void* ws, size_t ws_bytes, unsigned int* error, void* stream) {
+            void* ws, size_t ws_bytes, unsigned int* error, void* stream, int probe_role = 0, unsigned int probe_rounds = 0) {
     if (w == nullptr || w->q == nullptr || w->scale == nullptr || x == nullptr || y == nullptr) return DH_ERR_ARG;
     if (type_bytes(x_type) == 0 || type_bytes(y_type) == 0) return DH_ERR_ARG;
     if (!weight_ok(w->N, w->K)) return DH_ERR_SHAPE;
@@ -52,6 +52,8 @@ int product(const dh_fp8_blocks_t* w, bool gradient, const void* x, int x_type, 
     a.ldy = ldy;
     a.ws = ws;
     a.error = error;
+    a.probe_role = probe_role;
+    a.probe_rounds = probe_rounds;
     return cuda_status(dh::launch_fp8_blocks(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -81,6 +83,12 @@ int fp8_block_matmul(const dh_fp8_blocks_t* w, const void* x, int x_type, int64_
 int fp8_block_matmul_input_gradient(const dh_fp8_blocks_t* w, const void* dy, int dy_type, int64_t lddy, int M, void* dx, int dx_type,
                                     int64_t lddx, void* ws, size_t ws_bytes, unsigned int* error, void* stream) {
     return product(w, true, dy, dy_type, lddy, M, dx, dx_type, lddx, ws, ws_bytes, error, stream);
+}
+
+int fp8_block_matmul_wait_probe(const dh_fp8_blocks_t* w, const void* x, int M, void* y, void* ws, size_t ws_bytes, int role,
+                                unsigned int rounds, unsigned int* error, void* stream) {
+    if (w == nullptr || error == nullptr || role < 0 || role > 2 || rounds < 1 || rounds > 4096) return DH_ERR_ARG;
+    return product(w, false, x, DH_T_BF16, w->K, M, y, DH_T_BF16, w->N, ws, ws_bytes, error, stream, role, rounds);
 }
 
 }  // extern "C"

@@ -34,13 +34,15 @@ struct FewArgs {
     void* y;
     long long ldy;
     unsigned int* error;
-    uint32_t rounds;
+    uint32_t rounds;          // tries of a bounded wait, times kWaitSlices
+    int idle;                 // self-test: the role that does nothing (-1: none)
 };
 
 struct FewSync {
     uint64_t full[16], empty[16], acc_full[kBuffers], acc_empty[kBuffers], codes, received, room, issued;
     uint32_t tmem;
     unsigned int abort;
+    uint32_t copies;   // self-test: stages that the producer filled
 };
 
 __device__ __forceinline__ bool wait(FewSync& sy, uint64_t* bar, uint32_t parity, const FewArgs& a) {
@@ -105,6 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         mbar_init(&sy.issued, 1);
         mbar_init_fence();
         sy.abort = 0u;
+        sy.copies = 0u;
     }
     __syncwarp();
     if (warp == kIssuer) tc::tmem_alloc(&sy.tmem, F::kCols);
@@ -124,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         uint64_t policy;
         asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
         uint32_t it = 0, st = 0, phase = 1;
-        bool ok = true;
+        bool ok = a.idle != gemm::kRoleProducer;
         for (int t = first; ok && t < a.tiles; t += stride)
             for (int b = b0; b < b0 + count; ++b, ++it) {
                 if (it >= stages && !(ok = __all_sync(~0u, wait(sy, &sy.empty[st], phase, a)))) break;
@@ -144,6 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         // the copies in flight land before the CTA ends, whoever gave up (bounded)
         for (uint32_t b = it > stages ? it - stages : 0; b < it; ++b)
             if (!mbar_wait(&sy.full[b % stages], (b / stages) & 1, gemm::kDrainRounds)) break;
+        if (lane == 0) sy.copies = it;
         __syncwarp();
         if (splits > 1) cluster_wait();
     } else if (warp == kIssuer) {
@@ -152,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         const uint64_t first_a = GRADIENT ? tc::desc_operand_mn(base, kBlock) : tc::desc_operand(base);
         const uint64_t first_b = tc::desc_operand(FUSED ? smem_u32(codes) : base + kABytes);
         uint32_t n = 0, st = 0, phase = 0;
-        bool ok = !FUSED || __all_sync(~0u, wait(sy, &sy.codes, 0, a));
+        bool ok = a.idle != gemm::kRoleIssuer && (!FUSED || __all_sync(~0u, wait(sy, &sy.codes, 0, a)));
         for (int t = first; ok && t < a.tiles; t += stride)
             for (int b = 0; b < count; ++b, ++n) {
                 const uint32_t buf = n % kBuffers, use = n / kBuffers;
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         const int quarter = warp & 3, part = warp >> 2, local = quarter * 32 + lane;
         uint32_t n = 0, e = 0;
         bool joined = splits == 1;   // the cluster's start has been waited for
-        for (int t = first; t < a.tiles; t += stride, ++e) {
+        for (int t = a.idle != gemm::kRoleEpilogue ? first : a.tiles; t < a.tiles; t += stride, ++e) {
             const int row = t * kBlock + local;
             const float* sw = a.sw + static_cast<size_t>(t) * a.sw_j + static_cast<size_t>(b0) * a.sw_b;
             float next = __ldg(sw);
@@ -285,6 +289,11 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         cluster_sync_all();
     }
     tc::fence_after_sync();
+    if (a.idle >= 0 && threadIdx.x == 0) {   // the self-test: nothing of this CTA's is in flight
+        bool done = mbar_test(&sy.issued, 0);
+        for (uint32_t i = 0; i < stages && i < sy.copies; ++i) done = mbar_test(&sy.full[i], ((sy.copies - 1 - i) / stages) & 1) && done;
+        if (!done && a.error != nullptr) atomicOr(a.error, kDevErrUnfinished);
+    }
     if (warp == kIssuer) tc::tmem_free(tmem, F::kCols);
 }
 
@@ -363,7 +372,6 @@ cudaError_t launch_kernel(const CUtensorMap& map_w, const CUtensorMap& map_x, Fe
     }
     const int fit = (kSpace - F::rest(a.per, splits)) / F::kStage;
     a.stages = fit < 16 ? fit : 16;
-    a.rounds = kWaitLimit / gemm::kWaitSlices;
     const int clusters = clusters_of(splits), want = a.tiles < clusters ? a.tiles : clusters;
     return gemm::launch_early(kernel, dim3(static_cast<unsigned>(want * splits)), kThreads, kSmem, splits, stream, map_w, map_x, a);
 }
@@ -387,6 +395,8 @@ cudaError_t launch_sized(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, c
     a.y = f.y;
     a.ldy = f.ldy;
     a.error = f.error;
+    a.rounds = f.probe_rounds != 0 ? f.probe_rounds : kWaitLimit / gemm::kWaitSlices;
+    a.idle = f.probe_rounds != 0 ? f.probe_role : -1;
     float us;
     const int splits = choose_splits<NT, FUSED>(a.tiles, a.steps, &us);
     if (splits == 0) return cudaErrorInvalidValue;

@@ -46,7 +46,7 @@ struct Shape {
     int steps, split_steps;
     int a_mn, a_k, b_mn, b_k;       // first row (M / N) and first element of K of each operand
     unsigned int* error;            // DH_DEVERR_* word or null
-    uint32_t rounds;                // tries of a bounded wait, times kWaitSlices
+    uint32_t rounds;                // self-test: tries of a bounded wait, times kWaitSlices (0: a product's own)
     int idle;                       // self-test: the role that does nothing (-1: none)
     __host__ __device__ int tiles() const { return tiles_m * tiles_n; }
     __host__ __device__ int units() const { return whole + (tiles() - whole) * splits; }
@@ -96,13 +96,14 @@ struct Layout {
     static constexpr int kSmem = kStages * kBytes + 1024;
     static constexpr int kBuffers = 512 / TN < 4 ? 512 / TN : 4;        // accumulators in tensor memory
     static_assert(!(A_MN && kRows % kSpan != 0) && !(B_MN && kBRows % kSpan != 0), "whole boxes");
-    static_assert(kBytes % 1024 == 0 && TN % 32 == 0 && kStages >= 3, "stage layout");
+    static_assert(kStages <= 8 && kBytes % 1024 == 0 && TN % 32 == 0 && kStages >= 3, "stage layout");
 };
 
 struct Sync {
     uint64_t full[8], empty[8], acc_full[4], acc_empty[4], issued;
     uint32_t tmem;
     unsigned int abort;
+    uint32_t copies;   // self-test: stages that the producer filled
 };
 
 // One lane of a converged warp, known to the compiler as such: what it issues takes its
@@ -118,7 +119,7 @@ __device__ __forceinline__ bool elect_one() {
 static __device__ __noinline__ bool wait_longer(volatile unsigned int* abort, uint64_t* bar, uint32_t parity, uint32_t rounds,
                                                 unsigned int* error) {
     for (int i = 0; i < kWaitSlices; ++i) {
-        if (mbar_wait<false>(bar, parity, rounds)) return true;
+        if (mbar_wait(bar, parity, rounds)) return true;   // (about 1 us a round)
         if (*abort != 0u) return false;
     }
     *abort = 1u;
@@ -221,6 +222,7 @@ __global__ void __launch_bounds__(Op::Layout::kThreads, 1) product_kernel(const 
         mbar_init(&sy.issued, 1);
         mbar_init_fence();
         sy.abort = 0u;
+        sy.copies = 0u;
     }
     __syncwarp();
     if (warp == 0) tc::tmem_alloc_of<P>(&sy.tmem, 512);
@@ -270,6 +272,7 @@ __global__ void __launch_bounds__(Op::Layout::kThreads, 1) product_kernel(const 
             if (rank == 0 && !mbar_wait(&sy.full[b % kStages], (b / kStages) & 1, kDrainRounds)) break;
             if (P > 1 && !mbar_wait(&sy.empty[b % kStages], (b / kStages) & 1, kDrainRounds)) break;
         }
+        if (lane == 0) sy.copies = it;
     } else if (warp == L::kIssuer && rank == 0 && s.idle != kRoleIssuer) {
         constexpr uint32_t kIdesc = tc::idesc_f(Op::kFormat, L::kAMn, L::kBMn, kRows * P, L::kTN);
         constexpr bool kF8 = L::kElem == 1;
@@ -331,6 +334,12 @@ __global__ void __launch_bounds__(Op::Layout::kThreads, 1) product_kernel(const 
         cluster_sync_all();
     }
     tc::fence_after_sync();
+    if (s.idle >= 0 && rank == 0 && threadIdx.x == 0) {   // the self-test: nothing of this tile's is in flight
+        bool done = s.idle == kRoleIssuer || mbar_test(&sy.issued, 0);
+        for (uint32_t i = 0; i < static_cast<uint32_t>(kStages) && i < sy.copies; ++i)   // the last use of slot i
+            done = mbar_test(&sy.full[i], ((sy.copies - 1 - i) / kStages) & 1) && done;
+        if (!done && s.error != nullptr) atomicOr(s.error, kDevErrUnfinished);
+    }
     if (warp == 0) tc::tmem_free_of<P>(tmem, 512);
 }
 

@@ -180,6 +180,8 @@ struct CrossEntropyArgs {
     long long ld_dhead;
     void* ws;
     unsigned int* error;
+    int probe_role;          // the self-test of the loss's waits, where probe_rounds is not 0
+    uint32_t probe_rounds;
 };
 size_t cross_entropy_workspace_bytes(int T, int N, int K, bool loss, bool dhidden, bool dhead);
 cudaError_t launch_cross_entropy(const CrossEntropyArgs& a, cudaStream_t s);
@@ -199,6 +201,8 @@ struct Fp8BlockArgs {
     long long ldy;
     void* ws;
     unsigned int* error;     // device error word or null
+    int probe_role;          // the self-test of its waits, where probe_rounds is not 0
+    uint32_t probe_rounds;
 };
 size_t fp8_block_workspace_bytes(int M, int width, int out);
 cudaError_t launch_fp8_quantize_blocks(const uint16_t* W, int V, int K, const int32_t* idx, int N, uint8_t* q, float* scale, Workspace* ws,

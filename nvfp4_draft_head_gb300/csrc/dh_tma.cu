@@ -25,9 +25,19 @@ cudaError_t encode_map(CUtensorMap* map, const void* base, int elem, uint64_t co
     if (e != cudaSuccess) return e;
     const cuuint64_t dims[2] = {cols, rows}, strides[1] = {ld};
     const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elem), box_rows}, one[2] = {1, 1};
-    const CUresult r = encode(map, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims,
-                              strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const auto call = [&] {
+        return encode(map, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides,
+                      box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = call();
+    if (r != CUDA_SUCCESS) {   // a thread that has made no runtime call yet has no context: bind the device's
+        int dev = 0;
+        cudaError_t bound = cudaGetDevice(&dev);
+        if (bound == cudaSuccess) bound = cudaSetDevice(dev);
+        if (bound != cudaSuccess) return bound;
+        r = call();
+    }
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 

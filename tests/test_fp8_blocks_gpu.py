@@ -115,3 +115,168 @@ def test_input_gradient(M, N, K, tx, ty):
     check(dx, quantise(dy, 1)[2], wv, N)
     assert torch.equal(mm.input_gradient(dy, out_dtype=ty), dx)
     assert mm.device_error() == 0
+
+
+def layer(N, K, seed=0):
+    q, s, wv = quantise(weight(N, K, seed), 128)
+    return dh.FP8BlockMatmul(q.contiguous(), s.contiguous()), wv
+
+
+@pytest.mark.parametrize("M", [3, 40, 140])
+@pytest.mark.parametrize("tx,ld,offset", [(BF, 272, 0), (BF, 273, 1), (HF, 300, 4), (F, 259, 3), (F, 264, 2)])
+@pytest.mark.parametrize("ty,ldy,at", [(BF, 512, 0), (BF, 131, 1), (HF, 134, 2), (F, 133, 1), (F, 136, 4)])
+def test_strides_and_given_results(M, tx, ld, offset, ty, ldy, at):
+    N, K = 130, 256
+    mm, wv = layer(N, K)
+    x = rows(M, K, tx, ld=ld, offset=offset)
+    buf = torch.full((M * ldy + at + 8,), 7.0, dtype=ty, device=DEV)
+    y = torch.as_strided(buf, (M, N), (ldy, 1), at)
+    assert mm(x, y) is y
+    check(y, quantise(x, 1)[2], wv.t(), K)
+    assert torch.equal(mm(x.contiguous(), out_dtype=ty), y)
+    torch.as_strided(buf, (M, N), (ldy, 1), at).fill_(7.0)
+    assert (buf == 7).all(), "something beside the rows was written"
+    dx = torch.full((M, K + 3), 7.0, dtype=ty, device=DEV)
+    mm.input_gradient(y.fill_(0.5), dx[:, :K])
+    assert (dx[:, K:] == 7).all()
+    assert torch.equal(dx[:, :K], mm.input_gradient(y.contiguous(), out_dtype=ty))
+
+
+@pytest.mark.parametrize("M", [2, 33, 150])
+def test_rows_that_are_not_finite_and_zeros(M):
+    mm, wv = layer(300, 400)
+    x = rows(M, 400, F)
+    want = mm(x, out_dtype=F)
+    x[0] = 0.0
+    x[1, 399] = float("nan") if M != 33 else float("-inf")
+    y = mm(x, out_dtype=F)
+    assert y[1].isnan().all() and not y[0].any()
+    assert torch.equal(y[2:], want[2:])
+    dy = rows(M, 300, F)
+    want = mm.input_gradient(dy, out_dtype=F)
+    dy[0] = 1e-30                                     # below the smallest scale: zeros
+    dy[1, 0] = float("inf")
+    dx = mm.input_gradient(dy, out_dtype=F)
+    assert dx[1].isnan().all() and dx[0].abs().max() <= 1e-12 and torch.equal(dx[2:], want[2:])
+
+
+def test_a_row_of_the_weight():
+    """The gradient of one output feature is its row of the weight (1 is a code times a scale, to
+    fp32's rounding), the output of one input feature its column."""
+    mm, wv = layer(300, 400)
+    one = torch.eye(300, device=DEV)[[0, 127, 128, 299]].contiguous()
+    dx = mm.input_gradient(one, out_dtype=F)
+    assert ((dx.double() - wv[[0, 127, 128, 299]]).abs() <= 2.0 ** -21 * wv[[0, 127, 128, 299]].abs()).all()
+    one = torch.eye(400, device=DEV)[[0, 128, 399]].contiguous()
+    y = mm(one, out_dtype=F)
+    assert ((y.double() - wv[:, [0, 128, 399]].t()).abs() <= 2.0 ** -21 * wv[:, [0, 128, 399]].t().abs()).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 19500, 8192), (16, 6000, 8192), (1, 70000, 256)])
+def test_few_tokens_on_many_tiles(M, N, K):
+    """Clusters that exchange their sums for tile after tile."""
+    mm, wv = layer(N, K)
+    x = rows(M, K, BF)
+    y = mm(x)
+    check(y, quantise(x, 1)[2], wv.t(), K)
+    for _ in range(3):
+        assert torch.equal(mm(x), y)
+    assert mm.device_error() == 0
+
+
+@pytest.mark.parametrize("M,N,K,grad", [(200, 9000, 272, True), (150, 130, 6000, False), (129, 64026, 256, True), (16, 48, 70000, False),
+                                        (100, 40000, 256, True), (20, 48, 30000, False)])
+def test_long_contractions(M, N, K, grad):
+    K = K // 16 * 16
+    mm, wv = layer(N, K)
+    x = rows(M, N if grad else K, BF)
+    y = mm.input_gradient(x, out_dtype=F) if grad else mm(x, out_dtype=F)
+    check(y, quantise(x, 1)[2], wv if grad else wv.t(), x.shape[1])
+
+
+def test_no_tokens_and_float8_codes():
+    q, s, wv = quantise(weight(64, 128), 128)
+    mm = dh.FP8BlockMatmul(q.contiguous(), s.contiguous())
+    raw = dh.FP8BlockMatmul(q.contiguous().view(torch.uint8), s.contiguous())
+    x = rows(9, 128, BF)
+    assert torch.equal(mm(x), raw(x))
+    assert mm(x[:0]).shape == (0, 64) and mm.input_gradient(rows(1, 64, F)[:0]).shape == (0, 128)
+
+
+def test_refusals():
+    q, s, _ = quantise(weight(64, 128), 128)
+    q, s = q.contiguous(), s.contiguous()
+    mm = dh.FP8BlockMatmul(q, s)
+    x = rows(4, 128, BF)
+    for bad in (lambda: dh.FP8BlockMatmul(q.float(), s), lambda: dh.FP8BlockMatmul(q.t(), s), lambda: dh.FP8BlockMatmul(q, s.double()),
+                lambda: dh.FP8BlockMatmul(q, s.expand(2, 1)), lambda: dh.FP8BlockMatmul(q.cpu(), s), lambda: mm(x[:, :112]), lambda: mm(x.t()),
+                lambda: mm(x.double()), lambda: mm(x.cpu()), lambda: mm(x[0]), lambda: mm(x, out_dtype=torch.float64),
+                lambda: mm(x, torch.empty((4, 65), device=DEV)), lambda: mm(x, torch.empty((64, 4), device=DEV).t()),
+                lambda: mm.input_gradient(x), lambda: mm(x.float().requires_grad_()), lambda: mm.input_gradient(rows(4, 64, F).requires_grad_()),
+                lambda: mm(x[:1].expand(4, 128)), lambda: dh.fp8_quantize_blocks(weight(64, 128).float())):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: dh.FP8BlockMatmul(q[:, :120].contiguous(), s), lambda: dh.FP8BlockMatmul(q[:0], s[:0]),
+                lambda: dh.fp8_quantize_blocks(weight(64, 136))):
+        with pytest.raises(dh.DraftHeadError):
+            bad()
+    assert mm(x).shape == (4, 64)
+
+
+@pytest.mark.parametrize("M", [1, 300])
+def test_offsets_past_32_bits_in_the_weight(M):
+    N, K = 840_000, 2560
+    q = torch.randint(0, 0x78, (N, K), dtype=torch.uint8, device=DEV)
+    s = torch.rand((N // 128 + 1, 20), device=DEV) + 0.1
+    mm = dh.FP8BlockMatmul(q, s)
+    x = rows(M, K, BF)
+    y = mm(x)
+    for r in (0, 512_000, N - 1000):
+        wv = q[r:r + 1000].view(torch.float8_e4m3fn).double() * s.double()[torch.arange(r, r + 1000, device=DEV) // 128].repeat_interleave(128, 1)
+        check(y[:, r:r + 1000], quantise(x, 1)[2], wv.t(), K)
+
+
+def test_offsets_past_32_bits_in_the_results():
+    M, N, K = 40_000, 60_003, 16
+    mm, wv = layer(N, K)
+    x = rows(M, K, BF)
+    y = mm(x)
+    for r in (0, 35_700, M - 100):      # 35,700 x 60,003 is about 2^31
+        check(y[r:r + 100], quantise(x[r:r + 100], 1)[2], wv.t(), K)
+
+
+@pytest.mark.parametrize("M", [1, 16, 40, 200])
+def test_graphs(M):
+    mm, _ = layer(600, 2000)
+    a, b = rows(M, 2000, BF), rows(M, 2000, BF, seed=9)
+    want = [(mm(t), mm.input_gradient(mm(t))) for t in (a, b)]
+    x = a.clone()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            y = mm(x)
+            out = (y, mm.input_gradient(y))
+        graphs.append((g, out))
+    for i, t in ((0, a), (1, b), (0, a)):
+        x.copy_(t)
+        for g, _ in graphs:
+            g.replay()
+        for _, out in graphs:
+            assert torch.equal(out[0], want[i][0]) and torch.equal(out[1], want[i][1])
+
+
+def test_autograd():
+    mm, wv = layer(300, 400)
+    for M, tx in ((5, F), (150, BF)):
+        x = rows(M, 400, tx).requires_grad_()
+        y = dh.FP8BlockLinear.apply(x, mm, F)
+        assert torch.equal(y, mm(x.detach(), out_dtype=F))
+        up = rows(M, 300, F)
+        (dx,) = torch.autograd.grad(y, x, up, create_graph=True)
+        assert dx.dtype == tx and torch.equal(dx, mm.input_gradient(up, out_dtype=tx))
+        with pytest.raises(RuntimeError, match="differentiable once"):
+            (dx.float().square().sum() + x.float().sum()).backward()
+        dh.FP8BlockLinear.apply(x, mm, F).sum().backward()          # an expanded gradient
+        assert torch.equal(x.grad, mm.input_gradient(torch.ones((M, 300), device=DEV), out_dtype=tx))
+        assert not dh.FP8BlockLinear.apply(x.detach(), mm).requires_grad
