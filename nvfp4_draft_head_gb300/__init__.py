@@ -117,6 +117,10 @@ class dh_cross_entropy_t(C.Structure):
                 ("row_of", C.c_void_p), ("V", C.c_int)]
 
 
+_pack_cross_entropy = struct.Struct("@PPiiiiqqPPPi0P").pack
+assert struct.calcsize("@PPiiiiqqPPPi0P") == C.sizeof(dh_cross_entropy_t)
+
+
 def library_path() -> str:
     return _build.LIB_PATH
 
@@ -169,15 +173,15 @@ def lib():
         L.nvfp4_matmul_wait_probe.argtypes = [C.POINTER(dh_matmul_t), P, I, P, P, S, I, C.c_uint, P, P]
         L.draft_head_cross_entropy_workspace_bytes.argtypes = [I, I, I, C.c_uint]
         L.draft_head_cross_entropy_workspace_bytes.restype = S
-        L.draft_head_cross_entropy.argtypes = [C.POINTER(dh_cross_entropy_t), P, P, P, P, C.c_int64, P, C.c_int64, P, S, P, P]
-        L.draft_head_cross_entropy_backward.argtypes = [C.POINTER(dh_cross_entropy_t), P, P, P, C.c_int64, P, C.c_int64, P, S, P, P]
+        L.draft_head_cross_entropy.argtypes = [P, P, P, P, P, C.c_int64, P, C.c_int64, P, S, P, P]
+        L.draft_head_cross_entropy_backward.argtypes = [P, P, P, P, C.c_int64, P, C.c_int64, P, S, P, P]
         L.fp8_quantize_blocks.argtypes = [P, I, I, P, I, P, P, P, S, P]
         L.fp8_block_matmul_workspace_bytes.argtypes = [I, I, I]
         L.fp8_block_matmul_workspace_bytes.restype = S
         for fn in (L.fp8_block_matmul, L.fp8_block_matmul_input_gradient):
             fn.argtypes = [C.POINTER(dh_fp8_blocks_t), P, I, C.c_int64, I, P, I, C.c_int64, P, S, P, P]
         L.fp8_block_matmul_wait_probe.argtypes = [C.POINTER(dh_fp8_blocks_t), P, I, P, P, S, I, C.c_uint, P, P]
-        L.draft_head_cross_entropy_wait_probe.argtypes = [C.POINTER(dh_cross_entropy_t), P, P, S, I, C.c_uint, P, P]
+        L.draft_head_cross_entropy_wait_probe.argtypes = [P, P, P, S, I, C.c_uint, P, P]
         _lib = L
     return _lib
 
@@ -1079,45 +1083,63 @@ def linear_cross_entropy_device_error(device=None) -> int:
     return err
 
 
-def _rows16(t: torch.Tensor, name: str, shape, like: torch.Tensor | None = None) -> int:
-    """The row stride of a matrix with 16-byte aligned rows, checked."""
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)) or t.stride(1) != 1 and t.shape[1] > 1 or \
-            (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
-        raise ValueError(f"{name} must be a {'[T, K]' if shape is None else list(shape)} tensor with contiguous rows that do not overlap")
+def _rows16(t: torch.Tensor, name: str, rows: int, K: int, like: torch.Tensor | None = None) -> int:
+    """The row stride of a [rows, K] matrix with 16-byte aligned rows, checked (with `like`: its type
+    and device too)."""
+    if t.dim() != 2 or tuple(t.shape) != (rows, K):
+        raise ValueError(f"{name} must be a [{rows}, {K}] tensor")
+    ld, step = t.stride()
+    if (step != 1 and K > 1) or (rows > 1 and ld < K):
+        raise ValueError(f"{name}: rows must be contiguous and must not overlap")
     if like is not None and (t.dtype != like.dtype or t.device != like.device):
         raise ValueError(f"{name} must be {like.dtype} on {like.device}, as the hidden states are")
-    if t.data_ptr() % 16 or (t.shape[0] > 1 and t.stride(0) % 8):
+    if t.data_ptr() % 16 or (rows > 1 and ld % 8):
         raise ValueError(f"{name}: rows must be 16-byte aligned (a row stride that is a multiple of 8 elements)")
-    return t.stride(0)
+    return ld
 
 
-def _cross_entropy(hidden, head, tokens, weights, row_of) -> dh_cross_entropy_t:
-    """The descriptor of a call on T >= 1 tokens, its tensors checked."""
-    if hidden.dtype not in (torch.bfloat16, torch.float16) or not hidden.is_cuda:
+def _cross_entropy(hidden, head, tokens, weights, row_of):
+    """A call's dh_cross_entropy_t (as bytes), T, N and K, its tensors checked."""
+    dtype = hidden.dtype
+    if (dtype != torch.bfloat16 and dtype != torch.float16) or not hidden.is_cuda or hidden.dim() != 2:
         raise ValueError("hidden must be a [T, K] bfloat16 or float16 CUDA tensor")
-    ld_hidden = _rows16(hidden, "hidden", None)
     T, K = hidden.shape
-    if head.dim() != 2 or head.shape[1] != K or head.shape[0] < 1:
+    if head.dim() != 2 or head.shape[0] < 1:
         raise ValueError(f"head must be a [N, {K}] tensor of at least one row")
-    ld_head = _rows16(head, "head", head.shape, hidden)
-    _vector(tokens, "tokens", torch.int32, T, hidden.device)
-    _vector(weights, "weights", torch.float32, T, hidden.device)
-    _vector(row_of, "row_of", torch.int32, None, hidden.device)
-    return dh_cross_entropy_t(hidden.data_ptr(), head.data_ptr(), _TYPES[hidden.dtype], T, K, head.shape[0], ld_hidden, ld_head,
-                              tokens.data_ptr(), _ptr(weights), _ptr(row_of), 0 if row_of is None else row_of.numel())
+    N, device = head.shape[0], hidden.device
+    ld_hidden, ld_head = _rows16(hidden, "hidden", T, K), _rows16(head, "head", N, K, hidden)
+    _vector(tokens, "tokens", torch.int32, T, device)
+    _vector(weights, "weights", torch.float32, T, device)
+    _vector(row_of, "row_of", torch.int32, None, device)
+    try:
+        d = _pack_cross_entropy(hidden.data_ptr(), head.data_ptr(), _TYPES[dtype], T, K, N, ld_hidden, ld_head, tokens.data_ptr(),
+                                _ptr(weights) or 0, _ptr(row_of) or 0, 0 if row_of is None else row_of.numel())
+    except struct.error:   # a size past 32 bits
+        raise DraftHeadError("dh_cross_entropy_t", DH_ERR_SHAPE) from None
+    return d, T, N, K
 
 
-def _gradient_rows(out: torch.Tensor | None, like: torch.Tensor, name: str) -> torch.Tensor:
+def _gradient_rows(out: torch.Tensor | None, like: torch.Tensor, rows: int, K: int, name: str):
+    """A gradient's tensor and row stride."""
     if out is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    _rows16(out, name, like.shape, like)
-    return out
+        return torch.empty((rows, K), dtype=like.dtype, device=like.device), K
+    if out.data_ptr() == like.data_ptr():
+        raise ValueError(f"{name} must not be the tensor that it is the gradient of")
+    return out, _rows16(out, name, rows, K, like)
 
 
-def _cross_entropy_space(d: dh_cross_entropy_t, outputs: int, device) -> torch.Tensor:
-    nb = lib().draft_head_cross_entropy_workspace_bytes(d.T, d.N, d.K, outputs)
-    if nb == 0:
-        raise DraftHeadError("draft_head_cross_entropy_workspace_bytes", DH_ERR_SHAPE)
+_cross_entropy_bytes: dict = {}    # (T, N, K, outputs) -> bytes of workspace
+
+
+def _cross_entropy_space(T: int, N: int, K: int, outputs: int, device) -> torch.Tensor:
+    key = (T, N, K, outputs)
+    nb = _cross_entropy_bytes.get(key)
+    if nb is None:
+        nb = lib().draft_head_cross_entropy_workspace_bytes(T, N, K, outputs)
+        if nb == 0:
+            raise DraftHeadError("draft_head_cross_entropy_workspace_bytes", DH_ERR_SHAPE)
+        if len(_cross_entropy_bytes) < 4096:
+            _cross_entropy_bytes[key] = nb
     return torch.empty(nb, dtype=torch.uint8, device=device)
 
 
@@ -1126,24 +1148,25 @@ def linear_cross_entropy(hidden: torch.Tensor, head: torch.Tensor, tokens: torch
                          stream=None):
     """(loss float32 [T], dhidden [T, K], dhead [N, K]): per-token softmax cross entropy of
     hidden states [T, K] against the vocabulary of the head rows [N, K] (both bfloat16 or
-    both float16, rows 16-byte aligned), and the gradients of its sum, without logits in
-    memory. tokens: int32 [T], target ids with row_of (draft_head_row_map), head rows without
-    it; a token without a head row (-100, say) is left out, as a row of weight 0 is. weights:
-    float32 [T]. dhidden and dhead may be given tensors. The loss has no autograd graph (the
-    gradients are at hand; LinearCrossEntropy is the differentiable form). See
+    both float16, K % 8 == 0, rows 16-byte aligned), and the gradients of its sum, without
+    logits in memory. tokens: int32 [T], target ids with row_of (draft_head_row_map), head rows
+    without it; a token without a head row (-100, say) is left out, as a row of weight 0 is.
+    weights: float32 [T]. dhidden and dhead may be given tensors. The loss has no autograd
+    graph (the gradients are at hand; LinearCrossEntropy is the differentiable form). See
     draft_head_cross_entropy."""
     if stream is not None:
         return _on_stream(stream, linear_cross_entropy, hidden, head, tokens, weights, row_of, dhidden, dhead)
-    d = _cross_entropy(hidden, head, tokens, weights, row_of)
-    dx, dw = _gradient_rows(dhidden, hidden, "dhidden"), _gradient_rows(dhead, head, "dhead")
-    loss = torch.empty(d.T, dtype=torch.float32, device=hidden.device)
-    if d.T == 0:
+    d, T, N, K = _cross_entropy(hidden, head, tokens, weights, row_of)
+    (dx, ld_dx), (dw, ld_dw) = _gradient_rows(dhidden, hidden, T, K, "dhidden"), _gradient_rows(dhead, head, N, K, "dhead")
+    device = hidden.device
+    loss = torch.empty(T, dtype=torch.float32, device=device)
+    if T == 0:
         return loss, dx, dw.zero_()
     s = _stream_of(hidden)
-    ws = _cross_entropy_space(d, DH_CE_LOSS | DH_CE_DHIDDEN | DH_CE_DHEAD, hidden.device)
+    ws = _cross_entropy_space(T, N, K, DH_CE_LOSS | DH_CE_DHIDDEN | DH_CE_DHEAD, device)
     _check("draft_head_cross_entropy",
-           lib().draft_head_cross_entropy(C.byref(d), loss.data_ptr(), None, None, dx.data_ptr(), dx.stride(0), dw.data_ptr(),
-                                          dw.stride(0), ws.data_ptr(), ws.numel(), _ptr(_error_word(hidden.device)), s))
+           lib().draft_head_cross_entropy(d, loss.data_ptr(), None, None, dx.data_ptr(), ld_dx, dw.data_ptr(), ld_dw, ws.data_ptr(),
+                                          ws.numel(), _ptr(_error_word(device)), s))
     return loss, dx, dw
 
 
@@ -1153,14 +1176,16 @@ def linear_cross_entropy_forward(hidden: torch.Tensor, head: torch.Tensor, token
     normaliser for linear_cross_entropy_backward, and what rounding it left over."""
     if stream is not None:
         return _on_stream(stream, linear_cross_entropy_forward, hidden, head, tokens, weights, row_of)
-    d = _cross_entropy(hidden, head, tokens, weights, row_of)
-    loss, lse, rest = (torch.empty(d.T, dtype=torch.float32, device=hidden.device) for _ in range(3))
-    if d.T > 0:
+    d, T, N, K = _cross_entropy(hidden, head, tokens, weights, row_of)
+    device = hidden.device
+    loss = torch.empty(T, dtype=torch.float32, device=device)
+    lse, rest = torch.empty((2, T), dtype=torch.float32, device=device).unbind()
+    if T > 0:
         s = _stream_of(hidden)
-        ws = _cross_entropy_space(d, DH_CE_LOSS, hidden.device)
+        ws = _cross_entropy_space(T, N, K, DH_CE_LOSS, device)
         _check("draft_head_cross_entropy",
-               lib().draft_head_cross_entropy(C.byref(d), loss.data_ptr(), lse.data_ptr(), rest.data_ptr(), None, 0, None, 0,
-                                              ws.data_ptr(), ws.numel(), _ptr(_error_word(hidden.device)), s))
+               lib().draft_head_cross_entropy(d, loss.data_ptr(), lse.data_ptr(), rest.data_ptr(), None, 0, None, 0, ws.data_ptr(),
+                                              ws.numel(), _ptr(_error_word(device)), s))
     return loss, lse, rest
 
 
@@ -1175,19 +1200,19 @@ def linear_cross_entropy_backward(hidden: torch.Tensor, head: torch.Tensor, toke
         return _on_stream(stream, linear_cross_entropy_backward, hidden, head, tokens, lse, weights, rest, row_of, dhidden, dhead)
     if dhidden is False and dhead is False:
         raise ValueError("at least one of dhidden and dhead has to be wanted")
-    d = _cross_entropy(hidden, head, tokens, weights, row_of)
-    _vector(lse, "lse", torch.float32, d.T, hidden.device)
-    _vector(rest, "rest", torch.float32, d.T, hidden.device)
-    dx = None if dhidden is False else _gradient_rows(None if dhidden is True else dhidden, hidden, "dhidden")
-    dw = None if dhead is False else _gradient_rows(None if dhead is True else dhead, head, "dhead")
-    if d.T == 0:
+    d, T, N, K = _cross_entropy(hidden, head, tokens, weights, row_of)
+    device = hidden.device
+    _vector(lse, "lse", torch.float32, T, device)
+    _vector(rest, "rest", torch.float32, T, device)
+    dx, ld_dx = (None, 0) if dhidden is False else _gradient_rows(None if dhidden is True else dhidden, hidden, T, K, "dhidden")
+    dw, ld_dw = (None, 0) if dhead is False else _gradient_rows(None if dhead is True else dhead, head, N, K, "dhead")
+    if T == 0:
         return dx, None if dw is None else dw.zero_()
     s = _stream_of(hidden)
-    ws = _cross_entropy_space(d, (DH_CE_DHIDDEN if dx is not None else 0) | (DH_CE_DHEAD if dw is not None else 0), hidden.device)
+    ws = _cross_entropy_space(T, N, K, (DH_CE_DHIDDEN if dx is not None else 0) | (DH_CE_DHEAD if dw is not None else 0), device)
     _check("draft_head_cross_entropy_backward",
-           lib().draft_head_cross_entropy_backward(C.byref(d), lse.data_ptr(), _ptr(rest), _ptr(dx), 0 if dx is None else dx.stride(0),
-                                                   _ptr(dw), 0 if dw is None else dw.stride(0), ws.data_ptr(), ws.numel(),
-                                                   _ptr(_error_word(hidden.device)), s))
+           lib().draft_head_cross_entropy_backward(d, lse.data_ptr(), _ptr(rest), _ptr(dx), ld_dx, _ptr(dw), ld_dw, ws.data_ptr(),
+                                                   ws.numel(), _ptr(_error_word(device)), s))
     return dx, dw
 
 
@@ -1195,11 +1220,11 @@ def linear_cross_entropy_wait_probe(hidden: torch.Tensor, head: torch.Tensor, to
     """Enqueue the self-test of the bounded waits of linear_cross_entropy's products
     (draft_head_cross_entropy_wait_probe); linear_cross_entropy_device_error() tells how it
     ended."""
-    d = _cross_entropy(hidden, head, tokens, None, None)
-    s, loss = _stream_of(hidden), torch.empty(d.T, dtype=torch.float32, device=hidden.device)
-    ws = _cross_entropy_space(d, DH_CE_LOSS, hidden.device)
+    d, T, N, K = _cross_entropy(hidden, head, tokens, None, None)
+    s, loss = _stream_of(hidden), torch.empty(T, dtype=torch.float32, device=hidden.device)
+    ws = _cross_entropy_space(T, N, K, DH_CE_LOSS, hidden.device)
     _check("draft_head_cross_entropy_wait_probe",
-           lib().draft_head_cross_entropy_wait_probe(C.byref(d), loss.data_ptr(), ws.data_ptr(), ws.numel(), role, rounds,
+           lib().draft_head_cross_entropy_wait_probe(d, loss.data_ptr(), ws.data_ptr(), ws.numel(), role, rounds,
                                                      _ptr(_error_word(hidden.device)), s))
 
 

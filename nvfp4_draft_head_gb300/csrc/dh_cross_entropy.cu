@@ -59,6 +59,8 @@ struct Tokens {
         return id >= 0 && id < N ? id : -1;
     }
     __device__ __forceinline__ float w(int t) const { return weight != nullptr ? weight[t] : 1.0f; }
+    // Whether token t counts.
+    __device__ __forceinline__ bool live(int t) const { return w(t) != 0.0f && row(t) >= 0; }
 };
 
 // The power of two by which row weights are scaled before g is rounded: the largest finite
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Tokens tok, co
     if (rows.copy != nullptr) {
         constexpr int kPer = kJoinThreads / kJoinTokens;   // threads of a row
         const int row = blockIdx.x * kJoinTokens + threadIdx.x / kPer;
-        if (row < tok.T) rows.move(row, tok.w(row) != 0.0f && tok.row(row) >= 0, threadIdx.x % kPer, kPer);
+        if (row < tok.T) rows.move(row, tok.live(row), threadIdx.x % kPer, kPer);
     }
 }
 
@@ -273,6 +275,38 @@ struct Weights {   // g of a piece
     }
 };
 
+// The next accumulator's 128 columns of a thread's row, scaled and rounded, to `out` (`columns` of
+// them there, a multiple of 8): in 32-byte pieces where rows are so aligned (`wide`), else 16.
+// A row that does not count is zeros whatever it was multiplied by.
+template <class T, class A>
+__device__ __forceinline__ bool store_rows(A& acc, T* out, bool in, int columns, uint32_t offset, float scale, bool live, bool wide) {
+    const uint32_t at = acc.next();
+    if (at == ~0u) return false;
+#pragma unroll 1
+    for (int c = 0; c < kHalf && c < columns; c += 32) {
+        uint32_t r[32];
+        tc::tmem_load32(at + offset + c, r);
+        tc::tmem_load_wait();
+#pragma unroll
+        for (int i = 0; i < 32; i += 16) {
+            if (!in || c + i >= columns) break;
+            uint32_t v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = live ? rows::Elem<T>::pack2(__uint_as_float(r[i + 2 * j]) * scale, __uint_as_float(r[i + 2 * j + 1]) * scale) : 0u;
+            if (wide) {   // (then columns is a multiple of 16)
+                store32(out + c + i, v);
+            } else {
+                __stcg(reinterpret_cast<uint4*>(out + c + i), make_uint4(v[0], v[1], v[2], v[3]));
+                if (c + i + 8 < columns) __stcg(reinterpret_cast<uint4*>(out + c + i + 8), make_uint4(v[4], v[5], v[6], v[7]));
+            }
+        }
+        __syncwarp();
+    }
+    acc.release();
+    return true;
+}
+
 // dh: g (along the piece) times the piece's head rows, as 32-bit sums: [T][K] of whole tiles
 // and first parts, then the other parts of the tiles that are split, [split - 1][tile][256][256].
 template <class T>
@@ -287,10 +321,21 @@ struct Hidden {
         float* sum;
         float* parts;
         int add;      // to what earlier pieces left
+        // the results themselves, where one sum is all there is (null: sums)
+        T* out;
+        long long ld;
+        const uint32_t* wmax;
+        Tokens tok;
     };
-    __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int rank, Acc<Layout>& acc) {
+    template <class A2>
+    __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int rank, A2& acc) {
         const int local = rank * gemm::kRows + (warp & 3) * 32 + lane, row = t.m * kTM + local, half = warp >> 2;
         const int n0 = t.n * kTN + half * kHalf;
+        if (a.out != nullptr) {
+            const bool live = row < a.T_ && a.tok.live(row);
+            return store_rows<T>(acc, a.out + static_cast<size_t>(row) * a.ld + n0, row < a.T_, a.K - n0, (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf,
+                                 live ? exp2i(-scale_exponent<std::is_same<T, __half>::value>(*a.wmax)) : 0.0f, live, false);
+        }
         float* out;
         if (t.split <= 0) {
             out = a.sum + static_cast<size_t>(row) * a.K + n0;
@@ -340,37 +385,13 @@ struct Head {
         long long ld;
         int wide;                // rows 32-byte aligned
     };
-    __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int rank, Acc<Layout>& acc) {
+    template <class A2>
+    __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int rank, A2& acc) {
         const int row = (t.m * kPair + rank) * gemm::kRows + (warp & 3) * 32 + lane, half = warp >> 2;
         const int n0 = t.n * kTN + half * kHalf;
         const float scale = exp2i(-scale_exponent<kF16>(*a.wmax));
-        const uint32_t at = acc.next();
-        if (at == ~0u) return false;
-        const uint32_t from = at + (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf;
-        T* out = a.out + static_cast<size_t>(row) * a.ld + n0;
-#pragma unroll 1
-        for (int c = 0; c < kHalf && n0 + c < a.K; c += 32) {
-            uint32_t r[32];
-            tc::tmem_load32(from + c, r);
-            tc::tmem_load_wait();
-#pragma unroll
-            for (int i = 0; i < 32; i += 16) {
-                if (row >= a.rows || n0 + c + i >= a.K) break;
-                uint32_t v[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[j] = rows::Elem<T>::pack2(__uint_as_float(r[i + 2 * j]) * scale, __uint_as_float(r[i + 2 * j + 1]) * scale);
-                if (a.wide) {   // (then K is a multiple of 16)
-                    store32(out + c + i, v);
-                } else {
-                    __stcg(reinterpret_cast<uint4*>(out + c + i), make_uint4(v[0], v[1], v[2], v[3]));
-                    if (n0 + c + i + 8 < a.K) __stcg(reinterpret_cast<uint4*>(out + c + i + 8), make_uint4(v[4], v[5], v[6], v[7]));
-                }
-            }
-            __syncwarp();
-        }
-        acc.release();
-        return true;
+        return store_rows<T>(acc, a.out + static_cast<size_t>(row) * a.ld + n0, row < a.rows, a.K - n0,
+                             (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf, scale, true, a.wide);
     }
 };
 
@@ -390,7 +411,7 @@ __global__ void __launch_bounds__(256) sum_kernel(const Tokens tok, const Sums a
     const size_t total = static_cast<size_t>(tok.T) * per_row;
     for (size_t i = blockIdx.x * static_cast<size_t>(blockDim.x) + threadIdx.x; i < total; i += static_cast<size_t>(gridDim.x) * blockDim.x) {
         const int row = static_cast<int>(i / per_row), col = static_cast<int>(i % per_row) * 8;
-        const bool live = tok.w(row) != 0.0f && tok.row(row) >= 0;
+        const bool live = tok.live(row);
         const float4 x = __ldcs(reinterpret_cast<const float4*>(a.sum + i * 8)), y = __ldcs(reinterpret_cast<const float4*>(a.sum + i * 8 + 4));
         float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
         const int at = gemm::tile_index(a.tiles_m, a.tiles_n, row / kTM, col / kTN) - a.whole;
@@ -422,16 +443,18 @@ int piece_rows(int T, int N) {
 }
 
 // dh's tiles: whole ones as long as they fill all pairs of SMs, the rest in parts (at least
-// eight steps long) such that its rounds take the fewest steps, a part counted as eight more.
+// eight steps long) such that its rounds take the fewest steps, a part counted as eight more and
+// the sum of parts as twelve.
 // 4,096 x 64,026 x 2,560 (160 tiles for 76 pairs): see the top of the file.
 gemm::Shape hidden_tiles(int T, int K, int piece, unsigned int* error) {
     gemm::Shape s = gemm::whole_tiles(ceil_div(T, kTM), ceil_div(K, kTN), ceil_div(piece, 64), error);
-    const int pairs = sm_count() / 2 > 0 ? sm_count() / 2 : 1, rest = s.whole % pairs;
+    constexpr int pairs = 76;   // of the 152 SMs
+    const int rest = s.whole % pairs;
     if (rest == 0) return s;
     s.whole -= rest;
     long long least = 0;
     for (int p = 1; p <= 32 && (p == 1 || s.steps / p >= 8); ++p) {
-        const long long cost = static_cast<long long>(ceil_div(rest * p, pairs)) * ceil_div(s.steps, p) + 8 * p;
+        const long long cost = static_cast<long long>(ceil_div(rest * p, pairs)) * ceil_div(s.steps, p) + (p > 1 ? 12 + 8 * p : 0);
         if (p == 1 || cost < least) {
             least = cost;
             s.split_steps = ceil_div(s.steps, p);
@@ -483,15 +506,19 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
     T* hidden = dw ? reinterpret_cast<T*>(ws + sp.hidden) : nullptr;
     const Rows rows = {c.hidden, c.ld_hidden, c.K, hidden, wmax};
     cudaError_t e;
-    CUtensorMap map_h, map_w;
     using K1 = typename Stats<T, P>::Layout;
+    gemm::Jobs<Stats<T, P>> logits = {};
+    gemm::Jobs<Weights<T, P>> pieces = {};
+    CUtensorMap &map_h = logits.first.map_a, &map_w = logits.first.map_b;
     if ((e = gemm::encode_operand<K1, false>(&map_h, c.hidden, c.T, c.K, c.ld_hidden * 2, gemm::kRows)) != cudaSuccess) return e;
     if ((e = gemm::encode_operand<K1, false>(&map_w, c.head, c.N, c.K, c.ld_head * 2, K1::kBRows)) != cudaSuccess) return e;
+    pieces.first.map_a = map_h;
+    pieces.first.map_b = map_w;
     const int steps = ceil_div(c.K, K1::kK);
     const float* lse = c.lse_in;
     const float* rest = c.rest_in;
     if (loss) {
-        typename Stats<T, P>::Args a = {};
+        typename Stats<T, P>::Args& a = logits.first.args;
         a.shape = gemm::whole_tiles(tiles_m, ceil_div(c.N, kTN), steps, c.error);
         a.shape.rounds = c.probe_rounds;
         a.shape.idle = c.probe_role;
@@ -499,7 +526,7 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
         a.part = reinterpret_cast<float2*>(ws + sp.part);
         a.target = reinterpret_cast<float*>(ws + sp.target);
         a.wmax = wmax;
-        if ((e = gemm::launch<Stats<T, P>>(map_h, map_w, a, stream)) != cudaSuccess) return e;
+        if ((e = gemm::launch(logits, stream)) != cudaSuccess) return e;
         float* l = c.lse != nullptr ? c.lse : reinterpret_cast<float*>(ws + sp.lse);
         float* r = c.rest != nullptr ? c.rest : reinterpret_cast<float*>(ws + sp.rest);
         e = gemm::launch_early(join_kernel, dim3(static_cast<unsigned>(ceil_div(c.T, kJoinTokens))), kJoinThreads, 0, 1, stream, tok, a.part,
@@ -518,10 +545,11 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
     const gemm::Shape tiles_h = hidden_tiles(c.T, c.K, piece, c.error);   // of a full piece
     T* g = reinterpret_cast<T*>(ws + sp.g);
     float* sum = reinterpret_cast<float*>(ws + sp.sum);
+    const bool direct = c.N <= piece && ceil_div(ceil_div(c.N, 64), tiles_h.split_steps) == 1;   // dh is one sum
     int splits = 1;   // of dh's split tiles: those of the first piece, which is the largest
     for (int first = 0; first < c.N; first += piece) {
         const int count = c.N - first < piece ? c.N - first : piece;
-        typename Weights<T, P>::Args a = {};
+        typename Weights<T, P>::Args& a = pieces.first.args;
         a.shape = gemm::whole_tiles(tiles_m, ceil_div(count, kTN), steps, c.error);
         a.shape.b_mn = first;
         a.tok = tok;
@@ -532,13 +560,14 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
         a.ldg = piece;
         a.first = first;
         a.count = count;
-        if ((e = gemm::launch<Weights<T, P>>(map_h, map_w, a, stream)) != cudaSuccess) return e;
-        CUtensorMap map_a, map_b;
+        if ((e = gemm::launch(pieces, stream)) != cudaSuccess) return e;
+        gemm::Jobs<Hidden<T>, Head<T>> both = {};
         if (dh) {
             using L = typename Hidden<T>::Layout;
-            if ((e = gemm::encode_operand<L, false>(&map_a, g, c.T, count, static_cast<uint64_t>(piece) * 2, gemm::kRows)) != cudaSuccess) return e;
-            if ((e = gemm::encode_operand<L, true>(&map_b, c.head, c.K, c.N, c.ld_head * 2, 0)) != cudaSuccess) return e;
-            typename Hidden<T>::Args b = {};
+            auto& job = both.first;
+            if ((e = gemm::encode_operand<L, false>(&job.map_a, g, c.T, count, static_cast<uint64_t>(piece) * 2, gemm::kRows)) != cudaSuccess) return e;
+            if ((e = gemm::encode_operand<L, true>(&job.map_b, c.head, c.K, c.N, c.ld_head * 2, 0)) != cudaSuccess) return e;
+            auto& b = job.args;
             b.shape = tiles_h;
             b.shape.steps = ceil_div(count, L::kK);
             b.shape.splits = ceil_div(b.shape.steps, tiles_h.split_steps);
@@ -548,26 +577,30 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
             b.sum = sum;
             b.parts = reinterpret_cast<float*>(ws + sp.parts);
             b.add = first > 0;
+            if (direct) b.out = static_cast<T*>(c.dhidden);
+            b.ld = c.ld_dhidden;
+            b.wmax = wmax;
+            b.tok = tok;
             if (first == 0) splits = b.shape.splits;
-            if ((e = gemm::launch<Hidden<T>>(map_a, map_b, b, stream)) != cudaSuccess) return e;
         }
         if (dw) {
             using L = typename Head<T>::Layout;
-            if ((e = gemm::encode_operand<L, true>(&map_a, g, count, c.T, static_cast<uint64_t>(piece) * 2, 0)) != cudaSuccess) return e;
-            if ((e = gemm::encode_operand<L, true>(&map_b, hidden, c.K, c.T, static_cast<uint64_t>(c.K) * 2, 0)) != cudaSuccess) return e;
-            typename Head<T>::Args b = {};
-            const int all = ceil_div(c.T, L::kK);
-            b.shape = gemm::whole_tiles(ceil_div(count, kTM), ceil_div(c.K, kTN), all, c.error);
+            auto& job = both.second;
+            if ((e = gemm::encode_operand<L, true>(&job.map_a, g, count, c.T, static_cast<uint64_t>(piece) * 2, 0)) != cudaSuccess) return e;
+            if ((e = gemm::encode_operand<L, true>(&job.map_b, hidden, c.K, c.T, static_cast<uint64_t>(c.K) * 2, 0)) != cudaSuccess) return e;
+            auto& b = job.args;
+            b.shape = gemm::whole_tiles(ceil_div(count, kTM), ceil_div(c.K, kTN), ceil_div(c.T, L::kK), c.error);
             b.rows = count;
             b.K = c.K;
             b.wmax = wmax;
             b.out = static_cast<T*>(c.dhead) + static_cast<size_t>(first) * c.ld_dhead;
             b.ld = c.ld_dhead;
             b.wide = reinterpret_cast<uintptr_t>(c.dhead) % 32 == 0 && c.K % 16 == 0 && c.ld_dhead % 16 == 0;
-            if ((e = gemm::launch<Head<T>>(map_a, map_b, b, stream)) != cudaSuccess) return e;
         }
+        both.first.args.shape.error = c.error;   // (one gradient alone: the other has no tiles)
+        if ((e = gemm::launch(both, stream)) != cudaSuccess) return e;
     }
-    if (dh) {
+    if (dh && !direct) {
         const size_t total = static_cast<size_t>(c.T) * (c.K / 8), want = (total + 255) / 256, cap = static_cast<size_t>(sm_count()) * 8;
         const Sums sums = {sum, reinterpret_cast<float*>(ws + sp.parts), tiles_h.tiles_m, tiles_h.tiles_n, tiles_h.whole, splits};
         e = gemm::launch_early(sum_kernel<T>, dim3(static_cast<unsigned>(want < cap ? want : cap)), 256, 0, 1, stream, tok, sums, c.K, wmax,

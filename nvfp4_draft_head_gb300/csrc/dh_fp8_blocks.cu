@@ -190,7 +190,7 @@ struct Product {
         float* parts;         // the contraction in parts: their sums, [split][M][ldp]
         long long ldp;
     };
-    __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int rank, Acc<Layout>& acc) {
+    __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int, Acc<Layout>& acc) {
         constexpr int kPart = Layout::kPart;
         static_assert(kPart == 64 && Layout::kP == 1, "a warp's columns lie in one block of the weight");
         const int row0 = t.m * gemm::kRows + (warp & 3) * 32, row = row0 + lane, steps = t.steps;
@@ -297,11 +297,11 @@ cudaError_t product(const Fp8BlockArgs& f, const Plan& plan, const uint8_t* code
     using P = Product<TY, GRADIENT, TN>;
     using L = typename P::Layout;
     const int width = GRADIENT ? f.N : f.K, out = GRADIENT ? f.K : f.N, kb = ceil_div(f.K, kBlock);
-    CUtensorMap map_a, map_b;
-    cudaError_t e = gemm::encode_operand<L, false>(&map_a, codes, f.M, width, ldc, gemm::kRows);
+    gemm::Jobs<P> jobs = {};
+    cudaError_t e = gemm::encode_operand<L, false>(&jobs.first.map_a, codes, f.M, width, ldc, gemm::kRows);
     if (e != cudaSuccess) return e;
-    if ((e = gemm::encode_operand<L, GRADIENT>(&map_b, f.q, out, width, f.K, L::kBRows)) != cudaSuccess) return e;
-    typename P::Args a = {};
+    if ((e = gemm::encode_operand<L, GRADIENT>(&jobs.first.map_b, f.q, out, width, f.K, L::kBRows)) != cudaSuccess) return e;
+    typename P::Args& a = jobs.first.args;
     const int steps = ceil_div(width, kBlock);
     a.shape = gemm::whole_tiles(ceil_div(f.M, gemm::kRows), ceil_div(out, L::kTN), steps, f.error);
     a.shape.rounds = f.probe_rounds;
@@ -316,13 +316,13 @@ cudaError_t product(const Fp8BlockArgs& f, const Plan& plan, const uint8_t* code
     a.ldy = f.ldy;
     const uintptr_t at = reinterpret_cast<uintptr_t>(f.y) | (f.M == 1 ? 0 : static_cast<uintptr_t>(f.ldy) * sizeof(TY));
     a.align = at % 32 == 0 ? kPieces : at % 4 == 0 ? kWords : kAny;
-    if (plan.parts == 1) return gemm::launch<P>(map_a, map_b, a, s);
+    if (plan.parts == 1) return gemm::launch(jobs, s);
     a.shape.whole = 0;
     a.shape.splits = plan.parts;
     a.shape.split_steps = plan.part_steps;
     a.parts = parts;
     a.ldp = part_stride(out);
-    if ((e = gemm::launch<P>(map_a, map_b, a, s)) != cudaSuccess) return e;
+    if ((e = gemm::launch(jobs, s)) != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(ceil_div(out, 256)), static_cast<unsigned>(f.M));   // (parts: M is below 152 x 128)
     return gemm::launch_early(sum_kernel<TY>, grid, 256, 0, 1, s, parts, plan.parts, f.M, out, a.ldp, a.y, a.ldy);
 }

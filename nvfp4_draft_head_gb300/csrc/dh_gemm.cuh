@@ -170,6 +170,7 @@ __device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* ma
 }
 
 // The epilogue warps' turn through the accumulators.
+// (L: any of a launch's layouts, which differ in their operands alone)
 template <class L>
 struct Acc {
     Sync& sy;
@@ -195,21 +196,136 @@ struct Acc {
 
 // Op: Layout, Args (with `Shape shape`), kFormat (idesc_f), kChunk (steps of K that share an
 // accumulator: results that are scaled step by step take 1, those of a tile summed throughout by
-// the tensor cores kWholeTile), kAKeep / kBKeep (the operand is
-// read by other tiles too: kept in L2), and tile(args, tile, warp, lane, rank, acc), false when a
-// wait gave up.
+// the tensor cores kWholeTile), kAKeep / kBKeep (the operand is read by other tiles too: kept in
+// L2), and tile(args, tile, warp, lane, rank, acc), false when a wait gave up.
+
+// One product of a launch: its operands' maps and its arguments.
 template <class Op>
-__global__ void __launch_bounds__(Op::Layout::kThreads, 1) product_kernel(const __grid_constant__ CUtensorMap map_a,
-                                                              const __grid_constant__ CUtensorMap map_b,
-                                                              const __grid_constant__ typename Op::Args a) {
+struct Job {
+    using Operator = Op;
+    CUtensorMap map_a, map_b;
+    typename Op::Args args;
+};
+
+// The place of a role in the ring of stages, and of the issuer in the accumulators.
+struct Ring {
+    uint32_t it, st, phase, n;
+    template <class L>
+    __device__ __forceinline__ void step() {
+        ++it;
+        if (++st == static_cast<uint32_t>(L::kStages)) {
+            st = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+// A tile's copies, by the producer's warp.
+template <class Op>
+__device__ __forceinline__ bool produce(const Job<Op>& job, const Shape& s, int unit, int rank, Sync& sy, uint8_t* smem, Ring& r) {
     using L = typename Op::Layout;
+    constexpr int P = L::kP;
+    const uint64_t pol_a = Op::kAKeep ? policy_evict_last() : policy_evict_first();
+    const uint64_t pol_b = Op::kBKeep ? policy_evict_last() : policy_evict_first();
+    const Tile t = tile_at(job.args.shape, unit);
+    const Shape& o = job.args.shape;
+    const int am = o.a_mn + (t.m * P + rank) * kRows, bn = o.b_mn + t.n * L::kTN + rank * L::kBRows, k0 = t.k0 * L::kK;
+    for (int k = 0; k < t.steps; ++k) {
+        if (r.it >= static_cast<uint32_t>(L::kStages) && !__all_sync(~0u, wait_or_abort(sy, &sy.empty[r.st], r.phase, s))) return false;
+        uint8_t* dst = smem + r.st * L::kBytes;
+        uint32_t bar;
+        if constexpr (P == 1) bar = smem_u32(&sy.full[r.st]);
+        else bar = cluster_map(&sy.full[r.st], 0);
+        if (elect_one()) {
+            if (rank == 0) mbar_arrive_expect_tx(&sy.full[r.st], P * L::kBytes);
+            load_operand<L, L::kAMn>(dst, &job.map_a, kRows, am, o.a_k + k0 + k * L::kK, bar, pol_a);
+            load_operand<L, L::kBMn>(dst + L::kABytes, &job.map_b, L::kBRows, bn, o.b_k + k0 + k * L::kK, bar, pol_b);
+        }
+        __syncwarp();
+        r.step<L>();
+    }
+    return true;
+}
+
+// A tile's matrix instructions, by the issuer's warp.
+template <class Op>
+__device__ __forceinline__ bool issue(const Job<Op>& job, const Shape& s, int unit, uint32_t tmem, Sync& sy, uint8_t* smem, Ring& r) {
+    using L = typename Op::Layout;
+    constexpr int P = L::kP;
+    constexpr uint32_t kIdesc = tc::idesc_f(Op::kFormat, L::kAMn, L::kBMn, kRows * P, L::kTN);
+    constexpr bool kF8 = L::kElem == 1;
+    // 32 bytes of K: along a 128-byte row, or (MN-major) as many whole rows as elements
+    constexpr uint32_t kStepA = L::kAMn ? 32 / L::kElem * 128 / 16 : 2, kStepB = L::kBMn ? 32 / L::kElem * 128 / 16 : 2;
+    const uint32_t base = smem_u32(smem);
+    const uint64_t first_a = L::kAMn ? tc::desc_operand_mn(base, L::kK) : tc::desc_operand(base);
+    const uint64_t first_b = L::kBMn ? tc::desc_operand_mn(base + L::kABytes, L::kK) : tc::desc_operand(base + L::kABytes);
+    const int steps = tile_at(job.args.shape, unit).steps;
+    for (int k = 0; k < steps; ++k) {
+        const uint32_t use = r.n / L::kBuffers, b = r.n % L::kBuffers, d = tmem + b * L::kTN;
+        bool ok = wait_or_abort(sy, &sy.full[r.st], r.phase, s);   // the operands have landed,
+        if (k % Op::kChunk == 0 && use > 0)                        // and the accumulator has been read
+            ok = ok && wait_or_abort(sy, &sy.acc_empty[b], (use - 1) & 1, s);
+        if (!__all_sync(~0u, ok)) return false;
+        tc::fence_after_sync();
+        const uint64_t da = first_a + r.st * (L::kBytes / 16), db = first_b + r.st * (L::kBytes / 16);
+        const bool last = (k + 1) % Op::kChunk == 0 || k == steps - 1;
+        if (elect_one()) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) tc::mma_f<P, kF8>(d, da + kStepA * j, db + kStepB * j, kIdesc, k % Op::kChunk != 0 || j > 0);
+            if (last) tc::commit_all<P>(&sy.acc_full[b]);
+            tc::commit_all<P>(&sy.empty[r.st]);
+        }
+        __syncwarp();
+        if (last) ++r.n;
+        r.step<L>();
+    }
+    return true;
+}
+
+// Accumulators of a tile.
+template <class Op>
+__device__ __forceinline__ int chunks_of(const Job<Op>& job, int unit) {
+    return (tile_at(job.args.shape, unit).steps - 1) / Op::kChunk + 1;
+}
+
+// One product, or two of the same layout sizes that do not depend on one another: the second's
+// tiles follow the first's, and fill its last round over the SMs.
+template <class Op, class Op2 = void>
+struct Jobs {
+    using Layout = typename Op::Layout;
+    Job<Op> first;
+    Job<Op2> second;
+    static_assert(Layout::kP == Op2::Layout::kP && Layout::kBytes == Op2::Layout::kBytes && Layout::kTN == Op2::Layout::kTN &&
+                  Layout::kEpiWarps == Op2::Layout::kEpiWarps, "one ring for both");
+    __host__ __device__ int units() const { return first.args.shape.units() + second.args.shape.units(); }
+    // f(job, unit) of the job that this unit belongs to
+    template <class F>
+    __device__ __forceinline__ auto at(int unit, F f) const {
+        const int n = first.args.shape.units();
+        return unit < n ? f(first, unit) : f(second, unit - n);
+    }
+};
+template <class Op>
+struct Jobs<Op, void> {
+    using Layout = typename Op::Layout;
+    Job<Op> first;
+    __host__ __device__ int units() const { return first.args.shape.units(); }
+    template <class F>
+    __device__ __forceinline__ auto at(int unit, F f) const {
+        return f(first, unit);
+    }
+};
+
+template <class J>
+__global__ void __launch_bounds__(J::Layout::kThreads, 1) product_kernel(const __grid_constant__ J jobs) {
+    using L = typename J::Layout;
     constexpr int P = L::kP, kStages = L::kStages;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Sync sy;
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = P == 1 ? 0 : static_cast<int>(cluster_ctarank());
-    const Shape& s = a.shape;
+    const Shape& s = jobs.first.args.shape;   // (its error word, limits and self-test are the launch's)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sy.full[i], 1);
@@ -235,80 +351,25 @@ __global__ void __launch_bounds__(Op::Layout::kThreads, 1) product_kernel(const 
     tc::fence_after_sync();
     programmatic_wait();
     const uint32_t tmem = sy.tmem;
-    const int tiles = s.units();
+    const int units = jobs.units();
     const int first = static_cast<int>(blockIdx.x) / P, stride = static_cast<int>(gridDim.x) / P;
 
     // (the producer's and the issuer's warps run their loops whole, one elected lane issues)
     if (warp == L::kProducer && s.idle != kRoleProducer) {
-        const uint64_t keep = policy_evict_last(), once = policy_evict_first();
-        const uint64_t pol_a = Op::kAKeep ? keep : once, pol_b = Op::kBKeep ? keep : once;
-        uint32_t it = 0, st = 0, phase = 1;
-        bool ok = true;
-        for (int i = first; ok && i < tiles; i += stride) {
-            const Tile t = tile_at(s, i);
-            const int am = s.a_mn + (t.m * P + rank) * kRows, bn = s.b_mn + t.n * L::kTN + rank * L::kBRows;
-            const int steps = t.steps, k0 = t.k0 * L::kK;
-            for (int k = 0; k < steps; ++k, ++it) {
-                if (it >= static_cast<uint32_t>(kStages) && !(ok = __all_sync(~0u, wait_or_abort(sy, &sy.empty[st], phase, s)))) break;
-                uint8_t* dst = smem + st * L::kBytes;
-                uint32_t bar;
-                if constexpr (P == 1) bar = smem_u32(&sy.full[st]);
-                else bar = cluster_map(&sy.full[st], 0);
-                if (elect_one()) {
-                    if (rank == 0) mbar_arrive_expect_tx(&sy.full[st], P * L::kBytes);
-                    load_operand<L, L::kAMn>(dst, &map_a, kRows, am, s.a_k + k0 + k * L::kK, bar, pol_a);
-                    load_operand<L, L::kBMn>(dst + L::kABytes, &map_b, L::kBRows, bn, s.b_k + k0 + k * L::kK, bar, pol_b);
-                }
-                __syncwarp();
-                if (++st == static_cast<uint32_t>(kStages)) {
-                    st = 0;
-                    phase ^= 1u;
-                }
-            }
-        }
+        Ring r = {0, 0, 1, 0};   // the phase of `empty` before the current use of the slot
+        for (int i = first; i < units; i += stride)
+            if (!jobs.at(i, [&](const auto& job, int unit) { return produce(job, s, unit, rank, sy, smem, r); })) break;
         // The copies in flight land, and the last signals of other CTAs, before the CTAs end,
         // whoever gave up (a pair's copies complete on rank 0's barriers; all bounded).
-        for (uint32_t b = it > static_cast<uint32_t>(kStages) ? it - kStages : 0; b < it; ++b) {
+        for (uint32_t b = r.it > static_cast<uint32_t>(kStages) ? r.it - kStages : 0; b < r.it; ++b) {
             if (rank == 0 && !mbar_wait(&sy.full[b % kStages], (b / kStages) & 1, kDrainRounds)) break;
             if (P > 1 && !mbar_wait(&sy.empty[b % kStages], (b / kStages) & 1, kDrainRounds)) break;
         }
-        if (lane == 0) sy.copies = it;
+        if (lane == 0) sy.copies = r.it;
     } else if (warp == L::kIssuer && rank == 0 && s.idle != kRoleIssuer) {
-        constexpr uint32_t kIdesc = tc::idesc_f(Op::kFormat, L::kAMn, L::kBMn, kRows * P, L::kTN);
-        constexpr bool kF8 = L::kElem == 1;
-        // 32 bytes of K: along a 128-byte row, or (MN-major) as many whole rows as elements
-        constexpr uint32_t kStepA = L::kAMn ? 32 / L::kElem * 128 / 16 : 2, kStepB = L::kBMn ? 32 / L::kElem * 128 / 16 : 2;
-        const uint32_t base = smem_u32(smem);
-        const uint64_t first_a = L::kAMn ? tc::desc_operand_mn(base, L::kK) : tc::desc_operand(base);
-        const uint64_t first_b = L::kBMn ? tc::desc_operand_mn(base + L::kABytes, L::kK) : tc::desc_operand(base + L::kABytes);
-        uint32_t n = 0, st = 0, phase = 0;
-        bool ok = true;
-        for (int i = first; ok && i < tiles; i += stride) {
-            const int steps = tile_at(s, i).steps;
-            for (int k = 0; k < steps; ++k) {
-                const uint32_t use = n / L::kBuffers;
-                ok = wait_or_abort(sy, &sy.full[st], phase, s);   // the operands have landed,
-                if (k % Op::kChunk == 0 && use > 0)                // and the accumulator has been read
-                    ok = ok && wait_or_abort(sy, &sy.acc_empty[n % L::kBuffers], (use - 1) & 1, s);
-                if (!(ok = __all_sync(~0u, ok))) break;
-                const uint64_t da = first_a + st * (L::kBytes / 16), db = first_b + st * (L::kBytes / 16);
-                tc::fence_after_sync();
-                const uint32_t b = n % L::kBuffers, d = tmem + b * L::kTN;
-                const bool last = (k + 1) % Op::kChunk == 0 || k == steps - 1;
-                if (elect_one()) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) tc::mma_f<P, kF8>(d, da + kStepA * j, db + kStepB * j, kIdesc, k % Op::kChunk != 0 || j > 0);
-                    if (last) tc::commit_all<P>(&sy.acc_full[b]);
-                    tc::commit_all<P>(&sy.empty[st]);
-                }
-                __syncwarp();
-                if (last) ++n;
-                if (++st == static_cast<uint32_t>(kStages)) {
-                    st = 0;
-                    phase ^= 1u;
-                }
-            }
-        }
+        Ring r = {0, 0, 0, 0};
+        for (int i = first; i < units; i += stride)
+            if (!jobs.at(i, [&](const auto& job, int unit) { return issue(job, s, unit, tmem, sy, smem, r); })) break;
         // the issued instructions finish before tensor memory is freed, whoever gave up (bounded)
         if (elect_one()) tc::commit_own<P>(&sy.issued);
         __syncwarp();
@@ -318,13 +379,16 @@ __global__ void __launch_bounds__(Op::Layout::kThreads, 1) product_kernel(const 
         // place of one per warp)
         uint32_t n = 0;
         bool ok = true;
-        for (int i = first; ok && i < tiles; i += stride)
-            for (int u = (tile_at(s, i).steps - 1) / Op::kChunk; ok && u >= 0; --u, ++n)
+        for (int i = first; ok && i < units; i += stride)
+            for (int u = jobs.at(i, [&](const auto& job, int unit) { return chunks_of(job, unit); }); ok && u > 0; --u, ++n)
                 if ((ok = wait_or_abort(sy, &sy.acc_empty[n % L::kBuffers], (n / L::kBuffers) & 1, s))) arrive_rank0(&sy.acc_empty[n % L::kBuffers]);
     } else if (warp < L::kEpiWarps && s.idle != kRoleEpilogue) {
         Acc<L> acc(sy, s, tmem);
-        for (int i = first; i < tiles; i += stride)
-            if (!Op::tile(a, tile_at(s, i), warp, lane, rank, acc)) break;
+        for (int i = first; i < units; i += stride)
+            if (!jobs.at(i, [&](const auto& job, int unit) {
+                    return std::decay_t<decltype(job)>::Operator::tile(job.args, tile_at(job.args.shape, unit), warp, lane, rank, acc);
+                }))
+                break;
     }
     __syncwarp();
     tc::fence_before_sync();
@@ -387,9 +451,9 @@ cudaError_t encode_operand(CUtensorMap* map, const void* base, uint64_t mn, uint
     return MN ? encode_map(map, base, L::kElem, mn, k, ld_bytes, L::kK) : encode_map(map, base, L::kElem, k, mn, ld_bytes, box_mn);
 }
 
-template <class Op>
-cudaError_t launch(const CUtensorMap& map_a, const CUtensorMap& map_b, typename Op::Args a, cudaStream_t stream) {
-    using L = typename Op::Layout;
+template <class J>
+cudaError_t launch(J& jobs, cudaStream_t stream) {
+    using L = typename J::Layout;
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     constexpr int kDevices = 64;
@@ -399,18 +463,17 @@ cudaError_t launch(const CUtensorMap& map_a, const CUtensorMap& map_b, typename 
     if (e != cudaSuccess) return e;
     if (dev >= kDevices) return cudaErrorInvalidDevice;
     if (!known[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(product_kernel<Op>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+        e = cudaFuncSetAttribute(product_kernel<J>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
         if (e != cudaSuccess) return e;
         known[dev].store(true, std::memory_order_release);
     }
-    if (a.shape.rounds == 0) {
-        a.shape.rounds = kWaitLimit / kWaitSlices;
-        a.shape.idle = -1;
+    Shape& s = jobs.first.args.shape;
+    if (s.rounds == 0) {
+        s.rounds = kWaitLimit / kWaitSlices;
+        s.idle = -1;
     }
-    const long long tiles = a.shape.units();
-    const long long most = sms / L::kP;
-    return launch_early(product_kernel<Op>, dim3(static_cast<unsigned>((tiles < most ? tiles : most) * L::kP)), L::kThreads, L::kSmem, L::kP, stream,
-                        map_a, map_b, a);
+    const int units = jobs.units(), most = sms / L::kP;
+    return launch_early(product_kernel<J>, dim3(static_cast<unsigned>((units < most ? units : most) * L::kP)), L::kThreads, L::kSmem, L::kP, stream, jobs);
 }
 
 }  // namespace gemm
