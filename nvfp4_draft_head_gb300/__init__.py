@@ -1178,8 +1178,8 @@ def linear_cross_entropy_forward(hidden: torch.Tensor, head: torch.Tensor, token
         return _on_stream(stream, linear_cross_entropy_forward, hidden, head, tokens, weights, row_of)
     d, T, N, K = _cross_entropy(hidden, head, tokens, weights, row_of)
     device = hidden.device
-    loss = torch.empty(T, dtype=torch.float32, device=device)
-    lse, rest = torch.empty((2, T), dtype=torch.float32, device=device).unbind()
+    f32 = torch.float32
+    loss, lse, rest = torch.empty(T, dtype=f32, device=device), torch.empty(T, dtype=f32, device=device), torch.empty(T, dtype=f32, device=device)
     if T > 0:
         s = _stream_of(hidden)
         ws = _cross_entropy_space(T, N, K, DH_CE_LOSS, device)

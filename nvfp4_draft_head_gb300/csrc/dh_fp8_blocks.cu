@@ -174,7 +174,7 @@ __device__ __forceinline__ void store64(TY* y, long long ldy, const float (&v)[6
 // MN-major (its rows along the contraction) for dx.
 template <class TY, bool GRADIENT, int TN>
 struct Product {
-    using Layout = gemm::Layout<1, TN, 1, false, GRADIENT, TN / 16>;
+    using Layout = gemm::Layout<1, TN, 1, false, GRADIENT, TN / 16, 2>;
     static constexpr int kFormat = 0;
     static constexpr int kChunk = 1;
     static constexpr bool kAKeep = true, kBKeep = true;

@@ -81,10 +81,10 @@ __host__ __device__ inline int tile_index(int tiles_m, int tiles_n, int m, int n
     return g * kGroup * tiles_n + n * rows + m - g * kGroup;
 }
 
-template <int P, int TN, int ELEM, bool A_MN, bool B_MN, int EPI = 8>
+template <int P, int TN, int ELEM, bool A_MN, bool B_MN, int EPI = 8, int ISSUERS = 1>
 struct Layout {
     static constexpr int kP = P, kTN = TN, kElem = ELEM;
-    static constexpr int kEpiWarps = EPI, kProducer = EPI, kIssuer = EPI + 1, kThreads = 32 * (EPI + 2);
+    static constexpr int kEpiWarps = EPI, kProducer = EPI, kIssuer = EPI + 1, kIssuers = ISSUERS, kThreads = 32 * (EPI + 1 + ISSUERS);
     static constexpr int kPart = TN / (EPI / 4);                        // columns of an epilogue warp
     static constexpr bool kAMn = A_MN, kBMn = B_MN;
     static constexpr int kK = kStageBytes / ELEM;                       // elements of K per stage
@@ -92,11 +92,14 @@ struct Layout {
     static constexpr int kBRows = TN / P;                               // columns of B that a CTA loads
     static constexpr int kABytes = kRows * kStageBytes, kBBytes = kBRows * kStageBytes;
     static constexpr int kBytes = kABytes + kBBytes;
-    static constexpr int kStages = (227 * 1024 - 1024 - 1024) / kBytes < 8 ? (227 * 1024 - 1024 - 1024) / kBytes : 8;
+    // stages: a multiple of the issuers, which take the steps in turn (a wait by parity needs a
+    // waiter that has seen the slot's phase before)
+    static constexpr int kFit = (227 * 1024 - 1024 - 1024) / kBytes, kStages = (kFit < 8 ? kFit : 8) / ISSUERS * ISSUERS;
     static constexpr int kSmem = kStages * kBytes + 1024;
     static constexpr int kBuffers = 512 / TN < 4 ? 512 / TN : 4;        // accumulators in tensor memory
     static_assert(!(A_MN && kRows % kSpan != 0) && !(B_MN && kBRows % kSpan != 0), "whole boxes");
     static_assert(kStages <= 8 && kBytes % 1024 == 0 && TN % 32 == 0 && kStages >= 3, "stage layout");
+    static_assert(kBuffers % ISSUERS == 0, "and the accumulators");
 };
 
 struct Sync {
@@ -247,11 +250,14 @@ __device__ __forceinline__ bool produce(const Job<Op>& job, const Shape& s, int 
     return true;
 }
 
-// A tile's matrix instructions, by the issuer's warp.
+// A tile's matrix instructions, by an issuer's warp. With an accumulator per step two issuers take
+// the steps in turn: one alone takes 500 cycles for a step's waits and instructions, as
+// long as they run.
 template <class Op>
-__device__ __forceinline__ bool issue(const Job<Op>& job, const Shape& s, int unit, uint32_t tmem, Sync& sy, uint8_t* smem, Ring& r) {
+__device__ __forceinline__ bool issue(const Job<Op>& job, const Shape& s, int unit, int issuer, uint32_t tmem, Sync& sy, uint8_t* smem, Ring& r) {
     using L = typename Op::Layout;
     constexpr int P = L::kP;
+    static_assert(L::kIssuers == 1 || Op::kChunk == 1, "one issuer's instructions sum up in order");
     constexpr uint32_t kIdesc = tc::idesc_f(Op::kFormat, L::kAMn, L::kBMn, kRows * P, L::kTN);
     constexpr bool kF8 = L::kElem == 1;
     // 32 bytes of K: along a 128-byte row, or (MN-major) as many whole rows as elements
@@ -261,6 +267,11 @@ __device__ __forceinline__ bool issue(const Job<Op>& job, const Shape& s, int un
     const uint64_t first_b = L::kBMn ? tc::desc_operand_mn(base + L::kABytes, L::kK) : tc::desc_operand(base + L::kABytes);
     const int steps = tile_at(job.args.shape, unit).steps;
     for (int k = 0; k < steps; ++k) {
+        if (L::kIssuers > 1 && r.it % L::kIssuers != static_cast<uint32_t>(issuer)) {
+            ++r.n;
+            r.step<L>();
+            continue;
+        }
         const uint32_t use = r.n / L::kBuffers, b = r.n % L::kBuffers, d = tmem + b * L::kTN;
         bool ok = wait_or_abort(sy, &sy.full[r.st], r.phase, s);   // the operands have landed,
         if (k % Op::kChunk == 0 && use > 0)                        // and the accumulator has been read
@@ -335,7 +346,7 @@ __global__ void __launch_bounds__(J::Layout::kThreads, 1) product_kernel(const _
             mbar_init(&sy.acc_full[i], 1);
             mbar_init(&sy.acc_empty[i], L::kEpiWarps + (rank == 0 ? P - 1 : 0));   // rank 0: rank 1's forwarder too
         }
-        mbar_init(&sy.issued, 1);
+        mbar_init(&sy.issued, L::kIssuers);
         mbar_init_fence();
         sy.abort = 0u;
         sy.copies = 0u;
@@ -366,10 +377,10 @@ __global__ void __launch_bounds__(J::Layout::kThreads, 1) product_kernel(const _
             if (P > 1 && !mbar_wait(&sy.empty[b % kStages], (b / kStages) & 1, kDrainRounds)) break;
         }
         if (lane == 0) sy.copies = r.it;
-    } else if (warp == L::kIssuer && rank == 0 && s.idle != kRoleIssuer) {
+    } else if (warp >= L::kIssuer && rank == 0 && s.idle != kRoleIssuer) {
         Ring r = {0, 0, 0, 0};
         for (int i = first; i < units; i += stride)
-            if (!jobs.at(i, [&](const auto& job, int unit) { return issue(job, s, unit, tmem, sy, smem, r); })) break;
+            if (!jobs.at(i, [&](const auto& job, int unit) { return issue(job, s, unit, warp - L::kIssuer, tmem, sy, smem, r); })) break;
         // the issued instructions finish before tensor memory is freed, whoever gave up (bounded)
         if (elect_one()) tc::commit_own<P>(&sy.issued);
         __syncwarp();
