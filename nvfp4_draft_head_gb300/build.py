@@ -22,7 +22,8 @@ SOURCES = ["dh_abi.cu", "dh_quantize.cu", "dh_gemv.cu", "dh_gemv_nvfp4.cu", "dh_
            "dh_gemv_bf16.cu", "dh_static_ws.cu", "dh_gemv_nvfp4p.cu", "dh_gemv_nvfp4p_ldg.cu", "dh_pack.cu",
            "dh_gemv_w8a8.cu", "dh_gemv_linear.cu", "dh_logprobs.cu", "dh_distill.cu", "dh_rows_abi.cu", "dh_matmul.cu",
            "dh_matmul_abi.cu", "dh_tma.cu", "dh_cross_entropy.cu", "dh_cross_entropy_abi.cu",
-           "dh_fp8_blocks.cu", "dh_fp8_few.cu", "dh_fp8_blocks_abi.cu"]
+           "dh_fp8_blocks.cu", "dh_fp8_few_bf16.cu", "dh_fp8_few_f16.cu", "dh_fp8_few_f32.cu",
+           "dh_fp8_blocks_abi.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # -fno-gnu-unique: the launchers' per-device caches (function-local statics of
 # templates) stay private to each loaded copy of the library instead of being

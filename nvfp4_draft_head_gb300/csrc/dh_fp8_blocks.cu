@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const T* __restrict
     const bool in = m < static_cast<unsigned>(M);
     const int k = static_cast<int>(b) * kBlock + (threadIdx.x & 7) * 16, n = in ? min(16, width - k) : 0;
     uint4 w;
-    const float s = encode16<T, VEC>(x + static_cast<size_t>(m) * ldx + k, n, w);
+    const float s = encode16<T, VEC>(Rows<T>{x, ldx, M, width}, static_cast<int>(m), k, n, w);
     if (in && (threadIdx.x & 7) == 0) scales[static_cast<size_t>(b) * M + m] = s;
     if (n > 0) *reinterpret_cast<uint4*>(codes + static_cast<size_t>(m) * ldc + k) = w;
 }
@@ -275,6 +275,7 @@ Plan plan_of(int M, int out, int width) {
     }
     const float read = static_cast<float>(width) * out * (1.0f / 4.4e6f);
     if (best.us < read) best.us = read;
+    best.us += 3.0f;   // quantising before it
     return best;
 }
 long long part_stride(int out) { return (out + 7) / 8 * 8; }
@@ -336,11 +337,20 @@ cudaError_t run_many(const Fp8BlockArgs& f, const Plan& p, const uint8_t* codes,
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
+// Whether a product takes the form of few tokens.
+bool take_few(int M, int out, int width, FewPlan* few, Plan* many) {
+    *few = few_plan(M, out, width);
+    *many = plan_of(M, out, width);
+    return few->splits > 0 && (M <= 16 || few->us <= many->us);
+}
+
+template <class TY>
 cudaError_t run(const Fp8BlockArgs& f, cudaStream_t s) {
     const int width = f.gradient ? f.N : f.K, out = f.gradient ? f.K : f.N, ldc = ceil_div(width, 16) * 16;
-    if (f.M <= kFusedTokens && fused_fits(ceil_div(width, kBlock))) return launch_few(f, nullptr, 0, nullptr, s);
-    float few_us = 0.0f;
-    const bool few = f.M > kFusedTokens && few_supported(f, &few_us);
+    FewPlan few;
+    Plan p;
+    const bool use_few = take_few(f.M, out, width, &few, &p);
+    if (use_few && few.fused) return launch_few<TY>(f, few, nullptr, 0, nullptr, s);
     uint8_t* codes = static_cast<uint8_t*>(f.ws);
     float* scales = reinterpret_cast<float*>(codes + up256(static_cast<size_t>(f.M) * ldc));
     float* parts = reinterpret_cast<float*>(codes + up256(static_cast<size_t>(f.M) * ldc) +
@@ -349,17 +359,16 @@ cudaError_t run(const Fp8BlockArgs& f, cudaStream_t s) {
                           : f.x_type == DH_T_F16 ? quantize<__half>(f, width, codes, ldc, scales, s)
                                                  : quantize<float>(f, width, codes, ldc, scales, s);
     if (e != cudaSuccess) return e;
-    const Plan p = plan_of(f.M, out, width);
-    if (few && few_us <= p.us) return launch_few(f, codes, ldc, scales, s);
-    return f.y_type == DH_T_BF16  ? run_many<__nv_bfloat16>(f, p, codes, ldc, scales, parts, s)
-           : f.y_type == DH_T_F16 ? run_many<__half>(f, p, codes, ldc, scales, parts, s)
-                                  : run_many<float>(f, p, codes, ldc, scales, parts, s);
+    if (use_few) return launch_few<TY>(f, few, codes, ldc, scales, s);
+    return run_many<TY>(f, p, codes, ldc, scales, parts, s);
 }
 
 }  // namespace f8
 
 size_t fp8_block_workspace_bytes(int M, int width, int out) {
-    if (M <= f8::kFusedTokens && f8::fused_fits(f8::ceil_div(width, f8::kBlock))) return DH_WORKSPACE_ALIGN;   // not used
+    f8::FewPlan few;
+    f8::Plan many;
+    if (f8::take_few(M, out, width, &few, &many) && few.fused) return DH_WORKSPACE_ALIGN;   // not used
     return f8::up256(static_cast<size_t>(M) * (f8::ceil_div(width, 16) * 16)) +
            f8::up256(static_cast<size_t>(M) * f8::ceil_div(width, f8::kBlock) * sizeof(float)) + f8::up256(f8::parts_bytes(M, out, width));
 }
@@ -371,6 +380,12 @@ cudaError_t launch_fp8_quantize_blocks(const uint16_t* W, int V, int K, const in
     return cudaGetLastError();
 }
 
-cudaError_t launch_fp8_blocks(const Fp8BlockArgs& f, cudaStream_t s) { return f8::run(f, s); }
+cudaError_t launch_fp8_blocks(const Fp8BlockArgs& f, cudaStream_t s) {
+    switch (f.y_type) {
+        case DH_T_BF16: return f8::run<__nv_bfloat16>(f, s);
+        case DH_T_F16: return f8::run<__half>(f, s);
+        default: return f8::run<float>(f, s);
+    }
+}
 
 }  // namespace dh

@@ -19,16 +19,62 @@ __device__ __forceinline__ float block_scale(uint32_t top) {
     return top < 0x7F800000u ? act_fp8_scale(__uint_as_float(top)) : __uint_as_float(0x7FC00000u);
 }
 
-// 16 elements of a block held by eight lanes (n of them there): their codes, and the block's
-// scale, the same in all eight lanes.
+// Rows of activations: [M][width] of T, ld elements apart.
+template <class T>
+struct Rows {
+    const T* x;
+    long long ld;
+    int M, width;
+    __device__ __forceinline__ const T* at(int m, int k) const { return x + static_cast<size_t>(m) * ld + k; }
+    __device__ __forceinline__ const T* end() const { return at(M - 1, width); }
+};
+
+// 16 elements at p, which lie at any address: the 16-byte vectors that cover them, shifted (one
+// load per element made the quantiser of 4,912 x 13,925 three times as long). At the matrix's
+// ends, where a vector would reach beyond it, element by element.
+template <class T>
+__device__ __forceinline__ void load16_any(const T* p, const Rows<T>& rows, float (&v)[16]) {
+    constexpr int kVecs = static_cast<int>(sizeof(T)) + 1, kWords = 4 * kVecs;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p), first = at & ~static_cast<uintptr_t>(15);
+    if (first < reinterpret_cast<uintptr_t>(rows.x) || first + 16 * kVecs > reinterpret_cast<uintptr_t>(rows.end())) {
+        dh::rows::load16<T, false>(p, v);
+        return;
+    }
+    uint32_t w[kWords];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(first) + i);
+        w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+    }
+    const uint32_t off = static_cast<uint32_t>(at & 15);
+#pragma unroll
+    for (int b = 1; b <= 2; b <<= 1)   // whole words
+#pragma unroll
+        for (int i = 0; i + b < kWords; ++i) w[i] = off & (4 * b) ? w[i + b] : w[i];
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (off & 2) * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; i += dh::rows::Elem<T>::kVec) {
+        constexpr int kPer = 4 * static_cast<int>(sizeof(T));   // words of 16 elements
+        const int k = i * kPer / 16;
+        dh::rows::Elem<T>::unpack(make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]), reinterpret_cast<float(&)[dh::rows::Elem<T>::kVec]>(v[i]));
+    }
+}
+
+// 16 elements of row m from k, of a block held by eight lanes (n of them there): their codes, and
+// the block's scale, the same in all eight lanes.
 template <class T, bool VEC>
-__device__ __forceinline__ float encode16(const T* src, int n, uint4& codes) {
+__device__ __forceinline__ float encode16(const Rows<T>& rows, int m, int k, int n, uint4& codes) {
+    const T* src = rows.at(m, k);
     float v[16];
     if (n == 16) {
-        rows::load16<T, VEC>(src, v);
+        if constexpr (VEC) dh::rows::load16<T, true>(src, v);
+        else load16_any<T>(src, rows, v);
     } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = i < n ? rows::Elem<T>::load(src + i) : 0.0f;
+        for (int i = 0; i < 16; ++i) v[i] = i < n ? dh::rows::Elem<T>::load(src + i) : 0.0f;
     }
     uint32_t top = 0;
 #pragma unroll
@@ -54,15 +100,18 @@ inline bool rows_aligned16(const void* x, long long ld_bytes, int rows) {
     return (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && (rows == 1 || ld_bytes % 16 == 0);
 }
 
-// Products of up to kFewTokens tokens (dh_fp8_few.cu); scales null: x is quantised in the kernel.
-constexpr int kFewTokens = 128, kFusedTokens = 16;
-// Whether that form can take a product (its share of the steps fits a CTA), and about how long
-// it would be.
-bool few_supported(const Fp8BlockArgs& f, float* us);
-// Whether its fused form can take a product of this many steps, by the sizes alone: such a product
-// needs no workspace.
-bool fused_fits(int steps);
-cudaError_t launch_few(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, const float* scales, cudaStream_t s);
+// Products of up to kFewTokens tokens (dh_fp8_few.cuh): tokens that a tile has columns for, the CTAs
+// of a cluster that share the contraction (0: not in this form), whether the activations are
+// quantised in the kernel, and about how long it takes.
+constexpr int kFewTokens = 128;
+struct FewPlan {
+    int columns, splits;
+    bool fused;
+    float us;
+};
+FewPlan few_plan(int M, int out, int width);
+template <class TY>
+cudaError_t launch_few(const Fp8BlockArgs& f, const FewPlan& plan, const uint8_t* codes, int ldc, const float* scales, cudaStream_t s);
 
 }  // namespace f8
 }  // namespace dh

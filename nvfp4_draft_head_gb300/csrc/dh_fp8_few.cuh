@@ -5,9 +5,11 @@
 //
 // To have every SM read, the contraction is split over the CTAs of a cluster (1 to 8): each sums
 // its steps in registers, then sends each token's sums to the CTA that stores that token,
-// through distributed shared memory; sums are joined in the order of the ranks. Up to 16 tokens
-// the activations are quantised in the kernel too, by each CTA for its own steps, while its first
-// boxes of the weight are on their way: one launch in all.
+// through distributed shared memory; sums are joined in the order of the ranks. Where
+// they are few the activations are quantised in the kernel too, by each CTA for its own steps,
+// while its first boxes of the weight are on their way: one launch in all.
+#pragma once
+
 #include "dh_fp8_blocks.cuh"
 
 namespace dh {
@@ -183,13 +185,13 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         if (splits > 1) cluster_wait();
     } else {
         if (FUSED) {   // eight lanes per token and step
-            const TX* x = static_cast<const TX*>(a.x);
+            const Rows<TX> x = {static_cast<const TX*>(a.x), a.ldx, a.M, a.width};
+#pragma unroll 2
             for (int u0 = warp * 4; u0 < a.M * count; u0 += 4 * kEpiWarps) {
                 const int u = u0 + (lane >> 3), m = u % a.M, b = u / a.M, k = (b0 + b) * kBlock + (lane & 7) * 16;
                 const int n = b < count ? min(16, a.width - k) : 0;
                 uint4 w;
-                const TX* src = x + static_cast<size_t>(m) * a.ldx + k;
-                const float s = a.vec ? encode16<TX, true>(src, n, w) : encode16<TX, false>(src, n, w);
+                const float s = a.vec ? encode16<TX, true>(x, m, k, n, w) : encode16<TX, false>(x, m, k, n, w);
                 if (b < count) {
                     *reinterpret_cast<uint4*>(codes + (b * NT + m) * kBlock + (((lane & 7) ^ (m & 7)) << 4)) = w;
                     if ((lane & 7) == 0) scales[b * NT + m] = s;
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
 #pragma unroll
                     for (int i = 0; i < F::kPart; ++i) {
                         const int m = part * F::kPart + i;
-                        if (m < a.M) y[static_cast<size_t>(m) * a.ldy] = rows::Elem<TY>::store(sum[i]);
+                        if (m < a.M) y[static_cast<size_t>(m) * a.ldy] = dh::rows::Elem<TY>::store(sum[i]);
                     }
                 }
                 __syncwarp();
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             for (int slot = part; slot * splits + rank < a.M; slot += 2) {
                 float v = exchange[slot * kBlock + local];
                 for (int r = 1; r < splits; ++r) v += exchange[(r * slots + slot) * kBlock + local];
-                if (row < a.N) y[static_cast<size_t>(slot * splits + rank) * a.ldy] = rows::Elem<TY>::store(v);
+                if (row < a.N) y[static_cast<size_t>(slot * splits + rank) * a.ldy] = dh::rows::Elem<TY>::store(v);
             }
             __syncwarp();
             if (lane < splits) mbar_arrive_remote(cluster_map(&sy.room, lane));
@@ -299,62 +301,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
 
 // ------------------------------------------------------------------- host ----
 
-// Clusters of `size` CTAs of this memory that the device runs at once (clusters do not span its
-// graphics processing clusters: 152, 76, 46, 36, 28, 23, 15, 15 for 1 to 8).
-int clusters_of(int size) {
-    constexpr int kDevices = 64;
-    static std::atomic<int> known[kDevices][kMaxSplits + 1];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 0;
-    int n = known[dev][size].load(std::memory_order_acquire);
-    if (n > 0) return n;
-    const auto kernel = few_kernel<float, float, 32, false, false>;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3(static_cast<unsigned>(size));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSpace + 1024;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(size);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSpace + 1024) != cudaSuccess) return 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) return 0;
-    known[dev][size].store(n, std::memory_order_release);
-    return n;
-}
-
-// CTAs per cluster for `tiles` tiles of `steps` steps, by the time that a product would take:
-// rounds of tiles times a step's time (0.40 us; 0.60 where 128 tokens' sums are what takes it)
-// and a tile's end, which an exchange makes longer by the tokens. 0 where a CTA's share does not
-// fit its shared memory. Measured, us: 24 tokens x 4,608 x 2,560 9.2, 64 12, 128 16 (4 CTAs
-// each); 32 x 64,026 x 2,560 36 (1).
-template <int NT, bool FUSED>
-int choose_splits(int tiles, int steps, float* us) {
-    using F = Few<NT, FUSED>;
-    int best = 0;
-    for (int s = 1; s <= kMaxSplits; ++s) {
-        const int per = ceil_div(steps, s), clusters = clusters_of(s);
-        if (clusters == 0 || (s - 1) * per >= steps || F::rest(per, s) + 3 * F::kStage > kSpace) continue;
-        const float end = s == 1 ? 0.6f : 1.5f + 0.06f * NT;
-        const float cost = ceil_div(tiles, clusters) * (per * (NT < 128 ? 0.40f : 0.60f) + end);
-        if (best == 0 || cost < *us) {
-            best = s;
-            *us = cost;
-        }
-    }
-    return best;
-}
-
-bool fused_fits(int steps) {
-    using F = Few<16, true>;
-    for (int s = 1; s <= kMaxSplits; ++s) {
-        const int per = ceil_div(steps, s);
-        if ((s - 1) * per < steps && F::rest(per, s) + 3 * F::kStage <= kSpace) return true;
-    }
-    return false;
-}
+// Clusters of 1 to 8 CTAs of this memory that run at once (they do not span the GPU's processing
+// clusters).
+constexpr int kClusters[kMaxSplits + 1] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
 
 template <class TX, class TY, int NT, bool FUSED, bool GRADIENT>
 cudaError_t launch_kernel(const CUtensorMap& map_w, const CUtensorMap& map_x, FewArgs a, int splits, cudaStream_t stream) {
@@ -372,12 +321,12 @@ cudaError_t launch_kernel(const CUtensorMap& map_w, const CUtensorMap& map_x, Fe
     }
     const int fit = (kSpace - F::rest(a.per, splits)) / F::kStage;
     a.stages = fit < 16 ? fit : 16;
-    const int clusters = clusters_of(splits), want = a.tiles < clusters ? a.tiles : clusters;
+    const int want = a.tiles < kClusters[splits] ? a.tiles : kClusters[splits];
     return gemm::launch_early(kernel, dim3(static_cast<unsigned>(want * splits)), kThreads, kSmem, splits, stream, map_w, map_x, a);
 }
 
 template <class TX, class TY, int NT, bool FUSED>
-cudaError_t launch_sized(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, const float* scales, cudaStream_t s) {
+cudaError_t launch_sized(const Fp8BlockArgs& f, int splits, const uint8_t* codes, int ldc, const float* scales, cudaStream_t s) {
     const int width = f.gradient ? f.N : f.K, out = f.gradient ? f.K : f.N, kb = ceil_div(f.K, kBlock);
     FewArgs a = {};
     a.x = f.x;
@@ -397,9 +346,6 @@ cudaError_t launch_sized(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, c
     a.error = f.error;
     a.rounds = f.probe_rounds != 0 ? f.probe_rounds : kWaitLimit / gemm::kWaitSlices;
     a.idle = f.probe_rounds != 0 ? f.probe_role : -1;
-    float us;
-    const int splits = choose_splits<NT, FUSED>(a.tiles, a.steps, &us);
-    if (splits == 0) return cudaErrorInvalidValue;
     a.per = ceil_div(a.steps, splits);
     CUtensorMap map_w, map_x;
     // (the same box either way: 128 bytes of a row of W by 128 rows)
@@ -411,30 +357,23 @@ cudaError_t launch_sized(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, c
                       : launch_kernel<TX, TY, NT, FUSED, false>(map_w, map_x, a, splits, s);
 }
 
+template <class TX, class TY>
+cudaError_t launch_fused(const Fp8BlockArgs& f, const FewPlan& p, cudaStream_t s) {
+    return p.columns == 16   ? launch_sized<TX, TY, 16, true>(f, p.splits, nullptr, 0, nullptr, s)
+           : p.columns == 32 ? launch_sized<TX, TY, 32, true>(f, p.splits, nullptr, 0, nullptr, s)
+                             : launch_sized<TX, TY, 64, true>(f, p.splits, nullptr, 0, nullptr, s);
+}
+
 template <class TY>
-cudaError_t launch_typed(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, const float* scales, cudaStream_t s) {
-    if (scales == nullptr)
-        return f.x_type == DH_T_BF16  ? launch_sized<__nv_bfloat16, TY, 16, true>(f, nullptr, 0, nullptr, s)
-               : f.x_type == DH_T_F16 ? launch_sized<__half, TY, 16, true>(f, nullptr, 0, nullptr, s)
-                                      : launch_sized<float, TY, 16, true>(f, nullptr, 0, nullptr, s);
+cudaError_t launch_few(const Fp8BlockArgs& f, const FewPlan& p, const uint8_t* codes, int ldc, const float* scales, cudaStream_t s) {
+    if (p.fused)
+        return f.x_type == DH_T_BF16  ? launch_fused<__nv_bfloat16, TY>(f, p, s)
+               : f.x_type == DH_T_F16 ? launch_fused<__half, TY>(f, p, s)
+                                      : launch_fused<float, TY>(f, p, s);
     // (the element type of x matters to the fused form alone)
-    if (f.M <= 32) return launch_sized<float, TY, 32, false>(f, codes, ldc, scales, s);
-    if (f.M <= 64) return launch_sized<float, TY, 64, false>(f, codes, ldc, scales, s);
-    return launch_sized<float, TY, 128, false>(f, codes, ldc, scales, s);
-}
-
-bool few_supported(const Fp8BlockArgs& f, float* us) {
-    const int tiles = ceil_div(f.gradient ? f.K : f.N, kBlock), steps = ceil_div(f.gradient ? f.N : f.K, kBlock);
-    if (f.M > kFewTokens) return false;
-    return (f.M <= 32   ? choose_splits<32, false>(tiles, steps, us)
-            : f.M <= 64 ? choose_splits<64, false>(tiles, steps, us)
-                        : choose_splits<128, false>(tiles, steps, us)) != 0;
-}
-
-cudaError_t launch_few(const Fp8BlockArgs& f, const uint8_t* codes, int ldc, const float* scales, cudaStream_t s) {
-    return f.y_type == DH_T_BF16  ? launch_typed<__nv_bfloat16>(f, codes, ldc, scales, s)
-           : f.y_type == DH_T_F16 ? launch_typed<__half>(f, codes, ldc, scales, s)
-                                  : launch_typed<float>(f, codes, ldc, scales, s);
+    return p.columns == 32   ? launch_sized<float, TY, 32, false>(f, p.splits, codes, ldc, scales, s)
+           : p.columns == 64 ? launch_sized<float, TY, 64, false>(f, p.splits, codes, ldc, scales, s)
+                             : launch_sized<float, TY, 128, false>(f, p.splits, codes, ldc, scales, s);
 }
 
 }  // namespace f8

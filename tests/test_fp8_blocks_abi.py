@@ -20,7 +20,7 @@ def test_sizes(L):
     nb = L.fp8_block_matmul_workspace_bytes
     assert nb(1, 2560, 4608) == nb(16, 5120, 64) == 256          # quantised in the product's own kernel
     assert nb(1024, 2560, 4608) == 1024 * 2560 + 1024 * 20 * 4
-    assert nb(17, 1, 1) == 512 + 256                             # codes in rows of 16, one scale a token
+    assert nb(129, 1, 1) == 129 * 16 + 240 + 768             # codes in rows of 16, one scale a token
     assert nb(200, 64026, 2560) > 200 * 64032 + 200 * 501 * 4    # a long contraction: sums of its parts too
     assert nb(16, 1 << 20, 64) > 256                             # too long for that kernel's shared memory
     for m, w, o in ((0, 16, 16), (-1, 16, 16), (1, 0, 16), (1, 16, 0), ((1 << 24) + 1, 16, 16), (1 << 24, 1 << 20, 16), (1, (1 << 24) + 1, 1)):
