@@ -151,6 +151,7 @@ struct Rows {
     long long ld;
     int K;
     void* copy;              // [T][K] or null
+    int again;               // rows further on, the copy's second one (0: none)
     uint32_t* wmax;
     __device__ __forceinline__ void weigh(float w, bool live) const {
         const uint32_t bits = __float_as_uint(w) & 0x7FFFFFFFu;
@@ -159,7 +160,12 @@ struct Rows {
     __device__ __forceinline__ void move(int t, bool live, int i, int step) const {
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(hidden) + static_cast<size_t>(t) * ld);
         uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(copy) + static_cast<size_t>(t) * K);
-        for (; i < K / 8; i += step) dst[i] = live ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+        const size_t second = static_cast<size_t>(again) * (K / 8);
+        for (; i < K / 8; i += step) {
+            const uint4 v = live ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+            dst[i] = v;
+            if (second != 0) dst[second + i] = v;
+        }
     }
 };
 
@@ -235,6 +241,7 @@ struct Weights {   // g of a piece
         const float* rest;      // or null
         const uint32_t* wmax;
         T* g;                   // [T][ldg], ldg a multiple of 256
+        T* low;                 // what rounding g left over, or null
         int ldg;
         int first, count;       // the piece's rows of the head
     };
@@ -267,8 +274,23 @@ struct Weights {   // g of a piece
             }
             uint32_t v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = live ? rows::Elem<T>::pack2(g[2 * i] * w, g[2 * i + 1] * w) : 0u;
-            if (row < a.tok.T && c0 + c < a.count) store32(out + c, v);
+            for (int i = 0; i < 16; ++i) g[i] *= w;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = live ? rows::Elem<T>::pack2(g[2 * i], g[2 * i + 1]) : 0u;
+            const bool in = row < a.tok.T && c0 + c < a.count;
+            if (in) store32(out + c, v);
+            if (a.low != nullptr) {
+#pragma unroll
+                for (int i = 0; i < 16; i += 8) {
+                    float high[8];
+                    rows::Elem<T>::unpack(make_uint4(v[i / 2], v[i / 2 + 1], v[i / 2 + 2], v[i / 2 + 3]), high);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) g[i + k] -= high[k];
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = live ? rows::Elem<T>::pack2(g[2 * i], g[2 * i + 1]) : 0u;
+                if (in) store32(a.low + static_cast<size_t>(row) * a.ldg + c0 + c, v);
+            }
         }
         __syncwarp();
         return true;
@@ -300,6 +322,33 @@ __device__ __forceinline__ bool store_rows(A& acc, T* out, bool in, int columns,
                 __stcg(reinterpret_cast<uint4*>(out + c + i), make_uint4(v[0], v[1], v[2], v[3]));
                 if (c + i + 8 < columns) __stcg(reinterpret_cast<uint4*>(out + c + i + 8), make_uint4(v[4], v[5], v[6], v[7]));
             }
+        }
+        __syncwarp();
+    }
+    acc.release();
+    return true;
+}
+
+// The same as 32-bit sums (rows 32-byte aligned), added to what is there if `add`.
+template <class A>
+__device__ __forceinline__ bool store_sums(A& acc, float* out, bool in, int columns, uint32_t offset, bool add) {
+    const uint32_t at = acc.next();
+    if (at == ~0u) return false;
+#pragma unroll 1
+    for (int c = 0; c < kHalf && c < columns; c += 32) {
+        uint32_t r[32];
+        tc::tmem_load32(at + offset + c, r);
+        tc::tmem_load_wait();
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+            if (!in || c + i >= columns) break;
+            if (add) {
+                const float4 p = *reinterpret_cast<const float4*>(out + c + i), q = *reinterpret_cast<const float4*>(out + c + i + 4);
+                const float o[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) r[i + j] = __float_as_uint(o[j] + __uint_as_float(r[i + j]));
+            }
+            store32(out + c + i, r + i);
         }
         __syncwarp();
     }
@@ -343,29 +392,7 @@ struct Hidden {
             const int rest = a.shape.tiles() - a.shape.whole, at = gemm::tile_index(a.shape.tiles_m, a.shape.tiles_n, t.m, t.n) - a.shape.whole;
             out = a.parts + (static_cast<size_t>((t.split - 1) * rest + at) * kTM + local) * kTN + half * kHalf;
         }
-        const uint32_t at = acc.next();
-        if (at == ~0u) return false;
-        const uint32_t from = at + (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf;
-#pragma unroll 1
-        for (int c = 0; c < kHalf && n0 + c < a.K; c += 32) {
-            uint32_t r[32];
-            tc::tmem_load32(from + c, r);
-            tc::tmem_load_wait();
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-                if (row >= a.T_ || n0 + c + i >= a.K) break;
-                if (a.add) {
-                    const float4 p = *reinterpret_cast<const float4*>(out + c + i), q = *reinterpret_cast<const float4*>(out + c + i + 4);
-                    const float o[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) r[i + j] = __float_as_uint(o[j] + __uint_as_float(r[i + j]));
-                }
-                store32(out + c + i, r + i);
-            }
-            __syncwarp();
-        }
-        acc.release();
-        return true;
+        return store_sums(acc, out, row < a.T_, a.K - n0, (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf, a.add != 0);
     }
 };
 
@@ -384,49 +411,83 @@ struct Head {
         T* out;                  // the piece's first row
         long long ld;
         int wide;                // rows 32-byte aligned
+        float* parts;            // the tokens in parts: their sums, [split][tile][256][256] (null: results)
     };
     template <class A2>
     __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int rank, A2& acc) {
         const int row = (t.m * kPair + rank) * gemm::kRows + (warp & 3) * 32 + lane, half = warp >> 2;
         const int n0 = t.n * kTN + half * kHalf;
+        if (a.parts != nullptr) {
+            const int at = gemm::tile_index(a.shape.tiles_m, a.shape.tiles_n, t.m, t.n);
+            float* sums = a.parts + ((static_cast<size_t>(t.split) * a.shape.tiles() + at) * kTM + rank * gemm::kRows + (warp & 3) * 32 + lane) * kTN +
+                          half * kHalf;
+            return store_sums(acc, sums, row < a.rows, a.K - n0, (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf, false);
+        }
         const float scale = exp2i(-scale_exponent<kF16>(*a.wmax));
         return store_rows<T>(acc, a.out + static_cast<size_t>(row) * a.ld + n0, row < a.rows, a.K - n0,
                              (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf, scale, true, a.wide);
     }
 };
 
-// dh from the sums: eight elements per thread, the parts of a split tile in order. Rows that are
-// left out are zeros whatever the head holds.
+// dh from its sums, and dW from those of its parts: eight elements per thread, parts in order.
+// Rows of dh that are left out are zeros whatever the head holds.
 struct Sums {
+    size_t elements;           // of dh, in eights (0: none)
     const float* sum;
     const float* parts;
-    int tiles_m, tiles_n, whole, splits;
+    int tiles_m, tiles_n, whole, splits, terms;
+    void* out;
+    long long ld;
+    // dW
+    gemm::Shape head;          // its tiles, all in parts (splits; none: 0)
+    const float* head_parts;
+    void* head_out;
+    long long head_ld;
+    int head_rows;
 };
+__device__ __forceinline__ void add8(float (&v)[8], const float* p) {
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p + 4));
+    v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w, v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+}
 template <class T>
-__global__ void __launch_bounds__(256) sum_kernel(const Tokens tok, const Sums a, int K, const uint32_t* __restrict__ wmax,
-                                                  T* __restrict__ out, long long ld) {
+__global__ void __launch_bounds__(256) sum_kernel(const Tokens tok, const Sums a, int K, const uint32_t* __restrict__ wmax) {
     programmatic_wait();
     const float scale = exp2i(-scale_exponent<std::is_same<T, __half>::value>(*wmax));
     const unsigned per_row = K / 8;
-    const size_t total = static_cast<size_t>(tok.T) * per_row;
-    for (size_t i = blockIdx.x * static_cast<size_t>(blockDim.x) + threadIdx.x; i < total; i += static_cast<size_t>(gridDim.x) * blockDim.x) {
-        const int row = static_cast<int>(i / per_row), col = static_cast<int>(i % per_row) * 8;
-        const bool live = tok.live(row);
-        const float4 x = __ldcs(reinterpret_cast<const float4*>(a.sum + i * 8)), y = __ldcs(reinterpret_cast<const float4*>(a.sum + i * 8 + 4));
-        float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        const int at = gemm::tile_index(a.tiles_m, a.tiles_n, row / kTM, col / kTN) - a.whole;
-        if (at >= 0) {
-            const size_t step = static_cast<size_t>(a.tiles_m * a.tiles_n - a.whole) * kTM * kTN;
-            const float* p = a.parts + (static_cast<size_t>(at) * kTM + row % kTM) * kTN + col % kTN;
-            for (int s = 1; s < a.splits; ++s, p += step) {
-                const float4 b = __ldcs(reinterpret_cast<const float4*>(p)), c = __ldcs(reinterpret_cast<const float4*>(p + 4));
-                v[0] += b.x; v[1] += b.y; v[2] += b.z; v[3] += b.w;
-                v[4] += c.x; v[5] += c.y; v[6] += c.z; v[7] += c.w;
+    constexpr unsigned kTile = kTM * kTN / 8;
+    const size_t head = static_cast<size_t>(a.head.tiles()) * kTile;
+    for (size_t i = blockIdx.x * static_cast<size_t>(blockDim.x) + threadIdx.x; i < a.elements + head; i += static_cast<size_t>(gridDim.x) * blockDim.x) {
+        float v[8] = {};
+        T* out;
+        if (i < a.elements) {
+            const int row = static_cast<int>(i / per_row), col = static_cast<int>(i % per_row) * 8;
+            out = static_cast<T*>(a.out) + static_cast<size_t>(row) * a.ld + col;
+            for (int e = 0; e < a.terms; ++e) {
+                const int r = row + e * tok.T;
+                add8(v, a.sum + static_cast<size_t>(r) * K + col);
+                const int at = gemm::tile_index(a.tiles_m, a.tiles_n, r / kTM, col / kTN) - a.whole;
+                if (at < 0) continue;
+                const size_t step = static_cast<size_t>(a.tiles_m * a.tiles_n - a.whole) * kTM * kTN;
+                const float* p = a.parts + (static_cast<size_t>(at) * kTM + r % kTM) * kTN + col % kTN;
+                for (int s = 1; s < a.splits; ++s, p += step) add8(v, p);
             }
-        }
+            const bool live = tok.live(row);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = live ? v[j] * scale : 0.0f;
-        *reinterpret_cast<uint4*>(out + static_cast<size_t>(row) * ld + col) = rows::Elem<T>::pack(v);
+            for (int j = 0; j < 8; ++j) v[j] = live ? v[j] * scale : 0.0f;
+        } else {
+            const unsigned at = static_cast<unsigned>((i - a.elements) / kTile), in = static_cast<unsigned>((i - a.elements) % kTile) * 8;
+            gemm::Shape whole = a.head;
+            whole.whole = whole.tiles();
+            const Tile t = gemm::tile_at(whole, static_cast<int>(at));
+            const int row = t.m * kTM + static_cast<int>(in / kTN), col = t.n * kTN + static_cast<int>(in % kTN);
+            if (row >= a.head_rows || col >= K) continue;
+            out = static_cast<T*>(a.head_out) + static_cast<size_t>(row) * a.head_ld + col;
+            const float* p = a.head_parts + static_cast<size_t>(at) * kTM * kTN + in;
+            for (int s = 0; s < a.head.splits; ++s, p += static_cast<size_t>(a.head.tiles()) * kTM * kTN) add8(v, p);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] *= scale;
+        }
+        *reinterpret_cast<uint4*>(out) = rows::Elem<T>::pack(v);
     }
 }
 
@@ -464,8 +525,26 @@ gemm::Shape hidden_tiles(int T, int K, int piece, unsigned int* error) {
     return s;
 }
 
+// g in two terms, its 16-bit rounding and what that left over, as rows T .. 2 T - 1 of g, of dh's
+// sums and (the same hidden states again) of dW's contraction: for few tokens, whose roundings
+// do not average out, and for which the products' tiles have the room.
+int terms_of(int T) { return T <= 128 ? 2 : 1; }
+
+// dW's tiles where they are few and the tokens many: all in parts of at least eight steps, as many
+// as fill the pairs of SMs once (6,208 tokens, 5 rows of 4,592: 34 us of 105 were 18 tiles of 97
+// steps). A head of several pieces has tiles enough.
+gemm::Shape head_tiles(int rows, int N, int K, int piece, unsigned int* error) {
+    gemm::Shape s = gemm::whole_tiles(ceil_div(N, kTM), ceil_div(K, kTN), ceil_div(rows, 64), error);
+    if (N > piece || s.tiles() > 38 || s.steps < 16) return s;
+    const int p = 76 / s.tiles() < s.steps / 8 ? 76 / s.tiles() : s.steps / 8;
+    s.whole = 0;
+    s.split_steps = ceil_div(s.steps, p);
+    s.splits = ceil_div(s.steps, s.split_steps);
+    return s;
+}
+
 struct Space {
-    size_t wmax, part, target, lse, rest, g, hidden, sum, parts, bytes;
+    size_t wmax, part, target, lse, rest, g, hidden, sum, parts, head_parts, bytes;
 };
 Space space_of(int T, int N, int K, bool loss, bool dh, bool dw) {
     Space s = {};
@@ -482,11 +561,17 @@ Space space_of(int T, int N, int K, bool loss, bool dh, bool dw) {
         s.lse = take(t * 4);
         s.rest = take(t * 4);
     }
-    if (dh || dw) s.g = take(t * piece_rows(T, N) * 2);
-    if (dw) s.hidden = take(t * K * 2);
+    const int rows = terms_of(T) * T, piece = piece_rows(rows, N);
+    const size_t r = static_cast<size_t>(rows);
+    if (dh || dw) s.g = take(r * piece * 2);
+    if (dw) {
+        s.hidden = take(r * K * 2);
+        const gemm::Shape w = head_tiles(rows, N, K, piece, nullptr);
+        if (w.whole == 0) s.head_parts = take(static_cast<size_t>(w.units()) * kTM * kTN * 4);
+    }
     if (dh) {
-        const gemm::Shape h = hidden_tiles(T, K, piece_rows(T, N), nullptr);
-        s.sum = take(t * K * 4);
+        const gemm::Shape h = hidden_tiles(rows, K, piece, nullptr);
+        s.sum = take(r * K * 4);
         s.parts = take(static_cast<size_t>(h.tiles() - h.whole) * (h.splits - 1) * kTM * kTN * 4);
     }
     s.bytes = at;
@@ -504,7 +589,8 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
     uint32_t* wmax = reinterpret_cast<uint32_t*>(ws + sp.wmax);
     const int tiles_m = ceil_div(c.T, gemm::kRows * P);
     T* hidden = dw ? reinterpret_cast<T*>(ws + sp.hidden) : nullptr;
-    const Rows rows = {c.hidden, c.ld_hidden, c.K, hidden, wmax};
+    const int terms = terms_of(c.T), all_rows = terms * c.T;   // of g
+    const Rows rows = {c.hidden, c.ld_hidden, c.K, hidden, terms > 1 ? c.T : 0, wmax};
     cudaError_t e;
     using K1 = typename Stats<T, P>::Layout;
     gemm::Jobs<Stats<T, P>> logits = {};
@@ -541,11 +627,13 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
         if ((e = cudaMemsetAsync(wmax, 0, 4, stream)) != cudaSuccess) return e;
         if ((e = gemm::launch_early(rows_kernel, dim3(static_cast<unsigned>(c.T)), 128, 0, 1, stream, tok, rows)) != cudaSuccess) return e;
     }
-    const int piece = piece_rows(c.T, c.N);
-    const gemm::Shape tiles_h = hidden_tiles(c.T, c.K, piece, c.error);   // of a full piece
+    const int piece = piece_rows(all_rows, c.N);
+    const gemm::Shape tiles_h = hidden_tiles(all_rows, c.K, piece, c.error);   // of a full piece
+    const gemm::Shape tiles_w = head_tiles(all_rows, c.N, c.K, piece, c.error);
+    float* head_parts = dw && tiles_w.whole == 0 ? reinterpret_cast<float*>(ws + sp.head_parts) : nullptr;
     T* g = reinterpret_cast<T*>(ws + sp.g);
     float* sum = reinterpret_cast<float*>(ws + sp.sum);
-    const bool direct = c.N <= piece && ceil_div(ceil_div(c.N, 64), tiles_h.split_steps) == 1;   // dh is one sum
+    const bool direct = terms == 1 && c.N <= piece && ceil_div(ceil_div(c.N, 64), tiles_h.split_steps) == 1;   // dh is one sum
     int splits = 1;   // of dh's split tiles: those of the first piece, which is the largest
     for (int first = 0; first < c.N; first += piece) {
         const int count = c.N - first < piece ? c.N - first : piece;
@@ -557,6 +645,7 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
         a.rest = rest;
         a.wmax = wmax;
         a.g = g;
+        a.low = terms > 1 ? g + static_cast<size_t>(c.T) * piece : nullptr;
         a.ldg = piece;
         a.first = first;
         a.count = count;
@@ -565,14 +654,14 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
         if (dh) {
             using L = typename Hidden<T>::Layout;
             auto& job = both.first;
-            if ((e = gemm::encode_operand<L, false>(&job.map_a, g, c.T, count, static_cast<uint64_t>(piece) * 2, gemm::kRows)) != cudaSuccess) return e;
+            if ((e = gemm::encode_operand<L, false>(&job.map_a, g, all_rows, count, static_cast<uint64_t>(piece) * 2, gemm::kRows)) != cudaSuccess) return e;
             if ((e = gemm::encode_operand<L, true>(&job.map_b, c.head, c.K, c.N, c.ld_head * 2, 0)) != cudaSuccess) return e;
             auto& b = job.args;
             b.shape = tiles_h;
             b.shape.steps = ceil_div(count, L::kK);
             b.shape.splits = ceil_div(b.shape.steps, tiles_h.split_steps);
             b.shape.b_k = first;
-            b.T_ = c.T;
+            b.T_ = all_rows;
             b.K = c.K;
             b.sum = sum;
             b.parts = reinterpret_cast<float*>(ws + sp.parts);
@@ -586,10 +675,11 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
         if (dw) {
             using L = typename Head<T>::Layout;
             auto& job = both.second;
-            if ((e = gemm::encode_operand<L, true>(&job.map_a, g, count, c.T, static_cast<uint64_t>(piece) * 2, 0)) != cudaSuccess) return e;
-            if ((e = gemm::encode_operand<L, true>(&job.map_b, hidden, c.K, c.T, static_cast<uint64_t>(c.K) * 2, 0)) != cudaSuccess) return e;
+            if ((e = gemm::encode_operand<L, true>(&job.map_a, g, count, all_rows, static_cast<uint64_t>(piece) * 2, 0)) != cudaSuccess) return e;
+            if ((e = gemm::encode_operand<L, true>(&job.map_b, hidden, c.K, all_rows, static_cast<uint64_t>(c.K) * 2, 0)) != cudaSuccess) return e;
             auto& b = job.args;
-            b.shape = gemm::whole_tiles(ceil_div(count, kTM), ceil_div(c.K, kTN), ceil_div(c.T, L::kK), c.error);
+            b.shape = head_parts != nullptr ? tiles_w : gemm::whole_tiles(ceil_div(count, kTM), ceil_div(c.K, kTN), ceil_div(all_rows, L::kK), c.error);
+            b.parts = head_parts;
             b.rows = count;
             b.K = c.K;
             b.wmax = wmax;
@@ -600,11 +690,31 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
         both.first.args.shape.error = c.error;   // (one gradient alone: the other has no tiles)
         if ((e = gemm::launch(both, stream)) != cudaSuccess) return e;
     }
-    if (dh && !direct) {
-        const size_t total = static_cast<size_t>(c.T) * (c.K / 8), want = (total + 255) / 256, cap = static_cast<size_t>(sm_count()) * 8;
-        const Sums sums = {sum, reinterpret_cast<float*>(ws + sp.parts), tiles_h.tiles_m, tiles_h.tiles_n, tiles_h.whole, splits};
-        e = gemm::launch_early(sum_kernel<T>, dim3(static_cast<unsigned>(want < cap ? want : cap)), 256, 0, 1, stream, tok, sums, c.K, wmax,
-                               static_cast<T*>(c.dhidden), c.ld_dhidden);
+    const bool sum_dh = dh && !direct;
+    if (sum_dh || head_parts != nullptr) {
+        Sums sums = {};
+        if (sum_dh) {
+            sums.elements = static_cast<size_t>(c.T) * (c.K / 8);
+            sums.sum = sum;
+            sums.parts = reinterpret_cast<float*>(ws + sp.parts);
+            sums.tiles_m = tiles_h.tiles_m;
+            sums.tiles_n = tiles_h.tiles_n;
+            sums.whole = tiles_h.whole;
+            sums.splits = splits;
+            sums.terms = terms;
+            sums.out = c.dhidden;
+            sums.ld = c.ld_dhidden;
+        }
+        if (head_parts != nullptr) {
+            sums.head = tiles_w;
+            sums.head_parts = head_parts;
+            sums.head_out = c.dhead;
+            sums.head_ld = c.ld_dhead;
+            sums.head_rows = c.N;
+        }
+        const size_t total = sums.elements + static_cast<size_t>(sums.head.tiles()) * (kTM * kTN / 8);
+        const size_t want = (total + 255) / 256, cap = static_cast<size_t>(sm_count()) * 8;
+        e = gemm::launch_early(sum_kernel<T>, dim3(static_cast<unsigned>(want < cap ? want : cap)), 256, 0, 1, stream, tok, sums, c.K, wmax);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

@@ -12,7 +12,8 @@ A gradient is a product with g, |g error| <= |w| p (2 dz + 2^-15 + 2^-23 |lse|) 
 rounding; f16's scale keeps w in [2^14, 2^15), so its subnormals add at most 2^-25 2^-14 |w|max),
 (bf16 has 32-bit floats' range: the exponential, and g scaled by a power of two above 1 / (2
 |w|max), are zero below 2^-126, which adds at most 2^-126 (|w| + 2 |w|max)), summed with at
-most 2^-23 of the sum of magnitudes per addition, and rounded once:
+most 2^-23 of the sum of magnitudes per addition, and rounded once; up to 128 tokens have g in
+two terms, u^2 in place of u |g|:
   |error| <= sum_n |g error| |W| + N 2^-23 sum |g| |W| + u |dh|, the same over tokens for dW.
 In the 2-norm, where roundings are independent: those of g (as large, relative to the result,
 as those of the result) and of the result, and half a step below the type's range for each:
@@ -87,7 +88,7 @@ def reference(s, lse_given=None):
     g = torch.where(live[:, None], g * w[:, None], torch.zeros_like(g))
     p = torch.where(live[:, None], p, torch.zeros_like(p))
     small = (2.0 ** -39 if s["hidden"].dtype == torch.float16 else 2.0 ** -124) * w.abs().max()
-    ge = (w.abs() * (2 * dz + 2.0 ** -15 + 2.0 ** -23 * lse.abs()))[:, None] * p + u * g.abs() + small * live[:, None]
+    ge = (w.abs() * (2 * dz + 2.0 ** -15 + 2.0 ** -23 * lse.abs()))[:, None] * p + (u * u if T <= 128 else u) * g.abs() + small * live[:, None]
     ge = torch.where(live[:, None], ge, torch.zeros_like(ge))
     out["dhidden"], out["dhead"] = g @ W, g.t() @ hl
     tol["dhidden"] = ge @ W.abs() + N * 2.0 ** -23 * (g.abs() @ W.abs()) + u * out["dhidden"].abs()
