@@ -11,7 +11,9 @@
 // is written in 16 bits (the only [tokens x piece] array), and two products read it, one along
 // the piece (dh, added up over the pieces in 32 bits), one along the tokens (dW, final). The
 // product is three quarters useful: 8 T N K operations against the 6 that the mathematics has,
-// the price of not keeping T x N probabilities.
+// the price of not keeping T x N probabilities. (For up to 128 tokens the logits, T x N of them, are
+// less than the piece may take anyway, and reading the head again would be the work: a call that
+// computes both keeps them in its workspace between its products.)
 //
 // Roundings besides 32-bit arithmetic: g to the inputs' 16-bit type (the tensor cores take
 // nothing wider from it; its error is that of rounding the results again), scaled by a power of
@@ -75,9 +77,10 @@ __device__ __forceinline__ int scale_exponent(uint32_t wmax) {
 
 // The tensor cores' 32-bit sums are truncated, not rounded, as they grow: over the 160
 // instructions of 2,560 features a large logit loses 2e-6 of itself, four times what a product
-// in 32 bits is off by. So they sum 512 features at a time, which the epilogue adds up, rounded
-// (the loss of 4,095 x 64,026: off by 1.8e-6 -> see the top of the file).
-constexpr int kLogitChunk = 8;
+// in 32 bits is off by. So they sum some steps of 64 features at a time, which the epilogue adds
+// up, rounded: the loss of 4,095 x 64,026 was off by 1.8e-6, and is by 3.4e-7 with eight steps
+// (the same time; four cost 8 % there, and nothing where reading the head is the work).
+constexpr int logit_chunk(int P) { return P == 1 ? 4 : 8; }
 
 // A thread's 128 logits of one row.
 template <class L>
@@ -85,7 +88,7 @@ __device__ __forceinline__ bool sum_logits(Acc<L>& acc, int steps, uint32_t offs
 #pragma unroll
     for (int i = 0; i < kHalf; ++i) z[i] = 0.0f;
 #pragma unroll 1
-    for (int k = 0; k < steps; k += kLogitChunk) {
+    for (int k = 0; k < steps; k += logit_chunk(L::kP)) {
         const uint32_t at = acc.next();
         if (at == ~0u) return false;
 #pragma unroll
@@ -104,7 +107,7 @@ __device__ __forceinline__ bool sum_logits(Acc<L>& acc, int steps, uint32_t offs
 template <class T, int P>
 struct Stats {
     using Layout = gemm::Layout<P, kTN, 2, false, false>;
-    static constexpr int kFormat = std::is_same<T, __half>::value ? 0 : 1, kChunk = kLogitChunk;
+    static constexpr int kFormat = std::is_same<T, __half>::value ? 0 : 1, kChunk = logit_chunk(P);
     static constexpr bool kAKeep = true, kBKeep = true;
     struct Args {
         gemm::Shape shape;
@@ -112,6 +115,8 @@ struct Stats {
         float2* part;   // [2 tiles_n][T]: maximum and sum of 128 columns
         float* target;  // [T]: the token's logit
         uint32_t* wmax; // cleared for what follows
+        float* z;       // the logits, [T][ldz] (ldz a multiple of 256), or null
+        int ldz;
     };
     __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int rank, Acc<Layout>& acc) {
         const int row = (t.m * P + rank) * gemm::kRows + (warp & 3) * 32 + lane, half = warp >> 2;
@@ -124,6 +129,12 @@ struct Stats {
 #pragma unroll
             for (int i = 0; i < kHalf; ++i) z[i] = i < valid ? z[i] : kNegInf;
         }
+        if (P == 1 && a.z != nullptr && row < a.tok.T) {   // (few tokens: single CTAs)
+            float* out = a.z + static_cast<size_t>(row) * a.ldz + n0;
+#pragma unroll
+            for (int i = 0; i < kHalf; i += 8) store32(out + i, reinterpret_cast<const uint32_t*>(&z[i]));
+        }
+        __syncwarp();
         if (__any_sync(0xFFFFFFFFu, j >= 0 && j < kHalf)) {
             float y = 0.0f;
 #pragma unroll
@@ -177,6 +188,15 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
     s = s * exp2_approx((m - ref) * kLog2e) + s2 * exp2_approx((m2 - ref) * kLog2e);
     m = top;
 }
+// A row's normaliser from its maximum and sum: m + ln s, and what rounding that took away.
+struct Normaliser {
+    float m, ln, lse, rest;
+    __device__ __forceinline__ Normaliser(float m_, float s) : m(m_), ln(logf(s)), lse(m + ln) {
+        const float b = lse - m;   // (two-sum)
+        rest = (m - (lse - b)) + (ln - b);
+    }
+    __device__ __forceinline__ float loss(float target) const { return ln + (m - target); }
+};
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Tokens tok, const float2* __restrict__ part, int parts,
                                                             const float* __restrict__ target, float* __restrict__ loss,
                                                             float* __restrict__ lse, float* __restrict__ rest, const Rows rows) {
@@ -198,14 +218,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Tokens tok, co
     if (warp == 0 && lane < kJoinTokens && t < tok.T) {
 #pragma unroll 4
         for (int j = 1; j < kJoinWarps; ++j) join(m, s, all[j][lane].x, all[j][lane].y);
-        const float ln = logf(s), sum = m + ln, w = tok.w(t);
-        const bool live = w != 0.0f && tok.row(t) >= 0;
-        if (loss != nullptr) loss[t] = live ? w * (ln + (m - target[t])) : 0.0f;
-        if (lse != nullptr) lse[t] = sum;
-        if (rest != nullptr) {   // what the sum rounded away (two-sum)
-            const float b = sum - m;
-            rest[t] = (m - (sum - b)) + (ln - b);
-        }
+        const Normaliser n(m, s);
+        const float w = tok.w(t);
+        const bool live = tok.live(t);
+        if (loss != nullptr) loss[t] = live ? w * n.loss(target[t]) : 0.0f;
+        if (lse != nullptr) lse[t] = n.lse;
+        if (rest != nullptr) rest[t] = n.rest;
         if (rows.wmax != nullptr) rows.weigh(w, live);
     }
     if (rows.copy != nullptr) {
@@ -227,12 +245,42 @@ __global__ void __launch_bounds__(128) rows_kernel(const Tokens tok, const Rows 
     if (rows.copy != nullptr) rows.move(t, live, threadIdx.x, blockDim.x);
 }
 
+// A logit's probability.
+__device__ __forceinline__ float probability(float z, float lse, float rest) { return exp2_approx(((z - lse) - rest) * kLog2e); }
+
+// 16 elements of g from the probabilities p of columns c .. c + 15 (the token's own is j), weighted
+// by w: rounded to `out`, and what that leaves over to `low` (null: nowhere).
+template <class T>
+__device__ __forceinline__ void store_weights(float (&p)[16], int j, float w, bool live, T* out, T* low) {
+    if (j >= 0 && j < 16) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) p[i] = i == j ? p[i] - 1.0f : p[i];
+    }
+    uint32_t v[8];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) p[i] *= w;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = live ? rows::Elem<T>::pack2(p[2 * i], p[2 * i + 1]) : 0u;
+    store32(out, v);
+    if (low == nullptr) return;
+#pragma unroll
+    for (int i = 0; i < 16; i += 8) {
+        float high[8];
+        rows::Elem<T>::unpack(make_uint4(v[i / 2], v[i / 2 + 1], v[i / 2 + 2], v[i / 2 + 3]), high);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) p[i + k] -= high[k];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = live ? rows::Elem<T>::pack2(p[2 * i], p[2 * i + 1]) : 0u;
+    store32(low, v);
+}
+
 template <class T, int P>
 struct Weights {   // g of a piece
     using Layout = gemm::Layout<P, kTN, 2, false, false>;
     static constexpr bool kF16 = std::is_same<T, __half>::value;
     static constexpr int kFormat = kF16 ? 0 : 1;
-    static constexpr int kChunk = kLogitChunk;
+    static constexpr int kChunk = logit_chunk(P);
     static constexpr bool kAKeep = true, kBKeep = true;
     struct Args {
         gemm::Shape shape;
@@ -261,41 +309,88 @@ struct Weights {   // g of a piece
         float z[kHalf];
         if (!sum_logits(acc, t.steps, (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf, z)) return false;
         const int j = y - (a.first + c0);
-        const bool hit = __any_sync(0xFFFFFFFFu, j >= 0 && j < kHalf);
         T* out = a.g + static_cast<size_t>(row) * a.ldg + c0;
+        T* low = a.low != nullptr ? a.low + static_cast<size_t>(row) * a.ldg + c0 : nullptr;
 #pragma unroll
         for (int c = 0; c < kHalf; c += 16) {
-            float g[16];
+            float p[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) g[i] = exp2_approx(((z[c + i] - lse) - rest) * kLog2e);
-            if (hit) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) g[i] = c + i == j ? g[i] - 1.0f : g[i];
-            }
-            uint32_t v[8];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) g[i] *= w;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = live ? rows::Elem<T>::pack2(g[2 * i], g[2 * i + 1]) : 0u;
-            const bool in = row < a.tok.T && c0 + c < a.count;
-            if (in) store32(out + c, v);
-            if (a.low != nullptr) {
-#pragma unroll
-                for (int i = 0; i < 16; i += 8) {
-                    float high[8];
-                    rows::Elem<T>::unpack(make_uint4(v[i / 2], v[i / 2 + 1], v[i / 2 + 2], v[i / 2 + 3]), high);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) g[i + k] -= high[k];
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = live ? rows::Elem<T>::pack2(g[2 * i], g[2 * i + 1]) : 0u;
-                if (in) store32(a.low + static_cast<size_t>(row) * a.ldg + c0 + c, v);
-            }
+            for (int i = 0; i < 16; ++i) p[i] = probability(z[c + i], lse, rest);
+            if (row < a.tok.T && c0 + c < a.count) store_weights<T>(p, j - c, w, live, out + c, low != nullptr ? low + c : nullptr);
         }
         __syncwarp();
         return true;
     }
 };
+
+// g of few tokens from their kept logits, with the join: each CTA joins one token's parts (in the
+// order of join_kernel) and takes 4,096 columns.
+constexpr int kFewThreads = 256, kFewColumns = kFewThreads * 16;
+template <class T>
+__global__ void __launch_bounds__(kFewThreads) few_kernel(const Tokens tok, const float* __restrict__ z, int ldz,
+                                                          const float2* __restrict__ part, int parts, const float* __restrict__ target,
+                                                          float* __restrict__ loss, float* __restrict__ lse, float* __restrict__ rest,
+                                                          const Rows rows, T* __restrict__ g, T* __restrict__ low, int ldg) {
+    programmatic_wait();
+    constexpr int kSlots = kJoinThreads / kJoinTokens;
+    const int t = blockIdx.y, lane = threadIdx.x & 31;
+    __shared__ float2 all[kSlots / 4];
+    __shared__ uint32_t heaviest[kFewThreads / 32];
+    __shared__ float norm[2];
+    if (threadIdx.x < kSlots) {
+        float m = kNegInf, s = 0.0f;
+        for (int j = threadIdx.x; j < parts; j += kSlots) {
+            const float2 p = part[static_cast<size_t>(j) * tok.T + t];
+            join(m, s, p.x, p.y);
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) join(m, s, __shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, s, o));
+        if ((threadIdx.x & 3) == 0) all[threadIdx.x >> 2] = make_float2(m, s);
+    }
+    // the largest finite row weight in use
+    uint32_t heavy = 0u;
+    for (int i = threadIdx.x; i < tok.T; i += kFewThreads) {
+        const uint32_t bits = tok.live(i) ? __float_as_uint(tok.w(i)) & 0x7FFFFFFFu : 0u;
+        if (bits < 0x7F800000u && bits > heavy) heavy = bits;
+    }
+    heavy = __reduce_max_sync(~0u, heavy);
+    if (lane == 0) heaviest[threadIdx.x >> 5] = heavy;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kFewThreads / 32; ++i) heavy = max(heavy, heaviest[i]);
+    float w = tok.w(t);
+    const int y = tok.row(t);
+    const bool live = w != 0.0f && y >= 0;
+    if (threadIdx.x == 0) {
+        float m = all[0].x, s = all[0].y;
+        const int groups = (parts < kSlots ? parts + 3 : kSlots) / 4;   // (joining nothing changes nothing)
+        for (int j = 1; j < groups; ++j) join(m, s, all[j].x, all[j].y);
+        const Normaliser n(m, s);
+        norm[0] = n.lse, norm[1] = n.rest;
+        if (blockIdx.x == 0) {
+            loss[t] = live ? w * n.loss(target[t]) : 0.0f;
+            if (lse != nullptr) lse[t] = n.lse;
+            if (rest != nullptr) rest[t] = n.rest;
+            if (t == 0) *rows.wmax = heavy;
+        }
+    }
+    __syncthreads();
+    if (rows.copy != nullptr) rows.move(t, live, static_cast<int>(blockIdx.x) * kFewThreads + threadIdx.x, static_cast<int>(gridDim.x) * kFewThreads);
+    const int c = static_cast<int>(blockIdx.x) * kFewColumns + threadIdx.x * 16;
+    if (c >= ldg) return;   // (columns beyond N lie outside the products' maps)
+    w = ldexpf(w, scale_exponent<std::is_same<T, __half>::value>(heavy));
+    float p[16];
+    const float4* src = reinterpret_cast<const float4*>(z + static_cast<size_t>(t) * ldz + c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 q = __ldcs(src + i);
+        p[4 * i] = q.x, p[4 * i + 1] = q.y, p[4 * i + 2] = q.z, p[4 * i + 3] = q.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) p[i] = probability(p[i], norm[0], norm[1]);
+    const size_t at = static_cast<size_t>(t) * ldg + c;
+    store_weights<T>(p, y - c, w, live, g + at, low + at);
+}
 
 // The next accumulator's 128 columns of a thread's row, scaled and rounded, to `out` (`columns` of
 // them there, a multiple of 8): in 32-byte pieces where rows are so aligned (`wide`), else 16.
@@ -543,8 +638,11 @@ gemm::Shape head_tiles(int rows, int N, int K, int piece, unsigned int* error) {
     return s;
 }
 
+// Whether a call for both keeps its logits: few tokens whose vocabulary is one piece.
+bool keeps_logits(int T, int N) { return T <= gemm::kRows && N <= piece_rows(terms_of(T) * T, N); }
+
 struct Space {
-    size_t wmax, part, target, lse, rest, g, hidden, sum, parts, head_parts, bytes;
+    size_t z, wmax, part, target, lse, rest, g, hidden, sum, parts, head_parts, bytes;
 };
 Space space_of(int T, int N, int K, bool loss, bool dh, bool dw) {
     Space s = {};
@@ -564,6 +662,7 @@ Space space_of(int T, int N, int K, bool loss, bool dh, bool dw) {
     const int rows = terms_of(T) * T, piece = piece_rows(rows, N);
     const size_t r = static_cast<size_t>(rows);
     if (dh || dw) s.g = take(r * piece * 2);
+    if (loss && (dh || dw) && keeps_logits(T, N)) s.z = take(t * up256(N) * 4);
     if (dw) {
         s.hidden = take(r * K * 2);
         const gemm::Shape w = head_tiles(rows, N, K, piece, nullptr);
@@ -601,6 +700,8 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
     pieces.first.map_a = map_h;
     pieces.first.map_b = map_w;
     const int steps = ceil_div(c.K, K1::kK);
+    const bool kept = P == 1 && loss && (dh || dw) && keeps_logits(c.T, c.N);
+    const float2* part = reinterpret_cast<const float2*>(ws + sp.part);
     const float* lse = c.lse_in;
     const float* rest = c.rest_in;
     if (loss) {
@@ -612,11 +713,16 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
         a.part = reinterpret_cast<float2*>(ws + sp.part);
         a.target = reinterpret_cast<float*>(ws + sp.target);
         a.wmax = wmax;
+        if (kept) {
+            a.z = reinterpret_cast<float*>(ws + sp.z);
+            a.ldz = static_cast<int>(up256(c.N));
+        }
         if ((e = gemm::launch(logits, stream)) != cudaSuccess) return e;
         float* l = c.lse != nullptr ? c.lse : reinterpret_cast<float*>(ws + sp.lse);
         float* r = c.rest != nullptr ? c.rest : reinterpret_cast<float*>(ws + sp.rest);
-        e = gemm::launch_early(join_kernel, dim3(static_cast<unsigned>(ceil_div(c.T, kJoinTokens))), kJoinThreads, 0, 1, stream, tok, a.part,
-                               2 * a.shape.tiles_n, a.target, c.loss, l, r, dh || dw ? rows : Rows{});
+        if (!kept)
+            e = gemm::launch_early(join_kernel, dim3(static_cast<unsigned>(ceil_div(c.T, kJoinTokens))), kJoinThreads, 0, 1, stream, tok, a.part,
+                                   2 * a.shape.tiles_n, a.target, c.loss, l, r, dh || dw ? rows : Rows{});
         if (e != cudaSuccess) return e;
         lse = l;
         rest = r;
@@ -649,7 +755,14 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
         a.ldg = piece;
         a.first = first;
         a.count = count;
-        if ((e = gemm::launch(pieces, stream)) != cudaSuccess) return e;
+        if (kept) {
+            const dim3 grid(static_cast<unsigned>(ceil_div(count, kFewColumns)), static_cast<unsigned>(c.T));
+            e = gemm::launch_early(few_kernel<T>, grid, kFewThreads, 0, 1, stream, tok, logits.first.args.z, logits.first.args.ldz, part,
+                                   2 * ceil_div(c.N, kTN), logits.first.args.target, c.loss, c.lse, c.rest, rows, g, a.low, piece);
+        } else {
+            e = gemm::launch(pieces, stream);
+        }
+        if (e != cudaSuccess) return e;
         gemm::Jobs<Hidden<T>, Head<T>> both = {};
         if (dh) {
             using L = typename Hidden<T>::Layout;
