@@ -106,7 +106,7 @@ __device__ __forceinline__ bool sum_logits(Acc<L>& acc, int steps, uint32_t offs
 
 template <class T, int P>
 struct Stats {
-    using Layout = gemm::Layout<P, kTN, 2, false, false>;
+    using Layout = gemm::Layout<P, 1, kTN, 2, false, false>;
     static constexpr int kFormat = std::is_same<T, __half>::value ? 0 : 1, kChunk = logit_chunk(P);
     static constexpr bool kAKeep = true, kBKeep = true;
     struct Args {
@@ -277,7 +277,7 @@ __device__ __forceinline__ void store_weights(float (&p)[16], int j, float w, bo
 
 template <class T, int P>
 struct Weights {   // g of a piece
-    using Layout = gemm::Layout<P, kTN, 2, false, false>;
+    using Layout = gemm::Layout<P, 1, kTN, 2, false, false>;
     static constexpr bool kF16 = std::is_same<T, __half>::value;
     static constexpr int kFormat = kF16 ? 0 : 1;
     static constexpr int kChunk = logit_chunk(P);
@@ -455,7 +455,7 @@ __device__ __forceinline__ bool store_sums(A& acc, float* out, bool in, int colu
 // and first parts, then the other parts of the tiles that are split, [split - 1][tile][256][256].
 template <class T>
 struct Hidden {
-    using Layout = gemm::Layout<kPair, kTN, 2, false, true>;
+    using Layout = gemm::Layout<kPair, 1, kTN, 2, false, true>;
     static constexpr int kFormat = std::is_same<T, __half>::value ? 0 : 1;
     static constexpr int kChunk = gemm::kWholeTile;
     static constexpr bool kAKeep = true, kBKeep = true;
@@ -494,7 +494,7 @@ struct Hidden {
 // dW: the piece's g (along the tokens) times the hidden states, final.
 template <class T>
 struct Head {
-    using Layout = gemm::Layout<kPair, kTN, 2, true, true>;
+    using Layout = gemm::Layout<kPair, 1, kTN, 2, true, true>;
     static constexpr bool kF16 = std::is_same<T, __half>::value;
     static constexpr int kFormat = kF16 ? 0 : 1;
     static constexpr int kChunk = gemm::kWholeTile;

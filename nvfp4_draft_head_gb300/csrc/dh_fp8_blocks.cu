@@ -172,9 +172,9 @@ __device__ __forceinline__ void store64(TY* y, long long ldy, const float (&v)[6
 
 // Tokens along the rows of a tile, output features along its columns; W K-major for y, and
 // MN-major (its rows along the contraction) for dx.
-template <class TY, bool GRADIENT, int TN>
+template <class TY, bool GRADIENT, int TN, int SHARE>
 struct Product {
-    using Layout = gemm::Layout<1, TN, 1, false, GRADIENT, TN / 16, 2>;
+    using Layout = gemm::Layout<1, SHARE, TN, 1, false, GRADIENT, TN / 16, 2>;
     static constexpr int kFormat = 0;
     static constexpr int kChunk = 1;
     static constexpr bool kAKeep = true, kBKeep = true;
@@ -190,10 +190,10 @@ struct Product {
         float* parts;         // the contraction in parts: their sums, [split][M][ldp]
         long long ldp;
     };
-    __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int, Acc<Layout>& acc) {
+    __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int rank, Acc<Layout>& acc) {
         constexpr int kPart = Layout::kPart;
         static_assert(kPart == 64 && Layout::kP == 1, "a warp's columns lie in one block of the weight");
-        const int row0 = t.m * gemm::kRows + (warp & 3) * 32, row = row0 + lane, steps = t.steps;
+        const int row0 = (t.m * Layout::kCtas + rank) * gemm::kRows + (warp & 3) * 32, row = row0 + lane, steps = t.steps;
         const int n0 = t.n * Layout::kTN + (warp >> 2) * kPart;
         const bool in = row < a.M;
         // (columns beyond N: any scale)
@@ -249,10 +249,10 @@ __global__ void __launch_bounds__(256) sum_kernel(const float* __restrict__ part
 
 // ------------------------------------------------------------------- host ----
 
-// How a product of many tokens runs: the width of its tiles, and the parts of its contraction
-// where the tiles alone would leave SMs idle.
+// How a product of many tokens runs: the width of its tiles, the CTAs that share a tile's columns
+// of the weight, and the parts of its contraction where the tiles alone would leave SMs idle.
 struct Plan {
-    int tn, parts, part_steps;
+    int tn, share, parts, part_steps;
     float us;
 };
 
@@ -260,18 +260,25 @@ struct Plan {
 // 128-wide one: wide tiles have twice the work between two hand-overs, narrow ones spread a small
 // product over more SMs), or by reading the weight. Parts cost a second kernel. Measured, us: 200
 // tokens, gradient of 64,026 x 2,560 193 in one part; 512 x 4,608 x 2,560 15.0 wide, 13.3 narrow.
+// Wide tiles run two by two, row blocks that share their columns of the weight, where that adds no
+// round (an odd last row block leaves one of its two idle): 8,192 x 64,064 x 2,560 1,150 single,
+// 1,104 shared; 4,096 x 4,608 x 2,560 56.6 and 55.2.
 Plan plan_of(int M, int out, int width) {
     constexpr int kSms = 152;
     const int steps = ceil_div(width, kBlock);
-    Plan best = {256, 1, steps, 0.0f};
+    Plan best = {256, 1, 1, steps, 0.0f};
     for (int tn = 256; tn >= 128; tn /= 2) {
         const long long tiles = static_cast<long long>(ceil_div(M, gemm::kRows)) * ceil_div(out, tn);
         for (int p = 1; p <= 16 && (p == 1 || (p * tiles <= kSms && steps / p >= 4)); ++p) {
             const int part = ceil_div(steps, p);
             const float us = static_cast<float>((tiles * p + kSms - 1) / kSms) * (part * (tn == 256 ? 0.43f : 0.38f) + 1.5f) +
                              (p > 1 ? 3.0f + p * static_cast<float>(M) * out * 1.0e-6f : 0.0f);
-            if ((tn == 256 && p == 1) || us < best.us) best = {tn, ceil_div(steps, part), part, us};
+            if ((tn == 256 && p == 1) || us < best.us) best = {tn, 1, ceil_div(steps, part), part, us};
         }
+    }
+    if (best.tn == 256 && best.parts == 1) {
+        const long long rows = ceil_div(M, gemm::kRows), columns = ceil_div(out, 256);
+        if (((rows + 1) / 2 * columns + kSms / 2 - 1) / (kSms / 2) <= (rows * columns + kSms - 1) / kSms) best.share = 2;
     }
     const float read = static_cast<float>(width) * out * (1.0f / 4.4e6f);
     if (best.us < read) best.us = read;
@@ -293,18 +300,18 @@ cudaError_t quantize(const Fp8BlockArgs& f, int width, uint8_t* codes, int ldc, 
                               static_cast<const T*>(f.x), f.ldx, f.M, width, codes, ldc, scales);
 }
 
-template <class TY, bool GRADIENT, int TN>
+template <class TY, bool GRADIENT, int TN, int SHARE>
 cudaError_t product(const Fp8BlockArgs& f, const Plan& plan, const uint8_t* codes, int ldc, const float* scales, float* parts, cudaStream_t s) {
-    using P = Product<TY, GRADIENT, TN>;
+    using P = Product<TY, GRADIENT, TN, SHARE>;
     using L = typename P::Layout;
     const int width = GRADIENT ? f.N : f.K, out = GRADIENT ? f.K : f.N, kb = ceil_div(f.K, kBlock);
     gemm::Jobs<P> jobs = {};
     cudaError_t e = gemm::encode_operand<L, false>(&jobs.first.map_a, codes, f.M, width, ldc, gemm::kRows);
     if (e != cudaSuccess) return e;
-    if ((e = gemm::encode_operand<L, GRADIENT>(&jobs.first.map_b, f.q, out, width, f.K, L::kBRows)) != cudaSuccess) return e;
+    if ((e = gemm::encode_operand<L, GRADIENT>(&jobs.first.map_b, f.q, out, width, f.K, L::kBLoad)) != cudaSuccess) return e;
     typename P::Args& a = jobs.first.args;
     const int steps = ceil_div(width, kBlock);
-    a.shape = gemm::whole_tiles(ceil_div(f.M, gemm::kRows), ceil_div(out, L::kTN), steps, f.error);
+    a.shape = gemm::whole_tiles(ceil_div(f.M, gemm::kRows * L::kCtas), ceil_div(out, L::kTN), steps, f.error);
     a.shape.rounds = f.probe_rounds;
     a.shape.idle = f.probe_role;
     a.sx = scales;
@@ -330,9 +337,14 @@ cudaError_t product(const Fp8BlockArgs& f, const Plan& plan, const uint8_t* code
 
 template <class TY>
 cudaError_t run_many(const Fp8BlockArgs& f, const Plan& p, const uint8_t* codes, int ldc, const float* scales, float* parts, cudaStream_t s) {
-    if (p.tn == 256)
-        return f.gradient ? product<TY, true, 256>(f, p, codes, ldc, scales, parts, s) : product<TY, false, 256>(f, p, codes, ldc, scales, parts, s);
-    return f.gradient ? product<TY, true, 128>(f, p, codes, ldc, scales, parts, s) : product<TY, false, 128>(f, p, codes, ldc, scales, parts, s);
+    const auto with = [&](auto tn, auto share) {
+        constexpr int kTN = decltype(tn)::value, kShare = decltype(share)::value;
+        return f.gradient ? product<TY, true, kTN, kShare>(f, p, codes, ldc, scales, parts, s)
+                          : product<TY, false, kTN, kShare>(f, p, codes, ldc, scales, parts, s);
+    };
+    using One = std::integral_constant<int, 1>;
+    if (p.tn == 128) return with(std::integral_constant<int, 128>(), One());
+    return p.share == 2 ? with(std::integral_constant<int, 256>(), std::integral_constant<int, 2>()) : with(std::integral_constant<int, 256>(), One());
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }

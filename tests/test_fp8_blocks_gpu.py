@@ -194,6 +194,16 @@ def test_long_contractions(M, N, K, grad):
     check(y, quantise(x, 1)[2], wv if grad else wv.t(), x.shape[1])
 
 
+# wide tiles: one by one (three row blocks, which two by two would take a second round), two by two,
+# and with an odd last row block
+@pytest.mark.parametrize("M,out,width", [(300, 12640, 272), (2000, 4608, 528), (1100, 4592, 272)])
+@pytest.mark.parametrize("grad", [False, True])
+def test_wide_tiles(M, out, width, grad):
+    mm, wv = layer(*((width, out) if grad else (out, width)))
+    x = rows(M, width, BF)
+    check(mm.input_gradient(x, out_dtype=F) if grad else mm(x, out_dtype=F), quantise(x, 1)[2], wv if grad else wv.t(), width)
+
+
 def test_no_tokens_and_float8_codes():
     q, s, wv = quantise(weight(64, 128), 128)
     mm = dh.FP8BlockMatmul(q.contiguous(), s.contiguous())
