@@ -492,8 +492,8 @@ int fp8_quantize_blocks(const void *W, int V, int K, const int32_t *idx, int N, 
 
 /* Bytes of workspace of the two products below for M tokens of `width` features with `out`
  * results each (K and N for fp8_block_matmul, N and K for the gradient): the quantised
- * activations, and the sums of the contraction's parts where it is split (0 for an
- * unsupported shape). */
+ * activations, and the sums of the contraction's parts where it is split; 256 where the
+ * product quantises them itself and uses none (0 for an unsupported shape). */
 size_t fp8_block_matmul_workspace_bytes(int M, int width, int out);
 
 /* y = x W'^T with the activations quantised per token and block of 128 features, inside
@@ -502,7 +502,7 @@ size_t fp8_block_matmul_workspace_bytes(int M, int width, int out);
  * products exact, sums in fp32, one rounding to y's type. A block of x with a value that is
  * not finite makes its token's results NaN; tokens do not affect one another. x: [M][K] of
  * dh_type x_type, row stride ldx elements; y: [M][N] of y_type, stride ldy (ignored when
- * M == 1); both aligned to their element. 1 <= M <= 2^24. ws, error: as for nvfp4_matmul.
+ * M == 1); both aligned to their element; y may overlap neither x nor the weight. 1 <= M <= 2^24. ws, error: as for nvfp4_matmul.
  * Repeatable bit for bit. Capturable in a CUDA graph. */
 int fp8_block_matmul(const dh_fp8_blocks_t *w, const void *x, int x_type, int64_t ldx, int M, void *y, int y_type, int64_t ldy, void *ws,
                      size_t ws_bytes, unsigned int *error, void *stream);
@@ -523,7 +523,8 @@ int fp8_block_matmul_wait_probe(const dh_fp8_blocks_t *w, const void *x, int M, 
                                 unsigned int rounds, unsigned int *error, void *stream);
 
 /* Softmax cross entropy of T hidden states against the vocabulary given by N head
- * rows, and its gradients, without logits in memory (the pages have no counterpart: it
+ * rows, and its gradients, without the T x N logits in memory (but for up to 128 tokens
+ * whose gradients are computed in the same call: see the workspace) (the pages have no counterpart: it
  * is how the BF16 rows of a draft head are trained on the tokens themselves, before
  * they are quantised). With z = h_t . W_n and y_t the head row of tokens[t]:
  *   lse_t  = log sum_n e^z_tn,  loss_t = w_t (lse_t - z_ty),
@@ -563,16 +564,19 @@ typedef struct dh_cross_entropy {
 /* Bytes of workspace of a call with these outputs (0 for an unsupported shape): 8 bytes
  * per token and 128 head rows for the loss; for the gradients g of a piece of the
  * vocabulary in 16 bits (512 MiB at most while T <= 131,072) and, each where it is
- * wanted, 32-bit sums of dh and a copy of the hidden states. */
+ * wanted, 32-bit sums of dh (and of dW's tiles, where they are few and the tokens many) and
+ * a copy of the hidden states. Up to 128 tokens have g in two 16-bit terms, and, where the
+ * loss and a gradient are wanted together and the vocabulary is one piece, their logits in
+ * fp32 between the two. */
 size_t draft_head_cross_entropy_workspace_bytes(int T, int N, int K, unsigned int outputs);
 
 /* The loss (fp32 [T]) and, where their pointers are not NULL, the normaliser lse (fp32
  * [T]), what rounding it to fp32 left over, rest (fp32 [T]), dhidden ([T][K]) and dhead
  * ([N][K]) of the inputs' type, rows 16-byte aligned; the gradients are those of the
- * losses' sum. None of the outputs may overlap an input. ws: 256-byte aligned, no
- * initialisation; calls that overlap on the GPU must not share one. error: as for
+ * losses' sum. None of the outputs may overlap an input or another output. ws: 256-byte
+ * aligned, no initialisation; calls that overlap on the GPU must not share one. error: as for
  * nvfp4_matmul. Sums in 32 bits; g is rounded to 16 bits between its products (with a
- * power of two taken out), the gradients once more. Repeatable bit for bit. Capturable
+ * power of two taken out; up to 128 tokens to two such terms), the gradients once more. Repeatable bit for bit. Capturable
  * in a CUDA graph. */
 int draft_head_cross_entropy(const dh_cross_entropy_t *c, float *loss, float *lse, float *rest, void *dhidden, int64_t ld_dhidden,
                              void *dhead, int64_t ld_dhead, void *ws, size_t ws_bytes, unsigned int *error, void *stream);

@@ -27,7 +27,7 @@ Names follow the C ABI in include/drafthead.h:
   (_forward, _backward)    the loss alone; the gradient from its normaliser
   DistillTopK              the same as a torch.autograd function
   linear_cross_entropy     draft_head_cross_entropy: loss of the tokens under head rows
-                           and its gradients, without logits in memory
+                           and its gradients, without the [T, N] logits in memory
   (_forward, _backward)    the loss alone; the gradients from its normaliser
   LinearCrossEntropy       the same as a torch.autograd function
 A call given stream= works and allocates on that stream: its arguments have to be
@@ -720,7 +720,7 @@ class FP8BlockMatmul:
     fp8_quantize_blocks or an FP8 checkpoint (its weight_scale_inv); K % 16 == 0, any N.
     forward(x) = x W'^T for any number of tokens, x quantised per token and 128 features
     (W8A8), fp32 sums. An x that requires a gradient is refused: FP8BlockLinear is the
-    differentiable form."""
+    differentiable form. A given result may overlap neither the input nor the weight."""
 
     def __init__(self, q: torch.Tensor, scale: torch.Tensor, stream=None):
         if stream is not None:
@@ -793,15 +793,19 @@ class FP8BlockMatmul:
             if y.shape != (M, out) or y.dtype not in _TYPES or y.device != device or (y.stride(1) != 1 and out > 1) or \
                     (M > 1 and y.stride(0) < out):
                 raise ValueError(f"the result must be a [{M}, {out}] bfloat16, float16 or float32 tensor with contiguous rows on {device}")
+            if M > 0 and y.data_ptr() == x.data_ptr():
+                raise ValueError("the result must not be the input")
             out_dtype, ldy = y.dtype, y.stride(0)
         if M == 0:
             return y
         L, s = lib(), _stream_of(x)
         nb = self._bytes.get((M, width))
         if nb is None:
-            nb = self._bytes[M, width] = L.fp8_block_matmul_workspace_bytes(M, width, out)
+            nb = L.fp8_block_matmul_workspace_bytes(M, width, out)
             if nb == 0:
                 raise DraftHeadError(name, DH_ERR_SHAPE)
+            if len(self._bytes) < 4096:
+                self._bytes[M, width] = nb
         ws = self._none if nb == DH_WORKSPACE_ALIGN else torch.empty(nb, dtype=torch.uint8, device=device)
         st = getattr(L, name)(self.desc_ref, x.data_ptr(), t, ldx, M, y.data_ptr(), _TYPES[out_dtype], ldy, ws.data_ptr(), nb, self.error_ptr, s)
         if st != DH_OK:
@@ -1149,9 +1153,9 @@ def linear_cross_entropy(hidden: torch.Tensor, head: torch.Tensor, tokens: torch
     """(loss float32 [T], dhidden [T, K], dhead [N, K]): per-token softmax cross entropy of
     hidden states [T, K] against the vocabulary of the head rows [N, K] (both bfloat16 or
     both float16, K % 8 == 0, rows 16-byte aligned), and the gradients of its sum, without
-    logits in memory. tokens: int32 [T], target ids with row_of (draft_head_row_map), head rows
+    the [T, N] logits in memory (but for up to 128 tokens). tokens: int32 [T], target ids with row_of (draft_head_row_map), head rows
     without it; a token without a head row (-100, say) is left out, as a row of weight 0 is.
-    weights: float32 [T]. dhidden and dhead may be given tensors. The loss has no autograd
+    weights: float32 [T]. dhidden and dhead may be given tensors, which overlap no other. The loss has no autograd
     graph (the gradients are at hand; LinearCrossEntropy is the differentiable form). See
     draft_head_cross_entropy."""
     if stream is not None:
@@ -1232,7 +1236,9 @@ class LinearCrossEntropy(torch.autograd.Function):
     """loss [T] = LinearCrossEntropy.apply(hidden, head, tokens, weights, row_of);
     differentiable once in the hidden states, the head and the weights (a weight's
     derivative is the loss that its row has at weight 1). No logits are kept between the
-    passes: the backward pass multiplies them again from the normaliser."""
+    passes: the backward pass multiplies them again from the normaliser. (A backward pass that
+    is captured into a CUDA graph needs leaves of which no eager graph is alive, as torch has it
+    for every function: drop earlier losses first.)"""
 
     @staticmethod
     def forward(ctx, hidden, head, tokens, weights=None, row_of=None):
@@ -1262,7 +1268,8 @@ class LinearCrossEntropy(torch.autograd.Function):
 class FP8BlockLinear(torch.autograd.Function):
     """y [M, N] = FP8BlockLinear.apply(x, matmul, out_dtype): matmul (an FP8BlockMatmul) as a
     frozen layer, differentiable once in x: dx = matmul.input_gradient(dy), of x's type (the
-    rounding of x to FP8 passes the gradient straight through)."""
+    rounding of x to FP8 passes the gradient straight through). Captured backward passes: as
+    for LinearCrossEntropy."""
 
     @staticmethod
     def forward(ctx, x, matmul, out_dtype=torch.bfloat16):

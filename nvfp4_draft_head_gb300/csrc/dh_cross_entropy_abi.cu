@@ -34,7 +34,7 @@ int check(const dh_cross_entropy_t* c, void* dhidden, int64_t ld_dhidden, void* 
           const unsigned int* error, dh::CrossEntropyArgs& a) {
     if (c == nullptr || c->hidden == nullptr || c->head == nullptr || c->tokens == nullptr || ws == nullptr) return DH_ERR_ARG;
     if (c->type != DH_T_BF16 && c->type != DH_T_F16) return DH_ERR_ARG;
-    if (dhidden == c->hidden || dhead == c->head) return DH_ERR_ARG;   // not in place
+    if (dhidden == c->hidden || dhead == c->head || (dhidden != nullptr && dhidden == dhead)) return DH_ERR_ARG;   // not in place
     if (!shape_ok(c->T, c->N, c->K)) return DH_ERR_SHAPE;
     if (c->row_of != nullptr && c->V < 1) return DH_ERR_SHAPE;
     int st;

@@ -28,7 +28,7 @@ bool tokens_ok(int M, int width, int out) {
 int product(const dh_fp8_blocks_t* w, bool gradient, const void* x, int x_type, int64_t ldx, int M, void* y, int y_type, int64_t ldy,
             void* ws, size_t ws_bytes, unsigned int* error, void* stream, int probe_role = 0, unsigned int probe_rounds = 0) {
     if (w == nullptr || w->q == nullptr || w->scale == nullptr || x == nullptr || y == nullptr) return DH_ERR_ARG;
-    if (type_bytes(x_type) == 0 || type_bytes(y_type) == 0) return DH_ERR_ARG;
+    if (type_bytes(x_type) == 0 || type_bytes(y_type) == 0 || x == y) return DH_ERR_ARG;   // (not in place)
     if (!weight_ok(w->N, w->K)) return DH_ERR_SHAPE;
     const int width = gradient ? w->N : w->K, out = gradient ? w->K : w->N;
     if (!tokens_ok(M, width, out)) return DH_ERR_SHAPE;

@@ -6,7 +6,7 @@ import torch
 
 import nvfp4_draft_head_gb300 as dh
 
-A, B, WS = 0x10000, 0x20000, 0x100000
+A, B, WS, D = 0x10000, 0x20000, 0x100000, 0x101000
 
 
 @pytest.fixture(scope="module")
@@ -55,21 +55,21 @@ def test_descriptor(L, kw, status):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(loss=None), dh.DH_ERR_ARG), (dict(ws=None), dh.DH_ERR_ARG), (dict(dh=A), dh.DH_ERR_ARG), (dict(dw=B), dh.DH_ERR_ARG),
+    (dict(loss=None), dh.DH_ERR_ARG), (dict(ws=None), dh.DH_ERR_ARG), (dict(dh=A), dh.DH_ERR_ARG), (dict(dw=B), dh.DH_ERR_ARG), (dict(dw=WS), dh.DH_ERR_ARG),
     (dict(ldh=120), dh.DH_ERR_SHAPE), (dict(ldw=0), dh.DH_ERR_SHAPE), (dict(dh=WS + 8), dh.DH_ERR_ALIGN), (dict(ldw=132), dh.DH_ERR_ALIGN),
     (dict(loss=A + 2), dh.DH_ERR_ALIGN), (dict(lse=A + 1), dh.DH_ERR_ALIGN), (dict(rest=A + 1), dh.DH_ERR_ALIGN), (dict(err=A + 1), dh.DH_ERR_ALIGN),
     (dict(ws=WS + 64), dh.DH_ERR_WORKSPACE), (dict(nb=4096), dh.DH_ERR_WORKSPACE),
 ])
 def test_outputs(L, kw, status):
-    a = dict(loss=A, lse=None, rest=None, dh=WS, ldh=128, dw=WS, ldw=128, ws=WS, nb=1 << 30, err=None)
+    a = dict(loss=A, lse=None, rest=None, dh=WS, ldh=128, dw=D, ldw=128, ws=WS, nb=1 << 30, err=None)
     a.update(kw)
     assert L.draft_head_cross_entropy(desc(), a["loss"], a["lse"], a["rest"], a["dh"], a["ldh"], a["dw"], a["ldw"], a["ws"], a["nb"], a["err"],
                                       None) == status
 
 
 @pytest.mark.parametrize("args,status", [
-    ((None, None, WS, 128, WS, 128), dh.DH_ERR_ARG), ((A, None, None, 0, None, 0), dh.DH_ERR_ARG), ((A, A + 2, WS, 128, WS, 128), dh.DH_ERR_ALIGN),
-    ((A + 2, None, WS, 128, WS, 128), dh.DH_ERR_ALIGN),
+    ((None, None, WS, 128, D, 128), dh.DH_ERR_ARG), ((A, None, None, 0, None, 0), dh.DH_ERR_ARG), ((A, None, D, 128, D, 128), dh.DH_ERR_ARG),
+    ((A, A + 2, WS, 128, D, 128), dh.DH_ERR_ALIGN), ((A + 2, None, WS, 128, D, 128), dh.DH_ERR_ALIGN),
 ])
 def test_backward(L, args, status):
     assert L.draft_head_cross_entropy_backward(desc(), *args, WS, 1 << 30, None, None) == status

@@ -242,7 +242,9 @@ def test_refusals():
                 dict(hidden=torch.zeros((6, 68), dtype=h.dtype, device=DEV)[:, :64])):
         with pytest.raises(ValueError):
             dh.linear_cross_entropy(**{**s, **bad})
-    for bad in (dict(hidden=h[:, :60].contiguous(), head=W[:, :60].contiguous()), dict(dhidden=h), dict(dhead=W)):
+    square = torch.empty((40, 64), dtype=h.dtype, device=DEV)
+    for bad in (dict(hidden=h[:, :60].contiguous(), head=W[:, :60].contiguous()), dict(dhidden=h), dict(dhead=W),
+                dict(dhidden=square[:6], dhead=square)):
         with pytest.raises((dh.DraftHeadError, ValueError)):
             dh.linear_cross_entropy(**{**s, **bad})
     torch.cuda.synchronize()

@@ -6,7 +6,7 @@ import torch
 
 import nvfp4_draft_head_gb300 as dh
 
-A, WS = 0x10000, 0x100000
+A, B, WS = 0x10000, 0x20000, 0x100000
 
 
 @pytest.fixture(scope="module")
@@ -29,7 +29,7 @@ def test_sizes(L):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(q=None), dh.DH_ERR_ARG), (dict(scale=None), dh.DH_ERR_ARG), (dict(x=None), dh.DH_ERR_ARG), (dict(y=None), dh.DH_ERR_ARG),
-    (dict(xt=0), dh.DH_ERR_ARG), (dict(yt=4), dh.DH_ERR_ARG), (dict(ws=None), dh.DH_ERR_ARG),
+    (dict(xt=0), dh.DH_ERR_ARG), (dict(y=A), dh.DH_ERR_ARG), (dict(yt=4), dh.DH_ERR_ARG), (dict(ws=None), dh.DH_ERR_ARG),
     (dict(N=0), dh.DH_ERR_SHAPE), (dict(K=24), dh.DH_ERR_SHAPE), (dict(K=0), dh.DH_ERR_SHAPE), (dict(M=0), dh.DH_ERR_SHAPE),
     (dict(M=-3), dh.DH_ERR_SHAPE), (dict(M=(1 << 24) + 1), dh.DH_ERR_SHAPE), (dict(N=(1 << 24) + 1), dh.DH_ERR_SHAPE),
     (dict(ldx=127), dh.DH_ERR_SHAPE), (dict(ldy=-256), dh.DH_ERR_SHAPE),
@@ -38,12 +38,12 @@ def test_sizes(L):
     (dict(ws=WS + 16), dh.DH_ERR_WORKSPACE), (dict(nb=255), dh.DH_ERR_WORKSPACE), (dict(M=100, nb=256), dh.DH_ERR_WORKSPACE),
 ])
 def test_products(L, kw, status):
-    a = dict(N=256, K=256, q=A, scale=A, x=A, xt=dh.DH_T_BF16, ldx=256, M=4, y=A, yt=dh.DH_T_BF16, ldy=256, ws=WS, nb=1 << 20, err=None)
+    a = dict(N=256, K=256, q=A, scale=A, x=A, xt=dh.DH_T_BF16, ldx=256, M=4, y=B, yt=dh.DH_T_BF16, ldy=256, ws=WS, nb=1 << 20, err=None)
     a.update(kw)
     w = dh.dh_fp8_blocks_t(a["N"], a["K"], a["q"], a["scale"])
     for f in (L.fp8_block_matmul, L.fp8_block_matmul_input_gradient):
         assert f(C.byref(w), a["x"], a["xt"], a["ldx"], a["M"], a["y"], a["yt"], a["ldy"], a["ws"], a["nb"], a["err"], None) == status
-        assert f(None, A, 1, 256, 4, A, 1, 256, WS, 1 << 20, None, None) == dh.DH_ERR_ARG
+        assert f(None, A, 1, 256, 4, B, 1, 256, WS, 1 << 20, None, None) == dh.DH_ERR_ARG
 
 
 @pytest.mark.parametrize("args,status", [
@@ -68,7 +68,7 @@ def test_wait_probe(L, kw, status):
     a = dict(w=True, x=A, M=4, nb=1 << 20, role=1, rounds=16, err=A)
     a.update(kw)
     w = C.byref(dh.dh_fp8_blocks_t(128, 256, A, A)) if a["w"] else None
-    assert L.fp8_block_matmul_wait_probe(w, a["x"], a["M"], A, WS, a["nb"], a["role"], a["rounds"], a["err"], None) == status
+    assert L.fp8_block_matmul_wait_probe(w, a["x"], a["M"], B, WS, a["nb"], a["role"], a["rounds"], a["err"], None) == status
 
 
 def test_binding_refuses_host_tensors():

@@ -223,7 +223,7 @@ def test_refusals():
                 lambda: mm(x.double()), lambda: mm(x.cpu()), lambda: mm(x[0]), lambda: mm(x, out_dtype=torch.float64),
                 lambda: mm(x, torch.empty((4, 65), device=DEV)), lambda: mm(x, torch.empty((64, 4), device=DEV).t()),
                 lambda: mm.input_gradient(x), lambda: mm(x.float().requires_grad_()), lambda: mm.input_gradient(rows(4, 64, F).requires_grad_()),
-                lambda: mm(x[:1].expand(4, 128)), lambda: dh.fp8_quantize_blocks(weight(64, 128).float())):
+                lambda: mm(x[:1].expand(4, 128)), lambda: mm(x, x[:, :64]), lambda: dh.fp8_quantize_blocks(weight(64, 128).float())):
         with pytest.raises(ValueError):
             bad()
     for bad in (lambda: dh.FP8BlockMatmul(q[:, :120].contiguous(), s), lambda: dh.FP8BlockMatmul(q[:0], s[:0]),

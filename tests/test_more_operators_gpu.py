@@ -76,6 +76,38 @@ def test_training_a_head_behind_a_frozen_layer():
     assert dh.linear_cross_entropy_device_error() == 0
 
 
+@pytest.mark.parametrize("T", [40, 300])
+def test_captured_training_step(T):
+    """Forward and backward pass of both captured into one graph, with leaves of its own, and
+    replayed on other inputs."""
+    n, K = 1000, 256
+    layer = dh.FP8BlockMatmul.from_weight(rand((K, K), 3, K ** -0.5))
+    inputs = [(rand((T, K), 10 + i), rand((n, K), 20 + i, 0.1), (torch.arange(T, device="cuda", dtype=torch.int32) * (i + 3)) % n,
+               torch.rand(T, generator=torch.Generator("cuda").manual_seed(i), device="cuda")) for i in range(2)]
+
+    def step(x, rows, tokens, weights):
+        loss = dh.LinearCrossEntropy.apply(dh.FP8BlockLinear.apply(x, layer), rows, tokens, weights, None)
+        return (loss.detach(), *torch.autograd.grad(loss.sum(), (x, rows, weights)))
+
+    def leaves(a):
+        return tuple(t.clone().requires_grad_(t.is_floating_point()) for t in a)
+
+    want = [step(*leaves(a)) for a in inputs]
+    static = leaves(inputs[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(*static)
+    for i in (0, 1, 0):
+        with torch.no_grad():
+            for s, v in zip(static, inputs[i]):
+                s.copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want[i]):
+            assert torch.equal(a, b)
+    assert layer.device_error() == 0 and dh.linear_cross_entropy_device_error() == 0
+
+
 # ----------------------------------------------------------------- streams --
 
 def test_beside_pending_work():
