@@ -591,7 +591,7 @@ int draft_head_cross_entropy_backward(const dh_cross_entropy_t *c, const float *
 
 /* The self-test of draft_head_cross_entropy's waits, on the loss alone: roles, rounds and
  * error as for fp8_block_matmul_wait_probe (role 2 is waited for where an SM has more than
- * 1,024 features or two tiles). */
+ * 512 features or two tiles). */
 int draft_head_cross_entropy_wait_probe(const dh_cross_entropy_t *c, float *loss, void *ws, size_t ws_bytes, int role, unsigned int rounds,
                                         unsigned int *error, void *stream);
 

@@ -78,17 +78,19 @@ __device__ __forceinline__ int scale_exponent(uint32_t wmax) {
 // The tensor cores' 32-bit sums are truncated, not rounded, as they grow: over the 160
 // instructions of 2,560 features a large logit loses 2e-6 of itself, four times what a product
 // in 32 bits is off by. So they sum some steps of 64 features at a time, which the epilogue adds
-// up, rounded: the loss of 4,095 x 64,026 was off by 1.8e-6, and is by 3.4e-7 with eight steps
-// (the same time; four cost 8 % there, and nothing where reading the head is the work).
-constexpr int logit_chunk(int P) { return P == 1 ? 4 : 8; }
+// up, rounded: the loss of 4,095 x 64,026 was off by 1.8e-6, and is by 3.4e-7 with eight steps, as a
+// sum in 32 bits is. That of fewer features is off by less: there four steps (lse of 385 x 595 x 416
+// off by 1.3e-7, 2.2e-7 with eight; 4,096 x 64,026 x 416 159 us, 148; x 2,560 776, 743), and two where
+// reading the head is the work (24 x 308 x 576 9.1e-8, 1.4e-7 with four, the same time).
+int logit_chunk(int P, int steps) { return P == 1 ? 2 : steps <= 16 ? 4 : 8; }
 
 // A thread's 128 logits of one row.
 template <class L>
-__device__ __forceinline__ bool sum_logits(Acc<L>& acc, int steps, uint32_t offset, float (&z)[kHalf]) {
+__device__ __forceinline__ bool sum_logits(Acc<L>& acc, int steps, int chunk, uint32_t offset, float (&z)[kHalf]) {
 #pragma unroll
     for (int i = 0; i < kHalf; ++i) z[i] = 0.0f;
 #pragma unroll 1
-    for (int k = 0; k < steps; k += logit_chunk(L::kP)) {
+    for (int k = 0; k < steps; k += chunk) {
         const uint32_t at = acc.next();
         if (at == ~0u) return false;
 #pragma unroll
@@ -107,7 +109,7 @@ __device__ __forceinline__ bool sum_logits(Acc<L>& acc, int steps, uint32_t offs
 template <class T, int P>
 struct Stats {
     using Layout = gemm::Layout<P, 1, kTN, 2, false, false>;
-    static constexpr int kFormat = std::is_same<T, __half>::value ? 0 : 1, kChunk = logit_chunk(P);
+    static constexpr int kFormat = std::is_same<T, __half>::value ? 0 : 1, kChunk = gemm::kPerLaunch;
     static constexpr bool kAKeep = true, kBKeep = true;
     struct Args {
         gemm::Shape shape;
@@ -124,7 +126,7 @@ struct Stats {
         const int j = (row < a.tok.T ? a.tok.row(row) : -1) - n0;
         if (row == 0 && n0 == 0) *a.wmax = 0u;
         float z[kHalf];
-        if (!sum_logits(acc, t.steps, (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf, z)) return false;
+        if (!sum_logits(acc, t.steps, a.shape.chunk, (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf, z)) return false;
         if (valid < kHalf) {
 #pragma unroll
             for (int i = 0; i < kHalf; ++i) z[i] = i < valid ? z[i] : kNegInf;
@@ -280,7 +282,7 @@ struct Weights {   // g of a piece
     using Layout = gemm::Layout<P, 1, kTN, 2, false, false>;
     static constexpr bool kF16 = std::is_same<T, __half>::value;
     static constexpr int kFormat = kF16 ? 0 : 1;
-    static constexpr int kChunk = logit_chunk(P);
+    static constexpr int kChunk = gemm::kPerLaunch;
     static constexpr bool kAKeep = true, kBKeep = true;
     struct Args {
         gemm::Shape shape;
@@ -307,7 +309,7 @@ struct Weights {   // g of a piece
         const bool live = w != 0.0f;
         w = ldexpf(w, scale_exponent<kF16>(*a.wmax));
         float z[kHalf];
-        if (!sum_logits(acc, t.steps, (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf, z)) return false;
+        if (!sum_logits(acc, t.steps, a.shape.chunk, (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf, z)) return false;
         const int j = y - (a.first + c0);
         T* out = a.g + static_cast<size_t>(row) * a.ldg + c0;
         T* low = a.low != nullptr ? a.low + static_cast<size_t>(row) * a.ldg + c0 : nullptr;
@@ -707,6 +709,7 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
     if (loss) {
         typename Stats<T, P>::Args& a = logits.first.args;
         a.shape = gemm::whole_tiles(tiles_m, ceil_div(c.N, kTN), steps, c.error);
+        a.shape.chunk = logit_chunk(P, steps);
         a.shape.rounds = c.probe_rounds;
         a.shape.idle = c.probe_role;
         a.tok = tok;
@@ -745,6 +748,7 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
         const int count = c.N - first < piece ? c.N - first : piece;
         typename Weights<T, P>::Args& a = pieces.first.args;
         a.shape = gemm::whole_tiles(tiles_m, ceil_div(count, kTN), steps, c.error);
+        a.shape.chunk = logit_chunk(P, steps);
         a.shape.b_mn = first;
         a.tok = tok;
         a.lse = lse;

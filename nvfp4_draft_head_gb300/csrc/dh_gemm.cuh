@@ -49,11 +49,12 @@ struct Shape {
     unsigned int* error;            // DH_DEVERR_* word or null
     uint32_t rounds;                // self-test: tries of a bounded wait, times kWaitSlices (0: a product's own)
     int idle;                       // self-test: the role that does nothing (-1: none)
+    int chunk;                      // steps of K that share an accumulator, where the operator leaves it to the launch
     __host__ __device__ int tiles() const { return tiles_m * tiles_n; }
     __host__ __device__ int units() const { return whole + (tiles() - whole) * splits; }
 };
 
-constexpr int kWholeTile = 1 << 30;
+constexpr int kWholeTile = 1 << 30, kPerLaunch = 0;   // of an operator's kChunk
 
 enum Role { kRoleProducer, kRoleIssuer, kRoleEpilogue };
 
@@ -206,7 +207,7 @@ struct Acc {
 
 // Op: Layout, Args (with `Shape shape`), kFormat (idesc_f), kChunk (steps of K that share an
 // accumulator: results that are scaled step by step take 1, those of a tile summed throughout by
-// the tensor cores kWholeTile), kAKeep / kBKeep (the operand is read by other tiles too: kept in
+// the tensor cores kWholeTile; kPerLaunch: Shape's chunk, a power of two), kAKeep / kBKeep (the operand is read by other tiles too: kept in
 // L2), and tile(args, tile, warp, lane, rank, acc), false when a wait gave up.
 
 // One product of a launch: its operands' maps and its arguments.
@@ -275,6 +276,9 @@ __device__ __forceinline__ bool issue(const Job<Op>& job, const Shape& s, int un
     const uint64_t first_a = L::kAMn ? tc::desc_operand_mn(base, L::kK) : tc::desc_operand(base);
     const uint64_t first_b = L::kBMn ? tc::desc_operand_mn(base + L::kABytes, L::kK) : tc::desc_operand(base + L::kABytes);
     const int steps = tile_at(job.args.shape, unit).steps;
+    const auto first_of = [&](int k) {   // whether step k starts an accumulator
+        return Op::kChunk == kPerLaunch ? (k & (job.args.shape.chunk - 1)) == 0 : k % (Op::kChunk | (Op::kChunk == 0)) == 0;
+    };
     for (int k = 0; k < steps; ++k) {
         if (L::kIssuers > 1 && r.it % L::kIssuers != static_cast<uint32_t>(issuer)) {
             ++r.n;
@@ -283,15 +287,15 @@ __device__ __forceinline__ bool issue(const Job<Op>& job, const Shape& s, int un
         }
         const uint32_t use = r.n / L::kBuffers, b = r.n % L::kBuffers, d = tmem + b * L::kTN;
         bool ok = wait_or_abort(sy, &sy.full[r.st], r.phase, s);   // the operands have landed,
-        if (k % Op::kChunk == 0 && use > 0)                        // and the accumulator has been read
+        if (first_of(k) && use > 0)                                // and the accumulator has been read
             ok = ok && wait_or_abort(sy, &sy.acc_empty[b], (use - 1) & 1, s);
         if (!__all_sync(~0u, ok)) return false;
         tc::fence_after_sync();
         const uint64_t da = first_a + r.st * (L::kBytes / 16), db = first_b + r.st * (L::kBytes / 16);
-        const bool last = (k + 1) % Op::kChunk == 0 || k == steps - 1;
+        const bool begin = first_of(k), last = first_of(k + 1) || k == steps - 1;
         if (elect_one()) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) tc::mma_f<P, kF8>(d, da + kStepA * j, db + kStepB * j, kIdesc, k % Op::kChunk != 0 || j > 0);
+            for (int j = 0; j < 4; ++j) tc::mma_f<P, kF8>(d, da + kStepA * j, db + kStepB * j, kIdesc, !begin || j > 0);
             if (last) tc::commit_all<P>(&sy.acc_full[b]);
             if constexpr (L::kShare > 1) tc::commit_both(&sy.empty[r.st]);
             else tc::commit_all<P>(&sy.empty[r.st]);
@@ -306,7 +310,8 @@ __device__ __forceinline__ bool issue(const Job<Op>& job, const Shape& s, int un
 // Accumulators of a tile.
 template <class Op>
 __device__ __forceinline__ int chunks_of(const Job<Op>& job, int unit) {
-    return (tile_at(job.args.shape, unit).steps - 1) / Op::kChunk + 1;
+    const Shape& s = job.args.shape;
+    return (tile_at(s, unit).steps - 1) / (Op::kChunk == kPerLaunch ? s.chunk : Op::kChunk) + 1;
 }
 
 // One product, or two of the same layout sizes that do not depend on one another: the second's
