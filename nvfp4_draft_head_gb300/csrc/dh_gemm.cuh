@@ -14,8 +14,16 @@
 // of a layer then read the matrices as they lie, without transposed copies.
 //
 // Warps: eight or sixteen epilogue warps (four groups of 32 lanes, parts of the columns), a
-// producer thread, an issuer thread (rank 0's alone works). Every wait is bounded; who gives
+// producer's, one or two issuers' (a pair: rank 0's alone work). Every wait is bounded; who gives
 // up sets the CTA's abort flag and the caller's error word, and the others follow.
+//
+// What it reaches: 16-bit operands in pairs keep the tensor pipe busy for 95 to 97 of 100 cycles
+// (1,024 x 64,064 x 2,560); FP8 in single CTAs, 256 wide, with a sum of its own for every 128
+// features, 56 without sharing (2,048 x 64,064 x 2,560 270 us): a step lands 48 KB in an SM's shared
+// memory while its instructions take 512 cycles, and hands over an accumulator of half the tensor
+// memory. What changes that balance was measured there
+// (8,192 x 64,064): pairs 1,380 us, whose hand-over crosses CTAs; halves of the columns with
+// accumulators of their own 1,176, which read A twice; single CTAs 1,150, sharing B 1,104.
 #pragma once
 
 #include <atomic>
