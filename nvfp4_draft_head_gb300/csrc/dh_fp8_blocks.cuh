@@ -63,6 +63,16 @@ __device__ __forceinline__ void load16_any(const T* p, const Rows<T>& rows, floa
     }
 }
 
+// v / s, rounded to nearest, from inv = 1 / s so rounded: by Markstein's theorem one correction of
+// v inv by its exact remainder. (Compared with the IEEE division for every significand of s at
+// E4M3's ties and three neighbours on each side: no difference. Where the remainder underflows, v
+// is below 2^-100, and its code 0 either way.) Three operations an element in place of a
+// division's dozen: the quantiser of 8,192 x 2,560 took 26 us.
+__device__ __forceinline__ float quotient(float v, float s, float inv) {
+    const float q = v * inv;
+    return fmaf(fmaf(-q, s, v), inv, q);
+}
+
 // 16 elements of row m from k, of a block held by eight lanes (n of them there): their codes, and
 // the block's scale, the same in all eight lanes.
 template <class T, bool VEC>
@@ -81,13 +91,13 @@ __device__ __forceinline__ float encode16(const Rows<T>& rows, int m, int k, int
     for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    const float s = block_scale(top);
+    const float s = block_scale(top), inv = __frcp_rn(s);
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float q[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) q[j] = fminf(fmaxf(__fdiv_rn(v[4 * i + j], s), -448.0f), 448.0f);
+        for (int j = 0; j < 4; ++j) q[j] = quotient(v[4 * i + j], s, inv);   // (the conversion clamps)
         const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3);
         const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q[2], q[3]), __NV_SATFINITE, __NV_E4M3);
         w[i] = lo | (hi << 16);

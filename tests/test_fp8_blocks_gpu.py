@@ -160,6 +160,30 @@ def test_rows_that_are_not_finite_and_zeros(M):
     assert dx[1].isnan().all() and dx[0].abs().max() <= 1e-12 and torch.equal(dx[2:], want[2:])
 
 
+@pytest.mark.parametrize("M", [4, 40, 300])
+@pytest.mark.parametrize("tx", [F, HF, BF])
+def test_codes_at_ties(M, tx):
+    """The activations' codes themselves, through a weight of ones on the diagonal: each result
+    is a code times its scale, one product in 32 bits. Values at the ties between codes and next
+    to them, over all of E4M3's binades."""
+    K = 256
+    eye = torch.zeros((K, K), dtype=torch.uint8, device=DEV)
+    eye.fill_diagonal_(0x38)                          # 1.0
+    mm = dh.FP8BlockMatmul(eye, torch.ones((2, 2), device=DEV))
+    g = torch.Generator(DEV).manual_seed(M)
+    amax = (torch.rand((M, 2, 1), generator=g, device=DEV) + 1.0) * 10.0 ** torch.randint(-3, 3, (M, 2, 1), generator=g, device=DEV)
+    s = amax.to(tx).float() / torch.full_like(amax, 448.0)
+    ties = torch.randint(1, 32, (M, 2, 128), generator=g, device=DEV) * 2.0 ** torch.randint(-10, 4, (M, 2, 128), generator=g, device=DEV)
+    x = s * ties.float()
+    x = (x.view(torch.int32) + torch.randint(-2, 3, x.shape, generator=g, device=DEV, dtype=torch.int32)).view(F)
+    x *= torch.where(torch.rand(x.shape, generator=g, device=DEV) < 0.5, -1.0, 1.0)
+    x[:, :, 5:6] = amax
+    x = x.reshape(M, K).to(tx)
+    codes, scales, _ = quantise(x, 1)
+    y = mm(x, out_dtype=F)
+    assert torch.equal(y, codes.float() * scales.repeat_interleave(128, 1)), (y / scales.repeat_interleave(128, 1) != codes.float()).nonzero()[:4].tolist()
+
+
 def test_a_row_of_the_weight():
     """The gradient of one output feature is its row of the weight (1 is a code times a scale, to
     fp32's rounding), the output of one input feature its column."""
