@@ -9,10 +9,10 @@
 // they are few the activations are quantised in the kernel too, by each CTA for its own steps,
 // while its first boxes of the weight are on their way: one launch in all.
 //
-// What bounds it: reading the weight where that is long (100 x 64,026 x 2,560 to f32: 44 us, 4.3 TB/s
-// with its quantiser's 4; the head at 1 token 35, 4.7 TB/s), else the chain of a launch, a ring
-// of boxes, the exchange and the stores (1 x 4,608 x 2,560 8.5 us, 16 x 2,560 x 5,120 11.0). In the
-// wide form (tokens along the rows) these took 26.7 and 46.
+// What bounds it: reading the weight where that is long (the head of 64,026 x 2,560 at 1 token 30 us,
+// 5.4 TB/s, at 32 tokens 33: 501 tiles make four rounds over 152 SMs, the last of them of 45), else
+// the chain of a launch, a ring of boxes, the exchange and the stores (1 x 4,608 x 2,560 6.1 us,
+// 16 x 2,560 x 5,120 9.1; tokens along the rows, in one part, 26.7 and 46).
 #pragma once
 
 #include "dh_fp8_blocks.cuh"
