@@ -191,8 +191,8 @@ struct Product {
         TY* y;
         long long ldy;
         int align;            // RowAlign of y
-        float* parts;         // the contraction in parts: their sums, [split][M][ldp]
-        long long ldp;
+        float* parts;         // sums of the tiles in parts, [split][M][ldp], or, behind whole tiles (ldp 0),
+        int ldp;              // [split][tile][kCtas 128][TN]
     };
     __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int rank, Acc<Layout>& acc) {
         constexpr int kPart = Layout::kPart;
@@ -229,17 +229,22 @@ struct Product {
             }
             acc.release();
         }
-        if (n0 < a.N && a.parts != nullptr)
-            store64<float>(a.parts + (static_cast<size_t>(t.split) * a.M + row0) * a.ldp + n0, a.ldp, sum, a.M - row0, a.N - n0, kPieces, lane);
-        else if (n0 < a.N) store64<TY>(a.y + static_cast<size_t>(row0) * a.ldy + n0, a.ldy, sum, a.M - row0, a.N - n0, a.align, lane);
+        if (t.split >= 0) {
+            size_t to = (static_cast<size_t>(t.split) * a.M + row0) * a.ldp + n0;
+            if (a.ldp == 0) {
+                const int rest = a.shape.tiles() - a.shape.whole, at = gemm::tile_index(a.shape.tiles_m, a.shape.tiles_n, t.m, t.n) - a.shape.whole;
+                to = (((static_cast<size_t>(t.split) * rest + at) * Layout::kCtas + rank) * gemm::kRows + (warp & 3) * 32) * TN + (warp >> 2) * kPart;
+            }
+            if (n0 < a.N) store64<float>(a.parts + to, a.ldp == 0 ? TN : a.ldp, sum, a.M - row0, a.N - n0, kPieces, lane);
+        } else if (n0 < a.N) store64<TY>(a.y + static_cast<size_t>(row0) * a.ldy + n0, a.ldy, sum, a.M - row0, a.N - n0, a.align, lane);
         __syncwarp();
         return true;
     }
 };
 
-// y from the sums of the parts, in order.
+// y from the sums of its parts, in order, where all tiles are in parts.
 template <class TY>
-__global__ void __launch_bounds__(256) sum_kernel(const float* __restrict__ parts, int splits, int M, int N, long long ldp, TY* __restrict__ y,
+__global__ void __launch_bounds__(256) sum_kernel(const float* __restrict__ parts, int splits, int M, int N, int ldp, TY* __restrict__ y,
                                                   long long ldy) {
     programmatic_wait();
     const unsigned n = blockIdx.x * 256 + threadIdx.x, m = blockIdx.y;
@@ -251,48 +256,85 @@ __global__ void __launch_bounds__(256) sum_kernel(const float* __restrict__ part
     y[static_cast<size_t>(m) * ldy + n] = rows::Elem<TY>::store(v);
 }
 
+// The same for the tiles behind whole ones: 512 elements of a tile per CTA. (In the layout of whole
+// planes those would take [split][M][N]; where all tiles are in parts, that one is the shorter:
+// 300 x 1,024 x 2,560 8.2 us, 10.0 tile by tile.)
+constexpr int kSumElements = 512;
+template <class TY, int TN, int ROWS>
+__global__ void __launch_bounds__(256) rest_kernel(const float* __restrict__ parts, gemm::Shape shape, int M, int N, TY* __restrict__ y,
+                                                   long long ldy) {
+    programmatic_wait();
+    constexpr unsigned per = ROWS * TN / kSumElements;
+    const unsigned at = blockIdx.x / per, first = (blockIdx.x - at * per) * kSumElements + threadIdx.x;
+    const int index = shape.whole + static_cast<int>(at);
+    const size_t step = static_cast<size_t>(shape.tiles() - shape.whole) * (ROWS * TN);
+    shape.whole = shape.tiles();
+    const Tile t = gemm::tile_at(shape, index);
+    const float* p = parts + static_cast<size_t>(at) * (ROWS * TN) + first;
+    constexpr int kEach = kSumElements / 256;
+    float v[kEach] = {};
+    bool in[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) in[i] = t.m * ROWS + static_cast<int>((first + i * 256) / TN) < M;
+#pragma unroll 4
+    for (int s = 0; s < shape.splits; ++s) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) v[i] += in[i] ? p[s * step + i * 256] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int m = t.m * ROWS + static_cast<int>((first + i * 256) / TN), n = t.n * TN + static_cast<int>((first + i * 256) % TN);
+        if (in[i] && n < N) y[static_cast<size_t>(m) * ldy + n] = rows::Elem<TY>::store(v[i]);
+    }
+}
+
 // ------------------------------------------------------------------- host ----
 
+int part_stride(int out) { return (out + 7) / 8 * 8; }
+
 // How a product of many tokens runs: the width of its tiles, the CTAs that share a tile's columns
-// of the weight, and the parts of its contraction where the tiles alone would leave SMs idle.
+// of the weight, the tiles that are multiplied whole, and the parts of the contraction of the others,
+// which fill a round over the SMs.
 struct Plan {
-    int tn, share, parts, part_steps;
+    int tn, share, whole, parts, part_steps;
     float us;
+    int tiles(int M, int out) const { return ceil_div(M, gemm::kRows * share) * ceil_div(out, tn); }
+    size_t part_bytes(int M, int out) const {
+        if (parts == 1) return 0;
+        if (whole == 0) return static_cast<size_t>(parts) * M * part_stride(out) * sizeof(float);
+        return static_cast<size_t>(parts) * (tiles(M, out) - whole) * (share * gemm::kRows * tn) * sizeof(float);
+    }
 };
 
-// By rounds of tiles over the 152 SMs times a step's time (0.43 us in a 256-wide tile, 0.38 in a
-// 128-wide one: wide tiles have twice the work between two hand-overs, narrow ones spread a small
-// product over more SMs), or by reading the weight. Parts cost a second kernel. Measured, us: 200
-// tokens, gradient of 64,026 x 2,560 193 in one part; 512 x 4,608 x 2,560 15.0 wide, 13.3 narrow.
-// Wide tiles run two by two, row blocks that share their columns of the weight, where that adds no
-// round (an odd last row block leaves one of its two idle): 8,192 x 64,064 x 2,560 1,150 single,
-// 1,104 shared; 4,096 x 4,608 x 2,560 56.6 and 55.2.
+// By rounds of tiles over the 152 SMs times a step's time, or by reading the weight. A step takes
+// 0.43 us in a 256-wide tile, 0.42 where two row blocks share their columns of the weight (8,192 x
+// 64,064 x 2,560 1,150 and 1,104; 300 x 64,026 are three row blocks, which two by two take seven
+// rounds for five), 0.38 in a 128-wide one: wide tiles have twice the work between two hand-overs,
+// narrow ones spread a small product over more SMs (512 x 4,608 x 2,560 15.0 wide, 13.3 narrow). Parts
+// cost a second kernel: 200 tokens, gradient of 64,026 x 2,560 193 in one part, 55 in sixteen.
 Plan plan_of(int M, int out, int width) {
     constexpr int kSms = 152;
     const int steps = ceil_div(width, kBlock);
-    Plan best = {256, 1, 1, steps, 0.0f};
-    for (int tn = 256; tn >= 128; tn /= 2) {
-        const long long tiles = static_cast<long long>(ceil_div(M, gemm::kRows)) * ceil_div(out, tn);
-        for (int p = 1; p <= 16 && (p == 1 || (p * tiles <= kSms && steps / p >= 4)); ++p) {
+    Plan best = {};
+    constexpr struct { int tn, share; float step; } kForms[] = {{256, 1, 0.43f}, {256, 2, 0.42f}, {128, 1, 0.38f}};
+    for (const auto& f : kForms) {
+        const int slots = kSms / f.share;
+        const long long tiles = static_cast<long long>(ceil_div(M, gemm::kRows * f.share)) * ceil_div(out, f.tn), rest = tiles % slots;
+        const float tile = steps * f.step + 1.0f, full = static_cast<float>(tiles / slots) * tile;
+        const float whole = full + (rest > 0 ? tile : 0.0f);
+        if (best.tn == 0 || whole < best.us) best = {f.tn, f.share, static_cast<int>(tiles), 1, steps, whole};
+        const float most = static_cast<float>(M) * out, there = static_cast<float>(rest) * (f.share * gemm::kRows * f.tn);
+        for (int p = 2; rest > 0 && p <= 16 && steps / p >= 4; ++p) {
             const int part = ceil_div(steps, p);
-            const float us = static_cast<float>((tiles * p + kSms - 1) / kSms) * (part * (tn == 256 ? 0.43f : 0.38f) + 1.0f) +
-                             (p > 1 ? 2.0f + p * static_cast<float>(M) * out * 1.0e-6f : 0.0f);
-            if ((tn == 256 && p == 1) || us < best.us) best = {tn, 1, ceil_div(steps, part), part, us};
+            const float us = full + static_cast<float>((rest * p + slots - 1) / slots) * (part * f.step + 1.0f) + 2.0f +
+                             p * (there < most ? there : most) * 1.0e-6f;
+            if (us < best.us) best = {f.tn, f.share, static_cast<int>(tiles - rest), ceil_div(steps, part), part, us};
         }
-    }
-    if (best.tn == 256 && best.parts == 1) {
-        const long long rows = ceil_div(M, gemm::kRows), columns = ceil_div(out, 256);
-        if (((rows + 1) / 2 * columns + kSms / 2 - 1) / (kSms / 2) <= (rows * columns + kSms - 1) / kSms) best.share = 2;
     }
     const float read = static_cast<float>(width) * out * (1.0f / 4.4e6f);
     if (best.us < read) best.us = read;
     best.us += 2.5f;   // quantising before it
     return best;
-}
-long long part_stride(int out) { return (out + 7) / 8 * 8; }
-size_t parts_bytes(int M, int out, int width) {
-    const Plan p = plan_of(M, out, width);
-    return p.parts > 1 ? static_cast<size_t>(p.parts) * M * part_stride(out) * sizeof(float) : 0;
 }
 
 template <class T>
@@ -329,14 +371,19 @@ cudaError_t product(const Fp8BlockArgs& f, const Plan& plan, const uint8_t* code
     const uintptr_t at = reinterpret_cast<uintptr_t>(f.y) | (f.M == 1 ? 0 : static_cast<uintptr_t>(f.ldy) * sizeof(TY));
     a.align = at % 32 == 0 ? kPieces : at % 4 == 0 ? kWords : kAny;
     if (plan.parts == 1) return gemm::launch(jobs, s);
-    a.shape.whole = 0;
+    a.shape.whole = plan.whole;
     a.shape.splits = plan.parts;
     a.shape.split_steps = plan.part_steps;
     a.parts = parts;
-    a.ldp = part_stride(out);
+    a.ldp = plan.whole == 0 ? part_stride(out) : 0;
     if ((e = gemm::launch(jobs, s)) != cudaSuccess) return e;
-    const dim3 grid(static_cast<unsigned>(ceil_div(out, 256)), static_cast<unsigned>(f.M));   // (parts: M is below 152 x 128)
-    return gemm::launch_early(sum_kernel<TY>, grid, 256, 0, 1, s, parts, plan.parts, f.M, out, a.ldp, a.y, a.ldy);
+    if (plan.whole == 0) {
+        const dim3 grid(static_cast<unsigned>(ceil_div(out, 256)), static_cast<unsigned>(f.M));   // (M: rows of less than 152 tiles)
+        return gemm::launch_early(sum_kernel<TY>, grid, 256, 0, 1, s, parts, plan.parts, f.M, out, a.ldp, a.y, a.ldy);
+    }
+    constexpr int kTileRows = L::kCtas * gemm::kRows;
+    const dim3 grid(static_cast<unsigned>(a.shape.tiles() - plan.whole) * (kTileRows * TN / kSumElements));   // (less than 152 tiles)
+    return gemm::launch_early(rest_kernel<TY, TN, kTileRows>, grid, 256, 0, 1, s, parts, a.shape, f.M, out, a.y, a.ldy);
 }
 
 template <class TY>
@@ -389,7 +436,7 @@ size_t fp8_block_workspace_bytes(int M, int width, int out) {
     f8::Plan many;
     if (f8::take_few(M, out, width, &few, &many) && few.fused) return DH_WORKSPACE_ALIGN;   // not used
     return f8::up256(static_cast<size_t>(M) * (f8::ceil_div(width, 16) * 16)) +
-           f8::up256(static_cast<size_t>(M) * f8::ceil_div(width, f8::kBlock) * sizeof(float)) + f8::up256(f8::parts_bytes(M, out, width));
+           f8::up256(static_cast<size_t>(M) * f8::ceil_div(width, f8::kBlock) * sizeof(float)) + f8::up256(many.part_bytes(M, out));
 }
 
 cudaError_t launch_fp8_quantize_blocks(const uint16_t* W, int V, int K, const int32_t* idx, int N, uint8_t* q, float* scale, Workspace* ws,

@@ -219,8 +219,8 @@ def test_long_contractions(M, N, K, grad):
 
 
 # wide tiles: one by one (three row blocks, which two by two would take a second round), two by two,
-# and with an odd last row block
-@pytest.mark.parametrize("M,out,width", [(300, 12640, 272), (2000, 4608, 528), (1100, 4592, 272)])
+# and with an odd last row block; a round of whole tiles and the rest in parts of the contraction
+@pytest.mark.parametrize("M,out,width", [(300, 12640, 272), (2000, 4608, 528), (1100, 4592, 272), (1000, 5104, 4000)])
 @pytest.mark.parametrize("grad", [False, True])
 def test_wide_tiles(M, out, width, grad):
     mm, wv = layer(*((width, out) if grad else (out, width)))
