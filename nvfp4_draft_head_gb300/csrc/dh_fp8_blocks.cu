@@ -10,8 +10,8 @@
 // epilogue multiplies by the two scales and adds to 32-bit sums in registers.
 //
 // The product of many tokens is bound by that hand-over (dh_gemm.cuh): 8,192 x 64,026 x 2,560 takes
-// 1,117 us (2,400 TFLOP/s; 710 us at twice the measured bf16 rate), its quantiser about 20 of them; the
-// gradient of 4,096 x 4,608 x 2,560 58. Few tokens: dh_fp8_few.cuh.
+// 1,110 us (2,420 TFLOP/s; 710 us at twice the measured bf16 rate), its quantiser about 20 of them; the
+// gradient of 4,096 x 4,608 x 2,560 54.5. Few tokens: dh_fp8_few.cuh.
 #include "dh_fp8_blocks.cuh"
 
 namespace dh {
