@@ -310,23 +310,24 @@ struct Plan {
 // 0.43 us in a 256-wide tile, 0.42 where two row blocks share their columns of the weight (8,192 x
 // 64,064 x 2,560 1,150 and 1,104; 300 x 64,026 are three row blocks, which two by two take seven
 // rounds for five), 0.38 in a 128-wide one: wide tiles have twice the work between two hand-overs,
-// narrow ones spread a small product over more SMs (512 x 4,608 x 2,560 15.0 wide, 13.3 narrow). Parts
+// narrow ones spread a small product over more SMs (512 x 4,608 x 2,560 15.0 wide, 13.3 narrow). With one
+// row block, which alone reads its columns of the weight, 0.67 and 0.40 (1 x 20,000 x 2,560 17). Parts
 // cost a second kernel: 200 tokens, gradient of 64,026 x 2,560 193 in one part, 55 in sixteen.
 Plan plan_of(int M, int out, int width) {
     constexpr int kSms = 152;
     const int steps = ceil_div(width, kBlock);
     Plan best = {};
-    constexpr struct { int tn, share; float step; } kForms[] = {{256, 1, 0.43f}, {256, 2, 0.42f}, {128, 1, 0.38f}};
+    constexpr struct { int tn, share; float step, alone; } kForms[] = {{256, 1, 0.43f, 0.67f}, {256, 2, 0.42f, 0.67f}, {128, 1, 0.38f, 0.40f}};
     for (const auto& f : kForms) {
         const int slots = kSms / f.share;
         const long long tiles = static_cast<long long>(ceil_div(M, gemm::kRows * f.share)) * ceil_div(out, f.tn), rest = tiles % slots;
-        const float tile = steps * f.step + 1.0f, full = static_cast<float>(tiles / slots) * tile;
+        const float step = M <= gemm::kRows ? f.alone : f.step, tile = steps * step + 1.0f, full = static_cast<float>(tiles / slots) * tile;
         const float whole = full + (rest > 0 ? tile : 0.0f);
         if (best.tn == 0 || whole < best.us) best = {f.tn, f.share, static_cast<int>(tiles), 1, steps, whole};
         const float most = static_cast<float>(M) * out, there = static_cast<float>(rest) * (f.share * gemm::kRows * f.tn);
         for (int p = 2; rest > 0 && p <= 16 && steps / p >= 4; ++p) {
             const int part = ceil_div(steps, p);
-            const float us = full + static_cast<float>((rest * p + slots - 1) / slots) * (part * f.step + 1.0f) + 2.0f +
+            const float us = full + static_cast<float>((rest * p + slots - 1) / slots) * (part * step + 1.0f) + 2.0f +
                              p * (there < most ? there : most) * 1.0e-6f;
             if (us < best.us) best = {f.tn, f.share, static_cast<int>(tiles - rest), ceil_div(steps, part), part, us};
         }
@@ -400,14 +401,14 @@ cudaError_t run_many(const Fp8BlockArgs& f, const Plan& p, const uint8_t* codes,
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Whether a product takes the form of few tokens: up to 16 always (one launch of a product that
-// quantises itself, for three: 16 x 2,560 x 5,120 9.0 us and 8.6, but 12 and 15 as calls), more where it is
-// estimated shorter. Measured, us (few / many): 32 x 64,026 x 2,560 33 / 42, 64 37 / 37, 100 49 / 38; 32 x
-// 4,608 x 2,560 9.1 / 8.5, 64 10.1 / 8.7.
+// Whether a product takes the form of few tokens: where it is estimated shorter, and up to 16 also where
+// it is up to 4 us longer (one or two launches for two or three: 16 x 2,560 x 5,120 9.0 us and 8.6, but 11
+// and 15 as calls). Measured, us (few / many): 32 x 64,026 x 2,560 33 / 42, 64 37 / 37; 32 x 4,608 x 2,560
+// 9.1 / 8.5, 64 10.1 / 8.7.
 bool take_few(int M, int out, int width, FewPlan* few, Plan* many) {
     *few = few_plan(M, out, width);
     *many = plan_of(M, out, width);
-    return few->splits > 0 && (M <= 16 || few->us <= many->us);
+    return few->splits > 0 && few->us <= many->us + (M <= 16 ? 4.0f : 0.0f);
 }
 
 template <class TY>

@@ -114,7 +114,7 @@ inline bool rows_aligned16(const void* x, long long ld_bytes, int rows) {
 // Products of up to kFewTokens tokens (dh_fp8_few.cuh): tokens that a tile has columns for, the CTAs
 // of a cluster that share the contraction (0: not in this form), whether the activations are
 // quantised in the kernel, and about how long it takes.
-constexpr int kFewTokens = 128;
+constexpr int kFewTokens = 64;
 struct FewPlan {
     int columns, splits;
     bool fused;

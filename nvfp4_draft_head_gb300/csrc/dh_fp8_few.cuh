@@ -1,6 +1,6 @@
-// The FP8 block-scaled product (dh_fp8_blocks.cu) for up to 128 tokens, where reading the weight
+// The FP8 block-scaled product (dh_fp8_blocks.cu) for up to 64 tokens, where reading the weight
 // is the work: rows of the weight lie along the rows of a tile (128 of them), the tokens along
-// its 16 to 128 columns, so that the matrix instructions waste nothing on tokens that are not
+// its 16 to 64 columns, so that the matrix instructions waste nothing on tokens that are not
 // there, and a step of 128 features is one 16 KB box of the weight.
 //
 // To have every SM read, the contraction is split over the CTAs of a cluster (1 to 8): each sums
@@ -376,9 +376,8 @@ cudaError_t launch_few(const Fp8BlockArgs& f, const FewPlan& p, const uint8_t* c
                : f.x_type == DH_T_F16 ? launch_fused<__half, TY>(f, p, s)
                                       : launch_fused<float, TY>(f, p, s);
     // (the element type of x matters to the fused form alone)
-    return p.columns == 32   ? launch_sized<float, TY, 32, false>(f, p.splits, codes, ldc, scales, s)
-           : p.columns == 64 ? launch_sized<float, TY, 64, false>(f, p.splits, codes, ldc, scales, s)
-                             : launch_sized<float, TY, 128, false>(f, p.splits, codes, ldc, scales, s);
+    return p.columns == 32 ? launch_sized<float, TY, 32, false>(f, p.splits, codes, ldc, scales, s)
+                           : launch_sized<float, TY, 64, false>(f, p.splits, codes, ldc, scales, s);
 }
 
 }  // namespace f8

@@ -196,7 +196,7 @@ def test_a_row_of_the_weight():
     assert ((y.double() - wv[:, [0, 128, 399]].t()).abs() <= 2.0 ** -21 * wv[:, [0, 128, 399]].t().abs()).all()
 
 
-@pytest.mark.parametrize("M,N,K", [(5, 19500, 8192), (16, 6000, 8192), (1, 70000, 256)])
+@pytest.mark.parametrize("M,N,K", [(5, 19500, 8192), (16, 6000, 8192), (1, 70000, 256), (16, 19500, 2560), (33, 16000, 2560), (24, 1504, 1536)])
 def test_few_tokens_on_many_tiles(M, N, K):
     """Clusters that exchange their sums for tile after tile."""
     mm, wv = layer(N, K)

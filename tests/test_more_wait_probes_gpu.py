@@ -22,7 +22,7 @@ def rand(shape, seed, scale=1.0):
 # (M, N, K): few tokens with steps in the ring and more, in a cluster (48 rows leave SMs idle) and
 # alone; many, in narrow tiles (parts of six steps for four accumulators), in wide ones two by two
 # and in wide ones alone
-SIZES = {"one step": (3, 70, 128), "a cluster": (5, 48, 8192), "alone": (5, 20000, 2048), "quantised before": (20, 4608, 2560),
+SIZES = {"one step": (3, 70, 128), "a cluster": (5, 48, 8192), "alone": (5, 20000, 2048), "quantised before": (16, 19500, 2560),
          "narrow tiles": (300, 1000, 4096), "wide tiles": (2000, 4608, 1040), "wide tiles alone": (300, 12700, 1040)}
 
 
