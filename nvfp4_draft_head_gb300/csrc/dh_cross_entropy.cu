@@ -632,8 +632,12 @@ gemm::Shape hidden_tiles(int T, int K, int piece, unsigned int* error) {
 }
 
 // g in two terms, its 16-bit rounding and what that left over, as rows T .. 2 T - 1 of g, of dh's
-// sums and (the same hidden states again) of dW's contraction: for few tokens, whose roundings
-// do not average out, and for which the products' tiles have the room.
+// sums and (the same hidden states again) of dW's contraction: for few tokens, for which the
+// products' tiles have the room. One term makes the gradients' error 1.43 times that of rounding them
+// alone (64,026 x 2,560 bf16, relative 2-norm: 0.00238 and 0.00166); a second one takes it away at any
+// size and costs, in us (one term / two): 129 tokens 276 / 336, 256 293 / 379, 520 513 / 705, 4,096
+// 2,776 / 4,482; 100 tokens 230 in two. That error is within the gradients' own type, and a framework
+// that keeps its logits in 16 bits has it as well, so it is not paid for above 128 tokens.
 int terms_of(int T) { return T <= 128 ? 2 : 1; }
 
 // dW's tiles where they are few and the tokens many: all in parts of at least eight steps, as many
