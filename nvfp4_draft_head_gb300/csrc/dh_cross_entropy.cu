@@ -115,7 +115,7 @@ __device__ __forceinline__ bool sum_logits(Acc<L>& acc, int steps, int chunk, ui
 
 template <class T, int P>
 struct Stats {
-    using Layout = gemm::Layout<P, 1, kTN, 2, false, false>;
+    using Layout = gemm::Layout<P, kTN, 2, false, false>;
     static constexpr int kFormat = std::is_same<T, __half>::value ? 0 : 1, kChunk = gemm::kPerLaunch;
     static constexpr bool kAKeep = true, kBKeep = true;
     struct Args {
@@ -286,7 +286,7 @@ __device__ __forceinline__ void store_weights(float (&p)[16], int j, float w, bo
 
 template <class T, int P>
 struct Weights {   // g of a piece
-    using Layout = gemm::Layout<P, 1, kTN, 2, false, false>;
+    using Layout = gemm::Layout<P, kTN, 2, false, false>;
     static constexpr bool kF16 = std::is_same<T, __half>::value;
     static constexpr int kFormat = kF16 ? 0 : 1;
     static constexpr int kChunk = gemm::kPerLaunch;
@@ -464,7 +464,7 @@ __device__ __forceinline__ bool store_sums(A& acc, float* out, bool in, int colu
 // and first parts, then the other parts of the tiles that are split, [split - 1][tile][256][256].
 template <class T>
 struct Hidden {
-    using Layout = gemm::Layout<kPair, 1, kTN, 2, false, true>;
+    using Layout = gemm::Layout<kPair, kTN, 2, false, true>;
     static constexpr int kFormat = std::is_same<T, __half>::value ? 0 : 1;
     static constexpr int kChunk = gemm::kWholeTile;
     static constexpr bool kAKeep = true, kBKeep = true;
@@ -504,7 +504,7 @@ struct Hidden {
 // pieces where they are so aligned: backward of 333 x 248,320 1,424 us with 16-byte ones, 1,154.)
 template <class T>
 struct Head {
-    using Layout = gemm::Layout<kPair, 1, kTN, 2, true, true>;
+    using Layout = gemm::Layout<kPair, kTN, 2, true, true>;
     static constexpr bool kF16 = std::is_same<T, __half>::value;
     static constexpr int kFormat = kF16 ? 0 : 1;
     static constexpr int kChunk = gemm::kWholeTile;

@@ -10,8 +10,8 @@
 // epilogue multiplies by the two scales and adds to 32-bit sums in registers.
 //
 // The product of many tokens is bound by that hand-over (dh_gemm.cuh): 8,192 x 64,026 x 2,560 takes
-// 1,110 us (2,420 TFLOP/s; 710 us at twice the measured bf16 rate), its quantiser about 20 of them; the
-// gradient of 4,096 x 4,608 x 2,560 54.5. Few tokens: dh_fp8_few.cuh.
+// 1,150 us (2,330 TFLOP/s; 710 us at twice the measured bf16 rate), its quantiser about 20 of them; the
+// gradient of 4,096 x 4,608 x 2,560 54.4. Few tokens: dh_fp8_few.cuh.
 #include "dh_fp8_blocks.cuh"
 
 namespace dh {
@@ -176,9 +176,9 @@ __device__ __forceinline__ void store64(TY* y, long long ldy, const float (&v)[6
 
 // Tokens along the rows of a tile, output features along its columns; W K-major for y, and
 // MN-major (its rows along the contraction) for dx.
-template <class TY, bool GRADIENT, int TN, int SHARE>
+template <class TY, bool GRADIENT, int TN>
 struct Product {
-    using Layout = gemm::Layout<1, SHARE, TN, 1, false, GRADIENT, TN / 16, 2>;
+    using Layout = gemm::Layout<1, TN, 1, false, GRADIENT, TN / 16, 2>;
     static constexpr int kFormat = 0;
     static constexpr int kChunk = 1;
     static constexpr bool kAKeep = true, kBKeep = true;
@@ -192,12 +192,12 @@ struct Product {
         long long ldy;
         int align;            // RowAlign of y
         float* parts;         // sums of the tiles in parts, [split][M][ldp], or, behind whole tiles (ldp 0),
-        int ldp;              // [split][tile][kCtas 128][TN]
+        int ldp;              // [split][tile][128][TN]
     };
-    __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int rank, Acc<Layout>& acc) {
+    __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int, Acc<Layout>& acc) {
         constexpr int kPart = Layout::kPart;
         static_assert(kPart == 64 && Layout::kP == 1, "a warp's columns lie in one block of the weight");
-        const int row0 = (t.m * Layout::kCtas + rank) * gemm::kRows + (warp & 3) * 32, row = row0 + lane, steps = t.steps;
+        const int row0 = t.m * gemm::kRows + (warp & 3) * 32, row = row0 + lane, steps = t.steps;
         const int n0 = t.n * Layout::kTN + (warp >> 2) * kPart;
         const bool in = row < a.M;
         // (columns beyond N: any scale)
@@ -233,7 +233,7 @@ struct Product {
             size_t to = (static_cast<size_t>(t.split) * a.M + row0) * a.ldp + n0;
             if (a.ldp == 0) {
                 const int rest = a.shape.tiles() - a.shape.whole, at = gemm::tile_index(a.shape.tiles_m, a.shape.tiles_n, t.m, t.n) - a.shape.whole;
-                to = (((static_cast<size_t>(t.split) * rest + at) * Layout::kCtas + rank) * gemm::kRows + (warp & 3) * 32) * TN + (warp >> 2) * kPart;
+                to = ((static_cast<size_t>(t.split) * rest + at) * gemm::kRows + (warp & 3) * 32) * TN + (warp >> 2) * kPart;
             }
             if (n0 < a.N) store64<float>(a.parts + to, a.ldp == 0 ? TN : a.ldp, sum, a.M - row0, a.N - n0, kPieces, lane);
         } else if (n0 < a.N) store64<TY>(a.y + static_cast<size_t>(row0) * a.ldy + n0, a.ldy, sum, a.M - row0, a.N - n0, a.align, lane);
@@ -260,22 +260,22 @@ __global__ void __launch_bounds__(256) sum_kernel(const float* __restrict__ part
 // planes those would take [split][M][N]; where all tiles are in parts, that one is the shorter:
 // 300 x 1,024 x 2,560 8.2 us, 10.0 tile by tile.)
 constexpr int kSumElements = 512;
-template <class TY, int TN, int ROWS>
+template <class TY, int TN>
 __global__ void __launch_bounds__(256) rest_kernel(const float* __restrict__ parts, gemm::Shape shape, int M, int N, TY* __restrict__ y,
                                                    long long ldy) {
     programmatic_wait();
-    constexpr unsigned per = ROWS * TN / kSumElements;
+    constexpr unsigned per = gemm::kRows * TN / kSumElements;
     const unsigned at = blockIdx.x / per, first = (blockIdx.x - at * per) * kSumElements + threadIdx.x;
     const int index = shape.whole + static_cast<int>(at);
-    const size_t step = static_cast<size_t>(shape.tiles() - shape.whole) * (ROWS * TN);
+    const size_t step = static_cast<size_t>(shape.tiles() - shape.whole) * (gemm::kRows * TN);
     shape.whole = shape.tiles();
     const Tile t = gemm::tile_at(shape, index);
-    const float* p = parts + static_cast<size_t>(at) * (ROWS * TN) + first;
+    const float* p = parts + static_cast<size_t>(at) * (gemm::kRows * TN) + first;
     constexpr int kEach = kSumElements / 256;
     float v[kEach] = {};
     bool in[kEach];
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) in[i] = t.m * ROWS + static_cast<int>((first + i * 256) / TN) < M;
+    for (int i = 0; i < kEach; ++i) in[i] = t.m * gemm::kRows + static_cast<int>((first + i * 256) / TN) < M;
 #pragma unroll 4
     for (int s = 0; s < shape.splits; ++s) {
 #pragma unroll
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(256) rest_kernel(const float* __restrict__ par
     }
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-        const int m = t.m * ROWS + static_cast<int>((first + i * 256) / TN), n = t.n * TN + static_cast<int>((first + i * 256) % TN);
+        const int m = t.m * gemm::kRows + static_cast<int>((first + i * 256) / TN), n = t.n * TN + static_cast<int>((first + i * 256) % TN);
         if (in[i] && n < N) y[static_cast<size_t>(m) * ldy + n] = rows::Elem<TY>::store(v[i]);
     }
 }
@@ -292,44 +292,41 @@ __global__ void __launch_bounds__(256) rest_kernel(const float* __restrict__ par
 
 int part_stride(int out) { return (out + 7) / 8 * 8; }
 
-// How a product of many tokens runs: the width of its tiles, the CTAs that share a tile's columns
-// of the weight, the tiles that are multiplied whole, and the parts of the contraction of the others,
-// which fill a round over the SMs.
+// How a product of many tokens runs: the width of its tiles, the tiles that are multiplied whole,
+// and the parts of the contraction of the others, which fill a round over the SMs.
 struct Plan {
-    int tn, share, whole, parts, part_steps;
+    int tn, whole, parts, part_steps;
     float us;
-    int tiles(int M, int out) const { return ceil_div(M, gemm::kRows * share) * ceil_div(out, tn); }
+    int tiles(int M, int out) const { return ceil_div(M, gemm::kRows) * ceil_div(out, tn); }
     size_t part_bytes(int M, int out) const {
         if (parts == 1) return 0;
         if (whole == 0) return static_cast<size_t>(parts) * M * part_stride(out) * sizeof(float);
-        return static_cast<size_t>(parts) * (tiles(M, out) - whole) * (share * gemm::kRows * tn) * sizeof(float);
+        return static_cast<size_t>(parts) * (tiles(M, out) - whole) * (gemm::kRows * tn) * sizeof(float);
     }
 };
 
 // By rounds of tiles over the 152 SMs times a step's time, or by reading the weight. A step takes
-// 0.43 us in a 256-wide tile, 0.42 where two row blocks share their columns of the weight (8,192 x
-// 64,064 x 2,560 1,150 and 1,104; 300 x 64,026 are three row blocks, which two by two take seven
-// rounds for five), 0.38 in a 128-wide one: wide tiles have twice the work between two hand-overs,
-// narrow ones spread a small product over more SMs (512 x 4,608 x 2,560 15.0 wide, 13.3 narrow). With one
-// row block, which alone reads its columns of the weight, 0.67 and 0.40 (1 x 20,000 x 2,560 17). Parts
-// cost a second kernel: 200 tokens, gradient of 64,026 x 2,560 193 in one part, 55 in sixteen.
+// 0.43 us in a 256-wide tile, 0.38 in a 128-wide one: wide tiles have twice the work between two
+// hand-overs, narrow ones spread a small product over more SMs (512 x 4,608 x 2,560 15.0 wide,
+// 13.3 narrow). With one row block, which alone reads its columns of the weight, 0.67 and 0.40 (1 x
+// 20,000 x 2,560 17). Parts cost a second kernel: 200 tokens, gradient of 64,026 x 2,560 193 in one
+// part, 55 in sixteen.
 Plan plan_of(int M, int out, int width) {
     constexpr int kSms = 152;
     const int steps = ceil_div(width, kBlock);
     Plan best = {};
-    constexpr struct { int tn, share; float step, alone; } kForms[] = {{256, 1, 0.43f, 0.67f}, {256, 2, 0.42f, 0.67f}, {128, 1, 0.38f, 0.40f}};
+    constexpr struct { int tn; float step, alone; } kForms[] = {{256, 0.43f, 0.67f}, {128, 0.38f, 0.40f}};
     for (const auto& f : kForms) {
-        const int slots = kSms / f.share;
-        const long long tiles = static_cast<long long>(ceil_div(M, gemm::kRows * f.share)) * ceil_div(out, f.tn), rest = tiles % slots;
-        const float step = M <= gemm::kRows ? f.alone : f.step, tile = steps * step + 1.0f, full = static_cast<float>(tiles / slots) * tile;
+        const long long tiles = static_cast<long long>(ceil_div(M, gemm::kRows)) * ceil_div(out, f.tn), rest = tiles % kSms;
+        const float step = M <= gemm::kRows ? f.alone : f.step, tile = steps * step + 1.0f, full = static_cast<float>(tiles / kSms) * tile;
         const float whole = full + (rest > 0 ? tile : 0.0f);
-        if (best.tn == 0 || whole < best.us) best = {f.tn, f.share, static_cast<int>(tiles), 1, steps, whole};
-        const float most = static_cast<float>(M) * out, there = static_cast<float>(rest) * (f.share * gemm::kRows * f.tn);
+        if (best.tn == 0 || whole < best.us) best = {f.tn, static_cast<int>(tiles), 1, steps, whole};
+        const float most = static_cast<float>(M) * out, there = static_cast<float>(rest) * (gemm::kRows * f.tn);
         for (int p = 2; rest > 0 && p <= 16 && steps / p >= 4; ++p) {
             const int part = ceil_div(steps, p);
-            const float us = full + static_cast<float>((rest * p + slots - 1) / slots) * (part * step + 1.0f) + 2.0f +
+            const float us = full + static_cast<float>((rest * p + kSms - 1) / kSms) * (part * step + 1.0f) + 2.0f +
                              p * (there < most ? there : most) * 1.0e-6f;
-            if (us < best.us) best = {f.tn, f.share, static_cast<int>(tiles - rest), ceil_div(steps, part), part, us};
+            if (us < best.us) best = {f.tn, static_cast<int>(tiles - rest), ceil_div(steps, part), part, us};
         }
     }
     const float read = static_cast<float>(width) * out * (1.0f / 4.4e6f);
@@ -347,18 +344,18 @@ cudaError_t quantize(const Fp8BlockArgs& f, int width, uint8_t* codes, int ldc, 
                               static_cast<const T*>(f.x), f.ldx, f.M, width, codes, ldc, scales);
 }
 
-template <class TY, bool GRADIENT, int TN, int SHARE>
+template <class TY, bool GRADIENT, int TN>
 cudaError_t product(const Fp8BlockArgs& f, const Plan& plan, const uint8_t* codes, int ldc, const float* scales, float* parts, cudaStream_t s) {
-    using P = Product<TY, GRADIENT, TN, SHARE>;
+    using P = Product<TY, GRADIENT, TN>;
     using L = typename P::Layout;
     const int width = GRADIENT ? f.N : f.K, out = GRADIENT ? f.K : f.N, kb = ceil_div(f.K, kBlock);
     gemm::Jobs<P> jobs = {};
     cudaError_t e = gemm::encode_operand<L, false>(&jobs.first.map_a, codes, f.M, width, ldc, gemm::kRows);
     if (e != cudaSuccess) return e;
-    if ((e = gemm::encode_operand<L, GRADIENT>(&jobs.first.map_b, f.q, out, width, f.K, L::kBLoad)) != cudaSuccess) return e;
+    if ((e = gemm::encode_operand<L, GRADIENT>(&jobs.first.map_b, f.q, out, width, f.K, L::kBRows)) != cudaSuccess) return e;
     typename P::Args& a = jobs.first.args;
     const int steps = ceil_div(width, kBlock);
-    a.shape = gemm::whole_tiles(ceil_div(f.M, gemm::kRows * L::kCtas), ceil_div(out, L::kTN), steps, f.error);
+    a.shape = gemm::whole_tiles(ceil_div(f.M, gemm::kRows), ceil_div(out, L::kTN), steps, f.error);
     a.shape.rounds = f.probe_rounds;
     a.shape.idle = f.probe_role;
     a.sx = scales;
@@ -382,21 +379,18 @@ cudaError_t product(const Fp8BlockArgs& f, const Plan& plan, const uint8_t* code
         const dim3 grid(static_cast<unsigned>(ceil_div(out, 256)), static_cast<unsigned>(f.M));   // (M: rows of less than 152 tiles)
         return gemm::launch_early(sum_kernel<TY>, grid, 256, 0, 1, s, parts, plan.parts, f.M, out, a.ldp, a.y, a.ldy);
     }
-    constexpr int kTileRows = L::kCtas * gemm::kRows;
-    const dim3 grid(static_cast<unsigned>(a.shape.tiles() - plan.whole) * (kTileRows * TN / kSumElements));   // (less than 152 tiles)
-    return gemm::launch_early(rest_kernel<TY, TN, kTileRows>, grid, 256, 0, 1, s, parts, a.shape, f.M, out, a.y, a.ldy);
+    const dim3 grid(static_cast<unsigned>(a.shape.tiles() - plan.whole) * (gemm::kRows * TN / kSumElements));   // (less than 152 tiles)
+    return gemm::launch_early(rest_kernel<TY, TN>, grid, 256, 0, 1, s, parts, a.shape, f.M, out, a.y, a.ldy);
 }
 
 template <class TY>
 cudaError_t run_many(const Fp8BlockArgs& f, const Plan& p, const uint8_t* codes, int ldc, const float* scales, float* parts, cudaStream_t s) {
-    const auto with = [&](auto tn, auto share) {
-        constexpr int kTN = decltype(tn)::value, kShare = decltype(share)::value;
-        return f.gradient ? product<TY, true, kTN, kShare>(f, p, codes, ldc, scales, parts, s)
-                          : product<TY, false, kTN, kShare>(f, p, codes, ldc, scales, parts, s);
+    const auto with = [&](auto tn) {
+        constexpr int kTN = decltype(tn)::value;
+        return f.gradient ? product<TY, true, kTN>(f, p, codes, ldc, scales, parts, s)
+                          : product<TY, false, kTN>(f, p, codes, ldc, scales, parts, s);
     };
-    using One = std::integral_constant<int, 1>;
-    if (p.tn == 128) return with(std::integral_constant<int, 128>(), One());
-    return p.share == 2 ? with(std::integral_constant<int, 256>(), std::integral_constant<int, 2>()) : with(std::integral_constant<int, 256>(), One());
+    return p.tn == 128 ? with(std::integral_constant<int, 128>()) : with(std::integral_constant<int, 256>());
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }

@@ -7,11 +7,10 @@
 // loads its 128 rows of A and half of B: two thirds of the bytes that two single CTAs need
 // for the same 256 x TN, at 32 bytes of K per instruction. Single CTAs are for
 // products with an accumulator per step of K, which would wait for a pair's hand-over between
-// its CTAs; two of them (SHARE = 2) that multiply two row blocks by the same columns of B load
-// half of it each, for both (multicast): the same saving. A stage is 128 bytes of K (64
-// 16-bit elements, 128 FP8). An operand is K-major (its rows run along the contraction) or
-// MN-major (its rows run along M or N, one row per step of the contraction): both gradients
-// of a layer then read the matrices as they lie, without transposed copies.
+// its CTAs. A stage is 128 bytes of K (64 16-bit elements, 128 FP8). An operand is K-major (its
+// rows run along the contraction) or MN-major (its rows run along M or N, one row per step of the
+// contraction): both gradients of a layer then read the matrices as they lie, without transposed
+// copies.
 //
 // Warps: eight or sixteen epilogue warps (four groups of 32 lanes, parts of the columns), a
 // producer's, one or two issuers' (a pair: rank 0's alone work). Every wait is bounded; who gives
@@ -19,11 +18,11 @@
 //
 // What it reaches: 16-bit operands in pairs keep the tensor pipe busy for 95 to 97 of 100 cycles
 // (1,024 x 64,064 x 2,560); FP8 in single CTAs, 256 wide, with a sum of its own for every 128
-// features, 56 without sharing (2,048 x 64,064 x 2,560 270 us): a step lands 48 KB in an SM's shared
+// features, 56 (2,048 x 64,064 x 2,560 270 us): a step lands 48 KB in an SM's shared
 // memory while its instructions take 512 cycles, and hands over an accumulator of half the tensor
 // memory. What changes that balance was measured there
 // (8,192 x 64,064): pairs 1,380 us, whose hand-over crosses CTAs; halves of the columns with
-// accumulators of their own 1,176, which read A twice; single CTAs 1,150, sharing B 1,104.
+// accumulators of their own 1,176, which read A twice; single CTAs 1,150.
 #pragma once
 
 #include <atomic>
@@ -91,16 +90,15 @@ __host__ __device__ inline int tile_index(int tiles_m, int tiles_n, int m, int n
     return g * kGroup * tiles_n + n * rows + m - g * kGroup;
 }
 
-template <int P, int SHARE, int TN, int ELEM, bool A_MN, bool B_MN, int EPI = 8, int ISSUERS = 1>
+template <int P, int TN, int ELEM, bool A_MN, bool B_MN, int EPI = 8, int ISSUERS = 1>
 struct Layout {
-    static_assert(P == 1 || SHARE == 1, "a pair, or single CTAs that share B");
-    static constexpr int kP = P, kShare = SHARE, kCtas = P * SHARE, kTN = TN, kElem = ELEM;
+    static constexpr int kP = P, kTN = TN, kElem = ELEM;
     static constexpr int kEpiWarps = EPI, kProducer = EPI, kIssuer = EPI + 1, kIssuers = ISSUERS, kThreads = 32 * (EPI + 1 + ISSUERS);
     static constexpr int kPart = TN / (EPI / 4);                        // columns of an epilogue warp
     static constexpr bool kAMn = A_MN, kBMn = B_MN;
     static constexpr int kK = kStageBytes / ELEM;                       // elements of K per stage
     static constexpr int kSpan = 128 / ELEM;                            // elements of an MN-major box's rows
-    static constexpr int kBRows = TN / P, kBLoad = TN / kCtas;          // columns of B that a CTA holds, and loads
+    static constexpr int kBRows = TN / P;                               // columns of B that a CTA holds
     static constexpr int kABytes = kRows * kStageBytes, kBBytes = kBRows * kStageBytes;
     static constexpr int kBytes = kABytes + kBBytes;
     // stages: a multiple of the issuers, which take the steps in turn (a wait by parity needs a
@@ -108,7 +106,7 @@ struct Layout {
     static constexpr int kFit = (227 * 1024 - 1024 - 1024) / kBytes, kStages = (kFit < 8 ? kFit : 8) / ISSUERS * ISSUERS;
     static constexpr int kSmem = kStages * kBytes + 1024;
     static constexpr int kBuffers = 512 / TN < 4 ? 512 / TN : 4;        // accumulators in tensor memory
-    static_assert(!(A_MN && kRows % kSpan != 0) && !(B_MN && kBLoad % kSpan != 0), "whole boxes");
+    static_assert(!(A_MN && kRows % kSpan != 0) && !(B_MN && kBRows % kSpan != 0), "whole boxes");
     static_assert(kStages <= 8 && kBytes % 1024 == 0 && TN % 32 == 0 && kStages >= 3, "stage layout");
     static_assert(kBuffers % ISSUERS == 0, "and the accumulators");
 };
@@ -145,15 +143,10 @@ __device__ __forceinline__ bool wait_or_abort(Sync& sy, uint64_t* bar, uint32_t 
 }
 
 // A box of a tensor map into this CTA's shared memory, completing on `bar` (with a pair: a
-// shared::cluster address, rank 0's barrier); BOTH: into both CTAs of a cluster, completing on
-// each one's barrier at that offset.
-template <int P, bool BOTH = false>
+// shared::cluster address, rank 0's barrier).
+template <int P>
 __device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint64_t policy) {
-    if constexpr (BOTH)
-        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
-                     " [%0], [%1, {%2, %3}], [%4], %5, %6;"
-                     :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar), "h"(static_cast<uint16_t>(3)), "l"(policy) : "memory");
-    else if constexpr (P == 1)
+    if constexpr (P == 1)
         asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
                      " [%0], [%1, {%2, %3}], [%4], %5;"
                      :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar), "l"(policy) : "memory");
@@ -177,14 +170,14 @@ __device__ __forceinline__ void arrive_rank0(uint64_t* bar) {
 }
 
 // An operand's part of a stage: `rows` of M or N from `mn`, kK elements of K from `k`.
-template <class L, bool MN, bool BOTH>
+template <class L, bool MN>
 __device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* map, int rows, int mn, int k, uint32_t bar,
                                              uint64_t policy) {
     if constexpr (!MN) {
-        tma_2d<L::kP, BOTH>(dst, map, k, mn, bar, policy);
+        tma_2d<L::kP>(dst, map, k, mn, bar, policy);
     } else {
         for (int i = 0; i < rows / L::kSpan; ++i)   // boxes of kSpan elements x kK rows
-            tma_2d<L::kP, BOTH>(dst + i * L::kK * 128, map, mn + i * L::kSpan, k, bar, policy);
+            tma_2d<L::kP>(dst + i * L::kK * 128, map, mn + i * L::kSpan, k, bar, policy);
     }
 }
 
@@ -248,7 +241,7 @@ __device__ __forceinline__ bool produce(const Job<Op>& job, const Shape& s, int 
     const uint64_t pol_b = Op::kBKeep ? policy_evict_last() : policy_evict_first();
     const Tile t = tile_at(job.args.shape, unit);
     const Shape& o = job.args.shape;
-    const int am = o.a_mn + (t.m * L::kCtas + rank) * kRows, bn = o.b_mn + t.n * L::kTN + rank * L::kBLoad, k0 = t.k0 * L::kK;
+    const int am = o.a_mn + (t.m * P + rank) * kRows, bn = o.b_mn + t.n * L::kTN + rank * L::kBRows, k0 = t.k0 * L::kK;
     for (int k = 0; k < t.steps; ++k) {
         if (r.it >= static_cast<uint32_t>(L::kStages) && !__all_sync(~0u, wait_or_abort(sy, &sy.empty[r.st], r.phase, s))) return false;
         uint8_t* dst = smem + r.st * L::kBytes;
@@ -257,10 +250,8 @@ __device__ __forceinline__ bool produce(const Job<Op>& job, const Shape& s, int 
         else bar = cluster_map(&sy.full[r.st], 0);
         if (elect_one()) {
             if (P == 1 || rank == 0) mbar_arrive_expect_tx(&sy.full[r.st], P * L::kBytes);
-            load_operand<L, L::kAMn, false>(dst, &job.map_a, kRows, am, o.a_k + k0 + k * L::kK, bar, pol_a);
-            // (shared: this CTA's part of B, for both)
-            load_operand<L, L::kBMn, (L::kShare > 1)>(dst + L::kABytes + (L::kShare > 1 ? rank * L::kBLoad * kStageBytes : 0), &job.map_b,
-                                                      L::kBLoad, bn, o.b_k + k0 + k * L::kK, bar, pol_b);
+            load_operand<L, L::kAMn>(dst, &job.map_a, kRows, am, o.a_k + k0 + k * L::kK, bar, pol_a);
+            load_operand<L, L::kBMn>(dst + L::kABytes, &job.map_b, L::kBRows, bn, o.b_k + k0 + k * L::kK, bar, pol_b);
         }
         __syncwarp();
         r.step<L>();
@@ -305,8 +296,7 @@ __device__ __forceinline__ bool issue(const Job<Op>& job, const Shape& s, int un
 #pragma unroll
             for (int j = 0; j < 4; ++j) tc::mma_f<P, kF8>(d, da + kStepA * j, db + kStepB * j, kIdesc, !begin || j > 0);
             if (last) tc::commit_all<P>(&sy.acc_full[b]);
-            if constexpr (L::kShare > 1) tc::commit_both(&sy.empty[r.st]);
-            else tc::commit_all<P>(&sy.empty[r.st]);
+            tc::commit_all<P>(&sy.empty[r.st]);
         }
         __syncwarp();
         if (last) ++r.n;
@@ -329,8 +319,8 @@ struct Jobs {
     using Layout = typename Op::Layout;
     Job<Op> first;
     Job<Op2> second;
-    static_assert(Layout::kP == Op2::Layout::kP && Layout::kShare == Op2::Layout::kShare && Layout::kBytes == Op2::Layout::kBytes &&
-                  Layout::kTN == Op2::Layout::kTN && Layout::kEpiWarps == Op2::Layout::kEpiWarps, "one ring for both");
+    static_assert(Layout::kP == Op2::Layout::kP && Layout::kBytes == Op2::Layout::kBytes && Layout::kTN == Op2::Layout::kTN &&
+                  Layout::kEpiWarps == Op2::Layout::kEpiWarps, "one ring for both");
     __host__ __device__ int units() const { return first.args.shape.units() + second.args.shape.units(); }
     // f(job, unit) of the job that this unit belongs to
     template <class F>
@@ -358,12 +348,12 @@ __global__ void __launch_bounds__(J::Layout::kThreads, 1) product_kernel(const _
     __shared__ Sync sy;
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int rank = L::kCtas == 1 ? 0 : static_cast<int>(cluster_ctarank());
+    const int rank = P == 1 ? 0 : static_cast<int>(cluster_ctarank());
     const Shape& s = jobs.first.args.shape;   // (its error word, limits and self-test are the launch's)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sy.full[i], 1);
-            mbar_init(&sy.empty[i], L::kShare);   // every CTA that its B is for
+            mbar_init(&sy.empty[i], 1);
         }
         for (int i = 0; i < L::kBuffers; ++i) {
             mbar_init(&sy.acc_full[i], 1);
@@ -378,7 +368,7 @@ __global__ void __launch_bounds__(J::Layout::kThreads, 1) product_kernel(const _
     if (warp == 0) tc::tmem_alloc_of<P>(&sy.tmem, 512);
     tc::fence_before_sync();
     __syncthreads();
-    if constexpr (L::kCtas > 1) {   // the other CTA's barriers are ready too
+    if constexpr (P > 1) {   // the other CTA's barriers are ready too
         cluster_fence();
         cluster_sync_all();
     }
@@ -386,7 +376,7 @@ __global__ void __launch_bounds__(J::Layout::kThreads, 1) product_kernel(const _
     programmatic_wait();
     const uint32_t tmem = sy.tmem;
     const int units = jobs.units();
-    const int first = static_cast<int>(blockIdx.x) / L::kCtas, stride = static_cast<int>(gridDim.x) / L::kCtas;
+    const int first = static_cast<int>(blockIdx.x) / P, stride = static_cast<int>(gridDim.x) / P;
 
     // (the producer's and the issuer's warps run their loops whole, one elected lane issues)
     if (warp == L::kProducer && s.idle != kRoleProducer) {
@@ -397,7 +387,7 @@ __global__ void __launch_bounds__(J::Layout::kThreads, 1) product_kernel(const _
         // whoever gave up (a pair's copies complete on rank 0's barriers; all bounded).
         for (uint32_t b = r.it > static_cast<uint32_t>(kStages) ? r.it - kStages : 0; b < r.it; ++b) {
             if ((P == 1 || rank == 0) && !mbar_wait(&sy.full[b % kStages], (b / kStages) & 1, kDrainRounds)) break;
-            if (L::kCtas > 1 && !mbar_wait(&sy.empty[b % kStages], (b / kStages) & 1, kDrainRounds)) break;
+            if (P > 1 && !mbar_wait(&sy.empty[b % kStages], (b / kStages) & 1, kDrainRounds)) break;
         }
         if (lane == 0) sy.copies = r.it;
     } else if (warp >= L::kIssuer && (P == 1 || rank == 0) && s.idle != kRoleIssuer) {
@@ -427,7 +417,7 @@ __global__ void __launch_bounds__(J::Layout::kThreads, 1) product_kernel(const _
     __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
-    if constexpr (L::kCtas > 1) {   // neither CTA ends while the other still reads or signals it
+    if constexpr (P > 1) {   // neither CTA ends while the other still reads or signals it
         cluster_fence();
         cluster_sync_all();
     }
@@ -506,8 +496,8 @@ cudaError_t launch(J& jobs, cudaStream_t stream) {
         s.rounds = kWaitLimit / kWaitSlices;
         s.idle = -1;
     }
-    const int units = jobs.units(), most = sms / L::kCtas;
-    return launch_early(product_kernel<J>, dim3(static_cast<unsigned>((units < most ? units : most) * L::kCtas)), L::kThreads, L::kSmem, L::kCtas, stream, jobs);
+    const int units = jobs.units(), most = sms / L::kP;
+    return launch_early(product_kernel<J>, dim3(static_cast<unsigned>((units < most ? units : most) * L::kP)), L::kThreads, L::kSmem, L::kP, stream, jobs);
 }
 
 }  // namespace gemm

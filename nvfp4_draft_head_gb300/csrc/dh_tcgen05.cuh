@@ -109,12 +109,6 @@ __device__ __forceinline__ void commit_all(uint64_t* bar) {
     }
 }
 
-// The same for two single CTAs of a cluster.
-__device__ __forceinline__ void commit_both(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                 :: "r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3)) : "memory");
-}
-
 // The same for this CTA's barrier alone.
 template <int P>
 __device__ __forceinline__ void commit_own(uint64_t* bar) {
