@@ -356,7 +356,9 @@ __device__ __forceinline__ void named_bar_sync(int id, int threads) {
 // For a kernel launched with programmatic stream serialisation: waits until the kernel before
 // it on the stream has completed and its writes are visible; only then may the next one
 // start, so that a kernel's start says that everything before its predecessor is done. Before
-// it, such a kernel touches no global memory.
+// it, such a kernel touches no global memory; after it, what other kernels write is read with
+// ordinary loads (the non-coherent ones are for what nobody writes while the kernel runs, and it
+// runs since before its predecessor ended).
 __device__ __forceinline__ void programmatic_wait() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");

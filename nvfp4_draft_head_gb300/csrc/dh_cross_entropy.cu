@@ -206,9 +206,8 @@ struct Normaliser {
     }
     __device__ __forceinline__ float loss(float target) const { return ln + (m - target); }
 };
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Tokens tok, const float2* __restrict__ part, int parts,
-                                                            const float* __restrict__ target, float* __restrict__ loss,
-                                                            float* __restrict__ lse, float* __restrict__ rest, const Rows rows) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Tokens tok, const float2* part, int parts, const float* target,
+                                                            float* loss, float* lse, float* rest, const Rows rows) {
     programmatic_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, token = threadIdx.x % kJoinTokens, t = blockIdx.x * kJoinTokens + token;
     float m = kNegInf, s = 0.0f;
@@ -336,10 +335,9 @@ struct Weights {   // g of a piece
 // order of join_kernel) and takes 4,096 columns.
 constexpr int kFewThreads = 256, kFewColumns = kFewThreads * 16;
 template <class T>
-__global__ void __launch_bounds__(kFewThreads) few_kernel(const Tokens tok, const float* __restrict__ z, int ldz,
-                                                          const float2* __restrict__ part, int parts, const float* __restrict__ target,
-                                                          float* __restrict__ loss, float* __restrict__ lse, float* __restrict__ rest,
-                                                          const Rows rows, T* __restrict__ g, T* __restrict__ low, int ldg) {
+__global__ void __launch_bounds__(kFewThreads) few_kernel(const Tokens tok, const float* z, int ldz, const float2* part, int parts,
+                                                          const float* target, float* loss, float* lse, float* rest, const Rows rows,
+                                                          T* g, T* low, int ldg) {
     programmatic_wait();
     constexpr int kSlots = kJoinThreads / kJoinTokens;
     const int t = blockIdx.y, lane = threadIdx.x & 31;
@@ -555,7 +553,7 @@ __device__ __forceinline__ void add8(float (&v)[8], const float* p) {
     v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w, v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
 }
 template <class T>
-__global__ void __launch_bounds__(256) sum_kernel(const Tokens tok, const Sums a, int K, const uint32_t* __restrict__ wmax) {
+__global__ void __launch_bounds__(256) sum_kernel(const Tokens tok, const Sums a, int K, const uint32_t* wmax) {
     programmatic_wait();
     const float scale = exp2i(-scale_exponent<std::is_same<T, __half>::value>(*wmax));
     const unsigned per_row = K / 8;

@@ -27,8 +27,8 @@ using gemm::Tile;
 // codes [M][ldc] (ldc = width rounded up to 16, zeros beyond width), scales [blocks][M].
 constexpr int kQThreads = 256;
 template <class T, bool VEC>
-__global__ void __launch_bounds__(kQThreads) quantize_kernel(const T* __restrict__ x, long long ldx, int M, int width,
-                                                             uint8_t* __restrict__ codes, int ldc, float* __restrict__ scales) {
+__global__ void __launch_bounds__(kQThreads) quantize_kernel(const T* x, long long ldx, int M, int width, uint8_t* codes, int ldc,
+                                                             float* scales) {
     programmatic_wait();
     const unsigned per_row = static_cast<unsigned>(ceil_div(width, kBlock));
     const unsigned unit = blockIdx.x * (kQThreads / 8) + (threadIdx.x >> 3);   // < 2^31 (checked)
@@ -208,7 +208,7 @@ struct Product {
         for (int i = 0; i < kPart; ++i) sum[i] = 0.0f;
         const auto scale_at = [&](int b) {
             b = b < steps ? b : steps - 1;
-            return make_float2(__ldg(sx + static_cast<size_t>(b) * a.M), __ldg(sw + static_cast<size_t>(b) * a.sw_b));
+            return make_float2(sx[static_cast<size_t>(b) * a.M], __ldg(sw + static_cast<size_t>(b) * a.sw_b));
         };
         float2 s1 = scale_at(0), s2 = scale_at(1);   // two steps ahead: a load takes longer than a step
 #pragma unroll 1
@@ -244,8 +244,7 @@ struct Product {
 
 // y from the sums of its parts, in order, where all tiles are in parts.
 template <class TY>
-__global__ void __launch_bounds__(256) sum_kernel(const float* __restrict__ parts, int splits, int M, int N, int ldp, TY* __restrict__ y,
-                                                  long long ldy) {
+__global__ void __launch_bounds__(256) sum_kernel(const float* parts, int splits, int M, int N, int ldp, TY* y, long long ldy) {
     programmatic_wait();
     const unsigned n = blockIdx.x * 256 + threadIdx.x, m = blockIdx.y;
     if (n >= static_cast<unsigned>(N)) return;
@@ -261,8 +260,7 @@ __global__ void __launch_bounds__(256) sum_kernel(const float* __restrict__ part
 // 300 x 1,024 x 2,560 8.2 us, 10.0 tile by tile.)
 constexpr int kSumElements = 512;
 template <class TY, int TN>
-__global__ void __launch_bounds__(256) rest_kernel(const float* __restrict__ parts, gemm::Shape shape, int M, int N, TY* __restrict__ y,
-                                                   long long ldy) {
+__global__ void __launch_bounds__(256) rest_kernel(const float* parts, gemm::Shape shape, int M, int N, TY* y, long long ldy) {
     programmatic_wait();
     constexpr unsigned per = gemm::kRows * TN / kSumElements;
     const unsigned at = blockIdx.x / per, first = (blockIdx.x - at * per) * kSumElements + threadIdx.x;

@@ -43,7 +43,7 @@ __device__ __forceinline__ void load16_any(const T* p, const Rows<T>& rows, floa
     uint32_t w[kWords];
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(first) + i);
+        const uint4 q = reinterpret_cast<const uint4*>(first)[i];
         w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
     }
     const uint32_t off = static_cast<uint32_t>(at & 15);

@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         } else {
             for (int i = threadIdx.x; i < count * NT; i += 32 * kEpiWarps) {
                 const int m = i % NT, b = i / NT;
-                scales[i] = m < a.M ? __ldg(a.scales + static_cast<size_t>(b0 + b) * a.M + m) : 0.0f;
+                scales[i] = m < a.M ? a.scales[static_cast<size_t>(b0 + b) * a.M + m] : 0.0f;
             }
         }
         named_bar_sync(1, 32 * kEpiWarps);   // the scales are there for every warp
