@@ -467,6 +467,7 @@ __global__ void __launch_bounds__(Cfg<FMT, K, MT, LOGITS>::THREADS, Cfg<FMT, K, 
     // workspace and the outputs are used only after its completion.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
+    // (h by ordinary loads: the preceding kernel may write it while this one already runs)
     const uint32_t* h32 = reinterpret_cast<const uint32_t*>(a.h);
 
     if (C::RING && warp == NW + C::NRW) {
@@ -727,7 +728,7 @@ __global__ void __launch_bounds__(Cfg<FMT, K, MT, LOGITS>::THREADS, Cfg<FMT, K, 
                     // 16 drafts 53.4 -> 50.6 µs against 4-byte loads
 #pragma unroll
                     for (int j4 = 0; j4 < 4; ++j4) {
-                        const uint4 v = live ? __ldg(reinterpret_cast<const uint4*>(h32 + d * KW + k0 / 2) + j4)
+                        const uint4 v = live ? reinterpret_cast<const uint4*>(h32 + d * KW + k0 / 2)[j4]
                                              : make_uint4(0u, 0u, 0u, 0u);
                         const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -781,7 +782,7 @@ __global__ void __launch_bounds__(Cfg<FMT, K, MT, LOGITS>::THREADS, Cfg<FMT, K, 
 #pragma unroll
                 for (int ww = 0; ww < WPW; ++ww) {
                     const int kw = (128 * (wbase + ww * NW) + 4 * lane) / 2;  // u32 index of the lane's 4 values
-                    const uint2 v2 = __ldg(reinterpret_cast<const uint2*>(h32 + d * KW + kw));
+                    const uint2 v2 = *reinterpret_cast<const uint2*>(h32 + d * KW + kw);
                     const uint32_t w0 = v2.x, w1 = v2.y;
                     const uint32_t word = act_fp8_pair(w0, sx) | (act_fp8_pair(w1, sx) << 16);
 #pragma unroll
@@ -819,7 +820,7 @@ __global__ void __launch_bounds__(Cfg<FMT, K, MT, LOGITS>::THREADS, Cfg<FMT, K, 
                 // 4-byte loads)
 #pragma unroll
                 for (int j4 = 0; j4 < 4; ++j4) {
-                    const uint4 v = live ? __ldg(reinterpret_cast<const uint4*>(h32 + d * KW + k0 / 2) + j4)
+                    const uint4 v = live ? reinterpret_cast<const uint4*>(h32 + d * KW + k0 / 2)[j4]
                                          : make_uint4(0u, 0u, 0u, 0u);
                     hb[ww][nt][4 * j4] = v.x;
                     hb[ww][nt][4 * j4 + 1] = v.y;
@@ -834,7 +835,7 @@ __global__ void __launch_bounds__(Cfg<FMT, K, MT, LOGITS>::THREADS, Cfg<FMT, K, 
                 } else {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    const uint32_t w = live ? __ldg(h32 + d * KW + k0 / 2 + j) : 0u;
+                    const uint32_t w = live ? ld_u32(h32 + d * KW + k0 / 2 + j) : 0u;
                     hb[ww][nt][j] = w;
                     am = fmaxf(am, fmaxf(fabsf(bf16_lo(w)), fabsf(bf16_hi(w))));
                 }
