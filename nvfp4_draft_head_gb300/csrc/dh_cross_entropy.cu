@@ -91,9 +91,9 @@ __device__ __forceinline__ int scale_exponent(uint32_t wmax) {
 // reading the head is the work (24 x 308 x 576 9.1e-8, 1.4e-7 with four, the same time).
 int logit_chunk(int P, int steps) { return P == 1 ? 2 : steps <= 16 ? 4 : 8; }
 
-// A thread's 128 logits of one row.
+// A thread's 128 columns of one row, its accumulators added up.
 template <class L>
-__device__ __forceinline__ bool sum_logits(Acc<L>& acc, int steps, int chunk, uint32_t offset, float (&z)[kHalf]) {
+__device__ __forceinline__ bool sum_chunks(Acc<L>& acc, int steps, int chunk, uint32_t offset, float (&z)[kHalf]) {
 #pragma unroll
     for (int i = 0; i < kHalf; ++i) z[i] = 0.0f;
 #pragma unroll 1
@@ -133,7 +133,7 @@ struct Stats {
         const int j = (row < a.tok.T ? a.tok.row(row) : -1) - n0;
         if (row == 0 && n0 == 0) *a.wmax = 0u;
         float z[kHalf];
-        if (!sum_logits(acc, t.steps, a.shape.chunk, (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf, z)) return false;
+        if (!sum_chunks(acc, t.steps, a.shape.chunk, (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf, z)) return false;
         if (valid < kHalf) {
 #pragma unroll
             for (int i = 0; i < kHalf; ++i) z[i] = i < valid ? z[i] : kNegInf;
@@ -315,7 +315,7 @@ struct Weights {   // g of a piece
         const bool live = w != 0.0f;
         w = ldexpf(w, scale_exponent<kF16>(*a.wmax));
         float z[kHalf];
-        if (!sum_logits(acc, t.steps, a.shape.chunk, (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf, z)) return false;
+        if (!sum_chunks(acc, t.steps, a.shape.chunk, (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf, z)) return false;
         const int j = y - (a.first + c0);
         T* out = a.g + static_cast<size_t>(row) * a.ldg + c0;
         T* low = a.low != nullptr ? a.low + static_cast<size_t>(row) * a.ldg + c0 : nullptr;
@@ -399,63 +399,54 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const Tokens tok, cons
     store_weights<T>(p, y - c, w, live, g + at, low + at);
 }
 
-// The next accumulator's 128 columns of a thread's row, scaled and rounded, to `out` (`columns` of
-// them there, a multiple of 8): in 32-byte pieces where rows are so aligned (`wide`), else 16.
-// A row that does not count is zeros whatever it was multiplied by.
-template <class T, class A>
-__device__ __forceinline__ bool store_rows(A& acc, T* out, bool in, int columns, uint32_t offset, float scale, bool live, bool wide) {
-    const uint32_t at = acc.next();
-    if (at == ~0u) return false;
-#pragma unroll 1
-    for (int c = 0; c < kHalf && c < columns; c += 32) {
-        uint32_t r[32];
-        tc::tmem_load32(at + offset + c, r);
-        tc::tmem_load_wait();
+// The gradients' sums are truncated as the logits' are, and their contractions are longer: summed
+// throughout by the tensor cores, dW of 1,100,000 tokens was short by 3.7e-4 of itself. Sixteen steps at a
+// time leave 4e-6 and cost nothing (4,096 x 64,026 x 2,560 3,076 us, 3,096; 100 x 64,026 236, 233).
+constexpr int kGradientChunk = 16;
+
+// A thread's columns of one row (`columns` of 128, a multiple of 8), sixteen at a time to
+// put(column, values).
+template <class L, class Put>
+__device__ __forceinline__ bool each_sixteen(Acc<L>& acc, int steps, uint32_t offset, int columns, Put put) {
+    float z[kHalf];
+    if (!sum_chunks(acc, steps, kGradientChunk, offset, z)) return false;
 #pragma unroll
-        for (int i = 0; i < 32; i += 16) {
-            if (!in || c + i >= columns) break;
-            uint32_t v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[j] = live ? rows::Elem<T>::pack2(__uint_as_float(r[i + 2 * j]) * scale, __uint_as_float(r[i + 2 * j + 1]) * scale) : 0u;
-            if (wide) {   // (then columns is a multiple of 16)
-                store32(out + c + i, v);
-            } else {
-                __stcg(reinterpret_cast<uint4*>(out + c + i), make_uint4(v[0], v[1], v[2], v[3]));
-                if (c + i + 8 < columns) __stcg(reinterpret_cast<uint4*>(out + c + i + 8), make_uint4(v[4], v[5], v[6], v[7]));
-            }
-        }
-        __syncwarp();
-    }
-    acc.release();
+    for (int c = 0; c < kHalf; c += 16)
+        if (c < columns) put(c, z + c);
+    __syncwarp();
     return true;
 }
 
-// The same as 32-bit sums (rows 32-byte aligned), added to what is there if `add`.
-template <class A>
-__device__ __forceinline__ bool store_sums(A& acc, float* out, bool in, int columns, uint32_t offset, bool add) {
-    const uint32_t at = acc.next();
-    if (at == ~0u) return false;
-#pragma unroll 1
-    for (int c = 0; c < kHalf && c < columns; c += 32) {
-        uint32_t r[32];
-        tc::tmem_load32(at + offset + c, r);
-        tc::tmem_load_wait();
+// 16 columns (`columns` of them there, 8 or more), scaled and rounded, to `out`: in 32-byte pieces
+// where rows are so aligned (`wide`; then all 16 are there), else 16. A row that does not count is
+// zeros whatever it was multiplied by.
+template <class T>
+__device__ __forceinline__ void store_rounded(const float* z, T* out, int columns, float scale, bool live, bool wide) {
+    uint32_t v[8];
 #pragma unroll
-        for (int i = 0; i < 32; i += 8) {
-            if (!in || c + i >= columns) break;
-            if (add) {
-                const float4 p = *reinterpret_cast<const float4*>(out + c + i), q = *reinterpret_cast<const float4*>(out + c + i + 4);
-                const float o[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
-#pragma unroll
-                for (int j = 0; j < 8; ++j) r[i + j] = __float_as_uint(o[j] + __uint_as_float(r[i + j]));
-            }
-            store32(out + c + i, r + i);
-        }
-        __syncwarp();
+    for (int j = 0; j < 8; ++j) v[j] = live ? rows::Elem<T>::pack2(z[2 * j] * scale, z[2 * j + 1] * scale) : 0u;
+    if (wide) {
+        store32(out, v);
+    } else {
+        __stcg(reinterpret_cast<uint4*>(out), make_uint4(v[0], v[1], v[2], v[3]));
+        if (columns > 8) __stcg(reinterpret_cast<uint4*>(out + 8), make_uint4(v[4], v[5], v[6], v[7]));
     }
-    acc.release();
-    return true;
+}
+
+// The same as 32-bit sums (rows 32-byte aligned), added to what is there if `add`.
+__device__ __forceinline__ void store_sums(const float* z, float* out, int columns, bool add) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 8) {
+        if (i >= columns) break;
+        float v[8] = {};
+        if (add) {
+            const float4 p = *reinterpret_cast<const float4*>(out + i), q = *reinterpret_cast<const float4*>(out + i + 4);
+            v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w, v[4] = q.x, v[5] = q.y, v[6] = q.z, v[7] = q.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += z[i + j];
+        store32(out + i, reinterpret_cast<const uint32_t*>(v));
+    }
 }
 
 // dh: g (along the piece) times the piece's head rows, as 32-bit sums: [T][K] of whole tiles
@@ -464,7 +455,7 @@ template <class T>
 struct Hidden {
     using Layout = gemm::Layout<kPair, kTN, 2, false, true>;
     static constexpr int kFormat = std::is_same<T, __half>::value ? 0 : 1;
-    static constexpr int kChunk = gemm::kWholeTile;
+    static constexpr int kChunk = kGradientChunk;
     static constexpr bool kAKeep = true, kBKeep = true;
     struct Args {
         gemm::Shape shape;
@@ -482,19 +473,23 @@ struct Hidden {
     __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int rank, A2& acc) {
         const int local = rank * gemm::kRows + (warp & 3) * 32 + lane, row = t.m * kTM + local, half = warp >> 2;
         const int n0 = t.n * kTN + half * kHalf;
-        if (a.out != nullptr) {
-            const bool live = row < a.T_ && a.tok.live(row);
-            return store_rows<T>(acc, a.out + static_cast<size_t>(row) * a.ld + n0, row < a.T_, a.K - n0, (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf,
-                                 live ? exp2i(-scale_exponent<std::is_same<T, __half>::value>(*a.wmax)) : 0.0f, live, false);
-        }
-        float* out;
+        const bool in = row < a.T_;
+        const uint32_t offset = (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf;
+        const bool live = a.out != nullptr && in && a.tok.live(row);
+        const float scale = live ? exp2i(-scale_exponent<std::is_same<T, __half>::value>(*a.wmax)) : 0.0f;
+        T* out = a.out + static_cast<size_t>(row) * a.ld + n0;
+        float* sums;
         if (t.split <= 0) {
-            out = a.sum + static_cast<size_t>(row) * a.K + n0;
+            sums = a.sum + static_cast<size_t>(row) * a.K + n0;
         } else {
             const int rest = a.shape.tiles() - a.shape.whole, at = gemm::tile_index(a.shape.tiles_m, a.shape.tiles_n, t.m, t.n) - a.shape.whole;
-            out = a.parts + (static_cast<size_t>((t.split - 1) * rest + at) * kTM + local) * kTN + half * kHalf;
+            sums = a.parts + (static_cast<size_t>((t.split - 1) * rest + at) * kTM + local) * kTN + half * kHalf;
         }
-        return store_sums(acc, out, row < a.T_, a.K - n0, (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf, a.add != 0);
+        return each_sixteen(acc, t.steps, offset, a.K - n0, [&](int c, const float* z) {
+            if (!in) return;
+            if (a.out != nullptr) store_rounded<T>(z, out + c, a.K - n0 - c, scale, live, false);
+            else store_sums(z, sums + c, a.K - n0 - c, a.add != 0);
+        });
     }
 };
 
@@ -505,7 +500,7 @@ struct Head {
     using Layout = gemm::Layout<kPair, kTN, 2, true, true>;
     static constexpr bool kF16 = std::is_same<T, __half>::value;
     static constexpr int kFormat = kF16 ? 0 : 1;
-    static constexpr int kChunk = gemm::kWholeTile;
+    static constexpr int kChunk = kGradientChunk;
     static constexpr bool kAKeep = true, kBKeep = true;
     struct Args {
         gemm::Shape shape;
@@ -520,15 +515,18 @@ struct Head {
     __device__ static bool tile(const Args& a, const Tile& t, int warp, int lane, int rank, A2& acc) {
         const int row = (t.m * kPair + rank) * gemm::kRows + (warp & 3) * 32 + lane, half = warp >> 2;
         const int n0 = t.n * kTN + half * kHalf;
-        if (a.parts != nullptr) {
-            const int at = gemm::tile_index(a.shape.tiles_m, a.shape.tiles_n, t.m, t.n);
-            float* sums = a.parts + ((static_cast<size_t>(t.split) * a.shape.tiles() + at) * kTM + rank * gemm::kRows + (warp & 3) * 32 + lane) * kTN +
-                          half * kHalf;
-            return store_sums(acc, sums, row < a.rows, a.K - n0, (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf, false);
-        }
+        const bool in = row < a.rows;
+        const uint32_t offset = (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf;
+        const int at = gemm::tile_index(a.shape.tiles_m, a.shape.tiles_n, t.m, t.n);
+        float* sums = a.parts + ((static_cast<size_t>(t.split) * a.shape.tiles() + at) * kTM + rank * gemm::kRows + (warp & 3) * 32 + lane) * kTN +
+                      half * kHalf;
         const float scale = exp2i(-scale_exponent<kF16>(*a.wmax));
-        return store_rows<T>(acc, a.out + static_cast<size_t>(row) * a.ld + n0, row < a.rows, a.K - n0,
-                             (static_cast<uint32_t>(warp & 3) << 21) + half * kHalf, scale, true, a.wide);
+        T* out = a.out + static_cast<size_t>(row) * a.ld + n0;
+        return each_sixteen(acc, t.steps, offset, a.K - n0, [&](int c, const float* z) {
+            if (!in) return;
+            if (a.parts != nullptr) store_sums(z, sums + c, a.K - n0 - c, false);
+            else store_rounded<T>(z, out + c, a.K - n0 - c, scale, true, a.wide);
+        });
     }
 };
 
@@ -844,8 +842,10 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
         }
         const size_t total = sums.elements + static_cast<size_t>(sums.head.tiles()) * (kTM * kTN / 8);
         const size_t want = (total + 255) / 256, cap = static_cast<size_t>(sm_count()) * 8;
-        e = gemm::launch_early(sum_kernel<T>, dim3(static_cast<unsigned>(want < cap ? want : cap)), 256, 0, 1, stream, tok, sums, c.K, wmax);
-        if (e != cudaSuccess) return e;
+        // (not early: a product's CTA leaves no registers for this kernel's, which would all start on the few SMs
+        // that are through first: 100 x 64,026 x 2,560 241 us, 231)
+        sum_kernel<T><<<static_cast<unsigned>(want < cap ? want : cap), 256, 0, stream>>>(tok, sums, c.K, wmax);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     return cudaSuccess;
 }

@@ -61,7 +61,7 @@ struct Shape {
     __host__ __device__ int units() const { return whole + (tiles() - whole) * splits; }
 };
 
-constexpr int kWholeTile = 1 << 30, kPerLaunch = 0;   // of an operator's kChunk
+constexpr int kPerLaunch = 0;   // of an operator's kChunk
 
 enum Role { kRoleProducer, kRoleIssuer, kRoleEpilogue };
 
@@ -207,9 +207,9 @@ struct Acc {
 };
 
 // Op: Layout, Args (with `Shape shape`), kFormat (idesc_f), kChunk (steps of K that share an
-// accumulator: results that are scaled step by step take 1, those of a tile summed throughout by
-// the tensor cores kWholeTile; kPerLaunch: Shape's chunk, a power of two), kAKeep / kBKeep (the operand is read by other tiles too: kept in
-// L2), and tile(args, tile, warp, lane, rank, acc), false when a wait gave up.
+// accumulator: results that are scaled step by step take 1; kPerLaunch: Shape's chunk, a power of
+// two), kAKeep / kBKeep (the operand is read by other tiles too: kept in L2), and tile(args, tile,
+// warp, lane, rank, acc), false when a wait gave up.
 
 // One product of a launch: its operands' maps and its arguments.
 template <class Op>
