@@ -589,6 +589,12 @@ int draft_head_cross_entropy_backward(const dh_cross_entropy_t *c, const float *
                                       int64_t ld_dhidden, void *dhead, int64_t ld_dhead, void *ws, size_t ws_bytes,
                                       unsigned int *error, void *stream);
 
+/* *word: the device address of an error word of the library's own on the current device,
+ * for callers that keep none (zero at load, one per device until the process exits, so that
+ * it outlives captured graphs). draft_head_read_device_error(*word, ...) reads and clears
+ * it. */
+int draft_head_cross_entropy_error_word(void **word);
+
 /* The self-test of draft_head_cross_entropy's waits, on the loss alone: roles, rounds and
  * error as for fp8_block_matmul_wait_probe (role 2 is waited for where an SM has more than
  * 512 features or two tiles). */

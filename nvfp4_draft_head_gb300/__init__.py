@@ -68,7 +68,7 @@ EXPORTS = (
     "draft_head_static_read_device_error", "draft_head_row_map", "draft_head_token_logprobs", "draft_head_distill",
     "draft_head_distill_backward", "nvfp4_matmul_packed_bytes", "nvfp4_pack_matmul", "nvfp4_matmul_workspace_bytes",
     "nvfp4_matmul", "nvfp4_matmul_wait_probe", "draft_head_cross_entropy_workspace_bytes", "draft_head_cross_entropy",
-    "draft_head_cross_entropy_backward", "fp8_quantize_blocks", "fp8_block_matmul_workspace_bytes", "fp8_block_matmul",
+    "draft_head_cross_entropy_backward", "draft_head_cross_entropy_error_word", "fp8_quantize_blocks", "fp8_block_matmul_workspace_bytes", "fp8_block_matmul",
     "fp8_block_matmul_input_gradient", "fp8_block_matmul_wait_probe", "draft_head_cross_entropy_wait_probe",
 )
 
@@ -174,6 +174,7 @@ def lib():
         L.draft_head_cross_entropy_workspace_bytes.argtypes = [I, I, I, C.c_uint]
         L.draft_head_cross_entropy_workspace_bytes.restype = S
         L.draft_head_cross_entropy.argtypes = [P, P, P, P, P, C.c_int64, P, C.c_int64, P, S, P, P]
+        L.draft_head_cross_entropy_error_word.argtypes = [P]
         L.draft_head_cross_entropy_backward.argtypes = [P, P, P, P, C.c_int64, P, C.c_int64, P, S, P, P]
         L.fp8_quantize_blocks.argtypes = [P, I, I, P, I, P, P, P, S, P]
         L.fp8_block_matmul_workspace_bytes.argtypes = [I, I, I]
@@ -1062,15 +1063,17 @@ class DistillTopK(torch.autograd.Function):
 
 # ------------------------------------------- cross entropy against head rows --
 
-_error_words: dict = {}
+_error_words: dict = {}    # device -> address of the library's error word there
 
 
-def _error_word(device) -> torch.Tensor | None:
-    """This device's error word of operators without a handle (none for a call that is
-    captured before the first eager one: the word has to outlive the graph's pool)."""
+def _error_word(device) -> int:
+    """The error word on this device (the current one) of operators without a handle. It
+    belongs to the library: a call that is captured needs one that outlives the graph."""
     word = _error_words.get(device)
-    if word is None and not torch.cuda.is_current_stream_capturing():
-        word = _error_words.setdefault(device, torch.zeros(1, dtype=torch.int32, device=device))
+    if word is None:
+        address = C.c_void_p()
+        _check("draft_head_cross_entropy_error_word", lib().draft_head_cross_entropy_error_word(C.byref(address)))
+        word = _error_words.setdefault(device, address.value)
     return word
 
 
@@ -1078,13 +1081,12 @@ def linear_cross_entropy_device_error(device=None) -> int:
     """Read and clear the device error word of the linear_cross_entropy calls on `device`
     (the current one), after waiting for the device: DH_DEVERR_TIMEOUT where a bounded
     wait ran out, which makes results since the last reading invalid."""
-    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    torch.cuda.synchronize(device)
-    word = _error_words.get(device)
-    err = 0 if word is None else int(word.item())
-    if err:
-        word.zero_()
-    return err
+    err = C.c_int()
+    with torch.cuda.device(device):
+        torch.cuda.synchronize()
+        word = _error_word(torch.device("cuda", torch.cuda.current_device()))
+        _check("draft_head_read_device_error", lib().draft_head_read_device_error(word, C.byref(err), _stream()))
+    return err.value
 
 
 def _rows16(t: torch.Tensor, name: str, rows: int, K: int, like: torch.Tensor | None = None) -> int:
@@ -1170,7 +1172,7 @@ def linear_cross_entropy(hidden: torch.Tensor, head: torch.Tensor, tokens: torch
     ws = _cross_entropy_space(T, N, K, DH_CE_LOSS | DH_CE_DHIDDEN | DH_CE_DHEAD, device)
     _check("draft_head_cross_entropy",
            lib().draft_head_cross_entropy(d, loss.data_ptr(), None, None, dx.data_ptr(), ld_dx, dw.data_ptr(), ld_dw, ws.data_ptr(),
-                                          ws.numel(), _ptr(_error_word(device)), s))
+                                          ws.numel(), _error_word(device), s))
     return loss, dx, dw
 
 
@@ -1189,7 +1191,7 @@ def linear_cross_entropy_forward(hidden: torch.Tensor, head: torch.Tensor, token
         ws = _cross_entropy_space(T, N, K, DH_CE_LOSS, device)
         _check("draft_head_cross_entropy",
                lib().draft_head_cross_entropy(d, loss.data_ptr(), lse.data_ptr(), rest.data_ptr(), None, 0, None, 0, ws.data_ptr(),
-                                              ws.numel(), _ptr(_error_word(device)), s))
+                                              ws.numel(), _error_word(device), s))
     return loss, lse, rest
 
 
@@ -1216,7 +1218,7 @@ def linear_cross_entropy_backward(hidden: torch.Tensor, head: torch.Tensor, toke
     ws = _cross_entropy_space(T, N, K, (DH_CE_DHIDDEN if dx is not None else 0) | (DH_CE_DHEAD if dw is not None else 0), device)
     _check("draft_head_cross_entropy_backward",
            lib().draft_head_cross_entropy_backward(d, lse.data_ptr(), _ptr(rest), _ptr(dx), ld_dx, _ptr(dw), ld_dw, ws.data_ptr(),
-                                                   ws.numel(), _ptr(_error_word(device)), s))
+                                                   ws.numel(), _error_word(device), s))
     return dx, dw
 
 
@@ -1229,7 +1231,7 @@ def linear_cross_entropy_wait_probe(hidden: torch.Tensor, head: torch.Tensor, to
     ws = _cross_entropy_space(T, N, K, DH_CE_LOSS, hidden.device)
     _check("draft_head_cross_entropy_wait_probe",
            lib().draft_head_cross_entropy_wait_probe(d, loss.data_ptr(), ws.data_ptr(), ws.numel(), role, rounds,
-                                                     _ptr(_error_word(hidden.device)), s))
+                                                     _error_word(hidden.device), s))
 
 
 class LinearCrossEntropy(torch.autograd.Function):

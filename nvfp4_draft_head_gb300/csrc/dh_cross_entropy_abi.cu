@@ -12,6 +12,11 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? DH_OK : dh::record_cuda_error(e); }
 
+// The library's own error word, laid out as the head of a workspace (dh::Workspace: the word comes
+// first). In host code this name is a host-side stand-in: the address comes from
+// cudaGetSymbolAddress.
+static __device__ __align__(DH_WORKSPACE_ALIGN) unsigned int g_error_word;
+
 constexpr int kMaxT = 1 << 24, kMaxN = 1 << 24, kMaxK = 1 << 20;
 
 bool shape_ok(int T, int N, int K) {
@@ -107,6 +112,15 @@ int draft_head_cross_entropy_backward(const dh_cross_entropy_t* c, const float* 
     if ((st = check_space(a, ws, ws_bytes)) != DH_OK) return st;
     a.ws = ws;
     return cuda_status(dh::launch_cross_entropy(a, static_cast<cudaStream_t>(stream)));
+}
+
+int draft_head_cross_entropy_error_word(void** word) {
+    if (word == nullptr) return DH_ERR_ARG;
+    void* p = nullptr;
+    const cudaError_t e = cudaGetSymbolAddress(&p, g_error_word);
+    if (e != cudaSuccess) return dh::record_cuda_error(e);
+    *word = p;
+    return DH_OK;
 }
 
 int draft_head_cross_entropy_wait_probe(const dh_cross_entropy_t* c, float* loss, void* ws, size_t ws_bytes, int role, unsigned int rounds,
