@@ -1270,22 +1270,27 @@ class LinearCrossEntropy(torch.autograd.Function):
 class FP8BlockLinear(torch.autograd.Function):
     """y [M, N] = FP8BlockLinear.apply(x, matmul, out_dtype): matmul (an FP8BlockMatmul) as a
     frozen layer, differentiable once in x: dx = matmul.input_gradient(dy), of x's type (the
-    rounding of x to FP8 passes the gradient straight through). Captured backward passes: as
-    for LinearCrossEntropy."""
+    rounding of x to FP8 passes the gradient straight through, so dx does not depend on x, which
+    is not kept and may be changed in place). Captured backward passes: as for
+    LinearCrossEntropy."""
+
+    @classmethod
+    def apply(cls, x, matmul, out_dtype=torch.bfloat16):
+        # what stands for x, without its storage, where a second derivative is refused
+        tie = torch.slice_copy(x, 0, 0, 0) if x.requires_grad and x.dim() == 2 and torch.is_grad_enabled() else None
+        return super().apply(x, matmul, out_dtype, (tie,))
 
     @staticmethod
-    def forward(ctx, x, matmul, out_dtype=torch.bfloat16):
-        ctx.matmul, ctx.dtype = matmul, x.dtype
-        ctx.save_for_backward(x)
+    def forward(ctx, x, matmul, out_dtype, tie):
+        ctx.matmul, ctx.dtype, ctx.tie = matmul, x.dtype, tie
         return matmul(x.detach(), out_dtype=out_dtype)
 
     @staticmethod
     def backward(ctx, dy):
-        x, = ctx.saved_tensors
         with torch.no_grad():
             if dy.shape[0] > 1 and dy.stride(0) < dy.shape[1] or dy.stride(1) != 1:   # an expanded gradient
                 dy = dy.contiguous()
             dx = ctx.matmul.input_gradient(dy, out_dtype=ctx.dtype)
         if torch.is_grad_enabled():
-            dx = _Refuse.apply("FP8BlockLinear is differentiable once: its gradient has no derivative", dx, x, dy)
-        return dx, None, None
+            dx = _Refuse.apply("FP8BlockLinear is differentiable once: its gradient has no derivative", dx, dy, *ctx.tie)
+        return dx, None, None, None
