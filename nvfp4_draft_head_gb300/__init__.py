@@ -253,8 +253,8 @@ def draft_head_build_index(keep) -> tuple[np.ndarray, int]:
 def _gather_args(W: torch.Tensor, idx: torch.Tensor):
     if W.dtype != torch.bfloat16 or W.dim() != 2 or not W.is_cuda or not W.is_contiguous():
         raise ValueError("W must be a contiguous [V, K] bfloat16 CUDA tensor")
-    if idx.dtype != torch.int32 or idx.dim() != 1 or idx.device != W.device:
-        raise ValueError("idx must be an int32 vector on W's device")
+    if idx.dtype != torch.int32 or idx.dim() != 1 or idx.device != W.device or not idx.is_contiguous():
+        raise ValueError("idx must be a contiguous int32 vector on W's device")
     return W.shape[0], W.shape[1], idx.numel()
 
 
