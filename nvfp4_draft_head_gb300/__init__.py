@@ -730,7 +730,7 @@ class FP8BlockMatmul:
         if q.dtype not in (torch.uint8, torch.float8_e4m3fn) or q.dim() != 2 or not q.is_cuda or not q.is_contiguous():
             raise ValueError("q must be a contiguous [N, K] uint8 or float8_e4m3fn CUDA tensor")
         self.N, self.K = q.shape
-        if self.N < 1 or self.K < 16 or self.K % 16:
+        if self.N < 1 or self.N > 1 << 24 or self.K < 16 or self.K % 16 or self.K > 1 << 20:
             raise DraftHeadError("fp8_block_matmul", DH_ERR_SHAPE)
         if q.data_ptr() % 16:
             raise DraftHeadError("fp8_block_matmul", DH_ERR_ALIGN)
@@ -783,6 +783,8 @@ class FP8BlockMatmul:
         M = shape[0] if len(shape) == 2 else -1
         if M < 0 or shape[1] != width or t is None or x.device != device:
             raise ValueError(f"the input must be a [M, {width}] bfloat16, float16 or float32 tensor on {device}")
+        if M > 1 << 24:   # (the library's sizes are 32-bit)
+            raise DraftHeadError(name, DH_ERR_SHAPE)
         ldx, step = x.stride()
         if (step != 1 and width > 1) or (M > 1 and ldx < width):
             raise ValueError("the input's rows must be contiguous and must not overlap")
@@ -820,6 +822,8 @@ class FP8BlockMatmul:
         if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != self.K or x.device != self.q.device or not x.is_contiguous():
             raise ValueError(f"x must be a contiguous [M, {self.K}] bfloat16 tensor")
         M, s = x.shape[0], _stream_of(x)
+        if M > 1 << 24:
+            raise DraftHeadError("fp8_block_matmul_wait_probe", DH_ERR_SHAPE)
         y = torch.empty((M, self.N), dtype=torch.bfloat16, device=x.device)
         nb = lib().fp8_block_matmul_workspace_bytes(M, self.K, self.N)
         ws = torch.empty(nb, dtype=torch.uint8, device=x.device)

@@ -29,3 +29,19 @@ def test_ids_that_are_not_contiguous_are_refused(quantise):
         with pytest.raises(ValueError, match="contiguous"):
             quantise(W, bad, stream=torch.cuda.Stream())
     quantise(W, ids[::2].contiguous())
+
+
+def test_sizes_past_32_bits_are_refused():
+    """More tokens than the library's integers hold (one row of them, cut, would be computed)."""
+    mm = dh.FP8BlockMatmul.from_weight(rand((1, 16)))
+    dy = torch.empty((2 ** 32 + 1, 1), dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(dh.DraftHeadError, match="shape"):
+        mm.input_gradient(dy)
+    del dy
+    x = torch.empty((2 ** 24 + 1, 16), dtype=torch.bfloat16, device=DEV)
+    for call in (mm, mm.forward, lambda t: mm.wait_probe(t, 1, 16)):
+        with pytest.raises(dh.DraftHeadError, match="shape"):
+            call(x)
+    for shape in ((2 ** 24 + 1, 16), (1, 2 ** 20 + 16)):
+        with pytest.raises(dh.DraftHeadError, match="shape"):
+            dh.FP8BlockMatmul(torch.empty(shape, dtype=torch.uint8, device=DEV), torch.empty((-(-shape[0] // 128), -(-shape[1] // 128)), device=DEV))
