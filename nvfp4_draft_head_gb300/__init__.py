@@ -1133,7 +1133,7 @@ def _gradient_rows(out: torch.Tensor | None, like: torch.Tensor, rows: int, K: i
     """A gradient's tensor and row stride."""
     if out is None:
         return torch.empty((rows, K), dtype=like.dtype, device=like.device), K
-    if out.data_ptr() == like.data_ptr():
+    if out.data_ptr() == like.data_ptr() and rows > 0:
         raise ValueError(f"{name} must not be the tensor that it is the gradient of")
     return out, _rows16(out, name, rows, K, like)
 

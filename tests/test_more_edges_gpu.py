@@ -45,3 +45,23 @@ def test_sizes_past_32_bits_are_refused():
     for shape in ((2 ** 24 + 1, 16), (1, 2 ** 20 + 16)):
         with pytest.raises(dh.DraftHeadError, match="shape"):
             dh.FP8BlockMatmul(torch.empty(shape, dtype=torch.uint8, device=DEV), torch.empty((-(-shape[0] // 128), -(-shape[1] // 128)), device=DEV))
+
+
+@pytest.mark.parametrize("sliced", [False, True])
+def test_no_tokens_with_given_results(sliced):
+    """Empty tensors have no address of their own to tell them apart by."""
+    def none(dtype):
+        return torch.empty((4, 64), dtype=dtype, device=DEV)[:0] if sliced else torch.empty((0, 64), dtype=dtype, device=DEV)
+
+    head, tokens = rand((40, 64)), torch.empty(0, dtype=torch.int32, device=DEV)
+    h, dx, dw = none(torch.bfloat16), none(torch.bfloat16), torch.full((40, 64), 3.0, dtype=torch.bfloat16, device=DEV)
+    loss, got_dx, got_dw = dh.linear_cross_entropy(h, head, tokens, dhidden=dx, dhead=dw)
+    assert loss.shape == (0,) and got_dx is dx and got_dw is dw and not dw.any()
+    dw.fill_(3.0)
+    lse = torch.empty(0, device=DEV)
+    got_dx, got_dw = dh.linear_cross_entropy_backward(h, head, tokens, lse, dhidden=dx, dhead=dw)
+    assert got_dx is dx and got_dw is dw and not dw.any()
+    with pytest.raises(ValueError, match="gradient of"):
+        dh.linear_cross_entropy(h, head, tokens, dhead=head)
+    mm = dh.FP8BlockMatmul.from_weight(rand((64, 64)))
+    assert mm(h, dx) is dx and mm.input_gradient(h, dx) is dx
