@@ -1259,7 +1259,8 @@ class LinearCrossEntropy(torch.autograd.Function):
         with torch.no_grad():
             up = dloss.float()
             if ctx.needs_input_grad[0] or ctx.needs_input_grad[1]:
-                w = (up if weights is None else up * weights).contiguous()
+                # (a row of weight 0 stays left out whatever its loss's gradient is)
+                w = up.contiguous() if weights is None else (up * weights).masked_fill_(weights == 0, 0.0)
                 dx, dw = linear_cross_entropy_backward(hidden, head, tokens, lse, w, rest, row_of, dhidden=ctx.needs_input_grad[0],
                                                        dhead=ctx.needs_input_grad[1])
             if weights is not None and ctx.needs_input_grad[3]:

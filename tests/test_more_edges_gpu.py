@@ -65,3 +65,22 @@ def test_no_tokens_with_given_results(sliced):
         dh.linear_cross_entropy(h, head, tokens, dhead=head)
     mm = dh.FP8BlockMatmul.from_weight(rand((64, 64)))
     assert mm(h, dx) is dx and mm.input_gradient(h, dx) is dx
+
+
+@pytest.mark.parametrize("T", [60, 200])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_rows_that_are_left_out_have_any_gradient_of_their_loss(T, bad):
+    """Rows of weight 0 and tokens without a row: what comes back to their losses (0 / 0 of an empty
+    count, say) reaches nothing."""
+    h, head = rand((T, 64)).requires_grad_(), rand((300, 64), 2, 0.1).requires_grad_()
+    tokens = torch.arange(T, dtype=torch.int32, device=DEV)
+    weights = torch.rand(T, generator=torch.Generator(DEV).manual_seed(3), device=DEV) + 0.5
+    weights[::3] = 0.0
+    tokens[1::3] = -100
+    up = torch.ones(T, device=DEV)
+    loss = dh.LinearCrossEntropy.apply(h, head, tokens, weights)
+    want = torch.autograd.grad(loss, (h, head), up, retain_graph=True)
+    up[::3] = up[1::3] = bad
+    got = torch.autograd.grad(loss, (h, head), up)
+    assert all(torch.equal(a, b) and b.isfinite().all() for a, b in zip(got, want))
+    assert not got[0][::3].any() and not got[0][1::3].any() and got[0][2::3].any()
