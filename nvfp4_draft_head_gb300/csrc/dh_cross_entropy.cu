@@ -197,10 +197,11 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
     s = s * exp2_approx((m - ref) * kLog2e) + s2 * exp2_approx((m2 - ref) * kLog2e);
     m = top;
 }
-// A row's normaliser from its maximum and sum: m + ln s, and what rounding that took away.
+// A row's normaliser from its maximum and sum: m + ln s, and what rounding that took away. (A
+// maximum of -inf is that of no finite logits, as of a hidden state with an infinity: NaN.)
 struct Normaliser {
     float m, ln, lse, rest;
-    __device__ __forceinline__ Normaliser(float m_, float s) : m(m_), ln(logf(s)), lse(m + ln) {
+    __device__ __forceinline__ Normaliser(float m_, float s) : m(m_), ln(logf(m_ > kNegInf ? s : m_)), lse(m + ln) {
         const float b = lse - m;   // (two-sum)
         rest = (m - (lse - b)) + (ln - b);
     }

@@ -84,3 +84,25 @@ def test_rows_that_are_left_out_have_any_gradient_of_their_loss(T, bad):
     got = torch.autograd.grad(loss, (h, head), up)
     assert all(torch.equal(a, b) and b.isfinite().all() for a, b in zip(got, want))
     assert not got[0][::3].any() and not got[0][1::3].any() and got[0][2::3].any()
+
+
+@pytest.mark.parametrize("T,N", [(3, 40), (100, 700), (300, 700)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_a_row_whose_logits_are_all_minus_infinity(T, N, dtype):
+    """An infinity times head rows of one sign: no logit is NaN, and the loss, lse and dh are all the same,
+    in a row that is left out its lse."""
+    h, head = rand((T, 64), dtype=dtype), rand((N, 64), 2, 0.1, dtype)
+    head[:, 5] = -head[:, 5].abs() - 0.01
+    tokens = torch.arange(T, dtype=torch.int32, device=DEV) % N
+    want = dh.linear_cross_entropy_forward(h, head, tokens)
+    h[1, 5] = h[2, 5] = float("inf")
+    tokens[2] = -100
+    loss, lse, rest = dh.linear_cross_entropy_forward(h, head, tokens)
+    assert loss[1].isnan() and loss[2] == 0.0 and lse[1:3].isnan().all()
+    others = [i for i in range(T) if i not in (1, 2)]
+    assert torch.equal(loss[others], want[0][others]) and torch.equal(lse[others], want[1][others])
+    both, dx, dw = dh.linear_cross_entropy(h, head, tokens)
+    assert both[1].isnan() and both[2] == 0.0 and dx[1].isnan().all() and not dx[2].any() and dw.isnan().any()
+    assert dx[others].isfinite().all()
+    dx, _ = dh.linear_cross_entropy_backward(h, head, tokens, lse, rest=rest, dhead=False)
+    assert dx[1].isnan().all() and not dx[2].any() and dx[others].isfinite().all()
