@@ -427,9 +427,11 @@ cudaError_t run(const Fp8BlockArgs& f, cudaStream_t s) {
 size_t fp8_block_workspace_bytes(int M, int width, int out) {
     f8::FewPlan few;
     f8::Plan many;
-    if (f8::take_few(M, out, width, &few, &many) && few.fused) return DH_WORKSPACE_ALIGN;   // not used
+    const bool use_few = f8::take_few(M, out, width, &few, &many);
+    if (use_few && few.fused) return DH_WORKSPACE_ALIGN;   // not used
     return f8::up256(static_cast<size_t>(M) * (f8::ceil_div(width, 16) * 16)) +
-           f8::up256(static_cast<size_t>(M) * f8::ceil_div(width, f8::kBlock) * sizeof(float)) + f8::up256(many.part_bytes(M, out));
+           f8::up256(static_cast<size_t>(M) * f8::ceil_div(width, f8::kBlock) * sizeof(float)) +
+           (use_few ? 0 : f8::up256(many.part_bytes(M, out)));
 }
 
 cudaError_t launch_fp8_quantize_blocks(const uint16_t* W, int V, int K, const int32_t* idx, int N, uint8_t* q, float* scale, Workspace* ws,
