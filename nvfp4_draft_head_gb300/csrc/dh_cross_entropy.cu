@@ -37,6 +37,7 @@ namespace ce {
 
 using gemm::Acc;
 using gemm::ceil_div;
+using gemm::store32;
 using gemm::Tile;
 using rows::kLog2e;
 using rows::kNegInf;
@@ -48,12 +49,6 @@ __device__ __forceinline__ float exp2_approx(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
-}
-
-// 32 bytes, 32-byte aligned, in one store.
-__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
-    asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                 :: "l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
 }
 
 struct Tokens {

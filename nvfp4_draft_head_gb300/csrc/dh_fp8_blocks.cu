@@ -87,12 +87,6 @@ __global__ void __launch_bounds__(kWThreads) blocks_kernel(const uint16_t* __res
 
 // ----------------------------------------------------------------- product ----
 
-// 32 bytes, 32-byte aligned, in one store.
-__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
-    asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                 :: "l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
-}
-
 // 32 results of a row at `out`, 32-byte aligned, `valid` of them wanted.
 template <class TY>
 __device__ __forceinline__ void store_row(TY* out, const float* v, int valid) {
@@ -106,7 +100,7 @@ __device__ __forceinline__ void store_row(TY* out, const float* v, int valid) {
                 if constexpr (sizeof(TY) == 2) w[j] = rows::Elem<TY>::pack2(v[i + 2 * j], v[i + 2 * j + 1]);
                 else w[j] = __float_as_uint(v[i + j]);
             }
-            store32(out + i, w);
+            gemm::store32(out + i, w);
         } else {
 #pragma unroll
             for (int j = 0; j < kPer; ++j)

@@ -127,6 +127,12 @@ __device__ __forceinline__ bool elect_one() {
     return yes != 0u;
 }
 
+// 32 bytes, 32-byte aligned, in one store.
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+    asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 :: "l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+}
+
 // A bounded wait that gives up at once when another role of this CTA has.
 static __device__ __noinline__ bool wait_longer(volatile unsigned int* abort, uint64_t* bar, uint32_t parity, uint32_t rounds,
                                                 unsigned int* error) {
@@ -162,9 +168,11 @@ __device__ __forceinline__ uint64_t policy_evict_last() {
     return p;
 }
 
-// Arrive on rank 0's barrier. What the arrival orders are tensor-memory loads, by the tcgen05
-// fences; released at cluster scope it would wait for this thread's global accesses in flight
-// too, and a step of the FP8 product took 1.05 us.
+// Arrive on rank 0's barrier, with the default scope, this CTA's. What the arrival has to order are
+// tensor-memory loads alone: those have returned (tmem_load_wait) before the warps arrive that this
+// thread has waited for, and the tcgen05 fences on both sides keep them there. Released at cluster scope
+// it would wait for this thread's global accesses in flight too, and a step of the FP8 product took
+// 1.05 us.
 __device__ __forceinline__ void arrive_rank0(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_map(bar, 0)) : "memory");
 }
