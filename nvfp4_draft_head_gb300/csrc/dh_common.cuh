@@ -361,6 +361,12 @@ __device__ __forceinline__ void named_bar_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
 }
 
+// 32 bytes, 32-byte aligned, in one store.
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+    asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 :: "l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+}
+
 // For a kernel launched with programmatic stream serialisation: waits until the kernel before
 // it on the stream has completed and its writes are visible; only then may the next one
 // start, so that a kernel's start says that everything before its predecessor is done. Before

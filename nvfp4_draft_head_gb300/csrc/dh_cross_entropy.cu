@@ -37,7 +37,6 @@ namespace ce {
 
 using gemm::Acc;
 using gemm::ceil_div;
-using gemm::store32;
 using gemm::Tile;
 using rows::kLog2e;
 using rows::kNegInf;
@@ -607,7 +606,7 @@ int piece_rows(int T, int N) {
 // rounds of whole tiles, 2,985.
 gemm::Shape hidden_tiles(int T, int K, int piece, unsigned int* error) {
     gemm::Shape s = gemm::whole_tiles(ceil_div(T, kTM), ceil_div(K, kTN), ceil_div(piece, 64), error);
-    constexpr int pairs = 76;   // of the 152 SMs
+    constexpr int pairs = kSms / kPair;
     const int rest = s.whole % pairs;
     if (rest == 0) return s;
     s.whole -= rest;
@@ -637,8 +636,9 @@ int terms_of(int T) { return T <= 128 ? 2 : 1; }
 // steps). A head of several pieces has tiles enough.
 gemm::Shape head_tiles(int rows, int N, int K, int piece, unsigned int* error) {
     gemm::Shape s = gemm::whole_tiles(ceil_div(N, kTM), ceil_div(K, kTN), ceil_div(rows, 64), error);
-    if (N > piece || s.tiles() > 38 || s.steps < 16) return s;
-    const int p = 76 / s.tiles() < s.steps / 8 ? 76 / s.tiles() : s.steps / 8;
+    constexpr int pairs = kSms / kPair;
+    if (N > piece || s.tiles() > pairs / 2 || s.steps < 16) return s;
+    const int p = pairs / s.tiles() < s.steps / 8 ? pairs / s.tiles() : s.steps / 8;
     s.whole = 0;
     s.split_steps = ceil_div(s.steps, p);
     s.splits = ceil_div(s.steps, s.split_steps);

@@ -100,7 +100,7 @@ __device__ __forceinline__ void store_row(TY* out, const float* v, int valid) {
                 if constexpr (sizeof(TY) == 2) w[j] = rows::Elem<TY>::pack2(v[i + 2 * j], v[i + 2 * j + 1]);
                 else w[j] = __float_as_uint(v[i + j]);
             }
-            gemm::store32(out + i, w);
+            store32(out + i, w);
         } else {
 #pragma unroll
             for (int j = 0; j < kPer; ++j)
@@ -297,14 +297,13 @@ struct Plan {
     }
 };
 
-// By rounds of tiles over the 152 SMs times a step's time, or by reading the weight. A step takes
+// By rounds of tiles over the SMs times a step's time, or by reading the weight. A step takes
 // 0.43 us in a 256-wide tile, 0.38 in a 128-wide one: wide tiles have twice the work between two
 // hand-overs, narrow ones spread a small product over more SMs (512 x 4,608 x 2,560 15.0 wide,
 // 13.3 narrow). With one row block, which alone reads its columns of the weight, 0.67 and 0.40 (1 x
 // 20,000 x 2,560 17). Parts cost a second kernel: 200 tokens, gradient of 64,026 x 2,560 193 in one
 // part, 55 in sixteen.
 Plan plan_of(int M, int out, int width) {
-    constexpr int kSms = 152;
     const int steps = ceil_div(width, kBlock);
     Plan best = {};
     constexpr struct { int tn; float step, alone; } kForms[] = {{256, 0.43f, 0.67f}, {128, 0.38f, 0.40f}};
@@ -368,10 +367,10 @@ cudaError_t product(const Fp8BlockArgs& f, const Plan& plan, const uint8_t* code
     a.ldp = plan.whole == 0 ? part_stride(out) : 0;
     if ((e = gemm::launch(jobs, s)) != cudaSuccess) return e;
     if (plan.whole == 0) {
-        const dim3 grid(static_cast<unsigned>(ceil_div(out, 256)), static_cast<unsigned>(f.M));   // (M: rows of less than 152 tiles)
+        const dim3 grid(static_cast<unsigned>(ceil_div(out, 256)), static_cast<unsigned>(f.M));   // (M: rows of less than kSms tiles)
         return gemm::launch_early(sum_kernel<TY>, grid, 256, 0, 1, s, parts, plan.parts, f.M, out, a.ldp, a.y, a.ldy);
     }
-    const dim3 grid(static_cast<unsigned>(a.shape.tiles() - plan.whole) * (gemm::kRows * TN / kSumElements));   // (less than 152 tiles)
+    const dim3 grid(static_cast<unsigned>(a.shape.tiles() - plan.whole) * (gemm::kRows * TN / kSumElements));   // (less than kSms tiles)
     return gemm::launch_early(rest_kernel<TY, TN>, grid, 256, 0, 1, s, parts, a.shape, f.M, out, a.y, a.ldy);
 }
 

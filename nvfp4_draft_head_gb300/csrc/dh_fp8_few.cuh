@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
 
 // Clusters of 1 to 8 CTAs of this memory that run at once (they do not span the GPU's processing
 // clusters).
-constexpr int kClusters[kMaxSplits + 1] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+constexpr int kClusters[kMaxSplits + 1] = {0, kSms, kSms / 2, 46, 36, 28, 23, 15, 15};
 
 template <class TX, class TY, int NT, bool FUSED, bool GRADIENT>
 cudaError_t launch_kernel(const CUtensorMap& map_w, const CUtensorMap& map_x, FewArgs a, int splits, cudaStream_t stream) {

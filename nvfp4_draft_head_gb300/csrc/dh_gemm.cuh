@@ -127,12 +127,6 @@ __device__ __forceinline__ bool elect_one() {
     return yes != 0u;
 }
 
-// 32 bytes, 32-byte aligned, in one store.
-__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
-    asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                 :: "l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
-}
-
 // A bounded wait that gives up at once when another role of this CTA has.
 static __device__ __noinline__ bool wait_longer(volatile unsigned int* abort, uint64_t* bar, uint32_t parity, uint32_t rounds,
                                                 unsigned int* error) {

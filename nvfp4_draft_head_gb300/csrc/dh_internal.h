@@ -88,6 +88,10 @@ int record_cuda_error(cudaError_t e);
 // Number of SMs of the current device (cached per device).
 int sm_count();
 
+// SMs of a GB300, for which the tile plans of the many-token products are made: their workspaces are
+// sized without a device. (Launches take what sm_count() says; results are the same on any number.)
+constexpr int kSms = 152;
+
 // Logits rows of the token log-probability and distillation operators (dh_type
 // element types; ld in elements; inv_t = 1 / temperature; row_of may be null).
 struct LogprobArgs {

@@ -241,12 +241,6 @@ __device__ __forceinline__ void lds16(uint32_t addr, uint32_t& a, uint32_t& b, u
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(addr) : "memory");
 }
 
-// 32 bytes, 32-byte aligned, in one store.
-__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
-    asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                 :: "l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
-}
-
 // PROBE: the self-test of the waits (nvfp4_matmul_wait_probe): the role a.idle does
 // nothing, waits are short, and work still in flight at the end is recorded.
 template <class TY, int TN, bool PROBE>
