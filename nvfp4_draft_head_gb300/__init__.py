@@ -56,7 +56,7 @@ DH_DEVERR_UNFINISHED = 4
 DH_HEAD_IDX_ASCENDING = 1
 DH_T_BF16, DH_T_F16, DH_T_F32 = 1, 2, 3
 DH_MAX_TOP, DH_MAX_TEACHER = 128, 512
-DH_CE_LOSS, DH_CE_DHIDDEN, DH_CE_DHEAD = 1, 2, 4
+DH_CE_LOSS, DH_CE_DHIDDEN, DH_CE_DHEAD, DH_CE_TWO_TERMS = 1, 2, 4, 8
 
 EXPORTS = (
     "draft_head_build_index", "draft_head_quantize_workspace_bytes", "nvfp4_quantize_rows",
@@ -1108,7 +1108,7 @@ def _rows16(t: torch.Tensor, name: str, rows: int, K: int, like: torch.Tensor | 
     return ld
 
 
-def _cross_entropy(hidden, head, tokens, weights, row_of):
+def _cross_entropy(hidden, head, tokens, weights, row_of, two_terms=False):
     """A call's dh_cross_entropy_t (as bytes), T, N and K, its tensors checked."""
     dtype = hidden.dtype
     if (dtype != torch.bfloat16 and dtype != torch.float16) or not hidden.is_cuda or hidden.dim() != 2:
@@ -1122,7 +1122,7 @@ def _cross_entropy(hidden, head, tokens, weights, row_of):
     _vector(weights, "weights", torch.float32, T, device)
     _vector(row_of, "row_of", torch.int32, None, device)
     try:
-        d = _pack_cross_entropy(hidden.data_ptr(), head.data_ptr(), _TYPES[dtype], T, K, N, ld_hidden, ld_head, tokens.data_ptr(),
+        d = _pack_cross_entropy(hidden.data_ptr(), head.data_ptr(), _TYPES[dtype] | (DH_CE_TWO_TERMS if two_terms else 0), T, K, N, ld_hidden, ld_head, tokens.data_ptr(),
                                 _ptr(weights) or 0, _ptr(row_of) or 0, 0 if row_of is None else row_of.numel())
     except struct.error:   # a size past 32 bits
         raise DraftHeadError("dh_cross_entropy_t", DH_ERR_SHAPE) from None
@@ -1155,25 +1155,28 @@ def _cross_entropy_space(T: int, N: int, K: int, outputs: int, device) -> torch.
 
 def linear_cross_entropy(hidden: torch.Tensor, head: torch.Tensor, tokens: torch.Tensor, weights: torch.Tensor | None = None,
                          row_of: torch.Tensor | None = None, dhidden: torch.Tensor | None = None, dhead: torch.Tensor | None = None,
-                         stream=None):
+                         stream=None, two_terms: bool = False):
     """(loss float32 [T], dhidden [T, K], dhead [N, K]): per-token softmax cross entropy of
     hidden states [T, K] against the vocabulary of the head rows [N, K] (both bfloat16 or
-    both float16, K % 8 == 0, rows 16-byte aligned), and the gradients of its sum, without
-    the [T, N] logits in memory (but for up to 128 tokens). tokens: int32 [T], target ids with row_of (draft_head_row_map), head rows
-    without it; a token without a head row (-100, say) is left out, as a row of weight 0 is.
-    weights: float32 [T]. dhidden and dhead may be given tensors, which overlap no other. The loss has no autograd
-    graph (the gradients are at hand; LinearCrossEntropy is the differentiable form). See
-    draft_head_cross_entropy."""
+    both float16, K % 8 == 0, rows 16-byte aligned), and the gradients of its sum, without the
+    [T, N] logits in memory (but for up to 128 tokens; their gradient, in 16 bits, is there for a
+    piece of the vocabulary at a time, of up to 512 MiB). tokens: int32 [T], target ids with
+    row_of (draft_head_row_map), head rows without it; a token without a head row (-100, say) is
+    left out, as a row of weight 0 is. weights: float32 [T]. dhidden and dhead may be given
+    tensors, which overlap no other. two_terms: the logits' gradient in two 16-bit terms for more
+    than 128 tokens too, whose gradients then are off by their own rounding alone (1.43 times that
+    with one), at one and a half times the time. The loss has no autograd graph (the gradients are
+    at hand; LinearCrossEntropy is the differentiable form). See draft_head_cross_entropy."""
     if stream is not None:
-        return _on_stream(stream, linear_cross_entropy, hidden, head, tokens, weights, row_of, dhidden, dhead)
-    d, T, N, K = _cross_entropy(hidden, head, tokens, weights, row_of)
+        return _on_stream(stream, linear_cross_entropy, hidden, head, tokens, weights, row_of, dhidden, dhead, None, two_terms)
+    d, T, N, K = _cross_entropy(hidden, head, tokens, weights, row_of, two_terms)
     (dx, ld_dx), (dw, ld_dw) = _gradient_rows(dhidden, hidden, T, K, "dhidden"), _gradient_rows(dhead, head, N, K, "dhead")
     device = hidden.device
     loss = torch.empty(T, dtype=torch.float32, device=device)
     if T == 0:
         return loss, dx, dw.zero_()
     s = _stream_of(hidden)
-    ws = _cross_entropy_space(T, N, K, DH_CE_LOSS | DH_CE_DHIDDEN | DH_CE_DHEAD, device)
+    ws = _cross_entropy_space(T, N, K, DH_CE_LOSS | DH_CE_DHIDDEN | DH_CE_DHEAD | (DH_CE_TWO_TERMS if two_terms else 0), device)
     _check("draft_head_cross_entropy",
            lib().draft_head_cross_entropy(d, loss.data_ptr(), None, None, dx.data_ptr(), ld_dx, dw.data_ptr(), ld_dw, ws.data_ptr(),
                                           ws.numel(), _error_word(device), s))
@@ -1201,16 +1204,17 @@ def linear_cross_entropy_forward(hidden: torch.Tensor, head: torch.Tensor, token
 
 def linear_cross_entropy_backward(hidden: torch.Tensor, head: torch.Tensor, tokens: torch.Tensor, lse: torch.Tensor,
                                   weights: torch.Tensor | None = None, rest: torch.Tensor | None = None,
-                                  row_of: torch.Tensor | None = None, dhidden=True, dhead=True, stream=None):
+                                  row_of: torch.Tensor | None = None, dhidden=True, dhead=True, stream=None, two_terms: bool = False):
     """(dhidden, dhead) from linear_cross_entropy_forward's lse (and rest, which is 0 if it is
     not given); weights: float32 [T], the upstream gradient of each row's loss times the
     forward's weight. dhidden and dhead: True, a tensor to write, or False for none (then
-    None is returned in its place; not both)."""
+    None is returned in its place; not both). two_terms: as for linear_cross_entropy."""
     if stream is not None:
-        return _on_stream(stream, linear_cross_entropy_backward, hidden, head, tokens, lse, weights, rest, row_of, dhidden, dhead)
+        return _on_stream(stream, linear_cross_entropy_backward, hidden, head, tokens, lse, weights, rest, row_of, dhidden, dhead, None,
+                          two_terms)
     if dhidden is False and dhead is False:
         raise ValueError("at least one of dhidden and dhead has to be wanted")
-    d, T, N, K = _cross_entropy(hidden, head, tokens, weights, row_of)
+    d, T, N, K = _cross_entropy(hidden, head, tokens, weights, row_of, two_terms)
     device = hidden.device
     _vector(lse, "lse", torch.float32, T, device)
     _vector(rest, "rest", torch.float32, T, device)
@@ -1219,7 +1223,8 @@ def linear_cross_entropy_backward(hidden: torch.Tensor, head: torch.Tensor, toke
     if T == 0:
         return dx, None if dw is None else dw.zero_()
     s = _stream_of(hidden)
-    ws = _cross_entropy_space(T, N, K, (DH_CE_DHIDDEN if dx is not None else 0) | (DH_CE_DHEAD if dw is not None else 0), device)
+    outputs = (DH_CE_DHIDDEN if dx is not None else 0) | (DH_CE_DHEAD if dw is not None else 0) | (DH_CE_TWO_TERMS if two_terms else 0)
+    ws = _cross_entropy_space(T, N, K, outputs, device)
     _check("draft_head_cross_entropy_backward",
            lib().draft_head_cross_entropy_backward(d, lse.data_ptr(), _ptr(rest), _ptr(dx), ld_dx, _ptr(dw), ld_dw, ws.data_ptr(),
                                                    ws.numel(), _error_word(device), s))
@@ -1239,16 +1244,18 @@ def linear_cross_entropy_wait_probe(hidden: torch.Tensor, head: torch.Tensor, to
 
 
 class LinearCrossEntropy(torch.autograd.Function):
-    """loss [T] = LinearCrossEntropy.apply(hidden, head, tokens, weights, row_of);
+    """loss [T] = LinearCrossEntropy.apply(hidden, head, tokens, weights, row_of, two_terms);
     differentiable once in the hidden states, the head and the weights (a weight's
-    derivative is the loss that its row has at weight 1). No logits are kept between the
-    passes: the backward pass multiplies them again from the normaliser. (A backward pass that
+    derivative is the loss that its row has at weight 1, which takes the loss's product once
+    more). No logits are kept between the passes: the backward pass multiplies them again from
+    the normaliser. two_terms: as for linear_cross_entropy. (A backward pass that
     is captured into a CUDA graph needs leaves of which no eager graph is alive, as torch has it
     for every function: drop earlier losses first.)"""
 
     @staticmethod
-    def forward(ctx, hidden, head, tokens, weights=None, row_of=None):
+    def forward(ctx, hidden, head, tokens, weights=None, row_of=None, two_terms=False):
         loss, lse, rest = linear_cross_entropy_forward(hidden, head, tokens, weights, row_of)
+        ctx.two_terms = two_terms
         ctx.save_for_backward(hidden, head, tokens, lse, rest, weights, row_of)
         return loss
 
@@ -1262,14 +1269,14 @@ class LinearCrossEntropy(torch.autograd.Function):
                 # (a row of weight 0 stays left out whatever its loss's gradient is)
                 w = up.contiguous() if weights is None else (up * weights).masked_fill_(weights == 0, 0.0)
                 dx, dw = linear_cross_entropy_backward(hidden, head, tokens, lse, w, rest, row_of, dhidden=ctx.needs_input_grad[0],
-                                                       dhead=ctx.needs_input_grad[1])
+                                                       dhead=ctx.needs_input_grad[1], two_terms=ctx.two_terms)
             if weights is not None and ctx.needs_input_grad[3]:
                 dweights = up * linear_cross_entropy_forward(hidden, head, tokens, None, row_of)[0]
         if torch.is_grad_enabled():   # the caller asked for the gradients' graph
             dx, dw, dweights = (None if d is None else
                                 _Refuse.apply("LinearCrossEntropy is differentiable once: its gradient has no derivative", d, hidden,
                                               head, dloss, weights) for d in (dx, dw, dweights))
-        return dx, dw, None, dweights, None
+        return dx, dw, None, dweights, None, None
 
 
 class FP8BlockLinear(torch.autograd.Function):

@@ -18,8 +18,8 @@
 // Roundings besides 32-bit arithmetic: g to the inputs' 16-bit type (the tensor cores take
 // nothing wider from it; its error is that of rounding the results again), scaled by a power of
 // two so that the largest row weight lies just under 1 (bf16) or 2^15 (f16, whose probabilities
-// would be subnormal below 6e-5), in two terms for up to 128 tokens; the gradients once, at the
-// end.
+// would be subnormal below 6e-5), in two terms for up to 128 tokens or where the caller asks for
+// them; the gradients once, at the end.
 //
 // What bounds it. Many tokens: the tensor cores, whose pipe is busy for 95 to 97 of 100 cycles in
 // all four products, at the clock that the power limit leaves them (1.6 of 2.07 GHz): the loss of
@@ -628,8 +628,9 @@ gemm::Shape hidden_tiles(int T, int K, int piece, unsigned int* error) {
 // alone (64,026 x 2,560 bf16, relative 2-norm: 0.00238 and 0.00166); a second one takes it away at any
 // size and costs, in us (one term / two): 129 tokens 276 / 336, 256 293 / 379, 520 513 / 705, 4,096
 // 2,776 / 4,482; 100 tokens 230 in two. That error is within the gradients' own type, and a framework
-// that keeps its logits in 16 bits has it as well, so it is not paid for above 128 tokens.
-int terms_of(int T) { return T <= 128 ? 2 : 1; }
+// that keeps its logits in 16 bits has it as well, so above 128 tokens the second term is the caller's
+// choice (DH_CE_TWO_TERMS).
+int terms_of(int T, bool two_terms) { return two_terms || T <= 128 ? 2 : 1; }
 
 // dW's tiles where they are few and the tokens many: all in parts of at least eight steps, as many
 // as fill the pairs of SMs once (6,208 tokens, 5 rows of 4,592: 34 us of 105 were 18 tiles of 97
@@ -647,12 +648,12 @@ gemm::Shape head_tiles(int rows, int N, int K, int piece, unsigned int* error) {
 
 // Whether a call for both keeps its logits: few tokens whose vocabulary is one piece. Multiplied
 // again, 12 x 83,361 x 3,568 takes 449 us; kept, 347 (the head is read twice in place of three times).
-bool keeps_logits(int T, int N) { return T <= gemm::kRows && N <= piece_rows(terms_of(T) * T, N); }
+bool keeps_logits(int T, int N) { return T <= gemm::kRows && N <= piece_rows(terms_of(T, false) * T, N); }
 
 struct Space {
     size_t z, wmax, part, target, lse, rest, g, hidden, sum, parts, head_parts, bytes;
 };
-Space space_of(int T, int N, int K, bool loss, bool dh, bool dw) {
+Space space_of(int T, int N, int K, bool loss, bool dh, bool dw, bool two_terms) {
     Space s = {};
     size_t at = 256;   // wmax at 0
     const auto take = [&](size_t n) {
@@ -667,7 +668,7 @@ Space space_of(int T, int N, int K, bool loss, bool dh, bool dw) {
         s.lse = take(t * 4);
         s.rest = take(t * 4);
     }
-    const int rows = terms_of(T) * T, piece = piece_rows(rows, N);
+    const int rows = terms_of(T, two_terms) * T, piece = piece_rows(rows, N);
     const size_t r = static_cast<size_t>(rows);
     if (dh || dw) s.g = take(r * piece * 2);
     if (loss && (dh || dw) && keeps_logits(T, N)) s.z = take(t * up256(N) * 4);
@@ -691,13 +692,13 @@ Space space_of(int T, int N, int K, bool loss, bool dh, bool dw) {
 template <class T, int P>
 cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
     const bool loss = c.loss != nullptr, dh = c.dhidden != nullptr, dw = c.dhead != nullptr;
-    const Space sp = space_of(c.T, c.N, c.K, loss, dh, dw);
+    const Space sp = space_of(c.T, c.N, c.K, loss, dh, dw, c.two_terms);
     uint8_t* ws = static_cast<uint8_t*>(c.ws);
     Tokens tok = {c.tokens, c.row_of, c.weight, c.V, c.T, c.N};
     uint32_t* wmax = reinterpret_cast<uint32_t*>(ws + sp.wmax);
     const int tiles_m = ceil_div(c.T, gemm::kRows * P);
     T* hidden = dw ? reinterpret_cast<T*>(ws + sp.hidden) : nullptr;
-    const int terms = terms_of(c.T), all_rows = terms * c.T;   // of g
+    const int terms = terms_of(c.T, c.two_terms), all_rows = terms * c.T;   // of g
     const Rows rows = {c.hidden, c.ld_hidden, c.K, hidden, terms > 1 ? c.T : 0, wmax};
     cudaError_t e;
     using K1 = typename Stats<T, P>::Layout;
@@ -853,8 +854,8 @@ cudaError_t run_typed(const CrossEntropyArgs& c, cudaStream_t stream) {
 
 }  // namespace ce
 
-size_t cross_entropy_workspace_bytes(int T, int N, int K, bool loss, bool dhidden, bool dhead) {
-    return ce::space_of(T, N, K, loss, dhidden, dhead).bytes;
+size_t cross_entropy_workspace_bytes(int T, int N, int K, bool loss, bool dhidden, bool dhead, bool two_terms) {
+    return ce::space_of(T, N, K, loss, dhidden, dhead, two_terms).bytes;
 }
 
 cudaError_t launch_cross_entropy(const CrossEntropyArgs& a, cudaStream_t s) {

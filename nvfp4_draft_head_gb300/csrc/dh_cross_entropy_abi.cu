@@ -38,7 +38,8 @@ int64_t stride(int64_t ld, int rows, int K) { return rows > 1 ? ld : K; }
 int check(const dh_cross_entropy_t* c, void* dhidden, int64_t ld_dhidden, void* dhead, int64_t ld_dhead, const void* ws,
           const unsigned int* error, dh::CrossEntropyArgs& a) {
     if (c == nullptr || c->hidden == nullptr || c->head == nullptr || c->tokens == nullptr || ws == nullptr) return DH_ERR_ARG;
-    if (c->type != DH_T_BF16 && c->type != DH_T_F16) return DH_ERR_ARG;
+    const int type = c->type & ~static_cast<int>(DH_CE_TWO_TERMS);
+    if (type != DH_T_BF16 && type != DH_T_F16) return DH_ERR_ARG;
     if (dhidden == c->hidden || dhead == c->head || (dhidden != nullptr && dhidden == dhead)) return DH_ERR_ARG;   // not in place
     if (!shape_ok(c->T, c->N, c->K)) return DH_ERR_SHAPE;
     if (c->row_of != nullptr && c->V < 1) return DH_ERR_SHAPE;
@@ -50,7 +51,8 @@ int check(const dh_cross_entropy_t* c, void* dhidden, int64_t ld_dhidden, void* 
     if (!aligned(c->tokens, 4) || !aligned(c->weight, 4) || !aligned(c->row_of, 4) || !aligned(error, 4)) return DH_ERR_ALIGN;
     a.hidden = c->hidden;
     a.head = c->head;
-    a.type = c->type;
+    a.type = type;
+    a.two_terms = c->type != type;
     a.T = c->T;
     a.N = c->N;
     a.K = c->K;
@@ -70,7 +72,8 @@ int check(const dh_cross_entropy_t* c, void* dhidden, int64_t ld_dhidden, void* 
 
 int check_space(const dh::CrossEntropyArgs& a, void* ws, size_t ws_bytes) {
     return aligned(ws, DH_WORKSPACE_ALIGN) &&
-                   ws_bytes >= dh::cross_entropy_workspace_bytes(a.T, a.N, a.K, a.loss != nullptr, a.dhidden != nullptr, a.dhead != nullptr)
+                   ws_bytes >= dh::cross_entropy_workspace_bytes(a.T, a.N, a.K, a.loss != nullptr, a.dhidden != nullptr, a.dhead != nullptr,
+                                                                  a.two_terms)
                ? DH_OK
                : DH_ERR_WORKSPACE;
 }
@@ -80,8 +83,10 @@ int check_space(const dh::CrossEntropyArgs& a, void* ws, size_t ws_bytes) {
 extern "C" {
 
 size_t draft_head_cross_entropy_workspace_bytes(int T, int N, int K, unsigned int outputs) {
-    if (!shape_ok(T, N, K) || (outputs & ~7u) != 0u || outputs == 0u) return 0;
-    return dh::cross_entropy_workspace_bytes(T, N, K, (outputs & DH_CE_LOSS) != 0, (outputs & DH_CE_DHIDDEN) != 0, (outputs & DH_CE_DHEAD) != 0);
+    const unsigned int what = outputs & ~DH_CE_TWO_TERMS;
+    if (!shape_ok(T, N, K) || (what & ~7u) != 0u || what == 0u) return 0;
+    return dh::cross_entropy_workspace_bytes(T, N, K, (what & DH_CE_LOSS) != 0, (what & DH_CE_DHIDDEN) != 0, (what & DH_CE_DHEAD) != 0,
+                                             what != outputs);
 }
 
 int draft_head_cross_entropy(const dh_cross_entropy_t* c, float* loss, float* lse, float* rest, void* dhidden, int64_t ld_dhidden,

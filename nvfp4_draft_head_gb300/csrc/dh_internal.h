@@ -167,6 +167,7 @@ struct CrossEntropyArgs {
     const void* hidden;      // [T][K] of `type`
     const void* head;        // [N][K]
     int type;                // DH_T_BF16 or DH_T_F16
+    bool two_terms;          // g in two 16-bit terms at any T
     int T, N, K;
     long long ld_hidden, ld_head;
     const int32_t* tokens;   // [T]
@@ -187,7 +188,7 @@ struct CrossEntropyArgs {
     int probe_role;          // the self-test of the loss's waits, where probe_rounds is not 0
     uint32_t probe_rounds;
 };
-size_t cross_entropy_workspace_bytes(int T, int N, int K, bool loss, bool dhidden, bool dhead);
+size_t cross_entropy_workspace_bytes(int T, int N, int K, bool loss, bool dhidden, bool dhead, bool two_terms);
 cudaError_t launch_cross_entropy(const CrossEntropyArgs& a, cudaStream_t s);
 
 // FP8 product with a scale per block of 128 (dh_fp8_blocks.cu): y = x W'^T, or (gradient) with
