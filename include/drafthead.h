@@ -524,9 +524,10 @@ int fp8_block_matmul_wait_probe(const dh_fp8_blocks_t *w, const void *x, int M, 
 
 /* Softmax cross entropy of T hidden states against the vocabulary given by N head
  * rows, and its gradients, without the T x N logits in memory (but for up to 128 tokens
- * whose gradients are computed in the same call: see the workspace) (the pages have no counterpart: it
- * is how the BF16 rows of a draft head are trained on the tokens themselves, before
- * they are quantised). With z = h_t . W_n and y_t the head row of tokens[t]:
+ * whose gradients are computed in the same call; and their gradient g is, in 16 bits, a piece
+ * of the vocabulary at a time: see the workspace) (the pages have no counterpart: it is how
+ * the BF16 rows of a draft head are trained on the tokens themselves, before they are
+ * quantised). With z = h_t . W_n and y_t the head row of tokens[t]:
  *   lse_t  = log sum_n e^z_tn,  loss_t = w_t (lse_t - z_ty),
  *   g_tn   = w_t (e^(z_tn - lse_t) - [n = y_t]),  dh = g W,  dW = g^T h.
  * A token without a head row (row_of[token] < 0, an id outside [0, V), a row outside
@@ -581,8 +582,8 @@ size_t draft_head_cross_entropy_workspace_bytes(int T, int N, int K, unsigned in
  * losses' sum. None of the outputs may overlap an input or another output. ws: 256-byte
  * aligned, no initialisation; calls that overlap on the GPU must not share one. error: as for
  * nvfp4_matmul. Sums in 32 bits; g is rounded to 16 bits between its products (with a
- * power of two taken out; up to 128 tokens to two such terms), the gradients once more. Repeatable bit for bit. Capturable
- * in a CUDA graph. */
+ * power of two taken out; up to 128 tokens, or with DH_CE_TWO_TERMS, to two such terms),
+ * the gradients once more. Repeatable bit for bit. Capturable in a CUDA graph. */
 int draft_head_cross_entropy(const dh_cross_entropy_t *c, float *loss, float *lse, float *rest, void *dhidden, int64_t ld_dhidden,
                              void *dhead, int64_t ld_dhead, void *ws, size_t ws_bytes, unsigned int *error, void *stream);
 

@@ -1,5 +1,6 @@
 // Softmax cross entropy of hidden states against a vocabulary given by its head rows, and
-// its gradients, without the T x N logits in memory.
+// its gradients, without the T x N logits in memory (g, below, is: in 16 bits, a piece of the
+// vocabulary at a time).
 //
 //   z_tn = h_t . W_n,  m_t = max_n z_tn,  S_t = sum_n e^(z_tn - m_t),
 //   lse_t = m_t + ln S_t,  loss_t = w_t (ln S_t + (m_t - z_ty)),
@@ -23,7 +24,7 @@
 //
 // What bounds it. Many tokens: the tensor cores, whose pipe is busy for 95 to 97 of 100 cycles in
 // all four products, at the clock that the power limit leaves them (1.6 of 2.07 GHz): the loss of
-// 4,095 x 64,026 x 2,560 takes 680 us (1,970 TFLOP/s), the step of 4,096 2,980 (1,800 over its 8 TNK).
+// 4,095 x 64,026 x 2,560 takes 690 us (1,950 TFLOP/s), the step of 4,096 2,930 (1,830 over its 8 TNK).
 // Few tokens: reading the head, 61 x 64,026 in 60 us (5.5 TB/s), and for a small vocabulary the
 // chain of launches, 16 x 4,000 in 21 us.
 #include <cuda_bf16.h>
