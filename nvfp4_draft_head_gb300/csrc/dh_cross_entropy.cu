@@ -12,9 +12,9 @@
 // is written in 16 bits (the only [tokens x piece] array), and two products read it, one along
 // the piece (dh, added up over the pieces in 32 bits), one along the tokens (dW, final). The
 // product is three quarters useful: 8 T N K operations against the 6 that the mathematics has,
-// the price of not keeping T x N probabilities. (For up to 128 tokens the logits, T x N of them, are
-// less than the piece may take anyway, and reading the head again would be the work: a call that
-// computes both keeps them in its workspace between its products.)
+// the price of keeping no logits between the loss and the gradients. (For up to 128 tokens the
+// logits, T x N of them, are less than the piece may take anyway, and reading the head again would be
+// the work: a call that computes both keeps them in its workspace between its products.)
 //
 // Roundings besides 32-bit arithmetic: g to the inputs' 16-bit type (the tensor cores take
 // nothing wider from it; its error is that of rounding the results again), scaled by a power of
