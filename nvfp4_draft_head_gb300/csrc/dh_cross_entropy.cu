@@ -842,8 +842,11 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
         const size_t want = (total + 255) / 256, cap = static_cast<size_t>(sm_count()) * 8;
         // (not early: a product's CTA leaves no registers for this kernel's, which would all start on the few SMs
         // that are through first: 100 x 64,026 x 2,560 241 us, 231)
-        sum_kernel<T><<<static_cast<unsigned>(want < cap ? want : cap), 256, 0, stream>>>(tok, sums, c.K, wmax);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(want < cap ? want : cap));
+        cfg.blockDim = dim3(256);
+        cfg.stream = stream;
+        if ((e = cudaLaunchKernelEx(&cfg, sum_kernel<T>, tok, sums, c.K, wmax)) != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
