@@ -562,18 +562,19 @@ typedef struct dh_cross_entropy {
 #define DH_CE_DHIDDEN 2u
 #define DH_CE_DHEAD 4u
 /* With these, and with the descriptor's type: g in two 16-bit terms (its rounding, and what that
- * left over) at any number of tokens, as up to 128 have it anyway. The gradients are then off by
- * their own rounding alone; with one term by 1.43 times that (bf16 0.0024 and 0.0017 relative, in
- * the 2-norm). 4,096 tokens x 64,026 x 2,560 take 4.5 ms in place of 2.9. */
+ * left over) at any size, as up to 128 tokens, and up to 1,024 while T N K <= 2^28, have it
+ * anyway. The gradients are then off by their own rounding alone; with one term by 1.43 times
+ * that (bf16 0.0024 and 0.0017 relative, in the 2-norm). 4,096 tokens x 64,026 x 2,560 take
+ * 4.5 ms in place of 2.9. */
 #define DH_CE_TWO_TERMS 8u
 
 /* Bytes of workspace of a call with these outputs (0 for an unsupported shape): 8 bytes
  * per token and 128 head rows for the loss; for the gradients g of a piece of the
  * vocabulary in 16 bits (512 MiB at most while T <= 131,072) and, each where it is
  * wanted, 32-bit sums of dh (and of dW's tiles, where they are few and the tokens many) and
- * a copy of the hidden states. Up to 128 tokens have g in two 16-bit terms, and, where the
- * loss and a gradient are wanted together and the vocabulary is one piece, their logits in
- * fp32 between the two. */
+ * a copy of the hidden states; g and the copy twice where g has two terms. Up to 128 tokens
+ * have, where the loss and a gradient are wanted together and the vocabulary is one piece,
+ * their logits in fp32 between the two. */
 size_t draft_head_cross_entropy_workspace_bytes(int T, int N, int K, unsigned int outputs);
 
 /* The loss (fp32 [T]) and, where their pointers are not NULL, the normaliser lse (fp32
@@ -582,7 +583,7 @@ size_t draft_head_cross_entropy_workspace_bytes(int T, int N, int K, unsigned in
  * losses' sum. None of the outputs may overlap an input or another output. ws: 256-byte
  * aligned, no initialisation; calls that overlap on the GPU must not share one. error: as for
  * nvfp4_matmul. Sums in 32 bits; g is rounded to 16 bits between its products (with a
- * power of two taken out; up to 128 tokens, or with DH_CE_TWO_TERMS, to two such terms),
+ * power of two taken out; to two such terms where DH_CE_TWO_TERMS says),
  * the gradients once more. Repeatable bit for bit. Capturable in a CUDA graph. */
 int draft_head_cross_entropy(const dh_cross_entropy_t *c, float *loss, float *lse, float *rest, void *dhidden, int64_t ld_dhidden,
                              void *dhead, int64_t ld_dhead, void *ws, size_t ws_bytes, unsigned int *error, void *stream);

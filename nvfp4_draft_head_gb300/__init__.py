@@ -1163,9 +1163,9 @@ def linear_cross_entropy(hidden: torch.Tensor, head: torch.Tensor, tokens: torch
     piece of the vocabulary at a time, of up to 512 MiB). tokens: int32 [T], target ids with
     row_of (draft_head_row_map), head rows without it; a token without a head row (-100, say) is
     left out, as a row of weight 0 is. weights: float32 [T]. dhidden and dhead may be given
-    tensors, which overlap no other. two_terms: the logits' gradient in two 16-bit terms for more
-    than 128 tokens too, whose gradients then are off by their own rounding alone (1.43 times that
-    with one), at one and a half times the time. The loss has no autograd graph (the gradients are
+    tensors, which overlap no other. two_terms: the logits' gradient in two 16-bit terms at any
+    size, as few tokens and small products have it anyway; the gradients then are off by their own
+    rounding alone (1.43 times that with one term), at one and a half times the time. The loss has no autograd graph (the gradients are
     at hand; LinearCrossEntropy is the differentiable form). See draft_head_cross_entropy."""
     if stream is not None:
         return _on_stream(stream, linear_cross_entropy, hidden, head, tokens, weights, row_of, dhidden, dhead, None, two_terms)

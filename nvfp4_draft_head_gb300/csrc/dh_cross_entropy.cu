@@ -19,8 +19,8 @@
 // Roundings besides 32-bit arithmetic: g to the inputs' 16-bit type (the tensor cores take
 // nothing wider from it; its error is that of rounding the results again), scaled by a power of
 // two so that the largest row weight lies just under 1 (bf16) or 2^15 (f16, whose probabilities
-// would be subnormal below 6e-5), in two terms for up to 128 tokens or where the caller asks for
-// them; the gradients once, at the end.
+// would be subnormal below 6e-5), in two terms for few tokens, small products, or where the caller
+// asks for them; the gradients once, at the end.
 //
 // What bounds it. Many tokens: the tensor cores, whose pipe is busy for 95 to 97 of 100 cycles in
 // all four products, at the clock that the power limit leaves them (1.6 of 2.07 GHz): the loss of
@@ -624,14 +624,18 @@ gemm::Shape hidden_tiles(int T, int K, int piece, unsigned int* error) {
 }
 
 // g in two terms, its 16-bit rounding and what that left over, as rows T .. 2 T - 1 of g, of dh's
-// sums and (the same hidden states again) of dW's contraction: for few tokens, for which the
-// products' tiles have the room. One term makes the gradients' error 1.43 times that of rounding them
-// alone (64,026 x 2,560 bf16, relative 2-norm: 0.00238 and 0.00166); a second one takes it away at any
-// size and costs, in us (one term / two): 129 tokens 276 / 336, 256 293 / 379, 520 513 / 705, 4,096
-// 2,776 / 4,482; 100 tokens 230 in two. That error is within the gradients' own type, and a framework
-// that keeps its logits in 16 bits has it as well, so above 128 tokens the second term is the caller's
-// choice (DH_CE_TWO_TERMS).
-int terms_of(int T, bool two_terms) { return two_terms || T <= 128 ? 2 : 1; }
+// sums and (the same hidden states again) of dW's contraction. One term makes the gradients' error
+// 1.43 times that of rounding them alone (64,026 x 2,560 bf16, relative 2-norm: 0.00238 and 0.00166), and
+// up to 1.6 times where they are sums of few terms (191 x 230 x 128); a second one takes it away at any
+// size. So there are two where that costs little: for up to 128 tokens, for which the products' tiles
+// have the room, and for small products of up to 1,024, whose time is their launches' (device us, one term
+// / two: 200 x 230 x 128 18.6 / 20.7, 129 x 4,000 x 256 27.5 / 29.1, 256 x 4,096 x 256, T N K of 2^28,
+// 28.1 / 29.7). Beyond, it is the caller's choice (DH_CE_TWO_TERMS): 2^30 of 1,000 tokens 31.5 / 36.6, of
+// 4,096 50 / 61; 64,026 x 2,560, 129 tokens 276 / 336, 520 513 / 705, 4,096 2,776 / 4,482. (The error is
+// within the gradients' own type; who keeps 16-bit logits has it as well.)
+int terms_of(int T, int N, int K, bool two_terms) {
+    return two_terms || T <= 128 || (T <= 1024 && static_cast<long long>(T) * N * K <= 1ll << 28) ? 2 : 1;
+}
 
 // dW's tiles where they are few and the tokens many: all in parts of at least eight steps, as many
 // as fill the pairs of SMs once (6,208 tokens, 5 rows of 4,592: 34 us of 105 were 18 tiles of 97
@@ -649,7 +653,7 @@ gemm::Shape head_tiles(int rows, int N, int K, int piece, unsigned int* error) {
 
 // Whether a call for both keeps its logits: few tokens whose vocabulary is one piece. Multiplied
 // again, 12 x 83,361 x 3,568 takes 449 us; kept, 347 (the head is read twice in place of three times).
-bool keeps_logits(int T, int N) { return T <= gemm::kRows && N <= piece_rows(terms_of(T, false) * T, N); }
+bool keeps_logits(int T, int N) { return T <= gemm::kRows && N <= piece_rows(2 * T, N); }
 
 struct Space {
     size_t z, wmax, part, target, lse, rest, g, hidden, sum, parts, head_parts, bytes;
@@ -669,7 +673,7 @@ Space space_of(int T, int N, int K, bool loss, bool dh, bool dw, bool two_terms)
         s.lse = take(t * 4);
         s.rest = take(t * 4);
     }
-    const int rows = terms_of(T, two_terms) * T, piece = piece_rows(rows, N);
+    const int rows = terms_of(T, N, K, two_terms) * T, piece = piece_rows(rows, N);
     const size_t r = static_cast<size_t>(rows);
     if (dh || dw) s.g = take(r * piece * 2);
     if (loss && (dh || dw) && keeps_logits(T, N)) s.z = take(t * up256(N) * 4);
@@ -699,7 +703,7 @@ cudaError_t run(const CrossEntropyArgs& c, cudaStream_t stream) {
     uint32_t* wmax = reinterpret_cast<uint32_t*>(ws + sp.wmax);
     const int tiles_m = ceil_div(c.T, gemm::kRows * P);
     T* hidden = dw ? reinterpret_cast<T*>(ws + sp.hidden) : nullptr;
-    const int terms = terms_of(c.T, c.two_terms), all_rows = terms * c.T;   // of g
+    const int terms = terms_of(c.T, c.N, c.K, c.two_terms), all_rows = terms * c.T;   // of g
     const Rows rows = {c.hidden, c.ld_hidden, c.K, hidden, terms > 1 ? c.T : 0, wmax};
     cudaError_t e;
     using K1 = typename Stats<T, P>::Layout;

@@ -33,7 +33,11 @@ def test_two_terms_of_the_gradient(L):
     assert nb(300, 1000, 64, dh.DH_CE_LOSS | dh.DH_CE_TWO_TERMS) == nb(300, 1000, 64, dh.DH_CE_LOSS)
     assert nb(128, 1000, 64, 7 | dh.DH_CE_TWO_TERMS) == nb(128, 1000, 64, 7)
     # g and the copy of the hidden states once more
-    assert nb(1024, 1024, 64, dh.DH_CE_DHEAD | dh.DH_CE_TWO_TERMS) >= nb(1024, 1024, 64, dh.DH_CE_DHEAD) + 1024 * 1024 * 2 + 1024 * 64 * 2
+    assert nb(2048, 4096, 64, dh.DH_CE_DHEAD | dh.DH_CE_TWO_TERMS) >= nb(2048, 4096, 64, dh.DH_CE_DHEAD) + 2048 * 4096 * 2 + 2048 * 64 * 2
+    # small products of up to 1,024 tokens have both terms anyway (T N K <= 2^28)
+    for size, both in (((1024, 1024, 256), True), ((1024, 1025, 256), False), ((1025, 1024, 8), False), ((129, 1, 8), True), ((200, 64026, 16), True),
+                       ((200, 64026, 24), False)):
+        assert (nb(*size, 6) == nb(*size, 6 | dh.DH_CE_TWO_TERMS)) == both
     for t in (0, dh.DH_T_F32, 4, dh.DH_T_BF16 | 16):
         d = dh.dh_cross_entropy_t(0x10000, 0x20000, t | dh.DH_CE_TWO_TERMS, 4, 128, 100, 128, 128, 0x10000, None, None, 0)
         assert L.draft_head_cross_entropy(C.byref(d), 0x10000, None, None, None, 0, None, 0, 0x100000, 1 << 30, None, None) == dh.DH_ERR_ARG
